@@ -65,6 +65,8 @@ enum { HMOE_KEPT_NVFP4 = 0, HMOE_KEPT_MXFP4 = 1 };
 enum { HMOE_ACT_16BIT = 0, HMOE_ACT_MXFP4 = 1 };
 /* How hybrid_moe_forward runs the decode path (M <= 8). */
 enum { HMOE_DECODE_STAGED = 0, HMOE_DECODE_SINGLE_LAUNCH = 1 };
+/* Element types of the row movements (moe_permute and its kin). */
+enum { HMOE_DTYPE_BF16 = 0, HMOE_DTYPE_FP16 = 1, HMOE_DTYPE_FP32 = 2 };
 enum { HMOE_TIER_KEPT = 0, HMOE_TIER_NF3 = 1 };
 enum { HMOE_TENSOR_W13 = 0, HMOE_TENSOR_W2 = 1 };
 /* Stages of the forward, in launch order (see hybrid_moe_forward_stage). */
@@ -72,6 +74,9 @@ enum { HMOE_STAGE_ROUTE = 0, HMOE_STAGE_W13 = 1, HMOE_STAGE_W2 = 2, HMOE_STAGE_C
 
 /* Largest M served by the decode path (M <= 8, [P1] "How it works"). */
 #define HMOE_DECODE_MAX_M 8
+
+/* Most adapters of one moe_lora call (one per request, or one per request and expert). */
+#define HMOE_MAX_GROUPS 2048
 
 /* Layer descriptor, read once by moe_layer_create ([P2]: tier assignment comes
  * from the bit map; [P1]: scratch sizing from the maximum batched tokens).
@@ -378,6 +383,117 @@ hmoe_status moe_repack(const hmoe_layer* layer, const hmoe_expert_src* experts,
  * HMOE_ERR_ALIGN, HMOE_ERR_HIP. */
 hmoe_status moe_quantize_mxfp4(const float* in, int32_t rows, int32_t K, uint8_t* codes,
                                uint8_t* scales, hipStream_t stream);
+
+/* ---- operators around the experts -------------------------------------------------
+ *
+ * The row movements and the adapters a program needs when the experts' products run
+ * outside hybrid_moe_forward (fine-tuning beside the frozen packed weights, experts of its
+ * own, experts spread over processes), with their gradients. Shared rules:
+ *   - Matrices of rows have a row stride in elements (>= the row's length; the last axis is
+ *     contiguous) and need only element alignment; every other pointer 16 bytes.
+ *   - Index and weight arrays (topk_ids, topk_w, slot_row, ...) are contiguous.
+ *   - Outputs must not overlap inputs or each other, except where said.
+ *   - No call keeps anything between calls: scratch contents matter only while the call's
+ *     kernels run, so calls that may overlap in time need scratch buffers of their own.
+ *   - Results do not depend on timing: fixed-order sums, no floating-point atomics. */
+
+/* Bytes of scratch of moe_permute for M tokens (0 up to 1024 slots: scratch may then be
+ * NULL). Host arithmetic only. Errors: as moe_permute. */
+hmoe_status moe_permute_scratch_bytes(int32_t M, int32_t k, int32_t E, size_t* bytes);
+
+/* Tokens into expert order. With slot s = t * k + j, the slots whose id lies in [0, E) are
+ * sorted by id, ascending s inside an expert; slots with another id are dropped (a process
+ * that holds experts [a, a + E) passes id - a). Writes
+ *   rows          [M * k, H], row r = x[sorted_slots[r] / k] for r < expert_off[E]; rows at
+ *                 and past expert_off[E] are left as they were
+ *   sorted_slots  int32 [M * k]: slot of each row, -1 at and past expert_off[E]
+ *   slot_row      int32 [M, k]: row of each slot, -1 for a dropped slot
+ *   expert_off    int32 [E + 1]: first row of each expert, then the number of rows
+ * M = 0 writes expert_off only. Up to 1024 slots it is one launch.
+ * Errors: HMOE_ERR_INVALID_ARG (M < 0, k outside 1..16, E outside 1..1024, H < 1, a stride
+ * below H, an unknown dtype); HMOE_ERR_UNSUPPORTED (M * k > 2^24, or rows of 2^24 blocks of
+ * 4 KiB or more); HMOE_ERR_SCRATCH; HMOE_ERR_ALIGN; HMOE_ERR_HIP. */
+hmoe_status moe_permute(const void* x, int64_t x_stride, const int32_t* topk_ids, int32_t M,
+                        int32_t k, int32_t E, int32_t H, int32_t dtype, void* rows,
+                        int64_t rows_stride, int32_t* sorted_slots, int32_t* slot_row,
+                        int32_t* expert_off, void* scratch, size_t scratch_bytes,
+                        hipStream_t stream);
+
+/* Gradient of moe_permute: dx[t] = sum over j of drows[slot_row[t, j]], in fp32 with j
+ * ascending, rounded once; a token whose slots were all dropped gets zeros. drows
+ * [M * k, H], dx [M, H]. A slot_row entry outside [0, M * k) counts as dropped. M = 0 is a
+ * no-op. Errors: as moe_permute. */
+hmoe_status moe_permute_backward(const void* drows, int64_t drows_stride, const int32_t* slot_row,
+                                 int32_t M, int32_t k, int32_t H, int32_t dtype, void* dx,
+                                 int64_t dx_stride, hipStream_t stream);
+
+/* Rows back into tokens with the routing weights: y[t] = sum over j of topk_w[t, j] *
+ * rows[slot_row[t, j]], in fp32 with j ascending, rounded once; dropped slots add nothing.
+ * rows [M * k, H], topk_w fp32 [M, k], y [M, H]. A slot_row entry outside [0, M * k) counts
+ * as dropped. M = 0 is a no-op. Errors: as moe_permute. */
+hmoe_status moe_unpermute(const void* rows, int64_t rows_stride, const int32_t* slot_row,
+                          const float* topk_w, int32_t M, int32_t k, int32_t H, int32_t dtype,
+                          void* y, int64_t y_stride, hipStream_t stream);
+
+/* Gradients of moe_unpermute: drows[slot_row[t, j]] = topk_w[t, j] * dy[t] (rounded once) and
+ * dw[t, j] = <dy[t], rows[slot_row[t, j]]> in fp32, 0 for a dropped slot. Rows that no slot
+ * names are left as they were; no two slots may name the same row. dw fp32 [M, k]. M = 0 is
+ * a no-op. Errors: as moe_permute. */
+hmoe_status moe_unpermute_backward(const void* dy, int64_t dy_stride, const void* rows,
+                                   int64_t rows_stride, const int32_t* slot_row,
+                                   const float* topk_w, int32_t M, int32_t k, int32_t H,
+                                   int32_t dtype, void* drows, int64_t drows_stride, float* dw,
+                                   hipStream_t stream);
+
+/* Gradient of moe_route: dlogits fp32 [M, E], fully overwritten, from the ids and weights it
+ * wrote and dw fp32 [M, k]: w[t, j] (dw[t, j] - sum over i of w[t, i] dw[t, i]) at
+ * [t, topk_ids[t, j]], zero elsewhere. Ids outside [0, E) add nothing to dlogits; the same id
+ * twice adds up. M = 0 is a no-op.
+ * Errors: as moe_route. */
+hmoe_status moe_route_backward(const int32_t* topk_ids, const float* topk_w, const float* dw,
+                               int32_t M, int32_t E, int32_t k, float* dlogits,
+                               hipStream_t stream);
+
+/* Bytes of scratch of moe_lora and moe_lora_backward (host arithmetic only).
+ * Errors: as moe_lora. */
+hmoe_status moe_lora_scratch_bytes(int32_t M, int32_t G, int32_t K, int32_t N, int32_t rank,
+                                   size_t* forward_bytes, size_t* backward_bytes);
+
+/* Low-rank adapters of many requests beside one shared projection K -> N: for each row m
+ * with adapter g = ids[m]
+ *   z[m] = A[g] x[m] (fp32),   y[m] = base[m] + scale[g] * B[g] z[m] (one rounding).
+ * base is what the shared projection gave: a NULL base counts as zeros, and base may be y
+ * itself (same stride), which adds the adapters in place. A row whose id lies outside
+ * [0, G) has no adapter: y[m] = base[m], z[m] = 0. x, base, y, A, B are bf16 bits: x [M, K],
+ * base and y [M, N], A [G, rank, K], B [G, N, rank] (an adapter of lower rank is padded with
+ * zeros), scale fp32 [G]. z fp32 [M, rank] is what moe_lora_backward needs and may be NULL.
+ * A and B must be finite (an infinite entry gives infinities or NaN in the rows that use it).
+ * M = 0 is a no-op. Up to 1024 rows it is two launches.
+ * Errors: HMOE_ERR_INVALID_ARG (M < 0; G, K, N or rank < 1; a stride below the row's length;
+ * base == y with another stride); HMOE_ERR_UNSUPPORTED (K, N or rank not a multiple of 8,
+ * rank > 128, G > HMOE_MAX_GROUPS, M > 2^22, K or N > 2^20); HMOE_ERR_SCRATCH; HMOE_ERR_ALIGN;
+ * HMOE_ERR_HIP. */
+hmoe_status moe_lora(const uint16_t* x, int64_t x_stride, const int32_t* ids, const uint16_t* A,
+                     const uint16_t* B, const float* scale, int32_t M, int32_t G, int32_t K,
+                     int32_t N, int32_t rank, const uint16_t* base, int64_t base_stride,
+                     uint16_t* y, int64_t y_stride, float* z, void* scratch, size_t scratch_bytes,
+                     hipStream_t stream);
+
+/* Gradients of moe_lora, from dy [M, N], the forward's x and z:
+ *   dz[m] = scale[g] * B[g]^T dy[m] (fp32),   dx[m] = dbase[m] + A[g]^T dz[m] (one rounding),
+ *   dA[g] = sum of dz[m] x[m]^T,   dB[g] = scale[g] * sum of dy[m] z[m]^T
+ * over the rows of g. dbase [M, K] is the shared projection's own gradient with respect to
+ * x: NULL counts as zeros, and it may be dx itself (same stride). dA fp32 [G, rank, K] and
+ * dB fp32 [G, N, rank] are fully overwritten (zeros for an adapter without rows, so also at
+ * M = 0). The gradient with respect to base is dy itself.
+ * Errors: as moe_lora. */
+hmoe_status moe_lora_backward(const uint16_t* dy, int64_t dy_stride, const uint16_t* x,
+                              int64_t x_stride, const float* z, const int32_t* ids,
+                              const uint16_t* A, const uint16_t* B, const float* scale, int32_t M,
+                              int32_t G, int32_t K, int32_t N, int32_t rank,
+                              const uint16_t* dbase, int64_t dbase_stride, uint16_t* dx,
+                              int64_t dx_stride, float* dA, float* dB, void* scratch,
+                              size_t scratch_bytes, hipStream_t stream);
 
 /* Static string naming a status code. */
 const char* moe_status_string(hmoe_status status);

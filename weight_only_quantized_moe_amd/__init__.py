@@ -14,17 +14,20 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, Structure, byref, c_char_p, c_int32, c_size_t, c_void_p
+from ctypes import (POINTER, Structure, byref, c_char_p, c_int32, c_int64, c_size_t,
+                    c_void_p)
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libhmoe.so")
 
 KEPT_NVFP4, KEPT_MXFP4 = 0, 1
 DECODE_STAGED, DECODE_SINGLE_LAUNCH = 0, 1
 ACT_16BIT, ACT_MXFP4 = 0, 1
+DTYPE_BF16, DTYPE_FP16, DTYPE_FP32 = 0, 1, 2
 TIER_KEPT, TIER_NF3 = 0, 1
 TENSOR_W13, TENSOR_W2 = 0, 1
 STAGE_ROUTE, STAGE_W13, STAGE_W2, STAGE_COMBINE = 0, 1, 2, 3
 DECODE_MAX_M = 8
+MAX_GROUPS = 2048
 
 EXPORTED = (
     "moe_layer_create", "moe_layer_destroy", "moe_layer_query", "moe_scratch_bytes",
@@ -32,6 +35,9 @@ EXPORTED = (
     "moe_route", "moe_align", "moe_align_view", "moe_decode_view", "moe_topk_view",
     "hybrid_moe_forward", "hybrid_moe_forward_static", "hybrid_moe_forward_stage", "moe_dequant",
     "moe_repack", "moe_quantize_mxfp4",
+    "moe_permute_scratch_bytes", "moe_permute", "moe_permute_backward", "moe_unpermute",
+    "moe_unpermute_backward", "moe_route_backward",
+    "moe_lora_scratch_bytes", "moe_lora", "moe_lora_backward",
     "moe_status_string", "moe_last_error",
 )
 
@@ -127,6 +133,20 @@ def load_library() -> ctypes.CDLL:
     lib.moe_repack.restype = st
     lib.moe_quantize_mxfp4.argtypes = [c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p]
     lib.moe_quantize_mxfp4.restype = st
+    P, I, L = c_void_p, c_int32, c_int64
+    for name, args in {
+        "moe_permute_scratch_bytes": [I, I, I, POINTER(c_size_t)],
+        "moe_permute": [P, L, P, I, I, I, I, I, P, L, P, P, P, P, c_size_t, P],
+        "moe_permute_backward": [P, L, P, I, I, I, I, P, L, P],
+        "moe_unpermute": [P, L, P, P, I, I, I, I, P, L, P],
+        "moe_unpermute_backward": [P, L, P, L, P, P, I, I, I, I, P, L, P, P],
+        "moe_route_backward": [P, P, P, I, I, I, P, P],
+        "moe_lora_scratch_bytes": [I, I, I, I, I, POINTER(c_size_t), POINTER(c_size_t)],
+        "moe_lora": [P, L, P, P, P, P, I, I, I, I, I, P, L, P, L, P, P, c_size_t, P],
+        "moe_lora_backward": [P, L, P, L, P, P, P, P, P, I, I, I, I, I, P, L, P, L, P, P, P, c_size_t, P],
+    }.items():
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = st
     lib.moe_status_string.argtypes = [c_int32]
     lib.moe_status_string.restype = c_char_p
     lib.moe_last_error.argtypes = []
@@ -329,6 +349,207 @@ def moe_quantize_mxfp4(x, codes, scales, stream=None) -> None:
     rows, K = x.shape
     _check(load_library().moe_quantize_mxfp4(_ptr(x), rows, K, _ptr(codes), _ptr(scales),
                                              _stream(stream)))
+
+
+# ---- operators around the experts ---------------------------------------------------
+
+def _dtype_code(t) -> int:
+    """Element type of a rows tensor (int16 holds bf16 bits, as for the layer)."""
+    import torch
+    code = {torch.bfloat16: DTYPE_BF16, torch.int16: DTYPE_BF16, torch.float16: DTYPE_FP16,
+            torch.float32: DTYPE_FP32}.get(t.dtype)
+    if code is None:
+        raise ValueError(f"rows of {t.dtype}: expected bfloat16 (or its bits as int16), float16 "
+                         "or float32")
+    return code
+
+
+def _matrix(name: str, t, rows: int, cols: int, code: int) -> int:
+    """Checks a [rows, cols] matrix of the given element type; returns its row stride."""
+    if tuple(t.shape) != (rows, cols) or _dtype_code(t) != code:
+        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}, expected [{rows}, {cols}] of the "
+                         "other rows' type")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    return t.stride(0) if rows > 1 else cols
+
+
+def _array(name: str, t, shape: tuple, dtype: str) -> None:
+    if tuple(t.shape) != shape or str(t.dtype) != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}, expected contiguous {dtype} {shape}")
+
+
+class _On:
+    """The device of a call's tensors, made current for the launch, and its stream: the
+    given one, else that device's current stream."""
+
+    def __init__(self, stream, *tensors):
+        self.device = tensors[0].get_device()
+        if self.device < 0 or any(t is not None and t.get_device() != self.device for t in tensors):
+            raise ValueError("all tensors of a call must be on one GPU")
+        self.stream = stream
+
+    def __enter__(self):
+        import torch
+        self.before = torch.cuda.current_device()
+        if self.before != self.device:
+            torch.cuda.set_device(self.device)
+        return torch.cuda.current_stream().cuda_stream if self.stream is None else self.stream
+
+    def __exit__(self, *exc):
+        if self.before != self.device:
+            import torch
+            torch.cuda.set_device(self.before)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _room(scratch) -> tuple:
+    """Address and bytes of an optional scratch tensor."""
+    if scratch is None:
+        return None, 0
+    if not scratch.is_contiguous():
+        raise ValueError("scratch must be contiguous")
+    return scratch.data_ptr(), scratch.numel() * scratch.element_size()
+
+
+def moe_permute_scratch_bytes(M: int, top_k: int, num_experts: int) -> int:
+    n = c_size_t()
+    _check(load_library().moe_permute_scratch_bytes(M, top_k, num_experts, byref(n)))
+    return n.value
+
+
+def moe_permute(x, topk_ids, num_experts: int, rows, sorted_slots, slot_row, expert_off,
+                scratch=None, stream=None) -> None:
+    """x[M, H] into expert order: rows[M * k, H], sorted_slots i32 [M * k], slot_row i32
+    [M, k] and expert_off i32 [E + 1] (see include/hmoe.h). Ids outside [0, E) are dropped."""
+    M, k = topk_ids.shape
+    H = x.shape[1]
+    code = _dtype_code(x)
+    xs, rs = _matrix("x", x, M, H, code), _matrix("rows", rows, M * k, H, code)
+    _array("topk_ids", topk_ids, (M, k), "torch.int32")
+    _array("sorted_slots", sorted_slots, (M * k,), "torch.int32")
+    _array("slot_row", slot_row, (M, k), "torch.int32")
+    _array("expert_off", expert_off, (num_experts + 1,), "torch.int32")
+    ws, nbytes = _room(scratch)
+    with _On(stream, x, topk_ids, rows, sorted_slots, slot_row, expert_off, scratch) as st:
+        _check(load_library().moe_permute(
+            x.data_ptr(), xs, topk_ids.data_ptr(), M, k, num_experts, H, code, rows.data_ptr(), rs,
+            sorted_slots.data_ptr(), slot_row.data_ptr(), expert_off.data_ptr(), ws, nbytes, st))
+
+
+def moe_permute_backward(drows, slot_row, dx, stream=None) -> None:
+    """dx[M, H] = for each token the sum of its slots' drows[M * k, H]."""
+    M, k = slot_row.shape
+    H = drows.shape[1]
+    code = _dtype_code(drows)
+    ds, xs = _matrix("drows", drows, M * k, H, code), _matrix("dx", dx, M, H, code)
+    _array("slot_row", slot_row, (M, k), "torch.int32")
+    with _On(stream, drows, slot_row, dx) as st:
+        _check(load_library().moe_permute_backward(drows.data_ptr(), ds, slot_row.data_ptr(), M, k, H,
+                                                   code, dx.data_ptr(), xs, st))
+
+
+def moe_unpermute(rows, slot_row, topk_w, y, stream=None) -> None:
+    """y[M, H] = for each token the sum of its slots' rows[M * k, H] times topk_w f32 [M, k]."""
+    M, k = slot_row.shape
+    H = rows.shape[1]
+    code = _dtype_code(rows)
+    rs, ys = _matrix("rows", rows, M * k, H, code), _matrix("y", y, M, H, code)
+    _array("slot_row", slot_row, (M, k), "torch.int32")
+    _array("topk_w", topk_w, (M, k), "torch.float32")
+    with _On(stream, rows, slot_row, topk_w, y) as st:
+        _check(load_library().moe_unpermute(rows.data_ptr(), rs, slot_row.data_ptr(),
+                                            topk_w.data_ptr(), M, k, H, code, y.data_ptr(), ys, st))
+
+
+def moe_unpermute_backward(dy, rows, slot_row, topk_w, drows, dw, stream=None) -> None:
+    """Gradients of moe_unpermute: drows[M * k, H] (rows no slot names stay as they were) and
+    dw f32 [M, k]."""
+    M, k = slot_row.shape
+    H = rows.shape[1]
+    code = _dtype_code(rows)
+    ys, rs = _matrix("dy", dy, M, H, code), _matrix("rows", rows, M * k, H, code)
+    ds = _matrix("drows", drows, M * k, H, code)
+    _array("slot_row", slot_row, (M, k), "torch.int32")
+    _array("topk_w", topk_w, (M, k), "torch.float32")
+    _array("dw", dw, (M, k), "torch.float32")
+    with _On(stream, dy, rows, slot_row, topk_w, drows, dw) as st:
+        _check(load_library().moe_unpermute_backward(
+            dy.data_ptr(), ys, rows.data_ptr(), rs, slot_row.data_ptr(), topk_w.data_ptr(), M, k, H,
+            code, drows.data_ptr(), ds, dw.data_ptr(), st))
+
+
+def moe_route_backward(topk_ids, topk_w, dw, dlogits, stream=None) -> None:
+    """dlogits f32 [M, E] (fully overwritten) from moe_route's ids and weights and dw f32 [M, k]."""
+    M, k = topk_ids.shape
+    E = dlogits.shape[1]
+    _array("topk_ids", topk_ids, (M, k), "torch.int32")
+    _array("topk_w", topk_w, (M, k), "torch.float32")
+    _array("dw", dw, (M, k), "torch.float32")
+    _array("dlogits", dlogits, (M, E), "torch.float32")
+    with _On(stream, topk_ids, topk_w, dw, dlogits) as st:
+        _check(load_library().moe_route_backward(topk_ids.data_ptr(), topk_w.data_ptr(), dw.data_ptr(),
+                                                 M, E, k, dlogits.data_ptr(), st))
+
+
+def moe_lora_scratch_bytes(M: int, num_adapters: int, K: int, N: int, rank: int) -> tuple:
+    """Scratch bytes of moe_lora and of moe_lora_backward."""
+    f, b = c_size_t(), c_size_t()
+    _check(load_library().moe_lora_scratch_bytes(M, num_adapters, K, N, rank, byref(f), byref(b)))
+    return f.value, b.value
+
+
+def _adapters(M: int, ids, A, B, scale) -> tuple:
+    if A.dim() != 3 or B.dim() != 3 or A.shape[0] != B.shape[0] or A.shape[1] != B.shape[2]:
+        raise ValueError(f"A {tuple(A.shape)} and B {tuple(B.shape)}: expected [G, rank, K] and "
+                         "[G, N, rank]")
+    G, r, K = A.shape
+    for name, t in (("A", A), ("B", B)):
+        if _dtype_code(t) != DTYPE_BF16 or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous bfloat16")
+    _array("ids", ids, (M,), "torch.int32")
+    _array("scale", scale, (G,), "torch.float32")
+    return G, r, K, B.shape[1]
+
+
+def moe_lora(x, ids, A, B, scale, base, y, z=None, scratch=None, stream=None) -> None:
+    """y[M, N] = base + scale[g] * B[g] (A[g] x) with g = ids[m]; A bf16 [G, rank, K], B bf16
+    [G, N, rank], scale f32 [G]. base may be None (zeros) or y itself; z f32 [M, rank]
+    receives A[g] x for moe_lora_backward. Ids outside [0, G): no adapter."""
+    M = x.shape[0]
+    G, r, K, N = _adapters(M, ids, A, B, scale)
+    xs, ys = _matrix("x", x, M, K, DTYPE_BF16), _matrix("y", y, M, N, DTYPE_BF16)
+    bs = 0 if base is None else _matrix("base", base, M, N, DTYPE_BF16)
+    if z is not None:
+        _array("z", z, (M, r), "torch.float32")
+    ws, nbytes = _room(scratch)
+    with _On(stream, x, ids, A, B, scale, base, y, z, scratch) as st:
+        _check(load_library().moe_lora(
+            x.data_ptr(), xs, ids.data_ptr(), A.data_ptr(), B.data_ptr(), scale.data_ptr(), M, G, K, N,
+            r, _at(base), bs, y.data_ptr(), ys, _at(z), ws, nbytes, st))
+
+
+def moe_lora_backward(dy, x, z, ids, A, B, scale, dbase, dx, dA, dB, scratch=None,
+                      stream=None) -> None:
+    """Gradients of moe_lora: dx[M, K] = dbase + A[g]^T dz, dA f32 [G, rank, K] and dB f32
+    [G, N, rank] (fully overwritten). dbase may be None (zeros) or dx itself."""
+    M = x.shape[0]
+    G, r, K, N = _adapters(M, ids, A, B, scale)
+    ys, xs = _matrix("dy", dy, M, N, DTYPE_BF16), _matrix("x", x, M, K, DTYPE_BF16)
+    ds = _matrix("dx", dx, M, K, DTYPE_BF16)
+    bs = 0 if dbase is None else _matrix("dbase", dbase, M, K, DTYPE_BF16)
+    _array("z", z, (M, r), "torch.float32")
+    _array("dA", dA, (G, r, K), "torch.float32")
+    _array("dB", dB, (G, N, r), "torch.float32")
+    ws, nbytes = _room(scratch)
+    with _On(stream, dy, x, z, ids, A, B, scale, dbase, dx, dA, dB, scratch) as st:
+        _check(load_library().moe_lora_backward(
+            dy.data_ptr(), ys, x.data_ptr(), xs, z.data_ptr(), ids.data_ptr(), A.data_ptr(),
+            B.data_ptr(), scale.data_ptr(), M, G, K, N, r, _at(dbase), bs, dx.data_ptr(), ds,
+            dA.data_ptr(), dB.data_ptr(), ws, nbytes, st))
 
 
 class DeviceWeights:

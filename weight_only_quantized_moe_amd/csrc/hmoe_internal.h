@@ -105,6 +105,87 @@ hipError_t launch_mx_quant(const void* in, bool bf16, int rows, int K, const int
 hipError_t launch_prefill_x16(const Layer& L, const uint16_t* x, int M, void* scratch,
                               hipStream_t s);
 
+// route.hip: gradient of the top-k weights with respect to the logits
+hipError_t launch_route_backward(const int32_t* ids, const float* w, const float* dw, int M, int E,
+                                 int k, float* dlogits, hipStream_t s);
+
+// permute.hip: stable counting sort of n ids over G groups. groups = G drops ids outside
+// [0, G); groups = G + 1 makes them the last group. counts holds sort_count_words words;
+// slot_row may be null. tile_rows > 0 also cuts every group's run into tiles of that many
+// rows: tile_group [max_tiles] (-1 past the last tile) and tile_start [max_tiles].
+constexpr int kMaxGroups = HMOE_MAX_GROUPS;
+struct GroupSort {
+  const int32_t* ids;
+  int n, G, groups;
+  int32_t* counts;
+  int32_t* sorted;
+  int32_t* slot_row;
+  int32_t* off;
+  int tile_rows, max_tiles;
+  int32_t* tile_group;
+  int32_t* tile_start;
+};
+size_t sort_count_words(int n, int groups);
+hipError_t launch_sort(const GroupSort& g, hipStream_t s);
+
+// permute.hip: the row movements between token order and expert order (strides in
+// elements); up to kPermuteSmall ids one launch ranks and copies
+constexpr int kPermuteSmall = 1024;
+struct PermuteRows {
+  const void* src;
+  long src_stride;
+  void* dst;
+  long dst_stride;
+  const int32_t* slot_row;
+  int M, k, H;
+  int dtype, esize;
+};
+// whether M rows of `bytes` bytes fit one launch (2^24 blocks of 256 threads)
+bool row_grid_fits(long M, long bytes);
+hipError_t launch_permute(const PermuteRows& p, const int32_t* ids, int E, int32_t* sorted,
+                          int32_t* off, int32_t* counts, hipStream_t s);
+hipError_t launch_combine(const PermuteRows& p, const float* w, hipStream_t s);
+hipError_t launch_unpermute_bwd(const PermuteRows& p, const void* rows, long rows_stride,
+                                const float* w, float* dw, hipStream_t s);
+
+// lora.hip: adapters beside a shared projection
+constexpr int kMaxLoraRank = 128;
+struct Lora {
+  const uint16_t* x;        // [M, K], stride xs
+  long xs;
+  const int32_t* ids;       // [M]
+  const uint16_t* A;        // [G, r, K]
+  const uint16_t* B;        // [G, N, r]
+  const float* scale;       // [G]
+  int M, G, K, N, r;
+  const uint16_t* base;     // [M, N], stride bs; may be null
+  long bs;
+  uint16_t* y;              // [M, N], stride ys
+  long ys;
+  float* z;                 // [M, r]; may be null
+};
+struct LoraGrad {
+  const uint16_t* dy;       // [M, N]
+  long dys;
+  const uint16_t* x;        // [M, K]
+  long xs;
+  const float* z;           // [M, r]
+  const int32_t* ids;
+  const uint16_t* A;
+  const uint16_t* B;
+  const float* scale;
+  int M, G, K, N, r;
+  const uint16_t* dbase;    // [M, K]; may be null
+  long dbs;
+  uint16_t* dx;             // [M, K]
+  long dxs;
+  float* dA;                // [G, r, K]
+  float* dB;                // [G, N, r]
+};
+void lora_scratch(int M, int G, int K, int N, int r, size_t* forward, size_t* backward);
+hipError_t launch_lora(const Lora& p, void* scratch, hipStream_t s);
+hipError_t launch_lora_backward(const LoraGrad& p, void* scratch, hipStream_t s);
+
 // dequant.hip
 hipError_t launch_dequant(const Layer& L, const hmoe_weights& W, int expert, int tensor,
                           float* out_f32, uint16_t* out_bf16, hipStream_t s);

@@ -1,9 +1,11 @@
 // C ABI of libhmoe: layer creation and validation, the scratch planner, views into
-// scratch, and dispatch of the route / align / forward / dequant kernels.
+// scratch, and dispatch of the route / align / forward / dequant kernels and of the operators
+// around the experts (row movements, routing gradient, adapters).
 // Nothing here allocates, frees or synchronises device memory.
 #include <string.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <new>
 #include <string>
 
@@ -125,6 +127,85 @@ hmoe_status check_weights(const hmoe::Layer& L, const hmoe_weights* w) {
         !aligned(w->nf3_w2_s, 4))
       return fail(HMOE_ERR_ALIGN, "NF3-tier arrays: codes need 16-byte and scales 4-byte alignment");
   }
+  return HMOE_OK;
+}
+
+// ---- operators around the experts
+
+int element_size(int dtype) { return dtype == HMOE_DTYPE_FP32 ? 4 : 2; }
+
+hmoe_status check_permute_shape(int32_t M, int32_t k) {
+  if (M < 0) return fail(HMOE_ERR_INVALID_ARG, "M < 0");
+  if (k < 1 || k > hmoe::kMaxTopK) return fail(HMOE_ERR_INVALID_ARG, "k must be in [1, 16]");
+  if ((long)M * k > (1L << 24)) return fail(HMOE_ERR_UNSUPPORTED, "M * k > 2^24");
+  return HMOE_OK;
+}
+
+hmoe_status check_experts(int32_t E) {
+  if (E < 1 || E > hmoe::kMaxExperts) return fail(HMOE_ERR_INVALID_ARG, "E must be in [1, 1024]");
+  return HMOE_OK;
+}
+
+hmoe_status check_rows(int32_t M, int32_t H, int32_t dtype) {
+  if (H < 1) return fail(HMOE_ERR_INVALID_ARG, "H must be >= 1");
+  if (dtype != HMOE_DTYPE_BF16 && dtype != HMOE_DTYPE_FP16 && dtype != HMOE_DTYPE_FP32)
+    return fail(HMOE_ERR_INVALID_ARG, "unknown dtype");
+  if (!hmoe::row_grid_fits(M, (long)H * element_size(dtype)))
+    return fail(HMOE_ERR_UNSUPPORTED, "M rows of H elements are 2^24 blocks of 4 KiB or more");
+  return HMOE_OK;
+}
+
+// a matrix of rows: element-aligned, rows that do not overlap
+hmoe_status check_matrix(const char* name, const void* p, int64_t stride, int64_t cols, int esize) {
+  if (stride < cols)
+    return fail(HMOE_ERR_INVALID_ARG, std::string(name) + "'s row stride is below its row length");
+  if (stride > (int64_t(1) << 40))
+    return fail(HMOE_ERR_UNSUPPORTED, std::string(name) + "'s row stride is above 2^40");
+  if (!p || !aligned(p, esize))
+    return fail(HMOE_ERR_ALIGN, std::string(name) + " must be non-NULL and aligned to its elements");
+  return HMOE_OK;
+}
+
+hmoe_status check_arrays(const char* names, std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (!p || !aligned(p, 16))
+      return fail(HMOE_ERR_ALIGN, std::string(names) + " must be non-NULL and 16-byte aligned");
+  return HMOE_OK;
+}
+
+hmoe_status check_op_scratch(const void* scratch, size_t have, size_t need) {
+  if (have < need)
+    return fail(HMOE_ERR_SCRATCH, "scratch has " + std::to_string(have) + " bytes, needs " +
+                                      std::to_string(need));
+  if (need && (!scratch || !aligned(scratch, 256)))
+    return fail(HMOE_ERR_ALIGN, "scratch must be non-NULL and 256-byte aligned");
+  return HMOE_OK;
+}
+
+size_t permute_scratch(int32_t M, int32_t k, int32_t E) {
+  const int n = M * k;
+  return n <= hmoe::kPermuteSmall ? 0 : align256(hmoe::sort_count_words(n, E) * 4);
+}
+
+hmoe_status check_lora(int32_t M, int32_t G, int32_t K, int32_t N, int32_t rank) {
+  if (M < 0) return fail(HMOE_ERR_INVALID_ARG, "M < 0");
+  if (G < 1 || K < 1 || N < 1 || rank < 1)
+    return fail(HMOE_ERR_INVALID_ARG, "G, K, N and rank must be >= 1");
+  if (K % 8 || N % 8 || rank % 8)
+    return fail(HMOE_ERR_UNSUPPORTED, "K, N and rank must be multiples of 8");
+  if (rank > hmoe::kMaxLoraRank) return fail(HMOE_ERR_UNSUPPORTED, "rank > 128");
+  if (G > hmoe::kMaxGroups) return fail(HMOE_ERR_UNSUPPORTED, "G > 2048");
+  if (M > (1 << 22) || K > (1 << 20) || N > (1 << 20))
+    return fail(HMOE_ERR_UNSUPPORTED, "M > 2^22, or K or N > 2^20");
+  return HMOE_OK;
+}
+
+hmoe_status check_base(const char* name, const uint16_t* base, int64_t bs, const uint16_t* out,
+                       int64_t os, int64_t cols) {
+  if (!base) return HMOE_OK;
+  if (hmoe_status st = check_matrix(name, base, bs, cols, 2)) return st;
+  if (base == out && bs != os)
+    return fail(HMOE_ERR_INVALID_ARG, std::string(name) + " is the output itself with another stride");
   return HMOE_OK;
 }
 
@@ -530,6 +611,160 @@ hmoe_status moe_quantize_mxfp4(const float* in, int32_t rows, int32_t K, uint8_t
     return fail(HMOE_ERR_ALIGN, "in, codes and scales must be non-NULL, in and codes 16-byte aligned");
   hipError_t err = hmoe::launch_mx_quant(in, false, rows, K, nullptr, codes, scales, stream);
   if (err != hipSuccess) return hip_fail(err, "quantise launch");
+  return HMOE_OK;
+}
+
+hmoe_status moe_permute_scratch_bytes(int32_t M, int32_t k, int32_t E, size_t* bytes) {
+  if (hmoe_status st = check_permute_shape(M, k)) return st;
+  if (hmoe_status st = check_experts(E)) return st;
+  if (!bytes) return fail(HMOE_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = permute_scratch(M, k, E);
+  return HMOE_OK;
+}
+
+hmoe_status moe_permute(const void* x, int64_t x_stride, const int32_t* topk_ids, int32_t M,
+                        int32_t k, int32_t E, int32_t H, int32_t dtype, void* rows,
+                        int64_t rows_stride, int32_t* sorted_slots, int32_t* slot_row,
+                        int32_t* expert_off, void* scratch, size_t scratch_bytes,
+                        hipStream_t stream) {
+  if (hmoe_status st = check_permute_shape(M, k)) return st;
+  if (hmoe_status st = check_experts(E)) return st;
+  if (hmoe_status st = check_rows(M, H, dtype)) return st;
+  const int es = element_size(dtype);
+  if (hmoe_status st = check_arrays("expert_off", {expert_off})) return st;
+  if (M > 0) {
+    if (hmoe_status st = check_matrix("x", x, x_stride, H, es)) return st;
+    if (hmoe_status st = check_matrix("rows", rows, rows_stride, H, es)) return st;
+    if (hmoe_status st = check_arrays("topk_ids, sorted_slots and slot_row",
+                                      {topk_ids, sorted_slots, slot_row}))
+      return st;
+    if (hmoe_status st = check_op_scratch(scratch, scratch_bytes, permute_scratch(M, k, E))) return st;
+  }
+  const hmoe::PermuteRows p{x, x_stride, rows, rows_stride, slot_row, M, k, H, dtype, es};
+  hipError_t err = hmoe::launch_permute(p, topk_ids, E, sorted_slots, expert_off,
+                                        static_cast<int32_t*>(scratch), stream);
+  if (err != hipSuccess) return hip_fail(err, "permute launch");
+  return HMOE_OK;
+}
+
+hmoe_status moe_permute_backward(const void* drows, int64_t drows_stride, const int32_t* slot_row,
+                                 int32_t M, int32_t k, int32_t H, int32_t dtype, void* dx,
+                                 int64_t dx_stride, hipStream_t stream) {
+  if (hmoe_status st = check_permute_shape(M, k)) return st;
+  if (hmoe_status st = check_rows(M, H, dtype)) return st;
+  if (M == 0) return HMOE_OK;
+  const int es = element_size(dtype);
+  if (hmoe_status st = check_matrix("drows", drows, drows_stride, H, es)) return st;
+  if (hmoe_status st = check_matrix("dx", dx, dx_stride, H, es)) return st;
+  if (hmoe_status st = check_arrays("slot_row", {slot_row})) return st;
+  const hmoe::PermuteRows p{drows, drows_stride, dx, dx_stride, slot_row, M, k, H, dtype, es};
+  hipError_t err = hmoe::launch_combine(p, nullptr, stream);
+  if (err != hipSuccess) return hip_fail(err, "permute backward launch");
+  return HMOE_OK;
+}
+
+hmoe_status moe_unpermute(const void* rows, int64_t rows_stride, const int32_t* slot_row,
+                          const float* topk_w, int32_t M, int32_t k, int32_t H, int32_t dtype,
+                          void* y, int64_t y_stride, hipStream_t stream) {
+  if (hmoe_status st = check_permute_shape(M, k)) return st;
+  if (hmoe_status st = check_rows(M, H, dtype)) return st;
+  if (M == 0) return HMOE_OK;
+  const int es = element_size(dtype);
+  if (hmoe_status st = check_matrix("rows", rows, rows_stride, H, es)) return st;
+  if (hmoe_status st = check_matrix("y", y, y_stride, H, es)) return st;
+  if (hmoe_status st = check_arrays("slot_row and topk_w", {slot_row, topk_w})) return st;
+  const hmoe::PermuteRows p{rows, rows_stride, y, y_stride, slot_row, M, k, H, dtype, es};
+  hipError_t err = hmoe::launch_combine(p, topk_w, stream);
+  if (err != hipSuccess) return hip_fail(err, "unpermute launch");
+  return HMOE_OK;
+}
+
+hmoe_status moe_unpermute_backward(const void* dy, int64_t dy_stride, const void* rows,
+                                   int64_t rows_stride, const int32_t* slot_row,
+                                   const float* topk_w, int32_t M, int32_t k, int32_t H,
+                                   int32_t dtype, void* drows, int64_t drows_stride, float* dw,
+                                   hipStream_t stream) {
+  if (hmoe_status st = check_permute_shape(M, k)) return st;
+  if (hmoe_status st = check_rows(M, H, dtype)) return st;
+  if (M == 0) return HMOE_OK;
+  const int es = element_size(dtype);
+  if (hmoe_status st = check_matrix("dy", dy, dy_stride, H, es)) return st;
+  if (hmoe_status st = check_matrix("rows", rows, rows_stride, H, es)) return st;
+  if (hmoe_status st = check_matrix("drows", drows, drows_stride, H, es)) return st;
+  if (hmoe_status st = check_arrays("slot_row, topk_w and dw", {slot_row, topk_w, dw})) return st;
+  const hmoe::PermuteRows p{dy, dy_stride, drows, drows_stride, slot_row, M, k, H, dtype, es};
+  hipError_t err = hmoe::launch_unpermute_bwd(p, rows, rows_stride, topk_w, dw, stream);
+  if (err != hipSuccess) return hip_fail(err, "unpermute backward launch");
+  return HMOE_OK;
+}
+
+hmoe_status moe_route_backward(const int32_t* topk_ids, const float* topk_w, const float* dw,
+                               int32_t M, int32_t E, int32_t k, float* dlogits,
+                               hipStream_t stream) {
+  if (M < 0) return fail(HMOE_ERR_INVALID_ARG, "M < 0");
+  if (hmoe_status st = check_experts(E)) return st;
+  if (k < 1 || k > std::min(hmoe::kMaxTopK, (int)E))
+    return fail(HMOE_ERR_INVALID_ARG, "k must be in [1, min(16, E)]");
+  if (M == 0) return HMOE_OK;
+  if (hmoe_status st = check_arrays("topk_ids, topk_w, dw and dlogits", {topk_ids, topk_w, dw, dlogits}))
+    return st;
+  hipError_t err = hmoe::launch_route_backward(topk_ids, topk_w, dw, M, E, k, dlogits, stream);
+  if (err != hipSuccess) return hip_fail(err, "route backward launch");
+  return HMOE_OK;
+}
+
+hmoe_status moe_lora_scratch_bytes(int32_t M, int32_t G, int32_t K, int32_t N, int32_t rank,
+                                   size_t* forward_bytes, size_t* backward_bytes) {
+  if (hmoe_status st = check_lora(M, G, K, N, rank)) return st;
+  if (!forward_bytes || !backward_bytes) return fail(HMOE_ERR_INVALID_ARG, "bytes is NULL");
+  hmoe::lora_scratch(M, G, K, N, rank, forward_bytes, backward_bytes);
+  return HMOE_OK;
+}
+
+hmoe_status moe_lora(const uint16_t* x, int64_t x_stride, const int32_t* ids, const uint16_t* A,
+                     const uint16_t* B, const float* scale, int32_t M, int32_t G, int32_t K,
+                     int32_t N, int32_t rank, const uint16_t* base, int64_t base_stride,
+                     uint16_t* y, int64_t y_stride, float* z, void* scratch, size_t scratch_bytes,
+                     hipStream_t stream) {
+  if (hmoe_status st = check_lora(M, G, K, N, rank)) return st;
+  if (M == 0) return HMOE_OK;
+  if (hmoe_status st = check_matrix("x", x, x_stride, K, 2)) return st;
+  if (hmoe_status st = check_matrix("y", y, y_stride, N, 2)) return st;
+  if (hmoe_status st = check_base("base", base, base_stride, y, y_stride, N)) return st;
+  if (hmoe_status st = check_arrays("ids, A, B and scale", {ids, A, B, scale})) return st;
+  if (!aligned(z, 16)) return fail(HMOE_ERR_ALIGN, "z must be 16-byte aligned");
+  size_t need, back;
+  hmoe::lora_scratch(M, G, K, N, rank, &need, &back);
+  if (hmoe_status st = check_op_scratch(scratch, scratch_bytes, need)) return st;
+  const hmoe::Lora p{x, x_stride, ids, A, B, scale, M, G, K, N, rank, base, base_stride, y, y_stride, z};
+  hipError_t err = hmoe::launch_lora(p, scratch, stream);
+  if (err != hipSuccess) return hip_fail(err, "adapter launch");
+  return HMOE_OK;
+}
+
+hmoe_status moe_lora_backward(const uint16_t* dy, int64_t dy_stride, const uint16_t* x,
+                              int64_t x_stride, const float* z, const int32_t* ids,
+                              const uint16_t* A, const uint16_t* B, const float* scale, int32_t M,
+                              int32_t G, int32_t K, int32_t N, int32_t rank,
+                              const uint16_t* dbase, int64_t dbase_stride, uint16_t* dx,
+                              int64_t dx_stride, float* dA, float* dB, void* scratch,
+                              size_t scratch_bytes, hipStream_t stream) {
+  if (hmoe_status st = check_lora(M, G, K, N, rank)) return st;
+  if (hmoe_status st = check_arrays("A, B, scale, dA and dB", {A, B, scale, dA, dB})) return st;
+  if (M > 0) {
+    if (hmoe_status st = check_matrix("dy", dy, dy_stride, N, 2)) return st;
+    if (hmoe_status st = check_matrix("x", x, x_stride, K, 2)) return st;
+    if (hmoe_status st = check_matrix("dx", dx, dx_stride, K, 2)) return st;
+    if (hmoe_status st = check_base("dbase", dbase, dbase_stride, dx, dx_stride, K)) return st;
+    if (hmoe_status st = check_arrays("ids and z", {ids, z})) return st;
+  }
+  size_t forward, need;
+  hmoe::lora_scratch(M, G, K, N, rank, &forward, &need);
+  if (hmoe_status st = check_op_scratch(scratch, scratch_bytes, need)) return st;
+  const hmoe::LoraGrad p{dy, dy_stride, x, x_stride, z, ids, A, B, scale, M, G, K, N, rank,
+                         dbase, dbase_stride, dx, dx_stride, dA, dB};
+  hipError_t err = hmoe::launch_lora_backward(p, scratch, stream);
+  if (err != hipSuccess) return hip_fail(err, "adapter backward launch");
   return HMOE_OK;
 }
 

@@ -1,0 +1,602 @@
+// Tokens into expert order and back: a stable counting sort of the (token, rank) slots by
+// expert, the copy of every token's row to its slots' places (moe_permute), the weighted sum
+// of the slots' rows back into tokens (moe_unpermute), and both gradients. All of it is bound
+// by memory: nothing is computed on a row but one multiply-add per element, so each kernel
+// touches every row once with 16-byte accesses and keeps its sums in fp32 registers.
+//
+// Rows are addressed with the strides the caller gives. gfx950 reads and writes 16 bytes at
+// element alignment, so odd widths and strides take the same instructions as aligned ones;
+// only the last, partial vector of a row goes element by element.
+#include <limits.h>
+
+#include <algorithm>
+
+#include "device_common.h"
+#include "hmoe_internal.h"
+
+namespace hmoe {
+
+// ---------------------------------------------------------------------------
+// counting sort of n ids over G groups
+// ---------------------------------------------------------------------------
+
+constexpr int kSortThreads = 256;
+constexpr int kSortWaves = kSortThreads / kWave;
+// s_waitcnt operand waiting for LDS only (vmcnt 63, expcnt 7, lgkmcnt 0)
+constexpr int kSortWaitLds = 0xC07F;
+
+struct SortArgs {
+  const int32_t* ids;
+  int n, G;
+  int groups;           // G, or G + 1 when ids outside [0, G) form a group of their own
+  int chunk;            // ids per block
+  int nb;               // blocks
+  int32_t* counts;      // [nb, groups] (nb > 1)
+  int32_t* sorted;
+  int32_t* slot_row;    // may be null
+  int32_t* off;         // [groups + 1]
+  int tile_rows;        // rows per tile of the tile table (0: no table)
+  int max_tiles;
+  int32_t* tile_group;
+  int32_t* tile_start;
+};
+
+// group of an id: ids outside [0, G) are dropped (-1) or the group behind the last
+__device__ __forceinline__ int sort_key(int id, int G, int groups) {
+  return (unsigned)id < (unsigned)G ? id : (groups > G ? G : -1);
+}
+
+// inclusive sum over the block of one value per thread; *total: the block's sum
+__device__ __forceinline__ int block_scan(int v, int* s_part, int* total) {
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const int u = __shfl_up(v, o);
+    if (lane >= o) v += u;
+  }
+  __syncthreads();
+  if (lane == kWave - 1) s_part[wave] = v;
+  __syncthreads();
+  int add = 0, sum = 0;
+#pragma unroll
+  for (int w = 0; w < kSortWaves; ++w) {
+    const int p = s_part[w];
+    if (w < wave) add += p;
+    sum += p;
+  }
+  *total = sum;
+  return v + add;
+}
+
+// per-block group counts of a sort over several blocks
+__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
+  __shared__ int32_t s_cnt[kMaxGroups + 1];
+  for (int e = threadIdx.x; e < a.groups; e += kSortThreads) s_cnt[e] = 0;
+  __syncthreads();
+  const int c0 = min((long)blockIdx.x * a.chunk, (long)a.n), c1 = min(c0 + (long)a.chunk, (long)a.n);
+  for (int s = c0 + (int)threadIdx.x; s < c1; s += kSortThreads) {
+    const int e = sort_key(a.ids[s], a.G, a.groups);
+    if (e >= 0) atomicAdd(&s_cnt[e], 1);
+  }
+  __syncthreads();
+  int32_t* out = a.counts + (size_t)blockIdx.x * a.groups;
+  for (int e = threadIdx.x; e < a.groups; e += kSortThreads) out[e] = s_cnt[e];
+}
+
+// Places one block's chunk: every wave owns a contiguous part of it, so the order is that
+// of a serial counting sort whatever the timing. With one block the counts are its own;
+// else each block sums the count table of all blocks (read from L2).
+__global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
+  __shared__ int32_t s_w[kSortWaves][kMaxGroups + 1];  // per-wave counts, then positions
+  __shared__ int32_t s_base[kMaxGroups + 1];           // this block's first position per group
+  __shared__ int32_t s_tile[kMaxGroups + 2];           // exclusive tile counts
+  __shared__ int32_t s_part[kSortWaves];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid >> 6;
+  const int c0 = min((long)blockIdx.x * a.chunk, (long)a.n), c1 = min(c0 + (long)a.chunk, (long)a.n);
+  const int part = ((c1 - c0 + kSortThreads - 1) / kSortThreads) * kWave;  // ids per wave
+  const int w0 = min(c0 + wave * part, c1), w1 = min(w0 + part, c1);
+  for (int e = tid; e < a.groups; e += kSortThreads)
+    for (int w = 0; w < kSortWaves; ++w) s_w[w][e] = 0;
+  __syncthreads();
+  for (int s = w0 + lane; s < w1; s += kWave) {
+    const int e = sort_key(a.ids[s], a.G, a.groups);
+    if (e >= 0) atomicAdd(&s_w[wave][e], 1);
+  }
+  __syncthreads();
+  int placed = 0, tiles = 0;
+  for (int e0 = 0; e0 < a.groups; e0 += kSortThreads) {
+    const int e = e0 + tid;
+    int tot = 0, before = 0;
+    if (e < a.groups) {
+      if (a.nb == 1) {
+        for (int w = 0; w < kSortWaves; ++w) tot += s_w[w][e];
+      } else {
+        for (int b = 0; b < a.nb; ++b) {
+          const int c = a.counts[(size_t)b * a.groups + e];
+          tot += c;
+          if (b < (int)blockIdx.x) before += c;
+        }
+      }
+    }
+    int sum;
+    const int excl = placed + block_scan(tot, s_part, &sum) - tot;
+    placed += sum;
+    if (e < a.groups) {
+      int run = excl + before;
+      for (int w = 0; w < kSortWaves; ++w) {
+        const int c = s_w[w][e];
+        s_w[w][e] = run;
+        run += c;
+      }
+      if (blockIdx.x == 0) a.off[e] = excl;
+    }
+    if (a.tile_rows) {
+      const int nt = (tot + a.tile_rows - 1) / a.tile_rows;
+      const int tx = tiles + block_scan(nt, s_part, &sum) - nt;
+      tiles += sum;
+      if (e < a.groups) {
+        s_tile[e] = tx;
+        s_base[e] = excl;
+      }
+    }
+  }
+  if (blockIdx.x == 0 && tid == 0) a.off[a.groups] = placed;
+  __syncthreads();
+  const int gid = blockIdx.x * kSortThreads + tid, gsz = gridDim.x * kSortThreads;
+  for (int i = placed + gid; i < a.n; i += gsz) a.sorted[i] = -1;
+  if (a.tile_rows) {
+    // tile t belongs to the last group whose first tile is at or before t
+    for (int t = gid; t < a.max_tiles; t += gsz) {
+      int lo = 0, hi = a.groups - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_tile[mid] <= t) lo = mid; else hi = mid - 1;
+      }
+      const bool live = t < tiles;
+      a.tile_group[t] = live ? lo : -1;
+      a.tile_start[t] = live ? s_base[lo] + (t - s_tile[lo]) * a.tile_rows : 0;
+    }
+  }
+  int idbits = 1;
+  while ((1 << idbits) < a.groups) ++idbits;
+  for (int b0 = w0; b0 < w1; b0 += kWave) {
+    const int s = b0 + lane;
+    const int e0 = s < w1 ? sort_key(a.ids[s], a.G, a.groups) : -1;
+    const int e = max(e0, 0);
+    uint64_t m = __ballot(e0 >= 0);
+    for (int b = 0; b < idbits; ++b) {
+      const bool bit = (e >> b) & 1;
+      const uint64_t bb = __ballot(bit);
+      m &= bit ? bb : ~bb;
+    }
+    const int rank = __popcll(m & ((1ull << lane) - 1ull));
+    const int cnt = __popcll(m);
+    int pos = -1;
+    if (e0 >= 0) pos = s_w[wave][e] + rank;
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_s_waitcnt(kSortWaitLds);
+    if (e0 >= 0) {
+      a.sorted[pos] = s;
+      if (rank == cnt - 1) s_w[wave][e] += cnt;
+    }
+    if (a.slot_row && s < w1) a.slot_row[s] = pos;
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_s_waitcnt(kSortWaitLds);
+  }
+}
+
+// Blocks of a sort: 512 ids each, fewer and larger blocks where the count table that every
+// block reads (blocks * groups entries) would grow past 64 K entries.
+int sort_blocks(int n, int groups) {
+  const int want = (n + 511) / 512, cap = std::max(1, (1 << 16) / groups);
+  if (n <= 2048) return 1;
+  return std::min({want, cap, 256});
+}
+
+size_t sort_count_words(int n, int groups) {
+  const int nb = sort_blocks(n, groups);
+  return nb > 1 ? (size_t)nb * groups : 0;
+}
+
+hipError_t launch_sort(const GroupSort& g, hipStream_t s) {
+  SortArgs a{};
+  a.ids = g.ids;
+  a.n = g.n;
+  a.G = g.G;
+  a.groups = g.groups;
+  a.nb = sort_blocks(g.n, g.groups);
+  a.chunk = ((g.n + a.nb - 1) / a.nb + kSortThreads - 1) / kSortThreads * kSortThreads;
+  a.counts = g.counts;
+  a.sorted = g.sorted;
+  a.slot_row = g.slot_row;
+  a.off = g.off;
+  a.tile_rows = g.tile_rows;
+  a.max_tiles = g.max_tiles;
+  a.tile_group = g.tile_group;
+  a.tile_start = g.tile_start;
+  if (a.nb > 1) hipLaunchKernelGGL(sort_count_kernel, dim3(a.nb), dim3(kSortThreads), 0, s, a);
+  hipLaunchKernelGGL(sort_place_kernel, dim3(a.nb), dim3(kSortThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// rows
+// ---------------------------------------------------------------------------
+
+constexpr int kRowThreads = 256;
+
+// 16 bytes at element alignment
+struct __attribute__((packed, aligned(2))) Raw16 {
+  uint32_t w[4];
+};
+
+// element types of the rows: conversion of one 16-byte vector and of one element
+struct Bf16 {
+  static constexpr int kSize = 2, kVec = 8;
+  static __device__ __forceinline__ void unpack(const Raw16& v, float* f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = bf16_lo(v.w[i]);
+      f[2 * i + 1] = bf16_hi(v.w[i]);
+    }
+  }
+  static __device__ __forceinline__ Raw16 pack(const float* f) {
+    Raw16 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v.w[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
+    return v;
+  }
+  static __device__ __forceinline__ float load(const char* p) {
+    return bf16_lo(*reinterpret_cast<const uint16_t*>(p));
+  }
+  static __device__ __forceinline__ void store(char* p, float f) {
+    *reinterpret_cast<uint16_t*>(p) = (uint16_t)pack_bf16(f, 0.f);
+  }
+};
+
+struct Fp16 {
+  static constexpr int kSize = 2, kVec = 8;
+  static __device__ __forceinline__ void unpack(const Raw16& v, float* f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f16x2 h = __builtin_bit_cast(f16x2, v.w[i]);
+      f[2 * i] = (float)h[0];
+      f[2 * i + 1] = (float)h[1];
+    }
+  }
+  static __device__ __forceinline__ Raw16 pack(const float* f) {
+    Raw16 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v.w[i] = pack_f16(f[2 * i], f[2 * i + 1]);
+    return v;
+  }
+  static __device__ __forceinline__ float load(const char* p) {
+    return fp16_to_f32(*reinterpret_cast<const uint16_t*>(p));
+  }
+  static __device__ __forceinline__ void store(char* p, float f) {
+    *reinterpret_cast<uint16_t*>(p) = (uint16_t)pack_f16(f, 0.f);
+  }
+};
+
+struct Fp32 {
+  static constexpr int kSize = 4, kVec = 4;
+  static __device__ __forceinline__ void unpack(const Raw16& v, float* f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(v.w[i]);
+  }
+  static __device__ __forceinline__ Raw16 pack(const float* f) {
+    Raw16 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v.w[i] = __float_as_uint(f[i]);
+    return v;
+  }
+  static __device__ __forceinline__ float load(const char* p) { return *reinterpret_cast<const float*>(p); }
+  static __device__ __forceinline__ void store(char* p, float f) { *reinterpret_cast<float*>(p) = f; }
+};
+
+// Blocks of a row kernel: `chunks` blocks of 256 threads a token, 16 bytes a thread, on one
+// grid axis (block b: token b / chunks, bytes from (b % chunks) * 4096)
+struct RowPlace {
+  int t;
+  long at;
+};
+__device__ __forceinline__ RowPlace row_place(int chunks) {
+  const int t = blockIdx.x / (unsigned)chunks;
+  return {t, ((long)(blockIdx.x - t * chunks) * kRowThreads + threadIdx.x) * 16};
+}
+
+// the bytes [at, at + 16) of a row of `bytes` bytes; a row's last, partial vector is read
+// and written two bytes at a time (rows are whole elements of 2 or 4 bytes)
+__device__ __forceinline__ Raw16 load_raw(const char* row, long at, long bytes) {
+  Raw16 v{};
+  if (at + 16 <= bytes) {
+    v = *reinterpret_cast<const Raw16*>(row + at);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (at + 2 * i < bytes)
+        v.w[i >> 1] |= (uint32_t)*reinterpret_cast<const uint16_t*>(row + at + 2 * i) << (16 * (i & 1));
+  }
+  return v;
+}
+
+__device__ __forceinline__ void store_raw(char* row, long at, long bytes, const Raw16& v) {
+  if (at + 16 <= bytes) {
+    *reinterpret_cast<Raw16*>(row + at) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (at + 2 * i < bytes)
+        *reinterpret_cast<uint16_t*>(row + at + 2 * i) = (uint16_t)(v.w[i >> 1] >> (16 * (i & 1)));
+  }
+}
+
+// Copies each token's row to its slots' places: x is read once, every row written once.
+__global__ __launch_bounds__(kRowThreads) void permute_copy_kernel(
+    const char* __restrict__ x, long xs, const int32_t* __restrict__ slot_row, int k, int chunks,
+    long bytes, char* __restrict__ rows, long rs) {
+  const auto [tok, at] = row_place(chunks);
+  const long t = tok;
+  if (at >= bytes) return;
+  const Raw16 v = load_raw(x + t * xs, at, bytes);
+  for (int j = 0; j < k; ++j) {
+    const int r = slot_row[t * k + j];
+    if (r >= 0) store_raw(rows + (long)r * rs, at, bytes, v);
+  }
+}
+
+struct PermuteSmallArgs {
+  const char* x;
+  long xs;
+  const int32_t* ids;
+  int M, k, E, chunks;
+  long bytes;
+  char* rows;
+  long rs;
+  int32_t* sorted;
+  int32_t* slot_row;
+  int32_t* off;
+};
+
+// The whole permutation in one launch, for few ids: every block ranks its own token's slots
+// against all ids (16 lanes a slot: how many ids lie before it in the sorted order) while
+// its part of the token's row is on the way. One more block writes the offsets.
+__global__ __launch_bounds__(kRowThreads) void permute_small_kernel(PermuteSmallArgs a) {
+  __shared__ int32_t s_id[kPermuteSmall];
+  __shared__ int32_t s_cnt[kMaxExperts];
+  __shared__ int32_t s_row[kMaxTopK];
+  __shared__ int32_t s_part[kSortWaves];
+  const int tid = threadIdx.x, n = a.M * a.k;
+  const auto [t, at] = row_place(a.chunks);
+  const bool first = at < kRowThreads * 16;  // the token's first block
+  if (t == a.M) {  // offsets and the end of sorted_slots
+    for (int e = tid; e < a.E; e += kRowThreads) s_cnt[e] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += kRowThreads) {
+      const int e = a.ids[i];
+      if ((unsigned)e < (unsigned)a.E) atomicAdd(&s_cnt[e], 1);
+    }
+    __syncthreads();
+    int placed = 0;
+    for (int e0 = 0; e0 < a.E; e0 += kRowThreads) {
+      const int e = e0 + tid;
+      const int c = e < a.E ? s_cnt[e] : 0;
+      int sum;
+      const int incl = placed + block_scan(c, s_part, &sum);
+      placed += sum;
+      if (e < a.E) a.off[e] = incl - c;
+    }
+    if (tid == 0) a.off[a.E] = placed;
+    for (int i = placed + tid; i < n; i += kRowThreads) a.sorted[i] = -1;
+    return;
+  }
+  Raw16 v{};
+  if (at < a.bytes) v = load_raw(a.x + t * a.xs, at, a.bytes);
+  for (int i = tid; i < n; i += kRowThreads) {
+    const int e = a.ids[i];
+    s_id[i] = (unsigned)e < (unsigned)a.E ? e : INT_MAX;
+  }
+  __syncthreads();
+  const int j = tid >> 4;
+  if (j < a.k) {
+    const int s = t * a.k + j, e = s_id[s];
+    int before = 0;
+    for (int i = tid & 15; i < n; i += 16) before += s_id[i] < e || (s_id[i] == e && i < s);
+    before += xlane_i<8>(before);
+    before += xlane_i<4>(before);
+    before += xlane_i<2>(before);
+    before += xlane_i<1>(before);
+    if ((tid & 15) == 0) {
+      const int r = e != INT_MAX ? before : -1;
+      s_row[j] = r;
+      if (first) {
+        a.slot_row[s] = r;
+        if (r >= 0) a.sorted[r] = s;
+      }
+    }
+  }
+  __syncthreads();
+  if (at < a.bytes)
+    for (int q = 0; q < a.k; ++q) {
+      const int r = s_row[q];
+      if (r >= 0) store_raw(a.rows + (long)r * a.rs, at, a.bytes, v);
+    }
+}
+
+struct CombineArgs {
+  const char* rows;
+  long rs;
+  const int32_t* slot_row;
+  const float* w;   // null: plain sums (the gradient of the permutation)
+  int k, n, chunks;
+  long bytes;
+  char* y;
+  long ys;
+};
+
+// y[t] = sum_j w[t, j] * rows[slot_row[t, j]] in fp32, j ascending, rounded once. A thread
+// owns one 16-byte column of one token; the loads of up to eight rows are issued together
+// before the first is used, which is what keeps enough bytes in flight.
+template <typename T>
+__global__ __launch_bounds__(kRowThreads) void combine_kernel(CombineArgs a) {
+  constexpr int kBatch = 8;
+  const auto [tok, at] = row_place(a.chunks);
+  const long t = tok;
+  if (at >= a.bytes) return;
+  float acc[T::kVec] = {};
+  for (int j0 = 0; j0 < a.k; j0 += kBatch) {
+    Raw16 v[kBatch];
+    int r[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      r[i] = j0 + i < a.k ? a.slot_row[t * a.k + j0 + i] : -1;
+      if ((unsigned)r[i] < (unsigned)a.n) v[i] = load_raw(a.rows + (long)r[i] * a.rs, at, a.bytes);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if ((unsigned)r[i] < (unsigned)a.n) {
+        const float w = a.w ? a.w[t * a.k + j0 + i] : 1.f;
+        float f[T::kVec];
+        T::unpack(v[i], f);
+#pragma unroll
+        for (int q = 0; q < T::kVec; ++q) acc[q] = fmaf(w, f[q], acc[q]);
+      }
+  }
+  store_raw(a.y + t * a.ys, at, a.bytes, T::pack(acc));
+}
+
+struct UnpermuteBwdArgs {
+  const char* dy;
+  long dys;
+  const char* rows;
+  long rs;
+  const int32_t* slot_row;
+  const float* w;
+  int k, n;
+  long bytes;
+  char* drows;
+  long drs;
+  float* dw;
+};
+
+// drows[slot_row[t, j]] = w[t, j] * dy[t] and dw[t, j] = <dy[t], rows[slot_row[t, j]]>: one
+// block a token, so dy is read once and the dot products of all its slots stay in registers
+// until the row's end.
+template <typename T, int KM>
+__global__ __launch_bounds__(kRowThreads) void unpermute_bwd_kernel(UnpermuteBwdArgs a) {
+  __shared__ float s_dot[kRowThreads / kWave][KM];
+  const long t = blockIdx.x;
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
+  int r[KM];
+  float w[KM], dot[KM];
+#pragma unroll
+  for (int j = 0; j < KM; ++j) {
+    const int v = j < a.k ? a.slot_row[t * a.k + j] : -1;
+    r[j] = (unsigned)v < (unsigned)a.n ? v : -1;
+    w[j] = j < a.k ? a.w[t * a.k + j] : 0.f;
+    dot[j] = 0.f;
+  }
+  for (long at = threadIdx.x * 16; at < a.bytes; at += (long)blockDim.x * 16) {
+    Raw16 v[KM];
+    const Raw16 dv = load_raw(a.dy + t * a.dys, at, a.bytes);
+#pragma unroll
+    for (int j = 0; j < KM; ++j)
+      if (r[j] >= 0) v[j] = load_raw(a.rows + (long)r[j] * a.rs, at, a.bytes);
+    float d[T::kVec];
+    T::unpack(dv, d);
+#pragma unroll
+    for (int j = 0; j < KM; ++j)
+      if (r[j] >= 0) {
+        float f[T::kVec], g[T::kVec];
+        T::unpack(v[j], f);
+#pragma unroll
+        for (int q = 0; q < T::kVec; ++q) {
+          dot[j] = fmaf(d[q], f[q], dot[j]);
+          g[q] = w[j] * d[q];
+        }
+        store_raw(a.drows + (long)r[j] * a.drs, at, a.bytes, T::pack(g));
+      }
+  }
+#pragma unroll
+  for (int j = 0; j < KM; ++j) {
+    const float s = group_sum<64>(dot[j]);
+    if (lane == 0) s_dot[wave][j] = s;
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < a.k) {
+    float s = 0.f;
+    for (int i = 0; i < (int)blockDim.x / kWave; ++i) s += s_dot[i][threadIdx.x];
+    a.dw[t * a.k + threadIdx.x] = s;
+  }
+}
+
+template <typename F>
+static hipError_t by_type(int dtype, F f) {
+  switch (dtype) {
+    case HMOE_DTYPE_BF16: f(Bf16{}); break;
+    case HMOE_DTYPE_FP16: f(Fp16{}); break;
+    default: f(Fp32{}); break;
+  }
+  return hipGetLastError();
+}
+
+static int row_chunks(long bytes) { return (int)((bytes + kRowThreads * 16 - 1) / (kRowThreads * 16)); }
+
+bool row_grid_fits(long M, long bytes) {
+  return (M + 1) * ((bytes + kRowThreads * 16 - 1) / (kRowThreads * 16)) < (1L << 24);
+}
+
+hipError_t launch_permute(const PermuteRows& p, const int32_t* ids, int E, int32_t* sorted,
+                          int32_t* off, int32_t* counts, hipStream_t s) {
+  const long n = (long)p.M * p.k, bytes = (long)p.H * p.esize;
+  const int chunks = row_chunks(bytes);
+  if (n <= kPermuteSmall && E <= kMaxExperts) {
+    PermuteSmallArgs a{(const char*)p.src, p.src_stride * p.esize, ids, p.M, p.k, E, chunks, bytes,
+                       (char*)p.dst, p.dst_stride * p.esize, sorted, const_cast<int32_t*>(p.slot_row), off};
+    hipLaunchKernelGGL(permute_small_kernel, dim3(p.M * chunks + 1), dim3(kRowThreads), 0, s, a);
+    return hipGetLastError();
+  }
+  GroupSort g{};
+  g.ids = ids;
+  g.n = (int)n;
+  g.G = g.groups = E;
+  g.counts = counts;
+  g.sorted = sorted;
+  g.slot_row = const_cast<int32_t*>(p.slot_row);
+  g.off = off;
+  hipError_t err = launch_sort(g, s);
+  if (err != hipSuccess) return err;
+  hipLaunchKernelGGL(permute_copy_kernel, dim3(p.M * chunks), dim3(kRowThreads), 0, s,
+                     (const char*)p.src, p.src_stride * p.esize, p.slot_row, p.k, chunks, bytes, (char*)p.dst,
+                     p.dst_stride * p.esize);
+  return hipGetLastError();
+}
+
+hipError_t launch_combine(const PermuteRows& p, const float* w, hipStream_t s) {
+  const long bytes = (long)p.H * p.esize;
+  const int chunks = row_chunks(bytes);
+  CombineArgs a{(const char*)p.src, p.src_stride * p.esize, p.slot_row, w, p.k, p.M * p.k, chunks,
+                bytes, (char*)p.dst, p.dst_stride * p.esize};
+  return by_type(p.dtype, [&](auto t) {
+    hipLaunchKernelGGL(combine_kernel<decltype(t)>, dim3(p.M * chunks), dim3(kRowThreads), 0, s, a);
+  });
+}
+
+hipError_t launch_unpermute_bwd(const PermuteRows& p, const void* rows, long rows_stride,
+                                const float* w, float* dw, hipStream_t s) {
+  const long bytes = (long)p.H * p.esize;
+  UnpermuteBwdArgs a{(const char*)p.src, p.src_stride * p.esize, (const char*)rows,
+                     rows_stride * p.esize, p.slot_row, w, p.k, p.M * p.k, bytes, (char*)p.dst,
+                     p.dst_stride * p.esize, dw};
+  // threads: one 16-byte vector each up to 256
+  const int threads = bytes > 2048 ? 256 : bytes > 1024 ? 128 : 64;
+  return by_type(p.dtype, [&](auto t) {
+    using T = decltype(t);
+    if (p.k <= 8)
+      hipLaunchKernelGGL((unpermute_bwd_kernel<T, 8>), dim3(p.M), dim3(threads), 0, s, a);
+    else
+      hipLaunchKernelGGL((unpermute_bwd_kernel<T, kMaxTopK>), dim3(p.M), dim3(threads), 0, s, a);
+  });
+}
+
+}  // namespace hmoe

@@ -84,6 +84,64 @@ hipError_t launch_route_group(const Layer& L, const float* logits, int M, void* 
   return hipGetLastError();
 }
 
+// Gradient of the renormalised top-k weights: w = softmax over the selected logits, so
+// dl[e_j] = w_j (dw_j - sum_i w_i dw_i) and every other logit's gradient is zero. One wave
+// a token writes the whole row of E logits, four a lane, each picking its slots' values by
+// comparing ids: no zero fill before, no scatter, no order to depend on. Bound by the
+// M * E * 4 bytes it writes.
+struct __attribute__((packed, aligned(4))) F32x4 {
+  float v[4];
+};
+
+template <int KM>
+__global__ __launch_bounds__(kRouteWaves * kWave) void route_bwd_kernel(
+    const int32_t* __restrict__ ids, const float* __restrict__ w, const float* __restrict__ dw,
+    int M, int E, int k, float* __restrict__ dl) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const long t = blockIdx.x * (long)kRouteWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (t >= M) return;
+  int id[KM];
+  float g[KM], d[KM], sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < KM; ++j) {
+    id[j] = j < k ? ids[t * k + j] : -1;
+    g[j] = j < k ? w[t * k + j] : 0.f;
+    d[j] = j < k ? dw[t * k + j] : 0.f;
+    if (j < k) sum = fmaf(g[j], d[j], sum);
+  }
+#pragma unroll
+  for (int j = 0; j < KM; ++j) g[j] *= d[j] - sum;
+  float* row = dl + t * E;
+  for (int e = lane * 4; e < E; e += kWave * 4) {
+    F32x4 o;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float v = 0.f;
+#pragma unroll
+      for (int j = 0; j < KM; ++j) v += id[j] == e + q ? g[j] : 0.f;
+      o.v[q] = v;
+    }
+    if (e + 4 <= E) {
+      *reinterpret_cast<F32x4*>(row + e) = o;
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (e + q < E) row[e + q] = o.v[q];
+    }
+  }
+}
+
+hipError_t launch_route_backward(const int32_t* ids, const float* w, const float* dw, int M, int E,
+                                 int k, float* dlogits, hipStream_t s) {
+  if (M == 0) return hipSuccess;
+  const dim3 grid((M + kRouteWaves - 1) / kRouteWaves), block(kRouteWaves * kWave);
+  if (k <= 8)
+    hipLaunchKernelGGL(route_bwd_kernel<8>, grid, block, 0, s, ids, w, dw, M, E, k, dlogits);
+  else
+    hipLaunchKernelGGL(route_bwd_kernel<kMaxTopK>, grid, block, 0, s, ids, w, dw, M, E, k, dlogits);
+  return hipGetLastError();
+}
+
 TierMask make_tier_mask(const Layer& L) {
   TierMask m;
   for (int i = 0; i < kMaxExperts / 32; ++i) m.w[i] = L.nf3_mask[i];
