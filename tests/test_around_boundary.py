@@ -29,8 +29,8 @@ def _permute(M=4, k=2, E=8, H=16, dtype=0, x=A, xs=16, ids=A, rows=A, rs=16, srt
     ({"xs": 1 << 41}, UNSUPPORTED),
     ({"x": None}, ALIGN), ({"x": A + 1}, ALIGN), ({"dtype": 2, "x": A + 2}, ALIGN), ({"rows": None}, ALIGN),
     ({"ids": A + 4}, ALIGN), ({"srt": A + 8}, ALIGN), ({"sr": None}, ALIGN), ({"off": A + 4}, ALIGN),
-    ({"M": 4096}, SCRATCH), ({"M": 4096, "ws": A + 16, "nb": 1 << 30}, ALIGN),
-    ({"M": 4096, "ws": None, "nb": 1 << 30}, ALIGN),
+    ({"M": 8192}, SCRATCH), ({"M": 8192, "ws": A + 16, "nb": 1 << 30}, ALIGN),
+    ({"M": 8192, "ws": None, "nb": 1 << 30}, ALIGN),
 ])
 def test_permute_refusals(kw, status):
     assert _permute(**kw) == status
@@ -68,10 +68,7 @@ def test_route_backward_refusals():
         assert f(**kw) == ALIGN, kw
 
 
-_LORA = dict(M=4, G=3, K=64, N=32, r=8)
-
-
-def _lora(M=4, G=3, K=64, N=32, r=8, x=A, xs=None, ids=A, a=A, b=A, sc=A, base=A, bs=None, y=2 * A,
+def _lora(M=2000, G=3, K=64, N=32, r=8, x=A, xs=None, ids=A, a=A, b=A, sc=A, base=A, bs=None, y=2 * A,
           ys=None, z=None, ws=A, nb=1 << 40):
     return hm.load_library().moe_lora(x, K if xs is None else xs, ids, a, b, sc, M, G, K, N, r, base,
                                       N if bs is None else bs, y, N if ys is None else ys, z, ws, nb, None)
@@ -113,9 +110,10 @@ def test_scratch_planners():
     assert hm.moe_permute_scratch_bytes(4096, 8, 256) > 0
     assert hm.moe_permute_scratch_bytes(0, 1, 1) == 0
     f, b = hm.moe_lora_scratch_bytes(4096, 8, 6144, 4096, 64)
-    assert f >= 4096 * 64 * 4 and b >= 4096 * 64 * 4 + 8 * 64 * (6144 + 4096) * 2
-    need = hm.moe_lora_scratch_bytes(4, 3, 64, 32, 8)
-    assert _lora(nb=need[0] - 1) == SCRATCH and _lora_bwd(nb=need[1] - 1) == SCRATCH
+    assert f >= 4096 * 64 * 4 and b >= 4096 * 64 * 4 + 8 * 64 * 4096 * 2
+    assert hm.moe_lora_scratch_bytes(64, 48, 2048, 4096, 16)[0] == 0   # one launch for few rows
+    assert _lora(nb=hm.moe_lora_scratch_bytes(2000, 3, 64, 32, 8)[0] - 1) == SCRATCH
+    assert _lora_bwd(nb=hm.moe_lora_scratch_bytes(4, 3, 64, 32, 8)[1] - 1) == SCRATCH
     for args in ((-1, 1, 8, 8, 8), (1, 1, 8, 8, 0)):
         with pytest.raises(hm.HmoeError):
             hm.moe_lora_scratch_bytes(*args)

@@ -352,12 +352,29 @@ def moe_quantize_mxfp4(x, codes, scales, stream=None) -> None:
 
 
 # ---- operators around the experts ---------------------------------------------------
+#
+# Small calls take a few microseconds on the GPU, so the checks below are written to cost
+# little on the host: no strings or containers are built unless a check fails.
+
+_torch = None
+_CODES = {}
+
+
+def _load_torch():
+    global _torch
+    import torch
+    # int16 holds bf16 bits, as for the layer
+    _CODES.update({torch.bfloat16: DTYPE_BF16, torch.int16: DTYPE_BF16, torch.float16: DTYPE_FP16,
+                   torch.float32: DTYPE_FP32})
+    _torch = torch
+    return torch
+
 
 def _dtype_code(t) -> int:
-    """Element type of a rows tensor (int16 holds bf16 bits, as for the layer)."""
-    import torch
-    code = {torch.bfloat16: DTYPE_BF16, torch.int16: DTYPE_BF16, torch.float16: DTYPE_FP16,
-            torch.float32: DTYPE_FP32}.get(t.dtype)
+    """Element type of a rows tensor."""
+    if _torch is None:
+        _load_torch()
+    code = _CODES.get(t.dtype)
     if code is None:
         raise ValueError(f"rows of {t.dtype}: expected bfloat16 (or its bits as int16), float16 "
                          "or float32")
@@ -366,44 +383,47 @@ def _dtype_code(t) -> int:
 
 def _matrix(name: str, t, rows: int, cols: int, code: int) -> int:
     """Checks a [rows, cols] matrix of the given element type; returns its row stride."""
-    if tuple(t.shape) != (rows, cols) or _dtype_code(t) != code:
+    if t.shape != (rows, cols) or _CODES.get(t.dtype) != code:
         raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}, expected [{rows}, {cols}] of the "
-                         "other rows' type")
-    if cols > 1 and t.stride(1) != 1:
+                         "operator's row type")
+    s = t.stride()
+    if s[1] != 1 and cols > 1:
         raise ValueError(f"{name}: the last axis must be contiguous")
-    return t.stride(0) if rows > 1 else cols
+    return s[0] if rows > 1 else cols
 
 
-def _array(name: str, t, shape: tuple, dtype: str) -> None:
-    if tuple(t.shape) != shape or str(t.dtype) != dtype or not t.is_contiguous():
-        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}, expected contiguous {dtype} {shape}")
+def _ints(name: str, t, shape: tuple) -> None:
+    if t.shape != shape or t.dtype is not (_torch or _load_torch()).int32 or not t.is_contiguous():
+        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}, expected contiguous int32 {shape}")
 
 
-class _On:
-    """The device of a call's tensors, made current for the launch, and its stream: the
-    given one, else that device's current stream."""
-
-    def __init__(self, stream, *tensors):
-        self.device = tensors[0].get_device()
-        if self.device < 0 or any(t is not None and t.get_device() != self.device for t in tensors):
-            raise ValueError("all tensors of a call must be on one GPU")
-        self.stream = stream
-
-    def __enter__(self):
-        import torch
-        self.before = torch.cuda.current_device()
-        if self.before != self.device:
-            torch.cuda.set_device(self.device)
-        return torch.cuda.current_stream().cuda_stream if self.stream is None else self.stream
-
-    def __exit__(self, *exc):
-        if self.before != self.device:
-            import torch
-            torch.cuda.set_device(self.before)
+def _floats(name: str, t, shape: tuple) -> None:
+    if t.shape != shape or t.dtype is not _torch.float32 or not t.is_contiguous():
+        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}, expected contiguous float32 {shape}")
 
 
 def _at(t):
     return None if t is None else t.data_ptr()
+
+
+def _launch(function: str, stream, tensors: tuple, *args) -> None:
+    """Calls a C function on the tensors' device: its stream argument is the given one, else
+    that device's current stream. Tensors on different devices, or not on a GPU, are refused."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors of a call must be on one GPU")
+    if dev < 0:
+        raise ValueError("all tensors of a call must be on one GPU")
+    fn = getattr(_lib or load_library(), function)
+    cuda = _torch.cuda
+    if cuda.current_device() == dev:
+        status = fn(*args, _torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream)
+    else:
+        with cuda.device(dev):
+            status = fn(*args, _torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream)
+    if status:
+        _check(status)
 
 
 def _room(scratch) -> tuple:
@@ -412,7 +432,7 @@ def _room(scratch) -> tuple:
         return None, 0
     if not scratch.is_contiguous():
         raise ValueError("scratch must be contiguous")
-    return scratch.data_ptr(), scratch.numel() * scratch.element_size()
+    return scratch.data_ptr(), scratch.nbytes
 
 
 def moe_permute_scratch_bytes(M: int, top_k: int, num_experts: int) -> int:
@@ -426,73 +446,69 @@ def moe_permute(x, topk_ids, num_experts: int, rows, sorted_slots, slot_row, exp
     """x[M, H] into expert order: rows[M * k, H], sorted_slots i32 [M * k], slot_row i32
     [M, k] and expert_off i32 [E + 1] (see include/hmoe.h). Ids outside [0, E) are dropped."""
     M, k = topk_ids.shape
-    H = x.shape[1]
+    H = x.shape[-1]
     code = _dtype_code(x)
     xs, rs = _matrix("x", x, M, H, code), _matrix("rows", rows, M * k, H, code)
-    _array("topk_ids", topk_ids, (M, k), "torch.int32")
-    _array("sorted_slots", sorted_slots, (M * k,), "torch.int32")
-    _array("slot_row", slot_row, (M, k), "torch.int32")
-    _array("expert_off", expert_off, (num_experts + 1,), "torch.int32")
+    _ints("topk_ids", topk_ids, (M, k))
+    _ints("sorted_slots", sorted_slots, (M * k,))
+    _ints("slot_row", slot_row, (M, k))
+    _ints("expert_off", expert_off, (num_experts + 1,))
     ws, nbytes = _room(scratch)
-    with _On(stream, x, topk_ids, rows, sorted_slots, slot_row, expert_off, scratch) as st:
-        _check(load_library().moe_permute(
-            x.data_ptr(), xs, topk_ids.data_ptr(), M, k, num_experts, H, code, rows.data_ptr(), rs,
-            sorted_slots.data_ptr(), slot_row.data_ptr(), expert_off.data_ptr(), ws, nbytes, st))
+    _launch("moe_permute", stream, (x, topk_ids, rows, sorted_slots, slot_row, expert_off,
+            scratch), x.data_ptr(), xs, topk_ids.data_ptr(), M, k, num_experts, H, code,
+            rows.data_ptr(), rs, sorted_slots.data_ptr(), slot_row.data_ptr(),
+            expert_off.data_ptr(), ws, nbytes)
 
 
 def moe_permute_backward(drows, slot_row, dx, stream=None) -> None:
     """dx[M, H] = for each token the sum of its slots' drows[M * k, H]."""
     M, k = slot_row.shape
-    H = drows.shape[1]
+    H = drows.shape[-1]
     code = _dtype_code(drows)
     ds, xs = _matrix("drows", drows, M * k, H, code), _matrix("dx", dx, M, H, code)
-    _array("slot_row", slot_row, (M, k), "torch.int32")
-    with _On(stream, drows, slot_row, dx) as st:
-        _check(load_library().moe_permute_backward(drows.data_ptr(), ds, slot_row.data_ptr(), M, k, H,
-                                                   code, dx.data_ptr(), xs, st))
+    _ints("slot_row", slot_row, (M, k))
+    _launch("moe_permute_backward", stream, (drows, slot_row, dx), drows.data_ptr(), ds,
+            slot_row.data_ptr(), M, k, H, code, dx.data_ptr(), xs)
 
 
 def moe_unpermute(rows, slot_row, topk_w, y, stream=None) -> None:
     """y[M, H] = for each token the sum of its slots' rows[M * k, H] times topk_w f32 [M, k]."""
     M, k = slot_row.shape
-    H = rows.shape[1]
+    H = rows.shape[-1]
     code = _dtype_code(rows)
     rs, ys = _matrix("rows", rows, M * k, H, code), _matrix("y", y, M, H, code)
-    _array("slot_row", slot_row, (M, k), "torch.int32")
-    _array("topk_w", topk_w, (M, k), "torch.float32")
-    with _On(stream, rows, slot_row, topk_w, y) as st:
-        _check(load_library().moe_unpermute(rows.data_ptr(), rs, slot_row.data_ptr(),
-                                            topk_w.data_ptr(), M, k, H, code, y.data_ptr(), ys, st))
+    _ints("slot_row", slot_row, (M, k))
+    _floats("topk_w", topk_w, (M, k))
+    _launch("moe_unpermute", stream, (rows, slot_row, topk_w, y), rows.data_ptr(), rs,
+            slot_row.data_ptr(), topk_w.data_ptr(), M, k, H, code, y.data_ptr(), ys)
 
 
 def moe_unpermute_backward(dy, rows, slot_row, topk_w, drows, dw, stream=None) -> None:
     """Gradients of moe_unpermute: drows[M * k, H] (rows no slot names stay as they were) and
     dw f32 [M, k]."""
     M, k = slot_row.shape
-    H = rows.shape[1]
+    H = rows.shape[-1]
     code = _dtype_code(rows)
     ys, rs = _matrix("dy", dy, M, H, code), _matrix("rows", rows, M * k, H, code)
     ds = _matrix("drows", drows, M * k, H, code)
-    _array("slot_row", slot_row, (M, k), "torch.int32")
-    _array("topk_w", topk_w, (M, k), "torch.float32")
-    _array("dw", dw, (M, k), "torch.float32")
-    with _On(stream, dy, rows, slot_row, topk_w, drows, dw) as st:
-        _check(load_library().moe_unpermute_backward(
-            dy.data_ptr(), ys, rows.data_ptr(), rs, slot_row.data_ptr(), topk_w.data_ptr(), M, k, H,
-            code, drows.data_ptr(), ds, dw.data_ptr(), st))
+    _ints("slot_row", slot_row, (M, k))
+    _floats("topk_w", topk_w, (M, k))
+    _floats("dw", dw, (M, k))
+    _launch("moe_unpermute_backward", stream, (dy, rows, slot_row, topk_w, drows, dw),
+            dy.data_ptr(), ys, rows.data_ptr(), rs, slot_row.data_ptr(), topk_w.data_ptr(), M,
+            k, H, code, drows.data_ptr(), ds, dw.data_ptr())
 
 
 def moe_route_backward(topk_ids, topk_w, dw, dlogits, stream=None) -> None:
     """dlogits f32 [M, E] (fully overwritten) from moe_route's ids and weights and dw f32 [M, k]."""
     M, k = topk_ids.shape
-    E = dlogits.shape[1]
-    _array("topk_ids", topk_ids, (M, k), "torch.int32")
-    _array("topk_w", topk_w, (M, k), "torch.float32")
-    _array("dw", dw, (M, k), "torch.float32")
-    _array("dlogits", dlogits, (M, E), "torch.float32")
-    with _On(stream, topk_ids, topk_w, dw, dlogits) as st:
-        _check(load_library().moe_route_backward(topk_ids.data_ptr(), topk_w.data_ptr(), dw.data_ptr(),
-                                                 M, E, k, dlogits.data_ptr(), st))
+    E = dlogits.shape[-1]
+    _ints("topk_ids", topk_ids, (M, k))
+    _floats("topk_w", topk_w, (M, k))
+    _floats("dw", dw, (M, k))
+    _floats("dlogits", dlogits, (M, E))
+    _launch("moe_route_backward", stream, (topk_ids, topk_w, dw, dlogits), topk_ids.data_ptr(),
+            topk_w.data_ptr(), dw.data_ptr(), M, E, k, dlogits.data_ptr())
 
 
 def moe_lora_scratch_bytes(M: int, num_adapters: int, K: int, N: int, rank: int) -> tuple:
@@ -503,16 +519,15 @@ def moe_lora_scratch_bytes(M: int, num_adapters: int, K: int, N: int, rank: int)
 
 
 def _adapters(M: int, ids, A, B, scale) -> tuple:
-    if A.dim() != 3 or B.dim() != 3 or A.shape[0] != B.shape[0] or A.shape[1] != B.shape[2]:
-        raise ValueError(f"A {tuple(A.shape)} and B {tuple(B.shape)}: expected [G, rank, K] and "
-                         "[G, N, rank]")
-    G, r, K = A.shape
-    for name, t in (("A", A), ("B", B)):
-        if _dtype_code(t) != DTYPE_BF16 or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous bfloat16")
-    _array("ids", ids, (M,), "torch.int32")
-    _array("scale", scale, (G,), "torch.float32")
-    return G, r, K, B.shape[1]
+    a, b = A.shape, B.shape
+    if len(a) != 3 or len(b) != 3 or a[0] != b[0] or a[1] != b[2]:
+        raise ValueError(f"A {tuple(a)} and B {tuple(b)}: expected [G, rank, K] and [G, N, rank]")
+    if (_dtype_code(A) != DTYPE_BF16 or _dtype_code(B) != DTYPE_BF16 or not A.is_contiguous()
+            or not B.is_contiguous()):
+        raise ValueError("A and B must be contiguous bfloat16")
+    _ints("ids", ids, (M,))
+    _floats("scale", scale, (a[0],))
+    return a[0], a[1], a[2], b[1]
 
 
 def moe_lora(x, ids, A, B, scale, base, y, z=None, scratch=None, stream=None) -> None:
@@ -524,12 +539,11 @@ def moe_lora(x, ids, A, B, scale, base, y, z=None, scratch=None, stream=None) ->
     xs, ys = _matrix("x", x, M, K, DTYPE_BF16), _matrix("y", y, M, N, DTYPE_BF16)
     bs = 0 if base is None else _matrix("base", base, M, N, DTYPE_BF16)
     if z is not None:
-        _array("z", z, (M, r), "torch.float32")
+        _floats("z", z, (M, r))
     ws, nbytes = _room(scratch)
-    with _On(stream, x, ids, A, B, scale, base, y, z, scratch) as st:
-        _check(load_library().moe_lora(
-            x.data_ptr(), xs, ids.data_ptr(), A.data_ptr(), B.data_ptr(), scale.data_ptr(), M, G, K, N,
-            r, _at(base), bs, y.data_ptr(), ys, _at(z), ws, nbytes, st))
+    _launch("moe_lora", stream, (x, ids, A, B, scale, base, y, z, scratch), x.data_ptr(), xs,
+            ids.data_ptr(), A.data_ptr(), B.data_ptr(), scale.data_ptr(), M, G, K, N, r,
+            _at(base), bs, y.data_ptr(), ys, _at(z), ws, nbytes)
 
 
 def moe_lora_backward(dy, x, z, ids, A, B, scale, dbase, dx, dA, dB, scratch=None,
@@ -541,15 +555,14 @@ def moe_lora_backward(dy, x, z, ids, A, B, scale, dbase, dx, dA, dB, scratch=Non
     ys, xs = _matrix("dy", dy, M, N, DTYPE_BF16), _matrix("x", x, M, K, DTYPE_BF16)
     ds = _matrix("dx", dx, M, K, DTYPE_BF16)
     bs = 0 if dbase is None else _matrix("dbase", dbase, M, K, DTYPE_BF16)
-    _array("z", z, (M, r), "torch.float32")
-    _array("dA", dA, (G, r, K), "torch.float32")
-    _array("dB", dB, (G, N, r), "torch.float32")
+    _floats("z", z, (M, r))
+    _floats("dA", dA, (G, r, K))
+    _floats("dB", dB, (G, N, r))
     ws, nbytes = _room(scratch)
-    with _On(stream, dy, x, z, ids, A, B, scale, dbase, dx, dA, dB, scratch) as st:
-        _check(load_library().moe_lora_backward(
-            dy.data_ptr(), ys, x.data_ptr(), xs, z.data_ptr(), ids.data_ptr(), A.data_ptr(),
-            B.data_ptr(), scale.data_ptr(), M, G, K, N, r, _at(dbase), bs, dx.data_ptr(), ds,
-            dA.data_ptr(), dB.data_ptr(), ws, nbytes, st))
+    _launch("moe_lora_backward", stream, (dy, x, z, ids, A, B, scale, dbase, dx, dA, dB,
+            scratch), dy.data_ptr(), ys, x.data_ptr(), xs, z.data_ptr(), ids.data_ptr(),
+            A.data_ptr(), B.data_ptr(), scale.data_ptr(), M, G, K, N, r, _at(dbase), bs,
+            dx.data_ptr(), ds, dA.data_ptr(), dB.data_ptr(), ws, nbytes)
 
 
 class DeviceWeights:

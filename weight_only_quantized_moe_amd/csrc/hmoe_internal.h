@@ -112,8 +112,11 @@ hipError_t launch_route_backward(const int32_t* ids, const float* w, const float
 // permute.hip: stable counting sort of n ids over G groups. groups = G drops ids outside
 // [0, G); groups = G + 1 makes them the last group. counts holds sort_count_words words;
 // slot_row may be null. tile_rows > 0 also cuts every group's run into tiles of that many
-// rows: tile_group [max_tiles] (-1 past the last tile) and tile_start [max_tiles].
+// rows, described by tile [max_tiles] (group -1 past the last tile).
 constexpr int kMaxGroups = HMOE_MAX_GROUPS;
+struct SortTile {
+  int32_t group, start, rows, pad;
+};
 struct GroupSort {
   const int32_t* ids;
   int n, G, groups;
@@ -122,8 +125,7 @@ struct GroupSort {
   int32_t* slot_row;
   int32_t* off;
   int tile_rows, max_tiles;
-  int32_t* tile_group;
-  int32_t* tile_start;
+  SortTile* tile;
 };
 size_t sort_count_words(int n, int groups);
 hipError_t launch_sort(const GroupSort& g, hipStream_t s);

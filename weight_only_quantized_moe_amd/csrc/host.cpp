@@ -733,8 +733,8 @@ hmoe_status moe_lora(const uint16_t* x, int64_t x_stride, const int32_t* ids, co
   if (hmoe_status st = check_base("base", base, base_stride, y, y_stride, N)) return st;
   if (hmoe_status st = check_arrays("ids, A, B and scale", {ids, A, B, scale})) return st;
   if (!aligned(z, 16)) return fail(HMOE_ERR_ALIGN, "z must be 16-byte aligned");
-  size_t need, back;
-  hmoe::lora_scratch(M, G, K, N, rank, &need, &back);
+  size_t need;
+  hmoe::lora_scratch(M, G, K, N, rank, &need, nullptr);
   if (hmoe_status st = check_op_scratch(scratch, scratch_bytes, need)) return st;
   const hmoe::Lora p{x, x_stride, ids, A, B, scale, M, G, K, N, rank, base, base_stride, y, y_stride, z};
   hipError_t err = hmoe::launch_lora(p, scratch, stream);
@@ -758,8 +758,8 @@ hmoe_status moe_lora_backward(const uint16_t* dy, int64_t dy_stride, const uint1
     if (hmoe_status st = check_base("dbase", dbase, dbase_stride, dx, dx_stride, K)) return st;
     if (hmoe_status st = check_arrays("ids and z", {ids, z})) return st;
   }
-  size_t forward, need;
-  hmoe::lora_scratch(M, G, K, N, rank, &forward, &need);
+  size_t need;
+  hmoe::lora_scratch(M, G, K, N, rank, nullptr, &need);
   if (hmoe_status st = check_op_scratch(scratch, scratch_bytes, need)) return st;
   const hmoe::LoraGrad p{dy, dy_stride, x, x_stride, z, ids, A, B, scale, M, G, K, N, rank,
                          dbase, dbase_stride, dx, dx_stride, dA, dB};

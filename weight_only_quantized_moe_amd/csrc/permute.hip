@@ -20,10 +20,12 @@ namespace hmoe {
 // counting sort of n ids over G groups
 // ---------------------------------------------------------------------------
 
-constexpr int kSortThreads = 256;
-constexpr int kSortWaves = kSortThreads / kWave;
-// s_waitcnt operand waiting for LDS only (vmcnt 63, expcnt 7, lgkmcnt 0)
-constexpr int kSortWaitLds = 0xC07F;
+// threads of a sort block: every wave keeps a counter per group in LDS, so 16 waves up to
+// kSortWideGroups groups (41 KB of counters), 4 waves beyond
+constexpr int kSortWide = 1024, kSortNarrow = 256, kSortWideGroups = 640;
+// up to this many ids one block counts and places; more ids are counted and placed by
+// several blocks of kSortChunk ids in two launches
+constexpr int kSortOneBlock = 8192, kSortChunk = 2048;
 
 struct SortArgs {
   const int32_t* ids;
@@ -37,8 +39,7 @@ struct SortArgs {
   int32_t* off;         // [groups + 1]
   int tile_rows;        // rows per tile of the tile table (0: no table)
   int max_tiles;
-  int32_t* tile_group;
-  int32_t* tile_start;
+  SortTile* tile;
 };
 
 // group of an id: ids outside [0, G) are dropped (-1) or the group behind the last
@@ -47,6 +48,7 @@ __device__ __forceinline__ int sort_key(int id, int G, int groups) {
 }
 
 // inclusive sum over the block of one value per thread; *total: the block's sum
+template <int THREADS>
 __device__ __forceinline__ int block_scan(int v, int* s_part, int* total) {
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
 #pragma unroll
@@ -57,73 +59,116 @@ __device__ __forceinline__ int block_scan(int v, int* s_part, int* total) {
   __syncthreads();
   if (lane == kWave - 1) s_part[wave] = v;
   __syncthreads();
-  int add = 0, sum = 0;
+  int p = lane < THREADS / kWave ? s_part[lane] : 0;
 #pragma unroll
-  for (int w = 0; w < kSortWaves; ++w) {
-    const int p = s_part[w];
-    if (w < wave) add += p;
-    sum += p;
+  for (int o = 1; o < THREADS / kWave; o <<= 1) {
+    const int u = __shfl_up(p, o);
+    if (lane >= o) p += u;
   }
-  *total = sum;
+  *total = __shfl(p, THREADS / kWave - 1);
+  const int add = wave ? __shfl(p, wave - 1) : 0;
   return v + add;
 }
 
+// lanes of the wave with the same group as this one (0: none), from ballots over the bits
+__device__ __forceinline__ uint64_t same_group(int e, int bits) {
+  uint64_t m = __ballot(e >= 0);
+  for (int b = 0; b < bits; ++b) {
+    const bool bit = (e >> b) & 1;
+    const uint64_t bb = __ballot(bit);
+    m &= bit ? bb : ~bb;
+  }
+  return e >= 0 ? m : 0;
+}
+
+__device__ __forceinline__ int group_bits(int groups) { return groups > 1 ? 32 - __clz(groups - 1) : 0; }
+
+// adds the wave's ids to a counter per group: one LDS operation a group, not one a lane
+// (few groups would make 64 lanes wait for one address)
+__device__ __forceinline__ void count_groups(int e, int bits, int32_t* s_cnt) {
+  const uint64_t m = same_group(e, bits);
+  if (m && __ffsll((unsigned long long)m) - 1 == (int)(threadIdx.x & (kWave - 1)))
+    atomicAdd(&s_cnt[e], __popcll(m));
+}
+
 // per-block group counts of a sort over several blocks
-__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
+__global__ __launch_bounds__(kSortWide) void sort_count_kernel(SortArgs a) {
   __shared__ int32_t s_cnt[kMaxGroups + 1];
-  for (int e = threadIdx.x; e < a.groups; e += kSortThreads) s_cnt[e] = 0;
+  for (int e = threadIdx.x; e < a.groups; e += kSortWide) s_cnt[e] = 0;
   __syncthreads();
   const int c0 = min((long)blockIdx.x * a.chunk, (long)a.n), c1 = min(c0 + (long)a.chunk, (long)a.n);
-  for (int s = c0 + (int)threadIdx.x; s < c1; s += kSortThreads) {
-    const int e = sort_key(a.ids[s], a.G, a.groups);
-    if (e >= 0) atomicAdd(&s_cnt[e], 1);
+  const int bits = group_bits(a.groups);
+  for (int s0 = c0; s0 < c1; s0 += kSortWide) {
+    const int s = s0 + (int)threadIdx.x;
+    count_groups(s < c1 ? sort_key(a.ids[s], a.G, a.groups) : -1, bits, s_cnt);
   }
   __syncthreads();
   int32_t* out = a.counts + (size_t)blockIdx.x * a.groups;
-  for (int e = threadIdx.x; e < a.groups; e += kSortThreads) out[e] = s_cnt[e];
+  for (int e = threadIdx.x; e < a.groups; e += kSortWide) out[e] = s_cnt[e];
 }
 
 // Places one block's chunk: every wave owns a contiguous part of it, so the order is that
 // of a serial counting sort whatever the timing. With one block the counts are its own;
-// else each block sums the count table of all blocks (read from L2).
-__global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
-  __shared__ int32_t s_w[kSortWaves][kMaxGroups + 1];  // per-wave counts, then positions
-  __shared__ int32_t s_base[kMaxGroups + 1];           // this block's first position per group
-  __shared__ int32_t s_tile[kMaxGroups + 2];           // exclusive tile counts
-  __shared__ int32_t s_part[kSortWaves];
+// else each block sums the count table of all blocks (read from L2, eight loads in flight).
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void sort_place_kernel(SortArgs a) {
+  constexpr int kWaves = THREADS / kWave;
+  constexpr int kGroups = THREADS == kSortWide ? kSortWideGroups : kMaxGroups + 1;
+  constexpr int kBatch = 4, kTable = 8;
+  __shared__ int32_t s_w[kWaves][kGroups];  // per-wave counts, then positions
+  __shared__ int32_t s_base[kGroups];       // first row of each group
+  __shared__ int32_t s_tile[kGroups + 1];   // first tile of each group
+  __shared__ int32_t s_part[kWaves];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid >> 6;
   const int c0 = min((long)blockIdx.x * a.chunk, (long)a.n), c1 = min(c0 + (long)a.chunk, (long)a.n);
-  const int part = ((c1 - c0 + kSortThreads - 1) / kSortThreads) * kWave;  // ids per wave
+  const int part = ((c1 - c0 + THREADS - 1) / THREADS) * kWave;  // ids per wave
   const int w0 = min(c0 + wave * part, c1), w1 = min(w0 + part, c1);
-  for (int e = tid; e < a.groups; e += kSortThreads)
-    for (int w = 0; w < kSortWaves; ++w) s_w[w][e] = 0;
+  for (int e = tid; e < a.groups; e += THREADS)
+    for (int w = 0; w < kWaves; ++w) s_w[w][e] = 0;
   __syncthreads();
-  for (int s = w0 + lane; s < w1; s += kWave) {
-    const int e = sort_key(a.ids[s], a.G, a.groups);
-    if (e >= 0) atomicAdd(&s_w[wave][e], 1);
+  const int bits = group_bits(a.groups);
+  int id[kBatch];
+  auto load_ids = [&](int s0) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int s = s0 + i * kWave + lane;
+      id[i] = s < w1 ? sort_key(a.ids[s], a.G, a.groups) : -1;
+    }
+  };
+  for (int s0 = w0; s0 < w1; s0 += kBatch * kWave) {
+    load_ids(s0);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (s0 + i * kWave < w1) count_groups(id[i], bits, s_w[wave]);
   }
   __syncthreads();
   int placed = 0, tiles = 0;
-  for (int e0 = 0; e0 < a.groups; e0 += kSortThreads) {
+  for (int e0 = 0; e0 < a.groups; e0 += THREADS) {
     const int e = e0 + tid;
     int tot = 0, before = 0;
     if (e < a.groups) {
       if (a.nb == 1) {
-        for (int w = 0; w < kSortWaves; ++w) tot += s_w[w][e];
+        for (int w = 0; w < kWaves; ++w) tot += s_w[w][e];
       } else {
-        for (int b = 0; b < a.nb; ++b) {
-          const int c = a.counts[(size_t)b * a.groups + e];
-          tot += c;
-          if (b < (int)blockIdx.x) before += c;
+        for (int b0 = 0; b0 < a.nb; b0 += kTable) {
+          int c[kTable];
+#pragma unroll
+          for (int i = 0; i < kTable; ++i)
+            c[i] = b0 + i < a.nb ? a.counts[(size_t)(b0 + i) * a.groups + e] : 0;
+#pragma unroll
+          for (int i = 0; i < kTable; ++i) {
+            tot += c[i];
+            if (b0 + i < (int)blockIdx.x) before += c[i];
+          }
         }
       }
     }
     int sum;
-    const int excl = placed + block_scan(tot, s_part, &sum) - tot;
+    const int excl = placed + block_scan<THREADS>(tot, s_part, &sum) - tot;
     placed += sum;
     if (e < a.groups) {
       int run = excl + before;
-      for (int w = 0; w < kSortWaves; ++w) {
+      for (int w = 0; w < kWaves; ++w) {
         const int c = s_w[w][e];
         s_w[w][e] = run;
         run += c;
@@ -132,7 +177,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
     }
     if (a.tile_rows) {
       const int nt = (tot + a.tile_rows - 1) / a.tile_rows;
-      const int tx = tiles + block_scan(nt, s_part, &sum) - nt;
+      const int tx = tiles + block_scan<THREADS>(nt, s_part, &sum) - nt;
       tiles += sum;
       if (e < a.groups) {
         s_tile[e] = tx;
@@ -142,55 +187,60 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
   }
   if (blockIdx.x == 0 && tid == 0) a.off[a.groups] = placed;
   __syncthreads();
-  const int gid = blockIdx.x * kSortThreads + tid, gsz = gridDim.x * kSortThreads;
+  const int gid = blockIdx.x * THREADS + tid, gsz = gridDim.x * THREADS;
   for (int i = placed + gid; i < a.n; i += gsz) a.sorted[i] = -1;
   if (a.tile_rows) {
-    // tile t belongs to the last group whose first tile is at or before t
-    for (int t = gid; t < a.max_tiles; t += gsz) {
+    // Entry i is what block i of a launch takes. Blocks go to the 8 XCDs in turn, so the
+    // tiles are dealt out in 8 runs: neighbouring tiles, which read the same adapter, share
+    // an L2. Tile t belongs to the last group whose first tile is at or before t.
+    const int run = (tiles + 7) / 8;
+    for (int i = gid; i < a.max_tiles; i += gsz) {
+      const int t = (i >> 3) < run ? (i & 7) * run + (i >> 3) : tiles;
       int lo = 0, hi = a.groups - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (s_tile[mid] <= t) lo = mid; else hi = mid - 1;
       }
-      const bool live = t < tiles;
-      a.tile_group[t] = live ? lo : -1;
-      a.tile_start[t] = live ? s_base[lo] + (t - s_tile[lo]) * a.tile_rows : 0;
+      SortTile d{-1, 0, 0, 0};
+      if (t < tiles) {
+        const int end = lo + 1 < a.groups ? s_base[lo + 1] : placed;
+        d.group = lo;
+        d.start = s_base[lo] + (t - s_tile[lo]) * a.tile_rows;
+        d.rows = min(a.tile_rows, end - d.start);
+      }
+      a.tile[i] = d;
     }
   }
-  int idbits = 1;
-  while ((1 << idbits) < a.groups) ++idbits;
-  for (int b0 = w0; b0 < w1; b0 += kWave) {
-    const int s = b0 + lane;
-    const int e0 = s < w1 ? sort_key(a.ids[s], a.G, a.groups) : -1;
-    const int e = max(e0, 0);
-    uint64_t m = __ballot(e0 >= 0);
-    for (int b = 0; b < idbits; ++b) {
-      const bool bit = (e >> b) & 1;
-      const uint64_t bb = __ballot(bit);
-      m &= bit ? bb : ~bb;
+  for (int s0 = w0; s0 < w1; s0 += kBatch * kWave) {
+    if (w1 - w0 > kBatch * kWave) load_ids(s0);   // else they are still here
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (s0 + i * kWave >= w1) break;
+      const int s = s0 + i * kWave + lane;
+      const int e = max(id[i], 0);
+      const uint64_t m = same_group(id[i], bits);
+      const int rank = __popcll(m & ((1ull << lane) - 1ull));
+      const int cnt = __popcll(m);
+      int pos = -1;
+      if (id[i] >= 0) pos = s_w[wave][e] + rank;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      if (id[i] >= 0) {
+        a.sorted[pos] = s;
+        if (rank == cnt - 1) s_w[wave][e] += cnt;
+      }
+      if (a.slot_row && s < w1) a.slot_row[s] = pos;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
     }
-    const int rank = __popcll(m & ((1ull << lane) - 1ull));
-    const int cnt = __popcll(m);
-    int pos = -1;
-    if (e0 >= 0) pos = s_w[wave][e] + rank;
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_s_waitcnt(kSortWaitLds);
-    if (e0 >= 0) {
-      a.sorted[pos] = s;
-      if (rank == cnt - 1) s_w[wave][e] += cnt;
-    }
-    if (a.slot_row && s < w1) a.slot_row[s] = pos;
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_s_waitcnt(kSortWaitLds);
   }
 }
 
-// Blocks of a sort: 512 ids each, fewer and larger blocks where the count table that every
-// block reads (blocks * groups entries) would grow past 64 K entries.
-int sort_blocks(int n, int groups) {
-  const int want = (n + 511) / 512, cap = std::max(1, (1 << 16) / groups);
-  if (n <= 2048) return 1;
-  return std::min({want, cap, 256});
+// Blocks of a sort: fewer and larger ones where the count table that every block reads
+// (blocks * groups entries) would grow past 64 K entries.
+static int sort_blocks(int n, int groups) {
+  if (n <= kSortOneBlock) return 1;
+  return std::min({(n + kSortChunk - 1) / kSortChunk, std::max(1, (1 << 16) / groups), 256});
 }
 
 size_t sort_count_words(int n, int groups) {
@@ -205,17 +255,19 @@ hipError_t launch_sort(const GroupSort& g, hipStream_t s) {
   a.G = g.G;
   a.groups = g.groups;
   a.nb = sort_blocks(g.n, g.groups);
-  a.chunk = ((g.n + a.nb - 1) / a.nb + kSortThreads - 1) / kSortThreads * kSortThreads;
+  a.chunk = ((g.n + a.nb - 1) / a.nb + kSortWide - 1) / kSortWide * kSortWide;
   a.counts = g.counts;
   a.sorted = g.sorted;
   a.slot_row = g.slot_row;
   a.off = g.off;
   a.tile_rows = g.tile_rows;
   a.max_tiles = g.max_tiles;
-  a.tile_group = g.tile_group;
-  a.tile_start = g.tile_start;
-  if (a.nb > 1) hipLaunchKernelGGL(sort_count_kernel, dim3(a.nb), dim3(kSortThreads), 0, s, a);
-  hipLaunchKernelGGL(sort_place_kernel, dim3(a.nb), dim3(kSortThreads), 0, s, a);
+  a.tile = g.tile;
+  if (a.nb > 1) hipLaunchKernelGGL(sort_count_kernel, dim3(a.nb), dim3(kSortWide), 0, s, a);
+  if (g.groups <= kSortWideGroups)
+    hipLaunchKernelGGL(sort_place_kernel<kSortWide>, dim3(a.nb), dim3(kSortWide), 0, s, a);
+  else
+    hipLaunchKernelGGL(sort_place_kernel<kSortNarrow>, dim3(a.nb), dim3(kSortNarrow), 0, s, a);
   return hipGetLastError();
 }
 
@@ -365,7 +417,7 @@ __global__ __launch_bounds__(kRowThreads) void permute_small_kernel(PermuteSmall
   __shared__ int32_t s_id[kPermuteSmall];
   __shared__ int32_t s_cnt[kMaxExperts];
   __shared__ int32_t s_row[kMaxTopK];
-  __shared__ int32_t s_part[kSortWaves];
+  __shared__ int32_t s_part[kRowThreads / kWave];
   const int tid = threadIdx.x, n = a.M * a.k;
   const auto [t, at] = row_place(a.chunks);
   const bool first = at < kRowThreads * 16;  // the token's first block
@@ -382,7 +434,7 @@ __global__ __launch_bounds__(kRowThreads) void permute_small_kernel(PermuteSmall
       const int e = e0 + tid;
       const int c = e < a.E ? s_cnt[e] : 0;
       int sum;
-      const int incl = placed + block_scan(c, s_part, &sum);
+      const int incl = placed + block_scan<kRowThreads>(c, s_part, &sum);
       placed += sum;
       if (e < a.E) a.off[e] = incl - c;
     }

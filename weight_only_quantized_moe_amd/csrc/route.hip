@@ -85,60 +85,70 @@ hipError_t launch_route_group(const Layer& L, const float* logits, int M, void* 
 }
 
 // Gradient of the renormalised top-k weights: w = softmax over the selected logits, so
-// dl[e_j] = w_j (dw_j - sum_i w_i dw_i) and every other logit's gradient is zero. One wave
-// a token writes the whole row of E logits, four a lane, each picking its slots' values by
-// comparing ids: no zero fill before, no scatter, no order to depend on. Bound by the
-// M * E * 4 bytes it writes.
+// dl[e_j] = w_j (dw_j - sum_i w_i dw_i) and every other logit's gradient is zero. Bound by
+// the M * E * 4 bytes it writes. A wave takes four tokens, 16 lanes a token, so one load
+// each brings their ids, weights and gradients; it then builds 256 logits a token at a time
+// in LDS (zeros, the slots' values added in slot order) and writes them as 16 bytes a lane:
+// no fill before, no scatter to memory, no order to depend on.
 struct __attribute__((packed, aligned(4))) F32x4 {
   float v[4];
 };
+constexpr int kBwdTokens = 4, kBwdCols = 256;
 
-template <int KM>
+// LDS written by some lanes of the wave is read by others: no value is carried past here in
+// a register (the LDS operations themselves keep their order)
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 __global__ __launch_bounds__(kRouteWaves * kWave) void route_bwd_kernel(
     const int32_t* __restrict__ ids, const float* __restrict__ w, const float* __restrict__ dw,
     int M, int E, int k, float* __restrict__ dl) {
-  const int lane = threadIdx.x & (kWave - 1);
-  const long t = blockIdx.x * (long)kRouteWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (t >= M) return;
-  int id[KM];
-  float g[KM], d[KM], sum = 0.f;
+  __shared__ __align__(16) float s_row[kRouteWaves][kBwdTokens][kBwdCols];
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
+  const long t0 = (blockIdx.x * (long)kRouteWaves + wave) * kBwdTokens;
+  if (t0 >= M) return;
+  const int j = lane & 15, mine = lane >> 4;
+  const bool in = j < k && t0 + mine < M;
+  const long at = (t0 + mine) * k + j;
+  const int id = in ? ids[at] : -1;
+  const float wj = in ? w[at] : 0.f, dj = in ? dw[at] : 0.f;
+  const float g = wj * (dj - group_sum<16>(wj * dj));
+  float(*row)[kBwdCols] = s_row[wave];
+  for (int e0 = 0; e0 < E; e0 += kBwdCols) {
 #pragma unroll
-  for (int j = 0; j < KM; ++j) {
-    id[j] = j < k ? ids[t * k + j] : -1;
-    g[j] = j < k ? w[t * k + j] : 0.f;
-    d[j] = j < k ? dw[t * k + j] : 0.f;
-    if (j < k) sum = fmaf(g[j], d[j], sum);
-  }
+    for (int t = 0; t < kBwdTokens; ++t)
+      *reinterpret_cast<float4*>(&row[t][lane * 4]) = make_float4(0.f, 0.f, 0.f, 0.f);
+    wave_fence();
+    const bool here = (unsigned)id < (unsigned)E && id >= e0 && id < e0 + kBwdCols;
+    for (int i = 0; i < k; ++i)   // LDS operations of a wave keep their order
+      if (here && j == i) atomicAdd(&row[mine][id - e0], g);
+    wave_fence();
+    const int e = e0 + lane * 4;
 #pragma unroll
-  for (int j = 0; j < KM; ++j) g[j] *= d[j] - sum;
-  float* row = dl + t * E;
-  for (int e = lane * 4; e < E; e += kWave * 4) {
-    F32x4 o;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float v = 0.f;
-#pragma unroll
-      for (int j = 0; j < KM; ++j) v += id[j] == e + q ? g[j] : 0.f;
-      o.v[q] = v;
+    for (int t = 0; t < kBwdTokens; ++t) {
+      if (t0 + t >= M || e >= E) continue;
+      const float4 v = *reinterpret_cast<const float4*>(&row[t][lane * 4]);
+      float* out = dl + (t0 + t) * E + e;
+      if (e + 4 <= E) {
+        *reinterpret_cast<F32x4*>(out) = F32x4{{v.x, v.y, v.z, v.w}};
+      } else {
+        out[0] = v.x;
+        if (e + 1 < E) out[1] = v.y;
+        if (e + 2 < E) out[2] = v.z;
+      }
     }
-    if (e + 4 <= E) {
-      *reinterpret_cast<F32x4*>(row + e) = o;
-    } else {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (e + q < E) row[e + q] = o.v[q];
-    }
+    wave_fence();
   }
 }
 
 hipError_t launch_route_backward(const int32_t* ids, const float* w, const float* dw, int M, int E,
                                  int k, float* dlogits, hipStream_t s) {
   if (M == 0) return hipSuccess;
-  const dim3 grid((M + kRouteWaves - 1) / kRouteWaves), block(kRouteWaves * kWave);
-  if (k <= 8)
-    hipLaunchKernelGGL(route_bwd_kernel<8>, grid, block, 0, s, ids, w, dw, M, E, k, dlogits);
-  else
-    hipLaunchKernelGGL(route_bwd_kernel<kMaxTopK>, grid, block, 0, s, ids, w, dw, M, E, k, dlogits);
+  constexpr int kTokens = kRouteWaves * kBwdTokens;
+  hipLaunchKernelGGL(route_bwd_kernel, dim3((M + kTokens - 1) / kTokens), dim3(kRouteWaves * kWave), 0,
+                     s, ids, w, dw, M, E, k, dlogits);
   return hipGetLastError();
 }
 
