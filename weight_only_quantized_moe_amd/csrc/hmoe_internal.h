@@ -112,10 +112,11 @@ hipError_t launch_route_backward(const int32_t* ids, const float* w, const float
 // permute.hip: stable counting sort of n ids over G groups. groups = G drops ids outside
 // [0, G); groups = G + 1 makes them the last group. counts holds sort_count_words words;
 // slot_row may be null. tile_rows > 0 also cuts every group's run into tiles of that many
-// rows, described by tile [max_tiles] (group -1 past the last tile).
+// rows, described by tile [max_tiles] (group -1 for none, index: number of the tile in sorted
+// order), and writes each group's first tile to tile_first [groups + 1].
 constexpr int kMaxGroups = HMOE_MAX_GROUPS;
 struct SortTile {
-  int32_t group, start, rows, pad;
+  int32_t group, start, rows, index;
 };
 struct GroupSort {
   const int32_t* ids;
@@ -126,6 +127,7 @@ struct GroupSort {
   int32_t* off;
   int tile_rows, max_tiles;
   SortTile* tile;
+  int32_t* tile_first;
 };
 size_t sort_count_words(int n, int groups);
 hipError_t launch_sort(const GroupSort& g, hipStream_t s);

@@ -29,7 +29,7 @@ struct __attribute__((packed, aligned(2))) Half8 {  // 8 bf16 at any element
 struct __attribute__((packed, aligned(2))) Half4 {
   uint32_t w[2];
 };
-constexpr int kKStep = 64;   // K elements a wave takes at a time: two MFMAs deep
+constexpr int kKStep = 128;  // K elements a wave takes at a time: four MFMAs deep
 
 __device__ __forceinline__ u32x4 load8(const uint16_t* p) {
   const Half8 h = *reinterpret_cast<const Half8*>(p);
@@ -47,6 +47,54 @@ __device__ __forceinline__ float bf16_rest(float v, float hi) {
   return (__float_as_uint(hi) & 0x7F800000u) == 0x7F800000u ? 0.f : v - hi;
 }
 
+// ---- lane exchanges ----------------------------------------------------------------
+//
+// An MFMA operand wants lane l to hold row l % 16, but the memory pipe takes 64 bytes a
+// cycle only where four neighbouring lanes lie in one 64-byte piece: 16-byte loads with one
+// row a lane ran at 9.6 TB/s over the card from L2, with four lanes a row at 34 TB/s
+// (measured, 1 MiB buffer). So rows are read and written four lanes a row, four rows in four
+// instructions, and exchanged inside each four lanes in registers.
+
+__device__ __forceinline__ uint32_t quad_x1(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true);  // lane ^ 1
+}
+__device__ __forceinline__ uint32_t quad_x2(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true);  // lane ^ 2
+}
+
+// lane s of each four gets v[j] = lane j's v[s]
+__device__ __forceinline__ void quad_turn(u32x4 (&v)[4]) {
+  const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    uint32_t a0 = v[0][d], a1 = v[1][d], a2 = v[2][d], a3 = v[3][d];
+    // every lane takes part in every exchange: they stand outside the selections
+    const uint32_t x0 = quad_x1(a0), x1 = quad_x1(a1), x2 = quad_x1(a2), x3 = quad_x1(a3);
+    const uint32_t b0 = odd ? x1 : a0, b1 = odd ? a1 : x0;
+    const uint32_t b2 = odd ? x3 : a2, b3 = odd ? a3 : x2;
+    const uint32_t y0 = quad_x2(b0), y1 = quad_x2(b1), y2 = quad_x2(b2), y3 = quad_x2(b3);
+    v[0][d] = high ? y2 : b0;
+    v[2][d] = high ? b2 : y0;
+    v[1][d] = high ? y3 : b1;
+    v[3][d] = high ? b3 : y1;
+  }
+}
+
+// lane group q of 16 lanes gets v[j] = group j's v[q]
+__device__ __forceinline__ void group_turn(u32x4 (&v)[4]) {
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    const auto a = __builtin_amdgcn_permlane16_swap(v[0][d], v[1][d], false, false);
+    const auto b = __builtin_amdgcn_permlane16_swap(v[2][d], v[3][d], false, false);
+    const auto e = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false);
+    const auto f = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
+    v[0][d] = e[0];
+    v[2][d] = e[1];
+    v[1][d] = f[0];
+    v[3][d] = f[1];
+  }
+}
+
 // 8 rows of 4 neighbouring columns (two dwords a row) turned into 4 fragments of 8 rows of
 // one column each: fragment t is column t
 __device__ __forceinline__ void turn_8x4(const uint32_t (&v)[8][2], u32x4 (&f)[4]) {
@@ -58,26 +106,30 @@ __device__ __forceinline__ void turn_8x4(const uint32_t (&v)[8][2], u32x4 (&f)[4
                                       (t & 1) ? 0x07060302u : 0x05040100u);
 }
 
-// Which rows a block works on. With a tile table (many rows) it is looked up; without one,
+// Which rows a block works on. With a tile table (many rows) it is looked up: block b takes
+// entry b % tiles, and of a tile of more than RT rows its part b / tiles. Without a table,
 // block b is the tile that starts at row b if the rows of the same adapter before b fill
 // whole tiles, and has nothing to do otherwise.
 struct Tiles {
   const int32_t* ids;
-  int M, G;
+  int M, G, tiles;
   const int32_t* sorted;      // null: no table
   const SortTile* table;
 };
 
-// false: no tile. Else *g (G: rows without an adapter), s_rows[0 .. *n).
+// false: no tile. Else *g (G: rows without an adapter), s_rows[0 .. *n); with a table *index,
+// the tile's number, and *n may be 0 for a tile's second part.
 template <int RT>
-__device__ __forceinline__ bool find_tile(const Tiles& t, int* g, int* n, int32_t* s_rows) {
+__device__ __forceinline__ bool find_tile(const Tiles& t, int* g, int* n, int* index, int32_t* s_rows) {
   const int b = blockIdx.x;
   if (t.sorted) {
-    const SortTile d = t.table[b];
+    const int part = b >= t.tiles;
+    const SortTile d = t.table[part ? b - t.tiles : b];
     if (d.group < 0) return false;
     *g = d.group;
-    *n = d.rows;
-    if ((int)threadIdx.x < d.rows) s_rows[threadIdx.x] = t.sorted[d.start + threadIdx.x];
+    *index = d.index;
+    *n = max(0, min(RT, d.rows - part * RT));
+    if ((int)threadIdx.x < *n) s_rows[threadIdx.x] = t.sorted[d.start + part * RT + threadIdx.x];
     __syncthreads();
     return true;
   }
@@ -107,60 +159,52 @@ __device__ __forceinline__ bool find_tile(const Tiles& t, int* g, int* n, int32_
 }
 
 // s_red = X_rows W_g^T over the steps [s0, s1) of the reduction axis K, rows x ranks. The W
-// waves of the block take the steps of 64 in turn; then the upper half of the waves hands
+// waves of the block take the steps of 128 in turn; then the upper half of the waves hands
 // its sums to the lower half through LDS, and the lower half leaves its sums in s_red[wave]
-// for the caller to add in wave order. DEPTH
-// steps' loads are in flight at a time (as many as the registers allow).
+// for the caller to add in wave order. In a step lane group q holds K elements 32q .. 32q + 31
+// of its row for four MFMAs: the order of the reduction axis is free as long as both operands
+// share it. DEPTH steps' loads are in flight at a time (as many as the registers allow).
 template <int MT, int NT, int W, int DEPTH>
 __device__ __forceinline__ void shrink_tile(const uint16_t* x, long xs, const uint16_t* w, int K,
                                             int r, int n, const int32_t* s_rows, int s0, int s1,
                                             float (*s_red)[MT * NT * 256]) {
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
-  const int c = lane & 15, q = lane >> 4;
-  const uint16_t* xp[MT];
-  const uint16_t* wp[NT];
+  const int c = lane & 15, q = lane >> 4, at = q * 32 + (c & 3) * 8;
+  const uint16_t* xp[MT][4];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int rr = i * 16 + c;
-    xp[i] = x + (long)s_rows[rr < n ? rr : 0] * xs + q * 8;
-  }
+  for (int i = 0; i < MT; ++i)
 #pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int rr = i * 16 + c;
-    wp[i] = w + (long)(rr < r ? rr : 0) * K + q * 8;
-  }
+    for (int j = 0; j < 4; ++j) {
+      const int rr = i * 16 + (c & 12) + j;
+      xp[i][j] = x + (long)s_rows[rr < n ? rr : 0] * xs + at;
+    }
   f32x4 acc[MT][NT] = {};
   struct Step {
-    u32x4 x[MT][2], w[NT][2];
+    u32x4 x[MT][4], w[NT][4];
   };
   auto load = [&](Step& v, int st) {
     const int k = st * kKStep;
-    if (k + kKStep <= K) {
+    const bool in = k + at < K;   // fails only in the last step of a K that is no multiple of 128
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+    for (int j = 0; j < 4; ++j) {
 #pragma unroll
-        for (int i = 0; i < MT; ++i) v.x[i][h] = load8(xp[i] + k + h * 32);
+      for (int i = 0; i < MT; ++i) v.x[i][j] = in ? load8(xp[i][j] + k) : u32x4{};
 #pragma unroll
-        for (int i = 0; i < NT; ++i) v.w[i][h] = load8(wp[i] + k + h * 32);
-      }
-    } else {  // the last step of a K that is no multiple of 64
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const bool in = k + h * 32 + q * 8 < K;
-#pragma unroll
-        for (int i = 0; i < MT; ++i) v.x[i][h] = in ? load8(xp[i] + k + h * 32) : u32x4{};
-#pragma unroll
-        for (int i = 0; i < NT; ++i) v.w[i][h] = in ? load8(wp[i] + k + h * 32) : u32x4{};
-      }
+      for (int i = 0; i < NT; ++i)
+        v.w[i][j] = in ? load8(w + (long)min(i * 16 + (c & 12) + j, r - 1) * K + k + at) : u32x4{};
     }
   };
-  auto multiply = [&](const Step& v) {
+  auto multiply = [&](Step& v) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int i = 0; i < MT; ++i) quad_turn(v.x[i]);
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+    for (int j = 0; j < NT; ++j) {
+      quad_turn(v.w[j]);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = mfma(v.x[i][h], v.w[j][h], acc[i][j]);
+      for (int h = 0; h < 4; ++h)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) acc[i][j] = mfma(v.x[i][h], v.w[j][h], acc[i][j]);
+    }
   };
   Step ring[DEPTH];
 #pragma unroll
@@ -189,12 +233,12 @@ __device__ __forceinline__ void shrink_tile(const uint16_t* x, long xs, const ui
   __syncthreads();
 }
 
-// W_g z of a tile's rows, added to base: each wave takes 64 columns at a time. The small
-// matrix is the MFMA's first operand with its rows dealt out so that a lane ends up with
-// columns 8q .. 8q + 7 and 32 + 8q .. 32 + 8q + 7 of one row of y: base and y move as 16-byte
-// accesses, the four lanes of a row on 64 contiguous bytes. A fragment of W serves both bf16 parts of z; up to rank 16 (KS = 0) both
-// parts share one MFMA. TR: W is [r, N] (its columns are neighbours, turned in registers),
-// else [N, r].
+// W_g z of a tile's rows, added to base: each wave takes 128 columns at a time. The small
+// matrix is the MFMA's first operand with its rows dealt out so that a lane ends up with 32
+// neighbouring columns of one row of y, four 16-byte pieces that are exchanged inside four
+// lanes on the way from base and to y. A fragment of W serves both bf16 parts of z; up to
+// rank 16 (KS = 0) both parts share one MFMA. TR: W is [r, N] (a lane's 8 columns of 8 ranks
+// are turned in registers), else [N, r].
 struct ColumnArgs {
   int r, N;
   const uint16_t* w;     // matrix of the tile's adapter
@@ -212,141 +256,124 @@ struct ZShape {
   static constexpr int kRow = kSteps * 32 + 8;   // LDS row, padded off the banks
 };
 
-template <int MT, int KS, bool TR>
+constexpr int kCols = 128;
+
+template <int KS, bool TR>
 struct Columns {
   using Z = ZShape<KS>;
   const ColumnArgs& a;
   const bool live;
   const int n, c, q;
-  long row[MT];
+  int row[4];   // rows this lane reads and writes, -1: none
 
-  // what one group of 64 columns reads: base, and the fragments of W (TR: as they lie)
+  // what a group of columns starts with: base, and W's part for the first rank step as it lies
   struct Load {
-    u32x4 b[MT][2];
-    u32x4 w[Z::kSteps][4];
+    u32x4 base[4], w[2][4];
   };
 
   __device__ __forceinline__ Columns(const ColumnArgs& a, bool live, int n, const int32_t* s_rows)
       : a(a), live(live), n(n), c(threadIdx.x & 15), q((threadIdx.x & (kWave - 1)) >> 4) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) row[i] = s_rows[i * 16 + c < n ? i * 16 + c : 0];
+    for (int j = 0; j < 4; ++j) row[j] = (c & 12) + j < n ? s_rows[(c & 12) + j] : -1;
   }
 
   __device__ __forceinline__ void load(Load& l, int cg) const {
-    const int n0 = cg * 64, col = n0 + q * 8;
+    const int col = cg * kCols + q * 32 + (c & 3) * 8;
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        l.b[i][h] = u32x4{};
-        if (a.base && i * 16 + c < n && col + h * 32 < a.N)
-          l.b[i][h] = load8(a.base + row[i] * a.bs + col + h * 32);
-      }
-#pragma unroll
-    for (int ks = 0; ks < Z::kSteps; ++ks) {
-      // ranks of this lane's fragment, of W as of z
+    for (int j = 0; j < 4; ++j) {
+      l.base[j] = u32x4{};
+      if (a.base && row[j] >= 0 && col < a.N) l.base[j] = load8(a.base + row[j] * a.bs + col);
+    }
+    if (live) load_w(l.w, cg, 0);
+  }
+
+  // W's part for rank step ks
+  __device__ __forceinline__ void load_w(u32x4 (&v)[2][4], int cg, int ks) const {
+    if constexpr (TR) {
       int ch = (ks * 4 + q) * 8;
-      const bool in = live && ch < (Z::kPack ? 2 * a.r : a.r);
+      const int col = cg * kCols + (c >> 2) * 32 + (c & 3) * 8;
+      const bool in = col < a.N && ch < (Z::kPack ? 2 * a.r : a.r);
       if (Z::kPack && ch >= a.r) ch -= a.r;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) l.w[ks][t] = u32x4{};
-      if constexpr (TR) {
-        const int wc = n0 + (c & 2) * 16 + (c >> 2) * 8 + (c & 1) * 4;
-        if (in && wc < a.N) {
+      for (int e = 0; e < 8; ++e)
+        v[e >> 2][e & 3] = in ? load8(a.w + (long)(ch + e) * a.N + col) : u32x4{};
+    } else {
+      int ch = (ks * 4 + (c & 3)) * 8;
+      const bool in = ch < (Z::kPack ? 2 * a.r : a.r);
+      if (Z::kPack && ch >= a.r) ch -= a.r;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const Half4 h = *reinterpret_cast<const Half4*>(a.w + (long)(ch + j) * a.N + wc);
-            l.w[ks][j >> 1][(j & 1) * 2] = h.w[0];
-            l.w[ks][j >> 1][(j & 1) * 2 + 1] = h.w[1];
-          }
-        }
-      } else if (in) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int wc = min(n0 + (t >> 1) * 32 + (c >> 2) * 8 + (t & 1) * 4 + (c & 3), a.N - 1);
-          l.w[ks][t] = load8(a.w + (long)wc * a.r + ch);
-        }
+      for (int e = 0; e < 8; ++e) {
+        const int col = min(cg * kCols + (c >> 2) * 32 + ((e & 4) + q) * 4 + (e & 3), a.N - 1);
+        v[e >> 2][e & 3] = in ? load8(a.w + (long)col * a.r + ch) : u32x4{};
       }
     }
   }
 
-  __device__ __forceinline__ void finish(const Load& l, int cg, const u32x4 (&zf)[MT][Z::kSteps][Z::kParts]) const {
-    const int col = cg * 64 + q * 8;
-    f32x4 acc[MT][4] = {};
+  // base, W and z of one group of columns into y
+  __device__ __forceinline__ void finish(Load& l, int cg, const u32x4 (&zf)[Z::kSteps][Z::kParts]) const {
+    const int col = cg * kCols + q * 32 + (c & 3) * 8;
     if (live) {
+      f32x4 acc[8] = {};
 #pragma unroll
       for (int ks = 0; ks < Z::kSteps; ++ks) {
-        u32x4 wf[4];
-        if constexpr (TR) {
-          uint32_t v[8][2];
+        if (ks) load_w(l.w, cg, ks);
+        if constexpr (!TR) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            v[j][0] = l.w[ks][j >> 1][(j & 1) * 2];
-            v[j][1] = l.w[ks][j >> 1][(j & 1) * 2 + 1];
+          for (int h = 0; h < 2; ++h) {
+            quad_turn(l.w[h]);
+            group_turn(l.w[h]);
           }
-          turn_8x4(v, wf);
-        } else {
-#pragma unroll
-          for (int t = 0; t < 4; ++t) wf[t] = l.w[ks][t];
         }
 #pragma unroll
-        for (int p = 0; p < Z::kParts; ++p)
+        for (int t = 0; t < 8; ++t) {
+          u32x4 f;
+          if constexpr (TR) {  // column t of 8 ranks
 #pragma unroll
-          for (int i = 0; i < MT; ++i)
+            for (int p = 0; p < 4; ++p)
+              f[p] = __builtin_amdgcn_perm(l.w[p >> 1][(2 * p + 1) & 3][t >> 1],
+                                           l.w[p >> 1][(2 * p) & 3][t >> 1],
+                                           (t & 1) ? 0x07060302u : 0x05040100u);
+          } else {
+            f = l.w[t >> 2][t & 3];
+          }
 #pragma unroll
-            for (int t = 0; t < 4; ++t) acc[i][t] = mfma(wf[t], zf[i][ks][p], acc[i][t]);
+          for (int p = 0; p < Z::kParts; ++p) acc[t] = mfma(f, zf[ks][p], acc[t]);
+        }
       }
-    }
+      quad_turn(l.base);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      if (i * 16 + c >= n) continue;
-      // value o of the lane's 16: fragment o / 4, element o % 4 (TR: the other way round)
-      auto at = [&](int o) { return TR ? acc[i][o & 3][o >> 2] : acc[i][o >> 2][o & 3]; };
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (col + h * 32 >= a.N) continue;
-        Half8 o;
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-          const uint32_t bp = l.b[i][h][p];
-          o.w[p] = live ? pack_bf16(bf16_lo(bp) + at(h * 8 + 2 * p), bf16_hi(bp) + at(h * 8 + 2 * p + 1))
-                        : bp;
+          // columns 8j + 2p, 8j + 2p + 1 of the lane's 32
+          const uint32_t bp = l.base[j][p];
+          const float lo = TR ? acc[2 * p][j] : acc[2 * j + (p >> 1)][(p & 1) * 2];
+          const float hi = TR ? acc[2 * p + 1][j] : acc[2 * j + (p >> 1)][(p & 1) * 2 + 1];
+          l.base[j][p] = pack_bf16(bf16_lo(bp) + lo, bf16_hi(bp) + hi);
         }
-        *reinterpret_cast<Half8*>(a.y + row[i] * a.ys + col + h * 32) = o;
-      }
+      quad_turn(l.base);
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (row[j] >= 0 && col < a.N) {
+        const u32x4 v = l.base[j];
+        *reinterpret_cast<Half8*>(a.y + row[j] * a.ys + col) = Half8{{v[0], v[1], v[2], v[3]}};
+      }
   }
 
-  // groups cg, cg + W, ... below g1; `first` holds the loads of group cg. AHEAD: a second
-  // set of loads is in flight (where there are registers for it).
-  template <int W, bool AHEAD>
-  __device__ __forceinline__ void run(Load& first, int cg, int g1,
-                                      const uint16_t (*s_z)[MT * 16 * Z::kRow]) const {
-    u32x4 zf[MT][Z::kSteps][Z::kParts];
+  // groups cg, cg + W, ... below g1; `l` holds the loads of group cg
+  template <int W>
+  __device__ __forceinline__ void run(Load& l, int cg, int g1, const uint16_t (*s_z)[16 * Z::kRow]) const {
+    u32x4 zf[Z::kSteps][Z::kParts];
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int ks = 0; ks < Z::kSteps; ++ks)
 #pragma unroll
-      for (int ks = 0; ks < Z::kSteps; ++ks)
-#pragma unroll
-        for (int p = 0; p < Z::kParts; ++p)
-          zf[i][ks][p] = *reinterpret_cast<const u32x4*>(&s_z[p][(i * 16 + c) * Z::kRow + ks * 32 + q * 8]);
-    if constexpr (!AHEAD) {
-      while (cg < g1) {
-        finish(first, cg, zf);
-        cg += W;
-        if (cg < g1) load(first, cg);
-      }
-      return;
-    }
-    Load next;
+      for (int p = 0; p < Z::kParts; ++p)
+        zf[ks][p] = *reinterpret_cast<const u32x4*>(&s_z[p][c * Z::kRow + ks * 32 + q * 8]);
     while (cg < g1) {
-      if (cg + W < g1) load(next, cg + W);
-      finish(first, cg, zf);
+      finish(l, cg, zf);
       cg += W;
-      if (cg >= g1) break;
-      if (cg + W < g1) load(first, cg + W);
-      finish(next, cg, zf);
-      cg += W;
+      if (cg < g1) load(l, cg);
     }
   }
 };
@@ -387,18 +414,18 @@ struct ShrinkArgs {
   float* part;         // [splits, M, r]
 };
 
-constexpr int kShrinkWaves = 8;
+constexpr int kShrinkWaves = 4;
 
 // part[s][m] = W_g x[m] over split s of K
 template <int MT, int NT>
 __global__ __launch_bounds__(kShrinkWaves* kWave) void lora_shrink_kernel(ShrinkArgs a) {
   __shared__ int32_t s_rows[MT * 16];
   __shared__ __align__(16) float s_red[kShrinkWaves / 2][MT * NT * 256];
-  int g, n;
-  if (!find_tile<MT * 16>(a.tiles, &g, &n, s_rows)) return;
+  int g, n, index;
+  if (!find_tile<MT * 16>(a.tiles, &g, &n, &index, s_rows)) return;
   if (g == a.tiles.G) return;
   const int steps = (a.K + kKStep - 1) / kKStep;
-  shrink_tile<MT, NT, kShrinkWaves, (MT + NT <= 3 ? 4 : 2)>(a.x, a.xs, a.w + (long)g * a.r * a.K, a.K, a.r, n, s_rows,
+  shrink_tile<MT, NT, kShrinkWaves, (MT + NT <= 3 ? 2 : 1)>(a.x, a.xs, a.w + (long)g * a.r * a.K, a.K, a.r, n, s_rows,
                                     (int)((long)steps * blockIdx.y / a.splits),
                                     (int)((long)steps * (blockIdx.y + 1) / a.splits), s_red);
   float* out = a.part + (long)blockIdx.y * a.tiles.M * a.r;
@@ -421,32 +448,67 @@ struct ExpandArgs {
   int splits;
   const float* scale;    // [G]
   float* z;              // may be null
-  bool scaled_z;         // z receives scale * z
-  int col_groups;        // groups of 64 columns a block takes
+  int col_groups;        // groups of 128 columns a block takes
   ColumnArgs c;          // w: all adapters' matrices
+  // TR (backward): where the fragments of scale dz and scale z go, and z
+  uint16_t* frag[2];
+  const float* fz;
 };
 
 constexpr int kExpandWaves = 4;
 
+// rank / 16 rounded up to a power of two: rank tiles of the products over K and over rows
+__host__ __device__ constexpr int rank_tiles(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : r <= 64 ? 4 : 8; }
+
+// Half a tile of 32 rows of P [rows, r] (rows 16 half .. 16 half + 15) as the MFMA fragments
+// that sums over rows need: for each of three bf16 parts and each 16 ranks, lane (rank c, row
+// group q) holds rows 8q .. 8q + 7 of its rank, 1 KiB together. s_p: the half's rows, fp32;
+// rows past n and ranks past r are zeros.
+template <int LD>
+__device__ __forceinline__ void put_parts(const float (*s_p)[LD], int half, int n, int r, uint16_t* out) {
+  const int nt = rank_tiles(r);
+  for (int o = threadIdx.x; o < nt * 32; o += blockDim.x) {
+    const int lane = o & 31, i = o / 32;
+    const int rank = i * 16 + (lane & 15), row = (lane >> 4) * 8;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = rank < r && row + e < n ? s_p[row + e][rank] : 0.f;
+#pragma unroll
+    for (int part = 0; part < 3; ++part) {
+      Half8 h;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        h.w[p] = pack_bf16(v[2 * p], v[2 * p + 1]);
+        v[2 * p] = bf16_rest(v[2 * p], bf16_lo(h.w[p]));
+        v[2 * p + 1] = bf16_rest(v[2 * p + 1], bf16_hi(h.w[p]));
+      }
+      *reinterpret_cast<Half8*>(out + ((part * nt + i) * kWave + half * 32 + lane) * 8) = h;
+    }
+  }
+}
+
 // y = base + W_g (scale z): z's splits are added in order, scaled, split into two bf16 parts
-// and kept in LDS for the block's columns
-template <int MT, int KS, bool TR>
+// and kept in LDS for the block's columns. In the backward pass (TR) the first block of a
+// tile also leaves scale dz as fragments for the weight gradients, the last one scale z.
+template <int KS, bool TR>
 __global__ __launch_bounds__(kExpandWaves* kWave) void lora_expand_kernel(ExpandArgs a) {
   using Z = ZShape<KS>;
-  constexpr int RT = MT * 16;
-  __shared__ int32_t s_rows[RT];
-  __shared__ __align__(16) uint16_t s_z[Z::kParts][RT * Z::kRow];
-  int g, n;
-  if (!find_tile<RT>(a.tiles, &g, &n, s_rows)) return;
+  constexpr int kLd = TR ? Z::kSteps * 32 + 4 : 1;
+  __shared__ int32_t s_rows[16];
+  __shared__ __align__(16) uint16_t s_z[Z::kParts][16 * Z::kRow];
+  __shared__ __align__(16) float s_p[TR ? 16 : 1][kLd];
+  int g, n, index;
+  if (!find_tile<16>(a.tiles, &g, &n, &index, s_rows)) return;
   const bool live = g != a.tiles.G;
   const int r = a.c.r, quads = r / 4;
   ColumnArgs ca = a.c;
   if (live) ca.w += (long)g * ca.N * r;
-  const Columns<MT, KS, TR> cols(ca, live, n, s_rows);
-  const int g0 = blockIdx.y * a.col_groups, g1 = min(g0 + a.col_groups, (ca.N + 63) / 64);
+  const Columns<KS, TR> cols(ca, live, n, s_rows);
+  const int g0 = blockIdx.y * a.col_groups, g1 = min(g0 + a.col_groups, (ca.N + kCols - 1) / kCols);
   const int cg = g0 + (threadIdx.x >> 6);
-  typename Columns<MT, KS, TR>::Load first;  // on the way while z is put together
+  typename Columns<KS, TR>::Load first;  // on the way while z is put together
   if (cg < g1) cols.load(first, cg);
+  const bool head = blockIdx.y == 0;
   if (live) {
     const float sc = a.scale[g];
     const long part = (long)a.tiles.M * r;
@@ -459,23 +521,39 @@ __global__ __launch_bounds__(kExpandWaves* kWave) void lora_expand_kernel(Expand
         const float4 f = *reinterpret_cast<const float4*>(p + s * part);
         v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
       }
-      float sv[4];
+      if (!TR && a.z && head)
+        *reinterpret_cast<float4*>(a.z + (long)s_rows[row] * r + col) = make_float4(v[0], v[1], v[2], v[3]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sv[e] = v[e] * sc;
-      if (a.z && blockIdx.y == 0) {
-        const float* o = a.scaled_z ? sv : v;
-        *reinterpret_cast<float4*>(a.z + (long)s_rows[row] * r + col) = make_float4(o[0], o[1], o[2], o[3]);
-      }
-      put_z<KS>(s_z, row, col, r, sv);
+      for (int e = 0; e < 4; ++e) v[e] *= sc;
+      put_z<KS>(s_z, row, col, r, v);
+      if (TR && head) *reinterpret_cast<float4*>(&s_p[row][col]) = make_float4(v[0], v[1], v[2], v[3]);
     }
-    pad_z<KS, RT>(s_z, r);
-  } else if (a.z && blockIdx.y == 0) {
+    pad_z<KS, 16>(s_z, r);
+    if constexpr (TR) {
+      const int half = (int)blockIdx.x >= a.tiles.tiles;
+      const long at = (long)index * 3 * rank_tiles(r) * 512;
+      if (head) {
+        __syncthreads();
+        put_parts(s_p, half, n, r, a.frag[0] + at);
+      }
+      if (blockIdx.y == gridDim.y - 1) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < n * quads; i += kExpandWaves * kWave) {
+          const int row = i / quads, col = i % quads * 4;
+          const float4 f = *reinterpret_cast<const float4*>(a.fz + (long)s_rows[row] * r + col);
+          *reinterpret_cast<float4*>(&s_p[row][col]) = make_float4(f.x * sc, f.y * sc, f.z * sc, f.w * sc);
+        }
+        __syncthreads();
+        put_parts(s_p, half, n, r, a.frag[1] + at);
+      }
+    }
+  } else if (!TR && a.z && head) {
     for (int i = threadIdx.x; i < n * r; i += kExpandWaves * kWave)
       a.z[(long)s_rows[i / r] * r + i % r] = 0.f;
   }
   __syncthreads();
   if (!live && a.c.base == a.c.y) return;  // rows without an adapter stay
-  cols.template run<kExpandWaves, (KS <= 2)>(first, cg, g1, s_z);
+  cols.template run<kExpandWaves>(first, cg, g1, s_z);
 }
 
 struct FusedArgs {
@@ -490,10 +568,10 @@ struct FusedArgs {
   ColumnArgs c;
 };
 
-constexpr int kFusedWaves = 16;
+constexpr int kFusedWaves = 8;
 
-// Both products of a tile of 16 rows in one block, for few rows: the sixteen waves split K,
-// z never leaves LDS, then they split the block's columns. Blocks of one tile that take
+// Both products of a tile of 16 rows in one block, for few rows: the waves split K, z never
+// leaves LDS, then they split the block's columns. Blocks of one tile that take
 // different columns repeat the first product (its matrix comes from L2 again).
 template <int NT, int KS>
 __global__ __launch_bounds__(kFusedWaves* kWave) void lora_fused_kernel(FusedArgs a) {
@@ -501,21 +579,19 @@ __global__ __launch_bounds__(kFusedWaves* kWave) void lora_fused_kernel(FusedArg
   __shared__ int32_t s_rows[16];
   __shared__ __align__(16) float s_red[kFusedWaves / 2][NT * 256];
   __shared__ __align__(16) uint16_t s_z[Z::kParts][16 * Z::kRow];
-  int g, n;
-  if (!find_tile<16>(a.tiles, &g, &n, s_rows)) return;
+  int g, n, index;
+  if (!find_tile<16>(a.tiles, &g, &n, &index, s_rows)) return;
   const bool live = g != a.tiles.G;
   const int r = a.c.r;
   ColumnArgs ca = a.c;
   if (live) ca.w += (long)g * ca.N * r;
-  const Columns<1, KS, false> cols(ca, live, n, s_rows);
-  const int g0 = blockIdx.y * a.col_groups, g1 = min(g0 + a.col_groups, (ca.N + 63) / 64);
+  const Columns<KS, false> cols(ca, live, n, s_rows);
+  const int g0 = blockIdx.y * a.col_groups, g1 = min(g0 + a.col_groups, (ca.N + kCols - 1) / kCols);
   const int cg = g0 + (threadIdx.x >> 6);
-  // on the way during the first product (beyond rank 32 there are no registers for that)
-  typename Columns<1, KS, false>::Load first;
-  if (KS < 2 && cg < g1) cols.load(first, cg);
+  typename Columns<KS, false>::Load first;  // on the way during the first product
+  if (cg < g1) cols.load(first, cg);
   if (live) {
-    // 1024 threads have 128 registers each
-    shrink_tile<1, NT, kFusedWaves, (NT == 1 ? 3 : 1)>(a.x, a.xs, a.wa + (long)g * r * a.K, a.K, r, n, s_rows,
+    shrink_tile<1, NT, kFusedWaves, (NT == 1 ? 4 : NT == 2 ? 2 : 1)>(a.x, a.xs, a.wa + (long)g * r * a.K, a.K, r, n, s_rows,
                                                0, (a.K + kKStep - 1) / kKStep, s_red);
     const float sc = a.scale[g];
     for (int i = threadIdx.x; i < n * NT * 4; i += kFusedWaves * kWave) {
@@ -540,17 +616,16 @@ __global__ __launch_bounds__(kFusedWaves* kWave) void lora_fused_kernel(FusedArg
   }
   __syncthreads();
   if (!live && a.c.base == a.c.y) return;  // rows without an adapter stay
-  if (KS >= 2 && cg < g1) cols.load(first, cg);
-  cols.template run<kFusedWaves, (KS < 2)>(first, cg, g1, s_z);
+  cols.template run<kFusedWaves>(first, cg, g1, s_z);
 }
 
 struct WgradArgs {
   const int32_t* sorted;
   const int32_t* off;
+  const int32_t* tile_first;
   int r;
-  const float* scale;
-  // two products: [0] P = dz (scaled), X = x, out dA [G, r, C]; [1] P = z, X = dy, out dB [G, C, r]
-  const float* p[2];
+  // two products: [0] P = scale dz, X = x, out dA [G, r, C]; [1] P = scale z, X = dy, out dB [G, C, r]
+  const uint16_t* p[2];   // fragments of P, see Parts
   const uint16_t* x[2];
   long xs[2];
   int C[2], blocks[2];
@@ -562,12 +637,13 @@ constexpr int kWgradWaves = kWgradThreads / kWave;
 constexpr int kWgradRows = 2048;  // row indices kept in LDS at a time
 
 // out_g[p, c] = sum over the rows m of group g of P[m, p] X[m, c]. The reduction axis is the
-// row, so both operands are needed transposed: a lane reads 8 rows of 4 neighbouring columns
-// (8 bytes each, 128 contiguous bytes a row over 16 lanes) and turns them in registers into
-// the fragments of 4 MFMAs. P goes in as three bf16 parts (24 bits), so the fp32 result
-// carries no bf16 rounding. The block's eight waves take steps of 32 rows in turn, the next
-// step's loads in flight, and add up through LDS in wave order. Rows past the group's end
-// are zero in both operands. Ranks past NT * 16 go to further blocks (grid z).
+// row, so both operands are needed transposed: of X a lane reads 8 rows of 4 neighbouring
+// columns (8 bytes each, 128 contiguous bytes a row over 16 lanes) and turns them in registers
+// into the fragments of 4 MFMAs; P lies ready as fragments, in three bf16 parts (24 bits), so
+// the fp32 result carries no bf16 rounding. The block's eight waves take steps of 32 rows (one
+// tile) in turn, the next step's loads in flight, and add up through LDS in wave order. Rows
+// past the group's end are zero in both operands. Ranks past NT * 16 go to further blocks
+// (grid z).
 template <int NT>
 __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) {
   __shared__ float s_red[kWgradWaves][16][68];
@@ -577,16 +653,16 @@ __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) 
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid >> 6;
   const int c = lane & 15, q = lane >> 4;
   const int m0 = a.off[g], m1 = a.off[g + 1];
-  const float* P = a.p[side];
+  const int nt = NT * gridDim.z, i0 = blockIdx.z * NT;
+  const uint16_t* P = a.p[side] + ((long)a.tile_first[g] * 3 * nt + i0) * 512 + lane * 8;
   const uint16_t* X = a.x[side];
   const long xs = a.xs[side];
   const int C = a.C[side];
-  const float sc = side ? a.scale[g] : 1.f;
-  const int col = c0 + c * 4, r0 = blockIdx.z * NT * 16;
+  const int col = c0 + c * 4;
   f32x4 acc[NT][4] = {};
   struct Step {
     uint32_t x[8][2];
-    float p[NT][8];
+    u32x4 p[3][NT];
   };
   for (int mb = m0; mb < m1; mb += kWgradRows) {
     const int rows = min(kWgradRows, m1 - mb);
@@ -594,45 +670,31 @@ __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) 
     for (int i = tid; i < rows; i += kWgradThreads) s_idx[i] = a.sorted[mb + i];
     __syncthreads();
     auto load = [&](Step& v, int m) {
+      const uint16_t* p = P + (long)((mb - m0 + m) >> 5) * 3 * nt * 512;
+#pragma unroll
+      for (int part = 0; part < 3; ++part)
+#pragma unroll
+        for (int i = 0; i < NT; ++i) v.p[part][i] = load8(p + (part * nt + i) * 512);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int at = m + q * 8 + j;
-        const bool in = at < rows;
-        const long row = in ? s_idx[at] : 0;
         v.x[j][0] = v.x[j][1] = 0;
-        if (in && col < C) {
-          const Half4 h = *reinterpret_cast<const Half4*>(X + row * xs + col);
+        if (at < rows && col < C) {
+          const Half4 h = *reinterpret_cast<const Half4*>(X + s_idx[at] * xs + col);
           v.x[j][0] = h.w[0];
           v.x[j][1] = h.w[1];
         }
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          const int rr = r0 + i * 16 + c;
-          v.p[i][j] = in && rr < a.r ? P[row * a.r + rr] : 0.f;
-        }
       }
     };
-    auto multiply = [&](Step& v) {
+    auto multiply = [&](const Step& v) {
       u32x4 xf[4];
       turn_8x4(v.x, xf);
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
+      for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v.p[i][j] *= sc;
+        for (int part = 0; part < 3; ++part)
 #pragma unroll
-        for (int part = 0; part < 3; ++part) {
-          u32x4 pf;
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            float &lo = v.p[i][2 * p], &hi = v.p[i][2 * p + 1];
-            pf[p] = pack_bf16(lo, hi);
-            lo = bf16_rest(lo, bf16_lo(pf[p]));
-            hi = bf16_rest(hi, bf16_hi(pf[p]));
-          }
-#pragma unroll
-          for (int t = 0; t < 4; ++t) acc[i][t] = mfma(pf, xf[t], acc[i][t]);
-        }
-      }
+          for (int t = 0; t < 4; ++t) acc[i][t] = mfma(v.p[part][i], xf[t], acc[i][t]);
     };
     constexpr int kStride = kWgradWaves * 32;
     Step u, v;
@@ -659,7 +721,7 @@ __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) 
     for (int o = tid; o < 16 * 64; o += kWgradThreads) {
       // columns run fastest in dA, ranks in dB
       const int pr = side ? o & 15 : o >> 6, cc = side ? o >> 4 : o & 63;
-      const int rr = r0 + i * 16 + pr, cl = c0 + cc;
+      const int rr = (i0 + i) * 16 + pr, cl = c0 + cc;
       if (rr >= a.r || cl >= C) continue;
       float s = 0.f;
 #pragma unroll
@@ -712,15 +774,15 @@ struct Plan {
 };
 
 // Tile rows from the mean number of rows an adapter has: 32 rows share one read of the
-// adapter's matrices, 16 waste less where adapters have few rows. Accumulators bound
-// mt * nt to 8.
+// adapter's matrices, 16 waste less where adapters have few rows. The backward pass takes 32,
+// the depth of its sums over rows.
 Plan plan_tiles(int M, int G, int K, int r, bool backward) {
   Plan p;
-  p.nt = r <= 16 ? 1 : r <= 32 ? 2 : r <= 64 ? 4 : 8;
+  p.nt = rank_tiles(r);
   p.table = backward || M > kDirectRows;
   p.fused = !p.table && r <= kFusedRank && (long)r * K * 2 <= kFusedBytes;
   const int mean = M / std::max(1, std::min(G, M));
-  p.mt = p.fused ? 1 : std::min(mean >= 24 ? 2 : 1, 8 / p.nt);
+  p.mt = backward ? 2 : !p.table || p.nt == 8 || mean < 24 ? 1 : 2;
   p.rt = p.mt * 16;
   const int most = M / p.rt + std::min(G + 1, M);
   p.tiles = p.table ? (most + 7) / 8 * 8 : M;  // the table is dealt out over 8 XCDs
@@ -732,13 +794,13 @@ Plan plan_tiles(int M, int G, int K, int r, bool backward) {
 // wave of a block, at most 16 partial sums to add up again.
 int plan_splits(const Plan& p, int K) {
   const int steps = (K + kKStep - 1) / kKStep;
-  return std::max(1, std::min({(512 + p.busy - 1) / p.busy, (steps + kShrinkWaves - 1) / kShrinkWaves, 16}));
+  return std::max(1, std::min({(768 + p.busy - 1) / p.busy, (steps + kShrinkWaves - 1) / kShrinkWaves, 16}));
 }
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 struct Space {
-  size_t sorted, off, counts, tile, part, dz, bt, total;
+  size_t sorted, off, counts, tile, tile_first, part, frag[2], bt, total;
 };
 
 Space plan_space(int M, int G, int K, int N, int r, bool backward) {
@@ -755,10 +817,11 @@ Space plan_space(int M, int G, int K, int N, int r, bool backward) {
     s.off = take((size_t)(G + 2) * 4);
     s.counts = take(sort_count_words(M, G + 1) * 4);
     s.tile = take((size_t)p.tiles * sizeof(SortTile));
+    s.tile_first = take((size_t)(G + 2) * 4);
   }
   if (!p.fused) s.part = take((size_t)plan_splits(p, backward ? N : K) * M * r * 4);
   if (backward) {
-    s.dz = take((size_t)M * r * 4);
+    for (size_t& f : s.frag) f = take((size_t)p.tiles * 3 * p.nt * 1024);
     s.bt = take((size_t)G * r * N * 2);
   }
   s.total = at;
@@ -767,7 +830,7 @@ Space plan_space(int M, int G, int K, int N, int r, bool backward) {
 
 hipError_t make_tiles(const int32_t* ids, int M, int G, const Plan& p, const Space& sp, char* scratch,
                       Tiles* t, hipStream_t s) {
-  *t = Tiles{ids, M, G, nullptr, nullptr};
+  *t = Tiles{ids, M, G, p.tiles, nullptr, nullptr};
   if (!p.table) return hipSuccess;
   GroupSort g{};
   g.ids = ids;
@@ -780,6 +843,7 @@ hipError_t make_tiles(const int32_t* ids, int M, int G, const Plan& p, const Spa
   g.tile_rows = p.rt;
   g.max_tiles = p.tiles;
   g.tile = reinterpret_cast<SortTile*>(scratch + sp.tile);
+  g.tile_first = reinterpret_cast<int32_t*>(scratch + sp.tile_first);
   t->sorted = g.sorted;
   t->table = g.tile;
   return launch_sort(g, s);
@@ -797,6 +861,7 @@ hipError_t shrink(const Plan& p, const ShrinkArgs& a, hipStream_t s) {
   HMOE_SHRINK(1, 4);
   HMOE_SHRINK(2, 4);
   HMOE_SHRINK(1, 8);
+  HMOE_SHRINK(2, 8);
 #undef HMOE_SHRINK
   return hipGetLastError();
 }
@@ -806,41 +871,34 @@ int z_steps(int r) { return r <= 16 ? 0 : (r + 31) / 32; }
 
 template <bool TR>
 hipError_t expand(const Plan& p, ExpandArgs a, hipStream_t s) {
-  const int groups = (a.c.N + 63) / 64;
-  // columns a block: a multiple of its four waves' 64, as wide as still leaves about 1024
+  const int groups = (a.c.N + kCols - 1) / kCols;
+  // columns a block: a multiple of its four waves' 128, as wide as still leaves about 1024
   // blocks, so that few blocks add up z's splits again
-  const int want = std::max(1, (1024 + p.busy - 1) / p.busy);
+  const int want = std::max(1, (1024 + p.busy * p.mt - 1) / (p.busy * p.mt));
   const int rounds = std::max(1, (groups + want * kExpandWaves - 1) / (want * kExpandWaves));
   a.col_groups = rounds * kExpandWaves;
-  const dim3 grid(p.tiles, (groups + a.col_groups - 1) / a.col_groups), block(kExpandWaves * kWave);
-  const int ks = z_steps(a.c.r);
-#define HMOE_EXPAND(MT, KS)                                                         \
-  if (p.mt == MT && ks == KS)                                                       \
-  hipLaunchKernelGGL((lora_expand_kernel<MT, KS, TR>), grid, block, 0, s, a)
-  HMOE_EXPAND(1, 0);
-  HMOE_EXPAND(2, 0);
-  HMOE_EXPAND(1, 1);
-  HMOE_EXPAND(2, 1);
-  HMOE_EXPAND(1, 2);
-  HMOE_EXPAND(2, 2);
-  HMOE_EXPAND(1, 3);
-  HMOE_EXPAND(1, 4);
-#undef HMOE_EXPAND
+  const dim3 grid(p.tiles * p.mt, (groups + a.col_groups - 1) / a.col_groups);
+  const dim3 block(kExpandWaves * kWave);
+  switch (z_steps(a.c.r)) {
+    case 0: hipLaunchKernelGGL((lora_expand_kernel<0, TR>), grid, block, 0, s, a); break;
+    case 1: hipLaunchKernelGGL((lora_expand_kernel<1, TR>), grid, block, 0, s, a); break;
+    case 2: hipLaunchKernelGGL((lora_expand_kernel<2, TR>), grid, block, 0, s, a); break;
+    case 3: hipLaunchKernelGGL((lora_expand_kernel<3, TR>), grid, block, 0, s, a); break;
+    default: hipLaunchKernelGGL((lora_expand_kernel<4, TR>), grid, block, 0, s, a); break;
+  }
   return hipGetLastError();
 }
 
+template <int NT, int KS>
 hipError_t fused(const Plan& p, FusedArgs a, hipStream_t s) {
-  const int groups = (a.c.N + 63) / 64;
-  // columns a block: a multiple of its sixteen waves' 64, about 256 blocks in all
+  constexpr int kWaves = kFusedWaves;
+  const int groups = (a.c.N + kCols - 1) / kCols;
+  // columns a block: a multiple of its waves' 128, about 256 blocks in all
   const int want = std::max(1, 256 / p.busy);
-  const int rounds = std::max(1, (groups + want * kFusedWaves - 1) / (want * kFusedWaves));
-  a.col_groups = rounds * kFusedWaves;
-  const dim3 grid(p.tiles, (groups + a.col_groups - 1) / a.col_groups), block(kFusedWaves * kWave);
-  switch (z_steps(a.c.r)) {
-    case 0: hipLaunchKernelGGL((lora_fused_kernel<1, 0>), grid, block, 0, s, a); break;
-    case 1: hipLaunchKernelGGL((lora_fused_kernel<2, 1>), grid, block, 0, s, a); break;
-    default: hipLaunchKernelGGL((lora_fused_kernel<4, 2>), grid, block, 0, s, a); break;
-  }
+  const int rounds = std::max(1, (groups + want * kWaves - 1) / (want * kWaves));
+  a.col_groups = rounds * kWaves;
+  const dim3 grid(p.tiles, (groups + a.col_groups - 1) / a.col_groups);
+  hipLaunchKernelGGL((lora_fused_kernel<NT, KS>), grid, dim3(kWaves * kWave), 0, s, a);
   return hipGetLastError();
 }
 
@@ -855,9 +913,14 @@ hipError_t launch_lora(const Lora& l, void* scratch, hipStream_t s) {
   char* b = static_cast<char*>(scratch);
   const Plan p = plan_tiles(l.M, l.G, l.K, l.r, false);
   const ColumnArgs c{l.r, l.N, l.B, l.base, l.bs, l.y, l.ys};
-  if (p.fused)
-    return fused(p, FusedArgs{Tiles{l.ids, l.M, l.G, nullptr, nullptr}, l.x, l.xs, l.A, l.K, l.scale, l.z,
-                              0, c}, s);
+  if (p.fused) {
+    const FusedArgs a{Tiles{l.ids, l.M, l.G, p.tiles, nullptr, nullptr}, l.x, l.xs, l.A, l.K, l.scale, l.z, 0, c};
+    switch (z_steps(l.r)) {
+      case 0: return fused<1, 0>(p, a, s);
+      case 1: return fused<2, 1>(p, a, s);
+      default: return fused<4, 2>(p, a, s);
+    }
+  }
   const Space sp = plan_space(l.M, l.G, l.K, l.N, l.r, false);
   Tiles t;
   hipError_t err = make_tiles(l.ids, l.M, l.G, p, sp, b, &t, s);
@@ -866,7 +929,7 @@ hipError_t launch_lora(const Lora& l, void* scratch, hipStream_t s) {
   float* part = reinterpret_cast<float*>(b + sp.part);
   err = shrink(p, ShrinkArgs{t, l.x, l.xs, l.A, l.K, l.r, splits, part}, s);
   if (err != hipSuccess) return err;
-  return expand<false>(p, ExpandArgs{t, part, splits, l.scale, l.z, false, 0, c}, s);
+  return expand<false>(p, ExpandArgs{t, part, splits, l.scale, l.z, 0, c, {}, nullptr}, s);
 }
 
 hipError_t launch_lora_backward(const LoraGrad& l, void* scratch, hipStream_t s) {
@@ -876,7 +939,7 @@ hipError_t launch_lora_backward(const LoraGrad& l, void* scratch, hipStream_t s)
   Tiles t;
   hipError_t err = make_tiles(l.ids, l.M, l.G, p, sp, b, &t, s);
   if (err != hipSuccess) return err;
-  float* dz = reinterpret_cast<float*>(b + sp.dz);
+  uint16_t* frag[2] = {reinterpret_cast<uint16_t*>(b + sp.frag[0]), reinterpret_cast<uint16_t*>(b + sp.frag[1])};
   if (l.M > 0) {
     uint16_t* Bt = reinterpret_cast<uint16_t*>(b + sp.bt);
     const long blocks = ((long)l.G * (l.r / 8) * (l.N / 8) + 255) / 256;
@@ -888,11 +951,12 @@ hipError_t launch_lora_backward(const LoraGrad& l, void* scratch, hipStream_t s)
     err = shrink(p, ShrinkArgs{t, l.dy, l.dys, Bt, l.N, l.r, splits, part}, s);
     if (err != hipSuccess) return err;
     const ColumnArgs c{l.r, l.K, l.A, l.dbase, l.dbs, l.dx, l.dxs};
-    err = expand<true>(p, ExpandArgs{t, part, splits, l.scale, dz, true, 0, c}, s);
+    err = expand<true>(p, ExpandArgs{t, part, splits, l.scale, nullptr, 0, c, {frag[0], frag[1]}, l.z}, s);
     if (err != hipSuccess) return err;
   }
   const int32_t* off = reinterpret_cast<const int32_t*>(b + sp.off);
-  WgradArgs w{t.sorted, off, l.r, l.scale, {dz, l.z}, {l.x, l.dy}, {l.xs, l.dys}, {l.K, l.N},
+  const int32_t* tile_first = reinterpret_cast<const int32_t*>(b + sp.tile_first);
+  WgradArgs w{t.sorted, off, tile_first, l.r, {frag[0], frag[1]}, {l.x, l.dy}, {l.xs, l.dys}, {l.K, l.N},
               {(l.K + 63) / 64, (l.N + 63) / 64}, {l.dA, l.dB}};
   const dim3 grid(w.blocks[0] + w.blocks[1], l.G, p.nt == 8 ? 2 : 1), block(kWgradThreads);
   switch (p.nt) {

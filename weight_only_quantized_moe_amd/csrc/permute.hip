@@ -40,6 +40,7 @@ struct SortArgs {
   int tile_rows;        // rows per tile of the tile table (0: no table)
   int max_tiles;
   SortTile* tile;
+  int32_t* tile_first;  // [groups + 1]
 };
 
 // group of an id: ids outside [0, G) are dropped (-1) or the group behind the last
@@ -182,10 +183,14 @@ __global__ __launch_bounds__(THREADS) void sort_place_kernel(SortArgs a) {
       if (e < a.groups) {
         s_tile[e] = tx;
         s_base[e] = excl;
+        if (blockIdx.x == 0) a.tile_first[e] = tx;
       }
     }
   }
-  if (blockIdx.x == 0 && tid == 0) a.off[a.groups] = placed;
+  if (blockIdx.x == 0 && tid == 0) {
+    a.off[a.groups] = placed;
+    if (a.tile_rows) a.tile_first[a.groups] = tiles;
+  }
   __syncthreads();
   const int gid = blockIdx.x * THREADS + tid, gsz = gridDim.x * THREADS;
   for (int i = placed + gid; i < a.n; i += gsz) a.sorted[i] = -1;
@@ -207,6 +212,7 @@ __global__ __launch_bounds__(THREADS) void sort_place_kernel(SortArgs a) {
         d.group = lo;
         d.start = s_base[lo] + (t - s_tile[lo]) * a.tile_rows;
         d.rows = min(a.tile_rows, end - d.start);
+        d.index = t;
       }
       a.tile[i] = d;
     }
@@ -263,6 +269,7 @@ hipError_t launch_sort(const GroupSort& g, hipStream_t s) {
   a.tile_rows = g.tile_rows;
   a.max_tiles = g.max_tiles;
   a.tile = g.tile;
+  a.tile_first = g.tile_first;
   if (a.nb > 1) hipLaunchKernelGGL(sort_count_kernel, dim3(a.nb), dim3(kSortWide), 0, s, a);
   if (g.groups <= kSortWideGroups)
     hipLaunchKernelGGL(sort_place_kernel<kSortWide>, dim3(a.nb), dim3(kSortWide), 0, s, a);
