@@ -35,6 +35,10 @@ __device__ __forceinline__ u32x4 load8(const uint16_t* p) {
   const Half8 h = *reinterpret_cast<const Half8*>(p);
   return u32x4{h.w[0], h.w[1], h.w[2], h.w[3]};
 }
+// the same from a wave-uniform base and a 32-bit byte offset of the lane (one register)
+__device__ __forceinline__ u32x4 load8(const uint16_t* base, uint32_t bytes) {
+  return load8(reinterpret_cast<const uint16_t*>(reinterpret_cast<const char*>(base) + bytes));
+}
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
                                                  __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -129,7 +133,9 @@ __device__ __forceinline__ bool find_tile(const Tiles& t, int* g, int* n, int* i
     *g = d.group;
     *index = d.index;
     *n = max(0, min(RT, d.rows - part * RT));
-    if ((int)threadIdx.x < *n) s_rows[threadIdx.x] = t.sorted[d.start + part * RT + threadIdx.x];
+    // places past *n name row 0, so that whatever reads them stays inside the matrices
+    if (threadIdx.x < RT)
+      s_rows[threadIdx.x] = (int)threadIdx.x < *n ? t.sorted[d.start + part * RT + threadIdx.x] : 0;
     __syncthreads();
     return true;
   }
@@ -176,22 +182,38 @@ __device__ __forceinline__ void shrink_tile(const uint16_t* x, long xs, const ui
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int rr = i * 16 + (c & 12) + j;
-      xp[i][j] = x + (long)s_rows[rr < n ? rr : 0] * xs + at;
+      xp[i][j] = x + (long)s_rows[rr < n ? rr : 0] * xs;
     }
   f32x4 acc[MT][NT] = {};
   struct Step {
     u32x4 x[MT][4], w[NT][4];
   };
+  // No load stands behind a branch, so that a step's loads leave together. In the last step of
+  // a K that is no multiple of 128, lanes past the end read the step's start and their part of
+  // x is zeroed (W is finite). Ranks come in eights: four ranks of a tile all exist, or the
+  // lane reads others instead.
   auto load = [&](Step& v, int st) {
     const int k = st * kKStep;
-    const bool in = k + at < K;   // fails only in the last step of a K that is no multiple of 128
+    const bool in = k + at < K;
+    const int o = in ? k + at : k;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int i = 0; i < MT; ++i) v.x[i][j] = in ? load8(xp[i][j] + k) : u32x4{};
+      for (int j = 0; j < 4; ++j) v.x[i][j] = load8(xp[i][j] + o);
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
-        v.w[i][j] = in ? load8(w + (long)min(i * 16 + (c & 12) + j, r - 1) * K + k + at) : u32x4{};
+    for (int i = 0; i < NT; ++i) {
+      const int rank = i * 16 + (c & 12);
+      const uint32_t off = ((rank < r ? rank : 0) * K + o) * 2;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v.w[i][j] = load8(w + (long)j * K, off);
+    }
+    if (k + kKStep > K) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int d = 0; d < 4; ++d) v.x[i][j][d] = in ? v.x[i][j][d] : 0u;
     }
   };
   auto multiply = [&](Step& v) {
@@ -264,7 +286,7 @@ struct Columns {
   const ColumnArgs& a;
   const bool live;
   const int n, c, q;
-  int row[4];   // rows this lane reads and writes, -1: none
+  int row[4];   // rows this lane reads, and writes below n
 
   // what a group of columns starts with: base, and W's part for the first rank step as it lies
   struct Load {
@@ -274,49 +296,55 @@ struct Columns {
   __device__ __forceinline__ Columns(const ColumnArgs& a, bool live, int n, const int32_t* s_rows)
       : a(a), live(live), n(n), c(threadIdx.x & 15), q((threadIdx.x & (kWave - 1)) >> 4) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) row[j] = (c & 12) + j < n ? s_rows[(c & 12) + j] : -1;
+    for (int j = 0; j < 4; ++j) row[j] = s_rows[(c & 12) + j < n ? (c & 12) + j : 0];
   }
 
+  // No load stands behind a lane's own branch, so that they leave together: a lane without a
+  // row, column or rank of its own reads another one, which then goes nowhere (ranks: meets
+  // zeros of z, W being finite).
   __device__ __forceinline__ void load(Load& l, int cg) const {
-    const int col = cg * kCols + q * 32 + (c & 3) * 8;
+    const int col = cg * kCols + q * 32 + (c & 3) * 8, o = col < a.N ? col : 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      l.base[j] = u32x4{};
-      if (a.base && row[j] >= 0 && col < a.N) l.base[j] = load8(a.base + row[j] * a.bs + col);
-    }
+    for (int j = 0; j < 4; ++j)
+      l.base[j] = a.base ? load8(a.base + row[j] * a.bs + o) : u32x4{};
     if (live) load_w(l.w, cg, 0);
   }
 
-  // W's part for rank step ks
+  // W's part for rank step ks (columns and ranks come in eights: four rows or columns of W that
+  // a lane reads all exist, or it reads others instead)
   __device__ __forceinline__ void load_w(u32x4 (&v)[2][4], int cg, int ks) const {
     if constexpr (TR) {
       int ch = (ks * 4 + q) * 8;
+      if (ch >= a.r) ch = Z::kPack && ch < 2 * a.r ? ch - a.r : 0;
       const int col = cg * kCols + (c >> 2) * 32 + (c & 3) * 8;
-      const bool in = col < a.N && ch < (Z::kPack ? 2 * a.r : a.r);
-      if (Z::kPack && ch >= a.r) ch -= a.r;
+      const uint32_t off = (ch * a.N + (col < a.N ? col : 0)) * 2;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        v[e >> 2][e & 3] = in ? load8(a.w + (long)(ch + e) * a.N + col) : u32x4{};
+      for (int e = 0; e < 8; ++e) v[e >> 2][e & 3] = load8(a.w + (long)e * a.N, off);
     } else {
       int ch = (ks * 4 + (c & 3)) * 8;
-      const bool in = ch < (Z::kPack ? 2 * a.r : a.r);
-      if (Z::kPack && ch >= a.r) ch -= a.r;
+      if (ch >= a.r) ch = Z::kPack && ch < 2 * a.r ? ch - a.r : 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int col = min(cg * kCols + (c >> 2) * 32 + ((e & 4) + q) * 4 + (e & 3), a.N - 1);
-        v[e >> 2][e & 3] = in ? load8(a.w + (long)col * a.r + ch) : u32x4{};
+      for (int h = 0; h < 2; ++h) {
+        const int col = cg * kCols + (c >> 2) * 32 + h * 16 + q * 4;
+        const uint32_t off = ((col < a.N ? col : 0) * a.r + ch) * 2;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[h][e] = load8(a.w + e * a.r, off);
       }
     }
   }
 
   // base, W and z of one group of columns into y
-  __device__ __forceinline__ void finish(Load& l, int cg, const u32x4 (&zf)[Z::kSteps][Z::kParts]) const {
+  __device__ __forceinline__ void finish(Load& l, int cg, const uint16_t (*s_z)[16 * Z::kRow]) const {
     const int col = cg * kCols + q * 32 + (c & 3) * 8;
     if (live) {
       f32x4 acc[8] = {};
 #pragma unroll
       for (int ks = 0; ks < Z::kSteps; ++ks) {
         if (ks) load_w(l.w, cg, ks);
+        u32x4 zf[Z::kParts];
+#pragma unroll
+        for (int p = 0; p < Z::kParts; ++p)
+          zf[p] = *reinterpret_cast<const u32x4*>(&s_z[p][c * Z::kRow + ks * 32 + q * 8]);
         if constexpr (!TR) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -337,7 +365,7 @@ struct Columns {
             f = l.w[t >> 2][t & 3];
           }
 #pragma unroll
-          for (int p = 0; p < Z::kParts; ++p) acc[t] = mfma(f, zf[ks][p], acc[t]);
+          for (int p = 0; p < Z::kParts; ++p) acc[t] = mfma(f, zf[p], acc[t]);
         }
       }
       quad_turn(l.base);
@@ -355,7 +383,7 @@ struct Columns {
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (row[j] >= 0 && col < a.N) {
+      if ((c & 12) + j < n && col < a.N) {
         const u32x4 v = l.base[j];
         *reinterpret_cast<Half8*>(a.y + row[j] * a.ys + col) = Half8{{v[0], v[1], v[2], v[3]}};
       }
@@ -364,14 +392,8 @@ struct Columns {
   // groups cg, cg + W, ... below g1; `l` holds the loads of group cg
   template <int W>
   __device__ __forceinline__ void run(Load& l, int cg, int g1, const uint16_t (*s_z)[16 * Z::kRow]) const {
-    u32x4 zf[Z::kSteps][Z::kParts];
-#pragma unroll
-    for (int ks = 0; ks < Z::kSteps; ++ks)
-#pragma unroll
-      for (int p = 0; p < Z::kParts; ++p)
-        zf[ks][p] = *reinterpret_cast<const u32x4*>(&s_z[p][c * Z::kRow + ks * 32 + q * 8]);
     while (cg < g1) {
-      finish(l, cg, zf);
+      finish(l, cg, s_z);
       cg += W;
       if (cg < g1) load(l, cg);
     }
@@ -491,7 +513,7 @@ __device__ __forceinline__ void put_parts(const float (*s_p)[LD], int half, int 
 // and kept in LDS for the block's columns. In the backward pass (TR) the first block of a
 // tile also leaves scale dz as fragments for the weight gradients, the last one scale z.
 template <int KS, bool TR>
-__global__ __launch_bounds__(kExpandWaves* kWave) void lora_expand_kernel(ExpandArgs a) {
+__global__ __launch_bounds__(kExpandWaves* kWave, (KS <= 2 ? 4 : 2)) void lora_expand_kernel(ExpandArgs a) {
   using Z = ZShape<KS>;
   constexpr int kLd = TR ? Z::kSteps * 32 + 4 : 1;
   __shared__ int32_t s_rows[16];
@@ -516,10 +538,17 @@ __global__ __launch_bounds__(kExpandWaves* kWave) void lora_expand_kernel(Expand
       const int row = i / quads, col = i % quads * 4;
       const float* p = a.part + (long)s_rows[row] * r + col;
       float v[4] = {};
-#pragma unroll 4
-      for (int s = 0; s < a.splits; ++s) {
-        const float4 f = *reinterpret_cast<const float4*>(p + s * part);
-        v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+      for (int s0 = 0; s0 < a.splits; s0 += 4) {   // four loads leave together
+        float4 f[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          f[s] = *reinterpret_cast<const float4*>(p + min(s0 + s, a.splits - 1) * part);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const bool in = s0 + s < a.splits;
+          v[0] += in ? f[s].x : 0.f, v[1] += in ? f[s].y : 0.f;
+          v[2] += in ? f[s].z : 0.f, v[3] += in ? f[s].w : 0.f;
+        }
       }
       if (!TR && a.z && head)
         *reinterpret_cast<float4*>(a.z + (long)s_rows[row] * r + col) = make_float4(v[0], v[1], v[2], v[3]);
@@ -642,7 +671,7 @@ constexpr int kWgradRows = 2048;  // row indices kept in LDS at a time
 // into the fragments of 4 MFMAs; P lies ready as fragments, in three bf16 parts (24 bits), so
 // the fp32 result carries no bf16 rounding. The block's eight waves take steps of 32 rows (one
 // tile) in turn, the next step's loads in flight, and add up through LDS in wave order. Rows
-// past the group's end are zero in both operands. Ranks past NT * 16 go to further blocks
+// past the group's end are zeros of P. Ranks past NT * 16 go to further blocks
 // (grid z).
 template <int NT>
 __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) {
@@ -658,7 +687,7 @@ __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) 
   const uint16_t* X = a.x[side];
   const long xs = a.xs[side];
   const int C = a.C[side];
-  const int col = c0 + c * 4;
+  const int col = c0 + c * 4 < C ? c0 + c * 4 : 0;  // lanes past the end: columns that go nowhere
   f32x4 acc[NT][4] = {};
   struct Step {
     uint32_t x[8][2];
@@ -667,7 +696,8 @@ __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) 
   for (int mb = m0; mb < m1; mb += kWgradRows) {
     const int rows = min(kWgradRows, m1 - mb);
     __syncthreads();
-    for (int i = tid; i < rows; i += kWgradThreads) s_idx[i] = a.sorted[mb + i];
+    // the last step is filled up with the last row, which meets zeros of P
+    for (int i = tid; i < (rows + 31) / 32 * 32; i += kWgradThreads) s_idx[i] = a.sorted[mb + min(i, rows - 1)];
     __syncthreads();
     auto load = [&](Step& v, int m) {
       const uint16_t* p = P + (long)((mb - m0 + m) >> 5) * 3 * nt * 512;
@@ -677,13 +707,9 @@ __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) 
         for (int i = 0; i < NT; ++i) v.p[part][i] = load8(p + (part * nt + i) * 512);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int at = m + q * 8 + j;
-        v.x[j][0] = v.x[j][1] = 0;
-        if (at < rows && col < C) {
-          const Half4 h = *reinterpret_cast<const Half4*>(X + s_idx[at] * xs + col);
-          v.x[j][0] = h.w[0];
-          v.x[j][1] = h.w[1];
-        }
+        const Half4 h = *reinterpret_cast<const Half4*>(X + s_idx[m + q * 8 + j] * xs + col);
+        v.x[j][0] = h.w[0];
+        v.x[j][1] = h.w[1];
       }
     };
     auto multiply = [&](const Step& v) {

@@ -133,7 +133,8 @@ __global__ __launch_bounds__(THREADS) void sort_place_kernel(SortArgs a) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int s = s0 + i * kWave + lane;
-      id[i] = s < w1 ? sort_key(a.ids[s], a.G, a.groups) : -1;
+      id[i] = a.ids[min(s, w1 - 1)];   // no branch: the loads leave together
+      id[i] = s < w1 ? sort_key(id[i], a.G, a.groups) : -1;
     }
   };
   for (int s0 = w0; s0 < w1; s0 += kBatch * kWave) {
