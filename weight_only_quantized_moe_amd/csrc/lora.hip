@@ -127,8 +127,8 @@ template <int RT>
 __device__ __forceinline__ bool find_tile(const Tiles& t, int* g, int* n, int* index, int32_t* s_rows) {
   const int b = blockIdx.x;
   if (t.sorted) {
-    const int part = b >= t.tiles;
-    const SortTile d = t.table[part ? b - t.tiles : b];
+    const int part = b / t.tiles;
+    const SortTile d = t.table[b - part * t.tiles];
     if (d.group < 0) return false;
     *g = d.group;
     *index = d.index;
@@ -255,12 +255,11 @@ __device__ __forceinline__ void shrink_tile(const uint16_t* x, long xs, const ui
   __syncthreads();
 }
 
-// W_g z of a tile's rows, added to base: each wave takes 128 columns at a time. The small
-// matrix is the MFMA's first operand with its rows dealt out so that a lane ends up with 32
-// neighbouring columns of one row of y, four 16-byte pieces that are exchanged inside four
-// lanes on the way from base and to y. A fragment of W serves both bf16 parts of z; up to
-// rank 16 (KS = 0) both parts share one MFMA. TR: W is [r, N] (a lane's 8 columns of 8 ranks
-// are turned in registers), else [N, r].
+// W_g z of 16 rows, added to base: a wave takes 128 columns at a time. The columns are dealt
+// out to the MFMAs so that lane c of a group of 16 ends up with columns 8c .. 8c + 7 of four
+// rows: base and y move as 16-byte accesses, 16 lanes on 256 contiguous bytes of a row. A
+// fragment of W serves both bf16 parts of z; up to rank 16 (KS = 0) both parts share one MFMA.
+// TR: W is [r, N] (a lane's columns of 8 ranks are turned in registers), else [N, r].
 struct ColumnArgs {
   int r, N;
   const uint16_t* w;     // matrix of the tile's adapter
@@ -280,122 +279,132 @@ struct ZShape {
 
 constexpr int kCols = 128;
 
+// The lanes' place in a tile of 16 rows and 128 columns. No load stands behind a lane's own
+// branch, so that they leave together: a lane without a row, column or rank of its own reads
+// another one, which then goes nowhere (ranks: meets zeros of z, W being finite). Columns and
+// ranks come in eights: what a lane reads of 4 or 8 of them exists whole.
 template <int KS, bool TR>
 struct Columns {
   using Z = ZShape<KS>;
   const ColumnArgs& a;
-  const bool live;
   const int n, c, q;
   int row[4];   // rows this lane reads, and writes below n
 
-  // what a group of columns starts with: base, and W's part for the first rank step as it lies
+  // s_rows: the 16 rows, n of them
+  __device__ __forceinline__ Columns(const ColumnArgs& a, int n, const int32_t* s_rows)
+      : a(a), n(n), c(threadIdx.x & 15), q((threadIdx.x & (kWave - 1)) >> 4) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) row[j] = s_rows[q * 4 + j < n ? q * 4 + j : 0];
+  }
+
+  __device__ __forceinline__ void load_base(u32x4 (&b)[4], int cg) const {
+    const int col = cg * kCols + c * 8, o = col < a.N ? col : 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b[j] = a.base ? load8(a.base + row[j] * a.bs + o) : u32x4{};
+  }
+
+  // ranks ch .. ch + 7 of fragment step ks, chunk q, or others in place of such as do not exist
+  __device__ __forceinline__ int chunk(int ks, int q) const {
+    const int ch = (ks * 4 + q) * 8;
+    return ch < a.r ? ch : Z::kPack && ch < 2 * a.r ? ch - a.r : 0;
+  }
+
+  // half h of W's part for rank step ks as it lies
+  __device__ __forceinline__ void load_w(u32x4 (&v)[4], int cg, int ks, int h) const {
+    if constexpr (TR) {  // columns 8c + 4h .. + 3 of 8 ranks, two ranks a register set
+      const int col = cg * kCols + c * 8 + h * 4;
+      const uint32_t off = (chunk(ks, q) * a.N + (col < a.N ? col : h * 4)) * 2;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const Half4 f = *reinterpret_cast<const Half4*>(reinterpret_cast<const char*>(a.w + (long)e * a.N) + off);
+        v[e >> 1][(e & 1) * 2] = f.w[0];
+        v[e >> 1][(e & 1) * 2 + 1] = f.w[1];
+      }
+    } else {  // column 8 (c & 12) + 8e + 4h + q, ranks of chunk c & 3
+      const int ch = chunk(ks, c & 3);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int col = cg * kCols + ((c & 12) + e) * 8;
+        v[e] = load8(a.w + h * 4 * a.r, (((col < a.N ? col : 0) + q) * a.r + ch) * 2);
+      }
+    }
+  }
+
+  // what load_w brought, as the fragments of columns t = 4h .. 4h + 3
+  __device__ __forceinline__ static void turn_w(u32x4 (&v)[4]) {
+    if constexpr (TR) {
+      uint32_t x[8][2];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[e][0] = v[e >> 1][(e & 1) * 2];
+        x[e][1] = v[e >> 1][(e & 1) * 2 + 1];
+      }
+      turn_8x4(x, v);
+    } else {
+      quad_turn(v);
+      group_turn(v);
+    }
+  }
+
+  __device__ __forceinline__ void load_z(u32x4 (&zf)[Z::kParts], const uint16_t* s_z, int part, int ks) const {
+#pragma unroll
+    for (int p = 0; p < Z::kParts; ++p)
+      zf[p] = *reinterpret_cast<const u32x4*>(s_z + p * part + c * Z::kRow + ks * 32 + q * 8);
+  }
+
+  // y = base + acc (rows without an adapter: y = base)
+  __device__ __forceinline__ void store(const u32x4 (&b)[4], const f32x4 (&acc)[8], bool live, int cg) const {
+    const int col = cg * kCols + c * 8;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      Half8 o;
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+        o.w[p] = live ? pack_bf16(bf16_lo(b[j][p]) + acc[2 * p][j], bf16_hi(b[j][p]) + acc[2 * p + 1][j])
+                      : b[j][p];
+      if (q * 4 + j < n && col < a.N) *reinterpret_cast<Half8*>(a.y + row[j] * a.ys + col) = o;
+    }
+  }
+
+  // what a group of columns starts with: base, and W's part for the first rank step
   struct Load {
     u32x4 base[4], w[2][4];
   };
-
-  __device__ __forceinline__ Columns(const ColumnArgs& a, bool live, int n, const int32_t* s_rows)
-      : a(a), live(live), n(n), c(threadIdx.x & 15), q((threadIdx.x & (kWave - 1)) >> 4) {
+  __device__ __forceinline__ void load(Load& l, bool live, int cg) const {
+    load_base(l.base, cg);
+    if (live)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) row[j] = s_rows[(c & 12) + j < n ? (c & 12) + j : 0];
-  }
-
-  // No load stands behind a lane's own branch, so that they leave together: a lane without a
-  // row, column or rank of its own reads another one, which then goes nowhere (ranks: meets
-  // zeros of z, W being finite).
-  __device__ __forceinline__ void load(Load& l, int cg) const {
-    const int col = cg * kCols + q * 32 + (c & 3) * 8, o = col < a.N ? col : 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      l.base[j] = a.base ? load8(a.base + row[j] * a.bs + o) : u32x4{};
-    if (live) load_w(l.w, cg, 0);
-  }
-
-  // W's part for rank step ks (columns and ranks come in eights: four rows or columns of W that
-  // a lane reads all exist, or it reads others instead)
-  __device__ __forceinline__ void load_w(u32x4 (&v)[2][4], int cg, int ks) const {
-    if constexpr (TR) {
-      int ch = (ks * 4 + q) * 8;
-      if (ch >= a.r) ch = Z::kPack && ch < 2 * a.r ? ch - a.r : 0;
-      const int col = cg * kCols + (c >> 2) * 32 + (c & 3) * 8;
-      const uint32_t off = (ch * a.N + (col < a.N ? col : 0)) * 2;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e >> 2][e & 3] = load8(a.w + (long)e * a.N, off);
-    } else {
-      int ch = (ks * 4 + (c & 3)) * 8;
-      if (ch >= a.r) ch = Z::kPack && ch < 2 * a.r ? ch - a.r : 0;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int col = cg * kCols + (c >> 2) * 32 + h * 16 + q * 4;
-        const uint32_t off = ((col < a.N ? col : 0) * a.r + ch) * 2;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[h][e] = load8(a.w + e * a.r, off);
-      }
-    }
-  }
-
-  // base, W and z of one group of columns into y
-  __device__ __forceinline__ void finish(Load& l, int cg, const uint16_t (*s_z)[16 * Z::kRow]) const {
-    const int col = cg * kCols + q * 32 + (c & 3) * 8;
-    if (live) {
-      f32x4 acc[8] = {};
-#pragma unroll
-      for (int ks = 0; ks < Z::kSteps; ++ks) {
-        if (ks) load_w(l.w, cg, ks);
-        u32x4 zf[Z::kParts];
-#pragma unroll
-        for (int p = 0; p < Z::kParts; ++p)
-          zf[p] = *reinterpret_cast<const u32x4*>(&s_z[p][c * Z::kRow + ks * 32 + q * 8]);
-        if constexpr (!TR) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            quad_turn(l.w[h]);
-            group_turn(l.w[h]);
-          }
-        }
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          u32x4 f;
-          if constexpr (TR) {  // column t of 8 ranks
-#pragma unroll
-            for (int p = 0; p < 4; ++p)
-              f[p] = __builtin_amdgcn_perm(l.w[p >> 1][(2 * p + 1) & 3][t >> 1],
-                                           l.w[p >> 1][(2 * p) & 3][t >> 1],
-                                           (t & 1) ? 0x07060302u : 0x05040100u);
-          } else {
-            f = l.w[t >> 2][t & 3];
-          }
-#pragma unroll
-          for (int p = 0; p < Z::kParts; ++p) acc[t] = mfma(f, zf[p], acc[t]);
-        }
-      }
-      quad_turn(l.base);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          // columns 8j + 2p, 8j + 2p + 1 of the lane's 32
-          const uint32_t bp = l.base[j][p];
-          const float lo = TR ? acc[2 * p][j] : acc[2 * j + (p >> 1)][(p & 1) * 2];
-          const float hi = TR ? acc[2 * p + 1][j] : acc[2 * j + (p >> 1)][(p & 1) * 2 + 1];
-          l.base[j][p] = pack_bf16(bf16_lo(bp) + lo, bf16_hi(bp) + hi);
-        }
-      quad_turn(l.base);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if ((c & 12) + j < n && col < a.N) {
-        const u32x4 v = l.base[j];
-        *reinterpret_cast<Half8*>(a.y + row[j] * a.ys + col) = Half8{{v[0], v[1], v[2], v[3]}};
-      }
+      for (int h = 0; h < 2; ++h) load_w(l.w[h], cg, 0, h);
   }
 
   // groups cg, cg + W, ... below g1; `l` holds the loads of group cg
   template <int W>
-  __device__ __forceinline__ void run(Load& l, int cg, int g1, const uint16_t (*s_z)[16 * Z::kRow]) const {
+  __device__ __forceinline__ void run(Load& l, bool live, int cg, int g1,
+                                      const uint16_t (*s_z)[16 * Z::kRow]) const {
     while (cg < g1) {
-      finish(l, cg, s_z);
+      f32x4 acc[8] = {};
+      if (live) {
+#pragma unroll
+        for (int ks = 0; ks < Z::kSteps; ++ks) {
+          u32x4 zf[Z::kParts];
+          load_z(zf, s_z[0], 16 * Z::kRow, ks);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (ks) load_w(l.w[h], cg, ks, h);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            turn_w(l.w[h]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+              for (int p = 0; p < Z::kParts; ++p) acc[h * 4 + t] = mfma(zf[p], l.w[h][t], acc[h * 4 + t]);
+          }
+        }
+      }
+      store(l.base, acc, live, cg);
       cg += W;
-      if (cg < g1) load(l, cg);
+      if (cg < g1) load(l, live, cg);
     }
   }
 };
@@ -475,6 +484,7 @@ struct ExpandArgs {
   // TR (backward): where the fragments of scale dz and scale z go, and z
   uint16_t* frag[2];
   const float* fz;
+  int steps_per_tile;    // 32 rows each
 };
 
 constexpr int kExpandWaves = 4;
@@ -482,21 +492,21 @@ constexpr int kExpandWaves = 4;
 // rank / 16 rounded up to a power of two: rank tiles of the products over K and over rows
 __host__ __device__ constexpr int rank_tiles(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : r <= 64 ? 4 : 8; }
 
-// Half a tile of 32 rows of P [rows, r] (rows 16 half .. 16 half + 15) as the MFMA fragments
-// that sums over rows need: for each of three bf16 parts and each 16 ranks, lane (rank c, row
-// group q) holds rows 8q .. 8q + 7 of its rank, 1 KiB together. s_p: the half's rows, fp32;
-// rows past n and ranks past r are zeros.
-template <int LD>
-__device__ __forceinline__ void put_parts(const float (*s_p)[LD], int half, int n, int r, uint16_t* out) {
+// Rows RT * part, ... of a table entry of P [rows, r] (RT of them) as the MFMA fragments that
+// sums over rows need: for every 32 rows, each of three bf16 parts and each 16 ranks, lane (rank
+// c, row group q) holds rows 8q .. 8q + 7 of its rank, 1 KiB together. s_p: the rows, fp32, LD
+// apart; rows past n and ranks past r are zeros.
+template <int RT, int LD>
+__device__ __forceinline__ void put_parts(const float* s_p, int part, int n, int r, uint16_t* out) {
   const int nt = rank_tiles(r);
-  for (int o = threadIdx.x; o < nt * 32; o += blockDim.x) {
-    const int lane = o & 31, i = o / 32;
-    const int rank = i * 16 + (lane & 15), row = (lane >> 4) * 8;
+  for (int o = threadIdx.x; o < nt * RT * 2; o += blockDim.x) {
+    const int c = o & 15, row = o / 16 % (RT / 8) * 8, i = o / (RT * 2), rank = i * 16 + c;
     float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = rank < r && row + e < n ? s_p[row + e][rank] : 0.f;
+    for (int e = 0; e < 8; ++e) v[e] = rank < r && row + e < n ? s_p[(row + e) * LD + rank] : 0.f;
+    const int at = part * RT + row, lane = at % 32 * 2 + c;
 #pragma unroll
-    for (int part = 0; part < 3; ++part) {
+    for (int k = 0; k < 3; ++k) {
       Half8 h;
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
@@ -504,37 +514,70 @@ __device__ __forceinline__ void put_parts(const float (*s_p)[LD], int half, int 
         v[2 * p] = bf16_rest(v[2 * p], bf16_lo(h.w[p]));
         v[2 * p + 1] = bf16_rest(v[2 * p + 1], bf16_hi(h.w[p]));
       }
-      *reinterpret_cast<Half8*>(out + ((part * nt + i) * kWave + half * 32 + lane) * 8) = h;
+      *reinterpret_cast<Half8*>(out + (((at / 32 * 3 + k) * nt + i) * kWave + lane) * 8) = h;
     }
   }
 }
 
-// y = base + W_g (scale z): z's splits are added in order, scaled, split into two bf16 parts
-// and kept in LDS for the block's columns. In the backward pass (TR) the first block of a
-// tile also leaves scale dz as fragments for the weight gradients, the last one scale z.
-template <int KS, bool TR>
-__global__ __launch_bounds__(kExpandWaves* kWave, (KS <= 2 ? 4 : 2)) void lora_expand_kernel(ExpandArgs a) {
+// LDS of the second product: z as bf16 parts, and what its waves share
+template <int RW, int KS, bool TR>
+struct ExpandLds {
   using Z = ZShape<KS>;
-  constexpr int kLd = TR ? Z::kSteps * 32 + 4 : 1;
-  __shared__ int32_t s_rows[16];
-  __shared__ __align__(16) uint16_t s_z[Z::kParts][16 * Z::kRow];
-  __shared__ __align__(16) float s_p[TR ? 16 : 1][kLd];
+  static constexpr int kRows = RW * 16, kLd = Z::kSteps * 32 + 4;
+  static constexpr bool kDouble = KS <= 2;                        // two sets of W's fragments
+  static constexpr int kFrag = RW == 1 ? 0 : Z::kSteps * 8 * 1024;  // bytes of one set
+  static constexpr int kP = TR ? kRows * kLd * 4 : 0;             // dz or z in fp32, before the columns
+  static constexpr int kShared = std::max({kFrag * (kDouble ? 2 : 1), kP, 16});
+};
+
+// y = base + W_g (scale z): z's splits are added in order, scaled, split into two bf16 parts
+// and kept in LDS for the block's columns. RW = 1: 16 rows a block, each wave has columns of
+// its own. RW = 4: 64 rows, a wave 16 of them; the waves share each group of columns, and each
+// turns a part of W's fragments and puts it into LDS for all, which cuts W's way from L2 to a
+// quarter. In the backward pass (TR) the first block of a tile also leaves scale dz as
+// fragments for the weight gradients, the last one scale z.
+template <int RW, int KS, bool TR>
+__global__ __launch_bounds__(kExpandWaves* kWave, (KS <= 2 ? (RW == 1 && !(TR && KS == 2) ? 4 : 3) : 2))
+void lora_expand_kernel(ExpandArgs a) {
+  using Z = ZShape<KS>;
+  using L = ExpandLds<RW, KS, TR>;
+  constexpr int RT = RW * 16, kThreads = kExpandWaves * kWave;
+  __shared__ int32_t s_rows[RT];
+  __shared__ __align__(16) uint16_t s_z[Z::kParts][RT * Z::kRow];
+  __shared__ __align__(16) char s_shared[L::kShared];
+  float* s_p = reinterpret_cast<float*>(s_shared);
+  u32x4* s_w = reinterpret_cast<u32x4*>(s_shared);
   int g, n, index;
-  if (!find_tile<16>(a.tiles, &g, &n, &index, s_rows)) return;
-  const bool live = g != a.tiles.G;
-  const int r = a.c.r, quads = r / 4;
+  if (!find_tile<RT>(a.tiles, &g, &n, &index, s_rows)) return;
+  const bool live = g != a.tiles.G, head = blockIdx.y == 0;
+  const int r = a.c.r, quads = r / 4, lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
+  const int mine = RW == 1 ? 0 : wave * 16;  // first of this wave's rows
   ColumnArgs ca = a.c;
   if (live) ca.w += (long)g * ca.N * r;
-  const Columns<KS, TR> cols(ca, live, n, s_rows);
+  const Columns<KS, TR> cols(ca, max(0, min(16, n - mine)), s_rows + mine);
   const int g0 = blockIdx.y * a.col_groups, g1 = min(g0 + a.col_groups, (ca.N + kCols - 1) / kCols);
-  const int cg = g0 + (threadIdx.x >> 6);
-  typename Columns<KS, TR>::Load first;  // on the way while z is put together
-  if (cg < g1) cols.load(first, cg);
-  const bool head = blockIdx.y == 0;
+  int cg = RW == 1 ? g0 + wave : g0;
+  // the first loads are on the way while z is put together
+  constexpr int kPieces = 2 * Z::kSteps, kMine = (kPieces + kExpandWaves - 1) / kExpandWaves;
+  typename Columns<KS, TR>::Load first;
+  u32x4 base[4], raw[kMine][4];
+  auto load_pieces = [&](int cg) {  // this wave's pieces of W's fragments: (rank step, half)
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+      const int pc = k * kExpandWaves + wave;
+      if (kPieces % kExpandWaves == 0 || pc < kPieces) cols.load_w(raw[k], cg, pc >> 1, pc & 1);
+    }
+  };
+  if (RW == 1) {
+    if (cg < g1) cols.load(first, live, cg);
+  } else {
+    cols.load_base(base, cg);
+    if (live) load_pieces(cg);
+  }
   if (live) {
     const float sc = a.scale[g];
     const long part = (long)a.tiles.M * r;
-    for (int i = threadIdx.x; i < n * quads; i += kExpandWaves * kWave) {
+    for (int i = threadIdx.x; i < n * quads; i += kThreads) {
       const int row = i / quads, col = i % quads * 4;
       const float* p = a.part + (long)s_rows[row] * r + col;
       float v[4] = {};
@@ -555,34 +598,74 @@ __global__ __launch_bounds__(kExpandWaves* kWave, (KS <= 2 ? 4 : 2)) void lora_e
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] *= sc;
       put_z<KS>(s_z, row, col, r, v);
-      if (TR && head) *reinterpret_cast<float4*>(&s_p[row][col]) = make_float4(v[0], v[1], v[2], v[3]);
+      if (TR && head) *reinterpret_cast<float4*>(s_p + row * L::kLd + col) = make_float4(v[0], v[1], v[2], v[3]);
     }
-    pad_z<KS, 16>(s_z, r);
+    pad_z<KS, RT>(s_z, r);
     if constexpr (TR) {
-      const int half = (int)blockIdx.x >= a.tiles.tiles;
-      const long at = (long)index * 3 * rank_tiles(r) * 512;
+      const int pt = (int)blockIdx.x / a.tiles.tiles;
+      const long at = (long)index * a.steps_per_tile * 3 * rank_tiles(r) * 512;
       if (head) {
         __syncthreads();
-        put_parts(s_p, half, n, r, a.frag[0] + at);
+        put_parts<RT, L::kLd>(s_p, pt, n, r, a.frag[0] + at);
       }
       if (blockIdx.y == gridDim.y - 1) {
         __syncthreads();
-        for (int i = threadIdx.x; i < n * quads; i += kExpandWaves * kWave) {
+        for (int i = threadIdx.x; i < n * quads; i += kThreads) {
           const int row = i / quads, col = i % quads * 4;
           const float4 f = *reinterpret_cast<const float4*>(a.fz + (long)s_rows[row] * r + col);
-          *reinterpret_cast<float4*>(&s_p[row][col]) = make_float4(f.x * sc, f.y * sc, f.z * sc, f.w * sc);
+          *reinterpret_cast<float4*>(s_p + row * L::kLd + col) = make_float4(f.x * sc, f.y * sc, f.z * sc, f.w * sc);
         }
         __syncthreads();
-        put_parts(s_p, half, n, r, a.frag[1] + at);
+        put_parts<RT, L::kLd>(s_p, pt, n, r, a.frag[1] + at);
       }
     }
   } else if (!TR && a.z && head) {
-    for (int i = threadIdx.x; i < n * r; i += kExpandWaves * kWave)
-      a.z[(long)s_rows[i / r] * r + i % r] = 0.f;
+    for (int i = threadIdx.x; i < n * r; i += kThreads) a.z[(long)s_rows[i / r] * r + i % r] = 0.f;
   }
   __syncthreads();
   if (!live && a.c.base == a.c.y) return;  // rows without an adapter stay
-  cols.template run<kExpandWaves>(first, cg, g1, s_z);
+  if constexpr (RW == 1) {
+    cols.template run<kExpandWaves>(first, live, cg, g1, s_z);
+  } else {
+    for (int it = 0; cg < g1; ++cg, ++it) {
+      u32x4* buf = s_w + (L::kDouble ? (it & 1) * (L::kFrag / 16) : 0);
+      if (live) {
+#pragma unroll
+        for (int k = 0; k < kMine; ++k) {
+          const int pc = k * kExpandWaves + wave;
+          if (kPieces % kExpandWaves == 0 || pc < kPieces) {
+            cols.turn_w(raw[k]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) buf[(pc * 4 + t) * kWave + lane] = raw[k][t];
+          }
+        }
+      }
+      __syncthreads();
+      u32x4 next[4] = {};
+      if (cg + 1 < g1) {
+        if (live) load_pieces(cg + 1);
+        cols.load_base(next, cg + 1);
+      }
+      f32x4 acc[8] = {};
+      if (live) {
+#pragma unroll
+        for (int ks = 0; ks < Z::kSteps; ++ks) {
+          u32x4 zf[Z::kParts];
+          cols.load_z(zf, s_z[0] + mine * Z::kRow, RT * Z::kRow, ks);
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            const u32x4 f = buf[(ks * 8 + t) * kWave + lane];
+#pragma unroll
+            for (int p = 0; p < Z::kParts; ++p) acc[t] = mfma(zf[p], f, acc[t]);
+          }
+        }
+      }
+      cols.store(base, acc, live, cg);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) base[j] = next[j];
+      if (!L::kDouble) __syncthreads();
+    }
+  }
 }
 
 struct FusedArgs {
@@ -614,11 +697,11 @@ __global__ __launch_bounds__(kFusedWaves* kWave) void lora_fused_kernel(FusedArg
   const int r = a.c.r;
   ColumnArgs ca = a.c;
   if (live) ca.w += (long)g * ca.N * r;
-  const Columns<KS, false> cols(ca, live, n, s_rows);
+  const Columns<KS, false> cols(ca, n, s_rows);
   const int g0 = blockIdx.y * a.col_groups, g1 = min(g0 + a.col_groups, (ca.N + kCols - 1) / kCols);
   const int cg = g0 + (threadIdx.x >> 6);
   typename Columns<KS, false>::Load first;  // on the way during the first product
-  if (cg < g1) cols.load(first, cg);
+  if (cg < g1) cols.load(first, live, cg);
   if (live) {
     shrink_tile<1, NT, kFusedWaves, (NT == 1 ? 4 : NT == 2 ? 2 : 1)>(a.x, a.xs, a.wa + (long)g * r * a.K, a.K, r, n, s_rows,
                                                0, (a.K + kKStep - 1) / kKStep, s_red);
@@ -645,13 +728,14 @@ __global__ __launch_bounds__(kFusedWaves* kWave) void lora_fused_kernel(FusedArg
   }
   __syncthreads();
   if (!live && a.c.base == a.c.y) return;  // rows without an adapter stay
-  cols.template run<kFusedWaves>(first, cg, g1, s_z);
+  cols.template run<kFusedWaves>(first, live, cg, g1, s_z);
 }
 
 struct WgradArgs {
   const int32_t* sorted;
   const int32_t* off;
   const int32_t* tile_first;
+  int steps_per_tile;
   int r;
   // two products: [0] P = scale dz, X = x, out dA [G, r, C]; [1] P = scale z, X = dy, out dB [G, C, r]
   const uint16_t* p[2];   // fragments of P, see Parts
@@ -683,7 +767,7 @@ __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) 
   const int c = lane & 15, q = lane >> 4;
   const int m0 = a.off[g], m1 = a.off[g + 1];
   const int nt = NT * gridDim.z, i0 = blockIdx.z * NT;
-  const uint16_t* P = a.p[side] + ((long)a.tile_first[g] * 3 * nt + i0) * 512 + lane * 8;
+  const uint16_t* P = a.p[side] + ((long)a.tile_first[g] * a.steps_per_tile * 3 * nt + i0) * 512 + lane * 8;
   const uint16_t* X = a.x[side];
   const long xs = a.xs[side];
   const int C = a.C[side];
@@ -793,23 +877,28 @@ constexpr int kFusedBytes = 512 << 10;  // largest first matrix of the one-launc
 constexpr int kFusedRank = 64;          // and its largest rank (registers)
 
 struct Plan {
-  int mt, nt, rt, tiles;     // tile rows / 16, rank / 16 rounded up, tile rows, most tiles
-  int busy;                  // tiles that can hold rows, for the grids' second axis
-  bool table;                // a sort and a tile table come first
-  bool fused;                // both products in one launch
+  bool table;      // a sort and a tile table come first
+  bool fused;      // both products in one launch
+  bool wide;       // the second product's waves share its matrix
+  int nt;          // rank / 16, rounded up to a power of two
+  int rt;          // rows of a tile
+  int mt;          // rows / 16 that a block of the first product takes
+  int tiles;       // most tiles
+  int busy;        // how many of them can have rows
 };
 
-// Tile rows from the mean number of rows an adapter has: 32 rows share one read of the
-// adapter's matrices, 16 waste less where adapters have few rows. The backward pass takes 32,
-// the depth of its sums over rows.
+// Tile rows from the mean number of rows an adapter has: more rows share one read of the
+// adapter's matrices, fewer waste less where adapters have few rows. The backward pass takes
+// at least 32, the depth of its sums over rows.
 Plan plan_tiles(int M, int G, int K, int r, bool backward) {
   Plan p;
+  const int mean = M / std::max(1, std::min(G, M));
   p.nt = rank_tiles(r);
   p.table = backward || M > kDirectRows;
   p.fused = !p.table && r <= kFusedRank && (long)r * K * 2 <= kFusedBytes;
-  const int mean = M / std::max(1, std::min(G, M));
-  p.mt = backward ? 2 : !p.table || p.nt == 8 || mean < 24 ? 1 : 2;
-  p.rt = p.mt * 16;
+  p.wide = p.table && mean >= 48;
+  p.rt = p.wide ? 64 : backward ? 32 : !p.table || p.nt == 8 || mean < 24 ? 16 : 32;
+  p.mt = p.rt == 16 ? 1 : 2;
   const int most = M / p.rt + std::min(G + 1, M);
   p.tiles = p.table ? (most + 7) / 8 * 8 : M;  // the table is dealt out over 8 XCDs
   p.busy = std::max(1, std::min(most, M));
@@ -820,7 +909,7 @@ Plan plan_tiles(int M, int G, int K, int r, bool backward) {
 // wave of a block, at most 16 partial sums to add up again.
 int plan_splits(const Plan& p, int K) {
   const int steps = (K + kKStep - 1) / kKStep;
-  return std::max(1, std::min({(768 + p.busy - 1) / p.busy, (steps + kShrinkWaves - 1) / kShrinkWaves, 16}));
+  return std::max(1, std::min({(768 + p.busy * p.rt / (p.mt * 16) - 1) / (p.busy * p.rt / (p.mt * 16)), (steps + kShrinkWaves - 1) / kShrinkWaves, 16}));
 }
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -847,7 +936,7 @@ Space plan_space(int M, int G, int K, int N, int r, bool backward) {
   }
   if (!p.fused) s.part = take((size_t)plan_splits(p, backward ? N : K) * M * r * 4);
   if (backward) {
-    for (size_t& f : s.frag) f = take((size_t)p.tiles * 3 * p.nt * 1024);
+    for (size_t& f : s.frag) f = take((size_t)p.tiles * (p.rt / 32) * 3 * p.nt * 1024);
     s.bt = take((size_t)G * r * N * 2);
   }
   s.total = at;
@@ -876,7 +965,7 @@ hipError_t make_tiles(const int32_t* ids, int M, int G, const Plan& p, const Spa
 }
 
 hipError_t shrink(const Plan& p, const ShrinkArgs& a, hipStream_t s) {
-  const dim3 grid(p.tiles, a.splits), block(kShrinkWaves * kWave);
+  const dim3 grid(p.tiles * (p.rt / (p.mt * 16)), a.splits), block(kShrinkWaves * kWave);
 #define HMOE_SHRINK(MT, NT)                                                         \
   if (p.mt == MT && p.nt == NT)                                                     \
   hipLaunchKernelGGL((lora_shrink_kernel<MT, NT>), grid, block, 0, s, a)
@@ -895,24 +984,32 @@ hipError_t shrink(const Plan& p, const ShrinkArgs& a, hipStream_t s) {
 // MFMA steps of 32 ranks (0: both parts of z in one)
 int z_steps(int r) { return r <= 16 ? 0 : (r + 31) / 32; }
 
+template <int RW, bool TR>
+hipError_t expand_by_rank(const Plan& p, const ExpandArgs& a, dim3 grid, hipStream_t s) {
+  const dim3 block(kExpandWaves * kWave);
+  switch (z_steps(a.c.r)) {
+    case 0:
+      hipLaunchKernelGGL((lora_expand_kernel<RW, 0, TR>), grid, block, 0, s, a);
+      break;
+    case 1: hipLaunchKernelGGL((lora_expand_kernel<RW, 1, TR>), grid, block, 0, s, a); break;
+    case 2: hipLaunchKernelGGL((lora_expand_kernel<RW, 2, TR>), grid, block, 0, s, a); break;
+    case 3: hipLaunchKernelGGL((lora_expand_kernel<RW, 3, TR>), grid, block, 0, s, a); break;
+    default: hipLaunchKernelGGL((lora_expand_kernel<RW, 4, TR>), grid, block, 0, s, a); break;
+  }
+  return hipGetLastError();
+}
+
 template <bool TR>
 hipError_t expand(const Plan& p, ExpandArgs a, hipStream_t s) {
   const int groups = (a.c.N + kCols - 1) / kCols;
-  // columns a block: a multiple of its four waves' 128, as wide as still leaves about 1024
-  // blocks, so that few blocks add up z's splits again
-  const int want = std::max(1, (1024 + p.busy * p.mt - 1) / (p.busy * p.mt));
-  const int rounds = std::max(1, (groups + want * kExpandWaves - 1) / (want * kExpandWaves));
-  a.col_groups = rounds * kExpandWaves;
-  const dim3 grid(p.tiles * p.mt, (groups + a.col_groups - 1) / a.col_groups);
-  const dim3 block(kExpandWaves * kWave);
-  switch (z_steps(a.c.r)) {
-    case 0: hipLaunchKernelGGL((lora_expand_kernel<0, TR>), grid, block, 0, s, a); break;
-    case 1: hipLaunchKernelGGL((lora_expand_kernel<1, TR>), grid, block, 0, s, a); break;
-    case 2: hipLaunchKernelGGL((lora_expand_kernel<2, TR>), grid, block, 0, s, a); break;
-    case 3: hipLaunchKernelGGL((lora_expand_kernel<3, TR>), grid, block, 0, s, a); break;
-    default: hipLaunchKernelGGL((lora_expand_kernel<4, TR>), grid, block, 0, s, a); break;
-  }
-  return hipGetLastError();
+  const int parts = p.wide ? 1 : p.rt / 16, unit = p.wide ? 1 : kExpandWaves;
+  // columns a block: as few rounds of its waves as let all blocks be on the card at once
+  const int ks = z_steps(a.c.r), room = 256 * (ks <= 1 ? 4 : ks <= 3 ? 3 : 2);
+  const int rounds = std::max(1, (int)(((long)groups * p.busy * parts + (long)room * unit - 1) / ((long)room * unit)));
+  a.col_groups = std::min(rounds, (groups + unit - 1) / unit) * unit;
+  a.steps_per_tile = p.rt / 32;
+  const dim3 grid(p.tiles * parts, (groups + a.col_groups - 1) / a.col_groups);
+  return p.wide ? expand_by_rank<4, TR>(p, a, grid, s) : expand_by_rank<1, TR>(p, a, grid, s);
 }
 
 template <int NT, int KS>
@@ -955,7 +1052,7 @@ hipError_t launch_lora(const Lora& l, void* scratch, hipStream_t s) {
   float* part = reinterpret_cast<float*>(b + sp.part);
   err = shrink(p, ShrinkArgs{t, l.x, l.xs, l.A, l.K, l.r, splits, part}, s);
   if (err != hipSuccess) return err;
-  return expand<false>(p, ExpandArgs{t, part, splits, l.scale, l.z, 0, c, {}, nullptr}, s);
+  return expand<false>(p, ExpandArgs{t, part, splits, l.scale, l.z, 0, c, {}, nullptr, 0}, s);
 }
 
 hipError_t launch_lora_backward(const LoraGrad& l, void* scratch, hipStream_t s) {
@@ -977,12 +1074,12 @@ hipError_t launch_lora_backward(const LoraGrad& l, void* scratch, hipStream_t s)
     err = shrink(p, ShrinkArgs{t, l.dy, l.dys, Bt, l.N, l.r, splits, part}, s);
     if (err != hipSuccess) return err;
     const ColumnArgs c{l.r, l.K, l.A, l.dbase, l.dbs, l.dx, l.dxs};
-    err = expand<true>(p, ExpandArgs{t, part, splits, l.scale, nullptr, 0, c, {frag[0], frag[1]}, l.z}, s);
+    err = expand<true>(p, ExpandArgs{t, part, splits, l.scale, nullptr, 0, c, {frag[0], frag[1]}, l.z, 0}, s);
     if (err != hipSuccess) return err;
   }
   const int32_t* off = reinterpret_cast<const int32_t*>(b + sp.off);
   const int32_t* tile_first = reinterpret_cast<const int32_t*>(b + sp.tile_first);
-  WgradArgs w{t.sorted, off, tile_first, l.r, {frag[0], frag[1]}, {l.x, l.dy}, {l.xs, l.dys}, {l.K, l.N},
+  WgradArgs w{t.sorted, off, tile_first, p.rt / 32, l.r, {frag[0], frag[1]}, {l.x, l.dy}, {l.xs, l.dys}, {l.K, l.N},
               {(l.K + 63) / 64, (l.N + 63) / 64}, {l.dA, l.dB}};
   const dim3 grid(w.blocks[0] + w.blocks[1], l.G, p.nt == 8 ? 2 : 1), block(kWgradThreads);
   switch (p.nt) {
