@@ -118,6 +118,13 @@ constexpr int kMaxGroups = HMOE_MAX_GROUPS;
 struct SortTile {
   int32_t group, start, rows, index;
 };
+// A transposition [G, N, r] -> [G, r, N] of 16-bit values (N and r multiples of 8) that blocks
+// of the sort's last launch do beside it (in null: none).
+struct SortTranspose {
+  const uint16_t* in;
+  uint16_t* out;
+  int N, r, G;
+};
 struct GroupSort {
   const int32_t* ids;
   int n, G, groups;
@@ -128,6 +135,7 @@ struct GroupSort {
   int tile_rows, max_tiles;
   SortTile* tile;
   int32_t* tile_first;
+  SortTranspose turn;
 };
 size_t sort_count_words(int n, int groups);
 hipError_t launch_sort(const GroupSort& g, hipStream_t s);

@@ -13,6 +13,7 @@
 // in as a sum of bf16 parts (two where the result is rounded to bf16, three where it stays
 // fp32), so it is not rounded to 8 bits on the way.
 #include <algorithm>
+#include <type_traits>
 
 #include "device_common.h"
 #include "hmoe_internal.h"
@@ -169,7 +170,7 @@ __device__ __forceinline__ bool find_tile(const Tiles& t, int* g, int* n, int* i
 // its sums to the lower half through LDS, and the lower half leaves its sums in s_red[wave]
 // for the caller to add in wave order. In a step lane group q holds K elements 32q .. 32q + 31
 // of its row for four MFMAs: the order of the reduction axis is free as long as both operands
-// share it. DEPTH steps' loads are in flight at a time (as many as the registers allow).
+// share it. DEPTH > 1: that many steps' loads are in flight at a time.
 template <int MT, int NT, int W, int DEPTH>
 __device__ __forceinline__ void shrink_tile(const uint16_t* x, long xs, const uint16_t* w, int K,
                                             int r, int n, const int32_t* s_rows, int s0, int s1,
@@ -185,60 +186,113 @@ __device__ __forceinline__ void shrink_tile(const uint16_t* x, long xs, const ui
       xp[i][j] = x + (long)s_rows[rr < n ? rr : 0] * xs;
     }
   f32x4 acc[MT][NT] = {};
-  struct Step {
-    u32x4 x[MT][4], w[NT][4];
-  };
-  // No load stands behind a branch, so that a step's loads leave together. In the last step of
-  // a K that is no multiple of 128, lanes past the end read the step's start and their part of
-  // x is zeroed (W is finite). Ranks come in eights: four ranks of a tile all exist, or the
-  // lane reads others instead.
-  auto load = [&](Step& v, int st) {
-    const int k = st * kKStep;
-    const bool in = k + at < K;
-    const int o = in ? k + at : k;
+  // No load stands behind a branch of a lane's own, so that a step's loads leave together. In
+  // the last step of a K that is no multiple of 128, lanes past the end read the step's start
+  // and their part of x is zeroed (W is finite). Ranks come in eights: four ranks of a tile all
+  // exist, or the lane reads others instead.
+  auto load_x = [&](u32x4 (&v)[MT][4], int st) {
+    const int k = st * kKStep, o = k + at < K ? k + at : k;
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v.x[i][j] = load8(xp[i][j] + o);
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int rank = i * 16 + (c & 12);
-      const uint32_t off = ((rank < r ? rank : 0) * K + o) * 2;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v.w[i][j] = load8(w + (long)j * K, off);
-    }
-    if (k + kKStep > K) {
+      for (int j = 0; j < 4; ++j) v[i][j] = load8(xp[i][j] + o);
+  };
+  auto turn_x = [&](u32x4 (&v)[MT][4], int st) {
+    if ((st + 1) * kKStep > K) {
+      const bool in = st * kKStep + at < K;
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int d = 0; d < 4; ++d) v.x[i][j][d] = in ? v.x[i][j][d] : 0u;
+          for (int d = 0; d < 4; ++d) v[i][j][d] = in ? v[i][j][d] : 0u;
     }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) quad_turn(v[i]);
   };
-  auto multiply = [&](Step& v) {
+  auto load_w = [&](u32x4 (&v)[4], int st, int tile) {
+    const int k = st * kKStep, o = k + at < K ? k + at : k, rank = tile * 16 + (c & 12);
+    const uint32_t off = ((rank < r ? rank : 0) * K + o) * 2;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) quad_turn(v.x[i]);
+    for (int j = 0; j < 4; ++j) v[j] = load8(w + (long)j * K, off);
+  };
+  auto multiply = [&](const u32x4 (&x)[MT][4], u32x4 (&w)[4], int tile) {
+    quad_turn(w);
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      quad_turn(v.w[j]);
+    for (int h = 0; h < 4; ++h)
 #pragma unroll
-      for (int h = 0; h < 4; ++h)
+      for (int i = 0; i < MT; ++i) acc[i][tile] = mfma(x[i][h], w[h], acc[i][tile]);
+  };
+  // A load behind a condition would make every later wait count on its absence, and so wait for
+  // everything; the loops below load ahead without conditions and peel their ends.
+  const int mine = (s1 - s0 - wave + W - 1) / W;  // steps of this wave: s0 + wave + i W
+  auto step = [&](int i) { return s0 + wave + i * W; };
+  if constexpr (DEPTH > 1) {
+    u32x4 x[DEPTH][MT][4], v[DEPTH][NT][4];
+    auto load = [&](int d, int i) {
+      load_x(x[d], step(i));
 #pragma unroll
-        for (int i = 0; i < MT; ++i) acc[i][j] = mfma(v.x[i][h], v.w[j][h], acc[i][j]);
+      for (int t = 0; t < NT; ++t) load_w(v[d][t], step(i), t);
+    };
+    auto use = [&](int d, int i) {
+      turn_x(x[d], step(i));
+#pragma unroll
+      for (int t = 0; t < NT; ++t) multiply(x[d], v[d][t], t);
+    };
+    int i = 0;
+    if (mine >= DEPTH) {
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d) load(d, d);
+      for (; i + 2 * DEPTH <= mine; i += DEPTH) {
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+          use(d, i + d);
+          load(d, i + DEPTH + d);
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d) use(d, i + d);
+      i += DEPTH;
     }
-  };
-  Step ring[DEPTH];
+    // fewer than DEPTH left
+    const int left = mine - i;
 #pragma unroll
-  for (int d = 0; d < DEPTH; ++d)
-    if (s0 + wave + d * W < s1) load(ring[d], s0 + wave + d * W);
-  for (int st = s0 + wave; st < s1;) {
+    for (int d = 0; d < DEPTH - 1; ++d)
+      if (d < left) load(d, i + d);
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d) {
-      if (st >= s1) break;
-      multiply(ring[d]);
-      if (st + DEPTH * W < s1) load(ring[d], st + DEPTH * W);
-      st += W;
+    for (int d = 0; d < DEPTH - 1; ++d)
+      if (d < left) use(d, i + d);
+  } else {
+    // one set of W's registers, each tile of ranks loaded again as soon as it is used up, and
+    // two sets of x's: a step's loads are in flight while the one before is multiplied. Past
+    // rank 64 the set holds half the tiles.
+    constexpr int kW = NT == 8 ? 4 : NT;
+    u32x4 x[2][MT][4], v[kW][4];
+    auto use = [&](int d, int i, auto ahead) {
+      if constexpr (ahead.value) load_x(x[d ^ 1], step(i + 1));
+      turn_x(x[d], step(i));
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        multiply(x[d], v[t % kW], t);
+        if (t + kW < NT) load_w(v[t % kW], step(i), t + kW);
+        else if constexpr (ahead.value) load_w(v[t % kW], step(i + 1), t % kW);
+      }
+    };
+    if (mine > 0) {
+      load_x(x[0], step(0));
+#pragma unroll
+      for (int t = 0; t < kW; ++t) load_w(v[t], step(0), t);
+      int i = 0;
+      for (; i + 2 < mine; i += 2) {
+        use(0, i, std::true_type{});
+        use(1, i + 1, std::true_type{});
+      }
+      if (i + 1 < mine) {
+        use(0, i, std::true_type{});
+        use(1, i + 1, std::false_type{});
+      } else {
+        use(0, i, std::false_type{});
+      }
     }
   }
   auto each = [&](auto f) {
@@ -806,18 +860,25 @@ __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) 
 #pragma unroll
           for (int t = 0; t < 4; ++t) acc[i][t] = mfma(v.p[part][i], xf[t], acc[i][t]);
     };
+    // the next step's loads without a condition of their own (see first product)
     constexpr int kStride = kWgradWaves * 32;
     Step u, v;
     int m = wave * 32;
-    if (m < rows) load(u, m);
-    while (m < rows) {
-      if (m + kStride < rows) load(v, m + kStride);
-      multiply(u);
-      m += kStride;
-      if (m >= rows) break;
-      if (m + kStride < rows) load(u, m + kStride);
-      multiply(v);
-      m += kStride;
+    if (m < rows) {
+      load(u, m);
+      for (; m + 2 * kStride < rows; m += 2 * kStride) {
+        load(v, m + kStride);
+        multiply(u);
+        load(u, m + 2 * kStride);
+        multiply(v);
+      }
+      if (m + kStride < rows) {
+        load(v, m + kStride);
+        multiply(u);
+        multiply(v);
+      } else {
+        multiply(u);
+      }
     }
   }
 #pragma unroll
@@ -841,31 +902,6 @@ __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) 
   }
 }
 
-// B [G, N, r] -> [G, r, N], which makes dy B the same product as x A^T. A thread turns 8
-// columns of 8 ranks in registers: 16-byte reads and writes.
-__global__ __launch_bounds__(256) void lora_transpose_kernel(const uint16_t* in, uint16_t* out, int N,
-                                                             int r, int G) {
-  const int nb = N / 8, rb = r / 8;
-  const long i = blockIdx.x * 256L + threadIdx.x;
-  if (i >= (long)G * rb * nb) return;
-  const int b = (int)(i % nb);
-  const long gr = i / nb;
-  const int k = (int)(gr % rb);
-  const long g = gr / rb;
-  u32x4 v[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = load8(in + (g * N + b * 8 + j) * r + k * 8);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    Half8 o;
-#pragma unroll
-    for (int p = 0; p < 4; ++p)
-      o.w[p] = __builtin_amdgcn_perm(v[2 * p + 1][j >> 1], v[2 * p][j >> 1],
-                                     (j & 1) ? 0x07060302u : 0x05040100u);
-    *reinterpret_cast<Half8*>(out + (g * r + k * 8 + j) * N + b * 8) = o;
-  }
-}
-
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
@@ -874,6 +910,7 @@ namespace {
 
 constexpr int kDirectRows = 1024;       // up to this many rows a block finds its tile by itself
 constexpr int kFusedBytes = 512 << 10;  // largest first matrix of the one-launch form
+constexpr int kShrinkBlocks = 400;      // about this many blocks of the first product
 constexpr int kFusedRank = 64;          // and its largest rank (registers)
 
 struct Plan {
@@ -909,7 +946,8 @@ Plan plan_tiles(int M, int G, int K, int r, bool backward) {
 // wave of a block, at most 16 partial sums to add up again.
 int plan_splits(const Plan& p, int K) {
   const int steps = (K + kKStep - 1) / kKStep;
-  return std::max(1, std::min({(768 + p.busy * p.rt / (p.mt * 16) - 1) / (p.busy * p.rt / (p.mt * 16)), (steps + kShrinkWaves - 1) / kShrinkWaves, 16}));
+  const int blocks = p.busy * (p.rt / (p.mt * 16));
+  return std::max(1, std::min({(kShrinkBlocks + blocks - 1) / blocks, (steps + kShrinkWaves - 1) / kShrinkWaves, 16}));
 }
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -944,7 +982,7 @@ Space plan_space(int M, int G, int K, int N, int r, bool backward) {
 }
 
 hipError_t make_tiles(const int32_t* ids, int M, int G, const Plan& p, const Space& sp, char* scratch,
-                      Tiles* t, hipStream_t s) {
+                      Tiles* t, const SortTranspose& turn, hipStream_t s) {
   *t = Tiles{ids, M, G, p.tiles, nullptr, nullptr};
   if (!p.table) return hipSuccess;
   GroupSort g{};
@@ -959,6 +997,7 @@ hipError_t make_tiles(const int32_t* ids, int M, int G, const Plan& p, const Spa
   g.max_tiles = p.tiles;
   g.tile = reinterpret_cast<SortTile*>(scratch + sp.tile);
   g.tile_first = reinterpret_cast<int32_t*>(scratch + sp.tile_first);
+  g.turn = turn;
   t->sorted = g.sorted;
   t->table = g.tile;
   return launch_sort(g, s);
@@ -1004,7 +1043,7 @@ hipError_t expand(const Plan& p, ExpandArgs a, hipStream_t s) {
   const int groups = (a.c.N + kCols - 1) / kCols;
   const int parts = p.wide ? 1 : p.rt / 16, unit = p.wide ? 1 : kExpandWaves;
   // columns a block: as few rounds of its waves as let all blocks be on the card at once
-  const int ks = z_steps(a.c.r), room = 256 * (ks <= 1 ? 4 : ks <= 3 ? 3 : 2);
+  const int ks = z_steps(a.c.r), room = 256 * (ks <= 1 ? 3 : 2);
   const int rounds = std::max(1, (int)(((long)groups * p.busy * parts + (long)room * unit - 1) / ((long)room * unit)));
   a.col_groups = std::min(rounds, (groups + unit - 1) / unit) * unit;
   a.steps_per_tile = p.rt / 32;
@@ -1046,7 +1085,7 @@ hipError_t launch_lora(const Lora& l, void* scratch, hipStream_t s) {
   }
   const Space sp = plan_space(l.M, l.G, l.K, l.N, l.r, false);
   Tiles t;
-  hipError_t err = make_tiles(l.ids, l.M, l.G, p, sp, b, &t, s);
+  hipError_t err = make_tiles(l.ids, l.M, l.G, p, sp, b, &t, {}, s);
   if (err != hipSuccess) return err;
   const int splits = plan_splits(p, l.K);
   float* part = reinterpret_cast<float*>(b + sp.part);
@@ -1060,15 +1099,12 @@ hipError_t launch_lora_backward(const LoraGrad& l, void* scratch, hipStream_t s)
   const Plan p = plan_tiles(l.M, l.G, l.K, l.r, true);
   const Space sp = plan_space(l.M, l.G, l.K, l.N, l.r, true);
   Tiles t;
-  hipError_t err = make_tiles(l.ids, l.M, l.G, p, sp, b, &t, s);
+  // B^T [G, r, N], which makes dy B the same product as x A^T, is laid out beside the sort
+  uint16_t* Bt = reinterpret_cast<uint16_t*>(b + sp.bt);
+  hipError_t err = make_tiles(l.ids, l.M, l.G, p, sp, b, &t, SortTranspose{l.B, Bt, l.N, l.r, l.G}, s);
   if (err != hipSuccess) return err;
   uint16_t* frag[2] = {reinterpret_cast<uint16_t*>(b + sp.frag[0]), reinterpret_cast<uint16_t*>(b + sp.frag[1])};
   if (l.M > 0) {
-    uint16_t* Bt = reinterpret_cast<uint16_t*>(b + sp.bt);
-    const long blocks = ((long)l.G * (l.r / 8) * (l.N / 8) + 255) / 256;
-    hipLaunchKernelGGL(lora_transpose_kernel, dim3((unsigned)blocks), dim3(256), 0, s, l.B, Bt, l.N, l.r,
-                       l.G);
-    if ((err = hipGetLastError()) != hipSuccess) return err;
     const int splits = plan_splits(p, l.N);
     float* part = reinterpret_cast<float*>(b + sp.part);
     err = shrink(p, ShrinkArgs{t, l.dy, l.dys, Bt, l.N, l.r, splits, part}, s);

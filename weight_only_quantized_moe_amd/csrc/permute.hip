@@ -41,6 +41,7 @@ struct SortArgs {
   int max_tiles;
   SortTile* tile;
   int32_t* tile_first;  // [groups + 1]
+  SortTranspose turn;
 };
 
 // group of an id: ids outside [0, G) are dropped (-1) or the group behind the last
@@ -108,6 +109,33 @@ __global__ __launch_bounds__(kSortWide) void sort_count_kernel(SortArgs a) {
   for (int e = threadIdx.x; e < a.groups; e += kSortWide) out[e] = s_cnt[e];
 }
 
+// 16 bytes at element alignment
+struct __attribute__((packed, aligned(2))) Raw16 {
+  uint32_t w[4];
+};
+
+// eight columns of eight ranks a thread, turned in registers: 16-byte reads and writes
+__device__ __forceinline__ void transpose_block(const SortTranspose& t, long i) {
+  const int nb = t.N / 8, rb = t.r / 8;
+  if (i >= (long)t.G * rb * nb) return;
+  const int b = (int)(i % nb);
+  const long gr = i / nb, g = gr / rb;
+  const int k = (int)(gr % rb);
+  Raw16 v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    v[j] = *reinterpret_cast<const Raw16*>(t.in + (g * t.N + b * 8 + j) * t.r + k * 8);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    Raw16 o;
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+      o.w[p] = __builtin_amdgcn_perm(v[2 * p + 1].w[j >> 1], v[2 * p].w[j >> 1],
+                                     (j & 1) ? 0x07060302u : 0x05040100u);
+    *reinterpret_cast<Raw16*>(t.out + (g * t.r + k * 8 + j) * t.N + b * 8) = o;
+  }
+}
+
 // Places one block's chunk: every wave owns a contiguous part of it, so the order is that
 // of a serial counting sort whatever the timing. With one block the counts are its own;
 // else each block sums the count table of all blocks (read from L2, eight loads in flight).
@@ -120,6 +148,10 @@ __global__ __launch_bounds__(THREADS) void sort_place_kernel(SortArgs a) {
   __shared__ int32_t s_base[kGroups];       // first row of each group
   __shared__ int32_t s_tile[kGroups + 1];   // first tile of each group
   __shared__ int32_t s_part[kWaves];
+  if ((int)blockIdx.x >= a.nb) {  // blocks beside the sort
+    transpose_block(a.turn, (long)(blockIdx.x - a.nb) * THREADS + threadIdx.x);
+    return;
+  }
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid >> 6;
   const int c0 = min((long)blockIdx.x * a.chunk, (long)a.n), c1 = min(c0 + (long)a.chunk, (long)a.n);
   const int part = ((c1 - c0 + THREADS - 1) / THREADS) * kWave;  // ids per wave
@@ -193,7 +225,7 @@ __global__ __launch_bounds__(THREADS) void sort_place_kernel(SortArgs a) {
     if (a.tile_rows) a.tile_first[a.groups] = tiles;
   }
   __syncthreads();
-  const int gid = blockIdx.x * THREADS + tid, gsz = gridDim.x * THREADS;
+  const int gid = blockIdx.x * THREADS + tid, gsz = a.nb * THREADS;
   for (int i = placed + gid; i < a.n; i += gsz) a.sorted[i] = -1;
   if (a.tile_rows) {
     // Entry i is what block i of a launch takes. Blocks go to the 8 XCDs in turn, so the
@@ -272,10 +304,13 @@ hipError_t launch_sort(const GroupSort& g, hipStream_t s) {
   a.tile = g.tile;
   a.tile_first = g.tile_first;
   if (a.nb > 1) hipLaunchKernelGGL(sort_count_kernel, dim3(a.nb), dim3(kSortWide), 0, s, a);
+  a.turn = g.turn;
+  const long turns = g.turn.in ? (long)g.turn.G * (g.turn.N / 8) * (g.turn.r / 8) : 0;
+  auto blocks = [&](int threads) { return dim3((unsigned)(a.nb + (turns + threads - 1) / threads)); };
   if (g.groups <= kSortWideGroups)
-    hipLaunchKernelGGL(sort_place_kernel<kSortWide>, dim3(a.nb), dim3(kSortWide), 0, s, a);
+    hipLaunchKernelGGL(sort_place_kernel<kSortWide>, blocks(kSortWide), dim3(kSortWide), 0, s, a);
   else
-    hipLaunchKernelGGL(sort_place_kernel<kSortNarrow>, dim3(a.nb), dim3(kSortNarrow), 0, s, a);
+    hipLaunchKernelGGL(sort_place_kernel<kSortNarrow>, blocks(kSortNarrow), dim3(kSortNarrow), 0, s, a);
   return hipGetLastError();
 }
 
@@ -284,11 +319,6 @@ hipError_t launch_sort(const GroupSort& g, hipStream_t s) {
 // ---------------------------------------------------------------------------
 
 constexpr int kRowThreads = 256;
-
-// 16 bytes at element alignment
-struct __attribute__((packed, aligned(2))) Raw16 {
-  uint32_t w[4];
-};
 
 // element types of the rows: conversion of one 16-byte vector and of one element
 struct Bf16 {
