@@ -397,8 +397,8 @@ hmoe_status moe_quantize_mxfp4(const float* in, int32_t rows, int32_t K, uint8_t
  *     kernels run, so calls that may overlap in time need scratch buffers of their own.
  *   - Results do not depend on timing: fixed-order sums, no floating-point atomics. */
 
-/* Bytes of scratch of moe_permute for M tokens (0 up to 1024 slots: scratch may then be
- * NULL). Host arithmetic only. Errors: as moe_permute. */
+/* Bytes of scratch of moe_permute for M tokens (0 for few slots: scratch may then be NULL).
+ * Host arithmetic only. Errors: as moe_permute. */
 hmoe_status moe_permute_scratch_bytes(int32_t M, int32_t k, int32_t E, size_t* bytes);
 
 /* Tokens into expert order. With slot s = t * k + j, the slots whose id lies in [0, E) are
@@ -409,7 +409,7 @@ hmoe_status moe_permute_scratch_bytes(int32_t M, int32_t k, int32_t E, size_t* b
  *   sorted_slots  int32 [M * k]: slot of each row, -1 at and past expert_off[E]
  *   slot_row      int32 [M, k]: row of each slot, -1 for a dropped slot
  *   expert_off    int32 [E + 1]: first row of each expert, then the number of rows
- * M = 0 writes expert_off only. Up to 1024 slots it is one launch.
+ * M = 0 writes expert_off only. Up to 2048 slots it is one launch.
  * Errors: HMOE_ERR_INVALID_ARG (M < 0, k outside 1..16, E outside 1..1024, H < 1, a stride
  * below H, an unknown dtype); HMOE_ERR_UNSUPPORTED (M * k > 2^24, or rows of 2^24 blocks of
  * 4 KiB or more); HMOE_ERR_SCRATCH; HMOE_ERR_ALIGN; HMOE_ERR_HIP. */
@@ -468,7 +468,7 @@ hmoe_status moe_lora_scratch_bytes(int32_t M, int32_t G, int32_t K, int32_t N, i
  * base and y [M, N], A [G, rank, K], B [G, N, rank] (an adapter of lower rank is padded with
  * zeros), scale fp32 [G]. z fp32 [M, rank] is what moe_lora_backward needs and may be NULL.
  * A and B must be finite (an infinite entry gives infinities or NaN in the rows that use it).
- * M = 0 is a no-op. Up to 1024 rows it is two launches.
+ * M = 0 is a no-op. Up to 1024 rows it is one or two launches.
  * Errors: HMOE_ERR_INVALID_ARG (M < 0; G, K, N or rank < 1; a stride below the row's length;
  * base == y with another stride); HMOE_ERR_UNSUPPORTED (K, N or rank not a multiple of 8,
  * rank > 128, G > HMOE_MAX_GROUPS, M > 2^22, K or N > 2^20); HMOE_ERR_SCRATCH; HMOE_ERR_ALIGN;

@@ -87,8 +87,8 @@ def run_permute(hm, torch, x, ids, E, rows=None):
     return rows, srt, sr, off
 
 
-# 128 x 8 slots is the last single launch, 129 x 8 the first sort; 2048 slots the last sort in
-# one block; 5000 x 8 with 1024 experts has its block count bounded by the count table
+# 256 x 8 slots is the last single launch, 257 x 8 the first sort; 1024 x 8 the last sort in one
+# block; 5000 x 8 with 1024 experts has its block count bounded by the count table
 PERMUTE = [(0, 2, 4, 8, "bfloat16", "any"), (1, 1, 1, 1, "float32", "any"), (1, 8, 128, 2048, "bfloat16", "any"),
            (3, 16, 40, 13, "float16", "any"), (8, 8, 256, 6144, "bfloat16", "share"),
            (128, 8, 256, 96, "float16", "share"), (129, 8, 256, 96, "bfloat16", "share"),
@@ -96,7 +96,8 @@ PERMUTE = [(0, 2, 4, 8, "bfloat16", "any"), (1, 1, 1, 1, "float32", "any"), (1, 
            (256, 8, 64, 64, "bfloat16", "any"), (257, 8, 64, 65, "float32", "any"),
            (1500, 3, 1024, 8, "bfloat16", "share"), (5000, 8, 1024, 4, "float16", "any"),
            (4096, 8, 8, 4, "bfloat16", "one"), (2000, 2, 2, 40, "float32", "one"),
-           (1300, 16, 17, 24, "bfloat16", "any")]
+           (1300, 16, 17, 24, "bfloat16", "any"),
+           (1024, 8, 256, 24, "bfloat16", "share"), (1025, 8, 641, 24, "float16", "share"), (900, 9, 640, 17, "float32", "any")]
 
 
 @pytest.mark.parametrize("M,k,E,H,dtype,kind", PERMUTE)

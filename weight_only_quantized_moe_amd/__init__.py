@@ -358,55 +358,60 @@ def moe_quantize_mxfp4(x, codes, scales, stream=None) -> None:
 
 _torch = None
 _CODES = {}
+_I32 = _F32 = None
+_this_device = _raw_stream = None
+_functions = {}
 
 
 def _load_torch():
-    global _torch
+    global _torch, _I32, _F32, _this_device, _raw_stream
     import torch
     # int16 holds bf16 bits, as for the layer
     _CODES.update({torch.bfloat16: DTYPE_BF16, torch.int16: DTYPE_BF16, torch.float16: DTYPE_FP16,
                    torch.float32: DTYPE_FP32})
+    _I32, _F32 = torch.int32, torch.float32
+    _this_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
     _torch = torch
-    return torch
 
 
 def _dtype_code(t) -> int:
     """Element type of a rows tensor."""
-    if _torch is None:
-        _load_torch()
     code = _CODES.get(t.dtype)
     if code is None:
+        if _torch is None:
+            _load_torch()
+            return _dtype_code(t)
         raise ValueError(f"rows of {t.dtype}: expected bfloat16 (or its bits as int16), float16 "
                          "or float32")
     return code
 
 
-def _matrix(name: str, t, rows: int, cols: int, code: int) -> int:
-    """Checks a [rows, cols] matrix of the given element type; returns its row stride."""
-    if t.shape != (rows, cols) or _CODES.get(t.dtype) != code:
-        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}, expected [{rows}, {cols}] of the "
+def _matrix(name: str, t, shape: tuple, code: int) -> int:
+    """Checks a matrix of the given shape and element type; returns its row stride."""
+    if t.shape != shape or _CODES.get(t.dtype) != code:
+        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}, expected {list(shape)} of the "
                          "operator's row type")
+    if t.is_contiguous():
+        return shape[1]
     s = t.stride()
-    if s[1] != 1 and cols > 1:
+    if s[1] != 1 and shape[1] > 1:
         raise ValueError(f"{name}: the last axis must be contiguous")
-    return s[0] if rows > 1 else cols
+    return s[0] if shape[0] > 1 else shape[1]
 
 
-def _ints(name: str, t, shape: tuple) -> None:
-    if t.shape != shape or t.dtype is not (_torch or _load_torch()).int32 or not t.is_contiguous():
-        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}, expected contiguous int32 {shape}")
-
-
-def _floats(name: str, t, shape: tuple) -> None:
-    if t.shape != shape or t.dtype is not _torch.float32 or not t.is_contiguous():
-        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}, expected contiguous float32 {shape}")
+def _refuse(shape: tuple, dtype, **tensors) -> None:
+    """Names the first tensor that is not contiguous, of this shape and type."""
+    for name, t in tensors.items():
+        if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+            raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} (strides {t.stride()}), expected "
+                             f"contiguous {dtype} {tuple(shape)}")
 
 
 def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _launch(function: str, stream, tensors: tuple, *args) -> None:
+def _launch(function: str, stream, tensors, *args) -> None:
     """Calls a C function on the tensors' device: its stream argument is the given one, else
     that device's current stream. Tensors on different devices, or not on a GPU, are refused."""
     dev = tensors[0].get_device()
@@ -415,13 +420,14 @@ def _launch(function: str, stream, tensors: tuple, *args) -> None:
             raise ValueError("all tensors of a call must be on one GPU")
     if dev < 0:
         raise ValueError("all tensors of a call must be on one GPU")
-    fn = getattr(_lib or load_library(), function)
-    cuda = _torch.cuda
-    if cuda.current_device() == dev:
-        status = fn(*args, _torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream)
+    fn = _functions.get(function)
+    if fn is None:
+        fn = _functions[function] = getattr(load_library(), function)
+    if _this_device() == dev:
+        status = fn(*args, _raw_stream(dev) if stream is None else stream)
     else:
-        with cuda.device(dev):
-            status = fn(*args, _torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream)
+        with _torch.cuda.device(dev):
+            status = fn(*args, _raw_stream(dev) if stream is None else stream)
     if status:
         _check(status)
 
@@ -445,40 +451,49 @@ def moe_permute(x, topk_ids, num_experts: int, rows, sorted_slots, slot_row, exp
                 scratch=None, stream=None) -> None:
     """x[M, H] into expert order: rows[M * k, H], sorted_slots i32 [M * k], slot_row i32
     [M, k] and expert_off i32 [E + 1] (see include/hmoe.h). Ids outside [0, E) are dropped."""
-    M, k = topk_ids.shape
-    H = x.shape[-1]
     code = _dtype_code(x)
-    xs, rs = _matrix("x", x, M, H, code), _matrix("rows", rows, M * k, H, code)
-    _ints("topk_ids", topk_ids, (M, k))
-    _ints("sorted_slots", sorted_slots, (M * k,))
-    _ints("slot_row", slot_row, (M, k))
-    _ints("expert_off", expert_off, (num_experts + 1,))
+    shape = topk_ids.shape
+    M, k = shape
+    n, H = M * k, x.shape[-1]
+    xs, rs = _matrix("x", x, (M, H), code), _matrix("rows", rows, (n, H), code)
+    if not (topk_ids.dtype is _I32 and topk_ids.is_contiguous() and slot_row.dtype is _I32
+            and slot_row.shape == shape and slot_row.is_contiguous()):
+        _refuse(shape, _I32, topk_ids=topk_ids, slot_row=slot_row)
+    if not (sorted_slots.dtype is _I32 and sorted_slots.shape == (n,) and sorted_slots.is_contiguous()):
+        _refuse((n,), _I32, sorted_slots=sorted_slots)
+    if not (expert_off.dtype is _I32 and expert_off.shape == (num_experts + 1,)
+            and expert_off.is_contiguous()):
+        _refuse((num_experts + 1,), _I32, expert_off=expert_off)
     ws, nbytes = _room(scratch)
-    _launch("moe_permute", stream, (x, topk_ids, rows, sorted_slots, slot_row, expert_off,
-            scratch), x.data_ptr(), xs, topk_ids.data_ptr(), M, k, num_experts, H, code,
-            rows.data_ptr(), rs, sorted_slots.data_ptr(), slot_row.data_ptr(),
-            expert_off.data_ptr(), ws, nbytes)
+    _launch("moe_permute", stream, (x, topk_ids, rows, sorted_slots, slot_row, expert_off, scratch),
+            x.data_ptr(), xs, topk_ids.data_ptr(), M, k, num_experts, H, code, rows.data_ptr(), rs,
+            sorted_slots.data_ptr(), slot_row.data_ptr(), expert_off.data_ptr(), ws, nbytes)
 
 
 def moe_permute_backward(drows, slot_row, dx, stream=None) -> None:
     """dx[M, H] = for each token the sum of its slots' drows[M * k, H]."""
-    M, k = slot_row.shape
-    H = drows.shape[-1]
     code = _dtype_code(drows)
-    ds, xs = _matrix("drows", drows, M * k, H, code), _matrix("dx", dx, M, H, code)
-    _ints("slot_row", slot_row, (M, k))
+    shape = slot_row.shape
+    M, k = shape
+    H = drows.shape[-1]
+    ds, xs = _matrix("drows", drows, (M * k, H), code), _matrix("dx", dx, (M, H), code)
+    if not (slot_row.dtype is _I32 and slot_row.is_contiguous()):
+        _refuse(shape, _I32, slot_row=slot_row)
     _launch("moe_permute_backward", stream, (drows, slot_row, dx), drows.data_ptr(), ds,
             slot_row.data_ptr(), M, k, H, code, dx.data_ptr(), xs)
 
 
 def moe_unpermute(rows, slot_row, topk_w, y, stream=None) -> None:
     """y[M, H] = for each token the sum of its slots' rows[M * k, H] times topk_w f32 [M, k]."""
-    M, k = slot_row.shape
-    H = rows.shape[-1]
     code = _dtype_code(rows)
-    rs, ys = _matrix("rows", rows, M * k, H, code), _matrix("y", y, M, H, code)
-    _ints("slot_row", slot_row, (M, k))
-    _floats("topk_w", topk_w, (M, k))
+    shape = slot_row.shape
+    M, k = shape
+    H = rows.shape[-1]
+    rs, ys = _matrix("rows", rows, (M * k, H), code), _matrix("y", y, (M, H), code)
+    if not (slot_row.dtype is _I32 and slot_row.is_contiguous()):
+        _refuse(shape, _I32, slot_row=slot_row)
+    if not (topk_w.dtype is _F32 and topk_w.shape == shape and topk_w.is_contiguous()):
+        _refuse(shape, _F32, topk_w=topk_w)
     _launch("moe_unpermute", stream, (rows, slot_row, topk_w, y), rows.data_ptr(), rs,
             slot_row.data_ptr(), topk_w.data_ptr(), M, k, H, code, y.data_ptr(), ys)
 
@@ -486,27 +501,36 @@ def moe_unpermute(rows, slot_row, topk_w, y, stream=None) -> None:
 def moe_unpermute_backward(dy, rows, slot_row, topk_w, drows, dw, stream=None) -> None:
     """Gradients of moe_unpermute: drows[M * k, H] (rows no slot names stay as they were) and
     dw f32 [M, k]."""
-    M, k = slot_row.shape
-    H = rows.shape[-1]
     code = _dtype_code(rows)
-    ys, rs = _matrix("dy", dy, M, H, code), _matrix("rows", rows, M * k, H, code)
-    ds = _matrix("drows", drows, M * k, H, code)
-    _ints("slot_row", slot_row, (M, k))
-    _floats("topk_w", topk_w, (M, k))
-    _floats("dw", dw, (M, k))
-    _launch("moe_unpermute_backward", stream, (dy, rows, slot_row, topk_w, drows, dw),
-            dy.data_ptr(), ys, rows.data_ptr(), rs, slot_row.data_ptr(), topk_w.data_ptr(), M,
-            k, H, code, drows.data_ptr(), ds, dw.data_ptr())
+    shape = slot_row.shape
+    M, k = shape
+    n, H = M * k, rows.shape[-1]
+    ys, rs = _matrix("dy", dy, (M, H), code), _matrix("rows", rows, (n, H), code)
+    ds = _matrix("drows", drows, (n, H), code)
+    if not (slot_row.dtype is _I32 and slot_row.is_contiguous()):
+        _refuse(shape, _I32, slot_row=slot_row)
+    if not (topk_w.dtype is _F32 and topk_w.shape == shape and topk_w.is_contiguous()
+            and dw.dtype is _F32 and dw.shape == shape and dw.is_contiguous()):
+        _refuse(shape, _F32, topk_w=topk_w, dw=dw)
+    _launch("moe_unpermute_backward", stream, (dy, rows, slot_row, topk_w, drows, dw), dy.data_ptr(),
+            ys, rows.data_ptr(), rs, slot_row.data_ptr(), topk_w.data_ptr(), M, k, H, code,
+            drows.data_ptr(), ds, dw.data_ptr())
 
 
 def moe_route_backward(topk_ids, topk_w, dw, dlogits, stream=None) -> None:
     """dlogits f32 [M, E] (fully overwritten) from moe_route's ids and weights and dw f32 [M, k]."""
-    M, k = topk_ids.shape
+    if _torch is None:
+        _load_torch()
+    shape = topk_ids.shape
+    M, k = shape
     E = dlogits.shape[-1]
-    _ints("topk_ids", topk_ids, (M, k))
-    _floats("topk_w", topk_w, (M, k))
-    _floats("dw", dw, (M, k))
-    _floats("dlogits", dlogits, (M, E))
+    if not (topk_ids.dtype is _I32 and topk_ids.is_contiguous()):
+        _refuse(shape, _I32, topk_ids=topk_ids)
+    if not (topk_w.dtype is _F32 and topk_w.shape == shape and topk_w.is_contiguous()
+            and dw.dtype is _F32 and dw.shape == shape and dw.is_contiguous()):
+        _refuse(shape, _F32, topk_w=topk_w, dw=dw)
+    if not (dlogits.dtype is _F32 and dlogits.shape == (M, E) and dlogits.is_contiguous()):
+        _refuse((M, E), _F32, dlogits=dlogits)
     _launch("moe_route_backward", stream, (topk_ids, topk_w, dw, dlogits), topk_ids.data_ptr(),
             topk_w.data_ptr(), dw.data_ptr(), M, E, k, dlogits.data_ptr())
 
@@ -525,8 +549,10 @@ def _adapters(M: int, ids, A, B, scale) -> tuple:
     if (_dtype_code(A) != DTYPE_BF16 or _dtype_code(B) != DTYPE_BF16 or not A.is_contiguous()
             or not B.is_contiguous()):
         raise ValueError("A and B must be contiguous bfloat16")
-    _ints("ids", ids, (M,))
-    _floats("scale", scale, (a[0],))
+    if not (ids.dtype is _I32 and ids.shape == (M,) and ids.is_contiguous()):
+        _refuse((M,), _I32, ids=ids)
+    if not (scale.dtype is _F32 and scale.shape == (a[0],) and scale.is_contiguous()):
+        _refuse((a[0],), _F32, scale=scale)
     return a[0], a[1], a[2], b[1]
 
 
@@ -536,14 +562,14 @@ def moe_lora(x, ids, A, B, scale, base, y, z=None, scratch=None, stream=None) ->
     receives A[g] x for moe_lora_backward. Ids outside [0, G): no adapter."""
     M = x.shape[0]
     G, r, K, N = _adapters(M, ids, A, B, scale)
-    xs, ys = _matrix("x", x, M, K, DTYPE_BF16), _matrix("y", y, M, N, DTYPE_BF16)
-    bs = 0 if base is None else _matrix("base", base, M, N, DTYPE_BF16)
-    if z is not None:
-        _floats("z", z, (M, r))
+    xs, ys = _matrix("x", x, (M, K), DTYPE_BF16), _matrix("y", y, (M, N), DTYPE_BF16)
+    bs = 0 if base is None else _matrix("base", base, (M, N), DTYPE_BF16)
+    if z is not None and not (z.dtype is _F32 and z.shape == (M, r) and z.is_contiguous()):
+        _refuse((M, r), _F32, z=z)
     ws, nbytes = _room(scratch)
     _launch("moe_lora", stream, (x, ids, A, B, scale, base, y, z, scratch), x.data_ptr(), xs,
-            ids.data_ptr(), A.data_ptr(), B.data_ptr(), scale.data_ptr(), M, G, K, N, r,
-            _at(base), bs, y.data_ptr(), ys, _at(z), ws, nbytes)
+            ids.data_ptr(), A.data_ptr(), B.data_ptr(), scale.data_ptr(), M, G, K, N, r, _at(base),
+            bs, y.data_ptr(), ys, _at(z), ws, nbytes)
 
 
 def moe_lora_backward(dy, x, z, ids, A, B, scale, dbase, dx, dA, dB, scratch=None,
@@ -552,17 +578,17 @@ def moe_lora_backward(dy, x, z, ids, A, B, scale, dbase, dx, dA, dB, scratch=Non
     [G, N, rank] (fully overwritten). dbase may be None (zeros) or dx itself."""
     M = x.shape[0]
     G, r, K, N = _adapters(M, ids, A, B, scale)
-    ys, xs = _matrix("dy", dy, M, N, DTYPE_BF16), _matrix("x", x, M, K, DTYPE_BF16)
-    ds = _matrix("dx", dx, M, K, DTYPE_BF16)
-    bs = 0 if dbase is None else _matrix("dbase", dbase, M, K, DTYPE_BF16)
-    _floats("z", z, (M, r))
-    _floats("dA", dA, (G, r, K))
-    _floats("dB", dB, (G, N, r))
+    ys, xs = _matrix("dy", dy, (M, N), DTYPE_BF16), _matrix("x", x, (M, K), DTYPE_BF16)
+    ds = _matrix("dx", dx, (M, K), DTYPE_BF16)
+    bs = 0 if dbase is None else _matrix("dbase", dbase, (M, K), DTYPE_BF16)
+    _refuse((M, r), _F32, z=z)
+    _refuse((G, r, K), _F32, dA=dA)
+    _refuse((G, N, r), _F32, dB=dB)
     ws, nbytes = _room(scratch)
-    _launch("moe_lora_backward", stream, (dy, x, z, ids, A, B, scale, dbase, dx, dA, dB,
-            scratch), dy.data_ptr(), ys, x.data_ptr(), xs, z.data_ptr(), ids.data_ptr(),
-            A.data_ptr(), B.data_ptr(), scale.data_ptr(), M, G, K, N, r, _at(dbase), bs,
-            dx.data_ptr(), ds, dA.data_ptr(), dB.data_ptr(), ws, nbytes)
+    _launch("moe_lora_backward", stream, (dy, x, z, ids, A, B, scale, dbase, dx, dA, dB, scratch),
+            dy.data_ptr(), ys, x.data_ptr(), xs, z.data_ptr(), ids.data_ptr(), A.data_ptr(),
+            B.data_ptr(), scale.data_ptr(), M, G, K, N, r, _at(dbase), bs, dx.data_ptr(), ds,
+            dA.data_ptr(), dB.data_ptr(), ws, nbytes)
 
 
 class DeviceWeights:

@@ -141,8 +141,11 @@ size_t sort_count_words(int n, int groups);
 hipError_t launch_sort(const GroupSort& g, hipStream_t s);
 
 // permute.hip: the row movements between token order and expert order (strides in
-// elements); up to kPermuteSmall ids one launch ranks and copies
-constexpr int kPermuteSmall = 1024;
+// elements); up to kPermuteSmall ids one launch ranks and copies. Every block compares its
+// token's slots with all ids there: on MI355X, 8 slots a token, 2048 ids take 7.3 us (rows of
+// 2048 bf16) and 10.8 (6144) in one launch, 9.3 and 12.4 with a sort before the copy; 4096 ids
+// 12.2 and 26.4 against 12.9 and 18.6.
+constexpr int kPermuteSmall = 2048;
 struct PermuteRows {
   const void* src;
   long src_stride;

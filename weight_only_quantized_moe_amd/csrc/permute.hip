@@ -10,6 +10,7 @@
 #include <limits.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "device_common.h"
 #include "hmoe_internal.h"
@@ -395,12 +396,28 @@ __device__ __forceinline__ RowPlace row_place(int chunks) {
   return {t, ((long)(blockIdx.x - t * chunks) * kRowThreads + threadIdx.x) * 16};
 }
 
+// Rows that no cache will hold until they are used again are read and written past the caches'
+// replacement order (STREAM). On MI355X, bf16 rows of 6144, 8 slots a token, three sets of rows
+// in turn: the weighted sum at 2000 tokens (197 MB of rows) takes 38 us so and 47 otherwise, at
+// 700 (69 MB) 17.1 and 15.3; its gradient 83 and 87, 29 and 32 us, and at 300 (29 MB) 16.8 and
+// 13.7; the copy 49 and 54, and the same below 70 MB.
+constexpr long kStreamBytes = 64L << 20;
+
+typedef uint32_t Vec16 __attribute__((ext_vector_type(4), aligned(2)));
+
 // the bytes [at, at + 16) of a row of `bytes` bytes; a row's last, partial vector is read
 // and written two bytes at a time (rows are whole elements of 2 or 4 bytes)
+template <bool STREAM>
 __device__ __forceinline__ Raw16 load_raw(const char* row, long at, long bytes) {
   Raw16 v{};
   if (at + 16 <= bytes) {
-    v = *reinterpret_cast<const Raw16*>(row + at);
+    if constexpr (STREAM) {
+      const Vec16 q = __builtin_nontemporal_load(reinterpret_cast<const Vec16*>(row + at));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v.w[i] = q[i];
+    } else {
+      v = *reinterpret_cast<const Raw16*>(row + at);
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -410,9 +427,13 @@ __device__ __forceinline__ Raw16 load_raw(const char* row, long at, long bytes) 
   return v;
 }
 
+template <bool STREAM>
 __device__ __forceinline__ void store_raw(char* row, long at, long bytes, const Raw16& v) {
   if (at + 16 <= bytes) {
-    *reinterpret_cast<Raw16*>(row + at) = v;
+    if constexpr (STREAM)
+      __builtin_nontemporal_store(Vec16{v.w[0], v.w[1], v.w[2], v.w[3]}, reinterpret_cast<Vec16*>(row + at));
+    else
+      *reinterpret_cast<Raw16*>(row + at) = v;
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -422,16 +443,17 @@ __device__ __forceinline__ void store_raw(char* row, long at, long bytes, const 
 }
 
 // Copies each token's row to its slots' places: x is read once, every row written once.
+template <bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void permute_copy_kernel(
     const char* __restrict__ x, long xs, const int32_t* __restrict__ slot_row, int k, int chunks,
     long bytes, char* __restrict__ rows, long rs) {
   const auto [tok, at] = row_place(chunks);
   const long t = tok;
   if (at >= bytes) return;
-  const Raw16 v = load_raw(x + t * xs, at, bytes);
+  const Raw16 v = load_raw<false>(x + t * xs, at, bytes);
   for (int j = 0; j < k; ++j) {
     const int r = slot_row[t * k + j];
-    if (r >= 0) store_raw(rows + (long)r * rs, at, bytes, v);
+    if (r >= 0) store_raw<STREAM>(rows + (long)r * rs, at, bytes, v);
   }
 }
 
@@ -449,10 +471,10 @@ struct PermuteSmallArgs {
 };
 
 // The whole permutation in one launch, for few ids: every block ranks its own token's slots
-// against all ids (16 lanes a slot: how many ids lie before it in the sorted order) while
+// against all ids (how many lie before it in the sorted order, 16 to 64 lanes a slot) while
 // its part of the token's row is on the way. One more block writes the offsets.
 __global__ __launch_bounds__(kRowThreads) void permute_small_kernel(PermuteSmallArgs a) {
-  __shared__ int32_t s_id[kPermuteSmall];
+  __shared__ __align__(16) int32_t s_id[kPermuteSmall];
   __shared__ int32_t s_cnt[kMaxExperts];
   __shared__ int32_t s_row[kMaxTopK];
   __shared__ int32_t s_part[kRowThreads / kWave];
@@ -481,22 +503,27 @@ __global__ __launch_bounds__(kRowThreads) void permute_small_kernel(PermuteSmall
     return;
   }
   Raw16 v{};
-  if (at < a.bytes) v = load_raw(a.x + t * a.xs, at, a.bytes);
-  for (int i = tid; i < n; i += kRowThreads) {
-    const int e = a.ids[i];
-    s_id[i] = (unsigned)e < (unsigned)a.E ? e : INT_MAX;
+  if (at < a.bytes) v = load_raw<false>(a.x + t * a.xs, at, a.bytes);
+  // ids past the last and dropped ones sort behind every expert
+  const int quads = (n + 3) / 4;
+  for (int i = tid; i < quads * 4; i += kRowThreads) {
+    const int e = a.ids[min(i, n - 1)];
+    s_id[i] = i < n && (unsigned)e < (unsigned)a.E ? e : INT_MAX;
   }
   __syncthreads();
-  const int j = tid >> 4;
+  // 16, 32 or 64 lanes a slot
+  const int lanes = a.k <= 4 ? 64 : a.k <= 8 ? 32 : 16, j = tid / lanes;
   if (j < a.k) {
     const int s = t * a.k + j, e = s_id[s];
     int before = 0;
-    for (int i = tid & 15; i < n; i += 16) before += s_id[i] < e || (s_id[i] == e && i < s);
-    before += xlane_i<8>(before);
-    before += xlane_i<4>(before);
-    before += xlane_i<2>(before);
-    before += xlane_i<1>(before);
-    if ((tid & 15) == 0) {
+    for (int i = tid & (lanes - 1); i < quads; i += lanes) {
+      const int4 v = *reinterpret_cast<const int4*>(&s_id[i * 4]);
+      const int o = s - i * 4;  // equal ids of earlier slots come before
+      before += (v.x < e || (v.x == e && 0 < o)) + (v.y < e || (v.y == e && 1 < o)) +
+                (v.z < e || (v.z == e && 2 < o)) + (v.w < e || (v.w == e && 3 < o));
+    }
+    for (int o = lanes / 2; o > 0; o >>= 1) before += __shfl_xor(before, o);
+    if ((tid & (lanes - 1)) == 0) {
       const int r = e != INT_MAX ? before : -1;
       s_row[j] = r;
       if (first) {
@@ -509,7 +536,7 @@ __global__ __launch_bounds__(kRowThreads) void permute_small_kernel(PermuteSmall
   if (at < a.bytes)
     for (int q = 0; q < a.k; ++q) {
       const int r = s_row[q];
-      if (r >= 0) store_raw(a.rows + (long)r * a.rs, at, a.bytes, v);
+      if (r >= 0) store_raw<false>(a.rows + (long)r * a.rs, at, a.bytes, v);
     }
 }
 
@@ -527,7 +554,7 @@ struct CombineArgs {
 // y[t] = sum_j w[t, j] * rows[slot_row[t, j]] in fp32, j ascending, rounded once. A thread
 // owns one 16-byte column of one token; the loads of up to eight rows are issued together
 // before the first is used, which is what keeps enough bytes in flight.
-template <typename T>
+template <typename T, bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(CombineArgs a) {
   constexpr int kBatch = 8;
   const auto [tok, at] = row_place(a.chunks);
@@ -540,7 +567,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(CombineArgs a) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       r[i] = j0 + i < a.k ? a.slot_row[t * a.k + j0 + i] : -1;
-      if ((unsigned)r[i] < (unsigned)a.n) v[i] = load_raw(a.rows + (long)r[i] * a.rs, at, a.bytes);
+      if ((unsigned)r[i] < (unsigned)a.n) v[i] = load_raw<STREAM>(a.rows + (long)r[i] * a.rs, at, a.bytes);
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
@@ -552,7 +579,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(CombineArgs a) {
         for (int q = 0; q < T::kVec; ++q) acc[q] = fmaf(w, f[q], acc[q]);
       }
   }
-  store_raw(a.y + t * a.ys, at, a.bytes, T::pack(acc));
+  store_raw<STREAM>(a.y + t * a.ys, at, a.bytes, T::pack(acc));
 }
 
 struct UnpermuteBwdArgs {
@@ -572,7 +599,7 @@ struct UnpermuteBwdArgs {
 // drows[slot_row[t, j]] = w[t, j] * dy[t] and dw[t, j] = <dy[t], rows[slot_row[t, j]]>: one
 // block a token, so dy is read once and the dot products of all its slots stay in registers
 // until the row's end.
-template <typename T, int KM>
+template <typename T, int KM, bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void unpermute_bwd_kernel(UnpermuteBwdArgs a) {
   __shared__ float s_dot[kRowThreads / kWave][KM];
   const long t = blockIdx.x;
@@ -588,10 +615,10 @@ __global__ __launch_bounds__(kRowThreads) void unpermute_bwd_kernel(UnpermuteBwd
   }
   for (long at = threadIdx.x * 16; at < a.bytes; at += (long)blockDim.x * 16) {
     Raw16 v[KM];
-    const Raw16 dv = load_raw(a.dy + t * a.dys, at, a.bytes);
+    const Raw16 dv = load_raw<STREAM>(a.dy + t * a.dys, at, a.bytes);
 #pragma unroll
     for (int j = 0; j < KM; ++j)
-      if (r[j] >= 0) v[j] = load_raw(a.rows + (long)r[j] * a.rs, at, a.bytes);
+      if (r[j] >= 0) v[j] = load_raw<STREAM>(a.rows + (long)r[j] * a.rs, at, a.bytes);
     float d[T::kVec];
     T::unpack(dv, d);
 #pragma unroll
@@ -604,7 +631,7 @@ __global__ __launch_bounds__(kRowThreads) void unpermute_bwd_kernel(UnpermuteBwd
           dot[j] = fmaf(d[q], f[q], dot[j]);
           g[q] = w[j] * d[q];
         }
-        store_raw(a.drows + (long)r[j] * a.drs, at, a.bytes, T::pack(g));
+        store_raw<STREAM>(a.drows + (long)r[j] * a.drs, at, a.bytes, T::pack(g));
       }
   }
 #pragma unroll
@@ -620,12 +647,14 @@ __global__ __launch_bounds__(kRowThreads) void unpermute_bwd_kernel(UnpermuteBwd
   }
 }
 
+// f(row type, whether the rows are streamed)
 template <typename F>
-static hipError_t by_type(int dtype, F f) {
+static hipError_t by_type(int dtype, long row_bytes, F f) {
+  auto with = [&](auto t) { row_bytes > kStreamBytes ? f(t, std::true_type{}) : f(t, std::false_type{}); };
   switch (dtype) {
-    case HMOE_DTYPE_BF16: f(Bf16{}); break;
-    case HMOE_DTYPE_FP16: f(Fp16{}); break;
-    default: f(Fp32{}); break;
+    case HMOE_DTYPE_BF16: with(Bf16{}); break;
+    case HMOE_DTYPE_FP16: with(Fp16{}); break;
+    default: with(Fp32{}); break;
   }
   return hipGetLastError();
 }
@@ -656,7 +685,8 @@ hipError_t launch_permute(const PermuteRows& p, const int32_t* ids, int E, int32
   g.off = off;
   hipError_t err = launch_sort(g, s);
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL(permute_copy_kernel, dim3(p.M * chunks), dim3(kRowThreads), 0, s,
+  const auto copy = n * bytes > kStreamBytes ? permute_copy_kernel<true> : permute_copy_kernel<false>;
+  hipLaunchKernelGGL(copy, dim3(p.M * chunks), dim3(kRowThreads), 0, s,
                      (const char*)p.src, p.src_stride * p.esize, p.slot_row, p.k, chunks, bytes, (char*)p.dst,
                      p.dst_stride * p.esize);
   return hipGetLastError();
@@ -667,8 +697,8 @@ hipError_t launch_combine(const PermuteRows& p, const float* w, hipStream_t s) {
   const int chunks = row_chunks(bytes);
   CombineArgs a{(const char*)p.src, p.src_stride * p.esize, p.slot_row, w, p.k, p.M * p.k, chunks,
                 bytes, (char*)p.dst, p.dst_stride * p.esize};
-  return by_type(p.dtype, [&](auto t) {
-    hipLaunchKernelGGL(combine_kernel<decltype(t)>, dim3(p.M * chunks), dim3(kRowThreads), 0, s, a);
+  return by_type(p.dtype, (long)p.M * p.k * bytes, [&](auto t, auto stream) {
+    hipLaunchKernelGGL((combine_kernel<decltype(t), stream.value>), dim3(p.M * chunks), dim3(kRowThreads), 0, s, a);
   });
 }
 
@@ -680,12 +710,12 @@ hipError_t launch_unpermute_bwd(const PermuteRows& p, const void* rows, long row
                      p.dst_stride * p.esize, dw};
   // threads: one 16-byte vector each up to 256
   const int threads = bytes > 2048 ? 256 : bytes > 1024 ? 128 : 64;
-  return by_type(p.dtype, [&](auto t) {
+  return by_type(p.dtype, (long)p.M * p.k * bytes, [&](auto t, auto stream) {
     using T = decltype(t);
     if (p.k <= 8)
-      hipLaunchKernelGGL((unpermute_bwd_kernel<T, 8>), dim3(p.M), dim3(threads), 0, s, a);
+      hipLaunchKernelGGL((unpermute_bwd_kernel<T, 8, stream.value>), dim3(p.M), dim3(threads), 0, s, a);
     else
-      hipLaunchKernelGGL((unpermute_bwd_kernel<T, kMaxTopK>), dim3(p.M), dim3(threads), 0, s, a);
+      hipLaunchKernelGGL((unpermute_bwd_kernel<T, kMaxTopK, stream.value>), dim3(p.M), dim3(threads), 0, s, a);
   });
 }
 
