@@ -111,7 +111,7 @@ def test_scratch_planners():
     assert hm.moe_permute_scratch_bytes(0, 1, 1) == 0
     f, b = hm.moe_lora_scratch_bytes(4096, 8, 6144, 4096, 64)
     assert f > 4096 * 4 and b > 8 * 64 * 4096 * 2
-    assert hm.moe_lora_scratch_bytes(1024, 48, 2048, 4096, 64)[0] == 0    # one launch for few rows
+    assert hm.moe_lora_scratch_bytes(256, 48, 2048, 4096, 64)[0] == 0     # one launch for few rows
     assert _lora(nb=hm.moe_lora_scratch_bytes(2000, 3, 64, 32, 8)[0] - 1) == SCRATCH
     assert _lora_bwd(nb=hm.moe_lora_scratch_bytes(4, 3, 64, 32, 8)[1] - 1) == SCRATCH
     for args in ((-1, 1, 8, 8, 8), (1, 1, 8, 8, 0)):

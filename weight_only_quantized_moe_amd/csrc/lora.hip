@@ -115,6 +115,7 @@ __device__ __forceinline__ void turn_8x4(const uint32_t (&v)[8][2], u32x4 (&f)[4
 // entry b % tiles, and of a tile of more than RT rows its part b / tiles. Without a table,
 // block b is the tile that starts at row b if the rows of the same adapter before b fill
 // whole tiles, and has nothing to do otherwise.
+constexpr int kDirectRows = 256;  // up to this many rows a block finds its tile by itself
 struct Tiles {
   const int32_t* ids;
   int M, G, tiles;
@@ -140,16 +141,19 @@ __device__ __forceinline__ bool find_tile(const Tiles& t, int* g, int* n, int* i
     __syncthreads();
     return true;
   }
-  const int lane = threadIdx.x & (kWave - 1);
-  auto key = [&](int m) {
+  // all adapters' numbers into LDS with one wait, then every wave goes through them
+  __shared__ int32_t s_key[kDirectRows];
+  for (int m = threadIdx.x; m < t.M; m += blockDim.x) {
     const int id = t.ids[m];
-    return (unsigned)id < (unsigned)t.G ? id : t.G;
-  };
-  const int mine = key(b);
+    s_key[m] = (unsigned)id < (unsigned)t.G ? id : t.G;
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & (kWave - 1);
+  const int mine = s_key[b];
   int seen = 0, first = -1;  // rows of `mine` so far; their number before b
   for (int m0 = 0; m0 < t.M; m0 += kWave) {
     const int m = m0 + lane;
-    const uint64_t same = __ballot(m < t.M && key(min(m, t.M - 1)) == mine);
+    const uint64_t same = __ballot(m < t.M && s_key[min(m, t.M - 1)] == mine);
     if (first < 0 && b < m0 + kWave) {
       first = seen + __popcll(same & ((1ull << (b - m0)) - 1ull));
       if (first % RT) return false;
@@ -732,35 +736,48 @@ struct FusedArgs {
   float* z;              // may be null
   int col_groups;
   ColumnArgs c;
+  // TR (backward): as in ExpandArgs
+  uint16_t* frag[2];
+  const float* fz;
 };
 
 constexpr int kFusedWaves = 8;
 
 // Both products of a tile of 16 rows in one block, for few rows: the waves split K, z never
-// leaves LDS, then they split the block's columns. Blocks of one tile that take
-// different columns repeat the first product (its matrix comes from L2 again).
-template <int NT, int KS>
+// leaves LDS, then they split the block's columns. Blocks of one tile that take different
+// columns repeat the first product (its matrix comes from L2 again). TR: the backward pass, as
+// in the second product alone.
+template <int NT, int KS, bool TR>
 __global__ __launch_bounds__(kFusedWaves* kWave) void lora_fused_kernel(FusedArgs a) {
   using Z = ZShape<KS>;
+  constexpr int kLd = Z::kSteps * 32 + 4, kThreads = kFusedWaves * kWave;
   __shared__ int32_t s_rows[16];
   __shared__ __align__(16) float s_red[kFusedWaves / 2][NT * 256];
   __shared__ __align__(16) uint16_t s_z[Z::kParts][16 * Z::kRow];
+  __shared__ __align__(16) float s_p[TR ? 16 * kLd : 4];
   int g, n, index;
   if (!find_tile<16>(a.tiles, &g, &n, &index, s_rows)) return;
-  const bool live = g != a.tiles.G;
-  const int r = a.c.r;
+  const bool live = g != a.tiles.G, head = blockIdx.y == 0, tail = blockIdx.y == gridDim.y - 1;
+  const int r = a.c.r, quads = r / 4;
+  const int part = TR ? (int)blockIdx.x / a.tiles.tiles : 0;
+  const long at = TR ? (long)index * 3 * rank_tiles(r) * 512 : 0;
+  if (TR && n == 0) {  // an entry's empty second half: its fragments are zeros
+    if (live && head)
+      for (int i = 0; i < 2; ++i) put_parts<16, kLd>(s_p, part, 0, r, a.frag[i] + at);
+    return;
+  }
   ColumnArgs ca = a.c;
   if (live) ca.w += (long)g * ca.N * r;
-  const Columns<KS, false> cols(ca, n, s_rows);
+  const Columns<KS, TR> cols(ca, n, s_rows);
   const int g0 = blockIdx.y * a.col_groups, g1 = min(g0 + a.col_groups, (ca.N + kCols - 1) / kCols);
   const int cg = g0 + (threadIdx.x >> 6);
-  typename Columns<KS, false>::Load first;  // on the way during the first product
+  typename Columns<KS, TR>::Load first;  // on the way during the first product
   if (cg < g1) cols.load(first, live, cg);
   if (live) {
-    shrink_tile<1, NT, kFusedWaves, (NT == 1 ? 4 : NT == 2 ? 2 : 1)>(a.x, a.xs, a.wa + (long)g * r * a.K, a.K, r, n, s_rows,
-                                               0, (a.K + kKStep - 1) / kKStep, s_red);
+    shrink_tile<1, NT, kFusedWaves, (NT == 1 ? 4 : NT == 2 ? 2 : 1)>(
+        a.x, a.xs, a.wa + (long)g * r * a.K, a.K, r, n, s_rows, 0, (a.K + kKStep - 1) / kKStep, s_red);
     const float sc = a.scale[g];
-    for (int i = threadIdx.x; i < n * NT * 4; i += kFusedWaves * kWave) {
+    for (int i = threadIdx.x; i < n * NT * 4; i += kThreads) {
       const int row = i / (NT * 4), col = i % (NT * 4) * 4;
       if (col >= r) continue;
       float v[4] = {};
@@ -769,16 +786,30 @@ __global__ __launch_bounds__(kFusedWaves* kWave) void lora_fused_kernel(FusedArg
         const float4 f = *reinterpret_cast<const float4*>(&s_red[w][i * 4]);
         v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
       }
-      if (a.z && blockIdx.y == 0)
+      if (!TR && a.z && head)
         *reinterpret_cast<float4*>(a.z + (long)s_rows[row] * r + col) = make_float4(v[0], v[1], v[2], v[3]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] *= sc;
       put_z<KS>(s_z, row, col, r, v);
+      if (TR && head) *reinterpret_cast<float4*>(s_p + row * kLd + col) = make_float4(v[0], v[1], v[2], v[3]);
     }
     pad_z<KS, 16>(s_z, r);
-  } else if (a.z && blockIdx.y == 0) {
-    for (int i = threadIdx.x; i < n * r; i += kFusedWaves * kWave)
-      a.z[(long)s_rows[i / r] * r + i % r] = 0.f;
+    if (TR && head) {
+      __syncthreads();
+      put_parts<16, kLd>(s_p, part, n, r, a.frag[0] + at);
+    }
+    if (TR && tail) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < n * quads; i += kThreads) {
+        const int row = i / quads, col = i % quads * 4;
+        const float4 f = *reinterpret_cast<const float4*>(a.fz + (long)s_rows[row] * r + col);
+        *reinterpret_cast<float4*>(s_p + row * kLd + col) = make_float4(f.x * sc, f.y * sc, f.z * sc, f.w * sc);
+      }
+      __syncthreads();
+      put_parts<16, kLd>(s_p, part, n, r, a.frag[1] + at);
+    }
+  } else if (!TR && a.z && head) {
+    for (int i = threadIdx.x; i < n * r; i += kThreads) a.z[(long)s_rows[i / r] * r + i % r] = 0.f;
   }
   __syncthreads();
   if (!live && a.c.base == a.c.y) return;  // rows without an adapter stay
@@ -807,17 +838,19 @@ constexpr int kWgradRows = 2048;  // row indices kept in LDS at a time
 // row, so both operands are needed transposed: of X a lane reads 8 rows of 4 neighbouring
 // columns (8 bytes each, 128 contiguous bytes a row over 16 lanes) and turns them in registers
 // into the fragments of 4 MFMAs; P lies ready as fragments, in three bf16 parts (24 bits), so
-// the fp32 result carries no bf16 rounding. The block's eight waves take steps of 32 rows (one
-// tile) in turn, the next step's loads in flight, and add up through LDS in wave order. Rows
-// past the group's end are zeros of P. Ranks past NT * 16 go to further blocks
-// (grid z).
-template <int NT>
+// the fp32 result carries no bf16 rounding. A wave has 64 columns and goes through the rows in
+// steps of 32, the next step's loads in flight. SPLIT (many rows a group): the block's eight
+// waves share the columns, take steps in turn and add up through LDS in wave order; else each
+// wave has columns of its own and writes its registers. Rows past the group's end are zeros of
+// P. Ranks past NT * 16 go to further blocks (grid z).
+template <int NT, bool SPLIT>
 __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) {
-  __shared__ float s_red[kWgradWaves][16][68];
+  __shared__ float s_red[SPLIT ? kWgradWaves : 1][16][68];
   __shared__ int32_t s_idx[kWgradRows];
-  const int side = (int)blockIdx.x >= a.blocks[0];
-  const int c0 = ((int)blockIdx.x - (side ? a.blocks[0] : 0)) * 64, g = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid >> 6;
+  const int tile = SPLIT ? (int)blockIdx.x : (int)blockIdx.x * kWgradWaves + wave;
+  const int side = tile >= a.blocks[0], g = blockIdx.y;
+  const int c0 = (tile - (side ? a.blocks[0] : 0)) * 64;
   const int c = lane & 15, q = lane >> 4;
   const int m0 = a.off[g], m1 = a.off[g + 1];
   const int nt = NT * gridDim.z, i0 = blockIdx.z * NT;
@@ -860,10 +893,10 @@ __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) 
 #pragma unroll
           for (int t = 0; t < 4; ++t) acc[i][t] = mfma(v.p[part][i], xf[t], acc[i][t]);
     };
-    // the next step's loads without a condition of their own (see first product)
-    constexpr int kStride = kWgradWaves * 32;
+    // the next step's loads without a condition of their own (see the first product)
+    constexpr int kStride = (SPLIT ? kWgradWaves : 1) * 32;
     Step u, v;
-    int m = wave * 32;
+    int m = SPLIT ? wave * 32 : 0;
     if (m < rows) {
       load(u, m);
       for (; m + 2 * kStride < rows; m += 2 * kStride) {
@@ -881,22 +914,44 @@ __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) 
       }
     }
   }
+  // lane (c, q) holds ranks 4q .. 4q + 3 of columns 4c .. 4c + 3; columns run fastest in dA,
+  // ranks in dB
+  const int waves = SPLIT ? min(kWgradWaves, (m1 - m0 + 31) / 32) : 0;  // those with rows
+  if (waves <= 1) {
+    if (SPLIT && wave) return;
+    const int cl = c0 + c * 4;
+    if (tile >= a.blocks[0] + a.blocks[1] || cl >= C) return;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int rr = (i0 + i) * 16 + q * 4;
+      if (rr >= a.r) continue;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (side)
+          *reinterpret_cast<float4*>(a.out[1] + ((long)g * C + cl + k) * a.r + rr) =
+              make_float4(acc[i][k][0], acc[i][k][1], acc[i][k][2], acc[i][k][3]);
+        else
+          *reinterpret_cast<float4*>(a.out[0] + ((long)g * a.r + rr + k) * C + cl) =
+              make_float4(acc[i][0][k], acc[i][1][k], acc[i][2][k], acc[i][3][k]);
+      }
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
     __syncthreads();
+    if (wave < waves)
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+      for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s_red[wave][q * 4 + e][c * 4 + t] = acc[i][t][e];
+        for (int e = 0; e < 4; ++e) s_red[SPLIT ? wave : 0][q * 4 + e][c * 4 + t] = acc[i][t][e];
     __syncthreads();
     for (int o = tid; o < 16 * 64; o += kWgradThreads) {
-      // columns run fastest in dA, ranks in dB
       const int pr = side ? o & 15 : o >> 6, cc = side ? o >> 4 : o & 63;
       const int rr = (i0 + i) * 16 + pr, cl = c0 + cc;
       if (rr >= a.r || cl >= C) continue;
       float s = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWgradWaves; ++w) s += s_red[w][pr][cc];
+      for (int w = 0; w < waves; ++w) s += s_red[w][pr][cc];
       a.out[side][side ? ((long)g * C + cl) * a.r + rr : ((long)g * a.r + rr) * C + cl] = s;
     }
   }
@@ -908,8 +963,9 @@ __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) 
 
 namespace {
 
-constexpr int kDirectRows = 1024;       // up to this many rows a block finds its tile by itself
-constexpr int kFusedBytes = 512 << 10;  // largest first matrix of the one-launch form
+constexpr int kWgradAlone = 1024;       // waves of the weight gradients from which none shares rows
+constexpr int kFusedRows = 1024;        // most rows of the one-launch form
+constexpr int kFusedBytes = 512 << 10;  // its largest first matrix, half of that for few tiles
 constexpr int kShrinkBlocks = 400;      // about this many blocks of the first product
 constexpr int kFusedRank = 64;          // and its largest rank (registers)
 
@@ -927,14 +983,16 @@ struct Plan {
 // Tile rows from the mean number of rows an adapter has: more rows share one read of the
 // adapter's matrices, fewer waste less where adapters have few rows. The backward pass takes
 // at least 32, the depth of its sums over rows.
+// K: the first product's reduction axis
 Plan plan_tiles(int M, int G, int K, int r, bool backward) {
   Plan p;
   const int mean = M / std::max(1, std::min(G, M));
   p.nt = rank_tiles(r);
   p.table = backward || M > kDirectRows;
-  p.fused = !p.table && r <= kFusedRank && (long)r * K * 2 <= kFusedBytes;
-  p.wide = p.table && mean >= 48;
-  p.rt = p.wide ? 64 : backward ? 32 : !p.table || p.nt == 8 || mean < 24 ? 16 : 32;
+  p.fused = M <= kFusedRows && r <= kFusedRank &&
+            (long)r * K * 2 <= (M / 16 + std::min(G, M) >= 16 ? kFusedBytes : kFusedBytes / 2);
+  p.wide = p.table && !p.fused && mean >= 48;
+  p.rt = p.wide ? 64 : backward ? 32 : !p.table || p.fused || p.nt == 8 || mean < 24 ? 16 : 32;
   p.mt = p.rt == 16 ? 1 : 2;
   const int most = M / p.rt + std::min(G + 1, M);
   p.tiles = p.table ? (most + 7) / 8 * 8 : M;  // the table is dealt out over 8 XCDs
@@ -958,7 +1016,7 @@ struct Space {
 
 Space plan_space(int M, int G, int K, int N, int r, bool backward) {
   Space s{};
-  const Plan p = plan_tiles(M, G, K, r, backward);
+  const Plan p = plan_tiles(M, G, backward ? N : K, r, backward);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -1051,16 +1109,20 @@ hipError_t expand(const Plan& p, ExpandArgs a, hipStream_t s) {
   return p.wide ? expand_by_rank<4, TR>(p, a, grid, s) : expand_by_rank<1, TR>(p, a, grid, s);
 }
 
-template <int NT, int KS>
+template <bool TR>
 hipError_t fused(const Plan& p, FusedArgs a, hipStream_t s) {
-  constexpr int kWaves = kFusedWaves;
   const int groups = (a.c.N + kCols - 1) / kCols;
+  const int blocks = p.tiles * (p.rt / 16), busy = p.busy * (p.rt / 16);
   // columns a block: a multiple of its waves' 128, about 256 blocks in all
-  const int want = std::max(1, 256 / p.busy);
-  const int rounds = std::max(1, (groups + want * kWaves - 1) / (want * kWaves));
-  a.col_groups = rounds * kWaves;
-  const dim3 grid(p.tiles, (groups + a.col_groups - 1) / a.col_groups);
-  hipLaunchKernelGGL((lora_fused_kernel<NT, KS>), grid, dim3(kWaves * kWave), 0, s, a);
+  const int want = std::max(1, 256 / busy);
+  const int rounds = std::max(1, (groups + want * kFusedWaves - 1) / (want * kFusedWaves));
+  a.col_groups = rounds * kFusedWaves;
+  const dim3 grid(blocks, (groups + a.col_groups - 1) / a.col_groups), block(kFusedWaves * kWave);
+  switch (z_steps(a.c.r)) {
+    case 0: hipLaunchKernelGGL((lora_fused_kernel<1, 0, TR>), grid, block, 0, s, a); break;
+    case 1: hipLaunchKernelGGL((lora_fused_kernel<2, 1, TR>), grid, block, 0, s, a); break;
+    default: hipLaunchKernelGGL((lora_fused_kernel<4, 2, TR>), grid, block, 0, s, a); break;
+  }
   return hipGetLastError();
 }
 
@@ -1075,18 +1137,11 @@ hipError_t launch_lora(const Lora& l, void* scratch, hipStream_t s) {
   char* b = static_cast<char*>(scratch);
   const Plan p = plan_tiles(l.M, l.G, l.K, l.r, false);
   const ColumnArgs c{l.r, l.N, l.B, l.base, l.bs, l.y, l.ys};
-  if (p.fused) {
-    const FusedArgs a{Tiles{l.ids, l.M, l.G, p.tiles, nullptr, nullptr}, l.x, l.xs, l.A, l.K, l.scale, l.z, 0, c};
-    switch (z_steps(l.r)) {
-      case 0: return fused<1, 0>(p, a, s);
-      case 1: return fused<2, 1>(p, a, s);
-      default: return fused<4, 2>(p, a, s);
-    }
-  }
   const Space sp = plan_space(l.M, l.G, l.K, l.N, l.r, false);
   Tiles t;
   hipError_t err = make_tiles(l.ids, l.M, l.G, p, sp, b, &t, {}, s);
   if (err != hipSuccess) return err;
+  if (p.fused) return fused<false>(p, FusedArgs{t, l.x, l.xs, l.A, l.K, l.scale, l.z, 0, c, {}, nullptr}, s);
   const int splits = plan_splits(p, l.K);
   float* part = reinterpret_cast<float*>(b + sp.part);
   err = shrink(p, ShrinkArgs{t, l.x, l.xs, l.A, l.K, l.r, splits, part}, s);
@@ -1096,7 +1151,7 @@ hipError_t launch_lora(const Lora& l, void* scratch, hipStream_t s) {
 
 hipError_t launch_lora_backward(const LoraGrad& l, void* scratch, hipStream_t s) {
   char* b = static_cast<char*>(scratch);
-  const Plan p = plan_tiles(l.M, l.G, l.K, l.r, true);
+  const Plan p = plan_tiles(l.M, l.G, l.N, l.r, true);
   const Space sp = plan_space(l.M, l.G, l.K, l.N, l.r, true);
   Tiles t;
   // B^T [G, r, N], which makes dy B the same product as x A^T, is laid out beside the sort
@@ -1105,24 +1160,41 @@ hipError_t launch_lora_backward(const LoraGrad& l, void* scratch, hipStream_t s)
   if (err != hipSuccess) return err;
   uint16_t* frag[2] = {reinterpret_cast<uint16_t*>(b + sp.frag[0]), reinterpret_cast<uint16_t*>(b + sp.frag[1])};
   if (l.M > 0) {
-    const int splits = plan_splits(p, l.N);
-    float* part = reinterpret_cast<float*>(b + sp.part);
-    err = shrink(p, ShrinkArgs{t, l.dy, l.dys, Bt, l.N, l.r, splits, part}, s);
-    if (err != hipSuccess) return err;
     const ColumnArgs c{l.r, l.K, l.A, l.dbase, l.dbs, l.dx, l.dxs};
-    err = expand<true>(p, ExpandArgs{t, part, splits, l.scale, nullptr, 0, c, {frag[0], frag[1]}, l.z, 0}, s);
+    if (p.fused) {
+      err = fused<true>(p, FusedArgs{t, l.dy, l.dys, Bt, l.N, l.scale, nullptr, 0, c, {frag[0], frag[1]}, l.z}, s);
+    } else {
+      const int splits = plan_splits(p, l.N);
+      float* part = reinterpret_cast<float*>(b + sp.part);
+      err = shrink(p, ShrinkArgs{t, l.dy, l.dys, Bt, l.N, l.r, splits, part}, s);
+      if (err == hipSuccess)
+        err = expand<true>(p, ExpandArgs{t, part, splits, l.scale, nullptr, 0, c, {frag[0], frag[1]}, l.z, 0}, s);
+    }
     if (err != hipSuccess) return err;
   }
   const int32_t* off = reinterpret_cast<const int32_t*>(b + sp.off);
   const int32_t* tile_first = reinterpret_cast<const int32_t*>(b + sp.tile_first);
   WgradArgs w{t.sorted, off, tile_first, p.rt / 32, l.r, {frag[0], frag[1]}, {l.x, l.dy}, {l.xs, l.dys}, {l.K, l.N},
               {(l.K + 63) / 64, (l.N + 63) / 64}, {l.dA, l.dB}};
-  const dim3 grid(w.blocks[0] + w.blocks[1], l.G, p.nt == 8 ? 2 : 1), block(kWgradThreads);
-  switch (p.nt) {
-    case 1: hipLaunchKernelGGL(lora_wgrad_kernel<1>, grid, block, 0, s, w); break;
-    case 2: hipLaunchKernelGGL(lora_wgrad_kernel<2>, grid, block, 0, s, w); break;
-    default: hipLaunchKernelGGL(lora_wgrad_kernel<4>, grid, block, 0, s, w); break;
-  }
+  // a wave to each 64 columns of an adapter where that fills the chip's 1024 SIMDs, else eight
+  const int tiles = w.blocks[0] + w.blocks[1], halves = p.nt == 8 ? 2 : 1;
+  const bool split = (long)tiles * l.G * halves < kWgradAlone;
+  const dim3 grid(split ? tiles : (tiles + kWgradWaves - 1) / kWgradWaves, l.G, halves);
+  const dim3 block(kWgradThreads);
+#define HMOE_WGRAD(NT, SPLIT) hipLaunchKernelGGL((lora_wgrad_kernel<NT, SPLIT>), grid, block, 0, s, w)
+  if (split)
+    switch (p.nt) {
+      case 1: HMOE_WGRAD(1, true); break;
+      case 2: HMOE_WGRAD(2, true); break;
+      default: HMOE_WGRAD(4, true); break;
+    }
+  else
+    switch (p.nt) {
+      case 1: HMOE_WGRAD(1, false); break;
+      case 2: HMOE_WGRAD(2, false); break;
+      default: HMOE_WGRAD(4, false); break;
+    }
+#undef HMOE_WGRAD
   return hipGetLastError();
 }
 
