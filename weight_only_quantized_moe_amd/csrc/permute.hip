@@ -115,13 +115,15 @@ struct __attribute__((packed, aligned(2))) Raw16 {
   uint32_t w[4];
 };
 
-// eight columns of eight ranks a thread, turned in registers: 16-byte reads and writes
+// Eight columns of eight ranks a thread, turned in registers: 16-byte reads and writes. Threads
+// run over the ranks first, so that eight of them share a row's 128 bytes (rank 64) on the way
+// in and eight on the way out.
 __device__ __forceinline__ void transpose_block(const SortTranspose& t, long i) {
   const int nb = t.N / 8, rb = t.r / 8;
   if (i >= (long)t.G * rb * nb) return;
-  const int b = (int)(i % nb);
-  const long gr = i / nb, g = gr / rb;
-  const int k = (int)(gr % rb);
+  const int k = (int)(i % rb);
+  const long gb = i / rb, g = gb / nb;
+  const int b = (int)(gb % nb);
   Raw16 v[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j)
