@@ -306,15 +306,22 @@ class LoraCase:
 
 
 # ranks on both sides of 16, 32, 64 (packed parts, MFMA depths); rows on both sides of 16, 32,
-# 64 (tile rows), of 24 and 48 rows an adapter (tile heights) and of 1024 (tile table); K and N
-# below, at and past 64 (steps, column groups)
+# 64 (tile rows), of 24 and 48 rows an adapter (tile heights), of 128 and 2048 (how blocks find
+# their tiles) and of 1024 (one launch); adapters on both sides of 255 (counts a block holds);
+# K and N below, at and past 64 (steps, column groups); weight gradients with and without waves
+# that share rows
 LORA = [(1, 1, 8, 8, 8, "one"), (1, 16, 2048, 1536, 16, "any"), (2, 3, 72, 40, 24, "mixed"), (15, 1, 64, 64, 16, "one"),
         (16, 2, 128, 72, 32, "any"), (17, 1, 200, 136, 40, "one"), (33, 4, 264, 520, 64, "mixed"),
         (64, 48, 6144, 4096, 16, "mixed"), (65, 1, 320, 192, 8, "one"), (100, 4, 136, 64, 72, "runs"),
         (130, 2, 256, 264, 96, "mixed"), (200, 3, 512, 328, 128, "runs"), (150, 2048, 64, 64, 8, "any"),
         (1024, 5, 96, 88, 16, "mixed"), (1025, 5, 96, 88, 16, "mixed"), (1100, 2048, 24, 16, 8, "mixed"),
         (1500, 1, 200, 72, 64, "one"), (3000, 7, 72, 200, 48, "runs"), (2500, 40, 136, 24, 104, "mixed"),
-        (5000, 3, 64, 64, 24, "any"), (70, 2, 8, 16, 120, "none"), (1200, 2, 16, 8, 8, "none")]
+        (5000, 3, 64, 64, 24, "any"), (70, 2, 8, 16, 120, "none"), (1200, 2, 16, 8, 8, "none"),
+        (128, 5, 72, 64, 16, "mixed"), (129, 5, 72, 64, 16, "mixed"), (500, 255, 40, 88, 16, "mixed"),
+        (500, 256, 40, 88, 16, "mixed"), (900, 254, 2056, 72, 128, "any"), (2048, 9, 96, 88, 64, "mixed"),
+        (2049, 9, 96, 88, 64, "mixed"), (2048, 255, 24, 40, 40, "any"), (700, 1, 4104, 264, 64, "one"),
+        (1024, 60, 2048, 1536, 32, "mixed"), (90, 20, 4096, 4104, 64, "any"), (300, 70, 520, 2056, 128, "mixed"),
+        (120, 2, 8200, 136, 32, "mixed"), (2000, 1, 4096, 64, 24, "one")]
 
 
 @pytest.mark.parametrize("M,G,K,N,r,kind", LORA)

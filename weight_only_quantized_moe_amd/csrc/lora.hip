@@ -16,6 +16,7 @@
 #include <type_traits>
 
 #include "device_common.h"
+#include "group_count.h"
 #include "hmoe_internal.h"
 
 namespace hmoe {
@@ -111,62 +112,157 @@ __device__ __forceinline__ void turn_8x4(const uint32_t (&v)[8][2], u32x4 (&f)[4
                                       (t & 1) ? 0x07060302u : 0x05040100u);
 }
 
-// Which rows a block works on. With a tile table (many rows) it is looked up: block b takes
-// entry b % tiles, and of a tile of more than RT rows its part b / tiles. Without a table,
-// block b is the tile that starts at row b if the rows of the same adapter before b fill
-// whole tiles, and has nothing to do otherwise.
-constexpr int kDirectRows = 256;  // up to this many rows a block finds its tile by itself
+// Which rows a block works on: entry b % tiles of the tile table, and of a tile of more than RT
+// rows its part b / tiles. The table comes from a sort before the launch (kTable), or the first
+// launch does without one and leaves its tiles as the table for the second:
+// kRow   entry b is the tile that starts at row b, if the rows of the same adapter before b fill
+//        whole tiles; the entries of all other rows are idle.
+// kCount every block counts all ids by adapter and so finds tile b and its rows.
+// Rank 16, us a call, kRow and kCount: 6.9 and 8.6 (1 row, 2048 -> 1536 columns), 7.4 and 9.1
+// (64), 8.4 and 9.0 (200), 13.7 and 10.8 (200 rows, 4096 -> 4096), and kCount would take 16 more
+// to look through the counts of 2000 adapters. kCount and kTable: 8.7 and 12.2 (257 rows of 4
+// adapters, 2048 -> 1536), 10.2 and 13.7 (1000 of 30), 18.2 and 19.9 (2000 of 100), 26.0 and
+// 25.6 (4000 of 64).
+enum TileFind { kTable, kRow, kCount };
+constexpr int kRowRows = 128;                         // most rows of kRow
+constexpr int kCountRows = 2048, kCountGroups = 256;  // of kCount, with the group of no adapter
 struct Tiles {
   const int32_t* ids;
   int M, G, tiles;
-  const int32_t* sorted;      // null: no table
-  const SortTile* table;
+  int entry;           // rows of a tile
+  TileFind find;
+  int32_t* sorted;     // rows by adapter (null: no table is kept)
+  SortTile* table;
 };
 
-// false: no tile. Else *g (G: rows without an adapter), s_rows[0 .. *n); with a table *index,
-// the tile's number, and *n may be 0 for a tile's second part.
-template <int RT>
+// false: no tile. Else *g (G: rows without an adapter), s_rows[0 .. *n), *index: the tile's
+// number; *n may be 0 for a tile's second part. s_rows past *n names row 0, so that whatever
+// reads it stays inside the matrices.
+// ROWS: most rows of kCount, whose ids the block's THREADS hold in registers (0: only kTable).
+template <int RT, int ROWS, int THREADS>
 __device__ __forceinline__ bool find_tile(const Tiles& t, int* g, int* n, int* index, int32_t* s_rows) {
-  const int b = blockIdx.x;
-  if (t.sorted) {
-    const int part = b / t.tiles;
-    const SortTile d = t.table[b - part * t.tiles];
+  const int part = (int)blockIdx.x / t.tiles, e = (int)blockIdx.x - part * t.tiles;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid >> 6;
+  if (ROWS == 0 || t.find == kTable) {
+    const SortTile d = t.table[e];
     if (d.group < 0) return false;
     *g = d.group;
     *index = d.index;
     *n = max(0, min(RT, d.rows - part * RT));
-    // places past *n name row 0, so that whatever reads them stays inside the matrices
-    if (threadIdx.x < RT)
-      s_rows[threadIdx.x] = (int)threadIdx.x < *n ? t.sorted[d.start + part * RT + threadIdx.x] : 0;
+    if (tid < RT) s_rows[tid] = tid < *n ? t.sorted[d.start + part * RT + tid] : 0;
     __syncthreads();
     return true;
   }
-  // all adapters' numbers into LDS with one wait, then every wave goes through them
-  __shared__ int32_t s_key[kDirectRows];
-  for (int m = threadIdx.x; m < t.M; m += blockDim.x) {
-    const int id = t.ids[m];
-    s_key[m] = (unsigned)id < (unsigned)t.G ? id : t.G;
-  }
-  __syncthreads();
-  const int lane = threadIdx.x & (kWave - 1);
-  const int mine = s_key[b];
-  int seen = 0, first = -1;  // rows of `mine` so far; their number before b
-  for (int m0 = 0; m0 < t.M; m0 += kWave) {
-    const int m = m0 + lane;
-    const uint64_t same = __ballot(m < t.M && s_key[min(m, t.M - 1)] == mine);
-    if (first < 0 && b < m0 + kWave) {
-      first = seen + __popcll(same & ((1ull << (b - m0)) - 1ull));
-      if (first % RT) return false;
+  if constexpr (ROWS > 0) {
+    const bool put = t.sorted && blockIdx.y == 0;  // this block writes its entry
+    SortTile d{-1, 0, 0, 0};
+    if (tid < RT) s_rows[tid] = 0;
+    if (t.find == kRow) {
+      // all adapters' numbers into LDS with one wait, then every wave goes through them
+      __shared__ int32_t s_key[kRowRows];
+      for (int m = tid; m < t.M; m += THREADS) s_key[m] = sort_key(t.ids[m], t.G, t.G + 1);
+      __syncthreads();
+      const int mine = s_key[e];
+      int seen = 0, first = -1;  // rows of `mine` so far; their number before e
+      for (int m0 = 0; m0 < t.M; m0 += kWave) {
+        const int m = m0 + lane;
+        const uint64_t same = __ballot(m < t.M && s_key[min(m, t.M - 1)] == mine);
+        if (first < 0 && e < m0 + kWave) {
+          first = seen + __popcll(same & ((1ull << (e - m0)) - 1ull));
+          if (first % RT) {
+            if (put && tid == 0) t.table[e] = d;
+            return false;
+          }
+        }
+        const int rank = seen + __popcll(same & ((1ull << lane) - 1ull)) - first;
+        if (first >= 0 && (same >> lane & 1) && rank >= 0 && rank < RT) s_rows[rank] = m;
+        seen += __popcll(same);
+        if (first >= 0 && seen - first >= RT) break;
+      }
+      d = SortTile{mine, e * RT, min(RT, seen - first), e};
+    } else {
+      constexpr int kIds = ROWS / THREADS, kWaves = THREADS / kWave, kRuns = kCountGroups / kWave;
+      __shared__ int32_t s_cnt[kCountGroups];
+      __shared__ int32_t s_wave[kWaves];
+      const int groups = t.G + 1, run = (t.M + THREADS - 1) / THREADS;  // ids of a lane
+      const int w0 = wave * run * kWave;
+      int id[kIds];
+#pragma unroll
+      for (int i = 0; i < kIds; ++i)
+        if (i < run) id[i] = t.ids[min(w0 + i * kWave + lane, t.M - 1)];
+      for (int k = tid; k < groups; k += THREADS) s_cnt[k] = 0;
+      __syncthreads();
+      const int bits = group_bits(groups);
+#pragma unroll
+      for (int i = 0; i < kIds; ++i)
+        if (i < run) {
+          id[i] = w0 + i * kWave + lane < t.M ? sort_key(id[i], t.G, groups) : -1;
+          count_groups(id[i], bits, s_cnt);
+        }
+      __syncthreads();
+      // every wave for itself: tiles and rows up to each group (both below 2^16), in registers
+      const int h = t.entry;
+      int upto[kRuns], all = 0;
+#pragma unroll
+      for (int k = 0; k < kRuns; ++k)
+        if (k * kWave < groups) {
+          const int c = k * kWave + lane < groups ? s_cnt[k * kWave + lane] : 0;
+          int sum = (c + h - 1) / h << 16 | c;
+#pragma unroll
+          for (int o = 1; o < kWave; o <<= 1) {
+            const int u = __shfl_up(sum, o);
+            if (lane >= o) sum += u;
+          }
+          upto[k] = all + sum;
+          all += __shfl(sum, kWave - 1);
+        }
+      // Blocks go to the 8 XCDs in turn; a run of tiles (of one adapter mostly) goes to one.
+      const int total = all >> 16, per = (total + 7) / 8;
+      const int tile = e / 8 < per ? (e & 7) * per + e / 8 : total;
+      if (tile >= total) {
+        if (put && part == 0 && tid == 0) t.table[e] = d;
+        return false;
+      }
+      int first = 0;  // the tile's first row in its group
+#pragma unroll
+      for (int k = 0; k < kRuns; ++k)
+        if (k * kWave < groups && d.group < 0) {
+          const uint64_t past = __ballot((upto[k] >> 16) > tile);
+          if (past) {
+            const int l = __ffsll((unsigned long long)past) - 1, end = __shfl(upto[k], l);
+            const int rows = s_cnt[k * kWave + l];
+            first = (tile - (end >> 16) + (rows + h - 1) / h) * h;
+            d = SortTile{k * kWave + l, (end & 0xffff) - rows + first, min(h, rows - first), tile};
+          }
+        }
+      int seen = 0;
+#pragma unroll
+      for (int i = 0; i < kIds; ++i)
+        if (i < run) seen += __popcll(__ballot(id[i] == d.group));
+      if (lane == 0) s_wave[wave] = seen;
+      __syncthreads();
+      int rank = -(first + part * RT);  // of the group's next row, from this part's first
+      for (int w = 0; w < wave; ++w) rank += s_wave[w];
+#pragma unroll
+      for (int i = 0; i < kIds; ++i)
+        if (i < run) {
+          const uint64_t same = __ballot(id[i] == d.group);
+          const int at = rank + __popcll(same & ((1ull << lane) - 1ull));
+          if (id[i] == d.group && at >= 0 && at < min(RT, d.rows - part * RT)) s_rows[at] = w0 + i * kWave + lane;
+          rank += __popcll(same);
+        }
     }
-    const int rank = seen + __popcll(same & ((1ull << lane) - 1ull)) - first;
-    if (first >= 0 && (same >> lane & 1) && rank >= 0 && rank < RT) s_rows[rank] = m;
-    seen += __popcll(same);
-    if (first >= 0 && seen - first >= RT) break;
+    *g = d.group;
+    *index = d.index;
+    *n = max(0, min(RT, d.rows - part * RT));
+    __syncthreads();
+    if (put) {
+      if (part == 0 && tid == 0) t.table[e] = d;
+      if (tid < *n) t.sorted[d.start + part * RT + tid] = s_rows[tid];
+    }
+    return true;
   }
-  *g = mine;
-  *n = min(RT, seen - first);
-  __syncthreads();
-  return true;
+  return false;
 }
 
 // s_red = X_rows W_g^T over the steps [s0, s1) of the reduction axis K, rows x ranks. The W
@@ -511,7 +607,7 @@ __global__ __launch_bounds__(kShrinkWaves* kWave) void lora_shrink_kernel(Shrink
   __shared__ int32_t s_rows[MT * 16];
   __shared__ __align__(16) float s_red[kShrinkWaves / 2][MT * NT * 256];
   int g, n, index;
-  if (!find_tile<MT * 16>(a.tiles, &g, &n, &index, s_rows)) return;
+  if (!find_tile<MT * 16, kCountRows, kShrinkWaves * kWave>(a.tiles, &g, &n, &index, s_rows)) return;
   if (g == a.tiles.G) return;
   const int steps = (a.K + kKStep - 1) / kKStep;
   shrink_tile<MT, NT, kShrinkWaves, (MT + NT <= 3 ? 2 : 1)>(a.x, a.xs, a.w + (long)g * a.r * a.K, a.K, a.r, n, s_rows,
@@ -606,7 +702,7 @@ void lora_expand_kernel(ExpandArgs a) {
   float* s_p = reinterpret_cast<float*>(s_shared);
   u32x4* s_w = reinterpret_cast<u32x4*>(s_shared);
   int g, n, index;
-  if (!find_tile<RT>(a.tiles, &g, &n, &index, s_rows)) return;
+  if (!find_tile<RT, 0, kThreads>(a.tiles, &g, &n, &index, s_rows)) return;
   const bool live = g != a.tiles.G, head = blockIdx.y == 0;
   const int r = a.c.r, quads = r / 4, lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
   const int mine = RW == 1 ? 0 : wave * 16;  // first of this wave's rows
@@ -742,6 +838,7 @@ struct FusedArgs {
 };
 
 constexpr int kFusedWaves = 8;
+constexpr int kFusedRows = 1024;  // most rows of the one-launch form
 
 // Both products of a tile of 16 rows in one block, for few rows: the waves split K, z never
 // leaves LDS, then they split the block's columns. Blocks of one tile that take different
@@ -756,7 +853,7 @@ __global__ __launch_bounds__(kFusedWaves* kWave) void lora_fused_kernel(FusedArg
   __shared__ __align__(16) uint16_t s_z[Z::kParts][16 * Z::kRow];
   __shared__ __align__(16) float s_p[TR ? 16 * kLd : 4];
   int g, n, index;
-  if (!find_tile<16>(a.tiles, &g, &n, &index, s_rows)) return;
+  if (!find_tile<16, TR ? 0 : kFusedRows, kThreads>(a.tiles, &g, &n, &index, s_rows)) return;
   const bool live = g != a.tiles.G, head = blockIdx.y == 0, tail = blockIdx.y == gridDim.y - 1;
   const int r = a.c.r, quads = r / 4;
   const int part = TR ? (int)blockIdx.x / a.tiles.tiles : 0;
@@ -964,13 +1061,12 @@ __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) 
 namespace {
 
 constexpr int kWgradAlone = 1024;       // waves of the weight gradients from which none shares rows
-constexpr int kFusedRows = 1024;        // most rows of the one-launch form
 constexpr int kFusedBytes = 512 << 10;  // its largest first matrix, half of that for few tiles
 constexpr int kShrinkBlocks = 400;      // about this many blocks of the first product
 constexpr int kFusedRank = 64;          // and its largest rank (registers)
 
 struct Plan {
-  bool table;      // a sort and a tile table come first
+  TileFind find;
   bool fused;      // both products in one launch
   bool wide;       // the second product's waves share its matrix
   int nt;          // rank / 16, rounded up to a power of two
@@ -988,14 +1084,14 @@ Plan plan_tiles(int M, int G, int K, int r, bool backward) {
   Plan p;
   const int mean = M / std::max(1, std::min(G, M));
   p.nt = rank_tiles(r);
-  p.table = backward || M > kDirectRows;
   p.fused = M <= kFusedRows && r <= kFusedRank &&
             (long)r * K * 2 <= (M / 16 + std::min(G, M) >= 16 ? kFusedBytes : kFusedBytes / 2);
-  p.wide = p.table && !p.fused && mean >= 48;
-  p.rt = p.wide ? 64 : backward ? 32 : !p.table || p.fused || p.nt == 8 || mean < 24 ? 16 : 32;
+  p.find = backward || M > kCountRows || (M > kRowRows && G >= kCountGroups) ? kTable : M > kRowRows ? kCount : kRow;
+  p.wide = p.find != kRow && !p.fused && mean >= 48;
+  p.rt = p.wide ? 64 : backward ? 32 : p.find == kRow || p.fused || p.nt == 8 || mean < 24 ? 16 : 32;
   p.mt = p.rt == 16 ? 1 : 2;
   const int most = M / p.rt + std::min(G + 1, M);
-  p.tiles = p.table ? (most + 7) / 8 * 8 : M;  // the table is dealt out over 8 XCDs
+  p.tiles = p.find == kRow ? M : (most + 7) / 8 * 8;  // entries are dealt out over 8 XCDs
   p.busy = std::max(1, std::min(most, M));
   return p;
 }
@@ -1023,11 +1119,13 @@ Space plan_space(int M, int G, int K, int N, int r, bool backward) {
     at = align256(at + bytes);
     return o;
   };
-  if (p.table) {
-    s.sorted = take((size_t)M * 4);
+  if (p.find == kTable || !p.fused) {
+    s.sorted = take((size_t)M * (p.find == kRow ? p.rt : 1) * 4);
+    s.tile = take((size_t)p.tiles * sizeof(SortTile));
+  }
+  if (p.find == kTable) {
     s.off = take((size_t)(G + 2) * 4);
     s.counts = take(sort_count_words(M, G + 1) * 4);
-    s.tile = take((size_t)p.tiles * sizeof(SortTile));
     s.tile_first = take((size_t)(G + 2) * 4);
   }
   if (!p.fused) s.part = take((size_t)plan_splits(p, backward ? N : K) * M * r * 4);
@@ -1041,23 +1139,25 @@ Space plan_space(int M, int G, int K, int N, int r, bool backward) {
 
 hipError_t make_tiles(const int32_t* ids, int M, int G, const Plan& p, const Space& sp, char* scratch,
                       Tiles* t, const SortTranspose& turn, hipStream_t s) {
-  *t = Tiles{ids, M, G, p.tiles, nullptr, nullptr};
-  if (!p.table) return hipSuccess;
+  *t = Tiles{ids, M, G, p.tiles, p.rt, p.find, nullptr, nullptr};
+  if (p.find == kTable || !p.fused) {
+    t->sorted = reinterpret_cast<int32_t*>(scratch + sp.sorted);
+    t->table = reinterpret_cast<SortTile*>(scratch + sp.tile);
+  }
+  if (p.find != kTable) return hipSuccess;
   GroupSort g{};
   g.ids = ids;
   g.n = M;
   g.G = G;
   g.groups = G + 1;
   g.counts = reinterpret_cast<int32_t*>(scratch + sp.counts);
-  g.sorted = reinterpret_cast<int32_t*>(scratch + sp.sorted);
+  g.sorted = t->sorted;
   g.off = reinterpret_cast<int32_t*>(scratch + sp.off);
   g.tile_rows = p.rt;
   g.max_tiles = p.tiles;
-  g.tile = reinterpret_cast<SortTile*>(scratch + sp.tile);
+  g.tile = t->table;
   g.tile_first = reinterpret_cast<int32_t*>(scratch + sp.tile_first);
   g.turn = turn;
-  t->sorted = g.sorted;
-  t->table = g.tile;
   return launch_sort(g, s);
 }
 
@@ -1146,6 +1246,7 @@ hipError_t launch_lora(const Lora& l, void* scratch, hipStream_t s) {
   float* part = reinterpret_cast<float*>(b + sp.part);
   err = shrink(p, ShrinkArgs{t, l.x, l.xs, l.A, l.K, l.r, splits, part}, s);
   if (err != hipSuccess) return err;
+  t.find = kTable;
   return expand<false>(p, ExpandArgs{t, part, splits, l.scale, l.z, 0, c, {}, nullptr, 0}, s);
 }
 

@@ -13,6 +13,7 @@
 #include <type_traits>
 
 #include "device_common.h"
+#include "group_count.h"
 #include "hmoe_internal.h"
 
 namespace hmoe {
@@ -45,11 +46,6 @@ struct SortArgs {
   SortTranspose turn;
 };
 
-// group of an id: ids outside [0, G) are dropped (-1) or the group behind the last
-__device__ __forceinline__ int sort_key(int id, int G, int groups) {
-  return (unsigned)id < (unsigned)G ? id : (groups > G ? G : -1);
-}
-
 // inclusive sum over the block of one value per thread; *total: the block's sum
 template <int THREADS>
 __device__ __forceinline__ int block_scan(int v, int* s_part, int* total) {
@@ -71,27 +67,6 @@ __device__ __forceinline__ int block_scan(int v, int* s_part, int* total) {
   *total = __shfl(p, THREADS / kWave - 1);
   const int add = wave ? __shfl(p, wave - 1) : 0;
   return v + add;
-}
-
-// lanes of the wave with the same group as this one (0: none), from ballots over the bits
-__device__ __forceinline__ uint64_t same_group(int e, int bits) {
-  uint64_t m = __ballot(e >= 0);
-  for (int b = 0; b < bits; ++b) {
-    const bool bit = (e >> b) & 1;
-    const uint64_t bb = __ballot(bit);
-    m &= bit ? bb : ~bb;
-  }
-  return e >= 0 ? m : 0;
-}
-
-__device__ __forceinline__ int group_bits(int groups) { return groups > 1 ? 32 - __clz(groups - 1) : 0; }
-
-// adds the wave's ids to a counter per group: one LDS operation a group, not one a lane
-// (few groups would make 64 lanes wait for one address)
-__device__ __forceinline__ void count_groups(int e, int bits, int32_t* s_cnt) {
-  const uint64_t m = same_group(e, bits);
-  if (m && __ffsll((unsigned long long)m) - 1 == (int)(threadIdx.x & (kWave - 1)))
-    atomicAdd(&s_cnt[e], __popcll(m));
 }
 
 // per-block group counts of a sort over several blocks
