@@ -392,7 +392,8 @@ hmoe_status moe_quantize_mxfp4(const float* in, int32_t rows, int32_t K, uint8_t
  *   - Matrices of rows have a row stride in elements (>= the row's length; the last axis is
  *     contiguous) and need only element alignment; every other pointer 16 bytes.
  *   - Index and weight arrays (topk_ids, topk_w, slot_row, ...) are contiguous.
- *   - Outputs must not overlap inputs or each other, except where said.
+ *   - Outputs must not overlap inputs or each other, except where said (an output matrix that
+ *     starts where an input matrix does is refused: HMOE_ERR_INVALID_ARG).
  *   - No call keeps anything between calls: scratch contents matter only while the call's
  *     kernels run, so calls that may overlap in time need scratch buffers of their own.
  *   - Results do not depend on timing: fixed-order sums, no floating-point atomics. */
@@ -468,7 +469,8 @@ hmoe_status moe_lora_scratch_bytes(int32_t M, int32_t G, int32_t K, int32_t N, i
  * base and y [M, N], A [G, rank, K], B [G, N, rank] (an adapter of lower rank is padded with
  * zeros), scale fp32 [G]. z fp32 [M, rank] is what moe_lora_backward needs and may be NULL.
  * A and B must be finite (an infinite entry gives infinities or NaN in the rows that use it).
- * M = 0 is a no-op. Up to 1024 rows it is one or two launches.
+ * M = 0 is a no-op. It takes one to three launches, at most two for up to 128 rows and for up
+ * to 2048 rows of at most 255 adapters.
  * Errors: HMOE_ERR_INVALID_ARG (M < 0; G, K, N or rank < 1; a stride below the row's length;
  * base == y with another stride); HMOE_ERR_UNSUPPORTED (K, N or rank not a multiple of 8,
  * rank > 128, G > HMOE_MAX_GROUPS, M > 2^22, K or N > 2^20); HMOE_ERR_SCRATCH; HMOE_ERR_ALIGN;

@@ -14,7 +14,7 @@ OK, INVALID, UNSUPPORTED, ALIGN, CAPACITY, SCRATCH, HIP = range(7)
 A = 1 << 40          # never dereferenced: every call below fails before any launch
 
 
-def _permute(M=4, k=2, E=8, H=16, dtype=0, x=A, xs=16, ids=A, rows=A, rs=16, srt=A, sr=A, off=A,
+def _permute(M=4, k=2, E=8, H=16, dtype=0, x=A, xs=16, ids=A, rows=2 * A, rs=16, srt=A, sr=A, off=A,
              ws=None, nb=0):
     return hm.load_library().moe_permute(x, xs, ids, M, k, E, H, dtype, rows, rs, srt, sr, off, ws, nb,
                                          None)
@@ -40,13 +40,13 @@ def test_permute_refusals(kw, status):
 def test_row_gradients_refusals():
     lib = hm.load_library()
 
-    def back(M=4, k=2, H=16, dt=0, d=A, ds=16, sr=A, dx=A, xs=16):
+    def back(M=4, k=2, H=16, dt=0, d=A, ds=16, sr=A, dx=2 * A, xs=16):
         return lib.moe_permute_backward(d, ds, sr, M, k, H, dt, dx, xs, None)
 
-    def un(M=4, k=2, H=16, dt=0, r=A, rs=16, sr=A, w=A, y=A, ys=16):
+    def un(M=4, k=2, H=16, dt=0, r=A, rs=16, sr=A, w=A, y=2 * A, ys=16):
         return lib.moe_unpermute(r, rs, sr, w, M, k, H, dt, y, ys, None)
 
-    def unb(M=4, k=2, H=16, dt=0, dy=A, r=A, sr=A, w=A, dr=A, dw=A, s=16):
+    def unb(M=4, k=2, H=16, dt=0, dy=A, r=A, sr=A, w=A, dr=2 * A, dw=A, s=16):
         return lib.moe_unpermute_backward(dy, s, r, s, sr, w, M, k, H, dt, dr, s, dw, None)
 
     for f in (back, un, unb):
@@ -103,6 +103,31 @@ def test_lora_own_refusals():
     assert _lora_bwd(base=2 * A, bs=128) == INVALID
     assert _lora_bwd(z=None) == ALIGN and _lora_bwd(dA=None) == ALIGN and _lora_bwd(dB=A + 4) == ALIGN
     assert _lora_bwd(dx=None) == ALIGN and _lora_bwd(dxs=8) == INVALID and _lora_bwd(dy=None) == ALIGN
+
+
+def test_outputs_over_inputs_are_refused():
+    lib = hm.load_library()
+    assert _permute(rows=A) == INVALID
+    assert lib.moe_permute_backward(A, 16, A, 4, 2, 16, 0, A, 16, None) == INVALID
+    assert lib.moe_unpermute(A, 16, A, A, 4, 2, 16, 0, A, 16, None) == INVALID
+    for dy, r in ((2 * A, A), (A, 2 * A)):
+        assert lib.moe_unpermute_backward(dy, 16, r, 16, A, A, 4, 2, 16, 0, 2 * A, 16, A, None) == INVALID
+    assert _lora(y=A, base=None) == INVALID
+    assert _lora_bwd(dx=A, dy=3 * A, base=None) == INVALID and _lora_bwd(dx=A, x=3 * A, base=None) == INVALID
+    assert "input" in lib.moe_last_error().decode()
+
+
+def test_lora_scratch_over_all_sizes():
+    """Every accepted size has a finite plan, whose bytes hold what the two launches exchange."""
+    r = np.random.default_rng(3)
+    for _ in range(4000):
+        M, K, N = (int(2 ** r.uniform(0, e)) for e in (22, 17, 17))
+        G, rank = int(2 ** r.uniform(0, 11)), 8 * int(r.integers(1, 17))
+        f, b = hm.moe_lora_scratch_bytes(M, G, 8 * K, 8 * N, rank)
+        assert f % 256 == 0 and f < 1 << 42 and b < 1 << 45
+        assert b >= 2 * M * rank * 6 + G * rank * 8 * N * 2   # gradients' fragments, B turned
+        if M > 1024:
+            assert f >= M * rank * 4 + M * 4                  # z's parts, the sorted rows
 
 
 def test_scratch_planners():

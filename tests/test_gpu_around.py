@@ -321,7 +321,8 @@ LORA = [(1, 1, 8, 8, 8, "one"), (1, 16, 2048, 1536, 16, "any"), (2, 3, 72, 40, 2
         (500, 256, 40, 88, 16, "mixed"), (900, 254, 2056, 72, 128, "any"), (2048, 9, 96, 88, 64, "mixed"),
         (2049, 9, 96, 88, 64, "mixed"), (2048, 255, 24, 40, 40, "any"), (700, 1, 4104, 264, 64, "one"),
         (1024, 60, 2048, 1536, 32, "mixed"), (90, 20, 4096, 4104, 64, "any"), (300, 70, 520, 2056, 128, "mixed"),
-        (120, 2, 8200, 136, 32, "mixed"), (2000, 1, 4096, 64, 24, "one")]
+        (120, 2, 8200, 136, 32, "mixed"), (2000, 1, 4096, 64, 24, "one"),
+        (9000, 300, 24, 16, 8, "mixed"), (20000, 1500, 16, 8, 16, "any")]
 
 
 @pytest.mark.parametrize("M,G,K,N,r,kind", LORA)
@@ -515,7 +516,7 @@ def _sequence(hm, torch, M, seed):
     k, E, H = 4, 16, 136
     c = LoraCase(torch, M, 3, H, 72, 16, "mixed", seed)
     i32 = dict(dtype=torch.int32, device="cuda")
-    t = {"lg": rand(torch, seed, M, E), "x": c.x, "dyr": rand(torch, seed + 1, M, H, dtype="bfloat16"),
+    t = {"lg": rand(torch, seed, M, E), "aid": c.ids, "x": c.x, "dyr": rand(torch, seed + 1, M, H, dtype="bfloat16"),
          "ids": torch.zeros(M, k, **i32), "w": torch.zeros(M, k, device="cuda"),
          "rows": torch.zeros(M * k, H, dtype=torch.bfloat16, device="cuda"), "srt": torch.zeros(M * k, **i32),
          "sr": torch.zeros(M, k, **i32), "off": torch.zeros(E + 1, **i32), "u": torch.zeros_like(c.x),
@@ -538,11 +539,11 @@ def _sequence(hm, torch, M, seed):
         hm.moe_lora_backward(c.dy, t["x"], t["z"], c.ids, c.A, c.B, c.scale, t["dx0"], t["dx"], t["dA"], t["dB"],
                              ws[1], **kw)
 
-    outs = [n for n in t if n not in ("lg", "x", "dyr")]
+    outs = [n for n in t if n not in ("lg", "aid", "x", "dyr")]
     return t, outs, call
 
 
-@pytest.mark.parametrize("M", [6, 700, 1400])
+@pytest.mark.parametrize("M", [6, 200, 700, 1400, 2500])
 def test_graph_replays(hm, M):
     """A captured run of every operator, replayed on new inputs with eager work between."""
     torch = torch_mod()
@@ -555,6 +556,7 @@ def test_graph_replays(hm, M):
     for i in range(4):
         t["lg"].copy_(rand(torch, 100 + i, *t["lg"].shape))
         t["x"].copy_(rand(torch, 200 + i, *t["x"].shape, dtype="bfloat16"))
+        t["aid"].copy_(to_dev(lora_ids(M, 3, ("mixed", "one", "none", "runs")[i], i)))
         call()
         torch.cuda.synchronize()
         eager = {n: t[n].clone() for n in outs}

@@ -173,6 +173,13 @@ hmoe_status check_arrays(const char* names, std::initializer_list<const void*> p
   return HMOE_OK;
 }
 
+// an output that starts where an input does would be overwritten while it is read
+hmoe_status check_apart(const char* name, const void* out, std::initializer_list<const void*> ins) {
+  for (const void* p : ins)
+    if (p == out) return fail(HMOE_ERR_INVALID_ARG, std::string(name) + " is one of the inputs");
+  return HMOE_OK;
+}
+
 hmoe_status check_op_scratch(const void* scratch, size_t have, size_t need) {
   if (have < need)
     return fail(HMOE_ERR_SCRATCH, "scratch has " + std::to_string(have) + " bytes, needs " +
@@ -635,6 +642,7 @@ hmoe_status moe_permute(const void* x, int64_t x_stride, const int32_t* topk_ids
   if (M > 0) {
     if (hmoe_status st = check_matrix("x", x, x_stride, H, es)) return st;
     if (hmoe_status st = check_matrix("rows", rows, rows_stride, H, es)) return st;
+    if (hmoe_status st = check_apart("rows", rows, {x})) return st;
     if (hmoe_status st = check_arrays("topk_ids, sorted_slots and slot_row",
                                       {topk_ids, sorted_slots, slot_row}))
       return st;
@@ -656,6 +664,7 @@ hmoe_status moe_permute_backward(const void* drows, int64_t drows_stride, const 
   const int es = element_size(dtype);
   if (hmoe_status st = check_matrix("drows", drows, drows_stride, H, es)) return st;
   if (hmoe_status st = check_matrix("dx", dx, dx_stride, H, es)) return st;
+  if (hmoe_status st = check_apart("dx", dx, {drows})) return st;
   if (hmoe_status st = check_arrays("slot_row", {slot_row})) return st;
   const hmoe::PermuteRows p{drows, drows_stride, dx, dx_stride, slot_row, M, k, H, dtype, es};
   hipError_t err = hmoe::launch_combine(p, nullptr, stream);
@@ -672,6 +681,7 @@ hmoe_status moe_unpermute(const void* rows, int64_t rows_stride, const int32_t* 
   const int es = element_size(dtype);
   if (hmoe_status st = check_matrix("rows", rows, rows_stride, H, es)) return st;
   if (hmoe_status st = check_matrix("y", y, y_stride, H, es)) return st;
+  if (hmoe_status st = check_apart("y", y, {rows})) return st;
   if (hmoe_status st = check_arrays("slot_row and topk_w", {slot_row, topk_w})) return st;
   const hmoe::PermuteRows p{rows, rows_stride, y, y_stride, slot_row, M, k, H, dtype, es};
   hipError_t err = hmoe::launch_combine(p, topk_w, stream);
@@ -691,6 +701,7 @@ hmoe_status moe_unpermute_backward(const void* dy, int64_t dy_stride, const void
   if (hmoe_status st = check_matrix("dy", dy, dy_stride, H, es)) return st;
   if (hmoe_status st = check_matrix("rows", rows, rows_stride, H, es)) return st;
   if (hmoe_status st = check_matrix("drows", drows, drows_stride, H, es)) return st;
+  if (hmoe_status st = check_apart("drows", drows, {dy, rows})) return st;
   if (hmoe_status st = check_arrays("slot_row, topk_w and dw", {slot_row, topk_w, dw})) return st;
   const hmoe::PermuteRows p{dy, dy_stride, drows, drows_stride, slot_row, M, k, H, dtype, es};
   hipError_t err = hmoe::launch_unpermute_bwd(p, rows, rows_stride, topk_w, dw, stream);
@@ -731,6 +742,7 @@ hmoe_status moe_lora(const uint16_t* x, int64_t x_stride, const int32_t* ids, co
   if (hmoe_status st = check_matrix("x", x, x_stride, K, 2)) return st;
   if (hmoe_status st = check_matrix("y", y, y_stride, N, 2)) return st;
   if (hmoe_status st = check_base("base", base, base_stride, y, y_stride, N)) return st;
+  if (hmoe_status st = check_apart("y", y, {x})) return st;
   if (hmoe_status st = check_arrays("ids, A, B and scale", {ids, A, B, scale})) return st;
   if (!aligned(z, 16)) return fail(HMOE_ERR_ALIGN, "z must be 16-byte aligned");
   size_t need;
@@ -756,6 +768,7 @@ hmoe_status moe_lora_backward(const uint16_t* dy, int64_t dy_stride, const uint1
     if (hmoe_status st = check_matrix("x", x, x_stride, K, 2)) return st;
     if (hmoe_status st = check_matrix("dx", dx, dx_stride, K, 2)) return st;
     if (hmoe_status st = check_base("dbase", dbase, dbase_stride, dx, dx_stride, K)) return st;
+    if (hmoe_status st = check_apart("dx", dx, {dy, x})) return st;
     if (hmoe_status st = check_arrays("ids and z", {ids, z})) return st;
   }
   size_t need;

@@ -646,7 +646,7 @@ hipError_t launch_permute(const PermuteRows& p, const int32_t* ids, int E, int32
                           int32_t* off, int32_t* counts, hipStream_t s) {
   const long n = (long)p.M * p.k, bytes = (long)p.H * p.esize;
   const int chunks = row_chunks(bytes);
-  if (n <= kPermuteSmall && E <= kMaxExperts) {
+  if (n <= kPermuteSmall) {
     PermuteSmallArgs a{(const char*)p.src, p.src_stride * p.esize, ids, p.M, p.k, E, chunks, bytes,
                        (char*)p.dst, p.dst_stride * p.esize, sorted, const_cast<int32_t*>(p.slot_row), off};
     hipLaunchKernelGGL(permute_small_kernel, dim3(p.M * chunks + 1), dim3(kRowThreads), 0, s, a);
