@@ -925,6 +925,7 @@ struct WgradArgs {
   long xs[2];
   int C[2], blocks[2];
   float* out[2];
+  int split;              // waves that share the rows of 64 columns
 };
 
 constexpr int kWgradThreads = 512;
@@ -945,7 +946,8 @@ __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) 
   __shared__ float s_red[SPLIT ? kWgradWaves : 1][16][68];
   __shared__ int32_t s_idx[kWgradRows];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid >> 6;
-  const int tile = SPLIT ? (int)blockIdx.x : (int)blockIdx.x * kWgradWaves + wave;
+  const int abreast = SPLIT ? kWgradWaves / a.split : kWgradWaves;  // waves of a row range
+  const int tile = (int)blockIdx.x * abreast + wave % abreast, phase = wave / abreast;
   const int side = tile >= a.blocks[0], g = blockIdx.y;
   const int c0 = (tile - (side ? a.blocks[0] : 0)) * 64;
   const int c = lane & 15, q = lane >> 4;
@@ -991,19 +993,19 @@ __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) 
           for (int t = 0; t < 4; ++t) acc[i][t] = mfma(v.p[part][i], xf[t], acc[i][t]);
     };
     // the next step's loads without a condition of their own (see the first product)
-    constexpr int kStride = (SPLIT ? kWgradWaves : 1) * 32;
+    const int stride = SPLIT ? a.split * 32 : 32;
     Step u, v;
-    int m = SPLIT ? wave * 32 : 0;
+    int m = phase * 32;
     if (m < rows) {
       load(u, m);
-      for (; m + 2 * kStride < rows; m += 2 * kStride) {
-        load(v, m + kStride);
+      for (; m + 2 * stride < rows; m += 2 * stride) {
+        load(v, m + stride);
         multiply(u);
-        load(u, m + 2 * kStride);
+        load(u, m + 2 * stride);
         multiply(v);
       }
-      if (m + kStride < rows) {
-        load(v, m + kStride);
+      if (m + stride < rows) {
+        load(v, m + stride);
         multiply(u);
         multiply(v);
       } else {
@@ -1013,11 +1015,10 @@ __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) 
   }
   // lane (c, q) holds ranks 4q .. 4q + 3 of columns 4c .. 4c + 3; columns run fastest in dA,
   // ranks in dB
-  const int waves = SPLIT ? min(kWgradWaves, (m1 - m0 + 31) / 32) : 0;  // those with rows
-  if (waves <= 1) {
-    if (SPLIT && wave) return;
+  const int phases = SPLIT ? min(a.split, (m1 - m0 + 31) / 32) : 0;  // those with rows
+  if (phases <= 1) {
     const int cl = c0 + c * 4;
-    if (tile >= a.blocks[0] + a.blocks[1] || cl >= C) return;
+    if (phase || tile >= a.blocks[0] + a.blocks[1] || cl >= C) return;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const int rr = (i0 + i) * 16 + q * 4;
@@ -1037,18 +1038,19 @@ __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) 
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
     __syncthreads();
-    if (wave < waves)
+    if (phase < phases)
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s_red[SPLIT ? wave : 0][q * 4 + e][c * 4 + t] = acc[i][t][e];
     __syncthreads();
-    for (int o = tid; o < 16 * 64; o += kWgradThreads) {
+    // the waves of a tile add its 16 x 64 sums
+    for (int o = phase * kWave + lane; o < 16 * 64; o += a.split * kWave) {
       const int pr = side ? o & 15 : o >> 6, cc = side ? o >> 4 : o & 63;
       const int rr = (i0 + i) * 16 + pr, cl = c0 + cc;
-      if (rr >= a.r || cl >= C) continue;
+      if (rr >= a.r || cl >= C || tile >= a.blocks[0] + a.blocks[1]) continue;
       float s = 0.f;
-      for (int w = 0; w < waves; ++w) s += s_red[w][pr][cc];
+      for (int w = 0; w < phases; ++w) s += s_red[SPLIT ? w * abreast + wave % abreast : 0][pr][cc];
       a.out[side][side ? ((long)g * C + cl) * a.r + rr : ((long)g * a.r + rr) * C + cl] = s;
     }
   }
@@ -1060,7 +1062,6 @@ __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) 
 
 namespace {
 
-constexpr int kWgradAlone = 1024;       // waves of the weight gradients from which none shares rows
 constexpr int kFusedBytes = 512 << 10;  // its largest first matrix, half of that for few tiles
 constexpr int kShrinkBlocks = 400;      // about this many blocks of the first product
 constexpr int kFusedRank = 64;          // and its largest rank (registers)
@@ -1276,11 +1277,20 @@ hipError_t launch_lora_backward(const LoraGrad& l, void* scratch, hipStream_t s)
   const int32_t* off = reinterpret_cast<const int32_t*>(b + sp.off);
   const int32_t* tile_first = reinterpret_cast<const int32_t*>(b + sp.tile_first);
   WgradArgs w{t.sorted, off, tile_first, p.rt / 32, l.r, {frag[0], frag[1]}, {l.x, l.dy}, {l.xs, l.dys}, {l.K, l.N},
-              {(l.K + 63) / 64, (l.N + 63) / 64}, {l.dA, l.dB}};
-  // a wave to each 64 columns of an adapter where that fills the chip's 1024 SIMDs, else eight
+              {(l.K + 63) / 64, (l.N + 63) / 64}, {l.dA, l.dB}, 1};
+  // Waves share the rows of 64 columns until there are 1024 waves (a wave a SIMD), and on to
+  // 4096 while each keeps 200 rows, or 50 for every 16 ranks that it adds up through LDS. Us a
+  // call with 1, 2, 4, 8 waves sharing, 6144 -> 4096: 4000 rows of 4 adapters, rank 16: 100, 78,
+  // 72, 69; of 8, rank 16: 81, 74, 73, 73; of 8, rank 128: 156, 172, 188, -; 16000 of 4, rank
+  // 128: 584, 522, 472, 470; 512 of 2, rank 64: -, 59, 52, 55. 2048 -> 4096, 4000 of 16, rank 64:
+  // 77, 88.
   const int tiles = w.blocks[0] + w.blocks[1], halves = p.nt == 8 ? 2 : 1;
-  const bool split = (long)tiles * l.G * halves < kWgradAlone;
-  const dim3 grid(split ? tiles : (tiles + kWgradWaves - 1) / kWgradWaves, l.G, halves);
+  for (long waves = (long)tiles * l.G * halves;
+       w.split < kWgradWaves && (waves < 1024 || (waves < 4096 && l.M / l.G / (2 * w.split) >= std::max(200, 50 * p.nt))); waves *= 2)
+    w.split *= 2;
+  const bool split = w.split > 1;
+  const int abreast = kWgradWaves / w.split;
+  const dim3 grid((tiles + abreast - 1) / abreast, l.G, halves);
   const dim3 block(kWgradThreads);
 #define HMOE_WGRAD(NT, SPLIT) hipLaunchKernelGGL((lora_wgrad_kernel<NT, SPLIT>), grid, block, 0, s, w)
   if (split)
