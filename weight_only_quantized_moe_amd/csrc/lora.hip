@@ -52,6 +52,16 @@ __device__ __forceinline__ float bf16_rest(float v, float hi) {
   return (__float_as_uint(hi) & 0x7F800000u) == 0x7F800000u ? 0.f : v - hi;
 }
 
+// Kernel arguments into scalar registers here. The compiler would read them where they are
+// first used, behind the wait for a tile's rows and in the loops after it: the backward pass's
+// second product of 4001 rows, rank 16, took 26.5 us so, and 24.0 with its arguments read ahead
+// (the other kernels gain nothing).
+template <typename... T>
+__device__ __forceinline__ void read_ahead(const T&... v) {
+  auto one = [](auto u) { asm volatile("" ::"s"(u)); };
+  (one(v), ...);
+}
+
 // ---- lane exchanges ----------------------------------------------------------------
 //
 // An MFMA operand wants lane l to hold row l % 16, but the memory pipe takes 64 bytes a
@@ -143,14 +153,13 @@ __device__ __forceinline__ bool find_tile(const Tiles& t, int* g, int* n, int* i
   const int part = (int)blockIdx.x / t.tiles, e = (int)blockIdx.x - part * t.tiles;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid >> 6;
   if (ROWS == 0 || t.find == kTable) {
-    const SortTile d = t.table[e];
-    if (d.group < 0) return false;
+    const SortTile d = t.table[e];  // an idle entry has no rows
     *g = d.group;
     *index = d.index;
     *n = max(0, min(RT, d.rows - part * RT));
     if (tid < RT) s_rows[tid] = tid < *n ? t.sorted[d.start + part * RT + tid] : 0;
     __syncthreads();
-    return true;
+    return d.group >= 0;
   }
   if constexpr (ROWS > 0) {
     const bool put = t.sorted && blockIdx.y == 0;  // this block writes its entry
@@ -693,7 +702,7 @@ struct ExpandLds {
 // quarter. In the backward pass (TR) the first block of a tile also leaves scale dz as
 // fragments for the weight gradients, the last one scale z. Bound by base and y in HBM behind
 // the chain table, z's splits, columns: 4096 rows, rank 64, N = 4096: 24.9 us (67 MB, 2.7 TB/s;
-// 37 with RW = 1); backward, 4001 rows, rank 16, K = 6144: 26.6 us (98 MB, 3.7 TB/s; 34).
+// 37 with RW = 1); backward, 4001 rows, rank 16, K = 6144: 24.0 us (98 MB, 4.1 TB/s; 34).
 template <int RW, int KS, bool TR>
 __global__ __launch_bounds__(kExpandWaves* kWave, (KS <= 2 ? (RW == 1 && !(TR && KS == 2) ? 4 : 3) : 2))
 void lora_expand_kernel(ExpandArgs a) {
@@ -705,6 +714,8 @@ void lora_expand_kernel(ExpandArgs a) {
   __shared__ __align__(16) char s_shared[L::kShared];
   float* s_p = reinterpret_cast<float*>(s_shared);
   u32x4* s_w = reinterpret_cast<u32x4*>(s_shared);
+  read_ahead(a.part, a.splits, a.scale, a.z, a.col_groups, a.c.w, a.c.base, a.c.bs, a.c.y, a.c.ys);
+  if (TR) read_ahead(a.frag[0], a.frag[1], a.fz, a.steps_per_tile);
   int g, n, index;
   if (!find_tile<RT, 0, kThreads>(a.tiles, &g, &n, &index, s_rows)) return;
   const bool live = g != a.tiles.G, head = blockIdx.y == 0;
@@ -931,7 +942,6 @@ struct WgradArgs {
   long xs[2];
   int C[2], blocks[2];
   float* out[2];
-  int split;              // waves that share the rows of 64 columns
 };
 
 constexpr int kWgradThreads = 512;
@@ -943,19 +953,20 @@ constexpr int kWgradRows = 2048;  // row indices kept in LDS at a time
 // columns (8 bytes each, 128 contiguous bytes a row over 16 lanes) and turns them in registers
 // into the fragments of 4 MFMAs; P lies ready as fragments, in three bf16 parts (24 bits), so
 // the fp32 result carries no bf16 rounding. A wave has 64 columns and goes through the rows in
-// steps of 32, the next step's loads in flight. SPLIT: several of the block's waves share the
-// columns, take steps in turn and add up through LDS in wave order; else each wave has columns
-// of its own and writes its registers. Rows past the group's end are zeros of P. Ranks past
+// steps of 32, the next step's loads in flight. SHARE of the block's waves have
+// the same columns, take steps in turn and add up through LDS in wave order; a wave alone
+// writes its registers. Rows past the group's end are zeros of P. Ranks past
 // NT * 16 go to further blocks (grid z). Bound by the rows (each read once) at low ranks, by the
 // way of P's parts from L2 at high ones: 4001 rows of 4 adapters, 6144 and 4096 columns, rank
 // 16: 26 us (82 MB, 3.2 TB/s).
-template <int NT, bool SPLIT>
+template <int NT, int SHARE>
 __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) {
-  __shared__ float s_red[SPLIT ? kWgradWaves : 1][16][68];
+  __shared__ float s_red[SHARE > 1 ? kWgradWaves : 1][16][68];
   __shared__ int32_t s_idx[kWgradRows];
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid >> 6;
-  const int abreast = SPLIT ? kWgradWaves / a.split : kWgradWaves;  // waves of a row range
-  const int tile = (int)blockIdx.x * abreast + wave % abreast, phase = wave / abreast;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // the columns' addresses stay scalar
+  constexpr int kAbreast = kWgradWaves / SHARE;  // waves of a row range
+  const int tile = (int)blockIdx.x * kAbreast + wave % kAbreast, phase = wave / kAbreast;
   const int side = tile >= a.blocks[0], g = blockIdx.y;
   const int c0 = (tile - (side ? a.blocks[0] : 0)) * 64;
   const int c = lane & 15, q = lane >> 4;
@@ -1001,19 +1012,19 @@ __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) 
           for (int t = 0; t < 4; ++t) acc[i][t] = mfma(v.p[part][i], xf[t], acc[i][t]);
     };
     // the next step's loads without a condition of their own (see the first product)
-    const int stride = SPLIT ? a.split * 32 : 32;
+    constexpr int kStride = SHARE * 32;
     Step u, v;
     int m = phase * 32;
     if (m < rows) {
       load(u, m);
-      for (; m + 2 * stride < rows; m += 2 * stride) {
-        load(v, m + stride);
+      for (; m + 2 * kStride < rows; m += 2 * kStride) {
+        load(v, m + kStride);
         multiply(u);
-        load(u, m + 2 * stride);
+        load(u, m + 2 * kStride);
         multiply(v);
       }
-      if (m + stride < rows) {
-        load(v, m + stride);
+      if (m + kStride < rows) {
+        load(v, m + kStride);
         multiply(u);
         multiply(v);
       } else {
@@ -1023,7 +1034,7 @@ __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) 
   }
   // lane (c, q) holds ranks 4q .. 4q + 3 of columns 4c .. 4c + 3; columns run fastest in dA,
   // ranks in dB
-  const int phases = SPLIT ? min(a.split, (m1 - m0 + 31) / 32) : 0;  // those with rows
+  const int phases = SHARE > 1 ? min(SHARE, (m1 - m0 + 31) / 32) : 0;  // those with rows
   if (phases <= 1) {
     const int cl = c0 + c * 4;
     if (phase || tile >= a.blocks[0] + a.blocks[1] || cl >= C) return;
@@ -1050,15 +1061,15 @@ __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) 
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s_red[SPLIT ? wave : 0][q * 4 + e][c * 4 + t] = acc[i][t][e];
+        for (int e = 0; e < 4; ++e) s_red[SHARE > 1 ? wave : 0][q * 4 + e][c * 4 + t] = acc[i][t][e];
     __syncthreads();
     // the waves of a tile add its 16 x 64 sums
-    for (int o = phase * kWave + lane; o < 16 * 64; o += a.split * kWave) {
+    for (int o = phase * kWave + lane; o < 16 * 64; o += SHARE * kWave) {
       const int pr = side ? o & 15 : o >> 6, cc = side ? o >> 4 : o & 63;
       const int rr = (i0 + i) * 16 + pr, cl = c0 + cc;
       if (rr >= a.r || cl >= C || tile >= a.blocks[0] + a.blocks[1]) continue;
       float s = 0.f;
-      for (int w = 0; w < phases; ++w) s += s_red[SPLIT ? w * abreast + wave % abreast : 0][pr][cc];
+      for (int w = 0; w < phases; ++w) s += s_red[SHARE > 1 ? w * kAbreast + wave % kAbreast : 0][pr][cc];
       a.out[side][side ? ((long)g * C + cl) * a.r + rr : ((long)g * a.r + rr) * C + cl] = s;
     }
   }
@@ -1298,34 +1309,37 @@ hipError_t launch_lora_backward(const LoraGrad& l, void* scratch, hipStream_t s)
   const int32_t* off = reinterpret_cast<const int32_t*>(b + sp.off);
   const int32_t* tile_first = reinterpret_cast<const int32_t*>(b + sp.tile_first);
   WgradArgs w{t.sorted, off, tile_first, p.rt / 32, l.r, {frag[0], frag[1]}, {l.x, l.dy}, {l.xs, l.dys}, {l.K, l.N},
-              {(l.K + 63) / 64, (l.N + 63) / 64}, {l.dA, l.dB}, 1};
+              {(l.K + 63) / 64, (l.N + 63) / 64}, {l.dA, l.dB}};
   // Waves share the rows of 64 columns until there are 1024 waves (a wave a SIMD), and on to
-  // 4096 while each keeps 200 rows, or 50 for every 16 ranks that it adds up through LDS. Us a
-  // call with 1, 2, 4, 8 waves sharing, 6144 -> 4096: 4000 rows of 4 adapters, rank 16: 100, 78,
-  // 72, 69; of 8, rank 16: 81, 74, 73, 73; of 8, rank 128: 156, 172, 188, -; 16000 of 4, rank
-  // 128: 584, 522, 472, 470; 512 of 2, rank 64: -, 59, 52, 55. 2048 -> 4096, 4000 of 16, rank 64:
-  // 77, 88.
+  // 4096 while each keeps enough rows for what it adds up through LDS: 200, or 50 for every 16
+  // ranks, half of that where waves share already. Us a call with 1, 2, 4, 8 waves sharing, 6144
+  // -> 4096: 4000 rows of 4 adapters, rank 16: 100, 78, 72, 69; of 8, rank 16: 81, 74, 73, 73; of
+  // 8, rank 128: 156, 172, 188, -; 16000 of 4, rank 128: 584, 522, 472, 470; 512 of 2, rank 64:
+  // -, 59, 52, 55. 2048 -> 4096, 4000 of 16, rank 64: 77, 88.
   const int tiles = w.blocks[0] + w.blocks[1], halves = p.nt == 8 ? 2 : 1;
+  int share = 1;
   for (long waves = (long)tiles * l.G * halves;
-       w.split < kWgradWaves && (waves < 1024 || (waves < 4096 && l.M / l.G / (2 * w.split) >= std::max(200, 50 * p.nt))); waves *= 2)
-    w.split *= 2;
-  const bool split = w.split > 1;
-  const int abreast = kWgradWaves / w.split;
-  const dim3 grid((tiles + abreast - 1) / abreast, l.G, halves);
-  const dim3 block(kWgradThreads);
-#define HMOE_WGRAD(NT, SPLIT) hipLaunchKernelGGL((lora_wgrad_kernel<NT, SPLIT>), grid, block, 0, s, w)
-  if (split)
-    switch (p.nt) {
-      case 1: HMOE_WGRAD(1, true); break;
-      case 2: HMOE_WGRAD(2, true); break;
-      default: HMOE_WGRAD(4, true); break;
-    }
-  else
-    switch (p.nt) {
-      case 1: HMOE_WGRAD(1, false); break;
-      case 2: HMOE_WGRAD(2, false); break;
-      default: HMOE_WGRAD(4, false); break;
-    }
+       share < kWgradWaves &&
+       (waves < 1024 || (waves < 4096 && l.M / l.G / (2 * share) >= (share == 1 ? 50 : 25) * std::max(4, p.nt)));
+       waves *= 2)
+    share *= 2;
+  const int abreast = kWgradWaves / share;
+  const dim3 grid((tiles + abreast - 1) / abreast, l.G, halves), block(kWgradThreads);
+#define HMOE_WGRAD(NT, SHARE)         \
+  if (std::min(p.nt, 4) == NT && share == SHARE) \
+  hipLaunchKernelGGL((lora_wgrad_kernel<NT, SHARE>), grid, block, 0, s, w)
+  HMOE_WGRAD(1, 1);
+  HMOE_WGRAD(1, 2);
+  HMOE_WGRAD(1, 4);
+  HMOE_WGRAD(1, 8);
+  HMOE_WGRAD(2, 1);
+  HMOE_WGRAD(2, 2);
+  HMOE_WGRAD(2, 4);
+  HMOE_WGRAD(2, 8);
+  HMOE_WGRAD(4, 1);
+  HMOE_WGRAD(4, 2);
+  HMOE_WGRAD(4, 4);
+  HMOE_WGRAD(4, 8);
 #undef HMOE_WGRAD
   return hipGetLastError();
 }
