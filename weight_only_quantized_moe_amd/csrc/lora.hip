@@ -611,7 +611,7 @@ constexpr int kShrinkWaves = 4;
 
 // part[s][m] = W_g x[m] over split s of K. Bound by the way of x from HBM and of W from L2 into
 // the registers, which the few steps of a wave hide only in part: 4096 rows of 8 adapters, rank
-// 64, K = 6144: 22.6 us (50 MB of x, 2.2 TB/s; 17 with W held in L1, 13 with x there, 9 with both).
+// 64, K = 6144: 22.8 us (50 MB of x, 2.2 TB/s; 17 with W held in L1, 13 with x there, 9 with both).
 // Tiles of 64 rows a block, which halve W's way, were no faster.
 template <int MT, int NT>
 __global__ __launch_bounds__(kShrinkWaves* kWave) void lora_shrink_kernel(ShrinkArgs a) {
@@ -859,7 +859,7 @@ constexpr int kFusedRows = 1024;  // most rows of the one-launch form
 // leaves LDS, then they split the block's columns. Blocks of one tile that take different
 // columns repeat the first product (its matrix comes from L2 again). TR: the backward pass, as
 // in the second product alone. Bound by latency: find the tile, load, multiply, add up, load,
-// multiply, write. 1 row, 2048 -> 1536, rank 16: 7.2 us; 64 rows of 48 adapters, 6144 -> 4096:
+// multiply, write. 1 row, 2048 -> 1536, rank 16: 6.8 us; 64 rows of 48 adapters, 6144 -> 4096:
 // 11.5 us (13 MB).
 template <int NT, int KS, bool TR>
 __global__ __launch_bounds__(kFusedWaves* kWave) void lora_fused_kernel(FusedArgs a) {
@@ -937,7 +937,7 @@ struct WgradArgs {
   int steps_per_tile;
   int r;
   // two products: [0] P = scale dz, X = x, out dA [G, r, C]; [1] P = scale z, X = dy, out dB [G, C, r]
-  const uint16_t* p[2];   // fragments of P, see Parts
+  const uint16_t* p[2];   // fragments of P, see put_parts
   const uint16_t* x[2];
   long xs[2];
   int C[2], blocks[2];
@@ -958,7 +958,7 @@ constexpr int kWgradRows = 2048;  // row indices kept in LDS at a time
 // writes its registers. Rows past the group's end are zeros of P. Ranks past
 // NT * 16 go to further blocks (grid z). Bound by the rows (each read once) at low ranks, by the
 // way of P's parts from L2 at high ones: 4001 rows of 4 adapters, 6144 and 4096 columns, rank
-// 16: 26 us (82 MB, 3.2 TB/s).
+// 16: 23.7 us (82 MB, 3.5 TB/s).
 template <int NT, int SHARE>
 __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) {
   __shared__ float s_red[SHARE > 1 ? kWgradWaves : 1][16][68];
