@@ -23,8 +23,10 @@ namespace hmoe {
 // ---------------------------------------------------------------------------
 
 // threads of a sort block: every wave keeps a counter per group in LDS, so 16 waves up to
-// kSortWideGroups groups (41 KB of counters), 4 waves beyond
-constexpr int kSortWide = 1024, kSortNarrow = 256, kSortWideGroups = 640;
+// kSortWideGroups groups (41 KB of counters), 4 waves beyond. 4 waves also for up to
+// kSortFewIds ids, whose barriers cost less: the adapters' backward pass of 64 rows takes 16.0 us
+// so and 17.3 with 16 waves, of 1500 rows 25.8 and 24.5
+constexpr int kSortWide = 1024, kSortNarrow = 256, kSortWideGroups = 640, kSortFewIds = 1024;
 // up to this many ids one block counts and places; more ids are counted and placed by
 // several blocks of kSortChunk ids in two launches
 constexpr int kSortOneBlock = 8192, kSortChunk = 2048;
@@ -129,8 +131,9 @@ __global__ __launch_bounds__(THREADS) void sort_place_kernel(SortArgs a) {
   __shared__ int32_t s_base[kGroups];       // first row of each group
   __shared__ int32_t s_tile[kGroups + 1];   // first tile of each group
   __shared__ int32_t s_part[kWaves];
-  if ((int)blockIdx.x >= a.nb) {  // blocks beside the sort
-    transpose_block(a.turn, (long)(blockIdx.x - a.nb) * THREADS + threadIdx.x);
+  if ((int)blockIdx.x >= a.nb) {  // blocks beside the sort: four waves each, over more CUs
+    if (threadIdx.x < kSortNarrow)
+      transpose_block(a.turn, (long)(blockIdx.x - a.nb) * kSortNarrow + threadIdx.x);
     return;
   }
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid >> 6;
@@ -287,11 +290,11 @@ hipError_t launch_sort(const GroupSort& g, hipStream_t s) {
   if (a.nb > 1) hipLaunchKernelGGL(sort_count_kernel, dim3(a.nb), dim3(kSortWide), 0, s, a);
   a.turn = g.turn;
   const long turns = g.turn.in ? (long)g.turn.G * (g.turn.N / 8) * (g.turn.r / 8) : 0;
-  auto blocks = [&](int threads) { return dim3((unsigned)(a.nb + (turns + threads - 1) / threads)); };
-  if (g.groups <= kSortWideGroups)
-    hipLaunchKernelGGL(sort_place_kernel<kSortWide>, blocks(kSortWide), dim3(kSortWide), 0, s, a);
+  const dim3 blocks((unsigned)(a.nb + (turns + kSortNarrow - 1) / kSortNarrow));
+  if (g.groups <= kSortWideGroups && g.n > kSortFewIds)
+    hipLaunchKernelGGL(sort_place_kernel<kSortWide>, blocks, dim3(kSortWide), 0, s, a);
   else
-    hipLaunchKernelGGL(sort_place_kernel<kSortNarrow>, blocks(kSortNarrow), dim3(kSortNarrow), 0, s, a);
+    hipLaunchKernelGGL(sort_place_kernel<kSortNarrow>, blocks, dim3(kSortNarrow), 0, s, a);
   return hipGetLastError();
 }
 
