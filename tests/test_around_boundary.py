@@ -187,6 +187,38 @@ def test_binding_checks_tensors():
             lora(**kw)
 
 
+def test_binding_checks_gradients():
+    torch = pytest.importorskip("torch")
+    M, k, E, H, G, r, K, N = 4, 2, 8, 16, 3, 8, 64, 32
+    bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    z = torch.zeros
+
+    def lora(**kw):
+        t = dict(dy=z(M, N, dtype=bf), x=z(M, K, dtype=bf), z=z(M, r), ids=z(M, dtype=i32), A=z(G, r, K, dtype=bf),
+                 B=z(G, N, r, dtype=bf), scale=z(G), dbase=None, dx=z(M, K, dtype=bf), dA=z(G, r, K), dB=z(G, N, r))
+        hm.moe_lora_backward(**{**t, **kw})
+
+    def unpermute(**kw):
+        t = dict(dy=z(M, H), rows=z(M * k, H), slot_row=z(M, k, dtype=i32), topk_w=z(M, k), drows=z(M * k, H), dw=z(M, k))
+        hm.moe_unpermute_backward(**{**t, **kw})
+
+    def route(**kw):
+        t = dict(topk_ids=z(M, k, dtype=i32), topk_w=z(M, k), dw=z(M, k), dlogits=z(M, E))
+        hm.moe_route_backward(**{**t, **kw})
+
+    for f in (lora, unpermute, route):
+        with pytest.raises(ValueError, match="one GPU"):
+            f()
+    for f, kw in ((lora, {"z": None}), (lora, {"dA": z(G, r, K, dtype=bf)}), (lora, {"dB": z(G, r, N)}),
+                  (lora, {"dbase": z(M, N, dtype=bf)}), (lora, {"dx": z(M, K)}), (lora, {"dy": z(K, M, dtype=bf).t()}),
+                  (unpermute, {"dw": z(M, k, dtype=bf)}), (unpermute, {"drows": z(M, H)}),
+                  (unpermute, {"dy": z(M, H, dtype=bf)}), (unpermute, {"slot_row": z(M, k, dtype=f32)}),
+                  (route, {"dlogits": z(M, E, dtype=bf)}), (route, {"dw": z(M, k + 1)}),
+                  (route, {"topk_ids": z(k, M, dtype=i32).t()})):
+        with pytest.raises(ValueError):
+            f(**kw)
+
+
 # ---- the oracle's gradients against central differences of its forward forms ------------
 
 def _differences(f, v, step=1e-5):

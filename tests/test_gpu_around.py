@@ -323,7 +323,8 @@ LORA = [(1, 1, 8, 8, 8, "one"), (1, 16, 2048, 1536, 16, "any"), (2, 3, 72, 40, 2
         (1024, 60, 2048, 1536, 32, "mixed"), (90, 20, 4096, 4104, 64, "any"), (300, 70, 520, 2056, 128, "mixed"),
         (120, 2, 8200, 136, 32, "mixed"), (2000, 1, 4096, 64, 24, "one"),
         (9000, 300, 24, 16, 8, "mixed"), (20000, 1500, 16, 8, 16, "any"),
-        (7000, 3, 136, 24, 128, "mixed"), (7000, 400, 72, 16, 96, "mixed")]
+        (7000, 3, 136, 24, 128, "mixed"), (7000, 400, 72, 16, 96, "mixed"),
+        (4500, 1, 72, 64, 16, "one"), (4500, 20, 72, 64, 32, "one"), (4200, 2, 2056, 1544, 64, "runs")]
 
 
 @pytest.mark.parametrize("M,G,K,N,r,kind", LORA)

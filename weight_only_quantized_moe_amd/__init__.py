@@ -402,6 +402,8 @@ def _matrix(name: str, t, shape: tuple, code: int) -> int:
 def _refuse(shape: tuple, dtype, **tensors) -> None:
     """Names the first tensor that is not contiguous, of this shape and type."""
     for name, t in tensors.items():
+        if t is None:
+            raise ValueError(f"{name} is missing")
         if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
             raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} (strides {t.stride()}), expected "
                              f"contiguous {dtype} {tuple(shape)}")
