@@ -571,6 +571,40 @@ def test_graph_replays(hm, M):
             assert torch.equal(t[n], eager[n]), f"replay {i}: {n}"
 
 
+def test_graphs_share_scratch(hm):
+    """Captured calls of different sizes on one scratch buffer, replayed in turn on one stream:
+    nothing of one call's scratch reaches the next."""
+    torch = torch_mod()
+    cases = [LoraCase(torch, M, G, 136, 200, r, "mixed", s)
+             for s, (M, G, r) in enumerate([(2500, 5, 24), (7, 3, 16), (300, 9, 64), (1100, 300, 8)])]
+    ws = torch.empty(max(t.numel() for c in cases for t in c.scratch(hm, torch)), device="cuda")
+    runs = []
+    for c in cases:
+        y, z = torch.empty_like(c.base), torch.empty(c.M, c.r, device="cuda")
+        dx, dA, dB = torch.empty_like(c.dbase), torch.empty_like(c.A, dtype=torch.float32), torch.empty_like(c.B, dtype=torch.float32)
+
+        def call(c=c, y=y, z=z, dx=dx, dA=dA, dB=dB):
+            hm.moe_lora(c.x, c.ids, c.A, c.B, c.scale, c.base, y, z, ws)
+            hm.moe_lora_backward(c.dy, c.x, z, c.ids, c.A, c.B, c.scale, c.dbase, dx, dA, dB, ws)
+
+        call()
+        torch.cuda.synchronize()
+        outs = (y, z, dx, dA, dB)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        runs.append((g, call, outs, [t.clone() for t in outs]))
+    for i in range(3):
+        for g, call, outs, _ in runs:
+            for t in outs:
+                t.zero_()
+            ws.fill_(float("nan"))
+            g.replay() if i != 1 else call()
+        torch.cuda.synchronize()
+        for _, _, outs, want in runs:
+            assert all(torch.equal(t, w) for t, w in zip(outs, want)), i
+
+
 @pytest.mark.parametrize("M", [30, 1400])
 def test_two_streams_at_once(hm, M):
     """Calls on two streams with buffers of their own do not disturb each other."""
