@@ -24,8 +24,8 @@ namespace hmoe {
 
 // threads of a sort block: every wave keeps a counter per group in LDS, so 16 waves up to
 // kSortWideGroups groups (41 KB of counters), 4 waves beyond. 4 waves also for up to
-// kSortFewIds ids, whose barriers cost less: the adapters' backward pass of 64 rows takes 16.0 us
-// so and 17.3 with 16 waves, of 1500 rows 25.8 and 24.5
+// kSortFewIds ids, whose barriers cost less: the adapters' backward pass (2048 -> 1536, rank 8)
+// takes 15.3 us so and 17.6 with 16 waves at 64 rows of 8, 25.8 and 24.5 at 1500 of 2
 constexpr int kSortWide = 1024, kSortNarrow = 256, kSortWideGroups = 640, kSortFewIds = 1024;
 // up to this many ids one block counts and places; more ids are counted and placed by
 // several blocks of kSortChunk ids in two launches
@@ -94,7 +94,7 @@ struct __attribute__((packed, aligned(2))) Raw16 {
 
 // Eight columns of eight ranks a thread, turned in registers: 16-byte reads and writes. Threads
 // run over the ranks first, so that eight of them share a row's 128 bytes (rank 64) on the way
-// in and eight on the way out: 48 adapters of 4096 x 64 (50 MB moved) in 17 us with the sort, 32
+// in and eight on the way out: 48 adapters of 4096 x 64 (50 MB moved) in 16 us with the sort, 32
 // with the columns first.
 __device__ __forceinline__ void transpose_block(const SortTranspose& t, long i) {
   const int nb = t.N / 8, rb = t.r / 8;
