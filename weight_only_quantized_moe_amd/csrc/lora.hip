@@ -283,7 +283,11 @@ template <int MT, int NT, int W, int DEPTH>
 __device__ __forceinline__ void shrink_tile(const uint16_t* x, long xs, const uint16_t* w, int K,
                                             int r, int n, const int32_t* s_rows, int s0, int s1,
                                             float (*s_red)[MT * NT * 256]) {
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
+  // A scalar wave number takes addresses out of the lanes' registers, but loops of few loads then
+  // wait for each: 16 rows of rank 64 win 4% (15.3 to 14.7 us at 1000 rows of 30 adapters, 2048 ->
+  // 1536), one row of rank 16 loses half (10 to 21 us, 6144 -> 4096), 32 rows change by 4% either way.
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = MT == 1 && NT == 4 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : (int)(threadIdx.x >> 6);
   const int c = lane & 15, q = lane >> 4, at = q * 32 + (c & 3) * 8;
   const uint16_t* xp[MT][4];
 #pragma unroll
