@@ -9,8 +9,7 @@
 // use, and by writing y. So every product runs on bf16 MFMA from global memory into fragments,
 // rows of one adapter are gathered into tiles of 16, 32 or 64 (one read of its matrices each),
 // and the long axis K is split over waves and blocks when there are few tiles. z stays in fp32:
-// where it is an MFMA operand it goes in as a sum of bf16 parts (two where the result is
-// rounded to bf16, three where it stays fp32), so it is not rounded to 8 bits on the way.
+// where z or dz is an MFMA operand it goes in as a sum of three bf16 parts, which hold its 24 bits.
 #include <algorithm>
 #include <type_traits>
 
@@ -45,11 +44,17 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
                                                  __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// bf16 parts of an fp32 value: hi + lo (+ lo2) with the residue of each rounded next. A
-// value beyond bf16's range (infinite hi) has no residue.
-__device__ __forceinline__ float bf16_round(float v) { return bf16_lo(pack_bf16(v, 0.f)); }
-__device__ __forceinline__ float bf16_rest(float v, float hi) {
-  return (__float_as_uint(hi) & 0x7F800000u) == 0x7F800000u ? 0.f : v - hi;
+// An fp32 value as a sum of three bf16 parts, 8 of its 24 bits each: a part is the upper half of
+// what the parts before it leave, so every part is exact and no finite value becomes infinite. An
+// infinite value leaves nothing. part[k]: a's in the low half, b's in the high one.
+__device__ __forceinline__ void split_parts(float a, float b, uint32_t (&part)[3]) {
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    part[k] = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+    const float ra = a - bf16_lo(part[k]), rb = b - bf16_hi(part[k]);
+    a = k == 0 && __builtin_isinf(a) ? 0.f : ra;
+    b = k == 0 && __builtin_isinf(b) ? 0.f : rb;
+  }
 }
 
 // Kernel arguments into scalar registers here. The compiler would read them where they are
@@ -424,7 +429,7 @@ __device__ __forceinline__ void shrink_tile(const uint16_t* x, long xs, const ui
 // W_g z of 16 rows, added to base: a wave takes 128 columns at a time. The columns are dealt
 // out to the MFMAs so that lane c of a group of 16 ends up with columns 8c .. 8c + 7 of four
 // rows: base and y move as 16-byte accesses, 16 lanes on 256 contiguous bytes of a row. A
-// fragment of W serves both bf16 parts of z; up to rank 16 (KS = 0) both parts share one MFMA.
+// fragment of W serves all bf16 parts of z; up to rank 16 (KS = 0) the first two share one MFMA.
 // TR: W is [r, N] (a lane's columns of 8 ranks are turned in registers), else [N, r].
 struct ColumnArgs {
   int r, N;
@@ -435,12 +440,13 @@ struct ColumnArgs {
   long ys;
 };
 
+// z: rows of scale z in LDS, fp32, kLd apart; a lane makes its fragments of them
 template <int KS>
 struct ZShape {
-  static constexpr bool kPack = KS == 0;         // rank <= 16: hi and lo side by side
+  static constexpr bool kPack = KS == 0;         // rank <= 16: two parts side by side
   static constexpr int kSteps = kPack ? 1 : KS;
-  static constexpr int kParts = kPack ? 1 : 2;
-  static constexpr int kRow = kSteps * 32 + 8;   // LDS row, padded off the banks
+  static constexpr int kParts = kPack ? 2 : 3;   // fragments of a rank step
+  static constexpr int kLd = kSteps * 32 + 4;    // padded off the banks
 };
 
 constexpr int kCols = 128;
@@ -512,10 +518,31 @@ struct Columns {
     }
   }
 
-  __device__ __forceinline__ void load_z(u32x4 (&zf)[Z::kParts], const uint16_t* s_z, int part, int ks) const {
+  // fragments of z for all rank steps: 8 ranks of row c in three bf16 parts (zeros past r)
+  __device__ __forceinline__ void make_z(u32x4 (&zf)[Z::kSteps][Z::kParts], const float* s_z) const {
 #pragma unroll
-    for (int p = 0; p < Z::kParts; ++p)
-      zf[p] = *reinterpret_cast<const u32x4*>(s_z + p * part + c * Z::kRow + ks * 32 + q * 8);
+    for (int ks = 0; ks < Z::kSteps; ++ks) {
+      const int ch = (ks * 4 + q) * 8;
+      const float* z = s_z + c * Z::kLd + chunk(ks, q);
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; e += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(z + e);
+        v[e] = f.x, v[e + 1] = f.y, v[e + 2] = f.z, v[e + 3] = f.w;
+      }
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        uint32_t part[3];
+        split_parts(v[2 * d], v[2 * d + 1], part);
+        if constexpr (Z::kPack) {  // [first, second], [third, zeros]
+          zf[ks][0][d] = ch < a.r ? part[0] : ch < 2 * a.r ? part[1] : 0u;
+          zf[ks][1][d] = ch < a.r ? part[2] : 0u;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 3; ++k) zf[ks][k][d] = ch < a.r ? part[k] : 0u;
+        }
+      }
+    }
   }
 
   // y = base + acc (rows without an adapter: y = base)
@@ -546,14 +573,12 @@ struct Columns {
   // groups cg, cg + W, ... below g1; `l` holds the loads of group cg
   template <int W>
   __device__ __forceinline__ void run(Load& l, bool live, int cg, int g1,
-                                      const uint16_t (*s_z)[16 * Z::kRow]) const {
+                                      const u32x4 (&zf)[Z::kSteps][Z::kParts]) const {
     while (cg < g1) {
       f32x4 acc[8] = {};
       if (live) {
 #pragma unroll
         for (int ks = 0; ks < Z::kSteps; ++ks) {
-          u32x4 zf[Z::kParts];
-          load_z(zf, s_z[0], 16 * Z::kRow, ks);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (ks) load_w(l.w[h], cg, ks, h);
@@ -564,7 +589,7 @@ struct Columns {
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
-              for (int p = 0; p < Z::kParts; ++p) acc[h * 4 + t] = mfma(zf[p], l.w[h][t], acc[h * 4 + t]);
+              for (int p = 0; p < Z::kParts; ++p) acc[h * 4 + t] = mfma(zf[ks][p], l.w[h][t], acc[h * 4 + t]);
           }
         }
       }
@@ -574,33 +599,6 @@ struct Columns {
     }
   }
 };
-
-// four ranks of one row of z into LDS as bf16 parts (col: first rank; zeros past r)
-template <int KS, int N>
-__device__ __forceinline__ void put_z(uint16_t (*s_z)[N], int row, int col, int r, const float (&v)[4]) {
-  using Z = ZShape<KS>;
-  uint32_t hi[2], lo[2];
-#pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    hi[p] = pack_bf16(v[2 * p], v[2 * p + 1]);
-    lo[p] = pack_bf16(bf16_rest(v[2 * p], bf16_lo(hi[p])), bf16_rest(v[2 * p + 1], bf16_hi(hi[p])));
-  }
-  uint16_t* at = &s_z[0][row * Z::kRow + col];
-  *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
-  *reinterpret_cast<uint2*>(Z::kPack ? at + r : &s_z[Z::kParts - 1][row * Z::kRow + col]) =
-      make_uint2(lo[0], lo[1]);
-}
-
-// zeros in the ranks of z's LDS rows that pad them to whole MFMA steps
-template <int KS, int RT, int N>
-__device__ __forceinline__ void pad_z(uint16_t (*s_z)[N], int r) {
-  using Z = ZShape<KS>;
-  const int from = Z::kPack ? 2 * r : r, pad = (Z::kSteps * 32 - from) / 4;
-  for (int i = threadIdx.x; i < RT * pad; i += blockDim.x)
-#pragma unroll
-    for (int p = 0; p < Z::kParts; ++p)
-      *reinterpret_cast<uint2*>(&s_z[p][i / pad * Z::kRow + from + i % pad * 4]) = make_uint2(0, 0);
-}
 
 struct ShrinkArgs {
   Tiles tiles;
@@ -674,33 +672,32 @@ __device__ __forceinline__ void put_parts(const float* s_p, int part, int n, int
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = rank < r && row + e < n ? s_p[(row + e) * LD + rank] : 0.f;
     const int at = part * RT + row, lane = at % 32 * 2 + c;
+    Half8 h[3];
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      Half8 h;
+    for (int p = 0; p < 4; ++p) {
+      uint32_t w[3];
+      split_parts(v[2 * p], v[2 * p + 1], w);
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        h.w[p] = pack_bf16(v[2 * p], v[2 * p + 1]);
-        v[2 * p] = bf16_rest(v[2 * p], bf16_lo(h.w[p]));
-        v[2 * p + 1] = bf16_rest(v[2 * p + 1], bf16_hi(h.w[p]));
-      }
-      *reinterpret_cast<Half8*>(out + (((at / 32 * 3 + k) * nt + i) * kWave + lane) * 8) = h;
+      for (int k = 0; k < 3; ++k) h[k].w[p] = w[k];
     }
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      *reinterpret_cast<Half8*>(out + (((at / 32 * 3 + k) * nt + i) * kWave + lane) * 8) = h[k];
   }
 }
 
-// LDS of the second product: z as bf16 parts, and what its waves share
-template <int RW, int KS, bool TR>
+// LDS of the second product: z before the columns, then what its waves share
+template <int RW, int KS>
 struct ExpandLds {
   using Z = ZShape<KS>;
-  static constexpr int kRows = RW * 16, kLd = Z::kSteps * 32 + 4;
   static constexpr bool kDouble = KS <= 2;                        // two sets of W's fragments
   static constexpr int kFrag = RW == 1 ? 0 : Z::kSteps * 8 * 1024;  // bytes of one set
-  static constexpr int kP = TR ? kRows * kLd * 4 : 0;             // dz or z in fp32, before the columns
-  static constexpr int kShared = std::max({kFrag * (kDouble ? 2 : 1), kP, 16});
+  static constexpr int kZ = RW * 16 * Z::kLd * 4;
+  static constexpr int kShared = std::max(kFrag * (kDouble ? 2 : 1), kZ);
 };
 
-// y = base + W_g (scale z): z's splits are added in order, scaled, split into two bf16 parts
-// and kept in LDS for the block's columns. RW = 1: 16 rows a block, each wave has columns of
+// y = base + W_g (scale z): z's splits are added in order, scaled and put into LDS, from where
+// every lane makes the fragments that it keeps for the block's columns. RW = 1: 16 rows a block, each wave has columns of
 // its own. RW = 4: 64 rows, a wave 16 of them; the waves share each group of columns, and each
 // turns a part of W's fragments and puts it into LDS for all, which cuts W's way from L2 to a
 // quarter. In the backward pass (TR) the first block of a tile also leaves scale dz as
@@ -708,15 +705,14 @@ struct ExpandLds {
 // the chain table, z's splits, columns: 4096 rows, rank 64, N = 4096: 24.9 us (67 MB, 2.7 TB/s;
 // 37 with RW = 1); backward, 4001 rows, rank 16, K = 6144: 24.0 us (98 MB, 4.1 TB/s; 34).
 template <int RW, int KS, bool TR>
-__global__ __launch_bounds__(kExpandWaves* kWave, (KS <= 2 ? (RW == 1 && !(TR && KS == 2) ? 4 : 3) : 2))
+__global__ __launch_bounds__(kExpandWaves* kWave, (KS <= 2 ? (RW == 1 && KS + TR < 2 ? 4 : 3) : 2))
 void lora_expand_kernel(ExpandArgs a) {
   using Z = ZShape<KS>;
-  using L = ExpandLds<RW, KS, TR>;
+  using L = ExpandLds<RW, KS>;
   constexpr int RT = RW * 16, kThreads = kExpandWaves * kWave;
   __shared__ int32_t s_rows[RT];
-  __shared__ __align__(16) uint16_t s_z[Z::kParts][RT * Z::kRow];
   __shared__ __align__(16) char s_shared[L::kShared];
-  float* s_p = reinterpret_cast<float*>(s_shared);
+  float* s_z = reinterpret_cast<float*>(s_shared);
   u32x4* s_w = reinterpret_cast<u32x4*>(s_shared);
   read_ahead(a.part, a.splits, a.scale, a.z, a.col_groups, a.c.w, a.c.base, a.c.bs, a.c.y, a.c.ys);
   if (TR) read_ahead(a.frag[0], a.frag[1], a.fz, a.steps_per_tile);
@@ -747,6 +743,7 @@ void lora_expand_kernel(ExpandArgs a) {
     cols.load_base(base, cg);
     if (live) load_pieces(cg);
   }
+  u32x4 zf[Z::kSteps][Z::kParts];
   if (live) {
     const float sc = a.scale[g];
     const long part = (long)a.tiles.M * r;
@@ -768,28 +765,23 @@ void lora_expand_kernel(ExpandArgs a) {
       }
       if (!TR && a.z && head)
         *reinterpret_cast<float4*>(a.z + (long)s_rows[row] * r + col) = make_float4(v[0], v[1], v[2], v[3]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] *= sc;
-      put_z<KS>(s_z, row, col, r, v);
-      if (TR && head) *reinterpret_cast<float4*>(s_p + row * L::kLd + col) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(s_z + row * Z::kLd + col) = make_float4(v[0] * sc, v[1] * sc, v[2] * sc, v[3] * sc);
     }
-    pad_z<KS, RT>(s_z, r);
+    __syncthreads();
+    cols.make_z(zf, s_z + mine * Z::kLd);
     if constexpr (TR) {
       const int pt = (int)blockIdx.x / a.tiles.tiles;
       const long at = (long)index * a.steps_per_tile * 3 * rank_tiles(r) * 512;
-      if (head) {
-        __syncthreads();
-        put_parts<RT, L::kLd>(s_p, pt, n, r, a.frag[0] + at);
-      }
+      if (head) put_parts<RT, Z::kLd>(s_z, pt, n, r, a.frag[0] + at);
       if (blockIdx.y == gridDim.y - 1) {
         __syncthreads();
         for (int i = threadIdx.x; i < n * quads; i += kThreads) {
           const int row = i / quads, col = i % quads * 4;
           const float4 f = *reinterpret_cast<const float4*>(a.fz + (long)s_rows[row] * r + col);
-          *reinterpret_cast<float4*>(s_p + row * L::kLd + col) = make_float4(f.x * sc, f.y * sc, f.z * sc, f.w * sc);
+          *reinterpret_cast<float4*>(s_z + row * Z::kLd + col) = make_float4(f.x * sc, f.y * sc, f.z * sc, f.w * sc);
         }
         __syncthreads();
-        put_parts<RT, L::kLd>(s_p, pt, n, r, a.frag[1] + at);
+        put_parts<RT, Z::kLd>(s_z, pt, n, r, a.frag[1] + at);
       }
     }
   } else if (!TR && a.z && head) {
@@ -798,7 +790,7 @@ void lora_expand_kernel(ExpandArgs a) {
   __syncthreads();
   if (!live && a.c.base == a.c.y) return;  // rows without an adapter stay
   if constexpr (RW == 1) {
-    cols.template run<kExpandWaves>(first, live, cg, g1, s_z);
+    cols.template run<kExpandWaves>(first, live, cg, g1, zf);
   } else {
     for (int it = 0; cg < g1; ++cg, ++it) {
       u32x4* buf = s_w + (L::kDouble ? (it & 1) * (L::kFrag / 16) : 0);
@@ -823,13 +815,11 @@ void lora_expand_kernel(ExpandArgs a) {
       if (live) {
 #pragma unroll
         for (int ks = 0; ks < Z::kSteps; ++ks) {
-          u32x4 zf[Z::kParts];
-          cols.load_z(zf, s_z[0] + mine * Z::kRow, RT * Z::kRow, ks);
 #pragma unroll
           for (int t = 0; t < 8; ++t) {
             const u32x4 f = buf[(ks * 8 + t) * kWave + lane];
 #pragma unroll
-            for (int p = 0; p < Z::kParts; ++p) acc[t] = mfma(zf[p], f, acc[t]);
+            for (int p = 0; p < Z::kParts; ++p) acc[t] = mfma(zf[ks][p], f, acc[t]);
           }
         }
       }
@@ -868,11 +858,10 @@ constexpr int kFusedRows = 1024;  // most rows of the one-launch form
 template <int NT, int KS, bool TR>
 __global__ __launch_bounds__(kFusedWaves* kWave) void lora_fused_kernel(FusedArgs a) {
   using Z = ZShape<KS>;
-  constexpr int kLd = Z::kSteps * 32 + 4, kThreads = kFusedWaves * kWave;
+  constexpr int kThreads = kFusedWaves * kWave;
   __shared__ int32_t s_rows[16];
   __shared__ __align__(16) float s_red[kFusedWaves / 2][NT * 256];
-  __shared__ __align__(16) uint16_t s_z[Z::kParts][16 * Z::kRow];
-  __shared__ __align__(16) float s_p[TR ? 16 * kLd : 4];
+  __shared__ __align__(16) float s_z[16 * Z::kLd];
   int g, n, index;
   if (!find_tile<16, TR ? 0 : kFusedRows, kThreads>(a.tiles, &g, &n, &index, s_rows)) return;
   const bool live = g != a.tiles.G, head = blockIdx.y == 0, tail = blockIdx.y == gridDim.y - 1;
@@ -881,7 +870,7 @@ __global__ __launch_bounds__(kFusedWaves* kWave) void lora_fused_kernel(FusedArg
   const long at = TR ? (long)index * 3 * rank_tiles(r) * 512 : 0;
   if (TR && n == 0) {  // an entry's empty second half: its fragments are zeros
     if (live && head)
-      for (int i = 0; i < 2; ++i) put_parts<16, kLd>(s_p, part, 0, r, a.frag[i] + at);
+      for (int i = 0; i < 2; ++i) put_parts<16, Z::kLd>(s_z, part, 0, r, a.frag[i] + at);
     return;
   }
   ColumnArgs ca = a.c;
@@ -891,6 +880,7 @@ __global__ __launch_bounds__(kFusedWaves* kWave) void lora_fused_kernel(FusedArg
   const int cg = g0 + (threadIdx.x >> 6);
   typename Columns<KS, TR>::Load first;  // on the way during the first product
   if (cg < g1) cols.load(first, live, cg);
+  u32x4 zf[Z::kSteps][Z::kParts];
   if (live) {
     shrink_tile<1, NT, kFusedWaves, (NT == 1 ? 4 : NT == 2 ? 2 : 1)>(
         a.x, a.xs, a.wa + (long)g * r * a.K, a.K, r, n, s_rows, 0, (a.K + kKStep - 1) / kKStep, s_red);
@@ -906,32 +896,27 @@ __global__ __launch_bounds__(kFusedWaves* kWave) void lora_fused_kernel(FusedArg
       }
       if (!TR && a.z && head)
         *reinterpret_cast<float4*>(a.z + (long)s_rows[row] * r + col) = make_float4(v[0], v[1], v[2], v[3]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] *= sc;
-      put_z<KS>(s_z, row, col, r, v);
-      if (TR && head) *reinterpret_cast<float4*>(s_p + row * kLd + col) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(s_z + row * Z::kLd + col) = make_float4(v[0] * sc, v[1] * sc, v[2] * sc, v[3] * sc);
     }
-    pad_z<KS, 16>(s_z, r);
-    if (TR && head) {
-      __syncthreads();
-      put_parts<16, kLd>(s_p, part, n, r, a.frag[0] + at);
-    }
+    __syncthreads();
+    cols.make_z(zf, s_z);
+    if (TR && head) put_parts<16, Z::kLd>(s_z, part, n, r, a.frag[0] + at);
     if (TR && tail) {
       __syncthreads();
       for (int i = threadIdx.x; i < n * quads; i += kThreads) {
         const int row = i / quads, col = i % quads * 4;
         const float4 f = *reinterpret_cast<const float4*>(a.fz + (long)s_rows[row] * r + col);
-        *reinterpret_cast<float4*>(s_p + row * kLd + col) = make_float4(f.x * sc, f.y * sc, f.z * sc, f.w * sc);
+        *reinterpret_cast<float4*>(s_z + row * Z::kLd + col) = make_float4(f.x * sc, f.y * sc, f.z * sc, f.w * sc);
       }
       __syncthreads();
-      put_parts<16, kLd>(s_p, part, n, r, a.frag[1] + at);
+      put_parts<16, Z::kLd>(s_z, part, n, r, a.frag[1] + at);
     }
   } else if (!TR && a.z && head) {
     for (int i = threadIdx.x; i < n * r; i += kThreads) a.z[(long)s_rows[i / r] * r + i % r] = 0.f;
   }
   __syncthreads();
   if (!live && a.c.base == a.c.y) return;  // rows without an adapter stay
-  cols.template run<kFusedWaves>(first, live, cg, g1, s_z);
+  cols.template run<kFusedWaves>(first, live, cg, g1, zf);
 }
 
 struct WgradArgs {
