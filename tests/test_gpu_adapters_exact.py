@@ -47,10 +47,10 @@ def _taker(G, C, r):
     return b
 
 
-# rows: 3 and 100 find their tiles by comparing, 300 and 1500 by counting, 2500 by a sort; up to
-# 1024 one launch where the rank is at most 64; 25 rows an adapter or few take 16 or 32 rows a
-# block in the second product, hundreds 64. Ranks: on both sides of 16 and of each 32
-@pytest.mark.parametrize("M,G", [(3, 2), (100, 3), (300, 5), (1500, 60), (1500, 2), (2500, 100), (2500, 3)])
+# rows: 3 and 100 find their tiles by comparing, 300 and 1500 by counting, 2500 and more by a sort;
+# up to 1024 one launch where the rank is at most 64; tiles of 64 rows from 3000 rows on. Ranks: on
+# both sides of 16 and of each 32
+@pytest.mark.parametrize("M,G", [(3, 2), (100, 3), (300, 5), (1500, 60), (1500, 2), (2500, 100), (3200, 3)])
 @pytest.mark.parametrize("r", [8, 16, 24, 32, 40, 64, 72, 96, 104, 128])
 def test_small_operand_keeps_its_bits(hm, M, G, r):
     """y = base + s B z and dx = dbase + s A^T dz with z and dz of 20 bits, of which the result

@@ -7,7 +7,7 @@
 // With ranks of 8 to 128 the products do r / 2 operations a byte of x and y, far below what
 // the matrix cores could do: the kernels are bound by reading x, base and the matrices in
 // use, and by writing y. So every product runs on bf16 MFMA from global memory into fragments,
-// rows of one adapter are gathered into tiles of 16, 32 or 64 (one read of its matrices each),
+// rows of one adapter are gathered into tiles of 16 to 64 (one read of its matrices each),
 // and the long axis K is split over waves and blocks when there are few tiles. z stays in fp32:
 // where z or dz is an MFMA operand it goes in as a sum of three bf16 parts, which hold its 24 bits.
 #include <algorithm>
@@ -128,7 +128,7 @@ __device__ __forceinline__ void turn_8x4(const uint32_t (&v)[8][2], u32x4 (&f)[4
 
 // Which rows a block works on: entry b % tiles of the tile table, and of a tile of more than RT
 // rows its part b / tiles. The table comes from a sort before the launch (kTable), or the first
-// launch does without one and leaves its tiles as the table for the second:
+// launch does without one and leaves its tiles, of RT rows, as the table for the second:
 // kRow   entry b is the tile that starts at row b, if the rows of the same adapter before b fill
 //        whole tiles; the entries of all other rows are idle.
 // kCount every block counts all ids by adapter and so finds tile b and its rows.
@@ -143,21 +143,20 @@ constexpr int kCountRows = 2048, kCountGroups = 256;  // of kCount, with the gro
 struct Tiles {
   const int32_t* ids;
   int M, G, tiles;
-  int entry;           // rows of a tile
   TileFind find;
   int32_t* sorted;     // rows by adapter (null: no table is kept)
   SortTile* table;
 };
 
 // false: no tile. Else *g (G: rows without an adapter), s_rows[0 .. *n), *index: the tile's
-// number; *n may be 0 for a tile's second part. s_rows past *n names row 0, so that whatever
+// number; *n may be 0 for a part behind the first. s_rows past *n names row 0, so that whatever
 // reads it stays inside the matrices.
 // ROWS: most rows of kCount, whose ids the block's THREADS hold in registers (0: only kTable).
 template <int RT, int ROWS, int THREADS>
 __device__ __forceinline__ bool find_tile(const Tiles& t, int* g, int* n, int* index, int32_t* s_rows) {
-  const int part = (int)blockIdx.x / t.tiles, e = (int)blockIdx.x - part * t.tiles;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid >> 6;
   if (ROWS == 0 || t.find == kTable) {
+    const int part = (int)blockIdx.x / t.tiles, e = (int)blockIdx.x - part * t.tiles;
     const SortTile d = t.table[e];  // an idle entry has no rows
     *g = d.group;
     *index = d.index;
@@ -168,6 +167,7 @@ __device__ __forceinline__ bool find_tile(const Tiles& t, int* g, int* n, int* i
   }
   if constexpr (ROWS > 0) {
     const bool put = t.sorted && blockIdx.y == 0;  // this block writes its entry
+    const int e = blockIdx.x;
     SortTile d{-1, 0, 0, 0};
     if (tid < RT) s_rows[tid] = 0;
     if (t.find == kRow) {
@@ -214,13 +214,12 @@ __device__ __forceinline__ bool find_tile(const Tiles& t, int* g, int* n, int* i
         }
       __syncthreads();
       // every wave for itself: tiles and rows up to each group (both below 2^16), in registers
-      const int h = t.entry;
       int upto[kRuns], all = 0;
 #pragma unroll
       for (int k = 0; k < kRuns; ++k)
         if (k * kWave < groups) {
           const int c = k * kWave + lane < groups ? s_cnt[k * kWave + lane] : 0;
-          int sum = (c + h - 1) / h << 16 | c;
+          int sum = (c + RT - 1) / RT << 16 | c;
 #pragma unroll
           for (int o = 1; o < kWave; o <<= 1) {
             const int u = __shfl_up(sum, o);
@@ -233,7 +232,7 @@ __device__ __forceinline__ bool find_tile(const Tiles& t, int* g, int* n, int* i
       const int total = all >> 16, per = (total + 7) / 8;
       const int tile = e / 8 < per ? (e & 7) * per + e / 8 : total;
       if (tile >= total) {
-        if (put && part == 0 && tid == 0) t.table[e] = d;
+        if (put && tid == 0) t.table[e] = d;
         return false;
       }
       int first = 0;  // the tile's first row in its group
@@ -244,8 +243,8 @@ __device__ __forceinline__ bool find_tile(const Tiles& t, int* g, int* n, int* i
           if (past) {
             const int l = __ffsll((unsigned long long)past) - 1, end = __shfl(upto[k], l);
             const int rows = s_cnt[k * kWave + l];
-            first = (tile - (end >> 16) + (rows + h - 1) / h) * h;
-            d = SortTile{k * kWave + l, (end & 0xffff) - rows + first, min(h, rows - first), tile};
+            first = (tile - (end >> 16) + (rows + RT - 1) / RT) * RT;
+            d = SortTile{k * kWave + l, (end & 0xffff) - rows + first, min(RT, rows - first), tile};
           }
         }
       int seen = 0;
@@ -254,24 +253,24 @@ __device__ __forceinline__ bool find_tile(const Tiles& t, int* g, int* n, int* i
         if (i < run) seen += __popcll(__ballot(id[i] == d.group));
       if (lane == 0) s_wave[wave] = seen;
       __syncthreads();
-      int rank = -(first + part * RT);  // of the group's next row, from this part's first
+      int rank = -first;  // of the group's next row, from this tile's first
       for (int w = 0; w < wave; ++w) rank += s_wave[w];
 #pragma unroll
       for (int i = 0; i < kIds; ++i)
         if (i < run) {
           const uint64_t same = __ballot(id[i] == d.group);
           const int at = rank + __popcll(same & ((1ull << lane) - 1ull));
-          if (id[i] == d.group && at >= 0 && at < min(RT, d.rows - part * RT)) s_rows[at] = w0 + i * kWave + lane;
+          if (id[i] == d.group && at >= 0 && at < d.rows) s_rows[at] = w0 + i * kWave + lane;
           rank += __popcll(same);
         }
     }
     *g = d.group;
     *index = d.index;
-    *n = max(0, min(RT, d.rows - part * RT));
+    *n = d.rows;
     __syncthreads();
     if (put) {
-      if (part == 0 && tid == 0) t.table[e] = d;
-      if (tid < *n) t.sorted[d.start + part * RT + tid] = s_rows[tid];
+      if (tid == 0) t.table[e] = d;
+      if (tid < d.rows) t.sorted[d.start + tid] = s_rows[tid];
     }
     return true;
   }
@@ -620,7 +619,7 @@ __global__ __launch_bounds__(kShrinkWaves* kWave) void lora_shrink_kernel(Shrink
   __shared__ int32_t s_rows[MT * 16];
   __shared__ __align__(16) float s_red[kShrinkWaves / 2][MT * NT * 256];
   int g, n, index;
-  if (!find_tile<MT * 16, kCountRows, kShrinkWaves * kWave>(a.tiles, &g, &n, &index, s_rows)) return;
+  if (!find_tile<MT * 16, MT == 1 ? kCountRows : 0, kShrinkWaves * kWave>(a.tiles, &g, &n, &index, s_rows)) return;
   if (g == a.tiles.G) return;
   const int steps = (a.K + kKStep - 1) / kKStep;
   shrink_tile<MT, NT, kShrinkWaves, (MT + NT <= 3 ? 2 : 1)>(a.x, a.xs, a.w + (long)g * a.r * a.K, a.K, a.r, n, s_rows,
@@ -1070,8 +1069,9 @@ __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) 
 
 namespace {
 
-constexpr int kFusedBytes = 512 << 10;  // largest first matrix of the one-launch form, half for few tiles
-constexpr int kFusedRank = 64;          // and its largest rank (registers)
+constexpr int kFusedRank = 64;          // largest rank of the one-launch form (registers)
+constexpr int kWideRows = 3000, kWideMean = 48;  // fewest rows, in all and an adapter, of tiles of 64
+static_assert(kWideRows > kCountRows && kWideRows > kFusedRows, "tiles past 16 rows come from the sort");
 constexpr int kShrinkBlocks = 400;      // about this many blocks of the first product
 
 struct Plan {
@@ -1087,17 +1087,27 @@ struct Plan {
 
 // K: the first product's reduction axis.
 //
-// One launch for few rows: us a call in one and in two launches (a launch costs the host 3 us
-// more), first matrix of 64 KiB (2048, rank 16), 256 KiB (2048, rank 64) and 512 KiB (4096, rank
-// 64): 6.8, 7.8; 10.2, 9.2; 9.7 in two at 1 row, 7.2, 8.4; 12.1, 11.8; 18.6, 16.5 at 64 rows of
-// 48 adapters, 12.6, 14.2; 17.5, 17.4; 22.5, 24.9 at 512 of 16. Its blocks repeat the first
-// product for their columns, and a few tiles have the most such blocks.
+// One launch for few rows. Us a call among others in one and in two launches (a launch costs the
+// host 3 us more), first matrix of 64 KiB (2048, rank 16), 256 KiB (2048, rank 64) and 512 KiB
+// (4096, rank 64): 8.9, 11.4; 10.9, 12.2; 14.2, 12.1 at 1 row, 8.6, 11.2; 12.5, 11.9; 18.9, 16.1
+// at 64 rows of 48 adapters, 9.0, 11.2; 13.4, 13.0; 17.6, 14.8 at 200 of 8, 9.3, 11.5; 14.4, 14.3;
+// 19.1, 21.6 at 512 of 16, 10.2, 13.2; 15.4, 17.4; 24.0, 25.3 at 1000 of 30; at 512 KiB 18.0, 16.5
+// at 256 of 16 and 18.7, 17.6 at 400 of 16; at 768 KiB 22.3, 22.5 at 512 of 16, 27.2, 26.8 at 1000
+// of 30. Backward, 192 KiB (1536, rank 64), 256 KiB (4096, rank 32) and 512 KiB: 22.8, 23.0; 22.8,
+// 21.2; 30.4, 27.1 at 1 row, 20.5, 21.2; 20.9, 19.9; 27.5, 24.2 at 64 of 4, 30.1, 32.0; 29.5, 29.0;
+// 40.1, 39.2 at 512 of 16, 28.8, 32.9; 34.0, 36.0; 47.2, 50.0 at 1000 of 4.
 //
-// Tile rows from the mean number of rows an adapter has: more rows share one read of the
-// adapter's matrices, fewer waste less where adapters have few rows. The backward pass takes
-// at least 32, the depth of its sums over rows. 4096 -> 4096, us a call with tiles of 16, 32 and
-// 64: 2048 rows of 128 adapters, rank 64: 58, 68, 58; 4000 of 64, rank 64: 72, 72, 65; 4000 of 8,
-// rank 64: 53, 59, 48, rank 16: 37, 40, 38; 2048 of 36, rank 16: 23, 24, 25.
+// Tiles of 64 share one read of an adapter's matrices among more rows, small ones (16; 32 in the
+// backward pass, the depth of its sums over rows) waste less where adapters have few and leave
+// more blocks. Us a call with tiles of 16 and 64, 4096 -> 4096, ranks 16, 64 and 128: 18.5, 19.5;
+// 24.9, 25.7; 33.4, 32.3 at 1500 rows of 4 adapters, 22.5, 23.6; 31.7, 32.1; 48.5, 50.0 at 2048 of
+// 20, 26.7, 27.5; 38.7, 36.0; 55.7, 56.9 at 2500 of 20, 31.0, 30.7; 48.2, 44.5; 67.9, 60.9 at 3000
+// of 20, 48.0, 47.5; 70.7, 63.9; 99.8, 91.9 at 4000 of 64, 37.4, 37.9; 52.0, 47.6; 68.6, 67.3 at
+// 4000 of 8; fewer than 48 rows an adapter: 21.5, 25.5; 34.6, 37.2; 55.4, 58.4 at 1500 of 50, 151,
+// 151; 229, 238; 347, 368 at 16000 of 400 (but 49, 54; 82, 74; 114, 104 at 4000 of 100). Tiles of
+// 32 lay above the better of both at all of these but 2048 of 20. Backward, 32 and 64: 35.3, 34.9;
+// 53.7, 57.2; 77.0, 81.6 at 1500 of 4, 40.6, 39.6; 70.9, 72.7; 100, 109 at 2048 of 20, 54.4, 53.6;
+// 87.8, 84.8; 129, 120 at 3000 of 20, 61.6, 58.7; 105, 92; 164, 149 at 4000 of 8.
 //
 // Past rank 64 the first product's 32 rows take all registers of a wave; blocks take 16 until
 // there are 200 of 32: 2048 rows of 4 adapters, rank 128, 4096 -> 4096: 39 and 49 us,
@@ -1106,11 +1116,10 @@ Plan plan_tiles(int M, int G, int K, int r, bool backward) {
   Plan p;
   const int mean = M / std::max(1, std::min(G, M));
   p.nt = rank_tiles(r);
-  p.fused = M <= kFusedRows && r <= kFusedRank &&
-            (long)r * K * 2 <= (M / 16 + std::min(G, M) >= 16 ? kFusedBytes : kFusedBytes / 2);
+  p.fused = M <= kFusedRows && r <= kFusedRank && (long)r * K * 2 <= (M >= 512 ? 512 : backward ? 192 : 256) << 10;
   p.find = backward || M > kCountRows || (M > kRowRows && G >= kCountGroups) ? kTable : M > kRowRows ? kCount : kRow;
-  p.wide = p.find != kRow && !p.fused && mean >= 48;
-  p.rt = p.wide ? 64 : backward ? 32 : p.find == kRow || p.fused || p.nt == 8 || mean < 24 ? 16 : 32;
+  p.wide = M >= kWideRows && mean >= kWideMean;
+  p.rt = p.wide ? 64 : backward ? 32 : 16;
   const int most = M / p.rt + std::min(G + 1, M);
   p.tiles = p.find == kRow ? M : (most + 7) / 8 * 8;  // entries are dealt out over 8 XCDs
   p.busy = std::max(1, std::min(most, M));
@@ -1161,7 +1170,7 @@ Space plan_space(int M, int G, int K, int N, int r, bool backward) {
 
 hipError_t make_tiles(const int32_t* ids, int M, int G, const Plan& p, const Space& sp, char* scratch,
                       Tiles* t, const SortTranspose& turn, hipStream_t s) {
-  *t = Tiles{ids, M, G, p.tiles, p.rt, p.find, nullptr, nullptr};
+  *t = Tiles{ids, M, G, p.tiles, p.find, nullptr, nullptr};
   if (p.find == kTable || !p.fused) {
     t->sorted = reinterpret_cast<int32_t*>(scratch + sp.sorted);
     t->table = reinterpret_cast<SortTile*>(scratch + sp.tile);
