@@ -398,8 +398,8 @@ hmoe_status moe_quantize_mxfp4(const float* in, int32_t rows, int32_t K, uint8_t
  *     kernels run, so calls that may overlap in time need scratch buffers of their own.
  *   - Results do not depend on timing: fixed-order sums, no floating-point atomics. */
 
-/* Bytes of scratch of moe_permute for M tokens (0 for few slots: scratch may then be NULL).
- * Host arithmetic only. Errors: as moe_permute. */
+/* Bytes of scratch of moe_permute for at most M tokens (0 for few slots: scratch may then be
+ * NULL). Host arithmetic only. Errors: as moe_permute. */
 hmoe_status moe_permute_scratch_bytes(int32_t M, int32_t k, int32_t E, size_t* bytes);
 
 /* Tokens into expert order. With slot s = t * k + j, the slots whose id lies in [0, E) are
@@ -455,7 +455,8 @@ hmoe_status moe_route_backward(const int32_t* topk_ids, const float* topk_w, con
                                int32_t M, int32_t E, int32_t k, float* dlogits,
                                hipStream_t stream);
 
-/* Bytes of scratch of moe_lora and moe_lora_backward (host arithmetic only).
+/* Bytes of scratch of moe_lora and moe_lora_backward (host arithmetic only): enough for any call
+ * of at most M rows with the same G, K, N and rank; it never shrinks as M grows.
  * Errors: as moe_lora. */
 hmoe_status moe_lora_scratch_bytes(int32_t M, int32_t G, int32_t K, int32_t N, int32_t rank,
                                    size_t* forward_bytes, size_t* backward_bytes);

@@ -101,3 +101,26 @@ def test_small_operand_at_the_end_of_fp32(hm, M, r):
     dx, dA, dB = torch.empty_like(x), torch.empty_like(a), torch.empty_like(b)
     hm.moe_lora_backward(dy, x, z, ids, a.to(bf), b.to(bf), one, None, dx, dA, dB, ws)
     assert bool((dB[0, :, 0] == 127.75).all()) and not dB[0, :, 1:].any()
+
+
+@pytest.mark.parametrize("r", [16, 64])
+def test_scratch_of_the_largest_batch(hm, r):
+    """One buffer, planned for 3200 rows, and every smaller number of rows on it."""
+    torch = torch_mod()
+    G, C, bf = 16, 4096, torch.bfloat16
+    f, b = hm.moe_lora_scratch_bytes(3200, G, C, C, r)
+    fws, bws = (torch.empty(n, dtype=torch.uint8, device="cuda") for n in (f, b))
+    reader, taker = (to_dev(v).to(bf) for v in (_reader(G, r, C), _taker(G, C, r)))
+    one = torch.ones(G, device="cuda")
+    for M in (1, 8, 15, 16, 100, 511, 512, 1024, 1025, 2048, 2049, 3199, 3200):
+        x, low, _ = _bits(M, C, r)
+        ids = np.random.default_rng(M).integers(0, G, M).astype(np.int32)
+        xd, idd = to_dev(x).to(bf), to_dev(ids)
+        y, dx, z = torch.empty_like(xd), torch.empty_like(xd), torch.empty(M, r, device="cuda")
+        dA, dB = torch.empty(G, r, C, device="cuda"), torch.empty(G, C, r, device="cuda")
+        fws.fill_(255), bws.fill_(255)
+        hm.moe_lora(xd, idd, reader, taker, one, None, y, z, fws)
+        hm.moe_lora_backward(xd, xd.clone(), z, idd, taker.transpose(1, 2).contiguous(),
+                             reader.transpose(1, 2).contiguous(), one, None, dx, dA, dB, bws)
+        for t in (y, dx):
+            np.testing.assert_array_equal(t.double().cpu().numpy(), np.repeat(low[:, None], C, 1), str(M))

@@ -538,7 +538,7 @@ def moe_route_backward(topk_ids, topk_w, dw, dlogits, stream=None) -> None:
 
 
 def moe_lora_scratch_bytes(M: int, num_adapters: int, K: int, N: int, rank: int) -> tuple:
-    """Scratch bytes of moe_lora and of moe_lora_backward."""
+    """Scratch bytes of moe_lora and of moe_lora_backward for any call of at most M rows."""
     f, b = c_size_t(), c_size_t()
     _check(load_library().moe_lora_scratch_bytes(M, num_adapters, K, N, rank, byref(f), byref(b)))
     return f.value, b.value

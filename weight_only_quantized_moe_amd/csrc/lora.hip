@@ -1070,6 +1070,7 @@ __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) 
 namespace {
 
 constexpr int kFusedRank = 64;          // largest rank of the one-launch form (registers)
+constexpr int kFusedMany = 512;         // rows from which on it takes a larger first matrix
 constexpr int kWideRows = 3000, kWideMean = 48;  // fewest rows, in all and an adapter, of tiles of 64
 static_assert(kWideRows > kCountRows && kWideRows > kFusedRows, "tiles past 16 rows come from the sort");
 constexpr int kShrinkBlocks = 400;      // about this many blocks of the first product
@@ -1084,6 +1085,12 @@ struct Plan {
   int tiles;       // most tiles
   int busy;        // how many of them can have rows
 };
+
+bool finds_by_table(int M, int G, bool backward) {
+  return backward || M > kCountRows || (M > kRowRows && G >= kCountGroups);
+}
+// largest first matrix of the one-launch form
+int fused_bytes(int M, bool backward) { return (M >= kFusedMany ? 512 : backward ? 192 : 256) << 10; }
 
 // K: the first product's reduction axis.
 //
@@ -1105,7 +1112,8 @@ struct Plan {
 // of 20, 48.0, 47.5; 70.7, 63.9; 99.8, 91.9 at 4000 of 64, 37.4, 37.9; 52.0, 47.6; 68.6, 67.3 at
 // 4000 of 8; fewer than 48 rows an adapter: 21.5, 25.5; 34.6, 37.2; 55.4, 58.4 at 1500 of 50, 151,
 // 151; 229, 238; 347, 368 at 16000 of 400 (but 49, 54; 82, 74; 114, 104 at 4000 of 100). Tiles of
-// 32 lay above the better of both at all of these but 2048 of 20. Backward, 32 and 64: 35.3, 34.9;
+// 32 lay above the better of the two at 2048 of 20, 4000 of 64, 8 and 100, 1500 of 50 and 16000 of
+// 400. Backward, 32 and 64: 35.3, 34.9;
 // 53.7, 57.2; 77.0, 81.6 at 1500 of 4, 40.6, 39.6; 70.9, 72.7; 100, 109 at 2048 of 20, 54.4, 53.6;
 // 87.8, 84.8; 129, 120 at 3000 of 20, 61.6, 58.7; 105, 92; 164, 149 at 4000 of 8.
 //
@@ -1116,8 +1124,8 @@ Plan plan_tiles(int M, int G, int K, int r, bool backward) {
   Plan p;
   const int mean = M / std::max(1, std::min(G, M));
   p.nt = rank_tiles(r);
-  p.fused = M <= kFusedRows && r <= kFusedRank && (long)r * K * 2 <= (M >= 512 ? 512 : backward ? 192 : 256) << 10;
-  p.find = backward || M > kCountRows || (M > kRowRows && G >= kCountGroups) ? kTable : M > kRowRows ? kCount : kRow;
+  p.fused = M <= kFusedRows && r <= kFusedRank && (long)r * K * 2 <= fused_bytes(M, backward);
+  p.find = finds_by_table(M, G, backward) ? kTable : M > kRowRows ? kCount : kRow;
   p.wide = M >= kWideRows && mean >= kWideMean;
   p.rt = p.wide ? 64 : backward ? 32 : 16;
   const int most = M / p.rt + std::min(G + 1, M);
@@ -1129,10 +1137,13 @@ Plan plan_tiles(int M, int G, int K, int r, bool backward) {
 
 // Splits of the reduction axis: enough blocks to fill the card, at least one step for each
 // wave of a block, at most 16 partial sums to add up again.
-int plan_splits(const Plan& p, int K) {
+int most_splits(int K) {
   const int steps = (K + kKStep - 1) / kKStep;
+  return std::min((steps + kShrinkWaves - 1) / kShrinkWaves, 16);
+}
+int plan_splits(const Plan& p, int K) {
   const int blocks = p.busy * (p.rt / (p.mt * 16));
-  return std::max(1, std::min({(kShrinkBlocks + blocks - 1) / blocks, (steps + kShrinkWaves - 1) / kShrinkWaves, 16}));
+  return std::min((kShrinkBlocks + blocks - 1) / blocks, most_splits(K));
 }
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -1166,6 +1177,43 @@ Space plan_space(int M, int G, int K, int N, int r, bool backward) {
   }
   s.total = at;
   return s;
+}
+
+// Bytes that hold the space of every call of at most M rows, so that a buffer made for the largest
+// batch serves the smaller ones. The plans of fewer rows may take more of an array (other tiles,
+// more splits, two launches), so each array gets a bound that only grows with M:
+// splits     at most 16 and what K has; more than one only while blocks are few: there are at least
+//            M / 32 of them, so splits * M < kShrinkBlocks * 32 + M
+// entries    M / rt + the adapters, rt >= 16; kRow: one a row
+// fragments  32-row steps: entries at rt = 32; twice the entries of 64 rows hold them too
+size_t most_space(int M, int G, int K, int N, int r, bool backward) {
+  const long axis = backward ? N : K, matrix = axis * r * 2, adapters = std::min(G + 1, M);
+  // the most rows of a call in two launches, and of one that finds its tiles by comparing rows
+  long two = M;
+  if (r <= kFusedRank && M <= kFusedRows && matrix <= fused_bytes(kFusedMany, backward))
+    two = matrix <= fused_bytes(1, backward) ? 0 : std::min(M, kFusedMany - 1);
+  const long rows = backward ? 0 : std::min(two, (long)kRowRows);
+  const bool table = finds_by_table(M, G, backward);
+  auto entries = [&](int rt) { return (M / rt + adapters + 7) / 8 * 8; };
+  size_t total = 0;
+  auto add = [&](size_t bytes) { total += align256(bytes); };
+  if (table || two) {
+    add(std::max({rows * 16, two, table ? (long)M : 0}) * 4);
+    add(std::max(rows, entries(backward ? 32 : 16)) * sizeof(SortTile));
+  }
+  if (table) {
+    add((size_t)(G + 2) * 4);
+    add(sort_count_words(M, G + 1) * 4);
+    add((size_t)(G + 2) * 4);
+  }
+  add((size_t)std::min(two * most_splits(axis), two ? kShrinkBlocks * 32 + two : 0) * r * 4);
+  if (backward) {
+    const bool wide = M >= kWideRows && M / std::max(1, std::min(G, M)) >= kWideMean;
+    const size_t steps = wide ? 2 * entries(64) : entries(32);
+    for (int i = 0; i < 2; ++i) add(steps * 3 * rank_tiles(r) * 1024);
+    add((size_t)G * r * N * 2);
+  }
+  return total;
 }
 
 hipError_t make_tiles(const int32_t* ids, int M, int G, const Plan& p, const Space& sp, char* scratch,
@@ -1260,8 +1308,8 @@ hipError_t fused(const Plan& p, FusedArgs a, hipStream_t s) {
 }  // namespace
 
 void lora_scratch(int M, int G, int K, int N, int r, size_t* forward, size_t* backward) {
-  if (forward) *forward = plan_space(M, G, K, N, r, false).total;
-  if (backward) *backward = plan_space(M, G, K, N, r, true).total;
+  if (forward) *forward = most_space(M, G, K, N, r, false);
+  if (backward) *backward = most_space(M, G, K, N, r, true);
 }
 
 hipError_t launch_lora(const Lora& l, void* scratch, hipStream_t s) {
