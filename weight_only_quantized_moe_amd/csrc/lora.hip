@@ -1117,9 +1117,10 @@ int fused_bytes(int M, bool backward) { return (M >= kFusedMany ? 512 : backward
 // 53.7, 57.2; 77.0, 81.6 at 1500 of 4, 40.6, 39.6; 70.9, 72.7; 100, 109 at 2048 of 20, 54.4, 53.6;
 // 87.8, 84.8; 129, 120 at 3000 of 20, 61.6, 58.7; 105, 92; 164, 149 at 4000 of 8.
 //
-// Past rank 64 the first product's 32 rows take all registers of a wave; blocks take 16 until
-// there are 200 of 32: 2048 rows of 4 adapters, rank 128, 4096 -> 4096: 39 and 49 us,
-// 16000 of 100: 237 and 208.
+// Past rank 64 the first product's 32 rows take all registers of a wave; its blocks take 16 until
+// there are 140 of 32. Us a call with 16 and 32, rank 128, 4096 -> 4096: 61.4, 64.3 at 3000 rows of
+// 20 adapters, 66.9, 65.7 at 4000 of 8, 166, 153 at 8000 of 100; backward 109, 114 at 2048 of 4,
+// 119, 122 at 3000 of 20, 148, 146 at 4000 of 8, 422, 406 at 8000 of 100.
 Plan plan_tiles(int M, int G, int K, int r, bool backward) {
   Plan p;
   const int mean = M / std::max(1, std::min(G, M));
@@ -1131,7 +1132,7 @@ Plan plan_tiles(int M, int G, int K, int r, bool backward) {
   const int most = M / p.rt + std::min(G + 1, M);
   p.tiles = p.find == kRow ? M : (most + 7) / 8 * 8;  // entries are dealt out over 8 XCDs
   p.busy = std::max(1, std::min(most, M));
-  p.mt = p.rt == 16 || (p.nt == 8 && (long)p.busy * p.rt < 200 * 32) ? 1 : 2;
+  p.mt = p.rt == 16 || (p.nt == 8 && (long)p.busy * p.rt < 140 * 32) ? 1 : 2;
   return p;
 }
 
