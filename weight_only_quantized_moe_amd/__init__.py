@@ -366,21 +366,20 @@ _functions = {}
 def _load_torch():
     global _torch, _I32, _F32, _this_device, _raw_stream
     import torch
+    _I32, _F32 = torch.int32, torch.float32
+    _this_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
     # int16 holds bf16 bits, as for the layer
     _CODES.update({torch.bfloat16: DTYPE_BF16, torch.int16: DTYPE_BF16, torch.float16: DTYPE_FP16,
                    torch.float32: DTYPE_FP32})
-    _I32, _F32 = torch.int32, torch.float32
-    _this_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
-    _torch = torch
+    _torch = torch  # last: a thread that finds it set finds the rest
 
 
 def _dtype_code(t) -> int:
     """Element type of a rows tensor."""
+    if _torch is None:
+        _load_torch()
     code = _CODES.get(t.dtype)
     if code is None:
-        if _torch is None:
-            _load_torch()
-            return _dtype_code(t)
         raise ValueError(f"rows of {t.dtype}: expected bfloat16 (or its bits as int16), float16 "
                          "or float32")
     return code
