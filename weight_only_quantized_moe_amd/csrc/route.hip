@@ -88,9 +88,10 @@ hipError_t launch_route_group(const Layer& L, const float* logits, int M, void* 
 // dl[e_j] = w_j (dw_j - sum_i w_i dw_i) and every other logit's gradient is zero. Bound by
 // the M * E * 4 bytes it writes. A wave takes four tokens, 16 lanes a token, so one load
 // each brings their ids, weights and gradients; it then builds 256 logits a token at a time
-// in LDS (zeros, the slots' values added in slot order) and writes them as 16 bytes a lane:
-// no fill before, no scatter to memory, no order to depend on. 16384 tokens, 256 experts (18
-// MB): 7.7 us, 2.4 TB/s, of which a launch is about 2; 8 tokens 2.2 us.
+// in LDS (zeros, then the ids' values; the slots of one id are added up in registers, in slot
+// order, and its first one writes) and writes them as 16 bytes a lane: no fill before, no scatter
+// to memory, no order to depend on. 16384 tokens, 256 experts (18 MB): 7.7 us, 2.4 TB/s, of
+// which a launch is about 2; 8 tokens 2.2 us.
 struct __attribute__((packed, aligned(4))) F32x4 {
   float v[4];
 };
@@ -101,6 +102,23 @@ constexpr int kBwdTokens = 4, kBwdCols = 256;
 __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
+}
+
+// sum of the slots I .. k - 1 of the token that have this lane's id (a row of 16 lanes holds a
+// token's slots); a lane with such a slot before its own does not write
+template <int I>
+__device__ __forceinline__ void add_slots(int id, float g, int j, int k, bool& writes, float& sum) {
+  if constexpr (I < kMaxTopK) {
+    if (I >= k) return;
+    constexpr int kLane = 0x150 + I;  // lane I of each row
+    const int other = __builtin_amdgcn_update_dpp(0, id, kLane, 0xF, 0xF, true);
+    const float v = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(g), kLane, 0xF, 0xF, true));
+    if (other == id) {
+      sum += v;
+      writes = writes && I >= j;
+    }
+    add_slots<I + 1>(id, g, j, k, writes, sum);
+  }
 }
 
 __global__ __launch_bounds__(kRouteWaves * kWave) void route_bwd_kernel(
@@ -116,15 +134,16 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_bwd_kernel(
   const int id = in ? ids[at] : -1;
   const float wj = in ? w[at] : 0.f, dj = in ? dw[at] : 0.f;
   const float g = wj * (dj - group_sum<16>(wj * dj));
+  bool writes = (unsigned)id < (unsigned)E;
+  float sum = 0.f;
+  add_slots<0>(id, g, j, k, writes, sum);
   float(*row)[kBwdCols] = s_row[wave];
   for (int e0 = 0; e0 < E; e0 += kBwdCols) {
 #pragma unroll
     for (int t = 0; t < kBwdTokens; ++t)
       *reinterpret_cast<float4*>(&row[t][lane * 4]) = make_float4(0.f, 0.f, 0.f, 0.f);
     wave_fence();
-    const bool here = (unsigned)id < (unsigned)E && id >= e0 && id < e0 + kBwdCols;
-    for (int i = 0; i < k; ++i)   // LDS operations of a wave keep their order
-      if (here && j == i) atomicAdd(&row[mine][id - e0], g);
+    if (writes && id >= e0 && id < e0 + kBwdCols) row[mine][id - e0] = sum;
     wave_fence();
     const int e = e0 + lane * 4;
 #pragma unroll
