@@ -488,7 +488,10 @@ hmoe_status moe_lora(const uint16_t* x, int64_t x_stride, const int32_t* ids, co
  * over the rows of g. dbase [M, K] is the shared projection's own gradient with respect to
  * x: NULL counts as zeros, and it may be dx itself (same stride). dA fp32 [G, rank, K] and
  * dB fp32 [G, N, rank] are fully overwritten (zeros for an adapter without rows, so also at
- * M = 0). The gradient with respect to base is dy itself.
+ * M = 0). The gradient with respect to base is dy itself. The weight gradients take finite x, dy
+ * and z: where the formula has an infinity they have an infinity or NaN. It stays in its adapter,
+ * that of an x in its column of dA and that of a dy in its column of dB, dA and the row of dx; rows
+ * without an adapter may hold anything.
  * Errors: as moe_lora. */
 hmoe_status moe_lora_backward(const uint16_t* dy, int64_t dy_stride, const uint16_t* x,
                               int64_t x_stride, const float* z, const int32_t* ids,

@@ -124,3 +124,43 @@ def test_scratch_of_the_largest_batch(hm, r):
                              reader.transpose(1, 2).contiguous(), one, None, dx, dA, dB, bws)
         for t in (y, dx):
             np.testing.assert_array_equal(t.double().cpu().numpy(), np.repeat(low[:, None], C, 1), str(M))
+
+
+@pytest.mark.parametrize("M,r", [(40, 8), (40, 64), (700, 24), (3200, 16), (3200, 128)])
+@pytest.mark.parametrize("bad", ["inf", "nan"])
+def test_non_finite_values_stay_in_their_adapter(hm, M, r, bad):
+    """One infinite x reaches its adapter's column of dA, one infinite dy its adapter's column of
+    dB, its dA and its row of dx; every other value keeps its bits."""
+    torch = torch_mod()
+    G, K, N, bf = 3, 136, 200, torch.bfloat16
+    g = torch.Generator().manual_seed(M + r)
+    n = lambda *s: torch.randn(*s, generator=g).cuda()  # noqa: E731
+    x, dy, A, B = n(M, K).to(bf), n(M, N).to(bf), n(G, r, K).to(bf), n(G, N, r).to(bf)
+    z, scale = n(M, r), n(G)
+    ids = torch.randint(-1, G, (M,), generator=g, dtype=torch.int32)
+    ids[7] = 1
+    at = 7
+    if M > 40:
+        at = int((ids == 1).nonzero()[-1])               # the adapter's last row, which fills its last step
+    ids = ids.cuda()
+    ws = torch.empty(hm.moe_lora_scratch_bytes(M, G, K, N, r)[1], dtype=torch.uint8, device="cuda")
+
+    def run(x, dy):
+        out = (torch.empty(M, K, dtype=bf, device="cuda"), torch.empty(G, r, K, device="cuda"),
+               torch.empty(G, N, r, device="cuda"))
+        hm.moe_lora_backward(dy, x, z, ids, A, B, scale, None, *out, ws)
+        return out
+    dx, dA, dB = run(x, dy)
+    xb = x.clone()
+    xb[at, 33] = float(bad)
+    dx1, dA1, dB1 = run(xb, dy)
+    assert torch.equal(dx1, dx) and torch.equal(dB1, dB)
+    assert not dA1[1, :, 33].isfinite().any()
+    dA1[1, :, 33] = dA[1, :, 33]
+    assert torch.equal(dA1, dA)
+    db = dy.clone()
+    db[at, 77] = float(bad)
+    dx2, dA2, dB2 = run(x, db)
+    assert not dB2[1, 77].isfinite().any() and not dx2[at].isfinite().any() and not dA2[1].isfinite().any()
+    dB2[1, 77], dx2[at], dA2[1] = dB[1, 77], dx[at], dA[1]
+    assert torch.equal(dx2, dx) and torch.equal(dA2, dA) and torch.equal(dB2, dB)
