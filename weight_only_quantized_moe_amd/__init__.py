@@ -12,6 +12,7 @@ Build the library with ``python -m weight_only_quantized_moe_amd.build``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from ctypes import (POINTER, Structure, byref, c_char_p, c_int32, c_int64, c_size_t,
@@ -95,6 +96,10 @@ def load_library() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with "
                           "`python -m weight_only_quantized_moe_amd.build`")
+    # torch's HIP runtime first: the library then takes it. Loaded before torch, the library would
+    # bring the system's, and of two runtimes in one process the library's finds no device.
+    with contextlib.suppress(ImportError):
+        import torch  # noqa: F401
     lib = ctypes.CDLL(LIB_PATH)
     st = c_int32
     lib.moe_layer_create.argtypes = [POINTER(LayerDesc), POINTER(c_void_p)]
