@@ -392,8 +392,8 @@ hmoe_status moe_quantize_mxfp4(const float* in, int32_t rows, int32_t K, uint8_t
  *   - Matrices of rows have a row stride in elements (>= the row's length; the last axis is
  *     contiguous) and need only element alignment; every other pointer 16 bytes.
  *   - Index and weight arrays (topk_ids, topk_w, slot_row, ...) are contiguous.
- *   - Outputs must not overlap inputs or each other, except where said (an output matrix that
- *     starts where an input matrix does is refused: HMOE_ERR_INVALID_ARG).
+ *   - Outputs must not overlap inputs or each other, except where said (an output that starts
+ *     where an input or another output does is refused: HMOE_ERR_INVALID_ARG).
  *   - No call keeps anything between calls: scratch contents matter only while the call's
  *     kernels run, so calls that may overlap in time need scratch buffers of their own.
  *   - Results do not depend on timing: fixed-order sums, no floating-point atomics. */

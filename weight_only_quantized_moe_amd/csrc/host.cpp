@@ -173,10 +173,22 @@ hmoe_status check_arrays(const char* names, std::initializer_list<const void*> p
   return HMOE_OK;
 }
 
-// an output that starts where an input does would be overwritten while it is read
-hmoe_status check_apart(const char* name, const void* out, std::initializer_list<const void*> ins) {
-  for (const void* p : ins)
-    if (p == out) return fail(HMOE_ERR_INVALID_ARG, std::string(name) + " is one of the inputs");
+// An output that starts where an input or another output does would be written while that is read
+// or written. `also`: an input of which this holds for this output, while another may be it.
+struct Output {
+  const char* name;
+  const void* p;
+  const void* also = nullptr;
+};
+hmoe_status check_apart(std::initializer_list<const void*> ins, std::initializer_list<Output> outs) {
+  for (const Output* o = outs.begin(); o != outs.end(); ++o) {
+    if (!o->p) continue;
+    bool in = o->p == o->also;
+    for (const void* p : ins) in = in || p == o->p;
+    if (in) return fail(HMOE_ERR_INVALID_ARG, std::string(o->name) + " starts where an input does");
+    for (const Output* q = outs.begin(); q != o; ++q)
+      if (q->p == o->p) return fail(HMOE_ERR_INVALID_ARG, std::string(o->name) + " starts where " + q->name + " does");
+  }
   return HMOE_OK;
 }
 
@@ -642,11 +654,13 @@ hmoe_status moe_permute(const void* x, int64_t x_stride, const int32_t* topk_ids
   if (M > 0) {
     if (hmoe_status st = check_matrix("x", x, x_stride, H, es)) return st;
     if (hmoe_status st = check_matrix("rows", rows, rows_stride, H, es)) return st;
-    if (hmoe_status st = check_apart("rows", rows, {x})) return st;
     if (hmoe_status st = check_arrays("topk_ids, sorted_slots and slot_row",
                                       {topk_ids, sorted_slots, slot_row}))
       return st;
     if (hmoe_status st = check_op_scratch(scratch, scratch_bytes, permute_scratch(M, k, E))) return st;
+    if (hmoe_status st = check_apart({x, topk_ids}, {{"rows", rows}, {"sorted_slots", sorted_slots},
+                                                     {"slot_row", slot_row}, {"expert_off", expert_off}}))
+      return st;
   }
   const hmoe::PermuteRows p{x, x_stride, rows, rows_stride, slot_row, M, k, H, dtype, es};
   hipError_t err = hmoe::launch_permute(p, topk_ids, E, sorted_slots, expert_off,
@@ -664,8 +678,8 @@ hmoe_status moe_permute_backward(const void* drows, int64_t drows_stride, const 
   const int es = element_size(dtype);
   if (hmoe_status st = check_matrix("drows", drows, drows_stride, H, es)) return st;
   if (hmoe_status st = check_matrix("dx", dx, dx_stride, H, es)) return st;
-  if (hmoe_status st = check_apart("dx", dx, {drows})) return st;
   if (hmoe_status st = check_arrays("slot_row", {slot_row})) return st;
+  if (hmoe_status st = check_apart({drows, slot_row}, {{"dx", dx}})) return st;
   const hmoe::PermuteRows p{drows, drows_stride, dx, dx_stride, slot_row, M, k, H, dtype, es};
   hipError_t err = hmoe::launch_combine(p, nullptr, stream);
   if (err != hipSuccess) return hip_fail(err, "permute backward launch");
@@ -681,8 +695,8 @@ hmoe_status moe_unpermute(const void* rows, int64_t rows_stride, const int32_t* 
   const int es = element_size(dtype);
   if (hmoe_status st = check_matrix("rows", rows, rows_stride, H, es)) return st;
   if (hmoe_status st = check_matrix("y", y, y_stride, H, es)) return st;
-  if (hmoe_status st = check_apart("y", y, {rows})) return st;
   if (hmoe_status st = check_arrays("slot_row and topk_w", {slot_row, topk_w})) return st;
+  if (hmoe_status st = check_apart({rows, slot_row, topk_w}, {{"y", y}})) return st;
   const hmoe::PermuteRows p{rows, rows_stride, y, y_stride, slot_row, M, k, H, dtype, es};
   hipError_t err = hmoe::launch_combine(p, topk_w, stream);
   if (err != hipSuccess) return hip_fail(err, "unpermute launch");
@@ -701,8 +715,8 @@ hmoe_status moe_unpermute_backward(const void* dy, int64_t dy_stride, const void
   if (hmoe_status st = check_matrix("dy", dy, dy_stride, H, es)) return st;
   if (hmoe_status st = check_matrix("rows", rows, rows_stride, H, es)) return st;
   if (hmoe_status st = check_matrix("drows", drows, drows_stride, H, es)) return st;
-  if (hmoe_status st = check_apart("drows", drows, {dy, rows})) return st;
   if (hmoe_status st = check_arrays("slot_row, topk_w and dw", {slot_row, topk_w, dw})) return st;
+  if (hmoe_status st = check_apart({dy, rows, slot_row, topk_w}, {{"drows", drows}, {"dw", dw}})) return st;
   const hmoe::PermuteRows p{dy, dy_stride, drows, drows_stride, slot_row, M, k, H, dtype, es};
   hipError_t err = hmoe::launch_unpermute_bwd(p, rows, rows_stride, topk_w, dw, stream);
   if (err != hipSuccess) return hip_fail(err, "unpermute backward launch");
@@ -719,6 +733,7 @@ hmoe_status moe_route_backward(const int32_t* topk_ids, const float* topk_w, con
   if (M == 0) return HMOE_OK;
   if (hmoe_status st = check_arrays("topk_ids, topk_w, dw and dlogits", {topk_ids, topk_w, dw, dlogits}))
     return st;
+  if (hmoe_status st = check_apart({topk_ids, topk_w, dw}, {{"dlogits", dlogits}})) return st;
   hipError_t err = hmoe::launch_route_backward(topk_ids, topk_w, dw, M, E, k, dlogits, stream);
   if (err != hipSuccess) return hip_fail(err, "route backward launch");
   return HMOE_OK;
@@ -742,12 +757,12 @@ hmoe_status moe_lora(const uint16_t* x, int64_t x_stride, const int32_t* ids, co
   if (hmoe_status st = check_matrix("x", x, x_stride, K, 2)) return st;
   if (hmoe_status st = check_matrix("y", y, y_stride, N, 2)) return st;
   if (hmoe_status st = check_base("base", base, base_stride, y, y_stride, N)) return st;
-  if (hmoe_status st = check_apart("y", y, {x})) return st;
   if (hmoe_status st = check_arrays("ids, A, B and scale", {ids, A, B, scale})) return st;
   if (!aligned(z, 16)) return fail(HMOE_ERR_ALIGN, "z must be 16-byte aligned");
   size_t need;
   hmoe::lora_scratch(M, G, K, N, rank, &need, nullptr);
   if (hmoe_status st = check_op_scratch(scratch, scratch_bytes, need)) return st;
+  if (hmoe_status st = check_apart({x, ids, A, B, scale}, {{"y", y}, {"z", z, base}})) return st;
   const hmoe::Lora p{x, x_stride, ids, A, B, scale, M, G, K, N, rank, base, base_stride, y, y_stride, z};
   hipError_t err = hmoe::launch_lora(p, scratch, stream);
   if (err != hipSuccess) return hip_fail(err, "adapter launch");
@@ -768,12 +783,13 @@ hmoe_status moe_lora_backward(const uint16_t* dy, int64_t dy_stride, const uint1
     if (hmoe_status st = check_matrix("x", x, x_stride, K, 2)) return st;
     if (hmoe_status st = check_matrix("dx", dx, dx_stride, K, 2)) return st;
     if (hmoe_status st = check_base("dbase", dbase, dbase_stride, dx, dx_stride, K)) return st;
-    if (hmoe_status st = check_apart("dx", dx, {dy, x})) return st;
     if (hmoe_status st = check_arrays("ids and z", {ids, z})) return st;
   }
   size_t need;
   hmoe::lora_scratch(M, G, K, N, rank, nullptr, &need);
   if (hmoe_status st = check_op_scratch(scratch, scratch_bytes, need)) return st;
+  if (hmoe_status st = check_apart({dy, x, z, ids, A, B, scale}, {{"dx", dx}, {"dA", dA, dbase}, {"dB", dB, dbase}}))
+    return st;
   const hmoe::LoraGrad p{dy, dy_stride, x, x_stride, z, ids, A, B, scale, M, G, K, N, rank,
                          dbase, dbase_stride, dx, dx_stride, dA, dB};
   hipError_t err = hmoe::launch_lora_backward(p, scratch, stream);
