@@ -470,8 +470,8 @@ hmoe_status moe_lora_scratch_bytes(int32_t M, int32_t G, int32_t K, int32_t N, i
  * base and y [M, N], A [G, rank, K], B [G, N, rank] (an adapter of lower rank is padded with
  * zeros), scale fp32 [G]. z fp32 [M, rank] is what moe_lora_backward needs and may be NULL.
  * A and B must be finite (an infinite entry gives infinities or NaN in the rows that use it).
- * M = 0 is a no-op. It takes one to three launches, at most two for up to 128 rows and for up
- * to 2048 rows of at most 255 adapters.
+ * M = 0 is a no-op. It takes one to four launches: at most two for up to 128 rows and for up
+ * to 2048 rows of at most 255 adapters, at most three for up to 8192 rows.
  * Errors: HMOE_ERR_INVALID_ARG (M < 0; G, K, N or rank < 1; a stride below the row's length;
  * base == y with another stride); HMOE_ERR_UNSUPPORTED (K, N or rank not a multiple of 8,
  * rank > 128, G > HMOE_MAX_GROUPS, M > 2^22, K or N > 2^20); HMOE_ERR_SCRATCH; HMOE_ERR_ALIGN;
@@ -491,7 +491,8 @@ hmoe_status moe_lora(const uint16_t* x, int64_t x_stride, const int32_t* ids, co
  * M = 0). The gradient with respect to base is dy itself. The weight gradients take finite x, dy
  * and z: where the formula has an infinity they have an infinity or NaN. It stays in its adapter,
  * that of an x in its column of dA and that of a dy in its column of dB, dA and the row of dx; rows
- * without an adapter may hold anything.
+ * without an adapter may hold anything. It takes two to five launches, at most four for up to 8192
+ * rows.
  * Errors: as moe_lora. */
 hmoe_status moe_lora_backward(const uint16_t* dy, int64_t dy_stride, const uint16_t* x,
                               int64_t x_stride, const float* z, const int32_t* ids,
