@@ -58,8 +58,8 @@ __device__ __forceinline__ void split_parts(float a, float b, uint32_t (&part)[3
 }
 
 // Kernel arguments into scalar registers here. The compiler would read them where they are
-// first used, behind the wait for a tile's rows and in the loops after it: the backward pass's
-// second product of 4001 rows, rank 16, took 26.5 us so, and 24.0 with its arguments read ahead
+// first used, behind the wait for a tile's rows and in the loops after it: the backward pass of
+// 4001 rows, rank 16, takes 69.0 us so, and 66.8 with its second product's arguments read ahead
 // (the other kernels gain nothing).
 template <typename... T>
 __device__ __forceinline__ void read_ahead(const T&... v) {
@@ -132,10 +132,10 @@ __device__ __forceinline__ void turn_8x4(const uint32_t (&v)[8][2], u32x4 (&f)[4
 // kRow   entry b is the tile that starts at row b, if the rows of the same adapter before b fill
 //        whole tiles; the entries of all other rows are idle.
 // kCount every block counts all ids by adapter and so finds tile b and its rows.
-// Rank 16, us a call, kRow and kCount: 6.9 and 8.6 (1 row, 2048 -> 1536 columns), 7.4 and 9.1
-// (64), 8.4 and 9.0 (200), 13.7 and 10.8 (200 rows, 4096 -> 4096), and kCount would take 16 more
-// to look through the counts of 2000 adapters. kCount and kTable: 8.7 and 12.2 (257 rows of 4
-// adapters, 2048 -> 1536), 10.2 and 13.7 (1000 of 30), 18.2 and 19.9 (2000 of 100), 26.0 and
+// Rank 16, us of the card, kRow and kCount: 7.1 and 8.3 (1 row, 2048 -> 1536 columns), 7.5 and 8.7
+// (64), 8.5 and 8.7 (200), 13.6 and 10.5 (200 rows, 4096 -> 4096), and kCount would take 16 more
+// to look through the counts of 2000 adapters. kCount and kTable: 8.9 and 12.3 (257 rows of 4
+// adapters, 2048 -> 1536), 10.1 and 14.7 (1000 of 30), 18.4 and 19.9 (2000 of 100), 26.0 and
 // 25.6 (4000 of 64).
 enum TileFind { kTable, kRow, kCount };
 constexpr int kRowRows = 128;                         // most rows of kRow
@@ -288,8 +288,8 @@ __device__ __forceinline__ void shrink_tile(const uint16_t* x, long xs, const ui
                                             int r, int n, const int32_t* s_rows, int s0, int s1,
                                             float (*s_red)[MT * NT * 256]) {
   // A scalar wave number takes addresses out of the lanes' registers, but loops of few loads then
-  // wait for each: 16 rows of rank 64 win 4% (15.3 to 14.7 us at 1000 rows of 30 adapters, 2048 ->
-  // 1536), one row of rank 16 loses half (10 to 21 us, 6144 -> 4096), 32 rows change by 4% either way.
+  // wait for each: 16 rows of rank 64 win a little (35.3 to 34.4 us at 1500 rows of 50 adapters,
+  // 4096 -> 4096), one row of rank 16 loses half (10 to 20 us, 6144 -> 4096), 32 rows lose 1%.
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = MT == 1 && NT == 4 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : (int)(threadIdx.x >> 6);
   const int c = lane & 15, q = lane >> 4, at = q * 32 + (c & 3) * 8;
@@ -612,7 +612,7 @@ constexpr int kShrinkWaves = 4;
 
 // part[s][m] = W_g x[m] over split s of K. Bound by the way of x from HBM and of W from L2 into
 // the registers, which the few steps of a wave hide only in part: 4096 rows of 8 adapters, rank
-// 64, K = 6144: 22.8 us (50 MB of x, 2.2 TB/s; 17 with W held in L1, 13 with x there, 9 with both).
+// 64, K = 6144: 22.4 us (50 MB of x, 2.2 TB/s; 17 with W held in L1, 13 with x there, 9 with both).
 // Tiles of 64 rows a block, which halve W's way, were no faster.
 template <int MT, int NT>
 __global__ __launch_bounds__(kShrinkWaves* kWave) void lora_shrink_kernel(ShrinkArgs a) {
@@ -701,8 +701,8 @@ struct ExpandLds {
 // turns a part of W's fragments and puts it into LDS for all, which cuts W's way from L2 to a
 // quarter. In the backward pass (TR) the first block of a tile also leaves scale dz as
 // fragments for the weight gradients, the last one scale z. Bound by base and y in HBM behind
-// the chain table, z's splits, columns: 4096 rows, rank 64, N = 4096: 24.9 us (67 MB, 2.7 TB/s;
-// 37 with RW = 1); backward, 4001 rows, rank 16, K = 6144: 24.0 us (98 MB, 4.1 TB/s; 34).
+// the chain table, z's splits, columns: 4096 rows, rank 64, N = 4096: 25.4 us (67 MB, 2.6 TB/s;
+// 37 with RW = 1); backward, 4001 rows, rank 16, K = 6144: 24.2 us (98 MB, 4.1 TB/s; 35).
 template <int RW, int KS, bool TR>
 __global__ __launch_bounds__(kExpandWaves* kWave, (KS <= 2 ? (RW == 1 && KS + TR < 2 ? 4 : 3) : 2))
 void lora_expand_kernel(ExpandArgs a) {
@@ -852,8 +852,8 @@ constexpr int kFusedRows = 1024;  // most rows of the one-launch form
 // leaves LDS, then they split the block's columns. Blocks of one tile that take different
 // columns repeat the first product (its matrix comes from L2 again). TR: the backward pass, as
 // in the second product alone. Bound by latency: find the tile, load, multiply, add up, load,
-// multiply, write. 1 row, 2048 -> 1536, rank 16: 6.8 us; 64 rows of 48 adapters, 6144 -> 4096:
-// 11.5 us (13 MB).
+// multiply, write. 1 row, 2048 -> 1536, rank 16: 7.0 us; 64 rows of 48 adapters, 6144 -> 4096:
+// 11.7 us (13 MB).
 template <int NT, int KS, bool TR>
 __global__ __launch_bounds__(kFusedWaves* kWave) void lora_fused_kernel(FusedArgs a) {
   using Z = ZShape<KS>;
@@ -946,7 +946,7 @@ constexpr int kWgradRows = 2048;  // row indices kept in LDS at a time
 // writes its registers. Rows past the group's end are zeros of P. Ranks past
 // NT * 16 go to further blocks (grid z). Bound by the rows (each read once) at low ranks, by the
 // way of P's parts from L2 at high ones: 4001 rows of 4 adapters, 6144 and 4096 columns, rank
-// 16: 23.7 us (82 MB, 3.5 TB/s).
+// 16: 23.8 us (82 MB, 3.4 TB/s).
 template <int NT, int SHARE>
 __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) {
   __shared__ float s_red[SHARE > 1 ? kWgradWaves : 1][16][68];
