@@ -517,31 +517,51 @@ struct Columns {
     }
   }
 
-  // fragments of z for all rank steps: 8 ranks of row c in three bf16 parts (zeros past r)
+  // word d of a rank step's fragments of z: two ranks of row c in three bf16 parts (zeros past r)
+  __device__ __forceinline__ void split_z(uint32_t (&f)[Z::kParts], const float* s_z, int ks, int d) const {
+    const int ch = (ks * 4 + q) * 8;
+    const float2 v = *reinterpret_cast<const float2*>(s_z + c * Z::kLd + chunk(ks, q) + 2 * d);
+    uint32_t part[3];
+    split_parts(v.x, v.y, part);
+    if constexpr (Z::kPack) {  // [first, second], [third, zeros]
+      f[0] = ch < a.r ? part[0] : ch < 2 * a.r ? part[1] : 0u;
+      f[1] = ch < a.r ? part[2] : 0u;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 3; ++k) f[k] = ch < a.r ? part[k] : 0u;
+    }
+  }
+
+  // fragments of z for all rank steps, by each wave for its own 16 rows
   __device__ __forceinline__ void make_z(u32x4 (&zf)[Z::kSteps][Z::kParts], const float* s_z) const {
 #pragma unroll
-    for (int ks = 0; ks < Z::kSteps; ++ks) {
-      const int ch = (ks * 4 + q) * 8;
-      const float* z = s_z + c * Z::kLd + chunk(ks, q);
-      float v[8];
-#pragma unroll
-      for (int e = 0; e < 8; e += 4) {
-        const float4 f = *reinterpret_cast<const float4*>(z + e);
-        v[e] = f.x, v[e + 1] = f.y, v[e + 2] = f.z, v[e + 3] = f.w;
-      }
+    for (int ks = 0; ks < Z::kSteps; ++ks)
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
-        uint32_t part[3];
-        split_parts(v[2 * d], v[2 * d + 1], part);
-        if constexpr (Z::kPack) {  // [first, second], [third, zeros]
-          zf[ks][0][d] = ch < a.r ? part[0] : ch < 2 * a.r ? part[1] : 0u;
-          zf[ks][1][d] = ch < a.r ? part[2] : 0u;
-        } else {
+        uint32_t f[Z::kParts];
+        split_z(f, s_z, ks, d);
 #pragma unroll
-          for (int k = 0; k < 3; ++k) zf[ks][k][d] = ch < a.r ? part[k] : 0u;
-        }
+        for (int k = 0; k < Z::kParts; ++k) zf[ks][k][d] = f[k];
       }
+  }
+
+  // the same for a block whose W waves have the same 16 rows: each makes a part for all (1000 rows
+  // of 30 adapters, 2048 -> 1536, rank 64: 15.1 us, 15.5 with every wave for itself)
+  template <int W>
+  __device__ __forceinline__ void share_z(u32x4 (&zf)[Z::kSteps][Z::kParts], const float* s_z,
+                                          uint32_t (*s_zf)[Z::kParts][kWave][4]) const {
+    const int lane = threadIdx.x & (kWave - 1);
+    for (int i = threadIdx.x >> 6; i < Z::kSteps * 4; i += W) {
+      uint32_t f[Z::kParts];
+      split_z(f, s_z, i >> 2, i & 3);
+#pragma unroll
+      for (int k = 0; k < Z::kParts; ++k) s_zf[i >> 2][k][lane][i & 3] = f[k];
     }
+    __syncthreads();
+#pragma unroll
+    for (int ks = 0; ks < Z::kSteps; ++ks)
+#pragma unroll
+      for (int k = 0; k < Z::kParts; ++k) zf[ks][k] = *reinterpret_cast<const u32x4*>(s_zf[ks][k][lane]);
   }
 
   // y = base + acc (rows without an adapter: y = base)
@@ -696,7 +716,7 @@ struct ExpandLds {
 };
 
 // y = base + W_g (scale z): z's splits are added in order, scaled and put into LDS, from where
-// every lane makes the fragments that it keeps for the block's columns. RW = 1: 16 rows a block, each wave has columns of
+// the fragments are made that a lane keeps for the block's columns. RW = 1: 16 rows a block, each wave has columns of
 // its own. RW = 4: 64 rows, a wave 16 of them; the waves share each group of columns, and each
 // turns a part of W's fragments and puts it into LDS for all, which cuts W's way from L2 to a
 // quarter. In the backward pass (TR) the first block of a tile also leaves scale dz as
@@ -711,6 +731,7 @@ void lora_expand_kernel(ExpandArgs a) {
   constexpr int RT = RW * 16, kThreads = kExpandWaves * kWave;
   __shared__ int32_t s_rows[RT];
   __shared__ __align__(16) char s_shared[L::kShared];
+  __shared__ __align__(16) uint32_t s_zf[RW == 1 ? Z::kSteps : 1][Z::kParts][RW == 1 ? kWave : 1][4];
   float* s_z = reinterpret_cast<float*>(s_shared);
   u32x4* s_w = reinterpret_cast<u32x4*>(s_shared);
   read_ahead(a.part, a.splits, a.scale, a.z, a.col_groups, a.c.w, a.c.base, a.c.bs, a.c.y, a.c.ys);
@@ -767,7 +788,8 @@ void lora_expand_kernel(ExpandArgs a) {
       *reinterpret_cast<float4*>(s_z + row * Z::kLd + col) = make_float4(v[0] * sc, v[1] * sc, v[2] * sc, v[3] * sc);
     }
     __syncthreads();
-    cols.make_z(zf, s_z + mine * Z::kLd);
+    if constexpr (RW == 1) cols.template share_z<kExpandWaves>(zf, s_z, s_zf);
+    else cols.make_z(zf, s_z + mine * Z::kLd);
     if constexpr (TR) {
       const int pt = (int)blockIdx.x / a.tiles.tiles;
       const long at = (long)index * a.steps_per_tile * 3 * rank_tiles(r) * 512;
@@ -861,6 +883,7 @@ __global__ __launch_bounds__(kFusedWaves* kWave) void lora_fused_kernel(FusedArg
   __shared__ int32_t s_rows[16];
   __shared__ __align__(16) float s_red[kFusedWaves / 2][NT * 256];
   __shared__ __align__(16) float s_z[16 * Z::kLd];
+  __shared__ __align__(16) uint32_t s_zf[Z::kSteps][Z::kParts][kWave][4];
   int g, n, index;
   if (!find_tile<16, TR ? 0 : kFusedRows, kThreads>(a.tiles, &g, &n, &index, s_rows)) return;
   const bool live = g != a.tiles.G, head = blockIdx.y == 0, tail = blockIdx.y == gridDim.y - 1;
@@ -898,7 +921,7 @@ __global__ __launch_bounds__(kFusedWaves* kWave) void lora_fused_kernel(FusedArg
       *reinterpret_cast<float4*>(s_z + row * Z::kLd + col) = make_float4(v[0] * sc, v[1] * sc, v[2] * sc, v[3] * sc);
     }
     __syncthreads();
-    cols.make_z(zf, s_z);
+    cols.template share_z<kFusedWaves>(zf, s_z, s_zf);
     if (TR && head) put_parts<16, Z::kLd>(s_z, part, n, r, a.frag[0] + at);
     if (TR && tail) {
       __syncthreads();
