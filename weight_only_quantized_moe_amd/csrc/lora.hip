@@ -1332,8 +1332,11 @@ hipError_t fused(const Plan& p, FusedArgs a, hipStream_t s) {
 }  // namespace
 
 void lora_scratch(int M, int G, int K, int N, int r, size_t* forward, size_t* backward) {
-  if (forward) *forward = most_space(M, G, K, N, r, false);
-  if (backward) *backward = most_space(M, G, K, N, r, true);
+  // the bound holds the plan of M rows; were it ever short of it, a call would still not be let in
+  // with less than its own layout
+  auto bytes = [&](bool b) { return std::max(plan_space(M, G, K, N, r, b).total, most_space(M, G, K, N, r, b)); };
+  if (forward) *forward = bytes(false);
+  if (backward) *backward = bytes(true);
 }
 
 hipError_t launch_lora(const Lora& l, void* scratch, hipStream_t s) {
