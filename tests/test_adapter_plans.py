@@ -24,7 +24,7 @@ def test_scratch_never_shrinks_over_all_sizes():
         G, rank = int(2 ** r.uniform(0, 11)), 8 * int(r.integers(1, 17))
         K, N = (8 * int(2 ** r.uniform(0, 12)) for _ in range(2))
         rows = np.unique(np.concatenate([(2 ** r.uniform(0, 22, 60)).astype(np.int64), np.arange(18),
-                                         [127, 128, 129, 511, 512, 1024, 1025, 2048, 2049, 2999, 3000, 8192, 8193]]))
+                                         [127, 128, 129, 511, 512, 799, 800, 1024, 1025, 2048, 2049, 2999, 3000, 8192, 8193]]))
         _never_shrinks(rows, G, K, N, rank)
 
 

@@ -1093,8 +1093,8 @@ __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) 
 namespace {
 
 constexpr int kFusedRank = 64;          // largest rank of the one-launch form (registers)
-constexpr int kFusedMany = 512;         // rows from which on it takes a larger first matrix
-constexpr int kWideRows = 3000, kWideMean = 48;  // fewest rows, in all and an adapter, of tiles of 64
+constexpr int kFusedMany = 800;         // rows from which on it takes a larger first matrix
+constexpr int kWideRows = 3000, kWideMean = 60;  // fewest rows, in all and an adapter, of tiles of 64
 static_assert(kWideRows > kCountRows && kWideRows > kFusedRows, "tiles past 16 rows come from the sort");
 constexpr int kShrinkBlocks = 400;      // about this many blocks of the first product
 
@@ -1113,32 +1113,35 @@ bool finds_by_table(int M, int G, bool backward) {
   return backward || M > kCountRows || (M > kRowRows && G >= kCountGroups);
 }
 // largest first matrix of the one-launch form
-int fused_bytes(int M, bool backward) { return (M >= kFusedMany ? 512 : backward ? 192 : 256) << 10; }
+int fused_bytes(int M, bool backward) { return (backward ? 192 : M >= kFusedMany ? 512 : 256) << 10; }
 
 // K: the first product's reduction axis.
 //
 // One launch for few rows. Us a call among others in one and in two launches (a launch costs the
 // host 3 us more), first matrix of 64 KiB (2048, rank 16), 256 KiB (2048, rank 64) and 512 KiB
-// (4096, rank 64): 8.9, 11.4; 10.9, 12.2; 14.2, 12.1 at 1 row, 8.6, 11.2; 12.5, 11.9; 18.9, 16.1
-// at 64 rows of 48 adapters, 9.0, 11.2; 13.4, 13.0; 17.6, 14.8 at 200 of 8, 9.3, 11.5; 14.4, 14.3;
-// 19.1, 21.6 at 512 of 16, 10.2, 13.2; 15.4, 17.4; 24.0, 25.3 at 1000 of 30; at 512 KiB 18.0, 16.5
-// at 256 of 16 and 18.7, 17.6 at 400 of 16; at 768 KiB 22.3, 22.5 at 512 of 16, 27.2, 26.8 at 1000
-// of 30. Backward, 192 KiB (1536, rank 64), 256 KiB (4096, rank 32) and 512 KiB: 22.8, 23.0; 22.8,
-// 21.2; 30.4, 27.1 at 1 row, 20.5, 21.2; 20.9, 19.9; 27.5, 24.2 at 64 of 4, 30.1, 32.0; 29.5, 29.0;
-// 40.1, 39.2 at 512 of 16, 28.8, 32.9; 34.0, 36.0; 47.2, 50.0 at 1000 of 4.
+// (4096, rank 64): 9.0, 11.8; 10.6, 12.0; 13.9, 12.0 at 1 row, 8.8, 11.5; 12.4, 11.7; 18.4, 16.2
+// at 64 rows of 48 adapters, 8.9, 12.2; 12.8, 12.1; 17.2, 13.5 at 200 of 8, 9.0, 11.8; 13.9, 13.3;
+// 18.7, 17.5 at 512 of 16, 9.8, 12.8; 14.9, 17.2; 23.6, 24.5 at 1000 of 30; 256 KiB: 14.2, 14.8 at
+// 200 of 60, 15.2, 17.3 at 512 of 60; 512 KiB: 25.1, 27.7 at 512 of 60, 18.6, 17.5 at 700 of 4,
+// 19.4, 19.1 at 850 of 4, 22.7, 23.3 at 850 of 16; 768 KiB: 21.9, 19.3 at 512 of 16, 26.8, 26.9 at
+// 1000 of 30. Backward, 192 KiB (1536, rank 64), 256 KiB (4096, rank 32) and 512 KiB: 22.3, 22.2;
+// 22.5, 21.1; 30.0, 26.7 at 1 row, 20.4, 20.8; 21.2, 19.9; 27.2, 24.1 at 64 of 4, 29.9, 31.8; 29.6,
+// 29.0; 39.9, 39.1 at 512 of 16, 33.6, 35.3; 33.6, 35.2; 51.6, 50.8 at 1024 of 16, 53.4, 51.5;
+// 64.7, 58.4; 103, 94 at 1024 of 60.
 //
 // Tiles of 64 share one read of an adapter's matrices among more rows, small ones (16; 32 in the
 // backward pass, the depth of its sums over rows) waste less where adapters have few and leave
 // more blocks. Us a call with tiles of 16 and 64, 4096 -> 4096, ranks 16, 64 and 128: 18.5, 19.5;
 // 24.9, 25.7; 33.4, 32.3 at 1500 rows of 4 adapters, 22.5, 23.6; 31.7, 32.1; 48.5, 50.0 at 2048 of
-// 20, 26.7, 27.5; 38.7, 36.0; 55.7, 56.9 at 2500 of 20, 31.0, 30.7; 48.2, 44.5; 67.9, 60.9 at 3000
-// of 20, 48.0, 47.5; 70.7, 63.9; 99.8, 91.9 at 4000 of 64, 37.4, 37.9; 52.0, 47.6; 68.6, 67.3 at
-// 4000 of 8; fewer than 48 rows an adapter: 21.5, 25.5; 34.6, 37.2; 55.4, 58.4 at 1500 of 50, 151,
-// 151; 229, 238; 347, 368 at 16000 of 400 (but 49, 54; 82, 74; 114, 104 at 4000 of 100). Tiles of
+// 20, 26.5, 27.3; 38.6, 36.4; 55.5, 57.1 at 2500 of 20, 28.6, 30.5; 48.2, 44.0; 67.2, 60.5 at 3000
+// of 20, 47.8, 47.5; 70.9, 63.3; 98.2, 93.0 at 4000 of 64, 37.4, 38.8; 52.3, 47.4; 68.2, 65.4 at
+// 4000 of 8; rank 16 alone: 66.6, 65.1 at 8000 of 8, 97.9, 85.5 at 12000 of 60. Fewer than 60 rows
+// an adapter: 33.1, 38.0 at 3000 of 60, 21.5, 25.5; 34.6, 37.2; 55.4, 58.4 at 1500 of 50, 149, 152;
+// 227, 236; 345, 374 at 16000 of 400 (but 49, 55; 81, 75; 114, 105 at 4000 of 100). Tiles of
 // 32 lay above the better of the two at 2048 of 20, 4000 of 64, 8 and 100, 1500 of 50 and 16000 of
-// 400. Backward, 32 and 64: 35.3, 34.9;
-// 53.7, 57.2; 77.0, 81.6 at 1500 of 4, 40.6, 39.6; 70.9, 72.7; 100, 109 at 2048 of 20, 54.4, 53.6;
-// 87.8, 84.8; 129, 120 at 3000 of 20, 61.6, 58.7; 105, 92; 164, 149 at 4000 of 8.
+// 400. Backward, 32 and 64: 35.1, 34.8; 53.4, 57.0; 75.7, 81.2 at 1500 of 4, 40.8, 40.0; 71.4,
+// 72.9; 99, 108 at 2048 of 20, 54.7, 54.0; 87.4, 85.3; 128, 119 at 3000 of 20, 61.4, 58.6; 105, 92;
+// 163, 146 at 4000 of 8.
 //
 // Past rank 64 the first product's 32 rows take all registers of a wave; its blocks take 16 until
 // there are 140 of 32. Us a call with 16 and 32, rank 128, 4096 -> 4096: 61.4, 64.3 at 3000 rows of
