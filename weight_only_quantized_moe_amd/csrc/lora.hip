@@ -722,7 +722,7 @@ struct ExpandLds {
 // quarter. In the backward pass (TR) the first block of a tile also leaves scale dz as
 // fragments for the weight gradients, the last one scale z. Bound by base and y in HBM behind
 // the chain table, z's splits, columns: 4096 rows, rank 64, N = 4096: 25.4 us (67 MB, 2.6 TB/s;
-// 37 with RW = 1); backward, 4001 rows, rank 16, K = 6144: 24.2 us (98 MB, 4.1 TB/s; 35).
+// 37 with RW = 1); backward, 4001 rows, rank 16, K = 6144: 24.3 us (98 MB, 4.0 TB/s; 35).
 template <int RW, int KS, bool TR>
 __global__ __launch_bounds__(kExpandWaves* kWave, (KS <= 2 ? (RW == 1 && KS + TR < 2 ? 4 : 3) : 2))
 void lora_expand_kernel(ExpandArgs a) {
@@ -874,8 +874,8 @@ constexpr int kFusedRows = 1024;  // most rows of the one-launch form
 // leaves LDS, then they split the block's columns. Blocks of one tile that take different
 // columns repeat the first product (its matrix comes from L2 again). TR: the backward pass, as
 // in the second product alone. Bound by latency: find the tile, load, multiply, add up, load,
-// multiply, write. 1 row, 2048 -> 1536, rank 16: 7.0 us; 64 rows of 48 adapters, 6144 -> 4096:
-// 11.7 us (13 MB).
+// multiply, write. 1 row, 2048 -> 1536, rank 16: 6.9 us; 64 rows of 48 adapters, 6144 -> 4096:
+// 11.5 us (13 MB).
 template <int NT, int KS, bool TR>
 __global__ __launch_bounds__(kFusedWaves* kWave) void lora_fused_kernel(FusedArgs a) {
   using Z = ZShape<KS>;
@@ -969,7 +969,7 @@ constexpr int kWgradRows = 2048;  // row indices kept in LDS at a time
 // writes its registers. Rows past the group's end are zeros of P. Ranks past
 // NT * 16 go to further blocks (grid z). Bound by the rows (each read once) at low ranks, by the
 // way of P's parts from L2 at high ones: 4001 rows of 4 adapters, 6144 and 4096 columns, rank
-// 16: 23.8 us (82 MB, 3.4 TB/s).
+// 16: 23.9 us (82 MB, 3.4 TB/s).
 template <int NT, int SHARE>
 __global__ __launch_bounds__(kWgradThreads) void lora_wgrad_kernel(WgradArgs a) {
   __shared__ float s_red[SHARE > 1 ? kWgradWaves : 1][16][68];
