@@ -72,11 +72,17 @@ enum { HMOE_TENSOR_W13 = 0, HMOE_TENSOR_W2 = 1 };
 /* Stages of the forward, in launch order (see hybrid_moe_forward_stage). */
 enum { HMOE_STAGE_ROUTE = 0, HMOE_STAGE_W13 = 1, HMOE_STAGE_W2 = 2, HMOE_STAGE_COMBINE = 3 };
 
+/* Formats of a packed matrix (hmoe_packed). */
+enum { HMOE_WEIGHT_NVFP4 = 0, HMOE_WEIGHT_MXFP4 = 1, HMOE_WEIGHT_INT4 = 2 };
+
 /* Largest M served by the decode path (M <= 8, [P1] "How it works"). */
 #define HMOE_DECODE_MAX_M 8
 
 /* Most adapters of one moe_lora call (one per request, or one per request and expert). */
 #define HMOE_MAX_GROUPS 2048
+
+/* Most tokens of one moe_tokens call. */
+#define HMOE_TOKENS_MAX_M 16
 
 /* Layer descriptor, read once by moe_layer_create ([P2]: tier assignment comes
  * from the bit map; [P1]: scratch sizing from the maximum batched tokens).
@@ -501,6 +507,93 @@ hmoe_status moe_lora_backward(const uint16_t* dy, int64_t dy_stride, const uint1
                               const uint16_t* dbase, int64_t dbase_stride, uint16_t* dx,
                               int64_t dx_stride, float* dA, float* dB, void* scratch,
                               size_t scratch_bytes, hipStream_t stream);
+
+/* ---- matrices of 4-bit weights with group scales -----------------------------------
+ *
+ * The dense projections beside the experts (shared expert, attention, output head) in the
+ * kept tier's formats or in INT4, and a whole layer for a few tokens. The rules of the
+ * operators around the experts hold here too. Rows of activations are bf16 or fp16. */
+
+/* A packed matrix W [N, K] (device pointers, 16-byte aligned, owned by the caller, only
+ * read), or several of one shape behind one another (the experts of a layer):
+ *   q       u8 [N, K/2], element 2j in the low nibble of byte j
+ *   NVFP4   W = e2m1(q) * e4m3(s) * g: s u8 [N, K/16], g f32 [1] ([number of matrices])
+ *   MXFP4   W = e2m1(q) * 2^(s - 127): s u8 [N, K/32]; 255 is NaN
+ *   INT4    W = (q - z) * s: s of the activations' type [N, K/group], z u8 [N, K/group] (its low
+ *           four bits count) or NULL: 8 everywhere; group 32, 64 or 128
+ * K is a multiple of 32 and of the group. group is read for INT4 only, z for INT4 only, g for
+ * NVFP4 only. */
+typedef struct hmoe_packed {
+    int32_t format;
+    int32_t group;
+    const uint8_t* q;
+    const void* s;
+    const uint8_t* z;
+    const float* g;
+} hmoe_packed;
+
+/* Bytes of scratch of moe_linear and moe_linear_backward (host arithmetic only): enough for any
+ * call of at most M rows with the same K and N, whatever the format and type.
+ * Errors: as moe_linear. */
+hmoe_status moe_linear_scratch_bytes(int32_t M, int32_t K, int32_t N, size_t* forward_bytes,
+                                     size_t* backward_bytes);
+
+/* y[m] = base[m] + W x[m], summed in fp32 and rounded once: x [M, K], base and y [M, N]. A NULL
+ * base counts as zeros, base may be y itself (same stride), and a base stride of 0 gives every
+ * row the same base (a bias). Up to 64 rows the packed weights go into the matrix cores as exact
+ * numbers, in one launch without scratch; beyond, they are laid out as fp16 in scratch, in slabs
+ * of 64 MiB (exact for NVFP4; MXFP4 exact down to 2^-26 of the row's largest scale; INT4 rounded
+ * to fp16, 2^-11 of each weight). INT4: an infinity in x[m] gives NaN or infinities in y[m]; other
+ * rows are not touched. M = 0 is a no-op.
+ * Errors: HMOE_ERR_INVALID_ARG (w NULL; an unknown format, group or dtype; M < 0; K or N < 1; a
+ * stride below the row's length; base == y with another stride); HMOE_ERR_UNSUPPORTED (K not a
+ * multiple of 32 and of the group; M > 2^22, K or N > 2^20); HMOE_ERR_SCRATCH; HMOE_ERR_ALIGN;
+ * HMOE_ERR_HIP. */
+hmoe_status moe_linear(const void* x, int64_t x_stride, const hmoe_packed* w, int32_t M, int32_t K,
+                       int32_t N, int32_t dtype, const void* base, int64_t base_stride, void* y,
+                       int64_t y_stride, void* scratch, size_t scratch_bytes, hipStream_t stream);
+
+/* Gradient of moe_linear with respect to x: dx[m] = dbase[m] + W^T dy[m], dy [M, N], dbase and dx
+ * [M, K]; the weights are frozen, and the gradient with respect to base is dy itself. dbase as
+ * base above. M = 0 is a no-op. Errors: as moe_linear. */
+hmoe_status moe_linear_backward(const void* dy, int64_t dy_stride, const hmoe_packed* w, int32_t M,
+                                int32_t K, int32_t N, int32_t dtype, const void* dbase,
+                                int64_t dbase_stride, void* dx, int64_t dx_stride, void* scratch,
+                                size_t scratch_bytes, hipStream_t stream);
+
+/* A layer for a few tokens, from the tokens to its output. Experts: w13 holds E matrices [2I, H]
+ * (gate rows, then up rows), w2 E matrices [H, I], one format and group for both. The shared
+ * expert, if shared_inter = S > 0: shared_w13 [2S, H] and shared_w2 [H, S] in the same format,
+ * and shared_gate [H] or NULL. router [E, H] and shared_gate have the activations' type. */
+typedef struct hmoe_tokens {
+    int32_t num_experts, hidden, inter, top_k, shared_inter;
+    int32_t dtype;
+    const void* router;
+    const void* shared_gate;
+    hmoe_packed w13, w2, shared_w13, shared_w2;
+} hmoe_tokens;
+
+/* Bytes of scratch of moe_tokens: enough for any call of at most M tokens (host arithmetic only).
+ * Errors: as moe_tokens. */
+hmoe_status moe_tokens_scratch_bytes(int32_t M, int32_t E, int32_t H, int32_t I, int32_t k,
+                                     int32_t shared_inter, size_t* bytes);
+
+/* For M <= HMOE_TOKENS_MAX_M tokens x [M, H]:
+ *   l = router x;  the k largest by moe_route's rule, weights p their softmax;
+ *   y = base + sum over j of p_j W2_e (silu(Wg_e x) * (Wu_e x)) + sigmoid(shared_gate . x) * the
+ *       shared expert's (weight 1 without a gate)
+ * in fp32, rounded once; h goes into the second product with 16 of its bits. base [M, H] as in
+ * moe_linear. topk_ids int32 [M, k] and topk_w fp32 [M, k] receive the routing, each may be NULL.
+ * An expert that several tokens took is read once. Three launches. M = 0 is a no-op.
+ * Errors: HMOE_ERR_INVALID_ARG (layer NULL; M < 0; E outside 1..1024; k outside 1..min(16, E); H
+ * or I < 1, S < 0; an unknown format, group or dtype, matrices of different formats; strides as
+ * in moe_linear); HMOE_ERR_UNSUPPORTED (H, I or S not a multiple of 32 and of the group; H, I or S
+ * > 2^20); HMOE_ERR_CAPACITY (M > HMOE_TOKENS_MAX_M); HMOE_ERR_SCRATCH; HMOE_ERR_ALIGN;
+ * HMOE_ERR_HIP. */
+hmoe_status moe_tokens(const hmoe_tokens* layer, const void* x, int64_t x_stride, int32_t M,
+                       const void* base, int64_t base_stride, void* y, int64_t y_stride,
+                       int32_t* topk_ids, float* topk_w, void* scratch, size_t scratch_bytes,
+                       hipStream_t stream);
 
 /* Static string naming a status code. */
 const char* moe_status_string(hmoe_status status);

@@ -27,7 +27,9 @@ DTYPE_BF16, DTYPE_FP16, DTYPE_FP32 = 0, 1, 2
 TIER_KEPT, TIER_NF3 = 0, 1
 TENSOR_W13, TENSOR_W2 = 0, 1
 STAGE_ROUTE, STAGE_W13, STAGE_W2, STAGE_COMBINE = 0, 1, 2, 3
+WEIGHT_NVFP4, WEIGHT_MXFP4, WEIGHT_INT4 = 0, 1, 2
 DECODE_MAX_M = 8
+TOKENS_MAX_M = 16
 MAX_GROUPS = 2048
 
 EXPORTED = (
@@ -39,6 +41,8 @@ EXPORTED = (
     "moe_permute_scratch_bytes", "moe_permute", "moe_permute_backward", "moe_unpermute",
     "moe_unpermute_backward", "moe_route_backward",
     "moe_lora_scratch_bytes", "moe_lora", "moe_lora_backward",
+    "moe_linear_scratch_bytes", "moe_linear", "moe_linear_backward",
+    "moe_tokens_scratch_bytes", "moe_tokens",
     "moe_status_string", "moe_last_error",
 )
 
@@ -83,6 +87,18 @@ class DecodeView(Structure):
     _fields_ = [("counts", c_void_p), ("experts", c_void_p), ("num_slots", c_void_p),
                 ("slots", c_void_p), ("expert_tier", c_void_p), ("passes", c_void_p),
                 ("max_distinct", c_int32), ("sync_timeouts", c_void_p)]
+
+
+class Packed(Structure):
+    _fields_ = [("format", c_int32), ("group", c_int32), ("q", c_void_p), ("s", c_void_p),
+                ("z", c_void_p), ("g", c_void_p)]
+
+
+class TokensDesc(Structure):
+    _fields_ = [*((n, c_int32) for n in ("num_experts", "hidden", "inter", "top_k", "shared_inter",
+                                         "dtype")),
+                ("router", c_void_p), ("shared_gate", c_void_p),
+                *((n, Packed) for n in ("w13", "w2", "shared_w13", "shared_w2"))]
 
 
 _lib = None
@@ -149,6 +165,11 @@ def load_library() -> ctypes.CDLL:
         "moe_lora_scratch_bytes": [I, I, I, I, I, POINTER(c_size_t), POINTER(c_size_t)],
         "moe_lora": [P, L, P, P, P, P, I, I, I, I, I, P, L, P, L, P, P, c_size_t, P],
         "moe_lora_backward": [P, L, P, L, P, P, P, P, P, I, I, I, I, I, P, L, P, L, P, P, P, c_size_t, P],
+        "moe_linear_scratch_bytes": [I, I, I, POINTER(c_size_t), POINTER(c_size_t)],
+        "moe_linear": [P, L, P, I, I, I, I, P, L, P, L, P, c_size_t, P],
+        "moe_linear_backward": [P, L, P, I, I, I, I, P, L, P, L, P, c_size_t, P],
+        "moe_tokens_scratch_bytes": [I, I, I, I, I, I, POINTER(c_size_t)],
+        "moe_tokens": [P, P, L, I, P, L, P, L, P, P, P, c_size_t, P],
     }.items():
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = st
@@ -595,6 +616,155 @@ def moe_lora_backward(dy, x, z, ids, A, B, scale, dbase, dx, dA, dB, scratch=Non
             dy.data_ptr(), ys, x.data_ptr(), xs, z.data_ptr(), ids.data_ptr(), A.data_ptr(),
             B.data_ptr(), scale.data_ptr(), M, G, K, N, r, _at(dbase), bs, dx.data_ptr(), ds,
             dA.data_ptr(), dB.data_ptr(), ws, nbytes)
+
+
+# ---- matrices of 4-bit weights with group scales ---------------------------------------
+
+class PackedMatrix:
+    """A matrix of 4-bit weights on the GPU, [N, K] or several of them [E, N, K]; keeps its tensors.
+
+    q u8 [..., N, K/2]; s: NVFP4 u8 (or float8_e4m3fn) [..., N, K/16], MXFP4 u8 [..., N, K/32], INT4
+    bfloat16 or float16 [..., N, K/group]; z (INT4) u8 of s's shape or None; g (NVFP4) f32 with one
+    value per matrix (see include/hmoe.h)."""
+
+    def __init__(self, format: int, q, s, z=None, g=None, group: int = 0):
+        if _torch is None:
+            _load_torch()
+        torch = _torch
+        if format not in (WEIGHT_NVFP4, WEIGHT_MXFP4, WEIGHT_INT4):
+            raise ValueError(f"unknown format {format}")
+        if q.dim() not in (2, 3):
+            raise ValueError(f"q is {tuple(q.shape)}, expected [N, K/2] or [E, N, K/2]")
+        if format == WEIGHT_INT4 and group not in (32, 64, 128):
+            raise ValueError("group must be 32, 64 or 128")
+        self.group = {WEIGHT_NVFP4: 16, WEIGHT_MXFP4: 32}.get(format, group)
+        self.format, self.lead = format, tuple(q.shape[:-2])
+        self.rows, self.cols = q.shape[-2], 2 * q.shape[-1]
+        if self.cols % max(32, self.group):
+            raise ValueError(f"{self.cols} columns, expected a multiple of {max(32, self.group)}")
+        groups = (*q.shape[:-1], self.cols // self.group)
+        if q.dtype is not torch.uint8 or not q.is_contiguous():
+            _refuse(q.shape, torch.uint8, q=q)
+        if format == WEIGHT_INT4:
+            if s.dtype not in (torch.bfloat16, torch.float16):
+                raise ValueError(f"s is {s.dtype}, expected bfloat16 or float16")
+            _refuse(groups, s.dtype, s=s)
+            if z is not None:
+                _refuse(groups, torch.uint8, z=z)
+        else:
+            if format == WEIGHT_NVFP4 and s.dtype is torch.float8_e4m3fn:
+                s = s.view(torch.uint8)
+            _refuse(groups, torch.uint8, s=s)
+            z = None
+        if format == WEIGHT_NVFP4:
+            if g is None or g.dtype is not _F32 or g.numel() != (self.lead[0] if self.lead else 1) \
+                    or not g.is_contiguous():
+                raise ValueError("g must be contiguous float32 with one value per matrix")
+        else:
+            g = None
+        # the type of activations it takes: INT4's scales fix it
+        self.code = _CODES[s.dtype] if format == WEIGHT_INT4 else None
+        self.tensors = (q, s, z, g)
+        self.struct = Packed(format, self.group, _at(q), _at(s), _at(z), _at(g))
+        self._ref = byref(self.struct)
+
+    def _takes(self, name: str, code: int) -> None:
+        if code == DTYPE_FP32 or (self.code is not None and self.code != code):
+            raise ValueError(f"{name}: activations must be bfloat16 or float16, and of the type of "
+                             "INT4 scales")
+
+
+def _addend(name: str, t, shape: tuple, code: int) -> int:
+    """Row stride of an addend, which may be one row for all (expanded)."""
+    if t.shape == shape and _CODES.get(t.dtype) == code and t.stride(0) == 0 and shape[0] > 1 \
+            and t.stride(1) == 1:
+        return 0
+    return _matrix(name, t, shape, code)
+
+
+def moe_linear_scratch_bytes(M: int, K: int, N: int) -> tuple:
+    """Bytes of scratch of (moe_linear, moe_linear_backward) for a matrix [N, K]."""
+    f, b = c_size_t(), c_size_t()
+    _check(load_library().moe_linear_scratch_bytes(M, K, N, byref(f), byref(b)))
+    return f.value, b.value
+
+
+def moe_linear(x, w: PackedMatrix, y, base=None, scratch=None, stream=None) -> None:
+    """y[M, N] = base + x[M, K] W^T for a packed W [N, K]; base may be None (zeros), y itself, or
+    one row for all (a bias, expanded to [M, N])."""
+    code = _dtype_code(x)
+    w._takes("moe_linear", code)
+    if w.lead:
+        raise ValueError("moe_linear takes one matrix")
+    M, N, K = x.shape[0], w.rows, w.cols
+    xs, ys = _matrix("x", x, (M, K), code), _matrix("y", y, (M, N), code)
+    bs = 0 if base is None else _addend("base", base, (M, N), code)
+    ws, nbytes = _room(scratch)
+    _launch("moe_linear", stream, (x, *w.tensors, base, y, scratch), x.data_ptr(), xs, w._ref, M, K, N,
+            code, _at(base), bs, y.data_ptr(), ys, ws, nbytes)
+
+
+def moe_linear_backward(dy, w: PackedMatrix, dx, dbase=None, scratch=None, stream=None) -> None:
+    """Gradient of moe_linear: dx[M, K] = dbase + dy[M, N] W; dbase as base there."""
+    code = _dtype_code(dy)
+    w._takes("moe_linear_backward", code)
+    if w.lead:
+        raise ValueError("moe_linear_backward takes one matrix")
+    M, N, K = dy.shape[0], w.rows, w.cols
+    ys, xs = _matrix("dy", dy, (M, N), code), _matrix("dx", dx, (M, K), code)
+    bs = 0 if dbase is None else _addend("dbase", dbase, (M, K), code)
+    ws, nbytes = _room(scratch)
+    _launch("moe_linear_backward", stream, (dy, *w.tensors, dbase, dx, scratch), dy.data_ptr(), ys,
+            w._ref, M, K, N, code, _at(dbase), bs, dx.data_ptr(), xs, ws, nbytes)
+
+
+def moe_tokens_scratch_bytes(M: int, num_experts: int, hidden: int, inter: int, top_k: int,
+                             shared_inter: int = 0) -> int:
+    n = c_size_t()
+    _check(load_library().moe_tokens_scratch_bytes(M, num_experts, hidden, inter, top_k, shared_inter,
+                                                   byref(n)))
+    return n.value
+
+
+def moe_tokens(x, router, w13: PackedMatrix, w2: PackedMatrix, top_k: int, y, base=None, shared=None,
+               topk_ids=None, topk_w=None, scratch=None, stream=None) -> None:
+    """y[M, H] = base + the layer's output for M <= 16 tokens x[M, H]: router [E, H], experts w13
+    [E, 2I, H] and w2 [E, H, I], shared = (w13 [2S, H], w2 [H, S], gate [H] or None) or None.
+    topk_ids i32 [M, k] and topk_w f32 [M, k] receive the routing if given."""
+    code = _dtype_code(x)
+    M, H = x.shape
+    if len(w13.lead) != 1 or w2.lead != w13.lead or w13.cols != H or w2.rows != H \
+            or w13.rows != 2 * w2.cols:
+        raise ValueError("w13 must be [E, 2I, H] and w2 [E, H, I]")
+    E, I = w13.lead[0], w2.cols
+    s13, s2, gate, S = None, None, None, 0
+    mats = (w13, w2)
+    if shared is not None:
+        s13, s2, gate = shared
+        S = s2.cols
+        if s13.lead or s2.lead or s13.cols != H or s2.rows != H or s13.rows != 2 * S:
+            raise ValueError("the shared expert must be [2S, H] and [H, S]")
+        mats = (w13, w2, s13, s2)
+    for m in mats:
+        m._takes("moe_tokens", code)
+    for name, t, shape in (("router", router, (E, H)), ("shared gate", gate, (H,))):
+        if (t is not None or name == "router") and (t.shape != shape or _CODES.get(t.dtype) != code
+                                                    or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous {list(shape)} of the activations' type")
+    xs, ys = _matrix("x", x, (M, H), code), _matrix("y", y, (M, H), code)
+    bs = 0 if base is None else _addend("base", base, (M, H), code)
+    if topk_ids is not None:
+        _refuse((M, top_k), _I32, topk_ids=topk_ids)
+    if topk_w is not None:
+        _refuse((M, top_k), _F32, topk_w=topk_w)
+    none = Packed()
+    d = TokensDesc(E, H, I, top_k, S, code, router.data_ptr(), _at(gate), w13.struct, w2.struct,
+                   s13.struct if S else none, s2.struct if S else none)
+    ws, nbytes = _room(scratch)
+    _launch("moe_tokens", stream, (x, router, gate, base, y, topk_ids, topk_w, scratch,
+                                   *(t for m in mats for t in m.tensors)),
+            byref(d), x.data_ptr(), xs, M, _at(base), bs, y.data_ptr(), ys, _at(topk_ids), _at(topk_w),
+            ws, nbytes)
 
 
 class DeviceWeights:

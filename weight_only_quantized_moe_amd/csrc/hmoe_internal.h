@@ -201,6 +201,50 @@ void lora_scratch(int M, int G, int K, int N, int r, size_t* forward, size_t* ba
 hipError_t launch_lora(const Lora& p, void* scratch, hipStream_t s);
 hipError_t launch_lora_backward(const LoraGrad& p, void* scratch, hipStream_t s);
 
+// packed.h: a matrix of 4-bit weights with group scales, or several behind one another
+struct Packed {
+  const uint8_t* q;
+  const uint8_t* s;
+  const uint8_t* z;   // INT4 zero points; null: 8
+  const float* g;     // NVFP4: a scale per matrix
+  int format, group;
+};
+
+// linear.hip: products with a packed matrix W [N, K], and the gradient of their rows
+struct Linear {
+  Packed w;
+  int dtype;
+  const uint16_t* x;     // [M, K]; backward: dy [M, N]
+  long xs;
+  int M, K, N;
+  const uint16_t* base;  // [M, N]; backward: dbase [M, K]; may be null
+  long bs;
+  uint16_t* y;           // [M, N]; backward: dx [M, K]
+  long ys;
+};
+void linear_scratch(int M, int K, int N, size_t* forward, size_t* backward);
+hipError_t launch_linear(const Linear& p, bool back, void* scratch, hipStream_t s);
+
+// tokens.hip: a whole layer for a few tokens
+struct Tokens {
+  int dtype;
+  const uint16_t* x;      // [M, H]
+  long xs;
+  const uint16_t* router; // [E, H]
+  const uint16_t* gate;   // [H]; null: the shared expert's weight is 1
+  Packed w13, w2;         // [E][2 I, H] and [E][H, I]
+  Packed s13, s2;         // [2 S, H] and [H, S]
+  int M, E, H, I, k, S;
+  const uint16_t* base;   // [M, H]; may be null
+  long bs;
+  uint16_t* y;
+  long ys;
+  int32_t* topk_ids;      // [M, k]; may be null
+  float* topk_w;
+};
+size_t tokens_scratch(int M, int E, int I, int k, int S);
+hipError_t launch_tokens(const Tokens& p, void* scratch, hipStream_t s);
+
 // dequant.hip
 hipError_t launch_dequant(const Layer& L, const hmoe_weights& W, int expert, int tensor,
                           float* out_f32, uint16_t* out_bf16, hipStream_t s);

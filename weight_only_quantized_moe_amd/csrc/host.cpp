@@ -228,6 +228,95 @@ hmoe_status check_base(const char* name, const uint16_t* base, int64_t bs, const
   return HMOE_OK;
 }
 
+// ---- matrices of 4-bit weights
+
+// columns K of a packed matrix: whole groups, and whole column blocks of the kernels
+hmoe_status check_packed(const char* name, const hmoe_packed& w, int64_t K) {
+  const std::string who = name;
+  if (w.format != HMOE_WEIGHT_NVFP4 && w.format != HMOE_WEIGHT_MXFP4 && w.format != HMOE_WEIGHT_INT4)
+    return fail(HMOE_ERR_INVALID_ARG, who + ": unknown format");
+  const bool int4 = w.format == HMOE_WEIGHT_INT4;
+  if (int4 && w.group != 32 && w.group != 64 && w.group != 128)
+    return fail(HMOE_ERR_INVALID_ARG, who + ": group must be 32, 64 or 128");
+  if (K % 32 || (int4 && K % w.group))
+    return fail(HMOE_ERR_UNSUPPORTED, who + ": columns must be a multiple of 32 and of the group");
+  if (!w.q || !aligned(w.q, 16) || !w.s || !aligned(w.s, 16))
+    return fail(HMOE_ERR_ALIGN, who + ": q and s must be non-NULL and 16-byte aligned");
+  if (int4 && !aligned(w.z, 16)) return fail(HMOE_ERR_ALIGN, who + ": z must be 16-byte aligned");
+  if (w.format == HMOE_WEIGHT_NVFP4 && (!w.g || !aligned(w.g, 4)))
+    return fail(HMOE_ERR_ALIGN, who + ": g must be non-NULL and 4-byte aligned");
+  return HMOE_OK;
+}
+
+hmoe::Packed packed_of(const hmoe_packed& w) {
+  const bool int4 = w.format == HMOE_WEIGHT_INT4;
+  return {w.q, static_cast<const uint8_t*>(w.s), int4 ? w.z : nullptr,
+          w.format == HMOE_WEIGHT_NVFP4 ? w.g : nullptr, w.format,
+          int4 ? w.group : w.format == HMOE_WEIGHT_NVFP4 ? 16 : 32};
+}
+
+hmoe_status check_linear_shape(int32_t M, int32_t K, int32_t N) {
+  if (M < 0 || K < 1 || N < 1) return fail(HMOE_ERR_INVALID_ARG, "M must be >= 0, K and N >= 1");
+  if (K % 32) return fail(HMOE_ERR_UNSUPPORTED, "K must be a multiple of 32");
+  if (M > (1 << 22) || K > (1 << 20) || N > (1 << 20))
+    return fail(HMOE_ERR_UNSUPPORTED, "M > 2^22, or K or N > 2^20");
+  return HMOE_OK;
+}
+
+hmoe_status check_half(int32_t dtype) {
+  if (dtype != HMOE_DTYPE_BF16 && dtype != HMOE_DTYPE_FP16)
+    return fail(HMOE_ERR_INVALID_ARG, "dtype must be bf16 or fp16");
+  return HMOE_OK;
+}
+
+// an addend of rows: null, the output itself, a matrix, or one row for all (stride 0)
+hmoe_status check_addend(const char* name, const void* base, int64_t bs, const void* out, int64_t os,
+                         int64_t cols) {
+  if (!base) return HMOE_OK;
+  if (hmoe_status st = check_matrix(name, base, bs == 0 ? cols : bs, cols, 2)) return st;
+  if (base == out && bs != os)
+    return fail(HMOE_ERR_INVALID_ARG, std::string(name) + " is the output itself with another stride");
+  return HMOE_OK;
+}
+
+hmoe_status run_linear(const char* in_name, const void* x, int64_t xs, const hmoe_packed* w, int32_t M,
+                       int32_t K, int32_t N, int32_t dtype, const char* base_name, const void* base,
+                       int64_t bs, const char* out_name, void* y, int64_t ys, void* scratch,
+                       size_t scratch_bytes, bool back, hipStream_t stream) {
+  if (hmoe_status st = check_linear_shape(M, K, N)) return st;
+  if (hmoe_status st = check_half(dtype)) return st;
+  if (!w) return fail(HMOE_ERR_INVALID_ARG, "w is NULL");
+  if (hmoe_status st = check_packed("w", *w, K)) return st;
+  if (M == 0) return HMOE_OK;
+  const int in = back ? N : K, out = back ? K : N;
+  if (hmoe_status st = check_matrix(in_name, x, xs, in, 2)) return st;
+  if (hmoe_status st = check_matrix(out_name, y, ys, out, 2)) return st;
+  if (hmoe_status st = check_addend(base_name, base, bs, y, ys, out)) return st;
+  size_t need;
+  hmoe::linear_scratch(M, K, N, back ? nullptr : &need, back ? &need : nullptr);
+  if (hmoe_status st = check_op_scratch(scratch, scratch_bytes, need)) return st;
+  if (hmoe_status st = check_apart({x, w->q, w->s, w->z, w->g}, {{out_name, y}})) return st;
+  const hmoe::Linear p{packed_of(*w), dtype, static_cast<const uint16_t*>(x), xs, M, K, N,
+                       static_cast<const uint16_t*>(base), bs, static_cast<uint16_t*>(y), ys};
+  hipError_t err = hmoe::launch_linear(p, back, scratch, stream);
+  if (err != hipSuccess) return hip_fail(err, back ? "linear backward launch" : "linear launch");
+  return HMOE_OK;
+}
+
+hmoe_status check_tokens_shape(int32_t M, int32_t E, int32_t H, int32_t I, int32_t k, int32_t S) {
+  if (M < 0) return fail(HMOE_ERR_INVALID_ARG, "M < 0");
+  if (hmoe_status st = check_experts(E)) return st;
+  if (k < 1 || k > std::min(hmoe::kMaxTopK, (int)E))
+    return fail(HMOE_ERR_INVALID_ARG, "k must be in [1, min(16, E)]");
+  if (H < 1 || I < 1 || S < 0) return fail(HMOE_ERR_INVALID_ARG, "hidden and inter must be >= 1, shared_inter >= 0");
+  if (H % 32 || I % 32 || S % 32)
+    return fail(HMOE_ERR_UNSUPPORTED, "hidden, inter and shared_inter must be multiples of 32");
+  if (H > (1 << 20) || I > (1 << 20) || S > (1 << 20))
+    return fail(HMOE_ERR_UNSUPPORTED, "hidden, inter or shared_inter > 2^20");
+  if (M > HMOE_TOKENS_MAX_M) return fail(HMOE_ERR_CAPACITY, "M > HMOE_TOKENS_MAX_M");
+  return HMOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -794,6 +883,81 @@ hmoe_status moe_lora_backward(const uint16_t* dy, int64_t dy_stride, const uint1
                          dbase, dbase_stride, dx, dx_stride, dA, dB};
   hipError_t err = hmoe::launch_lora_backward(p, scratch, stream);
   if (err != hipSuccess) return hip_fail(err, "adapter backward launch");
+  return HMOE_OK;
+}
+
+hmoe_status moe_linear_scratch_bytes(int32_t M, int32_t K, int32_t N, size_t* forward_bytes,
+                                     size_t* backward_bytes) {
+  if (hmoe_status st = check_linear_shape(M, K, N)) return st;
+  if (!forward_bytes || !backward_bytes) return fail(HMOE_ERR_INVALID_ARG, "bytes is NULL");
+  hmoe::linear_scratch(M, K, N, forward_bytes, backward_bytes);
+  return HMOE_OK;
+}
+
+hmoe_status moe_linear(const void* x, int64_t x_stride, const hmoe_packed* w, int32_t M, int32_t K,
+                       int32_t N, int32_t dtype, const void* base, int64_t base_stride, void* y,
+                       int64_t y_stride, void* scratch, size_t scratch_bytes, hipStream_t stream) {
+  return run_linear("x", x, x_stride, w, M, K, N, dtype, "base", base, base_stride, "y", y, y_stride,
+                    scratch, scratch_bytes, false, stream);
+}
+
+hmoe_status moe_linear_backward(const void* dy, int64_t dy_stride, const hmoe_packed* w, int32_t M,
+                                int32_t K, int32_t N, int32_t dtype, const void* dbase,
+                                int64_t dbase_stride, void* dx, int64_t dx_stride, void* scratch,
+                                size_t scratch_bytes, hipStream_t stream) {
+  return run_linear("dy", dy, dy_stride, w, M, K, N, dtype, "dbase", dbase, dbase_stride, "dx", dx,
+                    dx_stride, scratch, scratch_bytes, true, stream);
+}
+
+hmoe_status moe_tokens_scratch_bytes(int32_t M, int32_t E, int32_t H, int32_t I, int32_t k,
+                                     int32_t shared_inter, size_t* bytes) {
+  if (hmoe_status st = check_tokens_shape(M, E, H, I, k, shared_inter)) return st;
+  if (!bytes) return fail(HMOE_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = hmoe::tokens_scratch(M, E, I, k, shared_inter);
+  return HMOE_OK;
+}
+
+hmoe_status moe_tokens(const hmoe_tokens* layer, const void* x, int64_t x_stride, int32_t M,
+                       const void* base, int64_t base_stride, void* y, int64_t y_stride,
+                       int32_t* topk_ids, float* topk_w, void* scratch, size_t scratch_bytes,
+                       hipStream_t stream) {
+  if (!layer) return fail(HMOE_ERR_INVALID_ARG, "layer is NULL");
+  const hmoe_tokens& t = *layer;
+  const int H = t.hidden, I = t.inter, S = t.shared_inter;
+  if (hmoe_status st = check_tokens_shape(M, t.num_experts, H, I, t.top_k, S)) return st;
+  if (hmoe_status st = check_half(t.dtype)) return st;
+  if (hmoe_status st = check_packed("w13", t.w13, H)) return st;
+  if (hmoe_status st = check_packed("w2", t.w2, I)) return st;
+  if (S > 0) {
+    if (hmoe_status st = check_packed("shared_w13", t.shared_w13, H)) return st;
+    if (hmoe_status st = check_packed("shared_w2", t.shared_w2, S)) return st;
+  }
+  const bool int4 = t.w13.format == HMOE_WEIGHT_INT4;
+  auto same = [&](const hmoe_packed& w) { return w.format == t.w13.format && (!int4 || w.group == t.w13.group); };
+  if (!same(t.w2) || (S > 0 && (!same(t.shared_w13) || !same(t.shared_w2))))
+    return fail(HMOE_ERR_INVALID_ARG, "the layer's matrices must have one format and group");
+  if (hmoe_status st = check_arrays("router", {t.router})) return st;
+  if (S > 0 && !aligned(t.shared_gate, 16)) return fail(HMOE_ERR_ALIGN, "shared_gate must be 16-byte aligned");
+  if (M == 0) return HMOE_OK;
+  if (hmoe_status st = check_matrix("x", x, x_stride, H, 2)) return st;
+  if (hmoe_status st = check_matrix("y", y, y_stride, H, 2)) return st;
+  if (hmoe_status st = check_addend("base", base, base_stride, y, y_stride, H)) return st;
+  if (!aligned(topk_ids, 16) || !aligned(topk_w, 16))
+    return fail(HMOE_ERR_ALIGN, "topk_ids and topk_w must be 16-byte aligned");
+  if (hmoe_status st = check_op_scratch(scratch, scratch_bytes, hmoe::tokens_scratch(M, t.num_experts, I, t.top_k, S)))
+    return st;
+  if (hmoe_status st = check_apart({x, t.router, t.shared_gate, t.w13.q, t.w13.s, t.w2.q, t.w2.s},
+                                   {{"y", y}, {"topk_ids", topk_ids, base}, {"topk_w", topk_w, base}}))
+    return st;
+  const hmoe::Tokens p{t.dtype, static_cast<const uint16_t*>(x), x_stride,
+                       static_cast<const uint16_t*>(t.router),
+                       S > 0 ? static_cast<const uint16_t*>(t.shared_gate) : nullptr,
+                       packed_of(t.w13), packed_of(t.w2),
+                       S > 0 ? packed_of(t.shared_w13) : hmoe::Packed{}, S > 0 ? packed_of(t.shared_w2) : hmoe::Packed{},
+                       M, t.num_experts, H, I, t.top_k, S, static_cast<const uint16_t*>(base), base_stride,
+                       static_cast<uint16_t*>(y), y_stride, topk_ids, topk_w};
+  hipError_t err = hmoe::launch_tokens(p, scratch, stream);
+  if (err != hipSuccess) return hip_fail(err, "tokens launch");
   return HMOE_OK;
 }
 
