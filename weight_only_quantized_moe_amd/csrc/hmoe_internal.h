@@ -242,7 +242,7 @@ struct Tokens {
   int32_t* topk_ids;      // [M, k]; may be null
   float* topk_w;
 };
-size_t tokens_scratch(int M, int E, int I, int k, int S);
+size_t tokens_scratch(int M, int E, int H, int I, int k, int S);
 hipError_t launch_tokens(const Tokens& p, void* scratch, hipStream_t s);
 
 // dequant.hip

@@ -913,7 +913,7 @@ hmoe_status moe_tokens_scratch_bytes(int32_t M, int32_t E, int32_t H, int32_t I,
                                      int32_t shared_inter, size_t* bytes) {
   if (hmoe_status st = check_tokens_shape(M, E, H, I, k, shared_inter)) return st;
   if (!bytes) return fail(HMOE_ERR_INVALID_ARG, "bytes is NULL");
-  *bytes = hmoe::tokens_scratch(M, E, I, k, shared_inter);
+  *bytes = hmoe::tokens_scratch(M, E, H, I, k, shared_inter);
   return HMOE_OK;
 }
 
@@ -944,7 +944,7 @@ hmoe_status moe_tokens(const hmoe_tokens* layer, const void* x, int64_t x_stride
   if (hmoe_status st = check_addend("base", base, base_stride, y, y_stride, H)) return st;
   if (!aligned(topk_ids, 16) || !aligned(topk_w, 16))
     return fail(HMOE_ERR_ALIGN, "topk_ids and topk_w must be 16-byte aligned");
-  if (hmoe_status st = check_op_scratch(scratch, scratch_bytes, hmoe::tokens_scratch(M, t.num_experts, I, t.top_k, S)))
+  if (hmoe_status st = check_op_scratch(scratch, scratch_bytes, hmoe::tokens_scratch(M, t.num_experts, H, I, t.top_k, S)))
     return st;
   if (hmoe_status st = check_apart({x, t.router, t.shared_gate, t.w13.q, t.w13.s, t.w2.q, t.w2.s},
                                    {{"y", y}, {"topk_ids", topk_ids, base}, {"topk_w", topk_w, base}}))

@@ -35,6 +35,114 @@ struct LinearRows {
   long ys;
 };
 
+// Up to 16 rows, K a multiple of 256: a wave keeps its PX pairs of steps of the rows in registers (x is
+// read once a block, however many columns the block takes), and the codes of the next columns are
+// requested pair by pair as those of the present ones are used up. A block takes items of 16 R
+// columns, grid-strided; the waves' sums of an item meet in LDS.
+template <int F, int X, int R, int PX>
+__global__ __launch_bounds__(512, PX == 1 ? 4 : 2) void linear_wide_kernel(LinearRows p) {
+  extern __shared__ float red[];   // [2][waves][R * 256]
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  const int K = p.K, items = (p.N + 16 * R - 1) / (16 * R);
+  const PairShare share = pair_share(wave, K / 256, PX);
+  u32x4 a[PX][2][1][4][1];
+  PairCodes c[PX][R];
+  StepScales<F, 2 * PX> now[R], then[R];
+  // A tile that would end past N starts earlier (rows past N are stand-ins only where N < 16); the
+  // columns before its own are another item's.
+  const TileLane at = tile_lane<F, 2 * PX>(lane, K, p.N);
+  auto tile_of = [&](int item, int r) __attribute__((always_inline)) {
+    return max(0, min(item * (16 * R) + 16 * r, p.N - 16));
+  };
+  auto scales = [&](StepScales<F, 2 * PX>(&to)[R], int item) __attribute__((always_inline)) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const TileBase t = tile_base<F>(p.w, tile_of(item, r), K, 2 * share.first);
+      load_scales(to[r], t.s, t.z, at);
+    }
+  };
+  auto codes = [&](int j, int item) __attribute__((always_inline)) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) load_pair(c[j][r], tile_base<F>(p.w, tile_of(item, r), K, 2 * (share.first + j)).q, at);
+  };
+  int item = blockIdx.x;
+  scales(now, item);
+#pragma unroll
+  for (int j = 0; j < PX; ++j) codes(j, item);
+  // rows past M are stand-ins: their sums are not written
+  const uint16_t* x = p.x + (long)min(lane & 15, p.M - 1) * p.xs + (lane >> 4) * 8;
+#pragma unroll
+  for (int j = 0; j < 2 * PX; ++j) load_rows<F, true>(a[j >> 1][j & 1], x, 2 * share.first + j, K);
+  const float g = F == kNv ? p.w.g[0] : 1.f;
+  for (int buf = 0;; buf ^= 1) {
+    const int next = item + gridDim.x;
+    f32x4 acc[R][1];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      acc[r][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+      default_zeros(now[r], p.w.z);
+    }
+    auto products = [&](auto P) __attribute__((always_inline)) {
+      constexpr int j = decltype(P)::value;
+      if (share.first + j < share.own) return;
+#pragma unroll
+      for (int r = 0; r < R; ++r) pair_product<F, X, X, PX, j, 1>(acc[r], c[j][r], now[r], a[j]);
+    };
+    // the two cases apart: a load behind a condition would make the waits count on its absence
+    if (next < items) {
+      scales(then, next);
+      each<PX>([&](auto P) __attribute__((always_inline)) {
+        products(P);
+        codes(decltype(P)::value, next);
+      });
+#pragma unroll
+      for (int r = 0; r < R; ++r) now[r] = then[r];
+    } else {
+      each<PX>(products);
+    }
+    float* sums = red + buf * (waves * R * 256);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sums[(wave * R + r) * 256 + i * 64 + lane] = acc[r][0][i];
+    __syncthreads();
+    for (int o = threadIdx.x; o < R * 256; o += blockDim.x) {
+      const int l = o & 63, m = (l >> 4) * 4 + ((o >> 6) & 3);
+      const int first = item * (16 * R) + 16 * (o >> 8), n = tile_of(item, o >> 8) + (l & 15);
+      if (m >= p.M || n < first || n >= p.N) continue;
+      float v = 0.f;
+      for (int w = 0; w < waves; ++w) v += sums[w * (R * 256) + o];
+      v *= g;
+      if (p.base) v += to_f32<X>(p.base[m * p.bs + n]);
+      p.y[m * p.ys + n] = from_f32<X>(v);
+    }
+    if (next >= items) return;
+    item = next;
+  }
+}
+
+template <int F, int X, int R, int PX>
+hipError_t run_wide(const LinearRows& p, hipStream_t s) {
+  const int items = (p.N + 16 * R - 1) / (16 * R), waves = (p.K / 256 + PX - 1) / PX;
+  const int blocks = std::min(items, 256 * (PX == 1 ? 16 / waves : 1));
+  hipLaunchKernelGGL((linear_wide_kernel<F, X, R, PX>), dim3((unsigned)blocks), dim3((unsigned)(waves * 64)),
+                     (size_t)2 * waves * R * 1024, s, p);
+  return hipGetLastError();
+}
+
+constexpr int kWideMaxK = 8 * 4 * 256;   // eight waves of four pairs
+
+template <int F, int X>
+hipError_t launch_wide(const LinearRows& p, hipStream_t s) {
+  const int pairs = p.K / 256;
+  const bool two = p.N >= 256 * 32;
+  if (pairs <= 8) return two ? run_wide<F, X, 2, 1>(p, s) : run_wide<F, X, 1, 1>(p, s);
+  if (pairs <= 16) return two ? run_wide<F, X, 2, 2>(p, s) : run_wide<F, X, 1, 2>(p, s);
+  if (pairs <= 24) return run_wide<F, X, 1, 3>(p, s);
+  return run_wide<F, X, 1, 4>(p, s);
+}
+
 // A block: 16 R columns n and 16 T rows m, the steps of 128 of K dealt to its waves. D: steps a
 // wave loads at once.
 template <int F, int X, int R, int T, int D>
@@ -56,27 +164,23 @@ __global__ __launch_bounds__(T == 1 ? 1024 : 512) void linear_rows_kernel(Linear
 #pragma unroll
     for (int t = 0; t < T; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  auto products = [&](const Codes<F>(&c)[R], u32x4 (&a)[4][T], int blocks) {
+  auto products = [&](const Codes<F>(&c)[R], u32x4 (&a)[1][4][T], int blocks) {
     if constexpr (is_int4(F)) {
 #pragma unroll
       for (int b = 0; b < 4; ++b)
 #pragma unroll
-        for (int t = 0; t < T; ++t) a[b][t] = int4_order(a[b][t]);
+        for (int t = 0; t < T; ++t) a[0][b][t] = int4_order(a[0][b][t]);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       Codes<F> v = c[r];
-      turn4(v.q);
-      block_product<F, X, X, 0, T>(acc[r], v, a[0], lane);
-      if (blocks > 1) block_product<F, X, X, 1, T>(acc[r], v, a[1], lane);
-      if (blocks > 2) block_product<F, X, X, 2, T>(acc[r], v, a[2], lane);
-      if (blocks > 3) block_product<F, X, X, 3, T>(acc[r], v, a[3], lane);
+      step_product<F, X, X, T, 1>(acc[r], v, a, blocks);
     }
   };
 
   for (int s0 = wave; s0 < full; s0 += waves * D) {
     Codes<F> c[D][R];
-    u32x4 a[D][4][T];
+    u32x4 a[D][1][4][T];
 #pragma unroll
     for (int d = 0; d < D; ++d) {
       const int s = min(s0 + d * waves, full - 1);
@@ -85,7 +189,7 @@ __global__ __launch_bounds__(T == 1 ? 1024 : 512) void linear_rows_kernel(Linear
 #pragma unroll
       for (int b = 0; b < 4; ++b)
 #pragma unroll
-        for (int t = 0; t < T; ++t) a[d][b][t] = load16(xr[t] + s * 128 + b * 32);
+        for (int t = 0; t < T; ++t) a[d][0][b][t] = load16(xr[t] + s * 128 + b * 32);
     }
 #pragma unroll
     for (int d = 0; d < D; ++d)
@@ -94,13 +198,13 @@ __global__ __launch_bounds__(T == 1 ? 1024 : 512) void linear_rows_kernel(Linear
   if (K % 128 && wave == full % waves) {
     const int blocks = K % 128 / 32;
     Codes<F> c[R];
-    u32x4 a[4][T];
+    u32x4 a[1][4][T];
 #pragma unroll
     for (int r = 0; r < R; ++r) load_codes<F, false>(c[r], row[r], full, K, lane);
 #pragma unroll
     for (int b = 0; b < 4; ++b)
 #pragma unroll
-      for (int t = 0; t < T; ++t) a[b][t] = load16(xr[t] + full * 128 + min(b, blocks - 1) * 32);
+      for (int t = 0; t < T; ++t) a[0][b][t] = load16(xr[t] + full * 128 + min(b, blocks - 1) * 32);
     products(c, a, blocks);
   }
 
@@ -136,6 +240,7 @@ template <int F, int X>
 hipError_t launch_rows(const LinearRows& p, hipStream_t s) {
   const int steps = std::max(1, p.K / 128);
   const int waves = std::min(8, steps);
+  if (p.M <= 16 && p.K % 256 == 0 && p.K <= kWideMaxK) return launch_wide<F, X>(p, s);
   if (p.M <= 16) return run_rows<F, X, 1, 1, 2>(p, waves, s);
   if (p.M <= 32) return run_rows<F, X, 2, 2, 1>(p, waves, s);
   return run_rows<F, X, 2, 4, 1>(p, std::min(waves, 4), s);

@@ -21,6 +21,8 @@
 //   activations therefore give NaN.
 #pragma once
 
+#include <type_traits>
+
 #include "device_common.h"
 #include "hmoe_internal.h"
 
@@ -211,37 +213,273 @@ __device__ __forceinline__ float block_scale(const Codes<F>& c) {
   return to_f32<S>((c.s[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
 }
 
-// acc[tt] += the products of column block T with the activations a[tt] (in int4_order for INT4)
-// of 16 rows each. X: type of the activations.
-template <int F, int X, int S, int T, int NT>
-__device__ __forceinline__ void block_product(f32x4 (&acc)[NT], const Codes<F>& c, const u32x4 (&a)[NT], int lane) {
-  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-  const uint32_t w = c.q[T];
+// acc[t] += the products of column blocks T to T + N - 1, one group or part of one, with the activations
+// a[t] (in int4_order for INT4) of 16 rows each, which may come as PARTS that add up to them. X: type
+// of the activations.
+template <int F, int X, int S, int T, int N, int NT, int PARTS>
+__device__ __forceinline__ void block_product(f32x4 (&acc)[NT], const Codes<F>& c, const u32x4 (&a)[PARTS][4][NT]) {
   if constexpr (F == kNv) {
+    static_assert(N == 1, "two groups a block");
     // the dword's 8 columns lie in group 2 T + (lane >= 32)
-    const float s = (T & 1) ? ((lane & 32) ? e4m3_to_f32<3>(c.s[T >> 1]) : e4m3_to_f32<2>(c.s[T >> 1]))
-                            : ((lane & 32) ? e4m3_to_f32<1>(c.s[T >> 1]) : e4m3_to_f32<0>(c.s[T >> 1]));
-    const u32x4 b = nvfp4_operand<X>(w, s);
+    const uint32_t v = c.s[T >> 1] >> (16 * (T & 1));
+    const float s = e4m3_to_f32<0>(threadIdx.x & 32 ? v >> 8 : v);
+    const u32x4 b = nvfp4_operand<X>(c.q[T], s);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) acc[t] = mfma16<X>(a[t], b, acc[t]);
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < PARTS; ++i) acc[t] = mfma16<X>(a[i][T][t], b, acc[t]);
+  } else if constexpr (F == kMx && X == kBf) {
+    // bf16 has every exponent: the conversion applies the scale (the mantissa bit makes byte 0
+    // 2^-127 and 255 NaN, and is not applied otherwise)
+    static_assert(N == 1, "a group a block");
+    const uint32_t v = T == 3 ? c.s[0] >> 1 : c.s[0] << (23 - 8 * T);
+    const float s = __uint_as_float((v & 0x7F800000u) | 0x00400000u);
+    const uint32_t w = c.q[T];
+    const u32x4 b{e2m1x2_bf16<0>(w, s), e2m1x2_bf16<1>(w, s), e2m1x2_bf16<2>(w, s), e2m1x2_bf16<3>(w, s)};
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < PARTS; ++i) acc[t] = mfma16<X>(a[i][T][t], b, acc[t]);
   } else {
     const float s = block_scale<F, S, T>(c);
-    u32x4 b, o;
-    if constexpr (F == kMx) {
-      b = e2m1_operand<X>(w);
-    } else {
-      b = int4_operand<X>(w);
-      o = int4_offset<X>(c.z >> (8 * (T * 32 / group_of(F))));
+    u32x4 o;
+    if constexpr (is_int4(F)) o = int4_offset<X>(c.z >> (8 * (T * 32 / group_of(F))));
+    f32x4 p[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) p[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const u32x4 b = F == kMx ? e2m1_operand<X>(c.q[T + n]) : int4_operand<X>(c.q[T + n]);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i) {
+          if constexpr (is_int4(F)) p[t] = mfma16<X>(a[i][T + n][t], o, p[t]);
+          p[t] = mfma16<X>(a[i][T + n][t], b, p[t]);
+        }
     }
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      f32x4 p = zero;
-      if constexpr (is_int4(F)) p = mfma16<X>(a[t], o, p);
-      p = mfma16<X>(a[t], b, p);
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(s, p[i], acc[t][i]);
-    }
+      for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(s, p[t][i], acc[t][i]);
   }
+}
+
+// The four column blocks of a step against 16 NT rows of activations in registers; blocks: those
+// inside K (four unless the step is a row's last). The codes' dwords are turned in place.
+template <int F, int X, int S, int NT, int PARTS>
+__device__ __forceinline__ void step_product(f32x4 (&acc)[NT], Codes<F>& c, const u32x4 (&a)[PARTS][4][NT], int blocks) {
+  turn4(c.q);
+  constexpr int N = group_of(F) <= 32 ? 1 : group_of(F) / 32;   // blocks of a group
+  block_product<F, X, S, 0, N, NT, PARTS>(acc, c, a);
+  if constexpr (N == 1)
+    if (blocks > 1) block_product<F, X, S, 1, N, NT, PARTS>(acc, c, a);
+  if constexpr (N <= 2)
+    if (blocks > 2) block_product<F, X, S, 2, N, NT, PARTS>(acc, c, a);
+  if constexpr (N == 1)
+    if (blocks > 3) block_product<F, X, S, 3, N, NT, PARTS>(acc, c, a);
+}
+
+// load_codes where only the last step of a row can be partial (ALL: none is)
+template <int F, bool ALL>
+__device__ __forceinline__ void load_step(Codes<F>& c, const PackedRow& r, int step, int K, int lane) {
+  if constexpr (ALL) {
+    load_codes<F, true>(c, r, step, K, lane);
+  } else {
+    if ((step + 1) * 128 <= K) load_codes<F, true>(c, r, step, K, lane);
+    else load_codes<F, false>(c, r, step, K, lane);
+  }
+}
+template <bool ALL>
+__device__ __forceinline__ int step_blocks(int step, int K) {
+  return ALL ? 4 : min(4, (K - step * 128) / 32);
+}
+
+// A step of a row of activations, in the order the format takes; p points at the lane's 8 columns of
+// the step's first block
+template <int F, bool ALL>
+__device__ __forceinline__ void load_rows(u32x4 (&a)[1][4][1], const uint16_t* p, int step, int K) {
+  const int last = step_blocks<ALL>(step, K) - 1;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    a[0][b][0] = load16(p + (long)step * 128 + min(b, last) * 32);
+    if constexpr (is_int4(F)) a[0][b][0] = int4_order(a[0][b][0]);
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// Pairs of steps: rows of whole multiples of 256 columns
+// ------------------------------------------------------------------------------------------
+// A pair of steps covers whole 128-byte lines of codes: one load takes rows 0 to 7 of the tile, the
+// other rows 8 to 15, and two lanes eight apart exchange what is the other's. The scales of a wave's
+// steps come in one load a row: each of the row's four lanes takes Q steps, and a step's scales are
+// spread from their lane when they are needed. On MI355X the experts' first products of eight
+// tokens (256 experts, 6144 to 2048, MXFP4) take 181 us with a load of 64 bytes a row and a load of
+// scales a step, 143 without the scales (wrong results), 124 with whole lines as well.
+template <int F>
+constexpr int step_scale_bytes() { return 128 / group_of(F) * scale_bytes(F); }   // 8, 4 or 2
+template <int F>
+constexpr int step_zero_bytes() { return is_int4(F) ? 128 / group_of(F) : 0; }
+
+struct PairCodes {
+  u32x4 a, b;   // as loaded; after split_pair, the first and second step's
+};
+
+// The lane's places in a tile of 16 rows, as 32-bit offsets from the tile's first row, so that a load
+// takes a scalar base and one register: of its piece of rows 0 to 7 (lo) and 8 to 15 (hi), and of its
+// row's scales and zero points. Rows at and past `rows` are stand-ins.
+struct TileLane {
+  uint32_t lo, hi, s, z;
+};
+template <int F, int STEPS>
+__device__ __forceinline__ TileLane tile_lane(int lane, int K, int rows);
+
+__device__ __forceinline__ void load_pair(PairCodes& c, const uint8_t* tile, const TileLane& at) {
+  c.a = *reinterpret_cast<const u32x4*>(tile + at.lo);
+  c.b = *reinterpret_cast<const u32x4*>(tile + at.hi);
+}
+__device__ __forceinline__ void split_pair(PairCodes& c) {
+  const bool up = threadIdx.x & 8;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = c.a[i], b = c.b[i], give = up ? a : b;
+    const uint32_t got = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)give, 0x128, 0xF, 0xF, true);   // row_ror:8
+    c.a[i] = up ? got : a;
+    c.b[i] = up ? b : got;
+  }
+}
+
+// The scales and zero points of STEPS steps of the lane's row, Q of them in this lane.
+template <int F, int STEPS>
+struct StepScales {
+  static constexpr int Q = STEPS > 4 ? 2 : 1;
+  static constexpr int kBytes = Q * step_scale_bytes<F>(), kZeros = Q * step_zero_bytes<F>();
+  uint32_t s[(kBytes + 3) / 4 > 1 ? (kBytes + 3) / 4 : 2], z[kZeros > 4 ? 2 : 1];
+};
+
+template <int N>
+__device__ __forceinline__ void load_bytes(uint32_t* out, const uint8_t* p) {
+  if constexpr (N == 16) {
+    const Any8 v = *reinterpret_cast<const Any8*>(p), w = *reinterpret_cast<const Any8*>(p + 8);
+    out[0] = v.w[0], out[1] = v.w[1], out[2] = w.w[0], out[3] = w.w[1];
+  } else if constexpr (N == 8) {
+    const Any8 v = *reinterpret_cast<const Any8*>(p);
+    out[0] = v.w[0], out[1] = v.w[1];
+  } else if constexpr (N == 4) {
+    out[0] = reinterpret_cast<const Any4*>(p)->w;
+  } else if constexpr (N == 2) {
+    out[0] = reinterpret_cast<const Any2*>(p)->w;
+  } else {
+    out[0] = *p;
+  }
+}
+
+template <int F, int STEPS>
+__device__ __forceinline__ TileLane tile_lane(int lane, int K, int rows) {
+  constexpr int Q = StepScales<F, STEPS>::Q;
+  const int piece = ((lane >> 4) + ((lane >> 3) & 1) * 4) * 16, half = K / 2, groups = K / group_of(F);
+  const int step = min(lane >> 4, STEPS / Q - 1) * Q, row = min(lane & 15, rows - 1);
+  return {(uint32_t)(min(lane & 7, rows - 1) * half + piece), (uint32_t)(min(8 + (lane & 7), rows - 1) * half + piece),
+          (uint32_t)(row * groups * scale_bytes(F) + step * step_scale_bytes<F>()),
+          (uint32_t)(row * groups + step * step_zero_bytes<F>())};
+}
+
+// s, z: the tile's first row at the wave's first step, all of whose steps lie inside the row; z null: 8
+// everywhere (the load then takes scales instead, which are no fewer bytes, so that no load stands
+// behind a condition)
+template <int F, int STEPS>
+__device__ __forceinline__ void load_scales(StepScales<F, STEPS>& v, const uint8_t* s, const uint8_t* z,
+                                            const TileLane& at) {
+  using T = StepScales<F, STEPS>;
+  load_bytes<T::kBytes>(v.s, s + at.s);
+  if constexpr (is_int4(F)) load_bytes<T::kZeros>(v.z, (z ? z : s) + at.z);
+}
+template <int F, int STEPS>
+__device__ __forceinline__ void default_zeros(StepScales<F, STEPS>& v, bool given) {
+  if constexpr (is_int4(F)) {
+    v.z[0] = given ? v.z[0] : 0x08080808u;
+    if constexpr (StepScales<F, STEPS>::kZeros > 4) v.z[1] = given ? v.z[1] : 0x08080808u;
+  }
+}
+
+// A tile's first row, n rows into the matrix, and its parts at a wave's first step.
+struct TileBase {
+  const uint8_t* q;
+  const uint8_t* s;
+  const uint8_t* z;
+};
+template <int F>
+__device__ __forceinline__ TileBase tile_base(const Packed& w, long n, int K, int step) {
+  const long groups = n * (K / group_of(F));
+  return {w.q + n * (K / 2) + step * 64, w.s + groups * scale_bytes(F) + step * step_scale_bytes<F>(),
+          is_int4(F) && w.z ? w.z + groups + step * step_zero_bytes<F>() : nullptr};
+}
+
+// the value that lane quarter Q of the row holds, in all four
+template <int Q>
+__device__ __forceinline__ uint32_t spread(uint32_t v) {
+  const uint32_t h = __builtin_amdgcn_permlane32_swap(v, v, false, false)[Q >> 1];
+  return __builtin_amdgcn_permlane16_swap(h, h, false, false)[Q & 1];
+}
+
+// Step J's scales into c
+template <int F, int STEPS, int J>
+__device__ __forceinline__ void take_scales(Codes<F>& c, const StepScales<F, STEPS>& v) {
+  constexpr int Q = StepScales<F, STEPS>::Q, sub = J % Q, lane4 = J / Q;
+  constexpr int bytes = step_scale_bytes<F>(), zeros = step_zero_bytes<F>();
+  c.s[1] = 0u;
+  if constexpr (bytes == 8) {
+    c.s[0] = spread<lane4>(v.s[2 * sub]);
+    c.s[1] = spread<lane4>(v.s[2 * sub + 1]);
+  } else if constexpr (bytes == 4) {
+    c.s[0] = spread<lane4>(v.s[sub]);
+  } else {
+    c.s[0] = spread<lane4>(v.s[0]) >> (16 * sub);
+  }
+  c.z = 0u;
+  if constexpr (zeros == 4) c.z = spread<lane4>(v.z[sub]);
+  else if constexpr (zeros > 0) c.z = spread<lane4>(v.z[0]) >> (8 * zeros * sub);
+}
+
+// The same for the first or second step of two, as a loop over them takes it
+template <int F>
+__device__ __forceinline__ void take_scales_of(Codes<F>& c, const StepScales<F, 2>& v, bool second) {
+  auto part = [&](uint32_t x) { return second ? spread<1>(x) : spread<0>(x); };
+  c.s[0] = part(v.s[0]);
+  c.s[1] = step_scale_bytes<F>() == 8 ? part(v.s[1]) : 0u;
+  c.z = is_int4(F) ? part(v.z[0]) : 0u;
+}
+
+// Pair P of a wave's PX: both steps' products.
+template <int F, int X, int S, int PX, int P, int PARTS>
+__device__ __forceinline__ void pair_product(f32x4 (&acc)[1], PairCodes& q, const StepScales<F, 2 * PX>& v,
+                                             const u32x4 (&a)[2][PARTS][4][1]) {
+  split_pair(q);
+  Codes<F> c;
+  c.q = q.a;
+  take_scales<F, 2 * PX, 2 * P>(c, v);
+  step_product<F, X, S, 1, PARTS>(acc, c, a[0], 4);
+  c.q = q.b;
+  take_scales<F, 2 * PX, 2 * P + 1>(c, v);
+  step_product<F, X, S, 1, PARTS>(acc, c, a[1], 4);
+}
+
+// for (P = 0; P < N; ++P) f(P) with P a constant
+template <int N, int P = 0, typename Fn>
+__device__ __forceinline__ void each(Fn&& f) {
+  if constexpr (P < N) {
+    f(std::integral_constant<int, P>{});
+    each<N, P + 1>(f);
+  }
+}
+
+// The wave's share of `pairs` pairs among `waves` waves of PX each: its first pair, and from which on
+// they are its own (the last wave starts early rather than reach past the row).
+struct PairShare {
+  int first, own;
+};
+__device__ __forceinline__ PairShare pair_share(int wave, int pairs, int PX) {
+  return {min(wave * PX, pairs - PX), wave * PX};
 }
 
 }  // namespace hmoe
