@@ -11,8 +11,8 @@
 // The 16-bit form of W for the tiled product is fp16 whatever the rows' type: (q - z) s needs 13
 // bits in general, and fp16 keeps 11 of them where bf16 would keep 8 and add as much error again
 // as the rounding of a bf16 output. So that no exponent is lost, a column of the product has a
-// power of two of its own (column_exponent_kernel) and bf16 rows enter as fp16 times a power of two
-// of their own (rows16_kernel; exact down to 2^-29 of the row's largest element, and 2^-39 of it
+// power of two of its own (linear_prep_kernel) and bf16 rows enter as fp16 times a power of two
+// of their own (exact down to 2^-29 of the row's largest element, and 2^-39 of it
 // for smaller ones). Both come back in fp32.
 #include <algorithm>
 
@@ -249,155 +249,300 @@ hipError_t launch_rows(const LinearRows& p, hipStream_t s) {
 // ------------------------------------------------------------------------------------------
 // many rows: operands of the tiled product
 // ------------------------------------------------------------------------------------------
-
-// Tile of the product, and what its operands are padded to: rows to tiles, the reduction axis to
-// steps (with zeros; rows behind the last are not written, and their sums are not read).
-constexpr int kTileM = 128, kTileN = 128, kStepK = 64;
+// Both operands are fp16 in fragment order: tiles of 16 rows by 32 of the reduction axis, 1 KiB each
+// with the 16 bytes of MFMA lane l at 16 l, all blocks of a tile's rows behind one another. So a
+// wave copies a tile into LDS by one contiguous load, and its reads there are contiguous too. The
+// reduction axis is padded with zeros to whole blocks; rows past the last are stand-ins.
+//
+// Columns of the product are dealt to tiles eight apart: tile 8 g + i holds columns 128 g + 8 c + i
+// for c = 0 .. 15. Then a lane's sums of eight tiles are eight neighbours of a row of y, and the
+// transposed form of W comes out of 8 x 8 blocks of codes in one lane's registers.
+constexpr int kBlockK = 32;
 constexpr long kSlabBytes = 64l << 20;   // of the 16-bit form of W at a time: a quarter of the Infinity Cache
+constexpr int kPrepThreads = 512;
 
-__device__ __forceinline__ long round_up(long v, long to) { return (v + to - 1) / to * to; }
+struct Prep {
+  const uint16_t* x;   // [M, C]
+  long xs;
+  int M, C, blocks;    // blocks of 32 of the reduction axis
+  uint16_t* rows;      // fragment order
+  int* ea;             // [M]
+  int row_blocks;      // thread blocks for the rows; the others take exponents
+  Packed w;
+  int K, N;
+  int* eb;             // exponents of the product's columns
+  int* done;           // tickets of the product, cleared here
+  int tickets;
+};
 
-// x [M, C] -> fp16 [M, Cp], zeros past C; rows of bf16 times 2^-e with e of the largest finite
-// |x| (it lands in [2^14, 2^15)), and exponent[m] = e. One block a row.
+// Rows of x: 16 a block. bf16 goes to fp16 times 2^-e with e of the row's largest finite |x|, which
+// lands in [2^14, 2^15).
 template <int X>
-__global__ __launch_bounds__(256) void rows16_kernel(const uint16_t* x, long xs, int C, int Cp, uint16_t* out,
-                                                     int* exponent) {
-  const long m = blockIdx.x;
-  const uint16_t* row = x + m * xs;
-  uint16_t* o = out + m * Cp;
+__device__ __forceinline__ void prep_rows(const Prep& p, int tile, uint32_t (&part)[kPrepThreads / 64][16]) {
+  constexpr int kWaves = kPrepThreads / 64;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, m = tile * 16 + (lane & 15);
+  const uint16_t* x = p.x + (long)min(m, p.M - 1) * p.xs;
+  auto load = [&](int b) {
+    const int c = b * kBlockK + (lane >> 4) * 8;
+    if (c + 8 <= p.C) return load16(x + c);
+    u32x4 v = {0u, 0u, 0u, 0u};
+    for (int i = 0; i < 8; ++i)
+      if (c + i < p.C) {
+        const uint32_t h = (uint32_t)x[c + i] << (16 * (i & 1));
+        v[0] |= i >> 1 == 0 ? h : 0u;
+        v[1] |= i >> 1 == 1 ? h : 0u;
+        v[2] |= i >> 1 == 2 ? h : 0u;
+        v[3] |= i >> 1 == 3 ? h : 0u;
+      }
+    return v;
+  };
   int e = 0;
   if constexpr (X == kBf) {
-    __shared__ uint32_t part[4];
     uint32_t top = 0;   // largest finite |x|, as bits
-    for (int c = threadIdx.x; c < C; c += 256) {
-      const uint32_t v = row[c] & 0x7FFFu;
-      if (v < 0x7F80u) top = max(top, v);
+    auto take = [&](const u32x4& v) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = v[i] & 0x7FFFu, hi = (v[i] >> 16) & 0x7FFFu;
+        top = max(top, lo < 0x7F80u ? lo : 0u);
+        top = max(top, hi < 0x7F80u ? hi : 0u);
+      }
+    };
+    for (int b = wave; b < p.blocks; b += 4 * kWaves) {
+      u32x4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = load(min(b + j * kWaves, p.blocks - 1));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) take(v[j]);
     }
     top = max(top, xlane_u32<32>(top));
     top = max(top, xlane_u32<16>(top));
-    top = max(top, xlane_u32<8>(top));
-    top = max(top, xlane_u32<4>(top));
-    top = max(top, xlane_u32<2>(top));
-    top = max(top, xlane_u32<1>(top));
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
+    if (lane < 16) part[wave][lane] = top;
     __syncthreads();
-    top = max(max(part[0], part[1]), max(part[2], part[3]));
+    top = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) top = max(top, part[w][lane & 15]);
     if (top) e = (int)(top >> 7) - 127 - 14;
   }
-  for (int c = threadIdx.x; c < Cp; c += 256) {
-    uint16_t v = 0;
-    if (c < C) v = X == kHf ? row[c] : from_f32<kHf>(ldexpf(to_f32<X>(row[c]), -e));
-    o[c] = v;
-  }
-  if (threadIdx.x == 0) exponent[m] = e;
-}
-
-// exponent[c] = e for each column c of the product, so that W 2^-e fits fp16. NVFP4: 0, without its
-// g (e2m1 * e4m3 is a number of fp16 as it is). Forward: c = n, over the groups of row n. Backward:
-// c = k, over the rows n of k's group.
-template <int F, int S, bool BACK>
-__global__ __launch_bounds__(256) void column_exponent_kernel(Packed w, int K, int N, int* exponent) {
-  constexpr int G = group_of(F);
-  const int c = blockIdx.x;   // forward: n, backward: group of k
-  int* out = BACK ? exponent + (long)c * G : exponent + c;
-  int e = 0;
-  if constexpr (F != kNv) {
-    __shared__ int part[4];
-    const int groups = K / G, count = BACK ? N : groups;
-    int top = -1000;          // exponent of the largest finite scale
-    for (int i = threadIdx.x; i < count; i += 256) {
-      const long at = BACK ? (long)i * groups + c : (long)c * groups + i;
-      if constexpr (F == kMx) {
-        const int b = w.s[at];
-        if (b < 255) top = max(top, b - 127);
-      } else {
-        const float s = fabsf(to_f32<S>(reinterpret_cast<const uint16_t*>(w.s)[at]));
-        if (s > 0.f && s < INFINITY) top = max(top, ilogbf(s));
+  uint16_t* out = p.rows + (long)tile * p.blocks * 512 + lane * 8;
+  for (int b = wave; b < p.blocks; b += 4 * kWaves) {
+    u32x4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = load(min(b + j * kWaves, p.blocks - 1));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (b + j * kWaves >= p.blocks) continue;
+      if constexpr (X == kBf) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w = v[j][i];
+          v[j][i] = pack_f16(ldexpf(bf16_lo(w), -e), ldexpf(bf16_hi(w), -e));
+        }
       }
+      *reinterpret_cast<u32x4*>(out + (long)(b + j * kWaves) * 512) = v[j];
     }
-    for (int b = 32; b; b >>= 1) top = max(top, __shfl_xor(top, b));
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
-    __syncthreads();
-    top = max(max(part[0], part[1]), max(part[2], part[3]));
-    // the largest scale lands in [2^10, 2^11), or at 2^12 for MXFP4: times 16, or 6, below 2^15
-    if (top != -1000) e = top - (F == kMx ? 12 : 10);
   }
-  const int n = BACK ? G : 1;
-  for (int i = threadIdx.x; i < n; i += 256) out[i] = e;
+  if (wave == 0 && lane < 16 && m < p.M) p.ea[m] = e;
 }
 
-// 32 codes of one row times 2^-e as fp16, in the order of the columns
+// The exponent of a scale where it is finite and not zero
 template <int F, int S>
-__device__ __forceinline__ void fp16_codes(const Packed& w, long n, int k, int K, int e, uint32_t (&out)[16]) {
-  constexpr int G = group_of(F);
-  const u32x4 q = *reinterpret_cast<const u32x4*>(w.q + n * (K / 2) + k / 2);
-  const long g = n * (K / G) + k / G;
-  if constexpr (F == kNv) {
-    const float s0 = e4m3_to_f32<0>(w.s[g]), s1 = e4m3_to_f32<0>(w.s[g + 1]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const u32x4 v = nvfp4_operand<kHf>(q[i], i < 2 ? s0 : s1);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) out[4 * i + j] = v[j];
-    }
+__device__ __forceinline__ int scale_exponent(const Packed& w, long at) {
+  if constexpr (F == kMx) {
+    const int b = w.s[at];
+    return b < 255 ? b - 127 : -1000;
   } else {
-    const float s = ldexpf(F == kMx ? e8m0_value(w.s[g]) : to_f32<S>(reinterpret_cast<const uint16_t*>(w.s)[g]), -e);
-    const float z = is_int4(F) ? (w.z ? (float)(w.z[g] & 15) : 8.f) : 0.f;
+    const float s = fabsf(to_f32<S>(reinterpret_cast<const uint16_t*>(w.s)[at]));
+    return s > 0.f && s < INFINITY ? ilogbf(s) : -1000;
+  }
+}
+// with the largest scale of a column of the product at exponent `top`, W 2^-e fits fp16: the largest
+// lands in [2^10, 2^11), or at 2^12 for MXFP4, times 16, or 6, below 2^15
+template <int F>
+__device__ __forceinline__ int column_exponent(int top) {
+  return top == -1000 ? 0 : top - (F == kMx ? 12 : 10);
+}
+
+// What the product needs besides W: its rows as fp16, an exponent for each of its columns (NVFP4 needs
+// none: e2m1 * e4m3 is a number of fp16 as it is), and its tickets at zero. Forward, a column is a row
+// n of W: a wave takes one. Backward it is a column k, with one exponent for its group over all n: a
+// block takes 8 groups, its lanes 8 rows of them at a time.
+template <int F, int X, bool BACK>
+__global__ __launch_bounds__(kPrepThreads) void linear_prep_kernel(Prep p) {
+  constexpr int kWaves = kPrepThreads / 64, G = group_of(F);
+  __shared__ uint32_t part[kWaves][16];
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < p.tickets; i += kPrepThreads) p.done[i] = 0;
+  if ((int)blockIdx.x < p.row_blocks) return prep_rows<X>(p, blockIdx.x, part);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, b = blockIdx.x - p.row_blocks, groups = p.K / G;
+  if constexpr (F == kNv) {
+    return;
+  } else if constexpr (!BACK) {
+    const int n = b * kWaves + wave;
+    if (n >= p.N) return;
+    int top = -1000;
+    for (int g = lane; g < groups; g += 64) top = max(top, scale_exponent<F, X>(p.w, (long)n * groups + g));
+    for (int d = 32; d; d >>= 1) top = max(top, __shfl_xor(top, d));
+    if (lane == 0) p.eb[n] = column_exponent<F>(top);
+  } else {
+    const int g = b * 8 + (lane & 7);
+    int top = -1000;
+    for (int n = wave * 8 + (lane >> 3); n < p.N; n += 8 * kWaves * 8) {
+      int e[8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint32_t b = q[i >> 2] >> (8 * (i & 3));
-      if constexpr (F == kMx) {
-        const f32x2 v = e2m1x2_f32<0>(b, 1.f);
-        out[i] = pack_f16(v[0] * s, v[1] * s);
-      } else {
-        out[i] = pack_f16(((float)(b & 15u) - z) * s, ((float)((b >> 4) & 15u) - z) * s);
-      }
+      for (int j = 0; j < 8; ++j)
+        e[j] = scale_exponent<F, X>(p.w, (long)min(n + j * 8 * kWaves, p.N - 1) * groups + min(g, groups - 1));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = max(top, e[j]);
+    }
+    for (int d = 32; d >= 8; d >>= 1) top = max(top, __shfl_xor(top, d));
+    if (lane < 8) part[wave][lane] = (uint32_t)top;
+    __syncthreads();
+    if (threadIdx.x < 8 * G) {
+      const int i = threadIdx.x / G, k = (b * 8 + i) * G + threadIdx.x % G;
+      top = -1000;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) top = max(top, (int)part[w][i]);
+      if (k < p.K) p.eb[k] = column_exponent<F>(top);
+    }
+    // groups of 128 are more columns than threads
+    for (int i = threadIdx.x + kPrepThreads; i < 8 * G; i += kPrepThreads) {
+      const int k = (b * 8 + i / G) * G + i % G;
+      top = -1000;
+      for (int w = 0; w < kWaves; ++w) top = max(top, (int)part[w][i / G]);
+      if (k < p.K) p.eb[k] = column_exponent<F>(top);
     }
   }
 }
 
-// rows [n0, n0 + rows) of W as fp16 [rows, Kp], zeros past K: a thread takes 32 columns
+struct Weights16 {
+  Packed w;
+  int K, N, first, cols, blocks;   // the slab's first column of the product and their number
+  const int* eb;
+  uint16_t* out;
+};
+
+// Eight codes times eight scales as fp16, in their order: the scales' pairs (0 1) (2 3) .. for E2M1,
+// (0 4) (1 5) .. for INT4, and the zero points' 16 + z likewise.
+template <int F>
+__device__ __forceinline__ u32x4 scaled_codes(uint32_t w, const uint32_t (&s)[4], const uint32_t (&z)[4]) {
+  auto mul = [](uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, (f16x2)(__builtin_bit_cast(f16x2, a) * __builtin_bit_cast(f16x2, b)));
+  };
+  auto sub = [](uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, (f16x2)(__builtin_bit_cast(f16x2, a) - __builtin_bit_cast(f16x2, b)));
+  };
+  const u32x4 v = is_int4(F) ? int4_operand<kHf>(w) : e2m1_operand<kHf>(w);
+  const uint32_t v0 = v[0], v1 = v[1], v2 = v[2], v3 = v[3];
+  if constexpr (!is_int4(F)) {
+    return u32x4{mul(v0, s[0]), mul(v1, s[1]), mul(v2, s[2]), mul(v3, s[3])};
+  } else {
+    const uint32_t a = mul(sub(v0, z[0]), s[0]), b = mul(sub(v1, z[1]), s[1]);
+    const uint32_t c = mul(sub(v2, z[2]), s[2]), d = mul(sub(v3, z[3]), s[3]);
+    return u32x4{__builtin_amdgcn_perm(b, a, 0x05040100u), __builtin_amdgcn_perm(d, c, 0x05040100u),
+                 __builtin_amdgcn_perm(b, a, 0x07060302u), __builtin_amdgcn_perm(d, c, 0x07060302u)};
+  }
+}
+// A group's scale times 2^-e as fp16 bits, and 16 + z
 template <int F, int S>
-__global__ __launch_bounds__(256) void weights16_kernel(Packed w, int n0, int rows, int K, int Kp, const int* exponent,
-                                                        uint16_t* out) {
-  const int units = Kp / 32;
-  const long u = (long)blockIdx.x * 256 + threadIdx.x;
-  if (u >= (long)rows * units) return;
-  const long r = u / units;
-  const int k = (int)(u % units) * 32;
-  uint32_t v[16] = {};
-  if (k < K) fp16_codes<F, S>(w, n0 + r, k, K, exponent[n0 + r], v);
-  u32x4* o = reinterpret_cast<u32x4*>(out + r * Kp + k);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = u32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+__device__ __forceinline__ uint32_t scale16(const Packed& w, long at, int e) {
+  float s;
+  if constexpr (F == kNv) s = e4m3_to_f32<0>(w.s[at]);
+  else if constexpr (F == kMx) s = ldexpf(e8m0_value(w.s[at]), -e);
+  else s = ldexpf(to_f32<S>(reinterpret_cast<const uint16_t*>(w.s)[at]), -e);
+  return pack_f16(s, s) & 0xFFFFu;
+}
+template <int F>
+__device__ __forceinline__ uint32_t zero16(const Packed& w, long at) {
+  if constexpr (!is_int4(F)) return 0u;
+  else return 0x4C00u | ((w.z ? w.z[at] & 15u : 8u) << 6);
 }
 
-// columns [k0, k0 + cols) of W, transposed, as fp16 [cols, Np], zeros past N: a block turns 64 rows
-// n and 128 columns k in LDS
+// The 16-bit form of rows [first, first + cols) of W, columns of the product. A wave takes one tile and
+// four steps of 128 of K.
 template <int F, int S>
-__global__ __launch_bounds__(256) void weights16_turned_kernel(Packed w, int k0, int cols, int K, int N, int Np,
-                                                               const int* exponent, uint16_t* out) {
-  constexpr int kPitch = 130;   // halves of a row in LDS: an odd number of dwords
-  __shared__ uint16_t tile[64 * kPitch];
-  const int n0 = blockIdx.x * 64, c0 = blockIdx.y * 128;
-  {
-    const int n = n0 + (threadIdx.x >> 2), k = c0 + (threadIdx.x & 3) * 32;
-    uint32_t v[16] = {};
-    if (n < N && k < cols) fp16_codes<F, S>(w, n, k0 + k, K, exponent[k0 + k], v);
-    uint32_t* t = reinterpret_cast<uint32_t*>(tile + (threadIdx.x >> 2) * kPitch + (threadIdx.x & 3) * 32);
+__global__ __launch_bounds__(512) void weights16_kernel(Weights16 p) {
+  constexpr int G = group_of(F);
+  const int lane = threadIdx.x & 63, i = threadIdx.x >> 6;
+  const int col = blockIdx.x * 128 + 8 * (lane & 15) + i;
+  const long n = p.first + min(col, p.cols - 1);
+  const int e = F == kNv ? 0 : p.eb[n];
+  const long groups = n * (p.K / G);
+  uint16_t* out = p.out + (long)(blockIdx.x * 8 + i) * p.blocks * 512 + lane * 8;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) t[i] = v[i];
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 128 * 8; i += 256) {
-    const int c = i >> 3, n = (i & 7) * 8;
-    if (c0 + c >= cols || n0 + n >= Np) continue;
-    u32x4 v;
+  for (int j = 0; j < 4; ++j) {
+    const int b0 = (blockIdx.y * 4 + j) * 4;      // first block of the step
+    if (b0 >= p.blocks) return;
+    u32x4 q = *reinterpret_cast<const u32x4*>(p.w.q + n * (p.K / 2) + min(b0 + (lane >> 4), p.blocks - 1) * 16);
+    turn4(q);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      v[j] = tile[(n + 2 * j) * kPitch + c] | (uint32_t)tile[(n + 2 * j + 1) * kPitch + c] << 16;
-    *reinterpret_cast<u32x4*>(out + (long)(c0 + c) * Np + n0 + n) = v;
+    for (int t = 0; t < 4; ++t) {
+      if (b0 + t >= p.blocks) continue;
+      const long g = groups + ((b0 + t) * kBlockK + (lane >> 4) * 8) / G;
+      const uint32_t s1 = scale16<F, S>(p.w, g, e), z1 = zero16<F>(p.w, g);
+      const uint32_t s2 = s1 | s1 << 16, z2 = z1 | z1 << 16;
+      const uint32_t s[4] = {s2, s2, s2, s2}, z[4] = {z2, z2, z2, z2};
+      *reinterpret_cast<u32x4*>(out + (long)(b0 + t) * 512) = scaled_codes<F>(q[t], s, z);
+    }
   }
+}
+
+// An 8 x 8 block of codes turned: in, dword j holds row j's eight codes; out, dword i column i's.
+__device__ __forceinline__ void turn_codes(uint32_t (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {   // halves
+    const uint32_t a = v[j], b = v[j + 4];
+    v[j] = __builtin_amdgcn_perm(b, a, 0x05040100u);
+    v[j + 4] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)     // bytes
+    if (!(j & 2)) {
+      const uint32_t a = v[j], b = v[j + 2];
+      v[j] = __builtin_amdgcn_perm(b, a, 0x06020400u);
+      v[j + 2] = __builtin_amdgcn_perm(b, a, 0x07030501u);
+    }
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {   // nibbles
+    const uint32_t a = v[j], b = v[j + 1];
+    v[j] = (a & 0x0F0F0F0Fu) | ((b & 0x0F0F0F0Fu) << 4);
+    v[j + 1] = ((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u);
+  }
+}
+
+// The 16-bit form of columns [first, first + cols) of W. A wave takes 32 rows n, one block of the
+// reduction axis, and 128 columns: each lane an 8 x 8 block of codes, whose rows' scales it multiplies in.
+template <int F, int S>
+__global__ __launch_bounds__(256) void weights16_turned_kernel(Weights16 p) {
+  constexpr int G = group_of(F);
+  const int lane = threadIdx.x & 63, block = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (block >= p.blocks) return;
+  const int c0 = min(blockIdx.y * 128 + 8 * (lane & 15), p.cols - 8);   // cols is a multiple of 32
+  const int k = p.first + c0, e = F == kNv ? 0 : p.eb[k];
+  uint32_t v[8], s1[8], z1[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int row = block * kBlockK + (lane >> 4) * 8 + j;
+    const long n = min(row, p.N - 1), g = n * (p.K / G) + k / G;
+    v[j] = *reinterpret_cast<const uint32_t*>(p.w.q + n * (p.K / 2) + k / 2);
+    s1[j] = scale16<F, S>(p.w, g, e);
+    z1[j] = zero16<F>(p.w, g);
+    if (row >= p.N) {   // zeros past N: 0, or (z - z)
+      v[j] = is_int4(F) ? ((z1[j] >> 6) & 15u) * 0x11111111u : 0u;
+      s1[j] = 0u;
+    }
+  }
+  turn_codes(v);
+  uint32_t s[4], z[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int a = is_int4(F) ? j : 2 * j, b = is_int4(F) ? j + 4 : 2 * j + 1;
+    s[j] = s1[a] | s1[b] << 16;
+    z[j] = z1[a] | z1[b] << 16;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<u32x4*>(p.out + ((long)(blockIdx.y * 8 + i) * p.blocks + block) * 512 + lane * 8) =
+        scaled_codes<F>(v[i], s, z);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -405,85 +550,198 @@ __global__ __launch_bounds__(256) void weights16_turned_kernel(Packed w, int k0,
 // ------------------------------------------------------------------------------------------
 
 struct Product16 {
-  const uint16_t* a;    // fp16 [M, Cp]
+  const uint16_t* a;    // M rows, fragment order
   const int* ea;        // [M]
-  const uint16_t* b;    // fp16 [cols, Cp]
-  const int* eb;        // [cols]
+  const uint16_t* b;    // cols columns, fragment order
+  const int* eb;        // [cols]; null: 0
   const float* g;       // NVFP4's scale of the matrix; null: 1
-  int M, cols, Cp;
+  int M, cols, blocks;
   const uint16_t* base; // [M, cols]; may be null
   long bs;
   uint16_t* y;
   long ys;
+  int splits;           // shares of the reduction axis
+  float* sums;          // [splits][thread blocks][threads][a thread's sums]
+  int* done;            // a ticket a tile
 };
 
-// y[m, c] = base[m, c] + g 2^(ea[m] + eb[c]) sum_i a[m, i] b[c, i]. A block of four waves takes 128 x 128,
-// a wave 64 x 64.
-template <int X>
-__global__ __launch_bounds__(256) void product16_kernel(Product16 p) {
-  __shared__ u32x4 sa[2][kTileM * 8], sb[2][kTileN * 8];   // 8 pieces of 16 bytes a row and step
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int m0 = blockIdx.y * kTileM, c0 = blockIdx.x * kTileN;
-  const int wm = (wave & 1) * 64, wc = (wave >> 1) * 64;
-  const int steps = p.Cp / kStepK;
-  f32x4 acc[4][4];
+template <int N>
+__device__ __forceinline__ void wait_vmem_at_most() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// y[m, c] = base[m, c] + g 2^(ea[m] + eb[c]) sum_i a[m, i] b[c, i]. A wave takes TM x TN tiles, a block
+// WM x WN waves. Blocks of the reduction axis pass through four buffers in LDS, three of them in
+// flight, loaded by copies that go past the registers; a wave reads the next block's fragments
+// while it multiplies the present one's. With splits > 1 the block of a tile that finishes last adds the
+// shares up in their order.
+template <int X, int TM, int TN, int WM, int WN>
+__global__ __launch_bounds__(WM * WN * 64, 1) void product16_kernel(Product16 p) {
+  constexpr int kWaves = WM * WN, kThreads = kWaves * 64, kStages = 4;
+  constexpr int BM = WM * TM, BN = WN * TN, kChunks = BM + BN, kLoads = (kChunks + kWaves - 1) / kWaves;
+  __shared__ u32x4 buffer[kStages][kChunks * 64];
+  __shared__ int s_last;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave % WM, wn = wave / WM;
+  // A thread block runs on XCD (its number mod 8): each XCD gets a run of tiles, column tiles of the
+  // same rows behind one another, so that its L2 holds their operands.
+  const int tiles_n = (p.cols + BN * 16 - 1) / (BN * 16), tiles = gridDim.x;
+  const int per = (tiles + 7) / 8, id = (int)blockIdx.x;
+  int tile = (id & 7) * per + (id >> 3);
+  const int full = tiles % 8 ? tiles % 8 : 8;     // XCDs with `per` tiles; the others have one less
+  if ((id & 7) > full) tile -= (id & 7) - full;
+  const int t_m = tile / tiles_n, t_n = tile % tiles_n;
+  const int m0 = t_m * BM * 16, c0 = t_n * BN * 16;
+  const int per_split = (p.blocks + p.splits - 1) / p.splits;
+  const int from = blockIdx.y * per_split, to = min(p.blocks, from + per_split);
+  // this wave's copies: chunk wave + i * kWaves of the stage, rows' tiles first
+  const uint16_t* src[kLoads];
+  uint32_t dst[kLoads];
+  const int tiles_a = (p.M + 15) / 16, tiles_b = (p.cols + 127) / 128 * 8;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const float g = p.g ? *p.g : 1.f;
-  u32x4 ra[4], rb[4];
-  auto load = [&](int s) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = i * 32 + (threadIdx.x >> 3), piece = threadIdx.x & 7;
-      ra[i] = *reinterpret_cast<const u32x4*>(p.a + (long)min(m0 + r, p.M - 1) * p.Cp + s * kStepK + piece * 8);
-      rb[i] = *reinterpret_cast<const u32x4*>(p.b + (long)min(c0 + r, p.cols - 1) * p.Cp + s * kStepK + piece * 8);
-    }
-  };
-  auto store = [&](int buf) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = i * 32 + (threadIdx.x >> 3), piece = (threadIdx.x & 7) ^ (r & 7);
-      sa[buf][r * 8 + piece] = ra[i];
-      sb[buf][r * 8 + piece] = rb[i];
-    }
-  };
-  load(0);
-  store(0);
-  __syncthreads();
-  for (int s = 0; s < steps; ++s) {
-    const int buf = s & 1;
-    if (s + 1 < steps) load(s + 1);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      u32x4 a[4], b[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int piece = (h * 4 + (lane >> 4)) ^ (lane & 7);
-        a[i] = sa[buf][(wm + i * 16 + (lane & 15)) * 8 + piece];
-        b[i] = sb[buf][(wc + i * 16 + (lane & 15)) * 8 + piece];
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = mfma16<kHf>(a[i], b[j], acc[i][j]);
-    }
-    if (s + 1 < steps) store(buf ^ 1);
-    __syncthreads();
+  for (int i = 0; i < kLoads; ++i) {
+    const int chunk = min(wave + i * kWaves, kChunks - 1);
+    const long t = chunk < BM ? min(t_m * BM + chunk, tiles_a - 1) : min(t_n * BN + chunk - BM, tiles_b - 1);
+    src[i] = (chunk < BM ? p.a : p.b) + t * p.blocks * 512;
+    dst[i] = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)&buffer[0][chunk * 64];
   }
+  auto copy = [&](int block) {   // past the last: a stand-in that nobody reads, so that the waits can count
+    const long at = (long)min(block, to - 1) * 512;
+    const uint32_t off = (uint32_t)((block - from) & (kStages - 1)) * (kChunks * 1024);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kLoads; ++i)
+      asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst[i] + off), "v"(lane * 16), "s"(src[i] + at)
+                   : "memory", "m0");
+  };
+  f32x4 acc[TM][TN];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+  for (int i = 0; i < TM; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int m = m0 + wm + i * 16 + (lane >> 4) * 4 + e, c = c0 + wc + j * 16 + (lane & 15);
-        if (m >= p.M || c >= p.cols) continue;
-        float v = ldexpf(acc[i][j][e], p.ea[m] + p.eb[c]) * g;
-        if (p.base) v += to_f32<X>(p.base[m * p.bs + c]);
-        p.y[m * p.ys + c] = from_f32<X>(v);
+    for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  u32x4 a[2][TM], b[2][TN];
+  auto read = [&](u32x4(&fa)[TM], u32x4(&fb)[TN], int block) __attribute__((always_inline)) {
+    const u32x4* s = buffer[(block - from) & (kStages - 1)];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) fa[i] = s[(wm * TM + i) * 64 + lane];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) fb[j] = s[(BM + wn * TN + j) * 64 + lane];
+  };
+  auto multiply = [&](const u32x4(&fa)[TM], const u32x4(&fb)[TN]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = mfma16<kHf>(fa[i], fb[j], acc[i][j]);
+  };
+  // Block k is in LDS once each wave has waited for its own copies of it and all have met. The buffer
+  // that is then filled held block k - 1, whose fragments every wave had before the meeting.
+  auto arrive = [&](int block) __attribute__((always_inline)) {
+    wait_vmem_at_most<2 * kLoads>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    copy(block + 3);
+  };
+  if (from < to) {
+    copy(from);
+    copy(from + 1);
+    copy(from + 2);
+    arrive(from);
+    read(a[0], b[0], from);
+    for (int k = from; k < to; k += 2) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // this block's fragments, before their buffer goes
+      arrive(k + 1);
+      read(a[1], b[1], k + 1);
+      multiply(a[0], b[0]);
+      if (k + 1 >= to) break;
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      arrive(k + 2);
+      read(a[0], b[0], k + 2);
+      multiply(a[1], b[1]);
+    }
+    wait_vmem_at_most<0>();
+  }
+  // The sums go through LDS, so that what follows is a loop (unrolled over the registers it would be
+  // 30 to 100 KB of code that each wave runs once): DI rows of tiles at a time, in the wave's own part.
+  __syncthreads();
+  constexpr int DI = TM * TN <= kChunks * kStages / kWaves ? TM : TM / 2;
+  f32x4* dump = reinterpret_cast<f32x4*>(&buffer[0][0]) + wave * (DI * TN * 64);
+  const float g = p.g ? *p.g : 1.f;
+  constexpr int kRun = TN < 8 ? TN : 8;      // neighbouring columns a lane has
+  struct __attribute__((packed, aligned(2))) Run { uint16_t h[kRun]; };
+#pragma unroll
+  for (int i0 = 0; i0 < TM; i0 += DI) {
+#pragma unroll
+    for (int i = 0; i < DI; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) dump[(i * TN + j) * 64 + lane] = acc[i0 + i][j];
+    if (DI == TM && p.splits > 1) {
+      constexpr int kTiles = TM * TN;
+      const long share = (long)gridDim.x * (kThreads * kTiles * 4);
+      float* sums = p.sums + ((long)tile * kWaves + wave) * (kTiles * 256) + lane;
+      float* own = sums + blockIdx.y * share;
+#pragma nounroll
+      for (int t = 0; t < kTiles; ++t) {
+        const f32x4 v = dump[t * 64 + lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          __hip_atomic_store(own + t * 256 + e * 64, v[e], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
+      wait_vmem_at_most<0>();
+      __syncthreads();
+      if (threadIdx.x == 0)
+        s_last = __hip_atomic_fetch_add(p.done + tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == p.splits - 1;
+      __syncthreads();
+      if (!s_last) return;
+#pragma nounroll
+      for (int t = 0; t < kTiles; ++t) {
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+        for (int z = 0; z < p.splits; z += 4) {   // four shares requested at a time, added in their order
+          float u[4][4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              u[q][e] = __hip_atomic_load(sums + min(z + q, p.splits - 1) * share + t * 256 + e * 64, __ATOMIC_RELAXED,
+                                          __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += z + q < p.splits ? u[q][e] : 0.f;
+        }
+        dump[t * 64 + lane] = v;
+      }
+    }
+#pragma nounroll
+    for (int j0 = 0; j0 < TN; j0 += kRun) {
+      const int t = wn * TN + j0, c = c0 + (t >> 3) * 128 + 8 * (lane & 15) + (t & 7);
+      if (c >= p.cols) continue;
+      int eb[kRun];
+#pragma unroll
+      for (int j = 0; j < kRun; ++j) eb[j] = p.eb ? p.eb[min(c + j, p.cols - 1)] : 0;
+#pragma nounroll
+      for (int r = 0; r < DI * 4; ++r) {
+        const int m = m0 + (wm * TM + i0 + (r >> 2)) * 16 + (lane >> 4) * 4 + (r & 3);
+        if (m >= p.M) continue;
+        const int ea = p.ea[m];
+        const float* from_lds = reinterpret_cast<const float*>(dump + ((r >> 2) * TN + j0) * 64 + lane) + (r & 3);
+        float v[kRun];
+#pragma unroll
+        for (int j = 0; j < kRun; ++j) v[j] = ldexpf(from_lds[j * 256], ea + eb[j]) * g;
+        uint16_t* y = p.y + m * p.ys + c;
+        const uint16_t* base = p.base ? p.base + m * p.bs + c : nullptr;
+        if (c + kRun <= p.cols) {
+          Run o;
+          if (base) o = *reinterpret_cast<const Run*>(base);
+#pragma unroll
+          for (int j = 0; j < kRun; ++j) o.h[j] = from_f32<X>(v[j] + (base ? to_f32<X>(o.h[j]) : 0.f));
+          *reinterpret_cast<Run*>(y) = o;
+        } else {
+#pragma unroll
+          for (int j = 0; j < kRun; ++j)
+            if (c + j < p.cols) y[j] = from_f32<X>(v[j] + (base ? to_f32<X>(base[j]) : 0.f));
+        }
+      }
+    }
+  }
 }
 
 // ------------------------------------------------------------------------------------------
@@ -496,27 +754,42 @@ constexpr int kRowsMax = 64;   // rows the packed product takes
 
 size_t pad256(size_t v) { return (v + 255) & ~size_t(255); }
 long up(long v, long to) { return (v + to - 1) / to * to; }
+int cdiv(long a, long b) { return (int)((a + b - 1) / b); }
 
-// Scratch of the tiled product: reduction axis C, output columns O.
+// How the tiled product of M rows and O columns over C runs: its tile (64 x 64 a wave or 128 x 128, or
+// 32 rows and 32 columns a wave for few rows), shares of the reduction axis, scratch.
+enum : int { kThin = 0, kMiddle = 1, kLarge = 2 };
 struct Plan16 {
-  long Cp = 0, slab = 0;          // padded reduction axis, output columns a slab
-  size_t rows = 0, ea = 0, eb = 0, weights = 0, total = 0;
+  int tile = kMiddle, blocks = 0, splits = 1;
+  long slab = 0;          // output columns a slab
+  size_t rows = 0, ea = 0, eb = 0, weights = 0, sums = 0, done = 0, total = 0;
+  int bm() const { return tile == kThin ? 32 : tile == kMiddle ? 128 : 256; }
+  int bn() const { return tile == kThin ? 128 : tile == kMiddle ? 128 : 256; }
+  int tiles(long M, long cols) const { return cdiv(M, bm()) * cdiv(cols, bn()); }
 };
 Plan16 plan16(long M, long C, long O) {
   Plan16 p;
-  p.Cp = up(C, kStepK);
-  p.slab = std::max<long>(128, kSlabBytes / (p.Cp * 2) / 128 * 128);
-  p.slab = std::min(p.slab, up(O, 128));
+  p.blocks = cdiv(C, kBlockK);
+  p.slab = std::max<long>(256, kSlabBytes / (p.blocks * 64l) / 256 * 256);
+  p.slab = std::min(p.slab, up(O, 256));
+  const long cols = std::min(p.slab, O);
+  p.tile = M <= 32 ? kThin : kMiddle;
+  if (p.tile == kMiddle && cdiv(M, 256) * cdiv(cols, 256) >= 192) p.tile = kLarge;
+  // shares: to two blocks a CU, of at least eight blocks each
+  const int tiles = p.tiles(M, cols);
+  if (p.tile != kLarge) p.splits = std::max(1, std::min({512 / std::max(tiles, 1), p.blocks / 8, 16}));
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t r = at;
     at += pad256(bytes);
     return r;
   };
-  p.rows = take((size_t)M * p.Cp * 2);
+  p.rows = take((size_t)up(M, 16) * p.blocks * 64);
   p.ea = take((size_t)M * 4);
   p.eb = take((size_t)up(O, 128) * 4);
-  p.weights = take((size_t)p.slab * p.Cp * 2);
+  p.weights = take((size_t)up(p.slab, 128) * p.blocks * 64);
+  p.sums = take(p.splits == 1 ? 0 : (size_t)p.splits * tiles * p.bm() * p.bn() * 4);
+  p.done = take((size_t)tiles * 4);
   p.total = at;
   return p;
 }
@@ -534,26 +807,35 @@ hipError_t launch_tiled(const Linear& p, char* scratch, hipStream_t s) {
   uint16_t* rows = reinterpret_cast<uint16_t*>(scratch + plan.rows);
   int* ea = reinterpret_cast<int*>(scratch + plan.ea);
   int* eb = reinterpret_cast<int*>(scratch + plan.eb);
+  int* done = reinterpret_cast<int*>(scratch + plan.done);
   uint16_t* weights = reinterpret_cast<uint16_t*>(scratch + plan.weights);
-  const int Cp = (int)plan.Cp;
-  hipLaunchKernelGGL((rows16_kernel<X>), dim3((unsigned)p.M), dim3(256), 0, s, p.x, p.xs, C, Cp, rows, ea);
-  RETURN_IF(hipGetLastError());
-  hipLaunchKernelGGL((column_exponent_kernel<F, X, BACK>), dim3((unsigned)(BACK ? O / group_of(F) : O)), dim3(256), 0, s,
-                     p.w, p.K, p.N, eb);
-  RETURN_IF(hipGetLastError());
   for (long o = 0; o < O; o += plan.slab) {
     const int cols = (int)std::min<long>(plan.slab, O - o);
+    const int tiles = plan.tiles(p.M, cols);
+    if (o == 0 || plan.splits > 1) {   // later slabs need the tickets at zero only
+      const int row_blocks = o == 0 ? cdiv(p.M, 16) : 0;
+      const int more = o > 0 ? 1 : F == kNv ? 0 : BACK ? cdiv(O / group_of(F), 8) : cdiv(O, kPrepThreads / 64);
+      const Prep prep{p.x, p.xs, p.M, C, plan.blocks, rows, ea, row_blocks, p.w, p.K, p.N, eb, done,
+                      plan.splits > 1 ? tiles : 0};
+      hipLaunchKernelGGL((linear_prep_kernel<F, X, BACK>), dim3((unsigned)(row_blocks + more)), dim3(kPrepThreads), 0, s,
+                         prep);
+      RETURN_IF(hipGetLastError());
+    }
+    const Weights16 w{p.w, p.K, p.N, (int)o, cols, plan.blocks, eb, weights};
     if constexpr (BACK)
-      hipLaunchKernelGGL((weights16_turned_kernel<F, X>), dim3((unsigned)(Cp / 64), (unsigned)((cols + 127) / 128)),
-                         dim3(256), 0, s, p.w, (int)o, cols, p.K, p.N, Cp, eb, weights);
+      hipLaunchKernelGGL((weights16_turned_kernel<F, X>), dim3((unsigned)cdiv(plan.blocks, 4), (unsigned)cdiv(cols, 128)),
+                         dim3(256), 0, s, w);
     else
-      hipLaunchKernelGGL((weights16_kernel<F, X>), dim3((unsigned)(((long)cols * (Cp / 32) + 255) / 256)), dim3(256), 0,
-                         s, p.w, (int)o, cols, p.K, Cp, eb, weights);
+      hipLaunchKernelGGL((weights16_kernel<F, X>), dim3((unsigned)cdiv(cols, 128), (unsigned)cdiv(plan.blocks, 16)),
+                         dim3(512), 0, s, w);
     RETURN_IF(hipGetLastError());
-    const Product16 q{rows, ea, weights, eb + o, F == kNv ? p.w.g : nullptr, p.M, cols, Cp, p.base ? p.base + o : nullptr, p.bs, p.y + o, p.ys};
-    hipLaunchKernelGGL((product16_kernel<X>), dim3((unsigned)((cols + kTileN - 1) / kTileN),
-                                                   (unsigned)((p.M + kTileM - 1) / kTileM)),
-                       dim3(256), 0, s, q);
+    const Product16 q{rows, ea, weights, F == kNv ? nullptr : eb + o, F == kNv ? p.w.g : nullptr, p.M, cols, plan.blocks,
+                      p.base ? p.base + o : nullptr, p.bs, p.y + o, p.ys, plan.splits,
+                      reinterpret_cast<float*>(scratch + plan.sums), done};
+    const dim3 grid((unsigned)tiles, (unsigned)plan.splits);
+    if (plan.tile == kThin) hipLaunchKernelGGL((product16_kernel<X, 2, 2, 1, 4>), grid, dim3(256), 0, s, q);
+    else if (plan.tile == kMiddle) hipLaunchKernelGGL((product16_kernel<X, 4, 4, 2, 2>), grid, dim3(256), 0, s, q);
+    else hipLaunchKernelGGL((product16_kernel<X, 8, 4, 2, 4>), grid, dim3(512), 0, s, q);
     RETURN_IF(hipGetLastError());
   }
   return hipSuccess;
