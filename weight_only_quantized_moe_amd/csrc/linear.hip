@@ -35,23 +35,24 @@ struct LinearRows {
   long ys;
 };
 
-// Up to 16 rows, K a multiple of 256: a wave keeps its PX pairs of steps of the rows in registers (x is
+// Up to 16 rows, K at least 256: a wave keeps its PX pairs of steps of the rows in registers (x is
 // read once a block, however many columns the block takes), and the codes of the next columns are
 // requested pair by pair as those of the present ones are used up. A block takes items of 16 R
 // columns, grid-strided; the waves' sums of an item meet in LDS.
-template <int F, int X, int R, int PX>
+template <int F, int X, int R, int PX, bool EXACT>
 __global__ __launch_bounds__(512, PX == 1 ? 4 : 2) void linear_wide_kernel(LinearRows p) {
   extern __shared__ float red[];   // [2][waves][R * 256]
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int K = p.K, items = (p.N + 16 * R - 1) / (16 * R);
-  const PairShare share = pair_share(wave, K / 256, PX);
+  const int pairs = (K + 255) / 256;
+  const PairShare share = pair_share(wave, pairs, PX);
   u32x4 a[PX][2][1][4][1];
   PairCodes c[PX][R];
   StepScales<F, 2 * PX> now[R], then[R];
   // A tile that would end past N starts earlier (rows past N are stand-ins only where N < 16); the
   // columns before its own are another item's.
-  const TileLane at = tile_lane<F, 2 * PX>(lane, K, p.N);
+  const TileLane<EXACT> at = tile_lane<F, 2 * PX, EXACT>(lane, K, p.N, 2 * share.first);
   auto tile_of = [&](int item, int r) __attribute__((always_inline)) {
     return max(0, min(item * (16 * R) + 16 * r, p.N - 16));
   };
@@ -59,12 +60,13 @@ __global__ __launch_bounds__(512, PX == 1 ? 4 : 2) void linear_wide_kernel(Linea
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const TileBase t = tile_base<F>(p.w, tile_of(item, r), K, 2 * share.first);
-      load_scales(to[r], t.s, t.z, at);
+      load_scales<F, 2 * PX, EXACT>(to[r], t.s, t.z, at);
     }
   };
   auto codes = [&](int j, int item) __attribute__((always_inline)) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) load_pair(c[j][r], tile_base<F>(p.w, tile_of(item, r), K, 2 * (share.first + j)).q, at);
+    for (int r = 0; r < R; ++r)
+      load_pair(c[j][r], tile_base<F>(p.w, tile_of(item, r), K, 2 * (share.first + j)).q, at, share.first + j == pairs - 1);
   };
   int item = blockIdx.x;
   scales(now, item);
@@ -73,7 +75,7 @@ __global__ __launch_bounds__(512, PX == 1 ? 4 : 2) void linear_wide_kernel(Linea
   // rows past M are stand-ins: their sums are not written
   const uint16_t* x = p.x + (long)min(lane & 15, p.M - 1) * p.xs + (lane >> 4) * 8;
 #pragma unroll
-  for (int j = 0; j < 2 * PX; ++j) load_rows<F, true>(a[j >> 1][j & 1], x, 2 * share.first + j, K);
+  for (int j = 0; j < 2 * PX; ++j) load_pair_rows<F, EXACT>(a[j >> 1][j & 1], x, 2 * share.first + j, K);
   const float g = F == kNv ? p.w.g[0] : 1.f;
   for (int buf = 0;; buf ^= 1) {
     const int next = item + gridDim.x;
@@ -122,25 +124,27 @@ __global__ __launch_bounds__(512, PX == 1 ? 4 : 2) void linear_wide_kernel(Linea
   }
 }
 
-template <int F, int X, int R, int PX>
+template <int F, int X, int R, int PX, bool EXACT>
 hipError_t run_wide(const LinearRows& p, hipStream_t s) {
-  const int items = (p.N + 16 * R - 1) / (16 * R), waves = (p.K / 256 + PX - 1) / PX;
+  const int items = (p.N + 16 * R - 1) / (16 * R), waves = ((p.K + 255) / 256 + PX - 1) / PX;
   const int blocks = std::min(items, 256 * (PX == 1 ? 16 / waves : 1));
-  hipLaunchKernelGGL((linear_wide_kernel<F, X, R, PX>), dim3((unsigned)blocks), dim3((unsigned)(waves * 64)),
+  hipLaunchKernelGGL((linear_wide_kernel<F, X, R, PX, EXACT>), dim3((unsigned)blocks), dim3((unsigned)(waves * 64)),
                      (size_t)2 * waves * R * 1024, s, p);
   return hipGetLastError();
 }
 
-constexpr int kWideMaxK = 8 * 4 * 256;   // eight waves of four pairs
+// eight waves of four pairs, or of two where the last pair is partial
+constexpr int wide_max_k(bool exact) { return 8 * (exact ? 4 : 2) * 256; }
 
 template <int F, int X>
 hipError_t launch_wide(const LinearRows& p, hipStream_t s) {
-  const int pairs = p.K / 256;
+  const int pairs = (p.K + 255) / 256;
   const bool two = p.N >= 256 * 32;
-  if (pairs <= 8) return two ? run_wide<F, X, 2, 1>(p, s) : run_wide<F, X, 1, 1>(p, s);
-  if (pairs <= 16) return two ? run_wide<F, X, 2, 2>(p, s) : run_wide<F, X, 1, 2>(p, s);
-  if (pairs <= 24) return run_wide<F, X, 1, 3>(p, s);
-  return run_wide<F, X, 1, 4>(p, s);
+  if (p.K % 256) return pairs <= 8 ? run_wide<F, X, 1, 1, false>(p, s) : run_wide<F, X, 1, 2, false>(p, s);
+  if (pairs <= 8) return two ? run_wide<F, X, 2, 1, true>(p, s) : run_wide<F, X, 1, 1, true>(p, s);
+  if (pairs <= 16) return two ? run_wide<F, X, 2, 2, true>(p, s) : run_wide<F, X, 1, 2, true>(p, s);
+  if (pairs <= 24) return run_wide<F, X, 1, 3, true>(p, s);
+  return run_wide<F, X, 1, 4, true>(p, s);
 }
 
 // A block: 16 R columns n and 16 T rows m, the steps of 128 of K dealt to its waves. D: steps a
@@ -240,7 +244,7 @@ template <int F, int X>
 hipError_t launch_rows(const LinearRows& p, hipStream_t s) {
   const int steps = std::max(1, p.K / 128);
   const int waves = std::min(8, steps);
-  if (p.M <= 16 && p.K % 256 == 0 && p.K <= kWideMaxK) return launch_wide<F, X>(p, s);
+  if (p.M <= 16 && p.K >= 256 && p.K <= wide_max_k(p.K % 256 == 0)) return launch_wide<F, X>(p, s);
   if (p.M <= 16) return run_rows<F, X, 1, 1, 2>(p, waves, s);
   if (p.M <= 32) return run_rows<F, X, 2, 2, 1>(p, waves, s);
   return run_rows<F, X, 2, 4, 1>(p, std::min(waves, 4), s);

@@ -308,7 +308,7 @@ __device__ __forceinline__ void load_rows(u32x4 (&a)[1][4][1], const uint16_t* p
 }
 
 // ------------------------------------------------------------------------------------------
-// Pairs of steps: rows of whole multiples of 256 columns
+// Pairs of steps: rows of at least 256 columns
 // ------------------------------------------------------------------------------------------
 // A pair of steps covers whole 128-byte lines of codes: one load takes rows 0 to 7 of the tile, the
 // other rows 8 to 15, and two lanes eight apart exchange what is the other's. The scales of a wave's
@@ -327,16 +327,30 @@ struct PairCodes {
 
 // The lane's places in a tile of 16 rows, as 32-bit offsets from the tile's first row, so that a load
 // takes a scalar base and one register: of its piece of rows 0 to 7 (lo) and 8 to 15 (hi), and of its
-// row's scales and zero points. Rows at and past `rows` are stand-ins.
+// row's scales and zero points. Rows at and past `rows` are stand-ins. Where K is not a multiple of 256
+// (EXACT false), the last pair is partial: pieces past K are stand-ins too (lo_end, hi_end), whose
+// columns meet zeros of x, and scales that would reach past the row are loaded from further in front
+// and shifted, zeros coming in.
+template <bool EXACT>
 struct TileLane {
   uint32_t lo, hi, s, z;
 };
-template <int F, int STEPS>
-__device__ __forceinline__ TileLane tile_lane(int lane, int K, int rows);
+template <>
+struct TileLane<false> {
+  uint32_t lo, hi, s, z, lo_end, hi_end;
+  int s_shift, z_shift;    // bits, per 8 bytes of the load
+  int s_shift2, z_shift2;  // of its second 8 bytes
+};
 
-__device__ __forceinline__ void load_pair(PairCodes& c, const uint8_t* tile, const TileLane& at) {
-  c.a = *reinterpret_cast<const u32x4*>(tile + at.lo);
-  c.b = *reinterpret_cast<const u32x4*>(tile + at.hi);
+template <bool EXACT>
+__device__ __forceinline__ void load_pair(PairCodes& c, const uint8_t* tile, const TileLane<EXACT>& at, bool end) {
+  uint32_t lo = at.lo, hi = at.hi;
+  if constexpr (!EXACT) {
+    lo = end ? at.lo_end : lo;
+    hi = end ? at.hi_end : hi;
+  }
+  c.a = *reinterpret_cast<const u32x4*>(tile + lo);
+  c.b = *reinterpret_cast<const u32x4*>(tile + hi);
 }
 __device__ __forceinline__ void split_pair(PairCodes& c) {
   const bool up = threadIdx.x & 8;
@@ -374,25 +388,59 @@ __device__ __forceinline__ void load_bytes(uint32_t* out, const uint8_t* p) {
   }
 }
 
-template <int F, int STEPS>
-__device__ __forceinline__ TileLane tile_lane(int lane, int K, int rows) {
-  constexpr int Q = StepScales<F, STEPS>::Q;
-  const int piece = ((lane >> 4) + ((lane >> 3) & 1) * 4) * 16, half = K / 2, groups = K / group_of(F);
-  const int step = min(lane >> 4, STEPS / Q - 1) * Q, row = min(lane & 15, rows - 1);
-  return {(uint32_t)(min(lane & 7, rows - 1) * half + piece), (uint32_t)(min(8 + (lane & 7), rows - 1) * half + piece),
-          (uint32_t)(row * groups * scale_bytes(F) + step * step_scale_bytes<F>()),
-          (uint32_t)(row * groups + step * step_zero_bytes<F>())};
+// first: the first of the wave's steps (in pairs, so even)
+template <int F, int STEPS, bool EXACT>
+__device__ __forceinline__ TileLane<EXACT> tile_lane(int lane, int K, int rows, int first) {
+  using T = StepScales<F, STEPS>;
+  constexpr int Q = T::Q;
+  const int place = (lane >> 4) + ((lane >> 3) & 1) * 4, half = K / 2, groups = K / group_of(F);
+  const int step = first + min(lane >> 4, STEPS / Q - 1) * Q, row = min(lane & 15, rows - 1);
+  const int lo = min(lane & 7, rows - 1) * half, hi = min(8 + (lane & 7), rows - 1) * half;
+  const int s = step * step_scale_bytes<F>(), z = step * step_zero_bytes<F>();
+  TileLane<EXACT> t;
+  t.lo = lo + place * 16;
+  t.hi = hi + place * 16;
+  t.s = row * groups * scale_bytes(F) + s;
+  t.z = row * groups + z;
+  if constexpr (!EXACT) {
+    const bool inside = K / 256 * 128 + place * 16 < half;
+    t.lo_end = lo + (inside ? place * 16 : 0);
+    t.hi_end = hi + (inside ? place * 16 : 0);
+    // how far each load (of at most 8 bytes) reaches past the row's end
+    constexpr int sn = T::kBytes < 8 ? T::kBytes : 8, zn = T::kZeros < 8 ? T::kZeros : 8;
+    t.s_shift = 8 * max(0, s + sn - groups * scale_bytes(F));
+    t.z_shift = 8 * max(0, z + zn - groups);
+    t.s_shift2 = 8 * max(0, s + 16 - groups * scale_bytes(F));
+    t.z_shift2 = 0;
+  }
+  return t;
 }
 
-// s, z: the tile's first row at the wave's first step, all of whose steps lie inside the row; z null: 8
-// everywhere (the load then takes scales instead, which are no fewer bytes, so that no load stands
-// behind a condition)
-template <int F, int STEPS>
+// N bytes (at most 8) at p that reach `shift` bits past what may be read: those come as zeros
+template <int N>
+__device__ __forceinline__ void load_shifted(uint32_t* out, const uint8_t* p, int shift) {
+  uint32_t w[2] = {0u, 0u};
+  load_bytes<N>(w, p - shift / 8);
+  uint64_t v = (uint64_t)w[1] << 32 | w[0];
+  v = shift < 8 * N ? v >> shift : 0ull;
+  out[0] = (uint32_t)v;
+  if constexpr (N == 8) out[1] = (uint32_t)(v >> 32);
+}
+
+// s, z: the tile's first row; z null: 8 everywhere (the load then takes scales instead, which are no
+// fewer bytes, so that no load stands behind a condition)
+template <int F, int STEPS, bool EXACT>
 __device__ __forceinline__ void load_scales(StepScales<F, STEPS>& v, const uint8_t* s, const uint8_t* z,
-                                            const TileLane& at) {
+                                            const TileLane<EXACT>& at) {
   using T = StepScales<F, STEPS>;
-  load_bytes<T::kBytes>(v.s, s + at.s);
-  if constexpr (is_int4(F)) load_bytes<T::kZeros>(v.z, (z ? z : s) + at.z);
+  if constexpr (EXACT) {
+    load_bytes<T::kBytes>(v.s, s + at.s);
+    if constexpr (is_int4(F)) load_bytes<T::kZeros>(v.z, (z ? z : s) + at.z);
+  } else {
+    load_shifted<T::kBytes < 8 ? T::kBytes : 8>(v.s, s + at.s, at.s_shift);
+    if constexpr (T::kBytes == 16) load_shifted<8>(v.s + 2, s + at.s + 8, at.s_shift2);
+    if constexpr (is_int4(F)) load_shifted<T::kZeros>(v.z, (z ? z : s) + at.z, at.z_shift);
+  }
 }
 template <int F, int STEPS>
 __device__ __forceinline__ void default_zeros(StepScales<F, STEPS>& v, bool given) {
@@ -402,7 +450,7 @@ __device__ __forceinline__ void default_zeros(StepScales<F, STEPS>& v, bool give
   }
 }
 
-// A tile's first row, n rows into the matrix, and its parts at a wave's first step.
+// A tile's first row, n rows into the matrix: its codes at a step, its scales and zero points.
 struct TileBase {
   const uint8_t* q;
   const uint8_t* s;
@@ -411,8 +459,7 @@ struct TileBase {
 template <int F>
 __device__ __forceinline__ TileBase tile_base(const Packed& w, long n, int K, int step) {
   const long groups = n * (K / group_of(F));
-  return {w.q + n * (K / 2) + step * 64, w.s + groups * scale_bytes(F) + step * step_scale_bytes<F>(),
-          is_int4(F) && w.z ? w.z + groups + step * step_zero_bytes<F>() : nullptr};
+  return {w.q + n * (K / 2) + step * 64, w.s + groups * scale_bytes(F), is_int4(F) && w.z ? w.z + groups : nullptr};
 }
 
 // the value that lane quarter Q of the row holds, in all four
@@ -480,6 +527,21 @@ struct PairShare {
 };
 __device__ __forceinline__ PairShare pair_share(int wave, int pairs, int PX) {
   return {min(wave * PX, pairs - PX), wave * PX};
+}
+
+// load_rows of a step that may lie past K in part or in whole: zeros there
+template <int F, bool EXACT>
+__device__ __forceinline__ void load_pair_rows(u32x4 (&a)[1][4][1], const uint16_t* p, int step, int K) {
+  if constexpr (EXACT) {
+    load_rows<F, true>(a, p, step, K);
+  } else {
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int c = step * 128 + b * 32;
+      a[0][b][0] = load16(p + min(c, K - 32)) & (c < K ? ~0u : 0u);
+      if constexpr (is_int4(F)) a[0][b][0] = int4_order(a[0][b][0]);
+    }
+  }
 }
 
 }  // namespace hmoe

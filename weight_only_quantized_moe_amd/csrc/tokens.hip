@@ -25,6 +25,7 @@ namespace {
 constexpr int kUpWaves = 8, kDownWaves = 8;
 constexpr int kRouterK = 1024;     // columns a block of the router takes
 constexpr int kDownCols = 64;      // columns of y a block of the second products takes
+constexpr int kMaxShares = 16;     // of the experts' steps
 constexpr int kMaxPairs = HMOE_TOKENS_MAX_M * kMaxTopK;   // (token, expert) pairs, so also experts in use
 
 // What the second launch leaves for the third.
@@ -57,7 +58,7 @@ TokensScratch tokens_plan(int M, int E, int H, int I, int k, int S) {
   // shares for two blocks a CU, and not more than give every wave a step
   const long steps = (long)std::min(M * k, E) * cdiv(I, 128) + cdiv(S, 128);
   t.tiles = cdiv(H, kDownCols);
-  t.shares = (int)std::max(1l, std::min({16l, 512l / t.tiles, steps / kDownWaves}));
+  t.shares = (int)std::max(1l, std::min({(long)kMaxShares, 512l / t.tiles, steps / kDownWaves}));
   t.sums = take((size_t)t.shares * t.tiles * M * kDownCols * 4);
   t.done = take((size_t)t.tiles * 4);
   return t;
@@ -328,10 +329,10 @@ __device__ __forceinline__ void finish_item(const TokensArgs& a, const Routing& 
   }
 }
 
-// Routing and the first products, H a multiple of 256. Every item multiplies the same tokens, so a
+// Routing and the first products, H at least 256 (EXACT: a multiple of it). Every item multiplies the same tokens, so a
 // wave keeps its PX pairs of steps of x in registers, and it requests the next item's codes pair by
 // pair as those of the present one are used up.
-template <int F, int X, int PX>
+template <int F, int X, int PX, bool EXACT>
 __global__ __launch_bounds__(kUpWaves * 64, PX == 1 ? 4 : 2) void tokens_up_kernel(TokensArgs a) {
   __shared__ Routing s;
   __shared__ float red[2][kUpWaves][2][256];        // the waves' sums; before, the waves' keys
@@ -339,11 +340,12 @@ __global__ __launch_bounds__(kUpWaves * 64, PX == 1 ? 4 : 2) void tokens_up_kern
   const Tokens& p = a.p;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int H = p.H;
-  const PairShare share = pair_share(wave, H / 256, PX);
+  const int pairs = (H + 255) / 256;
+  const PairShare share = pair_share(wave, pairs, PX);
   u32x4 xv[PX][2][1][4][1];
   const uint16_t* x = p.x + (long)min(lane & 15, p.M - 1) * p.xs + (lane >> 4) * 8;
 #pragma unroll
-  for (int j = 0; j < 2 * PX; ++j) load_rows<F, true>(xv[j >> 1][j & 1], x, 2 * share.first + j, H);
+  for (int j = 0; j < 2 * PX; ++j) load_pair_rows<F, EXACT>(xv[j >> 1][j & 1], x, 2 * share.first + j, H);
   route_block(a, s, reinterpret_cast<uint32_t*>(&red[0][0][0][0]));
   const int items = s.count * (p.I / 16) + p.S / 16;
   int item = blockIdx.x;
@@ -352,7 +354,7 @@ __global__ __launch_bounds__(kUpWaves * 64, PX == 1 ? 4 : 2) void tokens_up_kern
 
   PairCodes c[PX][2];
   StepScales<F, 2 * PX> now[2], then[2];
-  const TileLane at = tile_lane<F, 2 * PX>(lane, H, 16);
+  const TileLane<EXACT> at = tile_lane<F, 2 * PX, EXACT>(lane, H, 16, 2 * share.first);
   TileBase gate, up;
   auto rows_of = [&](const Item& v) __attribute__((always_inline)) {
     const Packed w = pick(v.shared, p.s13, p.w13);
@@ -361,12 +363,12 @@ __global__ __launch_bounds__(kUpWaves * 64, PX == 1 ? 4 : 2) void tokens_up_kern
     up = tile_base<F>(w, row0 + v.width, H, 2 * share.first);
   };
   auto scales = [&](StepScales<F, 2 * PX>(&to)[2]) __attribute__((always_inline)) {
-    load_scales(to[0], gate.s, gate.z, at);
-    load_scales(to[1], up.s, up.z, at);
+    load_scales<F, 2 * PX, EXACT>(to[0], gate.s, gate.z, at);
+    load_scales<F, 2 * PX, EXACT>(to[1], up.s, up.z, at);
   };
   auto codes = [&](int j) __attribute__((always_inline)) {
-    load_pair(c[j][0], gate.q + j * 128, at);
-    load_pair(c[j][1], up.q + j * 128, at);
+    load_pair(c[j][0], gate.q + j * 128, at, share.first + j == pairs - 1);
+    load_pair(c[j][1], up.q + j * 128, at, share.first + j == pairs - 1);
   };
   Item it = item_of<F>(p, s, item);
   rows_of(it);
@@ -413,7 +415,7 @@ __global__ __launch_bounds__(kUpWaves * 64, PX == 1 ? 4 : 2) void tokens_up_kern
   }
 }
 
-// The same for every other H: a step at a time, x read again for each item.
+// The same for every other H, narrower or wider: a step at a time, x read again for each item.
 template <int F, int X>
 __global__ __launch_bounds__(kUpWaves * 64, 2) void tokens_up_any_kernel(TokensArgs a) {
   __shared__ Routing s;
@@ -462,9 +464,9 @@ __global__ __launch_bounds__(kUpWaves * 64, 2) void tokens_up_any_kernel(TokensA
 // y: a block takes 64 columns and one share of the steps of all experts in use, dealt evenly to its
 // waves; four row tiles of W2 meet each piece of h that a wave loads. With several shares the
 // block that finishes last adds them up in their order: a share is written past the caches of its
-// own XCD, then counted. PAIRS: I and S are multiples of 256, and a wave's unit is a pair of steps;
-// else it is a step.
-template <int F, int X, bool PAIRS>
+// own XCD, then counted. PAIRS: I and S are at least 256 (EXACT: multiples of it), and a wave's unit is
+// a pair of steps; else it is a step.
+template <int F, int X, bool PAIRS, bool EXACT>
 __global__ __launch_bounds__(kDownWaves * 64, 4) void tokens_down_kernel(TokensArgs a) {
   constexpr int R = kDownCols / 16, kThreads = kDownWaves * 64, kUnit = PAIRS ? 256 : 128;
   __shared__ int s_expert[kMaxPairs];
@@ -505,7 +507,7 @@ __global__ __launch_bounds__(kDownWaves * 64, 4) void tokens_down_kernel(TokensA
     const uint32_t keep = hr < 0 ? 0u : ~0u;
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      const int at = min(b, blocks - 1) * 32;
+      const int at = PAIRS && !EXACT ? min(b * 32, v.K - 32 - step * 128) : min(b, blocks - 1) * 32;
       hv[0][b][0] = *reinterpret_cast<const u32x4*>(h + at);
       hv[1][b][0] = *reinterpret_cast<const u32x4*>(h + low + at);
     }
@@ -513,7 +515,7 @@ __global__ __launch_bounds__(kDownWaves * 64, 4) void tokens_down_kernel(TokensA
     for (int b = 0; b < 4; ++b)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        hv[i][b][0] &= keep;
+        hv[i][b][0] &= PAIRS && !EXACT && step * 128 + b * 32 >= v.K ? 0u : keep;
         if constexpr (is_int4(F) && !PAIRS) hv[i][b][0] = int4_order(hv[i][b][0]);
       }
   };
@@ -526,15 +528,16 @@ __global__ __launch_bounds__(kDownWaves * 64, 4) void tokens_down_kernel(TokensA
         StepScales<F, 2> v[R];
         const Packed w = pick(now.shared, p.s2, p.w2);
         const long first = row_of(now);
-        const TileLane at = tile_lane<F, 2>(lane, now.K, 16);
+        const TileLane<EXACT> at = tile_lane<F, 2, EXACT>(lane, now.K, 16, 2 * now.u);
+        const bool end = !EXACT && now.K % 256 && now.u == now.K / 256;
         u32x4 hv[2][4][1];
         rows(hv, now, 2 * now.u, 4);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           // H is a multiple of 32: a tile is whole or past it
           const TileBase t = tile_base<F>(w, first + (n0 + 16 * r < p.H ? n0 + 16 * r : 0), now.K, 2 * now.u);
-          load_scales(v[r], t.s, t.z, at);
-          load_pair(c[r], t.q, at);
+          load_scales<F, 2, EXACT>(v[r], t.s, t.z, at);
+          load_pair(c[r], t.q, at, end);
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -612,9 +615,12 @@ __global__ __launch_bounds__(kDownWaves * 64, 4) void tokens_down_kernel(TokensA
   for (int o = threadIdx.x; o < p.M * kDownCols; o += kThreads) {
     const int t = o / kDownCols, cl = o % kDownCols;
     if (n0 + cl >= p.H) continue;
-    float v = 0.f;
-    for (int i = 0; i < a.shares; ++i)
-      v += __hip_atomic_load(sums + i * share + o, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    float v = 0.f, u[kMaxShares];   // all shares requested at once, added in their order
+#pragma unroll
+    for (int i = 0; i < kMaxShares; ++i)
+      u[i] = __hip_atomic_load(sums + min(i, a.shares - 1) * share + o, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+    for (int i = 0; i < kMaxShares; ++i) v += i < a.shares ? u[i] : 0.f;
     finish(t, n0 + cl, v);
   }
 }
@@ -625,17 +631,19 @@ template <int F, int X>
 hipError_t run_up(const TokensArgs& a, hipStream_t s) {
   const Tokens& p = a.p;
   const long items = (long)std::min(p.M * p.k, p.E) * (p.I / 16) + p.S / 16;
-  const int pairs = p.H / 256;
-  if (p.H % 256 || pairs > 3 * kUpWaves) {
+  const int pairs = cdiv(p.H, 256), px = cdiv(pairs, kUpWaves);   // pairs a wave takes
+  const bool exact = p.H % 256 == 0;
+  if (p.H < 256 || px > (exact ? 3 : 2)) {
     const dim3 grid((unsigned)std::min<long>(items, 256));
     hipLaunchKernelGGL((tokens_up_any_kernel<F, X>), grid, dim3(kUpWaves * 64), 0, s, a);
     return hipGetLastError();
   }
-  const int px = cdiv(pairs, kUpWaves);   // pairs a wave takes
   const dim3 grid((unsigned)std::min<long>(items, px == 1 ? 512 : 256)), block((unsigned)cdiv(pairs, px) * 64);
-  if (px == 1) hipLaunchKernelGGL((tokens_up_kernel<F, X, 1>), grid, block, 0, s, a);
-  else if (px == 2) hipLaunchKernelGGL((tokens_up_kernel<F, X, 2>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((tokens_up_kernel<F, X, 3>), grid, block, 0, s, a);
+  if (!exact && px == 1) hipLaunchKernelGGL((tokens_up_kernel<F, X, 1, false>), grid, block, 0, s, a);
+  else if (!exact) hipLaunchKernelGGL((tokens_up_kernel<F, X, 2, false>), grid, block, 0, s, a);
+  else if (px == 1) hipLaunchKernelGGL((tokens_up_kernel<F, X, 1, true>), grid, block, 0, s, a);
+  else if (px == 2) hipLaunchKernelGGL((tokens_up_kernel<F, X, 2, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((tokens_up_kernel<F, X, 3, true>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 
@@ -649,12 +657,15 @@ hipError_t run_tokens(const TokensArgs& a, hipStream_t s) {
   err = run_up<F, X>(a, s);
   if (err != hipSuccess) return err;
   const dim3 down((unsigned)a.tiles, (unsigned)a.shares);
-  // the smaller INT4 groups' scales and zero points do not leave pairs the registers
-  constexpr bool kPairs = F != kI32 && F != kI64;
+  // the smaller INT4 groups' scales and zero points do not leave pairs the registers, nor do INT4's partial pairs
+  constexpr bool kPairs = F != kI32 && F != kI64, kEnds = !is_int4(F);
+  const dim3 block(kDownWaves * 64);
   if (kPairs && p.I % 256 == 0 && p.S % 256 == 0)
-    hipLaunchKernelGGL((tokens_down_kernel<F, X, kPairs>), down, dim3(kDownWaves * 64), 0, s, a);
+    hipLaunchKernelGGL((tokens_down_kernel<F, X, kPairs, true>), down, block, 0, s, a);
+  else if (kEnds && p.I >= 256 && (p.S == 0 || p.S >= 256))
+    hipLaunchKernelGGL((tokens_down_kernel<F, X, kEnds, !kEnds>), down, block, 0, s, a);
   else
-    hipLaunchKernelGGL((tokens_down_kernel<F, X, false>), down, dim3(kDownWaves * 64), 0, s, a);
+    hipLaunchKernelGGL((tokens_down_kernel<F, X, false, true>), down, block, 0, s, a);
   return hipGetLastError();
 }
 
