@@ -232,6 +232,102 @@ __global__ __launch_bounds__(T == 1 ? 1024 : 512) void linear_rows_kernel(Linear
   }
 }
 
+// The same for rows of at least 256 columns, a pair of steps at a time. The rows' fragments of a step
+// meet the codes of R tiles each; the second step's come while the first is multiplied.
+template <int F, int X, int R, int T, bool EXACT>
+__global__ __launch_bounds__(512, 2) void linear_rows_pair_kernel(LinearRows p) {
+  extern __shared__ float red[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  const int n0 = blockIdx.x * (16 * R), m0 = blockIdx.y * (16 * T), K = p.K, pairs = (K + 255) / 256;
+  auto tile_of = [&](int r) { return max(0, min(n0 + 16 * r, p.N - 16)); };   // as in linear_wide_kernel
+  const uint16_t* x[T];   // rows past M are stand-ins: their sums are not written
+#pragma unroll
+  for (int t = 0; t < T; ++t) x[t] = p.x + (long)min(m0 + 16 * t + (lane & 15), p.M - 1) * p.xs + (lane >> 4) * 8;
+  f32x4 acc[R][T];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int t = 0; t < T; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int pair = wave; pair < pairs; pair += waves) {
+    PairCodes c[R];
+    StepScales<F, 2> v[R];
+    const TileLane<EXACT> at = tile_lane<F, 2, EXACT>(lane, K, p.N, 2 * pair);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const TileBase b = tile_base<F>(p.w, tile_of(r), K, 2 * pair);
+      load_scales<F, 2, EXACT>(v[r], b.s, b.z, at);
+      load_pair(c[r], b.q, at, pair == pairs - 1);
+    }
+    u32x4 a[1][4][T];
+    auto rows = [&](int step) __attribute__((always_inline)) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int col = step * 128 + b * 32;
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+          a[0][b][t] = EXACT ? load16(x[t] + col) : load16(x[t] + min(col, K - 32)) & (col < K ? ~0u : 0u);
+      }
+    };
+    rows(2 * pair);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      default_zeros(v[r], p.w.z);
+      split_pair(c[r]);
+    }
+#pragma nounroll   // once through cold code for both steps
+    for (int step = 0;; ++step) {
+      if constexpr (is_int4(F)) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+          for (int t = 0; t < T; ++t) a[0][b][t] = int4_order(a[0][b][t]);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        Codes<F> k;
+        k.q = c[r].a;
+        take_scales_of<F>(k, v[r], step);
+        step_product<F, X, X, T, 1>(acc[r], k, a, 4);
+      }
+      if (step) break;
+      rows(2 * pair + 1);
+#pragma unroll
+      for (int r = 0; r < R; ++r) c[r].a = c[r].b;
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) red[(wave * (R * T) + r * T + t) * 256 + i * 64 + lane] = acc[r][t][i];
+  __syncthreads();
+  const float g = F == kNv ? p.w.g[0] : 1.f;
+  for (int o = threadIdx.x; o < R * T * 256; o += blockDim.x) {
+    const int l = o & 63, i = (o >> 6) & 3, rt = o >> 8;
+    const int first = n0 + 16 * (rt / T), n = tile_of(rt / T) + (l & 15), m = m0 + 16 * (rt % T) + (l >> 4) * 4 + i;
+    if (m >= p.M || n < first || n >= p.N) continue;
+    float v = 0.f;
+    for (int w = 0; w < waves; ++w) v += red[w * (R * T * 256) + o];
+    v *= g;
+    if (p.base) v += to_f32<X>(p.base[m * p.bs + n]);
+    p.y[m * p.ys + n] = from_f32<X>(v);
+  }
+}
+
+template <int F, int X, int R, int T>
+hipError_t run_rows_pairs(const LinearRows& p, hipStream_t s) {
+  const int waves = std::min(8, (p.K + 255) / 256);
+  const dim3 grid((unsigned)((p.N + 16 * R - 1) / (16 * R)), (unsigned)((p.M + 16 * T - 1) / (16 * T)));
+  const size_t lds = (size_t)waves * R * T * 1024;
+  if (p.K % 256 == 0)
+    hipLaunchKernelGGL((linear_rows_pair_kernel<F, X, R, T, true>), grid, dim3((unsigned)(waves * 64)), lds, s, p);
+  else
+    hipLaunchKernelGGL((linear_rows_pair_kernel<F, X, R, T, false>), grid, dim3((unsigned)(waves * 64)), lds, s, p);
+  return hipGetLastError();
+}
+
 template <int F, int X, int R, int T, int D>
 hipError_t run_rows(const LinearRows& p, int waves, hipStream_t s) {
   hipLaunchKernelGGL((linear_rows_kernel<F, X, R, T, D>),
@@ -240,11 +336,21 @@ hipError_t run_rows(const LinearRows& p, int waves, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Rows of a block of the packed product past 32: what the registers hold, less where every 32 columns have
+// a scale to multiply the sum by
+template <int F, int X>
+constexpr int rows_tile() { return F == kI32 || (F == kMx && X == kHf) ? 32 : 64; }
+
 template <int F, int X>
 hipError_t launch_rows(const LinearRows& p, hipStream_t s) {
   const int steps = std::max(1, p.K / 128);
   const int waves = std::min(8, steps);
   if (p.M <= 16 && p.K >= 256 && p.K <= wide_max_k(p.K % 256 == 0)) return launch_wide<F, X>(p, s);
+  if (p.K >= 256) {
+    if (p.M <= 16) return run_rows_pairs<F, X, 1, 1>(p, s);
+    if (p.M <= 32) return run_rows_pairs<F, X, 2, 2>(p, s);
+    return run_rows_pairs<F, X, 2, rows_tile<F, X>() / 16>(p, s);
+  }
   if (p.M <= 16) return run_rows<F, X, 1, 1, 2>(p, waves, s);
   if (p.M <= 32) return run_rows<F, X, 2, 2, 1>(p, waves, s);
   return run_rows<F, X, 2, 4, 1>(p, std::min(waves, 4), s);
@@ -263,7 +369,8 @@ hipError_t launch_rows(const LinearRows& p, hipStream_t s) {
 // transposed form of W comes out of 8 x 8 blocks of codes in one lane's registers.
 constexpr int kBlockK = 32;
 constexpr long kSlabBytes = 64l << 20;   // of the 16-bit form of W at a time: a quarter of the Infinity Cache
-constexpr int kPrepThreads = 512;
+constexpr int kPrepThreads = 1024;
+constexpr int kMaxSplits = 4;   // shares of the reduction axis of the tiled product
 
 struct Prep {
   const uint16_t* x;   // [M, C]
@@ -300,6 +407,24 @@ __device__ __forceinline__ void prep_rows(const Prep& p, int tile, uint32_t (&pa
       }
     return v;
   };
+  uint16_t* out = p.rows + (long)tile * p.blocks * 512 + lane * 8;
+  auto store = [&](int b, u32x4 v, int e) {
+    if constexpr (X == kBf) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w = v[i];
+        v[i] = pack_f16(ldexpf(bf16_lo(w), -e), ldexpf(bf16_hi(w), -e));
+      }
+    }
+    *reinterpret_cast<u32x4*>(out + (long)b * 512) = v;
+  };
+  // The wave's first HELD blocks stay in registers from the search for the largest to the writing.
+  constexpr int HELD = 12;
+  const int whole = p.C / kBlockK;   // blocks inside C
+  u32x4 held[HELD];
+#pragma unroll
+  for (int j = 0; j < HELD; ++j)
+    if (wave + j * kWaves < whole) held[j] = load16(x + (wave + j * kWaves) * kBlockK + (lane >> 4) * 8);
   int e = 0;
   if constexpr (X == kBf) {
     uint32_t top = 0;   // largest finite |x|, as bits
@@ -311,13 +436,11 @@ __device__ __forceinline__ void prep_rows(const Prep& p, int tile, uint32_t (&pa
         top = max(top, hi < 0x7F80u ? hi : 0u);
       }
     };
-    for (int b = wave; b < p.blocks; b += 4 * kWaves) {
-      u32x4 v[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = load(min(b + j * kWaves, p.blocks - 1));
-#pragma unroll
-      for (int j = 0; j < 4; ++j) take(v[j]);
-    }
+    for (int j = 0; j < HELD; ++j)
+      if (wave + j * kWaves < whole) take(held[j]);
+    for (int b = wave + HELD * kWaves; b < whole; b += kWaves) take(load(b));
+    if (whole < p.blocks && wave == 0) take(load(whole));
     top = max(top, xlane_u32<32>(top));
     top = max(top, xlane_u32<16>(top));
     if (lane < 16) part[wave][lane] = top;
@@ -327,24 +450,11 @@ __device__ __forceinline__ void prep_rows(const Prep& p, int tile, uint32_t (&pa
     for (int w = 0; w < kWaves; ++w) top = max(top, part[w][lane & 15]);
     if (top) e = (int)(top >> 7) - 127 - 14;
   }
-  uint16_t* out = p.rows + (long)tile * p.blocks * 512 + lane * 8;
-  for (int b = wave; b < p.blocks; b += 4 * kWaves) {
-    u32x4 v[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = load(min(b + j * kWaves, p.blocks - 1));
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (b + j * kWaves >= p.blocks) continue;
-      if constexpr (X == kBf) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t w = v[j][i];
-          v[j][i] = pack_f16(ldexpf(bf16_lo(w), -e), ldexpf(bf16_hi(w), -e));
-        }
-      }
-      *reinterpret_cast<u32x4*>(out + (long)(b + j * kWaves) * 512) = v[j];
-    }
-  }
+  for (int j = 0; j < HELD; ++j)
+    if (wave + j * kWaves < whole) store(wave + j * kWaves, held[j], e);
+  for (int b = wave + HELD * kWaves; b < whole; b += kWaves) store(b, load(b), e);
+  if (whole < p.blocks && wave == 0) store(whole, load(whole), e);
   if (wave == 0 && lane < 16 && m < p.M) p.ea[m] = e;
 }
 
@@ -513,24 +623,21 @@ __device__ __forceinline__ void turn_codes(uint32_t (&v)[8]) {
   }
 }
 
-// The 16-bit form of columns [first, first + cols) of W. A wave takes 32 rows n, one block of the
-// reduction axis, and 128 columns: each lane an 8 x 8 block of codes, whose rows' scales it multiplies in.
+// 32 rows n of W, block `block` of the reduction axis, and the lane's eight columns from k on: out[i] is
+// column k + i of rows 8 (lane >> 4) .. + 7 of the block as fp16 times 2^-e, zeros past N. Each lane
+// turns an 8 x 8 block of codes, and its rows' scales multiply what comes out.
 template <int F, int S>
-__global__ __launch_bounds__(256) void weights16_turned_kernel(Weights16 p) {
+__device__ __forceinline__ void turned_block(const Packed& w, int K, int N, int block, int k, int e, int lane, u32x4 (&out)[8]) {
   constexpr int G = group_of(F);
-  const int lane = threadIdx.x & 63, block = blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (block >= p.blocks) return;
-  const int c0 = min(blockIdx.y * 128 + 8 * (lane & 15), p.cols - 8);   // cols is a multiple of 32
-  const int k = p.first + c0, e = F == kNv ? 0 : p.eb[k];
   uint32_t v[8], s1[8], z1[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int row = block * kBlockK + (lane >> 4) * 8 + j;
-    const long n = min(row, p.N - 1), g = n * (p.K / G) + k / G;
-    v[j] = *reinterpret_cast<const uint32_t*>(p.w.q + n * (p.K / 2) + k / 2);
-    s1[j] = scale16<F, S>(p.w, g, e);
-    z1[j] = zero16<F>(p.w, g);
-    if (row >= p.N) {   // zeros past N: 0, or (z - z)
+    const long n = min(row, N - 1), g = n * (K / G) + k / G;
+    v[j] = *reinterpret_cast<const uint32_t*>(w.q + n * (K / 2) + k / 2);
+    s1[j] = scale16<F, S>(w, g, e);
+    z1[j] = zero16<F>(w, g);
+    if (row >= N) {   // 0, or (z - z), times 0
       v[j] = is_int4(F) ? ((z1[j] >> 6) & 15u) * 0x11111111u : 0u;
       s1[j] = 0u;
     }
@@ -544,9 +651,117 @@ __global__ __launch_bounds__(256) void weights16_turned_kernel(Weights16 p) {
     z[j] = z1[a] | z1[b] << 16;
   }
 #pragma unroll
+  for (int i = 0; i < 8; ++i) out[i] = scaled_codes<F>(v[i], s, z);
+}
+
+// The 16-bit form of columns [first, first + cols) of W. A wave takes a block of the reduction axis and
+// 128 columns.
+template <int F, int S>
+__global__ __launch_bounds__(256) void weights16_turned_kernel(Weights16 p) {
+  const int lane = threadIdx.x & 63, block = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (block >= p.blocks) return;
+  const int k = p.first + min(blockIdx.y * 128 + 8 * (lane & 15), p.cols - 8);   // cols is a multiple of 32
+  u32x4 v[8];
+  turned_block<F, S>(p.w, p.K, p.N, block, k, F == kNv ? 0 : p.eb[k], lane, v);
+#pragma unroll
   for (int i = 0; i < 8; ++i)
-    *reinterpret_cast<u32x4*>(p.out + ((long)(blockIdx.y * 8 + i) * p.blocks + block) * 512 + lane * 8) =
-        scaled_codes<F>(v[i], s, z);
+    *reinterpret_cast<u32x4*>(p.out + ((long)(blockIdx.y * 8 + i) * p.blocks + block) * 512 + lane * 8) = v[i];
+}
+
+// Up to 64 rows of the gradient without the 16-bit form in between: y[m, k] = base[m, k] + g 2^(ea[m] +
+// eb[k]) sum_n a[m, n] W[n, k] 2^-eb[k]. A block takes 128 columns, 16 T rows and a share of the blocks
+// of the reduction axis, which its waves take in turn; the last block of the columns to finish adds
+// the shares up in their order.
+struct TurnedRows {
+  Packed w;
+  const uint16_t* a;    // M rows, fragment order
+  const int* ea;
+  const int* eb;        // null: 0
+  int M, K, N, blocks;
+  const uint16_t* base;
+  long bs;
+  uint16_t* y;
+  long ys;
+  int splits;
+  float* sums;          // [splits][thread blocks][16 T * 128]
+  int* done;
+};
+constexpr int kMaxTurnedSplits = 8;
+
+template <int F, int X, int T>
+__global__ __launch_bounds__(256) void linear_turned_kernel(TurnedRows p) {
+  constexpr int kSums = 16 * T * 128;
+  extern __shared__ float red[];   // [4][kSums]
+  __shared__ int s_last;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int k = min(blockIdx.x * 128 + 8 * (lane & 15), p.K - 8), e = F == kNv ? 0 : p.eb[k];
+  f32x4 acc[T][8];
+#pragma unroll
+  for (int t = 0; t < T; ++t)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int tiles = (p.M + 15) / 16;
+  for (int b = blockIdx.y * 4 + wave; b < p.blocks; b += p.splits * 4) {
+    u32x4 a[T], v[8];
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+      a[t] = *reinterpret_cast<const u32x4*>(p.a + ((long)min(t, tiles - 1) * p.blocks + b) * 512 + lane * 8);
+    turned_block<F, X>(p.w, p.K, p.N, b, k, e, lane, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int t = 0; t < T; ++t) acc[t][i] = mfma16<kHf>(a[t], v[i], acc[t][i]);
+  }
+  // [row][column]: a lane's eight sums of a row are neighbours
+#pragma unroll
+  for (int t = 0; t < T; ++t)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f32x4* at = reinterpret_cast<f32x4*>(red + wave * kSums + (t * 16 + (lane >> 4) * 4 + j) * 128 + 8 * (lane & 15));
+      at[0] = f32x4{acc[t][0][j], acc[t][1][j], acc[t][2][j], acc[t][3][j]};
+      at[1] = f32x4{acc[t][4][j], acc[t][5][j], acc[t][6][j], acc[t][7][j]};
+    }
+  __syncthreads();
+  const float g = F == kNv ? p.w.g[0] : 1.f;
+  const int c0 = blockIdx.x * 128;
+  auto finish = [&](int o, float v) {
+    const int m = o >> 7, c = c0 + (o & 127);
+    if (m >= p.M || c >= p.K) return;
+    v = ldexpf(v, p.ea[m] + (F == kNv ? 0 : p.eb[c])) * g;
+    if (p.base) v += to_f32<X>(p.base[m * p.bs + c]);
+    p.y[m * p.ys + c] = from_f32<X>(v);
+  };
+  const long share = (long)gridDim.x * kSums;
+  float* sums = p.sums + (long)blockIdx.x * kSums;
+  for (int o = threadIdx.x; o < p.M * 128; o += 256) {
+    const float v = red[o] + red[kSums + o] + red[2 * kSums + o] + red[3 * kSums + o];
+    if (p.splits == 1) finish(o, v);
+    else __hip_atomic_store(sums + blockIdx.y * share + o, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  if (p.splits == 1) return;
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (threadIdx.x == 0)
+    s_last = __hip_atomic_fetch_add(p.done + blockIdx.x, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == p.splits - 1;
+  __syncthreads();
+  if (!s_last) return;
+#pragma nounroll
+  for (int o = threadIdx.x; o < min(kSums, p.M * 128); o += 4 * 256) {   // all shares of four sums requested at once
+    float u[4][kMaxTurnedSplits];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int z = 0; z < kMaxTurnedSplits; ++z)
+        u[q][z] = __hip_atomic_load(sums + min(z, p.splits - 1) * share + o + q * 256, __ATOMIC_RELAXED,
+                                    __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float v = 0.f;
+#pragma unroll
+      for (int z = 0; z < kMaxTurnedSplits; ++z) v += z < p.splits ? u[q][z] : 0.f;
+      finish(o + q * 256, v);
+    }
+  }
 }
 
 // ------------------------------------------------------------------------------------------
@@ -589,19 +804,19 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void product16_kernel(Product16 p)
   const int wm = wave % WM, wn = wave / WM;
   // A thread block runs on XCD (its number mod 8): each XCD gets a run of tiles, column tiles of the
   // same rows behind one another, so that its L2 holds their operands.
-  const int tiles_n = (p.cols + BN * 16 - 1) / (BN * 16), tiles = gridDim.x;
+  const int tiles_b = (p.cols + 127) / 128 * 8, tiles_n = (tiles_b + BN - 1) / BN, tiles = gridDim.x;
   const int per = (tiles + 7) / 8, id = (int)blockIdx.x;
   int tile = (id & 7) * per + (id >> 3);
   const int full = tiles % 8 ? tiles % 8 : 8;     // XCDs with `per` tiles; the others have one less
   if ((id & 7) > full) tile -= (id & 7) - full;
   const int t_m = tile / tiles_n, t_n = tile % tiles_n;
-  const int m0 = t_m * BM * 16, c0 = t_n * BN * 16;
+  const int m0 = t_m * BM * 16;
   const int per_split = (p.blocks + p.splits - 1) / p.splits;
   const int from = blockIdx.y * per_split, to = min(p.blocks, from + per_split);
   // this wave's copies: chunk wave + i * kWaves of the stage, rows' tiles first
   const uint16_t* src[kLoads];
   uint32_t dst[kLoads];
-  const int tiles_a = (p.M + 15) / 16, tiles_b = (p.cols + 127) / 128 * 8;
+  const int tiles_a = (p.M + 15) / 16;
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
     const int chunk = min(wave + i * kWaves, kChunks - 1);
@@ -696,27 +911,28 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void product16_kernel(Product16 p)
       __syncthreads();
       if (!s_last) return;
 #pragma nounroll
-      for (int t = 0; t < kTiles; ++t) {
-        f32x4 v = {0.f, 0.f, 0.f, 0.f};
-        for (int z = 0; z < p.splits; z += 4) {   // four shares requested at a time, added in their order
-          float u[4][4];
+      for (int t = 0; t < kTiles; t += 4) {   // all shares of four tiles requested at once, added in their order
+        float u[kMaxSplits][4][4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
+        for (int z = 0; z < kMaxSplits; ++z)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              u[q][e] = __hip_atomic_load(sums + min(z + q, p.splits - 1) * share + t * 256 + e * 64, __ATOMIC_RELAXED,
-                                          __HIP_MEMORY_SCOPE_AGENT);
+          for (int q = 0; q < 16; ++q)
+            u[z][q >> 2][q & 3] = __hip_atomic_load(sums + min(z, p.splits - 1) * share + t * 256 + q * 64,
+                                                    __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < 4; ++q) {
+          f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += z + q < p.splits ? u[q][e] : 0.f;
+          for (int z = 0; z < kMaxSplits; ++z)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += z < p.splits ? u[z][q][e] : 0.f;
+          dump[(t + q) * 64 + lane] = v;
         }
-        dump[t * 64 + lane] = v;
       }
     }
 #pragma nounroll
     for (int j0 = 0; j0 < TN; j0 += kRun) {
-      const int t = wn * TN + j0, c = c0 + (t >> 3) * 128 + 8 * (lane & 15) + (t & 7);
+      const int t = t_n * BN + wn * TN + j0, c = (t >> 3) * 128 + 8 * (lane & 15) + (t & 7);
       if (c >= p.cols) continue;
       int eb[kRun];
 #pragma unroll
@@ -754,22 +970,22 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void product16_kernel(Product16 p)
 
 namespace {
 
-constexpr int kRowsMax = 64;   // rows the packed product takes
+constexpr int kRowsMax = 64;   // rows that the packed product takes at least, and the turned one at most
 
 size_t pad256(size_t v) { return (v + 255) & ~size_t(255); }
 long up(long v, long to) { return (v + to - 1) / to * to; }
 int cdiv(long a, long b) { return (int)((a + b - 1) / b); }
 
-// How the tiled product of M rows and O columns over C runs: its tile (64 x 64 a wave or 128 x 128, or
-// 32 rows and 32 columns a wave for few rows), shares of the reduction axis, scratch.
-enum : int { kThin = 0, kMiddle = 1, kLarge = 2 };
+// How the tiled product of M rows and O columns over C runs: its tile, shares of the reduction axis,
+// scratch. Larger tiles read less of LDS and L2 a product; smaller ones fill the card.
+enum : int { kThin = 0, kSmall = 1, kMiddle = 2, kLarge = 3 };
 struct Plan16 {
-  int tile = kMiddle, blocks = 0, splits = 1;
+  int tile = kThin, blocks = 0, splits = 1;
   long slab = 0;          // output columns a slab
   size_t rows = 0, ea = 0, eb = 0, weights = 0, sums = 0, done = 0, total = 0;
-  int bm() const { return tile == kThin ? 32 : tile == kMiddle ? 128 : 256; }
-  int bn() const { return tile == kThin ? 128 : tile == kMiddle ? 128 : 256; }
-  int tiles(long M, long cols) const { return cdiv(M, bm()) * cdiv(cols, bn()); }
+  int bm() const { return tile == kThin ? 32 : tile == kSmall ? 64 : tile == kMiddle ? 128 : 256; }
+  int bn() const { return tile == kThin ? 128 : tile == kSmall ? 64 : tile == kMiddle ? 128 : 256; }
+  int tiles(long M, long cols) const { return cdiv(M, bm()) * cdiv(up(cols, 128), bn()); }
 };
 Plan16 plan16(long M, long C, long O) {
   Plan16 p;
@@ -777,11 +993,14 @@ Plan16 plan16(long M, long C, long O) {
   p.slab = std::max<long>(256, kSlabBytes / (p.blocks * 64l) / 256 * 256);
   p.slab = std::min(p.slab, up(O, 256));
   const long cols = std::min(p.slab, O);
-  p.tile = M <= 32 ? kThin : kMiddle;
-  if (p.tile == kMiddle && cdiv(M, 256) * cdiv(cols, 256) >= 192) p.tile = kLarge;
-  // shares: to two blocks a CU, of at least eight blocks each
+  // shares of at least eight blocks each
+  const int most = std::max(1, std::min(kMaxSplits, p.blocks / 8));
+  if (M > 32) {
+    for (p.tile = kLarge; p.tile > kSmall; --p.tile)
+      if (p.tiles(M, cols) * (p.tile == kLarge ? 1 : most) >= 192) break;
+  }
   const int tiles = p.tiles(M, cols);
-  if (p.tile != kLarge) p.splits = std::max(1, std::min({512 / std::max(tiles, 1), p.blocks / 8, 16}));
+  if (p.tile != kLarge) p.splits = std::max(1, std::min(512 / std::max(tiles, 1), most));
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t r = at;
@@ -792,8 +1011,37 @@ Plan16 plan16(long M, long C, long O) {
   p.ea = take((size_t)M * 4);
   p.eb = take((size_t)up(O, 128) * 4);
   p.weights = take((size_t)up(p.slab, 128) * p.blocks * 64);
-  p.sums = take(p.splits == 1 ? 0 : (size_t)p.splits * tiles * p.bm() * p.bn() * 4);
-  p.done = take((size_t)tiles * 4);
+  // an upper bound, so that more rows never need less: with shares there are at most 512 thread blocks
+  // of at most 128 x 128
+  p.sums = take(std::min<size_t>((size_t)kMaxSplits * up(M, 128) * up(p.slab, 128) * 4, 512ul * 128 * 128 * 4));
+  p.done = take(512 * 4);
+  p.total = at;
+  return p;
+}
+
+// The same for linear_turned_kernel
+struct PlanTurned {
+  int t = 1, blocks = 0, columns = 0, splits = 1;
+  size_t rows = 0, ea = 0, eb = 0, sums = 0, done = 0, total = 0;
+};
+PlanTurned plan_turned(int M, int K, int N) {
+  PlanTurned p;
+  p.t = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+  p.blocks = cdiv(N, kBlockK);
+  p.columns = cdiv(K, 128);
+  // shares: to two blocks a CU, and a block for every wave
+  p.splits = std::max(1, std::min({512 / p.columns, cdiv(p.blocks, 4), kMaxTurnedSplits}));
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t r = at;
+    at += pad256(bytes);
+    return r;
+  };
+  p.rows = take((size_t)p.t * 16 * p.blocks * 64);
+  p.ea = take((size_t)p.t * 16 * 4);
+  p.eb = take((size_t)p.columns * 128 * 4);
+  p.sums = take((size_t)p.splits * p.columns * p.t * 16 * 128 * 4);
+  p.done = take((size_t)p.columns * 4);
   p.total = at;
   return p;
 }
@@ -803,6 +1051,16 @@ Plan16 plan16(long M, long C, long O) {
     const hipError_t err_ = (expr);        \
     if (err_ != hipSuccess) return err_;   \
   } while (0)
+
+template <int F, int X, bool BACK>
+hipError_t run_prep(const Prep& p, int blocks, hipStream_t s) {
+  hipLaunchKernelGGL((linear_prep_kernel<F, X, BACK>), dim3((unsigned)blocks), dim3(kPrepThreads), 0, s, p);
+  return hipGetLastError();
+}
+template <int F, bool BACK>
+int exponent_blocks(int O) {
+  return F == kNv ? 0 : BACK ? cdiv(O / group_of(F), 8) : cdiv(O, kPrepThreads / 64);
+}
 
 template <int F, int X, bool BACK>
 hipError_t launch_tiled(const Linear& p, char* scratch, hipStream_t s) {
@@ -818,12 +1076,10 @@ hipError_t launch_tiled(const Linear& p, char* scratch, hipStream_t s) {
     const int tiles = plan.tiles(p.M, cols);
     if (o == 0 || plan.splits > 1) {   // later slabs need the tickets at zero only
       const int row_blocks = o == 0 ? cdiv(p.M, 16) : 0;
-      const int more = o > 0 ? 1 : F == kNv ? 0 : BACK ? cdiv(O / group_of(F), 8) : cdiv(O, kPrepThreads / 64);
+      const int more = o > 0 ? 1 : exponent_blocks<F, BACK>(O);
       const Prep prep{p.x, p.xs, p.M, C, plan.blocks, rows, ea, row_blocks, p.w, p.K, p.N, eb, done,
                       plan.splits > 1 ? tiles : 0};
-      hipLaunchKernelGGL((linear_prep_kernel<F, X, BACK>), dim3((unsigned)(row_blocks + more)), dim3(kPrepThreads), 0, s,
-                         prep);
-      RETURN_IF(hipGetLastError());
+      RETURN_IF((run_prep<F, X, BACK>(prep, row_blocks + more, s)));
     }
     const Weights16 w{p.w, p.K, p.N, (int)o, cols, plan.blocks, eb, weights};
     if constexpr (BACK)
@@ -838,6 +1094,7 @@ hipError_t launch_tiled(const Linear& p, char* scratch, hipStream_t s) {
                       reinterpret_cast<float*>(scratch + plan.sums), done};
     const dim3 grid((unsigned)tiles, (unsigned)plan.splits);
     if (plan.tile == kThin) hipLaunchKernelGGL((product16_kernel<X, 2, 2, 1, 4>), grid, dim3(256), 0, s, q);
+    else if (plan.tile == kSmall) hipLaunchKernelGGL((product16_kernel<X, 2, 2, 2, 2>), grid, dim3(256), 0, s, q);
     else if (plan.tile == kMiddle) hipLaunchKernelGGL((product16_kernel<X, 4, 4, 2, 2>), grid, dim3(256), 0, s, q);
     else hipLaunchKernelGGL((product16_kernel<X, 8, 4, 2, 4>), grid, dim3(512), 0, s, q);
     RETURN_IF(hipGetLastError());
@@ -846,9 +1103,48 @@ hipError_t launch_tiled(const Linear& p, char* scratch, hipStream_t s) {
 }
 
 template <int F, int X>
+hipError_t launch_turned(const Linear& p, char* scratch, hipStream_t s) {
+  const PlanTurned plan = plan_turned(p.M, p.K, p.N);
+  uint16_t* rows = reinterpret_cast<uint16_t*>(scratch + plan.rows);
+  int* ea = reinterpret_cast<int*>(scratch + plan.ea);
+  int* eb = reinterpret_cast<int*>(scratch + plan.eb);
+  int* done = reinterpret_cast<int*>(scratch + plan.done);
+  const int row_blocks = cdiv(p.M, 16);
+  const Prep prep{p.x, p.xs, p.M, p.N, plan.blocks, rows, ea, row_blocks, p.w, p.K, p.N, eb, done,
+                  plan.splits > 1 ? plan.columns : 0};
+  RETURN_IF((run_prep<F, X, true>(prep, row_blocks + exponent_blocks<F, true>(p.K), s)));
+  const TurnedRows q{p.w, rows, ea, eb, p.M, p.K, p.N, plan.blocks, p.base, p.bs, p.y, p.ys, plan.splits,
+                     reinterpret_cast<float*>(scratch + plan.sums), done};
+  const dim3 grid((unsigned)plan.columns, (unsigned)plan.splits);
+  const size_t lds = (size_t)4 * 16 * plan.t * 128 * 4;
+  if (plan.t == 1) hipLaunchKernelGGL((linear_turned_kernel<F, X, 1>), grid, dim3(256), lds, s, q);
+  else if (plan.t == 2) hipLaunchKernelGGL((linear_turned_kernel<F, X, 2>), grid, dim3(256), lds, s, q);
+  else hipLaunchKernelGGL((linear_turned_kernel<F, X, 4>), grid, dim3(256), lds, s, q);
+  return hipGetLastError();
+}
+
+// The most rows that the packed product takes: whole rounds of its blocks (32 columns and `tile` rows
+// each, one a CU) against the tiled product's three launches, in us as measured on MI355X: a round
+// of 2048 columns takes 11, of 6144 28.5; the tiled product 25 and its passes over the 16-bit forms
+// (3.5 TB/s) and the product (0.9 PFLOP/s). 128 rows of 6144 to 4096: 29 against 49, 256: 57 against
+// 58, 512: 110 against 75; 1024 rows of 2048 to 1536: 33 against 44.
+int rows_most(int K, int N, int tile) {
+  const double round = 2.0 + 0.0044 * K;
+  const long columns = cdiv(N, 32);
+  int most = kRowsMax;
+  for (int r = 1; r <= 8; ++r) {
+    const double M = (double)(256l * r / columns) * tile;
+    const double tiled = 25.0 + 2.5 * K * N / 3.5e6 + 4.0 * M * K / 3.5e6 + 2.0 * M * N * K / 0.9e9;
+    if (M > most && r * round < tiled) most = (int)std::min(M, 1024.0);   // (measured up to there)
+  }
+  return most;
+}
+
+template <int F, int X>
 hipError_t launch_any(const Linear& p, bool back, char* scratch, hipStream_t s) {
-  if (back) return launch_tiled<F, X, true>(p, scratch, s);
-  if (p.M > kRowsMax) return launch_tiled<F, X, false>(p, scratch, s);
+  if (back)
+    return p.M <= kRowsMax ? launch_turned<F, X>(p, scratch, s) : launch_tiled<F, X, true>(p, scratch, s);
+  if (p.M > rows_most(p.K, p.N, rows_tile<F, X>())) return launch_tiled<F, X, false>(p, scratch, s);
   return launch_rows<F, X>({p.w, p.x, p.xs, p.M, p.K, p.N, p.base, p.bs, p.y, p.ys}, s);
 }
 
@@ -866,8 +1162,12 @@ hipError_t launch_format(const Linear& p, bool back, char* scratch, hipStream_t 
 }  // namespace
 
 void linear_scratch(int M, int K, int N, size_t* forward, size_t* backward) {
-  if (forward) *forward = M > kRowsMax ? plan16(M, K, N).total : 0;
-  if (backward) *backward = M > 0 ? plan16(M, N, K).total : 0;
+  // (whatever the format: as for the shorter tiles of the packed product)
+  if (forward) *forward = M > rows_most(K, N, 32) ? plan16(M, K, N).total : 0;
+  if (backward) {
+    *backward = M > 0 ? plan_turned(std::min(M, kRowsMax), K, N).total : 0;
+    if (M > kRowsMax) *backward = std::max(*backward, plan16(M, N, K).total);
+  }
 }
 
 hipError_t launch_linear(const Linear& p, bool back, void* scratch, hipStream_t s) {
