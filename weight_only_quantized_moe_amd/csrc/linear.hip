@@ -790,15 +790,15 @@ __device__ __forceinline__ void wait_vmem_at_most() {
 }
 
 // y[m, c] = base[m, c] + g 2^(ea[m] + eb[c]) sum_i a[m, i] b[c, i]. A wave takes TM x TN tiles, a block
-// WM x WN waves. Blocks of the reduction axis pass through four buffers in LDS, three of them in
+// WM x WN waves. Blocks of the reduction axis pass through STAGES buffers in LDS, all but one of them in
 // flight, loaded by copies that go past the registers; a wave reads the next block's fragments
 // while it multiplies the present one's. With splits > 1 the block of a tile that finishes last adds the
 // shares up in their order.
-template <int X, int TM, int TN, int WM, int WN>
-__global__ __launch_bounds__(WM * WN * 64, 1) void product16_kernel(Product16 p) {
-  constexpr int kWaves = WM * WN, kThreads = kWaves * 64, kStages = 4;
+template <int X, int TM, int TN, int WM, int WN, int STAGES>
+__global__ __launch_bounds__(WM * WN * 64, 2) void product16_kernel(Product16 p) {
+  constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
   constexpr int BM = WM * TM, BN = WN * TN, kChunks = BM + BN, kLoads = (kChunks + kWaves - 1) / kWaves;
-  __shared__ u32x4 buffer[kStages][kChunks * 64];
+  __shared__ u32x4 buffer[STAGES][kChunks * 64];
   __shared__ int s_last;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % WM, wn = wave / WM;
@@ -824,9 +824,9 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void product16_kernel(Product16 p)
     src[i] = (chunk < BM ? p.a : p.b) + t * p.blocks * 512;
     dst[i] = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)&buffer[0][chunk * 64];
   }
-  auto copy = [&](int block) {   // past the last: a stand-in that nobody reads, so that the waits can count
+  auto copy = [&](int block, int slot) {   // past the last: a stand-in that nobody reads, so that the waits can count
     const long at = (long)min(block, to - 1) * 512;
-    const uint32_t off = (uint32_t)((block - from) & (kStages - 1)) * (kChunks * 1024);
+    const uint32_t off = (uint32_t)slot * (kChunks * 1024);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
       asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst[i] + off), "v"(lane * 16), "s"(src[i] + at)
@@ -838,8 +838,9 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void product16_kernel(Product16 p)
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   u32x4 a[2][TM], b[2][TN];
-  auto read = [&](u32x4(&fa)[TM], u32x4(&fb)[TN], int block) __attribute__((always_inline)) {
-    const u32x4* s = buffer[(block - from) & (kStages - 1)];
+  int slot = 0;   // of the block whose arrival was waited for last
+  auto read = [&](u32x4(&fa)[TM], u32x4(&fb)[TN]) __attribute__((always_inline)) {
+    const u32x4* s = buffer[slot];
 #pragma unroll
     for (int i = 0; i < TM; ++i) fa[i] = s[(wm * TM + i) * 64 + lane];
 #pragma unroll
@@ -854,26 +855,27 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void product16_kernel(Product16 p)
   // Block k is in LDS once each wave has waited for its own copies of it and all have met. The buffer
   // that is then filled held block k - 1, whose fragments every wave had before the meeting.
   auto arrive = [&](int block) __attribute__((always_inline)) {
-    wait_vmem_at_most<2 * kLoads>();
+    wait_vmem_at_most<(STAGES - 2) * kLoads>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    copy(block + 3);
+    const int before = slot;
+    slot = block == from ? 0 : slot + 1 == STAGES ? 0 : slot + 1;
+    copy(block + STAGES - 1, block == from ? STAGES - 1 : before);
   };
   if (from < to) {
-    copy(from);
-    copy(from + 1);
-    copy(from + 2);
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) copy(from + i, i);
     arrive(from);
-    read(a[0], b[0], from);
+    read(a[0], b[0]);
     for (int k = from; k < to; k += 2) {
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // this block's fragments, before their buffer goes
       arrive(k + 1);
-      read(a[1], b[1], k + 1);
+      read(a[1], b[1]);
       multiply(a[0], b[0]);
       if (k + 1 >= to) break;
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       arrive(k + 2);
-      read(a[0], b[0], k + 2);
+      read(a[0], b[0]);
       multiply(a[1], b[1]);
     }
     wait_vmem_at_most<0>();
@@ -881,7 +883,7 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void product16_kernel(Product16 p)
   // The sums go through LDS, so that what follows is a loop (unrolled over the registers it would be
   // 30 to 100 KB of code that each wave runs once): DI rows of tiles at a time, in the wave's own part.
   __syncthreads();
-  constexpr int DI = TM * TN <= kChunks * kStages / kWaves ? TM : TM / 2;
+  constexpr int DI = TM * TN <= kChunks * STAGES / kWaves ? TM : TM / 2;
   f32x4* dump = reinterpret_cast<f32x4*>(&buffer[0][0]) + wave * (DI * TN * 64);
   const float g = p.g ? *p.g : 1.f;
   constexpr int kRun = TN < 8 ? TN : 8;      // neighbouring columns a lane has
@@ -978,13 +980,13 @@ int cdiv(long a, long b) { return (int)((a + b - 1) / b); }
 
 // How the tiled product of M rows and O columns over C runs: its tile, shares of the reduction axis,
 // scratch. Larger tiles read less of LDS and L2 a product; smaller ones fill the card.
-enum : int { kThin = 0, kSmall = 1, kMiddle = 2, kLarge = 3 };
+enum : int { kThin = 0, kSmall = 1, kMiddle = 2, kWide = 3, kLarge = 4 };
 struct Plan16 {
   int tile = kThin, blocks = 0, splits = 1;
   long slab = 0;          // output columns a slab
   size_t rows = 0, ea = 0, eb = 0, weights = 0, sums = 0, done = 0, total = 0;
   int bm() const { return tile == kThin ? 32 : tile == kSmall ? 64 : tile == kMiddle ? 128 : 256; }
-  int bn() const { return tile == kThin ? 128 : tile == kSmall ? 64 : tile == kMiddle ? 128 : 256; }
+  int bn() const { return tile == kSmall ? 64 : tile == kLarge ? 256 : 128; }
   int tiles(long M, long cols) const { return cdiv(M, bm()) * cdiv(up(cols, 128), bn()); }
 };
 Plan16 plan16(long M, long C, long O) {
@@ -996,11 +998,22 @@ Plan16 plan16(long M, long C, long O) {
   // shares of at least eight blocks each
   const int most = std::max(1, std::min(kMaxSplits, p.blocks / 8));
   if (M > 32) {
-    for (p.tile = kLarge; p.tile > kSmall; --p.tile)
-      if (p.tiles(M, cols) * (p.tile == kLarge ? 1 : most) >= 192) break;
+    // 256 x 256 a CU at once, or two of 256 x 128, one of which alone takes 0.6 of the time of two:
+    // whichever's last round is fuller (384 large tiles 262 us, as 768 wide ones 217)
+    p.tile = kLarge;
+    const int large = p.tiles(M, cols);
+    p.tile = kWide;
+    const int wide = p.tiles(M, cols), rest = wide % 512;
+    const double t_large = cdiv(large, 256), t_wide = wide / 512 + (rest == 0 ? 0. : rest <= 256 ? 0.6 : 1.);
+    if (large >= 192 || wide >= 256) {
+      p.tile = t_wide < t_large ? kWide : kLarge;
+    } else {
+      p.tile = kMiddle;
+      if (p.tiles(M, cols) * most < 192) p.tile = kSmall;
+    }
   }
   const int tiles = p.tiles(M, cols);
-  if (p.tile != kLarge) p.splits = std::max(1, std::min(512 / std::max(tiles, 1), most));
+  if (p.tile < kWide) p.splits = std::max(1, std::min(512 / std::max(tiles, 1), most));
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t r = at;
@@ -1093,10 +1106,14 @@ hipError_t launch_tiled(const Linear& p, char* scratch, hipStream_t s) {
                       p.base ? p.base + o : nullptr, p.bs, p.y + o, p.ys, plan.splits,
                       reinterpret_cast<float*>(scratch + plan.sums), done};
     const dim3 grid((unsigned)tiles, (unsigned)plan.splits);
-    if (plan.tile == kThin) hipLaunchKernelGGL((product16_kernel<X, 2, 2, 1, 4>), grid, dim3(256), 0, s, q);
-    else if (plan.tile == kSmall) hipLaunchKernelGGL((product16_kernel<X, 2, 2, 2, 2>), grid, dim3(256), 0, s, q);
-    else if (plan.tile == kMiddle) hipLaunchKernelGGL((product16_kernel<X, 4, 4, 2, 2>), grid, dim3(256), 0, s, q);
-    else hipLaunchKernelGGL((product16_kernel<X, 8, 4, 2, 4>), grid, dim3(512), 0, s, q);
+    const dim3 block(plan.tile == kLarge ? 512 : 256);
+    switch (plan.tile) {
+      case kThin: hipLaunchKernelGGL((product16_kernel<X, 2, 2, 1, 4, 4>), grid, block, 0, s, q); break;
+      case kSmall: hipLaunchKernelGGL((product16_kernel<X, 2, 2, 2, 2, 4>), grid, block, 0, s, q); break;
+      case kMiddle: hipLaunchKernelGGL((product16_kernel<X, 4, 4, 2, 2, 4>), grid, block, 0, s, q); break;
+      case kWide: hipLaunchKernelGGL((product16_kernel<X, 8, 4, 2, 2, 3>), grid, block, 0, s, q); break;
+      default: hipLaunchKernelGGL((product16_kernel<X, 8, 4, 2, 4, 4>), grid, block, 0, s, q);
+    }
     RETURN_IF(hipGetLastError());
   }
   return hipSuccess;
