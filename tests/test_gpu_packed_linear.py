@@ -97,6 +97,38 @@ def test_widths(hm, fmt, K, N, dtype):
         run(hm, rng, fmt, M, K, N, True, dtype, "matrix" if M > 1 else None)
 
 
+# each number of pairs of 256 columns that a wave keeps, with the last pair whole and partial, one and two
+# tiles an item, and more columns than any of them takes
+@pytest.mark.parametrize("K,N", [(256, 40), (288, 40), (2048, 70), (2336, 33), (3840, 20), (4000, 20), (4096, 8200),
+                                 (5120, 24), (6144, 24), (7936, 24), (4128, 24), (2048, 8210)])
+@pytest.mark.parametrize("fmt", FORMATS, ids=IDS)
+def test_shares_of_the_reduction(hm, fmt, K, N):
+    step = max(fmt[1], 32)
+    K = -(-K // step) * step
+    rng = np.random.default_rng([K, N])
+    for M, dtype in ((1, "bf16"), (11, "fp16"), (33, "bf16")):
+        run(hm, rng, fmt, M, K, N, False, dtype, "matrix")
+
+
+# the tiled product's tiles and shares of the reduction axis, both sides of each choice, forward and back
+@pytest.mark.parametrize("M,K,N", [(65, 512, 20000), (1030, 256, 300), (1100, 1056, 700), (2049, 96, 1500),
+                                   (4100, 64, 4100), (2500, 288, 2100), (1025, 2048, 96)])
+def test_tiles(hm, M, K, N):
+    rng = np.random.default_rng([M, K, N])
+    for fmt, back, dtype in ((FORMATS[0], False, "bf16"), (FORMATS[2], False, "fp16"), (FORMATS[1], True, "bf16"),
+                             (FORMATS[3], True, "fp16")):
+        run(hm, rng, fmt, M, K, N, back, dtype, "matrix")
+
+
+@pytest.mark.parametrize("M", [1, 16, 17, 33, 64])
+@pytest.mark.parametrize("K,N", [(32, 5), (160, 31), (1056, 1000), (6144, 130), (512, 4133)])
+def test_gradient_of_few_rows(hm, M, K, N):
+    """The gradient straight from the codes: shares of n, partial blocks of 32 rows and of 128 columns."""
+    rng = np.random.default_rng([M, K, N])
+    for fmt, dtype in ((FORMATS[0], "fp16"), (FORMATS[1], "bf16"), (FORMATS[2], "bf16")):
+        run(hm, rng, fmt, M, K, N, True, dtype, "matrix")
+
+
 @pytest.mark.parametrize("back", [False, True])
 @pytest.mark.parametrize("base", [None, "matrix", "own", "bias"])
 @pytest.mark.parametrize("M", [1, 3, 20, 50, 90])

@@ -129,6 +129,25 @@ def test_odd_widths(hm, H, I, S):
         case(hm, rng, fmt, "bf16", 5, 7, H, I, 2, S=S)
 
 
+# pairs of 256 columns that a wave keeps of H, whole and partial; pairs and partial pairs of I and S
+@pytest.mark.parametrize("H,I,S", [(2048, 64, 0), (2080, 32, 0), (2560, 32, 32), (4096, 32, 0), (4224, 32, 0),
+                                   (6144, 32, 0), (6272, 32, 0), (64, 256, 256), (64, 512, 0), (64, 288, 352),
+                                   (96, 768, 256), (64, 384, 128), (64, 256, 96)])
+def test_shares_of_the_reduction(hm, H, I, S):
+    rng = np.random.default_rng([H, I, S, 1])
+    for fmt in (FORMATS[0], FORMATS[1], FORMATS[2], FORMATS[5]):
+        step = max(fmt[1], 32)
+        up = [-(-v // step) * step for v in (H, I, S)]
+        case(hm, rng, fmt, "bf16", 3, 5, up[0], up[1], 2, S=up[2])
+
+
+def test_many_shares_of_the_output(hm):
+    """All 16 shares of a column tile, and one."""
+    rng = np.random.default_rng(3)
+    case(hm, rng, FORMATS[1], "bf16", 16, 40, 64, 512, 8)
+    case(hm, rng, FORMATS[1], "bf16", 1, 3, 64, 32, 1)
+
+
 @pytest.mark.parametrize("E,k,M", [(1, 1, 1), (1, 1, 16), (16, 16, 16), (64, 8, 6), (65, 1, 4), (300, 16, 16),
                                    (1024, 16, 16)])
 def test_expert_counts(hm, E, k, M):

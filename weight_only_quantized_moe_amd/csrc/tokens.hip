@@ -461,11 +461,12 @@ __global__ __launch_bounds__(kUpWaves * 64, 2) void tokens_up_any_kernel(TokensA
   }
 }
 
-// y: a block takes 64 columns and one share of the steps of all experts in use, dealt evenly to its
-// waves; four row tiles of W2 meet each piece of h that a wave loads. With several shares the
+// y: a block takes 64 columns and one share of the units of all experts in use, which its waves take in
+// turn, so that they read neighbouring lines of the same rows; four row tiles of W2 meet each piece of h that a wave loads. With several shares the
 // block that finishes last adds them up in their order: a share is written past the caches of its
-// own XCD, then counted. PAIRS: I and S are at least 256 (EXACT: multiples of it), and a wave's unit is
-// a pair of steps; else it is a step.
+// own XCD, then counted. PAIRS: I and S are at least 256 (EXACT: multiples of it), and a unit is a pair
+// of steps; else it is a step. With the next pair's codes in flight beside, at twice the registers
+// and half the waves, eight tokens of the GLM-class layer (MXFP4) took 108 us against 103.
 template <int F, int X, bool PAIRS, bool EXACT>
 __global__ __launch_bounds__(kDownWaves * 64, 4) void tokens_down_kernel(TokensArgs a) {
   constexpr int R = kDownCols / 16, kThreads = kDownWaves * 64, kUnit = PAIRS ? 256 : 128;
@@ -486,8 +487,7 @@ __global__ __launch_bounds__(kDownWaves * 64, 4) void tokens_down_kernel(TokensA
   __syncthreads();
   const int m = lane & 15;
   const int units = (p.I + kUnit - 1) / kUnit, total = count * units + (p.S + kUnit - 1) / kUnit;
-  const int part = blockIdx.y * kDownWaves + wave, parts = a.shares * kDownWaves;
-  const int from = (int)((long)total * part / parts), to = (int)((long)total * (part + 1) / parts);
+  const int from = (int)((long)total * blockIdx.y / a.shares) + wave, to = (int)((long)total * (blockIdx.y + 1) / a.shares);
   f32x4 acc[R][1];
 #pragma unroll
   for (int r = 0; r < R; ++r) acc[r][0] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -497,25 +497,36 @@ __global__ __launch_bounds__(kDownWaves * 64, 4) void tokens_down_kernel(TokensA
     bool shared;
   };
   auto place = [&](int d, int u) { return Place{d, u, d == count ? p.S : p.I, d == count}; };
-  auto after = [&](const Place& v) { return v.u + 1 == units && !v.shared ? place(v.d + 1, 0) : place(v.d, v.u + 1); };
+  auto after = [&](const Place& v) {   // the wave's next unit
+    int d = v.d, u = v.u + kDownWaves;
+    while (d < count && u >= units) {
+      u -= units;
+      ++d;
+    }
+    return place(d, u);
+  };
   auto row_of = [&](const Place& v) { return v.shared ? 0l : (long)__builtin_amdgcn_readfirstlane(s_expert[v.d]) * p.H; };
-  // h of a step, both parts, zeros for tokens that did not take the expert
+  // h of a step, both parts, zeros for tokens that did not take the expert: only the lanes of the others
+  // load, which costs the address unit less than stand-ins would
   auto rows = [&](u32x4(&hv)[2][4][1], const Place& v, int step, int blocks) __attribute__((always_inline)) {
     const int hr = v.shared ? (m < p.M ? m : -1) : s_row[v.d * 16 + m];
     const uint16_t* h = (v.shared ? a.hs : a.h) + (long)max(hr, 0) * v.K + (lane >> 4) * 8 + step * 128;
     const long low = (long)(v.shared ? p.M : p.M * p.k) * v.K;
-    const uint32_t keep = hr < 0 ? 0u : ~0u;
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const int at = PAIRS && !EXACT ? min(b * 32, v.K - 32 - step * 128) : min(b, blocks - 1) * 32;
-      hv[0][b][0] = *reinterpret_cast<const u32x4*>(h + at);
-      hv[1][b][0] = *reinterpret_cast<const u32x4*>(h + low + at);
+    for (int b = 0; b < 4; ++b) hv[0][b][0] = hv[1][b][0] = u32x4{0u, 0u, 0u, 0u};
+    if (hr >= 0) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int at = PAIRS && !EXACT ? min(b * 32, v.K - 32 - step * 128) : min(b, blocks - 1) * 32;
+        hv[0][b][0] = *reinterpret_cast<const u32x4*>(h + at);
+        hv[1][b][0] = *reinterpret_cast<const u32x4*>(h + low + at);
+      }
     }
 #pragma unroll
     for (int b = 0; b < 4; ++b)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        hv[i][b][0] &= PAIRS && !EXACT && step * 128 + b * 32 >= v.K ? 0u : keep;
+        if (PAIRS && !EXACT && step * 128 + b * 32 >= v.K) hv[i][b][0] = u32x4{0u, 0u, 0u, 0u};
         if constexpr (is_int4(F) && !PAIRS) hv[i][b][0] = int4_order(hv[i][b][0]);
       }
   };
@@ -523,7 +534,7 @@ __global__ __launch_bounds__(kDownWaves * 64, 4) void tokens_down_kernel(TokensA
     Place now = place(min(from / units, count), 0);
     now.u = from - now.d * units;
     if constexpr (PAIRS) {
-      for (int f = from; f < to; ++f) {
+      for (int f = from; f < to; f += kDownWaves) {
         PairCodes c[R];
         StepScales<F, 2> v[R];
         const Packed w = pick(now.shared, p.s2, p.w2);
@@ -568,7 +579,7 @@ __global__ __launch_bounds__(kDownWaves * 64, 4) void tokens_down_kernel(TokensA
         now = after(now);
       }
     } else {
-      for (int f = from; f < to; ++f) {
+      for (int f = from; f < to; f += kDownWaves) {
         const int blocks = step_blocks<false>(now.u, now.K);
         Codes<F> c[R];
 #pragma unroll
