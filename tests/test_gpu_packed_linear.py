@@ -60,7 +60,7 @@ def run(hm, rng, fmt, M, K, N, back, dtype, base="matrix", strided=False, w=None
     ref = (P.linear_backward if back else P.linear)(x, W, None if base is None else b)
     in_sums = offset_values(w, W)
     sums = np.abs(x) @ (in_sums if back else in_sums.T) + (0.0 if base is None else np.abs(b))
-    tiled = back or M > 64
+    tiled = back or M > 64      # (some of these take the packed product, which rounds no weight)
     step = 2.0 ** -11 if tiled and f == "int4" else 2.0 ** -24   # weights rounded to fp16
     rms = None
     if tiled and f == "int4":
@@ -72,8 +72,8 @@ def run(hm, rng, fmt, M, K, N, back, dtype, base="matrix", strided=False, w=None
     assert torch.equal(ybuf, before)
 
 
-# rows: each number of row tiles the packed product takes, its last (64), and both sides of the tiled
-# product's tile
+# rows: each number of row tiles the packed product takes, both sides of the gradient's last few rows (64)
+# and of the tiled product's tiles; more forward rows are test_tiles'
 @pytest.mark.parametrize("M", [1, 2, 15, 16, 17, 32, 33, 64, 65, 128, 129, 300])
 @pytest.mark.parametrize("fmt", FORMATS, ids=IDS)
 def test_rows(hm, fmt, M):
@@ -143,7 +143,7 @@ def test_wide_scales(hm):
     many-row product keeps each column's own exponent."""
     rng = np.random.default_rng(5)
     for fmt in (FORMATS[1], FORMATS[3]):
-        for M in (3, 80):
+        for M in (3, 80, 1030):
             w = packed(rng, (40, 256), *fmt, "bf16", spread=0)
             far = 2.0 ** rng.integers(-30, 31, (40, 1))
             if fmt[0] == "mxfp4":
@@ -153,7 +153,7 @@ def test_wide_scales(hm):
             run(hm, rng, fmt, M, 256, 40, False, "bf16", None, w=w)
 
 
-@pytest.mark.parametrize("M", [4, 80])
+@pytest.mark.parametrize("M", [4, 80, 1030])
 @pytest.mark.parametrize("fmt", [FORMATS[0], FORMATS[1], FORMATS[2]], ids=["nvfp4", "mxfp4", "int4"])
 def test_whole_numbers_are_exact(hm, fmt, M):
     """Codes, scales and rows whose products and sums are whole numbers below 2^11: equal."""
@@ -179,7 +179,7 @@ def test_whole_numbers_are_exact(hm, fmt, M):
         assert np.array_equal(y.cpu().double().numpy(), ref)
 
 
-@pytest.mark.parametrize("M", [3, 70])
+@pytest.mark.parametrize("M", [3, 70, 1030])
 def test_special_values_stay_in_their_row(hm, M):
     """NaN and infinities in a row of x: its own row only; NaN scales: their column only."""
     import torch
@@ -215,11 +215,12 @@ def test_special_values_stay_in_their_row(hm, M):
             assert torch.isnan(dx[:, :width]).all() and torch.isfinite(dx[:, width:]).all()
 
 
-def test_extreme_rows(hm):
+@pytest.mark.parametrize("M", [70, 1030])
+def test_extreme_rows(hm, M):
     """Zero rows, rows near the ends of bf16's range, one row beside them."""
     import torch
     rng = np.random.default_rng(1)
-    M, K, N = 70, 256, 40
+    K, N = 256, 40
     w = packed(rng, (N, K), *FORMATS[3], "bf16")
     W = P.values(w)
     x = rng.standard_normal((M, K))
@@ -236,7 +237,7 @@ def test_extreme_rows(hm):
     check(got * scale, P.linear(x * scale, W), np.abs(x * scale) @ offset_values(w, W).T, K + 8, "bf16", 2.0 ** -11)
 
 
-@pytest.mark.parametrize("M", [2, 48, 100])
+@pytest.mark.parametrize("M", [2, 48, 100, 1030])
 @pytest.mark.parametrize("back", [False, True])
 def test_captured_and_on_another_stream(hm, M, back):
     """A captured call, replayed with new rows between eager calls on the same scratch."""
@@ -270,11 +271,12 @@ def test_captured_and_on_another_stream(hm, M, back):
         assert torch.equal(y, eager)
 
 
-def test_two_calls_at_once(hm):
+@pytest.mark.parametrize("M", [200, 1030])
+def test_two_calls_at_once(hm, M):
     """Two streams, each with its own scratch."""
     import torch
     rng = np.random.default_rng(3)
-    M, K, N = 200, 1024, 512
+    K, N = 1024, 512
     w = upload(packed(rng, (N, K), *FORMATS[0], "bf16"))
     xs = [torch.randn(M, K, device="cuda").bfloat16() for _ in range(2)]
     want = [torch.empty(M, N, dtype=torch.bfloat16, device="cuda") for _ in range(2)]

@@ -1,6 +1,8 @@
 """The operators on 4-bit matrices without a GPU: refusals of the C ABI and the binding, scratch
 planners, and the oracle's gradient against differences. Nothing here launches a kernel."""
 import ctypes
+import os
+import re
 
 import numpy as np
 import pytest
@@ -164,3 +166,12 @@ def test_oracle_codes():
     mx = {"fmt": "mxfp4", "q": np.array([[0x72] + [0] * 15], np.uint8), "s": np.array([[130]], np.uint8), "z": None,
           "g": None}
     assert P.values(mx)[0, 0] == 8.0 and P.values(mx)[0, 1] == 48.0
+
+
+@pytest.mark.parametrize("name", ["linear.hip", "tokens.hip", "packed.h"])
+def test_atomics_count_and_mask_only(name):
+    """Sums have a fixed order: read-modify-write atomics touch tickets and masks, no sums."""
+    with open(os.path.join(os.path.dirname(hm.__file__), "csrc", name)) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    for call in re.findall(r"\b\w*atomic(?:\w*_fetch_\w+|[A-Z]\w*)\s*\([^;]*", text):
+        assert re.match(r"atomicOr\(&s\.mask\[id\]|__hip_atomic_fetch_add\((p|a)\.done \+ ", call), call
