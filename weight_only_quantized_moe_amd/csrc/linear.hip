@@ -348,8 +348,11 @@ hipError_t launch_rows(const LinearRows& p, hipStream_t s) {
   if (p.M <= 16 && p.K >= 256 && p.K <= wide_max_k(p.K % 256 == 0)) return launch_wide<F, X>(p, s);
   if (p.K >= 256) {
     if (p.M <= 16) return run_rows_pairs<F, X, 1, 1>(p, s);
-    if (p.M <= 32) return run_rows_pairs<F, X, 2, 2>(p, s);
-    return run_rows_pairs<F, X, 2, rows_tile<F, X>() / 16>(p, s);
+    constexpr int T = rows_tile<F, X>() / 16;
+    // one tile of columns a block where two would leave half of the CUs without one
+    const bool one = (long)((p.N + 31) / 32) * ((p.M + 16 * T - 1) / (16 * T)) <= 128;
+    if (p.M <= 32) return one ? run_rows_pairs<F, X, 1, 2>(p, s) : run_rows_pairs<F, X, 2, 2>(p, s);
+    return one ? run_rows_pairs<F, X, 1, T>(p, s) : run_rows_pairs<F, X, 2, T>(p, s);
   }
   if (p.M <= 16) return run_rows<F, X, 1, 1, 2>(p, waves, s);
   if (p.M <= 32) return run_rows<F, X, 2, 2, 1>(p, waves, s);
