@@ -237,6 +237,27 @@ def test_extreme_rows(hm, M):
     check(got * scale, P.linear(x * scale, W), np.abs(x * scale) @ offset_values(w, W).T, K + 8, "bf16", 2.0 ** -11)
 
 
+@pytest.mark.parametrize("M", [4, 40, 100, 1030])
+def test_subnormal_rows(hm, M):
+    """fp16 rows of whole multiples of 2^-24, which fp16 holds below its normal numbers: all of them
+    count. Products are whole numbers of 2^-14 below 2^11 of them: equal."""
+    import torch
+    rng = np.random.default_rng(M)
+    K, N = 256, 40
+    w = packed(rng, (N, K), "int4", 32, False, "fp16")
+    w["s"], w["s_t"] = rounded(np.full_like(w["s"], 1024.0), "fp16")
+    W = P.values(w)
+    for back in (False, True):
+        n_in, n_out = (N, K) if back else (K, N)
+        x = np.where(rng.random((M, n_in)) < 0.2, rng.integers(-3, 4, (M, n_in)), 0) * 2.0 ** -24
+        y = torch.empty(M, n_out, dtype=torch.float16, device="cuda")
+        xd = torch.from_numpy(x).to(torch.float16).cuda()
+        (hm.moe_linear_backward if back else hm.moe_linear)(xd, upload(w), y, None, scratch(hm, M, K, N, back))
+        ref = x @ (W if back else W.T)
+        assert np.abs(ref).max() < 2048 * 2.0 ** -14
+        assert np.array_equal(y.cpu().double().numpy(), ref)
+
+
 @pytest.mark.parametrize("M", [2, 48, 100, 1030])
 @pytest.mark.parametrize("back", [False, True])
 def test_captured_and_on_another_stream(hm, M, back):

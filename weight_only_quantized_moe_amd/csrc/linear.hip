@@ -832,7 +832,9 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void product16_kernel(Product16 p)
     const uint32_t off = (uint32_t)slot * (kChunks * 1024);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
-      asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst[i] + off), "v"(lane * 16), "s"(src[i] + at)
+      // (a load into LDS may read m0 one wait state after it was written)
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst[i] + off), "v"(lane * 16),
+                   "s"(src[i] + at)
                    : "memory", "m0");
   };
   f32x4 acc[TM][TN];

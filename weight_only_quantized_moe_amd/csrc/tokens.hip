@@ -329,9 +329,10 @@ __device__ __forceinline__ void finish_item(const TokensArgs& a, const Routing& 
   }
 }
 
-// Routing and the first products, H at least 256 (EXACT: a multiple of it). Every item multiplies the same tokens, so a
-// wave keeps its PX pairs of steps of x in registers, and it requests the next item's codes pair by
-// pair as those of the present one are used up.
+// Routing and the first products, H at least 256 (EXACT: a multiple of it). Every item multiplies the
+// same tokens, so a wave keeps its PX pairs of steps of x in registers, and it requests the next item's
+// codes pair by pair as those of the present one are used up. Bound by HBM where items are many: 749 MB in
+// 132 us (eight tokens of the GLM-class layer, MXFP4); by routing (4 us) and cold code where they are few.
 template <int F, int X, int PX, bool EXACT>
 __global__ __launch_bounds__(kUpWaves * 64, PX == 1 ? 4 : 2) void tokens_up_kernel(TokensArgs a) {
   __shared__ Routing s;
@@ -462,9 +463,9 @@ __global__ __launch_bounds__(kUpWaves * 64, 2) void tokens_up_any_kernel(TokensA
 }
 
 // y: a block takes 64 columns and one share of the units of all experts in use, which its waves take in
-// turn, so that they read neighbouring lines of the same rows; four row tiles of W2 meet each piece of h that a wave loads. With several shares the
-// block that finishes last adds them up in their order: a share is written past the caches of its
-// own XCD, then counted. PAIRS: I and S are at least 256 (EXACT: multiples of it), and a unit is a pair
+// turn, so that they read neighbouring lines of the same rows; four row tiles of W2 meet each piece of
+// h that a wave loads. With several shares the block that finishes last adds them up in their order: a
+// share is written past the caches of its own XCD, then counted. PAIRS: I and S are at least 256 (EXACT: multiples of it), and a unit is a pair
 // of steps; else it is a step. With the next pair's codes in flight beside, at twice the registers
 // and half the waves, eight tokens of the GLM-class layer (MXFP4) took 108 us against 103.
 template <int F, int X, bool PAIRS, bool EXACT>
