@@ -586,7 +586,7 @@ hmoe_status moe_tokens_scratch_bytes(int32_t M, int32_t E, int32_t H, int32_t I,
  *   l = router x;  the k largest by moe_route's rule, weights p their softmax;
  *   y = base + sum over j of p_j W2_e (silu(Wg_e x) * (Wu_e x)) + sigmoid(shared_gate . x) * the
  *       shared expert's (weight 1 without a gate)
- * in fp32, rounded once; h goes into the second product with 16 of its bits. base [M, H] as in
+ * in fp32, rounded once; h goes into the second product with all of its 24 bits. base [M, H] as in
  * moe_linear. topk_ids int32 [M, k] and topk_w fp32 [M, k] receive the routing, each may be NULL.
  * An expert that several tokens took is read once. Three launches. M = 0 is a no-op.
  * Errors: HMOE_ERR_INVALID_ARG (layer NULL; M < 0; E outside 1..1024; k outside 1..min(16, E); H

@@ -1,0 +1,98 @@
+"""What enters the products of moe_linear, its gradient and moe_tokens is not rounded: an addend that takes
+the leading bits out of a result shows the ones below, which a result alone would round away."""
+import numpy as np
+import pytest
+
+from oracle import packed as P
+from packed_testlib import packed, rounded, upload
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def hm():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import weight_only_quantized_moe_amd as m
+    m.load_library()
+    return m
+
+
+def identity(fmt, N, K):
+    """A packed matrix whose row n is 1 in column n % K and 0 elsewhere (code 2 is 1.0)."""
+    q = np.zeros((N, K // 2), np.uint8)
+    n = np.arange(N)
+    q[n, n % K // 2] = np.where(n % 2, 0x20, 0x02)
+    w = {"fmt": fmt, "q": q, "z": None, "g": None, "group": 0}
+    if fmt == "nvfp4":
+        w["s"], w["g"] = np.full((N, K // 16), 0x38, np.uint8), np.ones(1, np.float32)
+    else:
+        w["s"] = np.full((N, K // 32), 127, np.uint8)
+    assert (P.values(w)[n, n % K] == 1).all() and P.values(w).sum() == N
+    return w
+
+
+def one_expert(w):
+    return dict(w, q=w["q"][None], s=w["s"][None])
+
+
+def tokens(hm, x, w13, w2, base, S):
+    """One expert of weight 1, or, with S, a shared expert beside one whose weights are zero."""
+    import torch
+    M, H = x.shape
+    zero = lambda w: dict(w, q=np.zeros_like(w["q"]))  # noqa: E731
+    shared = (upload(w13), upload(w2), None) if S else None
+    a, b = (one_expert(zero(w) if S else w) for w in (w13, w2))
+    y = torch.empty(M, H, dtype=x.dtype, device="cuda")
+    I = w2["q"].shape[1] * 2
+    ws = torch.full((hm.moe_tokens_scratch_bytes(M, 1, H, I, 1, I if S else 0),), 0xFF, dtype=torch.uint8, device="cuda")
+    hm.moe_tokens(x.cuda(), torch.zeros(1, H, dtype=x.dtype, device="cuda"), upload(a), upload(b), 1, y,
+                  None if base is None else base.cuda(), shared, scratch=ws)
+    return y.cpu().double().numpy()
+
+
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("H,I", [(64, 32), (64, 96), (256, 256), (320, 288)])   # steps, pairs, partial pairs
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_h_keeps_its_24_bits(hm, fmt, H, I, shared):
+    """y = base + h with base the fp16 nearest to -h: what is left is h below its eleventh bit. x has one
+    element other than zero, so that gate and up are one exact product each; silu is off by (|gate| + 4) of
+    fp32's half steps (exp's argument, exp, 1 +, reciprocal, product), the two products beside by one each."""
+    rng = np.random.default_rng([H, I])
+    w13 = packed(rng, (2 * I, H), fmt, spread=1)
+    W13 = P.values(w13)
+    M = 5
+    x = np.zeros((M, H))
+    cols = rng.choice(H, M, replace=False)
+    x[np.arange(M), cols] = rng.integers(3, 9, M) * 2.0
+    a, b = x @ W13[:I].T, x @ W13[I:].T
+    h = (a / (1 + np.exp(-a)) * b)[:, np.arange(H) % I]
+    base, bt = rounded(-h, "fp16")
+    y = tokens(hm, rounded(x, "fp16")[1], w13, identity(fmt, H, I), bt, shared)
+    want = h + base
+    tol = np.abs(h) * ((np.abs(a)[:, np.arange(H) % I] + 7) * 2.0 ** -24) * 1.01 + np.abs(want) * 2.0 ** -11 + 2.0 ** -25
+    # the test can tell 16 bits (off by up to 2^-17) from 24
+    assert (tol < np.abs(h) * 2.0 ** -18)[np.abs(h) > 0.25].any()
+    assert (np.abs(y - want) <= tol).all(), float((np.abs(y - want) / tol).max())
+
+
+@pytest.mark.parametrize("H,I", [(64, 32), (256, 256)])
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_an_infinite_h_is_infinite(hm, fmt, H, I):
+    """gate and up of 2^100 and more: h is an infinity, and so is y wherever its weight is not zero."""
+    rng = np.random.default_rng(I)
+    w13 = packed(rng, (2 * I, H), fmt)
+    w13["q"] = np.full_like(w13["q"], 0x22)       # positive weights
+    w2 = packed(rng, (H, I), fmt)
+    w2["q"] = np.where(rng.random(w2["q"].shape) < 0.5, 0x11, 0x19).astype(np.uint8)   # element 2j + 1: 0.5, 2j: +-0.5
+    w2["q"][:, 1:] = 0x22
+    x = np.zeros((3, H))
+    x[1, 0] = 2.0 ** 110
+    x[0, 1] = x[2, 2] = 1.0
+    y = tokens(hm, rounded(x, "bf16")[1], w13, w2, None, False)
+    W2 = P.values(w2)
+    up = (W2 > 0).all(1)
+    assert up.any() and not up.all()
+    assert (y[1, up] == np.inf).all() and np.isnan(y[1, ~up]).all()
+    assert np.isfinite(y[[0, 2]]).all()

@@ -90,7 +90,7 @@ __global__ __launch_bounds__(512, PX == 1 ? 4 : 2) void linear_wide_kernel(Linea
       constexpr int j = decltype(P)::value;
       if (share.first + j < share.own) return;
 #pragma unroll
-      for (int r = 0; r < R; ++r) pair_product<F, X, X, PX, j, 1>(acc[r], c[j][r], now[r], a[j]);
+      for (int r = 0; r < R; ++r) pair_product<F, X, X, PX, j>(acc[r], c[j][r], now[r], a[j]);
     };
     // the two cases apart: a load behind a condition would make the waits count on its absence
     if (next < items) {
@@ -179,7 +179,7 @@ __global__ __launch_bounds__(T == 1 ? 1024 : 512) void linear_rows_kernel(Linear
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       Codes<F> v = c[r];
-      step_product<F, X, X, T, 1>(acc[r], v, a, blocks);
+      step_product<F, X, X, T>(acc[r], v, a, blocks);
     }
   };
 
@@ -290,7 +290,7 @@ __global__ __launch_bounds__(512, 2) void linear_rows_pair_kernel(LinearRows p) 
         Codes<F> k;
         k.q = c[r].a;
         take_scales_of<F>(k, v[r], step);
-        step_product<F, X, X, T, 1>(acc[r], k, a, 4);
+        step_product<F, X, X, T>(acc[r], k, a, 4);
       }
       if (step) break;
       rows(2 * pair + 1);

@@ -267,17 +267,88 @@ __device__ __forceinline__ void block_product(f32x4 (&acc)[NT], const Codes<F>& 
 
 // The four column blocks of a step against 16 NT rows of activations in registers; blocks: those
 // inside K (four unless the step is a row's last). The codes' dwords are turned in place.
-template <int F, int X, int S, int NT, int PARTS>
-__device__ __forceinline__ void step_product(f32x4 (&acc)[NT], Codes<F>& c, const u32x4 (&a)[PARTS][4][NT], int blocks) {
+template <int F, int X, int S, int NT>
+__device__ __forceinline__ void step_product(f32x4 (&acc)[NT], Codes<F>& c, const u32x4 (&a)[1][4][NT], int blocks) {
   turn4(c.q);
   constexpr int N = group_of(F) <= 32 ? 1 : group_of(F) / 32;   // blocks of a group
-  block_product<F, X, S, 0, N, NT, PARTS>(acc, c, a);
+  block_product<F, X, S, 0, N, NT, 1>(acc, c, a);
   if constexpr (N == 1)
-    if (blocks > 1) block_product<F, X, S, 1, N, NT, PARTS>(acc, c, a);
+    if (blocks > 1) block_product<F, X, S, 1, N, NT, 1>(acc, c, a);
   if constexpr (N <= 2)
-    if (blocks > 2) block_product<F, X, S, 2, N, NT, PARTS>(acc, c, a);
+    if (blocks > 2) block_product<F, X, S, 2, N, NT, 1>(acc, c, a);
   if constexpr (N == 1)
-    if (blocks > 3) block_product<F, X, S, 3, N, NT, PARTS>(acc, c, a);
+    if (blocks > 3) block_product<F, X, S, 3, N, NT, 1>(acc, c, a);
+}
+
+// Eight fp32 values as three bf16 operands whose sum they are (24 bits, eight a part), in the order the
+// format takes. What is left of an infinity is nothing, but for INT4, whose offset makes it NaN in any case;
+// infinite: there may be one.
+template <int F>
+__device__ __forceinline__ void f32_operands(u32x4 (&a)[3], const f32x4 (&h)[2], bool infinite) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = is_int4(F) ? h[i & 1][i >> 1] : h[i >> 2][i & 3];
+#pragma unroll
+  for (int part = 0; part < 3; ++part)
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const uint32_t lo = __float_as_uint(v[i]), hi = __float_as_uint(v[i + 1]);
+      a[part][i >> 1] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);   // the high halves
+      v[i] -= __uint_as_float(lo & 0xFFFF0000u);
+      v[i + 1] -= __uint_as_float(hi & 0xFFFF0000u);
+    }
+  if (!is_int4(F) && infinite)   // (the same for all waves, and rare)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = a[0][i];
+      const uint32_t keep = ((w & 0x7FFFu) == 0x7F80u ? 0u : 0xFFFFu) | ((w & 0x7FFF0000u) == 0x7F800000u ? 0u : 0xFFFF0000u);
+      a[1][i] &= keep;
+      a[2][i] &= keep;
+    }
+}
+
+// The four column blocks of a step of R tiles against 16 rows of fp32 values: as step_product, block by
+// block, so that a block's parts are made once for all tiles. INT4's offsets meet the sum of the block's
+// values, which is the same for all tiles too. S: the 16-bit type of INT4 scales.
+template <int F, int S, int T, int R>
+__device__ __forceinline__ void blocks_product_f32(f32x4 (&acc)[R][1], const Codes<F> (&c)[R], const f32x4 (&h)[4][2],
+                                                   int blocks, bool infinite) {
+  if constexpr (T < 4) {
+    if (blocks <= T) return;
+    u32x4 parts[3];
+    f32_operands<F>(parts, h[T], infinite);
+    if constexpr (is_int4(F)) {
+      f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+      const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+#pragma unroll
+      for (int i = 0; i < 3; ++i) sum = mfma16<kBf>(parts[i], ones, sum);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float s = block_scale<F, S, T>(c[r]);
+        const float z = (float)(16u + ((c[r].z >> (8 * (T * 32 / group_of(F)))) & 15u));
+        const u32x4 b = int4_operand<kBf>(c[r].q[T]);
+        f32x4 p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 3; ++i) p = mfma16<kBf>(parts[i], b, p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[r][0][i] = fmaf(s, fmaf(-z, sum[i], p[i]), acc[r][0][i]);
+      }
+    } else {
+      u32x4 a[3][4][1];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) a[i][T][0] = parts[i];
+#pragma unroll
+      for (int r = 0; r < R; ++r) block_product<F, kBf, S, T, 1, 1, 3>(acc[r], c[r], a);
+    }
+    blocks_product_f32<F, S, T + 1, R>(acc, c, h, blocks, infinite);
+  }
+}
+template <int F, int S, int R>
+__device__ __forceinline__ void step_product_f32(f32x4 (&acc)[R][1], Codes<F> (&c)[R], const f32x4 (&h)[4][2], int blocks,
+                                                 bool infinite) {
+#pragma unroll
+  for (int r = 0; r < R; ++r) turn4(c[r].q);
+  blocks_product_f32<F, S, 0, R>(acc, c, h, blocks, infinite);
 }
 
 // load_codes where only the last step of a row can be partial (ALL: none is)
@@ -498,17 +569,17 @@ __device__ __forceinline__ void take_scales_of(Codes<F>& c, const StepScales<F, 
 }
 
 // Pair P of a wave's PX: both steps' products.
-template <int F, int X, int S, int PX, int P, int PARTS>
+template <int F, int X, int S, int PX, int P>
 __device__ __forceinline__ void pair_product(f32x4 (&acc)[1], PairCodes& q, const StepScales<F, 2 * PX>& v,
-                                             const u32x4 (&a)[2][PARTS][4][1]) {
+                                             const u32x4 (&a)[2][1][4][1]) {
   split_pair(q);
   Codes<F> c;
   c.q = q.a;
   take_scales<F, 2 * PX, 2 * P>(c, v);
-  step_product<F, X, S, 1, PARTS>(acc, c, a[0], 4);
+  step_product<F, X, S, 1>(acc, c, a[0], 4);
   c.q = q.b;
   take_scales<F, 2 * PX, 2 * P + 1>(c, v);
-  step_product<F, X, S, 1, PARTS>(acc, c, a[1], 4);
+  step_product<F, X, S, 1>(acc, c, a[1], 4);
 }
 
 // for (P = 0; P < N; ++P) f(P) with P a constant

@@ -10,9 +10,8 @@
 // columns to finish adds the shares up in their order. An expert that several tokens took is read
 // once: its tokens are rows of the same MFMA.
 //
-// h, times its routing weight and the second matrix's own scale, goes into the second product as
-// two bf16 parts (16 of its 24 bits, 2^-17 of its value off): rounding it to 16 bits once would
-// add an error like that of y's own rounding, and the matrix cores have the time.
+// h, times its routing weight and the second matrix's own scale, is kept in fp32 and goes into the second
+// product as three bf16 parts that hold all of its 24 bits: it is not rounded.
 #include <algorithm>
 
 #include "packed.h"
@@ -30,6 +29,7 @@ constexpr int kMaxPairs = HMOE_TOKENS_MAX_M * kMaxTopK;   // (token, expert) pai
 
 // What the second launch leaves for the third.
 struct TokensPlan {
+  int infinite;                  // whether an h is infinite (cleared by the first launch)
   int count;                     // experts in use, ascending
   int expert[kMaxPairs];
   int16_t row[kMaxPairs * 16];   // row of h of each token, -1: the token did not take this expert
@@ -37,7 +37,7 @@ struct TokensPlan {
 
 // Scratch, as offsets.
 struct TokensScratch {
-  size_t logits = 0, plan = 0, h = 0, hs = 0, sums = 0, done = 0, total = 0;   // h, hs: high parts, then low parts
+  size_t logits = 0, plan = 0, h = 0, hs = 0, sums = 0, done = 0, total = 0;
   int pitch = 0, parts = 0;   // of the logits: row pitch, shares of H
   int tiles = 0, shares = 0;  // of y: tiles of columns, shares of the experts' steps
 };
@@ -76,8 +76,8 @@ struct TokensArgs {
   float* logits;  // [parts, M, pitch]
   int pitch, parts;
   TokensPlan* plan;
-  uint16_t* h;    // [2, M k, I]
-  uint16_t* hs;   // [2, M, S]
+  float* h;       // [M k, I]
+  float* hs;      // [M, S]
   float* sums;    // [shares, tiles, M, 64]
   int* done;      // [tiles]: shares that are finished
   int tiles, shares;
@@ -90,8 +90,10 @@ __global__ __launch_bounds__(512) void tokens_router_kernel(TokensArgs a) {
   __shared__ float red[8][256];
   const Tokens& p = a.p;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  if (blockIdx.x == 0 && blockIdx.y == 0)   // the third launch counts from zero
+  if (blockIdx.x == 0 && blockIdx.y == 0) {   // the third launch counts from zero
     for (int i = threadIdx.x; i < a.tiles; i += 512) a.done[i] = 0;
+    if (threadIdx.x == 0) a.plan->infinite = 0;
+  }
   const int e = blockIdx.x * 16 + (lane & 15), rows = p.E + (p.gate ? 1 : 0);
   const uint16_t* r = (e < p.E ? p.router + (long)e * p.H : p.gate ? p.gate : p.router) + (lane >> 4) * 8;
   const uint16_t* x = p.x + (long)min(lane & 15, p.M - 1) * p.xs + (lane >> 4) * 8;
@@ -318,14 +320,9 @@ __device__ __forceinline__ void finish_item(const TokensArgs& a, const Routing& 
     gate *= v.g13;
     up *= v.g13;
     const float h = silu(gate) * up * (weight * v.g2);
-    const uint32_t hi = __float_as_uint(h) & 0xFFFF0000u;
-    const float lo = __builtin_isinf(h) ? 0.f : h - __uint_as_float(hi);
-    const long rows = v.shared ? p.M : p.M * p.k;
-    uint16_t* out = v.shared ? a.hs : a.h;
     const long r = v.shared ? t : s.off[v.d] + __popc(mask & ((1u << t) - 1u));
-    const long at = r * v.width + i;
-    out[at] = (uint16_t)(hi >> 16);
-    out[rows * v.width + at] = from_f32<kBf>(lo);
+    (v.shared ? a.hs : a.h)[r * v.width + i] = h;
+    if (__builtin_isinf(h)) a.plan->infinite = 1;
   }
 }
 
@@ -388,8 +385,8 @@ __global__ __launch_bounds__(kUpWaves * 64, PX == 1 ? 4 : 2) void tokens_up_kern
     auto products = [&](auto P) __attribute__((always_inline)) {
       constexpr int j = decltype(P)::value;
       if (share.first + j < share.own) return;
-      pair_product<F, X, X, PX, j, 1>(acc[0], c[j][0], now[0], xv[j]);
-      pair_product<F, X, X, PX, j, 1>(acc[1], c[j][1], now[1], xv[j]);
+      pair_product<F, X, X, PX, j>(acc[0], c[j][0], now[0], xv[j]);
+      pair_product<F, X, X, PX, j>(acc[1], c[j][1], now[1], xv[j]);
     };
     // the two cases apart: a load behind a condition would make the waits count on its absence
     if (next < items) {
@@ -450,7 +447,7 @@ __global__ __launch_bounds__(kUpWaves * 64, 2) void tokens_up_any_kernel(TokensA
         const int step = s0 + j * kUpWaves;
         if (step >= steps) continue;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) step_product<F, X, X, 1, 1>(acc[r], c[j][r], xv[j], step_blocks<false>(step, H));
+        for (int r = 0; r < 2; ++r) step_product<F, X, X, 1>(acc[r], c[j][r], xv[j], step_blocks<false>(step, H));
       }
     }
 #pragma unroll
@@ -465,8 +462,10 @@ __global__ __launch_bounds__(kUpWaves * 64, 2) void tokens_up_any_kernel(TokensA
 // y: a block takes 64 columns and one share of the units of all experts in use, which its waves take in
 // turn, so that they read neighbouring lines of the same rows; four row tiles of W2 meet each piece of
 // h that a wave loads. With several shares the block that finishes last adds them up in their order: a
-// share is written past the caches of its own XCD, then counted. PAIRS: I and S are at least 256 (EXACT: multiples of it), and a unit is a pair
-// of steps; else it is a step. With the next pair's codes in flight beside, at twice the registers
+// share is written past the caches of its own XCD, then counted. PAIRS: I and S are at least 256 (EXACT:
+// multiples of it), and a unit is a pair of steps; else it is a step. h comes as fp32 and is split here,
+// as three 16-bit planes of it would need 16 registers more (spills; two planes, 16 of the 24 bits, took 240
+// us instead of 249 for eight tokens of the GLM-class layer, MXFP4). With the next pair's codes in flight beside, at twice the registers
 // and half the waves, eight tokens of the GLM-class layer (MXFP4) took 108 us against 103.
 template <int F, int X, bool PAIRS, bool EXACT>
 __global__ __launch_bounds__(kDownWaves * 64, 4) void tokens_down_kernel(TokensArgs a) {
@@ -485,6 +484,7 @@ __global__ __launch_bounds__(kDownWaves * 64, 4) void tokens_down_kernel(TokensA
     if (i < most) s_expert[i] = a.plan->expert[i];
   }
   const int count = a.plan->count;
+  const bool infinite = a.plan->infinite;
   __syncthreads();
   const int m = lane & 15;
   const int units = (p.I + kUnit - 1) / kUnit, total = count * units + (p.S + kUnit - 1) / kUnit;
@@ -507,29 +507,21 @@ __global__ __launch_bounds__(kDownWaves * 64, 4) void tokens_down_kernel(TokensA
     return place(d, u);
   };
   auto row_of = [&](const Place& v) { return v.shared ? 0l : (long)__builtin_amdgcn_readfirstlane(s_expert[v.d]) * p.H; };
-  // h of a step, both parts, zeros for tokens that did not take the expert: only the lanes of the others
-  // load, which costs the address unit less than stand-ins would
-  auto rows = [&](u32x4(&hv)[2][4][1], const Place& v, int step, int blocks) __attribute__((always_inline)) {
+  // h of a step, zeros for tokens that did not take the expert: only the lanes of the others load, which
+  // costs the address unit less than stand-ins would
+  auto rows = [&](f32x4(&hv)[4][2], const Place& v, int step, int blocks) __attribute__((always_inline)) {
     const int hr = v.shared ? (m < p.M ? m : -1) : s_row[v.d * 16 + m];
-    const uint16_t* h = (v.shared ? a.hs : a.h) + (long)max(hr, 0) * v.K + (lane >> 4) * 8 + step * 128;
-    const long low = (long)(v.shared ? p.M : p.M * p.k) * v.K;
+    const float* h = (v.shared ? a.hs : a.h) + (long)max(hr, 0) * v.K + (lane >> 4) * 8 + step * 128;
 #pragma unroll
-    for (int b = 0; b < 4; ++b) hv[0][b][0] = hv[1][b][0] = u32x4{0u, 0u, 0u, 0u};
-    if (hr >= 0) {
+    for (int b = 0; b < 4; ++b) hv[b][0] = hv[b][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (hr < 0) return;
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int at = PAIRS && !EXACT ? min(b * 32, v.K - 32 - step * 128) : min(b, blocks - 1) * 32;
-        hv[0][b][0] = *reinterpret_cast<const u32x4*>(h + at);
-        hv[1][b][0] = *reinterpret_cast<const u32x4*>(h + low + at);
-      }
+    for (int b = 0; b < 4; ++b) {
+      if (PAIRS && !EXACT && step * 128 + b * 32 >= v.K) continue;
+      const float* at = h + min(b, blocks - 1) * 32;
+      hv[b][0] = *reinterpret_cast<const f32x4*>(at);
+      hv[b][1] = *reinterpret_cast<const f32x4*>(at + 4);
     }
-#pragma unroll
-    for (int b = 0; b < 4; ++b)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (PAIRS && !EXACT && step * 128 + b * 32 >= v.K) hv[i][b][0] = u32x4{0u, 0u, 0u, 0u};
-        if constexpr (is_int4(F) && !PAIRS) hv[i][b][0] = int4_order(hv[i][b][0]);
-      }
   };
   if (from < to) {
     Place now = place(min(from / units, count), 0);
@@ -542,7 +534,7 @@ __global__ __launch_bounds__(kDownWaves * 64, 4) void tokens_down_kernel(TokensA
         const long first = row_of(now);
         const TileLane<EXACT> at = tile_lane<F, 2, EXACT>(lane, now.K, 16, 2 * now.u);
         const bool end = !EXACT && now.K % 256 && now.u == now.K / 256;
-        u32x4 hv[2][4][1];
+        f32x4 hv[4][2];
         rows(hv, now, 2 * now.u, 4);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -558,20 +550,13 @@ __global__ __launch_bounds__(kDownWaves * 64, 4) void tokens_down_kernel(TokensA
         }
 #pragma nounroll   // once through cold code for both steps
         for (int step = 0;; ++step) {
-          if constexpr (is_int4(F)) {
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              hv[0][b][0] = int4_order(hv[0][b][0]);
-              hv[1][b][0] = int4_order(hv[1][b][0]);
-            }
-          }
+          Codes<F> k[R];
 #pragma unroll
           for (int r = 0; r < R; ++r) {
-            Codes<F> k;
-            k.q = c[r].a;
-            take_scales_of<F>(k, v[r], step);
-            step_product<F, kBf, X, 1, 2>(acc[r], k, hv, 4);
+            k[r].q = c[r].a;
+            take_scales_of<F>(k[r], v[r], step);
           }
+          step_product_f32<F, X, R>(acc, k, hv, 4, infinite);
           if (step) break;
           rows(hv, now, 2 * now.u + 1, 4);
 #pragma unroll
@@ -587,10 +572,9 @@ __global__ __launch_bounds__(kDownWaves * 64, 4) void tokens_down_kernel(TokensA
         for (int r = 0; r < R; ++r)
           load_step<F, false>(c[r], packed_row<F>(pick(now.shared, p.s2, p.w2), row_of(now) + min(n0 + 16 * r + m, p.H - 1),
                                                   now.K, lane), now.u, now.K, lane);
-        u32x4 hv[2][4][1];
+        f32x4 hv[4][2];
         rows(hv, now, now.u, blocks);
-#pragma unroll
-        for (int r = 0; r < R; ++r) step_product<F, kBf, X, 1, 2>(acc[r], c[r], hv, blocks);
+        step_product_f32<F, X, R>(acc, c, hv, blocks, infinite);
         now = after(now);
       }
     }
@@ -669,13 +653,14 @@ hipError_t run_tokens(const TokensArgs& a, hipStream_t s) {
   err = run_up<F, X>(a, s);
   if (err != hipSuccess) return err;
   const dim3 down((unsigned)a.tiles, (unsigned)a.shares);
-  // the smaller INT4 groups' scales and zero points do not leave pairs the registers, nor do INT4's partial pairs
-  constexpr bool kPairs = F != kI32 && F != kI64, kEnds = !is_int4(F);
+  // INT4's scales and zero points do not leave pairs the registers: with half the waves instead, eight tokens
+  // of a layer of 256 experts, 6144 to 2048, g128 take 342 us against 307 by steps
+  constexpr bool kPairs = !is_int4(F);
   const dim3 block(kDownWaves * 64);
   if (kPairs && p.I % 256 == 0 && p.S % 256 == 0)
     hipLaunchKernelGGL((tokens_down_kernel<F, X, kPairs, true>), down, block, 0, s, a);
-  else if (kEnds && p.I >= 256 && (p.S == 0 || p.S >= 256))
-    hipLaunchKernelGGL((tokens_down_kernel<F, X, kEnds, !kEnds>), down, block, 0, s, a);
+  else if (kPairs && p.I >= 256 && (p.S == 0 || p.S >= 256))
+    hipLaunchKernelGGL((tokens_down_kernel<F, X, kPairs, !kPairs>), down, block, 0, s, a);
   else
     hipLaunchKernelGGL((tokens_down_kernel<F, X, false, true>), down, block, 0, s, a);
   return hipGetLastError();
@@ -701,7 +686,7 @@ hipError_t launch_tokens(const Tokens& p, void* scratch, hipStream_t s) {
   const TokensScratch t = tokens_plan(p.M, p.E, p.H, p.I, p.k, p.S);
   char* ws = static_cast<char*>(scratch);
   const TokensArgs a{p, reinterpret_cast<float*>(ws + t.logits), t.pitch, t.parts, reinterpret_cast<TokensPlan*>(ws + t.plan),
-                     reinterpret_cast<uint16_t*>(ws + t.h), reinterpret_cast<uint16_t*>(ws + t.hs),
+                     reinterpret_cast<float*>(ws + t.h), reinterpret_cast<float*>(ws + t.hs),
                      reinterpret_cast<float*>(ws + t.sums), reinterpret_cast<int*>(ws + t.done), t.tiles, t.shares};
   return p.dtype == HMOE_DTYPE_FP16 ? run_format<kHf>(a, s) : run_format<kBf>(a, s);
 }
