@@ -295,8 +295,9 @@ hmoe_status run_linear(const char* in_name, const void* x, int64_t xs, const hmo
   size_t need;
   hmoe::linear_scratch(M, K, N, back ? nullptr : &need, back ? &need : nullptr);
   if (hmoe_status st = check_op_scratch(scratch, scratch_bytes, need)) return st;
-  if (hmoe_status st = check_apart({x, w->q, w->s, w->z, w->g}, {{out_name, y}})) return st;
-  const hmoe::Linear p{packed_of(*w), dtype, static_cast<const uint16_t*>(x), xs, M, K, N,
+  const hmoe::Packed m = packed_of(*w);
+  if (hmoe_status st = check_apart({x, m.q, m.s, m.z, m.g}, {{out_name, y}})) return st;
+  const hmoe::Linear p{m, dtype, static_cast<const uint16_t*>(x), xs, M, K, N,
                        static_cast<const uint16_t*>(base), bs, static_cast<uint16_t*>(y), ys};
   hipError_t err = hmoe::launch_linear(p, back, scratch, stream);
   if (err != hipSuccess) return hip_fail(err, back ? "linear backward launch" : "linear launch");
@@ -946,16 +947,16 @@ hmoe_status moe_tokens(const hmoe_tokens* layer, const void* x, int64_t x_stride
     return fail(HMOE_ERR_ALIGN, "topk_ids and topk_w must be 16-byte aligned");
   if (hmoe_status st = check_op_scratch(scratch, scratch_bytes, hmoe::tokens_scratch(M, t.num_experts, H, I, t.top_k, S)))
     return st;
-  if (hmoe_status st = check_apart({x, t.router, t.shared_gate, t.w13.q, t.w13.s, t.w2.q, t.w2.s},
+  const hmoe::Packed none{}, w13 = packed_of(t.w13), w2 = packed_of(t.w2);
+  const hmoe::Packed s13 = S > 0 ? packed_of(t.shared_w13) : none, s2 = S > 0 ? packed_of(t.shared_w2) : none;
+  const void* gate = S > 0 ? t.shared_gate : nullptr;
+  if (hmoe_status st = check_apart({x, t.router, gate, w13.q, w13.s, w13.z, w13.g, w2.q, w2.s, w2.z, w2.g,
+                                    s13.q, s13.s, s13.z, s13.g, s2.q, s2.s, s2.z, s2.g},
                                    {{"y", y}, {"topk_ids", topk_ids, base}, {"topk_w", topk_w, base}}))
     return st;
-  const hmoe::Tokens p{t.dtype, static_cast<const uint16_t*>(x), x_stride,
-                       static_cast<const uint16_t*>(t.router),
-                       S > 0 ? static_cast<const uint16_t*>(t.shared_gate) : nullptr,
-                       packed_of(t.w13), packed_of(t.w2),
-                       S > 0 ? packed_of(t.shared_w13) : hmoe::Packed{}, S > 0 ? packed_of(t.shared_w2) : hmoe::Packed{},
-                       M, t.num_experts, H, I, t.top_k, S, static_cast<const uint16_t*>(base), base_stride,
-                       static_cast<uint16_t*>(y), y_stride, topk_ids, topk_w};
+  const hmoe::Tokens p{t.dtype, static_cast<const uint16_t*>(x), x_stride, static_cast<const uint16_t*>(t.router),
+                       static_cast<const uint16_t*>(gate), w13, w2, s13, s2, M, t.num_experts, H, I, t.top_k, S,
+                       static_cast<const uint16_t*>(base), base_stride, static_cast<uint16_t*>(y), y_stride, topk_ids, topk_w};
   hipError_t err = hmoe::launch_tokens(p, scratch, stream);
   if (err != hipSuccess) return hip_fail(err, "tokens launch");
   return HMOE_OK;
