@@ -558,7 +558,7 @@ hmoe_status moe_linear(const void* x, int64_t x_stride, const hmoe_packed* w, in
 /* Gradient of moe_linear with respect to x: dx[m] = dbase[m] + W^T dy[m], dy [M, N], dbase and dx
  * [M, K]; the weights are frozen, and the gradient with respect to base is dy itself (for a bias, its
  * sum over the rows). dbase as base above. W and dy are rounded as by moe_linear's fp16 form, W with an
- * exponent for each group of columns. Two launches up to 64 rows, three beyond (more past one slab).
+ * exponent for each group of columns, but INT4 weights are not rounded up to 64 rows. Two launches up to 64 rows, three beyond (more past one slab).
  * M = 0 is a no-op. Errors: as moe_linear. */
 hmoe_status moe_linear_backward(const void* dy, int64_t dy_stride, const hmoe_packed* w, int32_t M,
                                 int32_t K, int32_t N, int32_t dtype, const void* dbase,

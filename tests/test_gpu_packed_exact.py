@@ -96,3 +96,34 @@ def test_an_infinite_h_is_infinite(hm, fmt, H, I):
     assert up.any() and not up.all()
     assert (y[1, up] == np.inf).all() and np.isnan(y[1, ~up]).all()
     assert np.isfinite(y[[0, 2]]).all()
+
+
+def weights_alone(hm, M, K, N, back, group, zero, dtype):
+    """base + W, row by row: rows of x (or of dy) with one element of 1, base the nearest to -W. What is left
+    of a weight of up to 16 bits below its first 8 or 11 is a number of the type: equal."""
+    import torch
+    rng = np.random.default_rng([M, K, N, back, group, zero])
+    w = packed(rng, (N, K), "int4", group, zero, dtype, spread=0)
+    w["s"], w["s_t"] = rounded(rng.uniform(1.0, 8.0, (N, K // group)), dtype)
+    W = P.values(w)
+    n_in, n_out = (N, K) if back else (K, N)
+    at = rng.integers(0, n_in, M)
+    x = np.zeros((M, n_in))
+    x[np.arange(M), at] = 1.0
+    mine = W[at] if back else W[:, at].T
+    base, bt = rounded(-mine, dtype)
+    left = mine + base
+    assert (rounded(left, dtype)[0] == left).all() and (left != 0).mean() > 0.1
+    y = torch.empty(M, n_out, dtype=bt.dtype, device="cuda")
+    n = hm.moe_linear_scratch_bytes(M, K, N)[back]
+    ws = torch.full((max(n, 256),), 0xFF, dtype=torch.uint8, device="cuda")
+    (hm.moe_linear_backward if back else hm.moe_linear)(rounded(x, dtype)[1].cuda(), upload(w), y, bt.cuda(), ws)
+    assert np.array_equal(y.cpu().double().numpy(), left)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("group,zero", [(32, True), (64, True), (128, True), (32, False), (128, False)])
+@pytest.mark.parametrize("M", [1, 16, 30, 64])
+def test_int4_weights_are_whole_in_few_rows(hm, M, group, zero, dtype):
+    for back in (False, True):
+        weights_alone(hm, M, 384, 150, back, group, zero, dtype)

@@ -541,25 +541,28 @@ struct Weights16 {
 };
 
 // Eight codes times eight scales as fp16, in their order: the scales' pairs (0 1) (2 3) .. for E2M1,
-// (0 4) (1 5) .. for INT4, and the zero points' 16 + z likewise.
+// (0 4) (1 5) .. for INT4, and the zero points' 16 + z likewise. INT4 takes up to 16 bits: what fp16 leaves
+// of a product goes to `low`, if it is wanted, and is exact there (its last place is that of the scale).
 template <int F>
-__device__ __forceinline__ u32x4 scaled_codes(uint32_t w, const uint32_t (&s)[4], const uint32_t (&z)[4]) {
-  auto mul = [](uint32_t a, uint32_t b) {
-    return __builtin_bit_cast(uint32_t, (f16x2)(__builtin_bit_cast(f16x2, a) * __builtin_bit_cast(f16x2, b)));
-  };
-  auto sub = [](uint32_t a, uint32_t b) {
-    return __builtin_bit_cast(uint32_t, (f16x2)(__builtin_bit_cast(f16x2, a) - __builtin_bit_cast(f16x2, b)));
-  };
+__device__ __forceinline__ u32x4 scaled_codes(uint32_t w, const uint32_t (&s)[4], const uint32_t (&z)[4], u32x4* low = nullptr) {
+  auto half2 = [](uint32_t a) { return __builtin_bit_cast(f16x2, a); };
+  auto bits = [](f16x2 a) { return __builtin_bit_cast(uint32_t, a); };
   const u32x4 v = is_int4(F) ? int4_operand<kHf>(w) : e2m1_operand<kHf>(w);
-  const uint32_t v0 = v[0], v1 = v[1], v2 = v[2], v3 = v[3];
-  if constexpr (!is_int4(F)) {
-    return u32x4{mul(v0, s[0]), mul(v1, s[1]), mul(v2, s[2]), mul(v3, s[3])};
-  } else {
-    const uint32_t a = mul(sub(v0, z[0]), s[0]), b = mul(sub(v1, z[1]), s[1]);
-    const uint32_t c = mul(sub(v2, z[2]), s[2]), d = mul(sub(v3, z[3]), s[3]);
-    return u32x4{__builtin_amdgcn_perm(b, a, 0x05040100u), __builtin_amdgcn_perm(d, c, 0x05040100u),
-                 __builtin_amdgcn_perm(b, a, 0x07060302u), __builtin_amdgcn_perm(d, c, 0x07060302u)};
+  uint32_t hi[4], lo[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t vi = v[i];
+    const f16x2 c = is_int4(F) ? half2(vi) - half2(z[i]) : half2(vi), p = c * half2(s[i]);
+    hi[i] = bits(p);
+    lo[i] = is_int4(F) && low ? bits(__builtin_elementwise_fma(c, half2(s[i]), -p)) : 0u;
   }
+  if constexpr (!is_int4(F)) return u32x4{hi[0], hi[1], hi[2], hi[3]};
+  auto order = [](const uint32_t(&a)[4]) {
+    return u32x4{__builtin_amdgcn_perm(a[1], a[0], 0x05040100u), __builtin_amdgcn_perm(a[3], a[2], 0x05040100u),
+                 __builtin_amdgcn_perm(a[1], a[0], 0x07060302u), __builtin_amdgcn_perm(a[3], a[2], 0x07060302u)};
+  };
+  if (low) *low = order(lo);
+  return order(hi);
 }
 // A group's scale times 2^-e as fp16 bits, and 16 + z
 template <int F, int S>
@@ -628,11 +631,12 @@ __device__ __forceinline__ void turn_codes(uint32_t (&v)[8]) {
   }
 }
 
-// 32 rows n of W, block `block` of the reduction axis, and the lane's eight columns from k on: out[i] is
-// column k + i of rows 8 (lane >> 4) .. + 7 of the block as fp16 times 2^-e, zeros past N. Each lane
-// turns an 8 x 8 block of codes, and its rows' scales multiply what comes out.
-template <int F, int S>
-__device__ __forceinline__ void turned_block(const Packed& w, int K, int N, int block, int k, int e, int lane, u32x4 (&out)[8]) {
+// 32 rows n of W, block `block` of the reduction axis, and the lane's eight columns from k on: take(i, operand,
+// low) is given column k + i of rows 8 (lane >> 4) .. + 7 of the block as fp16 times 2^-e, zeros past N, and for
+// INT4, if LOW, what that leaves of it. Each lane turns an 8 x 8 block of codes, and its rows' scales multiply
+// what comes out.
+template <int F, int S, bool LOW, typename Fn>
+__device__ __forceinline__ void turned_block(const Packed& w, int K, int N, int block, int k, int e, int lane, Fn&& take) {
   constexpr int G = group_of(F);
   uint32_t v[8], s1[8], z1[8];
 #pragma unroll
@@ -656,7 +660,11 @@ __device__ __forceinline__ void turned_block(const Packed& w, int K, int N, int 
     z[j] = z1[a] | z1[b] << 16;
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) out[i] = scaled_codes<F>(v[i], s, z);
+  for (int i = 0; i < 8; ++i) {
+    u32x4 low;
+    const u32x4 v16 = scaled_codes<F>(v[i], s, z, LOW ? &low : nullptr);
+    take(i, v16, low);
+  }
 }
 
 // The 16-bit form of columns [first, first + cols) of W. A wave takes a block of the reduction axis and
@@ -666,15 +674,13 @@ __global__ __launch_bounds__(256) void weights16_turned_kernel(Weights16 p) {
   const int lane = threadIdx.x & 63, block = blockIdx.x * 4 + (threadIdx.x >> 6);
   if (block >= p.blocks) return;
   const int k = p.first + min(blockIdx.y * 128 + 8 * (lane & 15), p.cols - 8);   // cols is a multiple of 32
-  u32x4 v[8];
-  turned_block<F, S>(p.w, p.K, p.N, block, k, F == kNv ? 0 : p.eb[k], lane, v);
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    *reinterpret_cast<u32x4*>(p.out + ((long)(blockIdx.y * 8 + i) * p.blocks + block) * 512 + lane * 8) = v[i];
+  turned_block<F, S, false>(p.w, p.K, p.N, block, k, F == kNv ? 0 : p.eb[k], lane, [&](int i, u32x4 v, u32x4) {
+    *reinterpret_cast<u32x4*>(p.out + ((long)(blockIdx.y * 8 + i) * p.blocks + block) * 512 + lane * 8) = v;
+  });
 }
 
 // Up to 64 rows of the gradient without the 16-bit form in between: y[m, k] = base[m, k] + g 2^(ea[m] +
-// eb[k]) sum_n a[m, n] W[n, k] 2^-eb[k]. A block takes 128 columns, 16 T rows and a share of the blocks
+// eb[k]) sum_n a[m, n] W[n, k] 2^-eb[k], INT4 as two fp16 numbers. A block takes 128 columns, 16 T rows and a share of the blocks
 // of the reduction axis, which its waves take in turn; the last block of the columns to finish adds
 // the shares up in their order.
 struct TurnedRows {
@@ -707,15 +713,17 @@ __global__ __launch_bounds__(256) void linear_turned_kernel(TurnedRows p) {
     for (int i = 0; i < 8; ++i) acc[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int tiles = (p.M + 15) / 16;
   for (int b = blockIdx.y * 4 + wave; b < p.blocks; b += p.splits * 4) {
-    u32x4 a[T], v[8];
+    u32x4 a[T];
 #pragma unroll
     for (int t = 0; t < T; ++t)
       a[t] = *reinterpret_cast<const u32x4*>(p.a + ((long)min(t, tiles - 1) * p.blocks + b) * 512 + lane * 8);
-    turned_block<F, X>(p.w, p.K, p.N, b, k, e, lane, v);
+    turned_block<F, X, is_int4(F)>(p.w, p.K, p.N, b, k, e, lane, [&](int i, u32x4 v, u32x4 low) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+      for (int t = 0; t < T; ++t) acc[t][i] = mfma16<kHf>(a[t], v, acc[t][i]);
+      if constexpr (is_int4(F))   // the matrix cores have the time
 #pragma unroll
-      for (int t = 0; t < T; ++t) acc[t][i] = mfma16<kHf>(a[t], v[i], acc[t][i]);
+        for (int t = 0; t < T; ++t) acc[t][i] = mfma16<kHf>(a[t], low, acc[t][i]);
+    });
   }
   // [row][column]: a lane's eight sums of a row are neighbours
 #pragma unroll
