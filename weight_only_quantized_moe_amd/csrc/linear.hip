@@ -148,15 +148,12 @@ hipError_t launch_wide(const LinearRows& p, hipStream_t s) {
   return run_wide<F, X, 1, 4, true>(p, s);
 }
 
-// A block: 16 R columns n and 16 T rows m, the steps of 128 of K dealt to its waves. D: steps a
-// wave loads at once.
-template <int F, int X, int R, int T, int D>
-__global__ __launch_bounds__(T == 1 ? 1024 : 512) void linear_rows_kernel(LinearRows p) {
-  extern __shared__ float red[];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+// Fewer than 256 columns: a wave takes 16 R columns n and 16 T rows m, and the one or two steps of K.
+template <int F, int X, int R, int T>
+__global__ __launch_bounds__(64) void linear_rows_kernel(LinearRows p) {
+  const int lane = threadIdx.x;
   const int n0 = blockIdx.x * (16 * R), m0 = blockIdx.y * (16 * T);
-  const int K = p.K, full = K / 128;
+  const int K = p.K;
   PackedRow row[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) row[r] = packed_row<F>(p.w, min(n0 + 16 * r + (lane & 15), p.N - 1), K, lane);
@@ -168,72 +165,38 @@ __global__ __launch_bounds__(T == 1 ? 1024 : 512) void linear_rows_kernel(Linear
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int t = 0; t < T; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  auto products = [&](const Codes<F>(&c)[R], u32x4 (&a)[1][4][T], int blocks) {
-    if constexpr (is_int4(F)) {
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-#pragma unroll
-        for (int t = 0; t < T; ++t) a[0][b][t] = int4_order(a[0][b][t]);
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      Codes<F> v = c[r];
-      step_product<F, X, X, T>(acc[r], v, a, blocks);
-    }
-  };
-
-  for (int s0 = wave; s0 < full; s0 += waves * D) {
-    Codes<F> c[D][R];
-    u32x4 a[D][1][4][T];
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-      const int s = min(s0 + d * waves, full - 1);
-#pragma unroll
-      for (int r = 0; r < R; ++r) load_codes<F, true>(c[d][r], row[r], s, K, lane);
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-#pragma unroll
-        for (int t = 0; t < T; ++t) a[d][0][b][t] = load16(xr[t] + s * 128 + b * 32);
-    }
-#pragma unroll
-    for (int d = 0; d < D; ++d)
-      if (s0 + d * waves < full) products(c[d], a[d], 4);
-  }
-  if (K % 128 && wave == full % waves) {
-    const int blocks = K % 128 / 32;
+  for (int step = 0; step * 128 < K; ++step) {
+    const int blocks = step_blocks<false>(step, K);
     Codes<F> c[R];
     u32x4 a[1][4][T];
 #pragma unroll
-    for (int r = 0; r < R; ++r) load_codes<F, false>(c[r], row[r], full, K, lane);
+    for (int r = 0; r < R; ++r) load_step<F, false>(c[r], row[r], step, K, lane);
 #pragma unroll
     for (int b = 0; b < 4; ++b)
 #pragma unroll
-      for (int t = 0; t < T; ++t) a[0][b][t] = load16(xr[t] + full * 128 + min(b, blocks - 1) * 32);
-    products(c, a, blocks);
+      for (int t = 0; t < T; ++t) {
+        a[0][b][t] = load16(xr[t] + step * 128 + min(b, blocks - 1) * 32);
+        if constexpr (is_int4(F)) a[0][b][t] = int4_order(a[0][b][t]);
+      }
+#pragma unroll
+    for (int r = 0; r < R; ++r) step_product<F, X, X, T>(acc[r], c[r], a, blocks);
   }
-
+  const float g = F == kNv ? p.w.g[0] : 1.f;
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int t = 0; t < T; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) red[(wave * (R * T) + r * T + t) * 256 + i * 64 + lane] = acc[r][t][i];
-  __syncthreads();
-  const float g = F == kNv ? p.w.g[0] : 1.f;
-  for (int o = threadIdx.x; o < R * T * 256; o += blockDim.x) {
-    const int l = o & 63, i = (o >> 6) & 3, rt = o >> 8;
-    const int n = n0 + 16 * (rt / T) + (l & 15), m = m0 + 16 * (rt % T) + (l >> 4) * 4 + i;
-    if (m >= p.M || n >= p.N) continue;
-    float v = 0.f;
-    for (int w = 0; w < waves; ++w) v += red[w * (R * T * 256) + o];
-    v *= g;
-    if (p.base) v += to_f32<X>(p.base[m * p.bs + n]);
-    p.y[m * p.ys + n] = from_f32<X>(v);
-  }
+      for (int i = 0; i < 4; ++i) {
+        const int n = n0 + 16 * r + (lane & 15), m = m0 + 16 * t + (lane >> 4) * 4 + i;
+        if (m >= p.M || n >= p.N) continue;
+        float v = acc[r][t][i] * g;
+        if (p.base) v += to_f32<X>(p.base[m * p.bs + n]);
+        p.y[m * p.ys + n] = from_f32<X>(v);
+      }
 }
 
-// The same for rows of at least 256 columns, a pair of steps at a time. The rows' fragments of a step
+// Rows of at least 256 columns: 16 R columns n and 16 T rows m a block, pairs of steps dealt to its waves. The rows' fragments of a step
 // meet the codes of R tiles each; the second step's come while the first is multiplied. Bound by the
 // address unit (a fragment touches 16 lines of x): 64 rows 6144 to 4096, NVFP4, 26 us.
 template <int F, int X, int R, int T, bool EXACT>
@@ -330,11 +293,10 @@ hipError_t run_rows_pairs(const LinearRows& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int F, int X, int R, int T, int D>
-hipError_t run_rows(const LinearRows& p, int waves, hipStream_t s) {
-  hipLaunchKernelGGL((linear_rows_kernel<F, X, R, T, D>),
-                     dim3((unsigned)((p.N + 16 * R - 1) / (16 * R)), (unsigned)((p.M + 16 * T - 1) / (16 * T))),
-                     dim3((unsigned)(waves * 64)), (size_t)waves * R * T * 1024, s, p);
+template <int F, int X, int R, int T>
+hipError_t run_rows(const LinearRows& p, hipStream_t s) {
+  hipLaunchKernelGGL((linear_rows_kernel<F, X, R, T>),
+                     dim3((unsigned)((p.N + 16 * R - 1) / (16 * R)), (unsigned)((p.M + 16 * T - 1) / (16 * T))), dim3(64), 0, s, p);
   return hipGetLastError();
 }
 
@@ -345,8 +307,6 @@ constexpr int rows_tile() { return F == kI32 || (F == kMx && X == kHf) ? 32 : 64
 
 template <int F, int X>
 hipError_t launch_rows(const LinearRows& p, hipStream_t s) {
-  const int steps = std::max(1, p.K / 128);
-  const int waves = std::min(8, steps);
   if (p.M <= 16 && p.K >= 256 && p.K <= wide_max_k(p.K % 256 == 0)) return launch_wide<F, X>(p, s);
   if (p.K >= 256) {
     if (p.M <= 16) return run_rows_pairs<F, X, 1, 1>(p, s);
@@ -356,9 +316,9 @@ hipError_t launch_rows(const LinearRows& p, hipStream_t s) {
     if (p.M <= 32) return one ? run_rows_pairs<F, X, 1, 2>(p, s) : run_rows_pairs<F, X, 2, 2>(p, s);
     return one ? run_rows_pairs<F, X, 1, T>(p, s) : run_rows_pairs<F, X, 2, T>(p, s);
   }
-  if (p.M <= 16) return run_rows<F, X, 1, 1, 2>(p, waves, s);
-  if (p.M <= 32) return run_rows<F, X, 2, 2, 1>(p, waves, s);
-  return run_rows<F, X, 2, 4, 1>(p, std::min(waves, 4), s);
+  if (p.M <= 16) return run_rows<F, X, 1, 1>(p, s);
+  if (p.M <= 32) return run_rows<F, X, 2, 2>(p, s);
+  return run_rows<F, X, 2, 4>(p, s);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -516,18 +476,12 @@ __global__ __launch_bounds__(kPrepThreads) void linear_prep_kernel(Prep p) {
     for (int d = 32; d >= 8; d >>= 1) top = max(top, __shfl_xor(top, d));
     if (lane < 8) part[wave][lane] = (uint32_t)top;
     __syncthreads();
+    static_assert(8 * G <= kPrepThreads, "a thread a column");
     if (threadIdx.x < 8 * G) {
       const int i = threadIdx.x / G, k = (b * 8 + i) * G + threadIdx.x % G;
       top = -1000;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) top = max(top, (int)part[w][i]);
-      if (k < p.K) p.eb[k] = column_exponent<F>(top);
-    }
-    // groups of 128 are more columns than threads
-    for (int i = threadIdx.x + kPrepThreads; i < 8 * G; i += kPrepThreads) {
-      const int k = (b * 8 + i / G) * G + i % G;
-      top = -1000;
-      for (int w = 0; w < kWaves; ++w) top = max(top, (int)part[w][i / G]);
       if (k < p.K) p.eb[k] = column_exponent<F>(top);
     }
   }
@@ -811,7 +765,8 @@ __device__ __forceinline__ void wait_vmem_at_most() {
 template <int X, int TM, int TN, int WM, int WN, int STAGES>
 __global__ __launch_bounds__(WM * WN * 64, 2) void product16_kernel(Product16 p) {
   constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
-  constexpr int BM = WM * TM, BN = WN * TN, kChunks = BM + BN, kLoads = (kChunks + kWaves - 1) / kWaves;
+  constexpr int BM = WM * TM, BN = WN * TN, kChunks = BM + BN, kLoads = kChunks / kWaves;
+  static_assert(BM % kWaves == 0 && BN % kWaves == 0, "a copy is of rows or of columns for all waves");
   __shared__ u32x4 buffer[STAGES][kChunks * 64];
   __shared__ int s_last;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -833,9 +788,9 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void product16_kernel(Product16 p)
   const int tiles_a = (p.M + 15) / 16;
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
-    const int chunk = min(wave + i * kWaves, kChunks - 1);
-    const long t = chunk < BM ? min(t_m * BM + chunk, tiles_a - 1) : min(t_n * BN + chunk - BM, tiles_b - 1);
-    src[i] = (chunk < BM ? p.a : p.b) + t * p.blocks * 512;
+    const int chunk = wave + i * kWaves;
+    const long t = i * kWaves < BM ? min(t_m * BM + chunk, tiles_a - 1) : min(t_n * BN + chunk - BM, tiles_b - 1);
+    src[i] = (i * kWaves < BM ? p.a : p.b) + t * p.blocks * 512;
     dst[i] = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)&buffer[0][chunk * 64];
   }
   auto copy = [&](int block, int slot) {   // past the last: a stand-in that nobody reads, so that the waits can count
@@ -996,12 +951,12 @@ int cdiv(long a, long b) { return (int)((a + b - 1) / b); }
 
 // How the tiled product of M rows and O columns over C runs: its tile, shares of the reduction axis,
 // scratch. Larger tiles read less of LDS and L2 a product; smaller ones fill the card.
-enum : int { kThin = 0, kSmall = 1, kMiddle = 2, kWide = 3, kLarge = 4 };
+enum : int { kSmall, kMiddle, kWide, kLarge };
 struct Plan16 {
-  int tile = kThin, blocks = 0, splits = 1;
+  int tile = kSmall, blocks = 0, splits = 1;
   long slab = 0;          // output columns a slab
   size_t rows = 0, ea = 0, eb = 0, weights = 0, sums = 0, done = 0, total = 0;
-  int bm() const { return tile == kThin ? 32 : tile == kSmall ? 64 : tile == kMiddle ? 128 : 256; }
+  int bm() const { return tile == kSmall ? 64 : tile == kMiddle ? 128 : 256; }
   int bn() const { return tile == kSmall ? 64 : tile == kLarge ? 256 : 128; }
   int tiles(long M, long cols) const { return cdiv(M, bm()) * cdiv(up(cols, 128), bn()); }
 };
@@ -1013,20 +968,18 @@ Plan16 plan16(long M, long C, long O) {
   const long cols = std::min(p.slab, O);
   // shares of at least eight blocks each
   const int most = std::max(1, std::min(kMaxSplits, p.blocks / 8));
-  if (M > 32) {
-    // 256 x 256 a CU at once, or two of 256 x 128, one of which alone takes 0.6 of the time of two:
-    // whichever's last round is fuller (384 large tiles 262 us, as 768 wide ones 215)
-    p.tile = kLarge;
-    const int large = p.tiles(M, cols);
-    p.tile = kWide;
-    const int wide = p.tiles(M, cols), rest = wide % 512;
-    const double t_large = cdiv(large, 256), t_wide = wide / 512 + (rest == 0 ? 0. : rest <= 256 ? 0.6 : 1.);
-    if (large >= 192 || wide >= 256) {
-      p.tile = t_wide < t_large ? kWide : kLarge;
-    } else {
-      p.tile = kMiddle;
-      if (p.tiles(M, cols) * most < 192) p.tile = kSmall;
-    }
+  // 256 x 256 a CU at once, or two of 256 x 128, one of which alone takes 0.6 of the time of two:
+  // whichever's last round is fuller (384 large tiles 262 us, as 768 wide ones 215)
+  p.tile = kLarge;
+  const int large = p.tiles(M, cols);
+  p.tile = kWide;
+  const int wide = p.tiles(M, cols), rest = wide % 512;
+  const double t_large = cdiv(large, 256), t_wide = wide / 512 + (rest == 0 ? 0. : rest <= 256 ? 0.6 : 1.);
+  if (large >= 192 || wide >= 256) {
+    p.tile = t_wide < t_large ? kWide : kLarge;
+  } else {
+    p.tile = kMiddle;
+    if (p.tiles(M, cols) * most < 192) p.tile = kSmall;
   }
   const int tiles = p.tiles(M, cols);
   if (p.tile < kWide) p.splits = std::max(1, std::min(512 / std::max(tiles, 1), most));
@@ -1124,7 +1077,6 @@ hipError_t launch_tiled(const Linear& p, char* scratch, hipStream_t s) {
     const dim3 grid((unsigned)tiles, (unsigned)plan.splits);
     const dim3 block(plan.tile == kLarge ? 512 : 256);
     switch (plan.tile) {
-      case kThin: hipLaunchKernelGGL((product16_kernel<X, 2, 2, 1, 4, 4>), grid, block, 0, s, q); break;
       case kSmall: hipLaunchKernelGGL((product16_kernel<X, 2, 2, 2, 2, 4>), grid, block, 0, s, q); break;
       case kMiddle: hipLaunchKernelGGL((product16_kernel<X, 4, 4, 2, 2, 4>), grid, block, 0, s, q); break;
       case kWide: hipLaunchKernelGGL((product16_kernel<X, 8, 4, 2, 2, 3>), grid, block, 0, s, q); break;

@@ -409,8 +409,7 @@ struct TileLane {
 template <>
 struct TileLane<false> {
   uint32_t lo, hi, s, z, lo_end, hi_end;
-  int s_shift, z_shift;    // bits, per 8 bytes of the load
-  int s_shift2, z_shift2;  // of its second 8 bytes
+  int s_shift, z_shift;    // bits
 };
 
 template <bool EXACT>
@@ -477,12 +476,10 @@ __device__ __forceinline__ TileLane<EXACT> tile_lane(int lane, int K, int rows, 
     const bool inside = K / 256 * 128 + place * 16 < half;
     t.lo_end = lo + (inside ? place * 16 : 0);
     t.hi_end = hi + (inside ? place * 16 : 0);
-    // how far each load (of at most 8 bytes) reaches past the row's end
-    constexpr int sn = T::kBytes < 8 ? T::kBytes : 8, zn = T::kZeros < 8 ? T::kZeros : 8;
-    t.s_shift = 8 * max(0, s + sn - groups * scale_bytes(F));
-    t.z_shift = 8 * max(0, z + zn - groups);
-    t.s_shift2 = 8 * max(0, s + 16 - groups * scale_bytes(F));
-    t.z_shift2 = 0;
+    static_assert(T::kBytes <= 8 && T::kZeros <= 8, "partial pairs: a lane loads one step's scales");
+    // how far the load reaches past the row's end
+    t.s_shift = 8 * max(0, s + T::kBytes - groups * scale_bytes(F));
+    t.z_shift = 8 * max(0, z + T::kZeros - groups);
   }
   return t;
 }
@@ -508,8 +505,7 @@ __device__ __forceinline__ void load_scales(StepScales<F, STEPS>& v, const uint8
     load_bytes<T::kBytes>(v.s, s + at.s);
     if constexpr (is_int4(F)) load_bytes<T::kZeros>(v.z, (z ? z : s) + at.z);
   } else {
-    load_shifted<T::kBytes < 8 ? T::kBytes : 8>(v.s, s + at.s, at.s_shift);
-    if constexpr (T::kBytes == 16) load_shifted<8>(v.s + 2, s + at.s + 8, at.s_shift2);
+    load_shifted<T::kBytes>(v.s, s + at.s, at.s_shift);
     if constexpr (is_int4(F)) load_shifted<T::kZeros>(v.z, (z ? z : s) + at.z, at.z_shift);
   }
 }
