@@ -127,3 +127,11 @@ def weights_alone(hm, M, K, N, back, group, zero, dtype):
 def test_int4_weights_are_whole_in_few_rows(hm, M, group, zero, dtype):
     for back in (False, True):
         weights_alone(hm, M, 384, 150, back, group, zero, dtype)
+
+
+# the tiled product: one slab's shares of the reduction axis, and whole tiles
+@pytest.mark.parametrize("group,zero", [(32, True), (64, True), (128, True), (32, False), (128, False)])
+@pytest.mark.parametrize("M,K,N", [(70, 384, 150), (1030, 384, 150), (1300, 128, 4001)])
+def test_int4_weights_are_whole_in_many_fp16_rows(hm, M, K, N, group, zero):
+    for back in (False, True):
+        weights_alone(hm, M, K, N, back, group, zero, "fp16")

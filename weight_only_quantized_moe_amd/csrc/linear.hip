@@ -333,7 +333,7 @@ hipError_t launch_rows(const LinearRows& p, hipStream_t s) {
 // for c = 0 .. 15. Then a lane's sums of eight tiles are eight neighbours of a row of y, and the
 // transposed form of W comes out of 8 x 8 blocks of codes in one lane's registers.
 constexpr int kBlockK = 32;
-constexpr long kSlabBytes = 64l << 20;   // of the 16-bit form of W at a time: a quarter of the Infinity Cache
+constexpr long kSlabBytes = 64l << 20;   // of the 16-bit form of W at a time, each of its parts: a quarter of the Infinity Cache
 constexpr int kPrepThreads = 1024;
 constexpr int kMaxSplits = 4;   // shares of the reduction axis of the tiled product
 
@@ -487,9 +487,14 @@ __global__ __launch_bounds__(kPrepThreads) void linear_prep_kernel(Prep p) {
   }
 }
 
+// INT4 with fp16 scales takes up to 15 bits: two fp16 numbers a weight, in blocks of the reduction axis behind
+// one another. With bf16 scales it takes 11, and 12 with zero points.
+template <int F, int S>
+constexpr bool in_two() { return is_int4(F) && S == kHf; }
+
 struct Weights16 {
   Packed w;
-  int K, N, first, cols, blocks;   // the slab's first column of the product and their number
+  int K, N, first, cols, blocks;   // the slab's first column of the product and their number; blocks of the rows
   const int* eb;
   uint16_t* out;
 };
@@ -543,7 +548,8 @@ __global__ __launch_bounds__(512) void weights16_kernel(Weights16 p) {
   const long n = p.first + min(col, p.cols - 1);
   const int e = F == kNv ? 0 : p.eb[n];
   const long groups = n * (p.K / G);
-  uint16_t* out = p.out + (long)(blockIdx.x * 8 + i) * p.blocks * 512 + lane * 8;
+  constexpr int kParts = in_two<F, S>() ? 2 : 1;
+  uint16_t* out = p.out + (long)(blockIdx.x * 8 + i) * p.blocks * kParts * 512 + lane * 8;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int b0 = (blockIdx.y * 4 + j) * 4;      // first block of the step
@@ -557,7 +563,10 @@ __global__ __launch_bounds__(512) void weights16_kernel(Weights16 p) {
       const uint32_t s1 = scale16<F, S>(p.w, g, e), z1 = zero16<F>(p.w, g);
       const uint32_t s2 = s1 | s1 << 16, z2 = z1 | z1 << 16;
       const uint32_t s[4] = {s2, s2, s2, s2}, z[4] = {z2, z2, z2, z2};
-      *reinterpret_cast<u32x4*>(out + (long)(b0 + t) * 512) = scaled_codes<F>(q[t], s, z);
+      u32x4 low;
+      u32x4* to = reinterpret_cast<u32x4*>(out + (long)(b0 + t) * kParts * 512);
+      to[0] = scaled_codes<F>(q[t], s, z, kParts == 2 ? &low : nullptr);
+      if constexpr (kParts == 2) to[64] = low;
     }
   }
 }
@@ -628,8 +637,11 @@ __global__ __launch_bounds__(256) void weights16_turned_kernel(Weights16 p) {
   const int lane = threadIdx.x & 63, block = blockIdx.x * 4 + (threadIdx.x >> 6);
   if (block >= p.blocks) return;
   const int k = p.first + min(blockIdx.y * 128 + 8 * (lane & 15), p.cols - 8);   // cols is a multiple of 32
-  turned_block<F, S, false>(p.w, p.K, p.N, block, k, F == kNv ? 0 : p.eb[k], lane, [&](int i, u32x4 v, u32x4) {
-    *reinterpret_cast<u32x4*>(p.out + ((long)(blockIdx.y * 8 + i) * p.blocks + block) * 512 + lane * 8) = v;
+  constexpr int kParts = in_two<F, S>() ? 2 : 1;
+  turned_block<F, S, kParts == 2>(p.w, p.K, p.N, block, k, F == kNv ? 0 : p.eb[k], lane, [&](int i, u32x4 v, u32x4 low) {
+    u32x4* to = reinterpret_cast<u32x4*>(p.out + ((long)(blockIdx.y * 8 + i) * p.blocks + block) * kParts * 512 + lane * 8);
+    to[0] = v;
+    if constexpr (kParts == 2) to[64] = low;
   });
 }
 
@@ -741,7 +753,7 @@ struct Product16 {
   const uint16_t* b;    // cols columns, fragment order
   const int* eb;        // [cols]; null: 0
   const float* g;       // NVFP4's scale of the matrix; null: 1
-  int M, cols, blocks;
+  int M, cols, blocks;  // blocks of the reduction axis as b has them
   const uint16_t* base; // [M, cols]; may be null
   long bs;
   uint16_t* y;
@@ -761,8 +773,8 @@ __device__ __forceinline__ void wait_vmem_at_most() {
 // flight, loaded by copies that go past the registers; a wave reads the next block's fragments
 // while it multiplies the present one's. With splits > 1 the block of a tile that finishes last adds the
 // shares up in their order. 4096 rows 6144 to 4096 take 185 us, 1.1 PFLOP/s, near what LDS gives: a wave
-// reads 12 KiB for 32 MFMAs.
-template <int X, int TM, int TN, int WM, int WN, int STAGES>
+// reads 12 KiB for 32 MFMAs. PARTS: blocks of b for each block of a.
+template <int X, int TM, int TN, int WM, int WN, int STAGES, int PARTS>
 __global__ __launch_bounds__(WM * WN * 64, 2) void product16_kernel(Product16 p) {
   constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
   constexpr int BM = WM * TM, BN = WN * TN, kChunks = BM + BN, kLoads = kChunks / kWaves;
@@ -790,17 +802,18 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void product16_kernel(Product16 p)
   for (int i = 0; i < kLoads; ++i) {
     const int chunk = wave + i * kWaves;
     const long t = i * kWaves < BM ? min(t_m * BM + chunk, tiles_a - 1) : min(t_n * BN + chunk - BM, tiles_b - 1);
-    src[i] = (i * kWaves < BM ? p.a : p.b) + t * p.blocks * 512;
+    src[i] = i * kWaves < BM ? p.a + t * (p.blocks / PARTS) * 512 : p.b + t * p.blocks * 512;
     dst[i] = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)&buffer[0][chunk * 64];
   }
   auto copy = [&](int block, int slot) {   // past the last: a stand-in that nobody reads, so that the waits can count
-    const long at = (long)min(block, to - 1) * 512;
+    block = min(block, to - 1);
+    const long at_a = (long)(block / PARTS) * 512, at_b = (long)block * 512;
     const uint32_t off = (uint32_t)slot * (kChunks * 1024);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
       // (a load into LDS may read m0 one wait state after it was written)
       asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst[i] + off), "v"(lane * 16),
-                   "s"(src[i] + at)
+                   "s"(src[i] + (i * kWaves < BM ? at_a : at_b))
                    : "memory", "m0");
   };
   f32x4 acc[TM][TN];
@@ -954,20 +967,22 @@ int cdiv(long a, long b) { return (int)((a + b - 1) / b); }
 enum : int { kSmall, kMiddle, kWide, kLarge };
 struct Plan16 {
   int tile = kSmall, blocks = 0, splits = 1;
+  int parts = 1;          // blocks of W's 16-bit form for each block of the rows
   long slab = 0;          // output columns a slab
   size_t rows = 0, ea = 0, eb = 0, weights = 0, sums = 0, done = 0, total = 0;
   int bm() const { return tile == kSmall ? 64 : tile == kMiddle ? 128 : 256; }
   int bn() const { return tile == kSmall ? 64 : tile == kLarge ? 256 : 128; }
   int tiles(long M, long cols) const { return cdiv(M, bm()) * cdiv(up(cols, 128), bn()); }
 };
-Plan16 plan16(long M, long C, long O) {
+Plan16 plan16(long M, long C, long O, int parts) {
   Plan16 p;
   p.blocks = cdiv(C, kBlockK);
+  p.parts = parts;
   p.slab = std::max<long>(256, kSlabBytes / (p.blocks * 64l) / 256 * 256);
   p.slab = std::min(p.slab, up(O, 256));
   const long cols = std::min(p.slab, O);
   // shares of at least eight blocks each
-  const int most = std::max(1, std::min(kMaxSplits, p.blocks / 8));
+  const int most = std::max(1, std::min(kMaxSplits, p.blocks * parts / 8));
   // 256 x 256 a CU at once, or two of 256 x 128, one of which alone takes 0.6 of the time of two:
   // whichever's last round is fuller (384 large tiles 262 us, as 768 wide ones 215)
   p.tile = kLarge;
@@ -992,7 +1007,7 @@ Plan16 plan16(long M, long C, long O) {
   p.rows = take((size_t)up(M, 16) * p.blocks * 64);
   p.ea = take((size_t)M * 4);
   p.eb = take((size_t)up(O, 128) * 4);
-  p.weights = take((size_t)up(p.slab, 128) * p.blocks * 64);
+  p.weights = take((size_t)up(p.slab, 128) * p.blocks * parts * 64);
   // an upper bound, so that more rows never need less: with shares there are at most 512 thread blocks
   // of at most 128 x 128
   p.sums = take(std::min<size_t>((size_t)kMaxSplits * up(M, 128) * up(p.slab, 128) * 4, 512ul * 128 * 128 * 4));
@@ -1047,7 +1062,8 @@ int exponent_blocks(int O) {
 template <int F, int X, bool BACK>
 hipError_t launch_tiled(const Linear& p, char* scratch, hipStream_t s) {
   const int C = BACK ? p.N : p.K, O = BACK ? p.K : p.N;
-  const Plan16 plan = plan16(p.M, C, O);
+  constexpr int kParts = in_two<F, X>() ? 2 : 1;
+  const Plan16 plan = plan16(p.M, C, O, kParts);
   uint16_t* rows = reinterpret_cast<uint16_t*>(scratch + plan.rows);
   int* ea = reinterpret_cast<int*>(scratch + plan.ea);
   int* eb = reinterpret_cast<int*>(scratch + plan.eb);
@@ -1071,16 +1087,16 @@ hipError_t launch_tiled(const Linear& p, char* scratch, hipStream_t s) {
       hipLaunchKernelGGL((weights16_kernel<F, X>), dim3((unsigned)cdiv(cols, 128), (unsigned)cdiv(plan.blocks, 16)),
                          dim3(512), 0, s, w);
     RETURN_IF(hipGetLastError());
-    const Product16 q{rows, ea, weights, F == kNv ? nullptr : eb + o, F == kNv ? p.w.g : nullptr, p.M, cols, plan.blocks,
-                      p.base ? p.base + o : nullptr, p.bs, p.y + o, p.ys, plan.splits,
+    const Product16 q{rows, ea, weights, F == kNv ? nullptr : eb + o, F == kNv ? p.w.g : nullptr, p.M, cols,
+                      plan.blocks * kParts, p.base ? p.base + o : nullptr, p.bs, p.y + o, p.ys, plan.splits,
                       reinterpret_cast<float*>(scratch + plan.sums), done};
     const dim3 grid((unsigned)tiles, (unsigned)plan.splits);
     const dim3 block(plan.tile == kLarge ? 512 : 256);
     switch (plan.tile) {
-      case kSmall: hipLaunchKernelGGL((product16_kernel<X, 2, 2, 2, 2, 4>), grid, block, 0, s, q); break;
-      case kMiddle: hipLaunchKernelGGL((product16_kernel<X, 4, 4, 2, 2, 4>), grid, block, 0, s, q); break;
-      case kWide: hipLaunchKernelGGL((product16_kernel<X, 8, 4, 2, 2, 3>), grid, block, 0, s, q); break;
-      default: hipLaunchKernelGGL((product16_kernel<X, 8, 4, 2, 4, 4>), grid, block, 0, s, q);
+      case kSmall: hipLaunchKernelGGL((product16_kernel<X, 2, 2, 2, 2, 4, kParts>), grid, block, 0, s, q); break;
+      case kMiddle: hipLaunchKernelGGL((product16_kernel<X, 4, 4, 2, 2, 4, kParts>), grid, block, 0, s, q); break;
+      case kWide: hipLaunchKernelGGL((product16_kernel<X, 8, 4, 2, 2, 3, kParts>), grid, block, 0, s, q); break;
+      default: hipLaunchKernelGGL((product16_kernel<X, 8, 4, 2, 4, 4, kParts>), grid, block, 0, s, q);
     }
     RETURN_IF(hipGetLastError());
   }
@@ -1113,13 +1129,14 @@ hipError_t launch_turned(const Linear& p, char* scratch, hipStream_t s) {
 // of 2048 columns takes 11, of 6144 28.5; the tiled product 25 and its passes over the 16-bit forms
 // (3.5 TB/s) and the product (0.9 PFLOP/s). 128 rows of 6144 to 4096: 29 against 49, 256: 57 against
 // 58, 512: 110 against 75; 1024 rows of 2048 to 1536: 33 against 44.
-int rows_most(int K, int N, int tile) {
+// parts: the product's, as many times as long.
+int rows_most(int K, int N, int tile, int parts) {
   const double round = 2.0 + 0.0044 * K;
   const long columns = cdiv(N, 32);
   int most = kRowsMax;
   for (int r = 1; r <= 8; ++r) {
     const double M = (double)(256l * r / columns) * tile;
-    const double tiled = 25.0 + 2.5 * K * N / 3.5e6 + 4.0 * M * K / 3.5e6 + 2.0 * M * N * K / 0.9e9;
+    const double tiled = 25.0 + 2.5 * K * N / 3.5e6 + 4.0 * M * K / 3.5e6 + 2.0 * parts * M * N * K / 0.9e9;
     if (M > most && r * round < tiled) most = (int)std::min(M, 1024.0);   // (measured up to there)
   }
   return most;
@@ -1129,7 +1146,7 @@ template <int F, int X>
 hipError_t launch_any(const Linear& p, bool back, char* scratch, hipStream_t s) {
   if (back)
     return p.M <= kRowsMax ? launch_turned<F, X>(p, scratch, s) : launch_tiled<F, X, true>(p, scratch, s);
-  if (p.M > rows_most(p.K, p.N, rows_tile<F, X>())) return launch_tiled<F, X, false>(p, scratch, s);
+  if (p.M > rows_most(p.K, p.N, rows_tile<F, X>(), in_two<F, X>() ? 2 : 1)) return launch_tiled<F, X, false>(p, scratch, s);
   return launch_rows<F, X>({p.w, p.x, p.xs, p.M, p.K, p.N, p.base, p.bs, p.y, p.ys}, s);
 }
 
@@ -1147,11 +1164,12 @@ hipError_t launch_format(const Linear& p, bool back, char* scratch, hipStream_t 
 }  // namespace
 
 void linear_scratch(int M, int K, int N, size_t* forward, size_t* backward) {
-  // (whatever the format: as for the shorter tiles of the packed product)
-  if (forward) *forward = M > rows_most(K, N, 32) ? plan16(M, K, N).total : 0;
+  // whatever the format and type: as for the shorter tiles of the packed product, and the larger form of W
+  auto tiled = [&](int C, int O) { return std::max(plan16(M, C, O, 1).total, plan16(M, C, O, 2).total); };
+  if (forward) *forward = M > rows_most(K, N, 32, 1) ? tiled(K, N) : 0;
   if (backward) {
     *backward = M > 0 ? plan_turned(std::min(M, kRowsMax), K, N).total : 0;
-    if (M > kRowsMax) *backward = std::max(*backward, plan16(M, N, K).total);
+    if (M > kRowsMax) *backward = std::max(*backward, tiled(N, K));
   }
 }
 
