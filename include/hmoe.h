@@ -543,10 +543,12 @@ hmoe_status moe_linear_scratch_bytes(int32_t M, int32_t K, int32_t N, size_t* fo
  * row the same base (a bias). Up to 64 rows, and as many more as pay (up to 1024), the packed weights go
  * into the matrix cores as exact numbers, in one launch; where moe_linear_scratch_bytes says 0 it needs
  * no scratch. Beyond, they are laid out in scratch as fp16 with an exponent for each row of W, in slabs
- * of 64 MiB: exact for NVFP4, for MXFP4 down to 2^-35 of the row's largest scale, INT4 as two fp16 numbers
- * with fp16 scales (exact), rounded to one (2^-11 of each weight) with bf16 ones; bf16 rows enter as fp16 with an exponent of their own (exact down to 2^-29 of
- * the row's largest element, within 2^-39 of it below). INT4: an infinity in x[m] gives NaN or
- * infinities in y[m]; other rows are not touched. M = 0 is a no-op.
+ * of 64 MiB: exact for NVFP4, for MXFP4 down to 2^-35 of the row's largest scale, for INT4 down to 2^-24 of
+ * it (below, a scale enters within 2^-33 of the largest). With fp16 scales an INT4 weight is two fp16
+ * numbers; with bf16 ones a zero point enters with the sum of its group's x. bf16 rows enter as fp16 with
+ * an exponent of their own: exact down to 2^-29 of the row's largest element, within 2^-39 of it below
+ * (2^-27 and 2^-35 with INT4's zero points). INT4: an infinity in x[m] gives NaN or infinities in y[m];
+ * other rows are not touched. M = 0 is a no-op.
  * Errors: HMOE_ERR_INVALID_ARG (w NULL; an unknown format, group or dtype; M < 0; K or N < 1; a
  * stride below the row's length; base == y with another stride); HMOE_ERR_UNSUPPORTED (K not a
  * multiple of 32 and of the group; M > 2^22, K or N > 2^20); HMOE_ERR_SCRATCH; HMOE_ERR_ALIGN;
@@ -557,9 +559,10 @@ hmoe_status moe_linear(const void* x, int64_t x_stride, const hmoe_packed* w, in
 
 /* Gradient of moe_linear with respect to x: dx[m] = dbase[m] + W^T dy[m], dy [M, N], dbase and dx
  * [M, K]; the weights are frozen, and the gradient with respect to base is dy itself (for a bias, its
- * sum over the rows). dbase as base above. W and dy are rounded as by moe_linear's fp16 form, W with an
- * exponent for each group of columns, but INT4 weights are not rounded up to 64
- * rows. Two launches up to 64 rows, three beyond (more past one slab).
+ * sum over the rows). dbase as base above. W and dy enter as in moe_linear's fp16 form, W
+ * with an exponent for each group of columns: what is said of the row's largest scale there goes here for
+ * the largest of the group over all rows of W. Two launches up to 64 rows, three beyond (five with bf16 rows and
+ * INT4's zero points; more past one slab).
  * M = 0 is a no-op. Errors: as moe_linear. */
 hmoe_status moe_linear_backward(const void* dy, int64_t dy_stride, const hmoe_packed* w, int32_t M,
                                 int32_t K, int32_t N, int32_t dtype, const void* dbase,

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 from oracle import packed as P
-from packed_testlib import packed, rounded, upload
+from packed_testlib import check, offset_values, packed, rounded, upload
 
 pytestmark = pytest.mark.gpu
 
@@ -135,3 +135,32 @@ def test_int4_weights_are_whole_in_few_rows(hm, M, group, zero, dtype):
 def test_int4_weights_are_whole_in_many_fp16_rows(hm, M, K, N, group, zero):
     for back in (False, True):
         weights_alone(hm, M, K, N, back, group, zero, "fp16")
+
+
+@pytest.mark.parametrize("group,zero", [(32, True), (64, True), (128, True), (32, False), (128, False)])
+@pytest.mark.parametrize("M,K,N", [(70, 384, 150), (1030, 384, 150), (1300, 128, 4001), (66, 8192, 300), (70, 128, 5000)])
+def test_int4_weights_are_whole_in_many_bf16_rows(hm, M, K, N, group, zero):
+    """Zero points are a product of their own there: of the groups' sums of x, or of dy and (8 - z) s."""
+    for back in (False, True):
+        weights_alone(hm, M, K, N, back, group, zero, "bf16")
+
+
+@pytest.mark.parametrize("back", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M,K,N", [(200, 640, 333), (1100, 2176, 520)])
+def test_zero_points_at_both_ends(hm, M, K, N, group, back):
+    """Codes and zero points of 0 and 15, where the two products cancel most."""
+    import torch
+    rng = np.random.default_rng([M, K, N, group])
+    w = packed(rng, (N, K), "int4", group, True, "bf16", spread=1)
+    w["q"] = rng.choice([0x00, 0xFF, 0xF0, 0x0F], w["q"].shape).astype(np.uint8)
+    w["z"] = rng.choice([0, 15, 0xF0], w["z"].shape).astype(np.uint8)
+    W = P.values(w)
+    n_in, n_out = (N, K) if back else (K, N)
+    x, xt = rounded(rng.standard_normal((M, n_in)) + 1.0, "bf16")
+    y = torch.empty(M, n_out, dtype=torch.bfloat16, device="cuda")
+    ws = torch.full((hm.moe_linear_scratch_bytes(M, K, N)[back],), 0xFF, dtype=torch.uint8, device="cuda")
+    (hm.moe_linear_backward if back else hm.moe_linear)(xt.cuda(), upload(w), y, None, ws)
+    ref = (P.linear_backward if back else P.linear)(x, W)
+    S = offset_values(w, W)
+    check(y, ref, np.abs(x) @ (S if back else S.T), n_in + 8, "bf16")

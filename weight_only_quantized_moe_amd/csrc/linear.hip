@@ -336,24 +336,58 @@ constexpr int kBlockK = 32;
 constexpr long kSlabBytes = 64l << 20;   // of the 16-bit form of W at a time, each of its parts: a quarter of the Infinity Cache
 constexpr int kPrepThreads = 1024;
 constexpr int kMaxSplits = 4;   // shares of the reduction axis of the tiled product
+constexpr int kTickets = 8192;  // of a product: of the tiles with shares, or of 128 columns each
 
 struct Prep {
   const uint16_t* x;   // [M, C]
   long xs;
   int M, C, blocks;    // blocks of 32 of the reduction axis
+  int sums;            // blocks of sums over a group each behind them, twice (see group_sums)
   uint16_t* rows;      // fragment order
   int* ea;             // [M]
   int row_blocks;      // thread blocks for the rows; the others take exponents
   Packed w;
   int K, N;
   int* eb;             // exponents of the product's columns
-  int* done;           // tickets of the product, cleared here
-  int tickets;
+  int* done;           // tickets of the products, cleared here
 };
 
+// INT4 with bf16 scales and zero points: a weight takes 12 bits, one more than fp16 has. The tiled product
+// takes it apart, (q - z) s = (q - 8) s + (8 - z) s, into two of 11, and the second is the same for a group.
+// Forward, it meets the sum of the group's x, so that the reduction axis goes on with the groups:
+//   sum_k x[k] (q[k] - 8) s[g(k)]  +  sum_g (sum_(k of g) x[k]) (8 - z[g]) s[g]
+// with the sums as two fp16 numbers 2^-kSumShift as large, in two runs of blocks. Backward, the product of dy
+// and (8 - z) s is added to all columns of a group. Both scales leave room for what a sum of 128 takes.
+constexpr int kSumShift = 3, kSumRowTop = 10, kSumScaleTop = 8;
+
+// The sums over the groups of the tile's rows, behind their blocks: those of the rows times 2^-(e + kSumShift).
+template <int G>
+__device__ __forceinline__ void group_sums(const Prep& p, const uint16_t* x, int tile, int e, int wave, int waves) {
+  const int lane = threadIdx.x & 63, groups = p.K / G;
+  uint16_t* out = p.rows + ((long)tile * (p.blocks + 2 * p.sums) + p.blocks) * 512 + lane * 8;
+  for (int u = wave; u < p.sums * 8; u += waves) {   // an eighth of a block: one group a lane
+    const int b = u >> 3, g = b * 32 + (lane >> 4) * 8 + (u & 7);
+    float sum = 0.f;
+    if (g < groups)
+#pragma unroll
+      for (int c = 0; c < G; c += 8) {
+        const u32x4 v = load16(x + (long)g * G + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w = v[i];
+          sum += ldexpf(bf16_lo(w), -e - kSumShift) + ldexpf(bf16_hi(w), -e - kSumShift);
+        }
+      }
+    const uint32_t hi = pack_f16(sum, sum) & 0xFFFFu;
+    const float rest = sum - fp16_to_f32(hi);
+    out[(long)b * 512 + (u & 7)] = (uint16_t)hi;
+    out[(long)(p.sums + b) * 512 + (u & 7)] = (uint16_t)pack_f16(rest, rest);
+  }
+}
+
 // Rows of x: 16 a block. bf16 goes to fp16 times 2^-e with e of the row's largest finite |x|, which
-// lands in [2^14, 2^15).
-template <int X>
+// lands in [2^14, 2^15), or at 2^kSumRowTop where sums follow.
+template <int F, int X>
 __device__ __forceinline__ void prep_rows(const Prep& p, int tile, uint32_t (&part)[kPrepThreads / 64][16]) {
   constexpr int kWaves = kPrepThreads / 64;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, m = tile * 16 + (lane & 15);
@@ -372,7 +406,7 @@ __device__ __forceinline__ void prep_rows(const Prep& p, int tile, uint32_t (&pa
       }
     return v;
   };
-  uint16_t* out = p.rows + (long)tile * p.blocks * 512 + lane * 8;
+  uint16_t* out = p.rows + (long)tile * (p.blocks + 2 * p.sums) * 512 + lane * 8;
   auto store = [&](int b, u32x4 v, int e) {
     if constexpr (X == kBf) {
 #pragma unroll
@@ -413,7 +447,7 @@ __device__ __forceinline__ void prep_rows(const Prep& p, int tile, uint32_t (&pa
     top = 0;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) top = max(top, part[w][lane & 15]);
-    if (top) e = (int)(top >> 7) - 127 - 14;
+    if (top) e = (int)(top >> 7) - 127 - (p.sums ? kSumRowTop : 14);
   }
 #pragma unroll
   for (int j = 0; j < HELD; ++j)
@@ -421,6 +455,7 @@ __device__ __forceinline__ void prep_rows(const Prep& p, int tile, uint32_t (&pa
   for (int b = wave + HELD * kWaves; b < whole; b += kWaves) store(b, load(b), e);
   if (whole < p.blocks && wave == 0) store(whole, load(whole), e);
   if (wave == 0 && lane < 16 && m < p.M) p.ea[m] = e;
+  if constexpr (is_int4(F) && X == kBf) group_sums<group_of(F)>(p, x, tile, e, wave, kWaves);
 }
 
 // The exponent of a scale where it is finite and not zero
@@ -435,10 +470,11 @@ __device__ __forceinline__ int scale_exponent(const Packed& w, long at) {
   }
 }
 // with the largest scale of a column of the product at exponent `top`, W 2^-e fits fp16: the largest
-// lands in [2^10, 2^11), or at 2^12 for MXFP4, times 16, or 6, below 2^15
+// lands in [2^10, 2^11), or at 2^12 for MXFP4, times 16, or 6, below 2^15; with sums of groups in the rows
+// at 2^kSumScaleTop, as (8 - z) s enters 2^kSumShift as large
 template <int F>
-__device__ __forceinline__ int column_exponent(int top) {
-  return top == -1000 ? 0 : top - (F == kMx ? 12 : 10);
+__device__ __forceinline__ int column_exponent(int top, bool sums) {
+  return top == -1000 ? 0 : top - (F == kMx ? 12 : sums ? kSumScaleTop : 10);
 }
 
 // What the product needs besides W: its rows as fp16, an exponent for each of its columns (NVFP4 needs
@@ -450,8 +486,8 @@ __global__ __launch_bounds__(kPrepThreads) void linear_prep_kernel(Prep p) {
   constexpr int kWaves = kPrepThreads / 64, G = group_of(F);
   __shared__ uint32_t part[kWaves][16];
   if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < p.tickets; i += kPrepThreads) p.done[i] = 0;
-  if ((int)blockIdx.x < p.row_blocks) return prep_rows<X>(p, blockIdx.x, part);
+    for (int i = threadIdx.x; i < kTickets; i += kPrepThreads) p.done[i] = 0;
+  if ((int)blockIdx.x < p.row_blocks) return prep_rows<F, X>(p, blockIdx.x, part);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, b = blockIdx.x - p.row_blocks, groups = p.K / G;
   if constexpr (F == kNv) {
     return;
@@ -461,7 +497,7 @@ __global__ __launch_bounds__(kPrepThreads) void linear_prep_kernel(Prep p) {
     int top = -1000;
     for (int g = lane; g < groups; g += 64) top = max(top, scale_exponent<F, X>(p.w, (long)n * groups + g));
     for (int d = 32; d; d >>= 1) top = max(top, __shfl_xor(top, d));
-    if (lane == 0) p.eb[n] = column_exponent<F>(top);
+    if (lane == 0) p.eb[n] = column_exponent<F>(top, p.sums);
   } else {
     const int g = b * 8 + (lane & 7);
     int top = -1000;
@@ -482,19 +518,21 @@ __global__ __launch_bounds__(kPrepThreads) void linear_prep_kernel(Prep p) {
       top = -1000;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) top = max(top, (int)part[w][i]);
-      if (k < p.K) p.eb[k] = column_exponent<F>(top);
+      if (k < p.K) p.eb[k] = column_exponent<F>(top, false);
     }
   }
 }
 
 // INT4 with fp16 scales takes up to 15 bits: two fp16 numbers a weight, in blocks of the reduction axis behind
-// one another. With bf16 scales it takes 11, and 12 with zero points.
+// one another. With bf16 scales and z = 8 it takes 11.
 template <int F, int S>
 constexpr bool in_two() { return is_int4(F) && S == kHf; }
 
 struct Weights16 {
   Packed w;
   int K, N, first, cols, blocks;   // the slab's first column of the product and their number; blocks of the rows
+  const uint8_t* z;                // zero points that were taken out of w, and the blocks of their sums
+  int sums;
   const int* eb;
   uint16_t* out;
 };
@@ -538,8 +576,14 @@ __device__ __forceinline__ uint32_t zero16(const Packed& w, long at) {
   else return 0x4C00u | ((w.z ? w.z[at] & 15u : 8u) << 6);
 }
 
+// (8 - z) s 2^-e of a group: at most 11 bits with a bf16 scale
+template <int S>
+__device__ __forceinline__ float offset_weight(const Packed& w, const uint8_t* z, long at, int e) {
+  return ldexpf((8.f - (float)(z[at] & 15u)) * to_f32<S>(reinterpret_cast<const uint16_t*>(w.s)[at]), -e);
+}
+
 // The 16-bit form of rows [first, first + cols) of W, columns of the product. A wave takes one tile and
-// four steps of 128 of K.
+// four steps of 128 of K, or a block of groups.
 template <int F, int S>
 __global__ __launch_bounds__(512) void weights16_kernel(Weights16 p) {
   constexpr int G = group_of(F);
@@ -549,7 +593,20 @@ __global__ __launch_bounds__(512) void weights16_kernel(Weights16 p) {
   const int e = F == kNv ? 0 : p.eb[n];
   const long groups = n * (p.K / G);
   constexpr int kParts = in_two<F, S>() ? 2 : 1;
-  uint16_t* out = p.out + (long)(blockIdx.x * 8 + i) * p.blocks * kParts * 512 + lane * 8;
+  uint16_t* out = p.out + (long)(blockIdx.x * 8 + i) * (p.blocks * kParts + 2 * p.sums) * 512 + lane * 8;
+  if constexpr (is_int4(F) && S == kBf)
+    if (const int b = (int)blockIdx.y - (p.blocks + 15) / 16; b >= 0) {   // (8 - z) s, for both parts of the sums
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int g = b * 32 + (lane >> 4) * 8 + j;
+        v[j] = g < p.K / G ? offset_weight<S>(p.w, p.z, groups + g, e - kSumShift) : 0.f;
+      }
+      const u32x4 h = {pack_f16(v[0], v[1]), pack_f16(v[2], v[3]), pack_f16(v[4], v[5]), pack_f16(v[6], v[7])};
+      *reinterpret_cast<u32x4*>(out + (long)(p.blocks + b) * 512) = h;
+      *reinterpret_cast<u32x4*>(out + (long)(p.blocks + p.sums + b) * 512) = h;
+      return;
+    }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int b0 = (blockIdx.y * 4 + j) * 4;      // first block of the step
@@ -643,6 +700,23 @@ __global__ __launch_bounds__(256) void weights16_turned_kernel(Weights16 p) {
     to[0] = v;
     if constexpr (kParts == 2) to[64] = low;
   });
+}
+
+// (8 - z) s of the groups [first, first + cols), columns of a product over n, times the 2^-e of their columns
+// of W. A block takes a block of the reduction axis and 128 groups, a wave one tile of them.
+template <int F>
+__global__ __launch_bounds__(512) void offsets16_turned_kernel(Weights16 p) {
+  constexpr int G = group_of(F);
+  const int lane = threadIdx.x & 63, i = threadIdx.x >> 6, block = blockIdx.x, groups = p.K / G;
+  const int g = min(p.first + (int)blockIdx.y * 128 + 8 * (lane & 15) + i, groups - 1), e = p.eb[g * G];
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int n = block * kBlockK + (lane >> 4) * 8 + j;
+    v[j] = n < p.N ? offset_weight<kBf>(p.w, p.z, (long)n * groups + g, e) : 0.f;
+  }
+  *reinterpret_cast<u32x4*>(p.out + ((long)(blockIdx.y * 8 + i) * p.blocks + block) * 512 + lane * 8) =
+      u32x4{pack_f16(v[0], v[1]), pack_f16(v[2], v[3]), pack_f16(v[4], v[5]), pack_f16(v[6], v[7])};
 }
 
 // Up to 64 rows of the gradient without the 16-bit form in between: y[m, k] = base[m, k] + g 2^(ea[m] +
@@ -760,7 +834,11 @@ struct Product16 {
   long ys;
   int splits;           // shares of the reduction axis
   float* sums;          // [splits][thread blocks][threads][a thread's sums]
-  int* done;            // a ticket a tile
+  int* done;            // a ticket a tile: zero before and after
+  float* raw;           // where the sums go as they are, instead of y; null: nowhere
+  const float* add;     // added to the sums: a value for each 2^add_shift columns; null: nothing
+  long raw_row;         // rows of raw or add
+  int add_shift;
 };
 
 template <int N>
@@ -896,6 +974,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void product16_kernel(Product16 p)
         s_last = __hip_atomic_fetch_add(p.done + tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == p.splits - 1;
       __syncthreads();
       if (!s_last) return;
+      if (threadIdx.x == 0) __hip_atomic_store(p.done + tile, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 #pragma nounroll
       for (int t = 0; t < kTiles; t += 4) {   // all shares of four tiles requested at once, added in their order
         float u[kMaxSplits][4][4];
@@ -929,9 +1008,16 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void product16_kernel(Product16 p)
         if (m >= p.M) continue;
         const int ea = p.ea[m];
         const float* from_lds = reinterpret_cast<const float*>(dump + ((r >> 2) * TN + j0) * 64 + lane) + (r & 3);
+        if (X == kBf && PARTS == 1 && p.raw) {
+#pragma unroll
+          for (int j = 0; j < kRun; ++j)
+            if (c + j < p.cols) p.raw[m * p.raw_row + c + j] = from_lds[j * 256];
+          continue;
+        }
+        const float more = X == kBf && PARTS == 1 && p.add ? p.add[m * p.raw_row + (c >> p.add_shift)] : 0.f;
         float v[kRun];
 #pragma unroll
-        for (int j = 0; j < kRun; ++j) v[j] = ldexpf(from_lds[j * 256], ea + eb[j]) * g;
+        for (int j = 0; j < kRun; ++j) v[j] = ldexpf(from_lds[j * 256] + more, ea + eb[j]) * g;
         uint16_t* y = p.y + m * p.ys + c;
         const uint16_t* base = p.base ? p.base + m * p.bs + c : nullptr;
         if (c + kRun <= p.cols) {
@@ -962,58 +1048,85 @@ size_t pad256(size_t v) { return (v + 255) & ~size_t(255); }
 long up(long v, long to) { return (v + to - 1) / to * to; }
 int cdiv(long a, long b) { return (int)((a + b - 1) / b); }
 
-// How the tiled product of M rows and O columns over C runs: its tile, shares of the reduction axis,
-// scratch. Larger tiles read less of LDS and L2 a product; smaller ones fill the card.
+// How a product of M rows and `cols` columns over `blocks` blocks runs. Larger tiles read less of LDS and L2 a
+// product; smaller ones fill the card.
 enum : int { kSmall, kMiddle, kWide, kLarge };
-struct Plan16 {
-  int tile = kSmall, blocks = 0, splits = 1;
-  int parts = 1;          // blocks of W's 16-bit form for each block of the rows
-  long slab = 0;          // output columns a slab
-  size_t rows = 0, ea = 0, eb = 0, weights = 0, sums = 0, done = 0, total = 0;
+struct Tile16 {
+  int tile = kLarge, splits = 1;
   int bm() const { return tile == kSmall ? 64 : tile == kMiddle ? 128 : 256; }
   int bn() const { return tile == kSmall ? 64 : tile == kLarge ? 256 : 128; }
   int tiles(long M, long cols) const { return cdiv(M, bm()) * cdiv(up(cols, 128), bn()); }
 };
-Plan16 plan16(long M, long C, long O, int parts) {
-  Plan16 p;
-  p.blocks = cdiv(C, kBlockK);
-  p.parts = parts;
-  p.slab = std::max<long>(256, kSlabBytes / (p.blocks * 64l) / 256 * 256);
-  p.slab = std::min(p.slab, up(O, 256));
-  const long cols = std::min(p.slab, O);
-  // shares of at least eight blocks each
-  const int most = std::max(1, std::min(kMaxSplits, p.blocks * parts / 8));
+Tile16 tile16(long M, long cols, int blocks) {
+  Tile16 p;
   // 256 x 256 a CU at once, or two of 256 x 128, one of which alone takes 0.6 of the time of two:
   // whichever's last round is fuller (384 large tiles 262 us, as 768 wide ones 215)
-  p.tile = kLarge;
   const int large = p.tiles(M, cols);
   p.tile = kWide;
   const int wide = p.tiles(M, cols), rest = wide % 512;
   const double t_large = cdiv(large, 256), t_wide = wide / 512 + (rest == 0 ? 0. : rest <= 256 ? 0.6 : 1.);
   if (large >= 192 || wide >= 256) {
     p.tile = t_wide < t_large ? kWide : kLarge;
-  } else {
-    p.tile = kMiddle;
-    if (p.tiles(M, cols) * most < 192) p.tile = kSmall;
+    return p;
   }
-  const int tiles = p.tiles(M, cols);
-  if (p.tile < kWide) p.splits = std::max(1, std::min(512 / std::max(tiles, 1), most));
+  // shares of at least eight blocks each
+  const int most = std::max(1, std::min(kMaxSplits, blocks / 8));
+  p.tile = kMiddle;
+  if (p.tiles(M, cols) * most < 192) p.tile = kSmall;
+  p.splits = std::max(1, std::min(512 / std::max(p.tiles(M, cols), 1), most));
+  return p;
+}
+
+// How the tiled product of M rows and O columns over C runs, and its scratch. parts: blocks of W's 16-bit
+// form for each block of the rows; sums: blocks of groups' sums behind the rows', twice; groups: columns of the
+// product of dy and the zero points.
+struct Plan16 {
+  Tile16 main;
+  int blocks = 0, parts = 1, sums = 0;
+  long slab = 0;          // output columns a slab
+  size_t rows = 0, ea = 0, eb = 0, weights = 0, shares = 0, done = 0, add = 0, total = 0;
+  int all_blocks() const { return blocks * parts + 2 * sums; }
+};
+Plan16 plan16(long M, long C, long O, int parts, int sums, long groups) {
+  Plan16 p;
+  p.blocks = cdiv(C, kBlockK);
+  p.parts = parts;
+  p.sums = sums;
+  p.slab = std::max<long>(256, kSlabBytes / (p.blocks * 64l) / 256 * 256);
+  p.slab = std::min(p.slab, up(O, 256));
+  p.main = tile16(M, std::min(p.slab, O), p.all_blocks());
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t r = at;
     at += pad256(bytes);
     return r;
   };
-  p.rows = take((size_t)up(M, 16) * p.blocks * 64);
+  p.rows = take((size_t)up(M, 16) * (p.blocks + 2 * sums) * 64);
   p.ea = take((size_t)M * 4);
   p.eb = take((size_t)up(O, 128) * 4);
-  p.weights = take((size_t)up(p.slab, 128) * p.blocks * parts * 64);
+  p.weights = take((size_t)up(p.slab, 128) * p.all_blocks() * 64);
   // an upper bound, so that more rows never need less: with shares there are at most 512 thread blocks
   // of at most 128 x 128
-  p.sums = take(std::min<size_t>((size_t)kMaxSplits * up(M, 128) * up(p.slab, 128) * 4, 512ul * 128 * 128 * 4));
-  p.done = take(512 * 4);
+  p.shares = take(std::min<size_t>((size_t)kMaxSplits * up(M, 128) * up(p.slab, 128) * 4, 512ul * 128 * 128 * 4));
+  p.done = take(kTickets * 4);
+  p.add = take((size_t)M * groups * 4);
   p.total = at;
   return p;
+}
+// Of a call: F and X as the kernels have them; zeros: zero points come with it.
+template <int F, int X, bool BACK>
+Plan16 plan16_of(long M, long K, long N, bool zeros) {
+  const long groups = is_int4(F) && X == kBf && zeros ? K / group_of(F) : 0;
+  return plan16(M, BACK ? N : K, BACK ? K : N, in_two<F, X>() ? 2 : 1, BACK ? 0 : cdiv(groups, 32), BACK ? groups : 0);
+}
+// Scratch of any call
+size_t tiled_scratch(long M, long K, long N, bool back) {
+  auto most = [&](auto BACK) {
+    constexpr bool B = decltype(BACK)::value;
+    return std::max({plan16_of<kNv, kBf, B>(M, K, N, false).total, plan16_of<kI32, kHf, B>(M, K, N, false).total,
+                     plan16_of<kI32, kBf, B>(M, K, N, true).total});
+  };
+  return back ? most(std::true_type{}) : most(std::false_type{});
 }
 
 // The same for linear_turned_kernel
@@ -1038,7 +1151,7 @@ PlanTurned plan_turned(int M, int K, int N) {
   p.ea = take((size_t)p.t * 16 * 4);
   p.eb = take((size_t)p.columns * 128 * 4);
   p.sums = take((size_t)p.splits * p.columns * p.t * 16 * 128 * 4);
-  p.done = take((size_t)p.columns * 4);
+  p.done = take(kTickets * 4);
   p.total = at;
   return p;
 }
@@ -1059,46 +1172,64 @@ int exponent_blocks(int O) {
   return F == kNv ? 0 : BACK ? cdiv(O / group_of(F), 8) : cdiv(O, kPrepThreads / 64);
 }
 
+template <int X, int PARTS>
+hipError_t run_product(const Product16& q, const Tile16& t, hipStream_t s) {
+  const dim3 grid((unsigned)t.tiles(q.M, q.cols), (unsigned)t.splits);
+  const dim3 block(t.tile == kLarge ? 512 : 256);
+  switch (t.tile) {
+    case kSmall: hipLaunchKernelGGL((product16_kernel<X, 2, 2, 2, 2, 4, PARTS>), grid, block, 0, s, q); break;
+    case kMiddle: hipLaunchKernelGGL((product16_kernel<X, 4, 4, 2, 2, 4, PARTS>), grid, block, 0, s, q); break;
+    case kWide: hipLaunchKernelGGL((product16_kernel<X, 8, 4, 2, 2, 3, PARTS>), grid, block, 0, s, q); break;
+    default: hipLaunchKernelGGL((product16_kernel<X, 8, 4, 2, 4, 4, PARTS>), grid, block, 0, s, q);
+  }
+  return hipGetLastError();
+}
+
 template <int F, int X, bool BACK>
 hipError_t launch_tiled(const Linear& p, char* scratch, hipStream_t s) {
+  constexpr int kParts = in_two<F, X>() ? 2 : 1, G = group_of(F);
   const int C = BACK ? p.N : p.K, O = BACK ? p.K : p.N;
-  constexpr int kParts = in_two<F, X>() ? 2 : 1;
-  const Plan16 plan = plan16(p.M, C, O, kParts);
+  const bool zeros = is_int4(F) && X == kBf && p.w.z;
+  const Plan16 plan = plan16_of<F, X, BACK>(p.M, p.K, p.N, zeros);
   uint16_t* rows = reinterpret_cast<uint16_t*>(scratch + plan.rows);
   int* ea = reinterpret_cast<int*>(scratch + plan.ea);
   int* eb = reinterpret_cast<int*>(scratch + plan.eb);
   int* done = reinterpret_cast<int*>(scratch + plan.done);
   uint16_t* weights = reinterpret_cast<uint16_t*>(scratch + plan.weights);
+  float* shares = reinterpret_cast<float*>(scratch + plan.shares);
+  float* add = BACK && zeros ? reinterpret_cast<float*>(scratch + plan.add) : nullptr;
+  const int row_blocks = cdiv(p.M, 16);
+  const Prep prep{p.x, p.xs, p.M, C, plan.blocks, plan.sums, rows, ea, row_blocks, p.w, p.K, p.N, eb, done};
+  RETURN_IF((run_prep<F, X, BACK>(prep, row_blocks + exponent_blocks<F, BACK>(O), s)));
+  Packed alone = p.w;
+  if (zeros) alone.z = nullptr;
+  if constexpr (BACK && is_int4(F) && X == kBf)
+    if (zeros)
+      for (long o = 0; o < p.K / G; o += plan.slab) {
+        const int cols = (int)std::min<long>(plan.slab, p.K / G - o);
+        const Weights16 w{p.w, p.K, p.N, (int)o, cols, plan.blocks, p.w.z, 0, eb, weights};
+        hipLaunchKernelGGL((offsets16_turned_kernel<F>), dim3((unsigned)plan.blocks, (unsigned)cdiv(cols, 128)), dim3(512), 0,
+                           s, w);
+        RETURN_IF(hipGetLastError());
+        const Tile16 tile = tile16(p.M, cols, plan.blocks);
+        const Product16 q{rows, ea, weights, nullptr, nullptr, p.M, cols, plan.blocks, nullptr, 0, nullptr, 0,
+                          tile.splits, shares, done, add + o, nullptr, p.K / G, 0};
+        RETURN_IF((run_product<X, 1>(q, tile, s)));
+      }
   for (long o = 0; o < O; o += plan.slab) {
     const int cols = (int)std::min<long>(plan.slab, O - o);
-    const int tiles = plan.tiles(p.M, cols);
-    if (o == 0 || plan.splits > 1) {   // later slabs need the tickets at zero only
-      const int row_blocks = o == 0 ? cdiv(p.M, 16) : 0;
-      const int more = o > 0 ? 1 : exponent_blocks<F, BACK>(O);
-      const Prep prep{p.x, p.xs, p.M, C, plan.blocks, rows, ea, row_blocks, p.w, p.K, p.N, eb, done,
-                      plan.splits > 1 ? tiles : 0};
-      RETURN_IF((run_prep<F, X, BACK>(prep, row_blocks + more, s)));
-    }
-    const Weights16 w{p.w, p.K, p.N, (int)o, cols, plan.blocks, eb, weights};
+    const Weights16 w{alone, p.K, p.N, (int)o, cols, plan.blocks, p.w.z, plan.sums, eb, weights};
     if constexpr (BACK)
       hipLaunchKernelGGL((weights16_turned_kernel<F, X>), dim3((unsigned)cdiv(plan.blocks, 4), (unsigned)cdiv(cols, 128)),
                          dim3(256), 0, s, w);
     else
-      hipLaunchKernelGGL((weights16_kernel<F, X>), dim3((unsigned)cdiv(cols, 128), (unsigned)cdiv(plan.blocks, 16)),
-                         dim3(512), 0, s, w);
+      hipLaunchKernelGGL((weights16_kernel<F, X>),
+                         dim3((unsigned)cdiv(cols, 128), (unsigned)(cdiv(plan.blocks, 16) + plan.sums)), dim3(512), 0, s, w);
     RETURN_IF(hipGetLastError());
     const Product16 q{rows, ea, weights, F == kNv ? nullptr : eb + o, F == kNv ? p.w.g : nullptr, p.M, cols,
-                      plan.blocks * kParts, p.base ? p.base + o : nullptr, p.bs, p.y + o, p.ys, plan.splits,
-                      reinterpret_cast<float*>(scratch + plan.sums), done};
-    const dim3 grid((unsigned)tiles, (unsigned)plan.splits);
-    const dim3 block(plan.tile == kLarge ? 512 : 256);
-    switch (plan.tile) {
-      case kSmall: hipLaunchKernelGGL((product16_kernel<X, 2, 2, 2, 2, 4, kParts>), grid, block, 0, s, q); break;
-      case kMiddle: hipLaunchKernelGGL((product16_kernel<X, 4, 4, 2, 2, 4, kParts>), grid, block, 0, s, q); break;
-      case kWide: hipLaunchKernelGGL((product16_kernel<X, 8, 4, 2, 2, 3, kParts>), grid, block, 0, s, q); break;
-      default: hipLaunchKernelGGL((product16_kernel<X, 8, 4, 2, 4, 4, kParts>), grid, block, 0, s, q);
-    }
-    RETURN_IF(hipGetLastError());
+                      plan.all_blocks(), p.base ? p.base + o : nullptr, p.bs, p.y + o, p.ys, plan.main.splits, shares, done,
+                      nullptr, add ? add + o / G : nullptr, p.K / G, G == 32 ? 5 : G == 64 ? 6 : 7};
+    RETURN_IF((run_product<X, kParts>(q, plan.main, s)));
   }
   return hipSuccess;
 }
@@ -1111,8 +1242,7 @@ hipError_t launch_turned(const Linear& p, char* scratch, hipStream_t s) {
   int* eb = reinterpret_cast<int*>(scratch + plan.eb);
   int* done = reinterpret_cast<int*>(scratch + plan.done);
   const int row_blocks = cdiv(p.M, 16);
-  const Prep prep{p.x, p.xs, p.M, p.N, plan.blocks, rows, ea, row_blocks, p.w, p.K, p.N, eb, done,
-                  plan.splits > 1 ? plan.columns : 0};
+  const Prep prep{p.x, p.xs, p.M, p.N, plan.blocks, 0, rows, ea, row_blocks, p.w, p.K, p.N, eb, done};
   RETURN_IF((run_prep<F, X, true>(prep, row_blocks + exponent_blocks<F, true>(p.K), s)));
   const TurnedRows q{p.w, rows, ea, eb, p.M, p.K, p.N, plan.blocks, p.base, p.bs, p.y, p.ys, plan.splits,
                      reinterpret_cast<float*>(scratch + plan.sums), done};
@@ -1164,12 +1294,11 @@ hipError_t launch_format(const Linear& p, bool back, char* scratch, hipStream_t 
 }  // namespace
 
 void linear_scratch(int M, int K, int N, size_t* forward, size_t* backward) {
-  // whatever the format and type: as for the shorter tiles of the packed product, and the larger form of W
-  auto tiled = [&](int C, int O) { return std::max(plan16(M, C, O, 1).total, plan16(M, C, O, 2).total); };
-  if (forward) *forward = M > rows_most(K, N, 32, 1) ? tiled(K, N) : 0;
+  // whatever the format and type: as for the shorter tiles of the packed product
+  if (forward) *forward = M > rows_most(K, N, 32, 1) ? tiled_scratch(M, K, N, false) : 0;
   if (backward) {
     *backward = M > 0 ? plan_turned(std::min(M, kRowsMax), K, N).total : 0;
-    if (M > kRowsMax) *backward = std::max(*backward, tiled(N, K));
+    if (M > kRowsMax) *backward = std::max(*backward, tiled_scratch(M, K, N, true));
   }
 }
 
