@@ -542,7 +542,8 @@ hmoe_status moe_linear_scratch_bytes(int32_t M, int32_t K, int32_t N, size_t* fo
  * base counts as zeros, base may be y itself (same stride), and a base stride of 0 gives every
  * row the same base (a bias). Up to 64 rows, and as many more as pay (up to 1024), the packed weights go
  * into the matrix cores as exact numbers, in one launch; where moe_linear_scratch_bytes says 0 it needs
- * no scratch. Beyond, they are laid out in scratch as fp16 with an exponent for each row of W, in slabs
+ * no scratch; these sums are taken in fp32 before g (NVFP4: of x * e2m1 * e4m3; INT4: of x * (16 + q)), so
+ * from |x| near 2^128 / (2688 K), or 2^128 / (31 K), on they may overflow. Beyond, they are laid out in scratch as fp16 with an exponent for each row of W, in slabs
  * of 64 MiB: exact for NVFP4, for MXFP4 down to 2^-35 of the row's largest scale, for INT4 down to 2^-24 of
  * it (below, a scale enters within 2^-33 of the largest). With fp16 scales an INT4 weight is two fp16
  * numbers; with bf16 ones a zero point enters with the sum of its group's x. bf16 rows enter as fp16 with

@@ -780,7 +780,7 @@ __global__ __launch_bounds__(256) void linear_turned_kernel(TurnedRows p) {
   auto finish = [&](int o, float v) {
     const int m = o >> 7, c = c0 + (o & 127);
     if (m >= p.M || c >= p.K) return;
-    v = ldexpf(v, p.ea[m] + (F == kNv ? 0 : p.eb[c])) * g;
+    v = ldexpf(v * g, p.ea[m] + (F == kNv ? 0 : p.eb[c]));   // (g first: without it the value may lie past fp32)
     if (p.base) v += to_f32<X>(p.base[m * p.bs + c]);
     p.y[m * p.ys + c] = from_f32<X>(v);
   };
@@ -1017,7 +1017,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void product16_kernel(Product16 p)
         const float more = X == kBf && PARTS == 1 && p.add ? p.add[m * p.raw_row + (c >> p.add_shift)] : 0.f;
         float v[kRun];
 #pragma unroll
-        for (int j = 0; j < kRun; ++j) v[j] = ldexpf(from_lds[j * 256] + more, ea + eb[j]) * g;
+        for (int j = 0; j < kRun; ++j) v[j] = ldexpf((from_lds[j * 256] + more) * g, ea + eb[j]);
         uint16_t* y = p.y + m * p.ys + c;
         const uint16_t* base = p.base ? p.base + m * p.bs + c : nullptr;
         if (c + kRun <= p.cols) {
