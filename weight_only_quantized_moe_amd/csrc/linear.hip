@@ -1150,7 +1150,7 @@ PlanTurned plan_turned(int M, int K, int N) {
   p.rows = take((size_t)p.t * 16 * p.blocks * 64);
   p.ea = take((size_t)p.t * 16 * 4);
   p.eb = take((size_t)p.columns * 128 * 4);
-  p.sums = take((size_t)p.splits * p.columns * p.t * 16 * 128 * 4);
+  p.sums = take(p.splits > 1 ? (size_t)p.splits * p.columns * p.t * 16 * 128 * 4 : 0);
   p.done = take(kTickets * 4);
   p.total = at;
   return p;
