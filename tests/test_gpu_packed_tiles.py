@@ -92,7 +92,7 @@ def test_large_layers(hm):
 def test_forward_slabs(hm, fmt, dtype):
     """Two slabs of columns without shares of the reduction axis, and two with."""
     run(hm, fmt, dtype, 66, 64, 530000, False, LARGE, 2)
-    run(hm, fmt, dtype, 140, 4096, 8400, False, MIDDLE, 2)
+    run(hm, fmt, dtype, 420, 4096, 8400, False, MIDDLE, 2)
 
 
 @pytest.mark.parametrize("fmt,dtype", [(NV, "bf16"), (MX, "fp16"), (I64Z, "bf16"), (I128, "fp16")])

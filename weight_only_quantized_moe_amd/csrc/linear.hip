@@ -1255,28 +1255,32 @@ hipError_t launch_turned(const Linear& p, char* scratch, hipStream_t s) {
 }
 
 // The most rows that the packed product takes: whole rounds of its blocks (32 columns and `tile` rows
-// each, one a CU) against the tiled product's three launches, in us as measured on MI355X: a round
-// of 2048 columns takes 11, of 6144 28.5; the tiled product 25 and its passes over the 16-bit forms
-// (3.5 TB/s) and the product (0.9 PFLOP/s). 128 rows of 6144 to 4096: 29 against 49, 256: 57 against
-// 58, 512: 110 against 75; 1024 rows of 2048 to 1536: 33 against 44.
-// parts: the product's, as many times as long.
-int rows_most(int K, int N, int tile, int parts) {
-  const double round = 2.0 + 0.0044 * K;
+// each, one a CU) against the tiled product's three launches, in us as measured on MI355X: a round of 64 rows and
+// 6144 columns takes 29, of 32 rows 19; the tiled product 25, its passes over the 16-bit forms (3.5 TB/s), the
+// product (0.9 PFLOP/s), and 8 for zero points that enter apart. parts: of a weight in the tiled product.
+// 6144 to 4096, packed against tiled: NVFP4 128 rows 30 and 51, 256 57 and 64, 512 112 and 82; INT4 g32 with zero
+// points, bf16, 128 rows 40 and 61, 256 77 and 75; g128, fp16, 512 rows 118 and 129. 2048 to 1536: 1024 rows 36 and 49.
+int rows_most(int K, int N, int tile, int parts, bool zeros) {
+  const double round = 2.0 + (tile == 32 ? 0.0028 : 0.0044) * K;
   const long columns = cdiv(N, 32);
   int most = kRowsMax;
   for (int r = 1; r <= 8; ++r) {
     const double M = (double)(256l * r / columns) * tile;
-    const double tiled = 25.0 + 2.5 * K * N / 3.5e6 + 4.0 * M * K / 3.5e6 + 2.0 * parts * M * N * K / 0.9e9;
+    const double tiled = 25.0 + (zeros ? 8.0 : 0.0) + (0.5 + 2.0 * parts) * K * N / 3.5e6 + 4.0 * M * K / 3.5e6 +
+                         2.0 * parts * M * N * K / 0.9e9;
     if (M > most && r * round < tiled) most = (int)std::min(M, 1024.0);   // (measured up to there)
   }
   return most;
 }
+// the fewest of any format and type (two parts and zero points only make the tiled product longer)
+int rows_most_least(int K, int N) { return std::min(rows_most(K, N, 32, 1, false), rows_most(K, N, 64, 1, false)); }
 
 template <int F, int X>
 hipError_t launch_any(const Linear& p, bool back, char* scratch, hipStream_t s) {
   if (back)
     return p.M <= kRowsMax ? launch_turned<F, X>(p, scratch, s) : launch_tiled<F, X, true>(p, scratch, s);
-  if (p.M > rows_most(p.K, p.N, rows_tile<F, X>(), in_two<F, X>() ? 2 : 1)) return launch_tiled<F, X, false>(p, scratch, s);
+  const bool zeros = is_int4(F) && X == kBf && p.w.z;
+  if (p.M > rows_most(p.K, p.N, rows_tile<F, X>(), in_two<F, X>() ? 2 : 1, zeros)) return launch_tiled<F, X, false>(p, scratch, s);
   return launch_rows<F, X>({p.w, p.x, p.xs, p.M, p.K, p.N, p.base, p.bs, p.y, p.ys}, s);
 }
 
@@ -1294,8 +1298,8 @@ hipError_t launch_format(const Linear& p, bool back, char* scratch, hipStream_t 
 }  // namespace
 
 void linear_scratch(int M, int K, int N, size_t* forward, size_t* backward) {
-  // whatever the format and type: as for the shorter tiles of the packed product
-  if (forward) *forward = M > rows_most(K, N, 32, 1) ? tiled_scratch(M, K, N, false) : 0;
+  // whatever the format and type
+  if (forward) *forward = M > rows_most_least(K, N) ? tiled_scratch(M, K, N, false) : 0;
   if (backward) {
     *backward = M > 0 ? plan_turned(std::min(M, kRowsMax), K, N).total : 0;
     if (M > kRowsMax) *backward = std::max(*backward, tiled_scratch(M, K, N, true));
