@@ -543,8 +543,8 @@ hmoe_status moe_linear_scratch_bytes(int32_t M, int32_t K, int32_t N, size_t* fo
  * row the same base (a bias). Up to 64 rows, and as many more as pay (up to 1024), the packed weights go
  * into the matrix cores as exact numbers, in one launch; where moe_linear_scratch_bytes says 0 it needs
  * no scratch; these sums are taken in fp32 before g (NVFP4: of x * e2m1 * e4m3; INT4: of x * (16 + q)), so
- * from |x| near 2^128 / (2688 K), or 2^128 / (31 K), on they may overflow. Beyond, they are laid out in scratch as fp16 with an exponent for each row of W, in slabs
- * of 64 MiB: exact for NVFP4, for MXFP4 down to 2^-35 of the row's largest scale, for INT4 down to 2^-24 of
+ * from |x| near 2^128 / (2688 K), or 2^128 / (31 K), on they may overflow. Beyond, they are laid out in
+ * scratch as fp16 with an exponent for each row of W, in slabs of 64 MiB: exact for NVFP4, for MXFP4 down to 2^-35 of the row's largest scale, for INT4 down to 2^-24 of
  * it (below, a scale enters within 2^-33 of the largest). With fp16 scales an INT4 weight is two fp16
  * numbers; with bf16 ones a zero point enters with the sum of its group's x. bf16 rows enter as fp16 with
  * an exponent of their own: exact down to 2^-29 of the row's largest element, within 2^-39 of it below
@@ -562,16 +562,16 @@ hmoe_status moe_linear(const void* x, int64_t x_stride, const hmoe_packed* w, in
  * [M, K]; the weights are frozen, and the gradient with respect to base is dy itself (for a bias, its
  * sum over the rows). dbase as base above. W and dy enter as in moe_linear's fp16 form, W
  * with an exponent for each group of columns: what is said of the row's largest scale there goes here for
- * the largest of the group over all rows of W. Two launches up to 64 rows, three beyond (five with bf16 rows and
- * INT4's zero points; more past one slab).
- * M = 0 is a no-op. Errors: as moe_linear. */
+ * the largest of the group over all rows of W. Two launches up to 64 rows, three beyond (five with bf16
+ * rows and INT4's zero points; more past one slab). M = 0 is a no-op. Errors: as moe_linear. */
 hmoe_status moe_linear_backward(const void* dy, int64_t dy_stride, const hmoe_packed* w, int32_t M,
                                 int32_t K, int32_t N, int32_t dtype, const void* dbase,
                                 int64_t dbase_stride, void* dx, int64_t dx_stride, void* scratch,
                                 size_t scratch_bytes, hipStream_t stream);
 
 /* A layer for a few tokens, from the tokens to its output. Experts: w13 holds E matrices [2I, H]
- * (gate rows, then up rows), w2 E matrices [H, I], one format and group for both. The shared
+ * (gate rows, then up rows), w2 E matrices [H, I], one format and group for both and for all experts: a
+ * layer with an NF3 tier (a bit map) goes through hybrid_moe_forward. The shared
  * expert, if shared_inter = S > 0: shared_w13 [2S, H] and shared_w2 [H, S] in the same format,
  * and shared_gate [H] or NULL. router [E, H] and shared_gate have the activations' type. */
 typedef struct hmoe_tokens {

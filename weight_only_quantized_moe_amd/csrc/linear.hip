@@ -8,12 +8,13 @@
 // time so that the slab stays in the caches, and one tiled product (product16_kernel) serves both
 // directions; the backward pass lays W out transposed.
 //
-// The 16-bit form of W for the tiled product is fp16 whatever the rows' type: (q - z) s needs 13
-// bits in general, and fp16 keeps 11 of them where bf16 would keep 8 and add as much error again
-// as the rounding of a bf16 output. So that no exponent is lost, a column of the product has a
-// power of two of its own (linear_prep_kernel) and bf16 rows enter as fp16 times a power of two
-// of their own (exact down to 2^-29 of the row's largest element, and 2^-39 of it
-// for smaller ones). Both come back in fp32.
+// The 16-bit form of W for the tiled product is fp16 whatever the rows' type, as it keeps 11 bits where bf16
+// would keep 8. It is exact: NVFP4 and MXFP4 take no more, and INT4's (q - z) s, 12 bits with bf16 scales and 15
+// with fp16 ones, comes apart in one of two ways (see in_two and group_sums). So that exponents are kept, a
+// column of the product has a power of two of its own (linear_prep_kernel), which holds INT4 scales down to 2^-24
+// of the largest that share it, and bf16 rows enter as fp16 times a power of two of their own (exact down to
+// 2^-29 of the row's largest element, and within 2^-39 of it below; 2^-27 and 2^-35 where sums of groups
+// follow). Both come back in fp32.
 #include <algorithm>
 
 #include "packed.h"
@@ -196,9 +197,9 @@ __global__ __launch_bounds__(64) void linear_rows_kernel(LinearRows p) {
       }
 }
 
-// Rows of at least 256 columns: 16 R columns n and 16 T rows m a block, pairs of steps dealt to its waves. The rows' fragments of a step
-// meet the codes of R tiles each; the second step's come while the first is multiplied. Bound by the
-// address unit (a fragment touches 16 lines of x): 64 rows 6144 to 4096, NVFP4, 26 us.
+// Rows of at least 256 columns: 16 R columns n and 16 T rows m a block, pairs of steps dealt to its waves.
+// The rows' fragments of a step meet the codes of R tiles each; the second step's come while the first is
+// multiplied. Bound by the address unit (a fragment touches 16 lines of x): 64 rows 6144 to 4096, NVFP4, 26 us.
 template <int F, int X, int R, int T, bool EXACT>
 __global__ __launch_bounds__(512, 2) void linear_rows_pair_kernel(LinearRows p) {
   extern __shared__ float red[];
@@ -357,7 +358,9 @@ struct Prep {
 // Forward, it meets the sum of the group's x, so that the reduction axis goes on with the groups:
 //   sum_k x[k] (q[k] - 8) s[g(k)]  +  sum_g (sum_(k of g) x[k]) (8 - z[g]) s[g]
 // with the sums as two fp16 numbers 2^-kSumShift as large, in two runs of blocks. Backward, the product of dy
-// and (8 - z) s is added to all columns of a group. Both scales leave room for what a sum of 128 takes.
+// and (8 - z) s is added to all columns of a group. Both scales leave room for what a sum of 128 takes. 4096
+// rows 6144 to 4096, g64, take 240 us, 4001 rows of the gradient 273; rounded to fp16 234 and 255, as two numbers
+// about 376 and 405.
 constexpr int kSumShift = 3, kSumRowTop = 10, kSumScaleTop = 8;
 
 // The sums over the groups of the tile's rows, behind their blocks: those of the rows times 2^-(e + kSumShift).
@@ -524,7 +527,7 @@ __global__ __launch_bounds__(kPrepThreads) void linear_prep_kernel(Prep p) {
 }
 
 // INT4 with fp16 scales takes up to 15 bits: two fp16 numbers a weight, in blocks of the reduction axis behind
-// one another. With bf16 scales and z = 8 it takes 11.
+// one another. 4096 rows 6144 to 4096 take 370 us, as one number 235. With bf16 scales and z = 8 it takes 11.
 template <int F, int S>
 constexpr bool in_two() { return is_int4(F) && S == kHf; }
 
@@ -720,8 +723,8 @@ __global__ __launch_bounds__(512) void offsets16_turned_kernel(Weights16 p) {
 }
 
 // Up to 64 rows of the gradient without the 16-bit form in between: y[m, k] = base[m, k] + g 2^(ea[m] +
-// eb[k]) sum_n a[m, n] W[n, k] 2^-eb[k], INT4 as two fp16 numbers. A block takes 128 columns, 16 T rows and a share of the blocks
-// of the reduction axis, which its waves take in turn; the last block of the columns to finish adds
+// eb[k]) sum_n a[m, n] W[n, k] 2^-eb[k], INT4 as two fp16 numbers (24 rows 2048 to 1536, g64: 19.3 us a call, 18.9
+// as one). A block takes 128 columns, 16 T rows and a share of the blocks of the reduction axis, which its waves take in turn; the last block of the columns to finish adds
 // the shares up in their order.
 struct TurnedRows {
   Packed w;
@@ -850,8 +853,10 @@ __device__ __forceinline__ void wait_vmem_at_most() {
 // WM x WN waves. Blocks of the reduction axis pass through STAGES buffers in LDS, all but one of them in
 // flight, loaded by copies that go past the registers; a wave reads the next block's fragments
 // while it multiplies the present one's. With splits > 1 the block of a tile that finishes last adds the
-// shares up in their order. 4096 rows 6144 to 4096 take 185 us, 1.1 PFLOP/s, near what LDS gives: a wave
-// reads 12 KiB for 32 MFMAs. PARTS: blocks of b for each block of a.
+// shares up in their order. 4096 rows 6144 to 4096 take 188 us, 1.1 PFLOP/s, near what LDS gives: a wave
+// reads 12 KiB for 32 MFMAs. PARTS: blocks of b for each block of a. An output of so many rows of W that a slab is a
+// few hundred columns leaves CUs without a tile: 128 rows of dy through a head of 100001 rows, 2048 columns, take
+// eight slabs of 116 us.
 template <int X, int TM, int TN, int WM, int WN, int STAGES, int PARTS>
 __global__ __launch_bounds__(WM * WN * 64, 2) void product16_kernel(Product16 p) {
   constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
@@ -1060,7 +1065,7 @@ struct Tile16 {
 Tile16 tile16(long M, long cols, int blocks) {
   Tile16 p;
   // 256 x 256 a CU at once, or two of 256 x 128, one of which alone takes 0.6 of the time of two:
-  // whichever's last round is fuller (384 large tiles 262 us, as 768 wide ones 215)
+  // whichever's last round is fuller (384 large tiles 262 us, as 768 wide ones 214 to 229)
   const int large = p.tiles(M, cols);
   p.tile = kWide;
   const int wide = p.tiles(M, cols), rest = wide % 512;
@@ -1167,6 +1172,8 @@ hipError_t run_prep(const Prep& p, int blocks, hipStream_t s) {
   hipLaunchKernelGGL((linear_prep_kernel<F, X, BACK>), dim3((unsigned)blocks), dim3(kPrepThreads), 0, s, p);
   return hipGetLastError();
 }
+// (Backward that is few blocks, each of which goes through all rows of W: 18 us for 4096 rows of 6144 columns,
+// g64, but 487 for the 100001 rows of a head of 2048, MXFP4.)
 template <int F, bool BACK>
 int exponent_blocks(int O) {
   return F == kNv ? 0 : BACK ? cdiv(O / group_of(F), 8) : cdiv(O, kPrepThreads / 64);

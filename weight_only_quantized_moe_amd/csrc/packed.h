@@ -12,9 +12,9 @@
 // t, and a group scale is one factor of the product's column n = l & 15.
 //
 // The codes go into the product as exact 16-bit numbers and the sums are fp32:
-//   E2M1 is exact in both 16-bit types. MXFP4 scales multiply the fp32 sum of their 32 columns,
-//   which holds for every exponent in either type. E4M3 times E2M1 has 6 significant bits and is
-//   formed before the product (its groups of 16 would halve the MFMA's depth).
+//   E2M1 is exact in both 16-bit types. MXFP4 scales: bf16 has every exponent and the conversion of the
+//   codes applies them; fp16 has not, and they multiply the fp32 sum of their 32 columns. E4M3 times E2M1
+//   has 6 significant bits and is formed before the product (its groups of 16 would halve the MFMA's depth).
 //   INT4 becomes 16 + q by one shift and one and-or (the code lands in the low bits of a
 //   mantissa whose unit is 1), and a second product with the constant -(16 + z) into the same sum
 //   takes the offset out again: both are exact, and the matrix cores have the time. Infinite

@@ -464,9 +464,9 @@ __global__ __launch_bounds__(kUpWaves * 64, 2) void tokens_up_any_kernel(TokensA
 // h that a wave loads. With several shares the block that finishes last adds them up in their order: a
 // share is written past the caches of its own XCD, then counted. PAIRS: I and S are at least 256 (EXACT:
 // multiples of it), and a unit is a pair of steps; else it is a step. h comes as fp32 and is split here,
-// as three 16-bit planes of it would need 16 registers more (spills; two planes, 16 of the 24 bits, took 240
-// us instead of 249 for eight tokens of the GLM-class layer, MXFP4). With the next pair's codes in flight beside, at twice the registers
-// and half the waves, eight tokens of the GLM-class layer (MXFP4) took 108 us against 103.
+// as three 16-bit planes of it would need 16 registers more (spills). Eight tokens of the GLM-class layer
+// (MXFP4) take 116 us; two planes, 16 of h's 24 bits, took 104, and with the next pair's codes in flight
+// beside, at twice the registers and half the waves, 108.
 template <int F, int X, bool PAIRS, bool EXACT>
 __global__ __launch_bounds__(kDownWaves * 64, 4) void tokens_down_kernel(TokensArgs a) {
   constexpr int R = kDownCols / 16, kThreads = kDownWaves * 64, kUnit = PAIRS ? 256 : 128;
@@ -629,6 +629,9 @@ hipError_t run_up(const TokensArgs& a, hipStream_t s) {
   const long items = (long)std::min(p.M * p.k, p.E) * (p.I / 16) + p.S / 16;
   const int pairs = cdiv(p.H, 256), px = cdiv(pairs, kUpWaves);   // pairs a wave takes
   const bool exact = p.H % 256 == 0;
+  // A wave keeps at most three pairs of x and two tiles of codes for each (226 to 242 of its 256 registers), of
+  // partial pairs two, so wider layers go a step at a time: 64 experts, 7168 to 2048, MXFP4, eight tokens take 302
+  // us here, where 6144 take 101.
   if (p.H < 256 || px > (exact ? 3 : 2)) {
     const dim3 grid((unsigned)std::min<long>(items, 256));
     hipLaunchKernelGGL((tokens_up_any_kernel<F, X>), grid, dim3(kUpWaves * 64), 0, s, a);
