@@ -164,3 +164,13 @@ def test_zero_points_at_both_ends(hm, M, K, N, group, back):
     ref = (P.linear_backward if back else P.linear)(x, W)
     S = offset_values(w, W)
     check(y, ref, np.abs(x) @ (S if back else S.T), n_in + 8, "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M", [40, 1100])
+def test_one_group(hm, M, group, dtype):
+    """A row of W that is one group, and one row of W."""
+    for back in (False, True):
+        weights_alone(hm, M, group, 40, back, group, True, dtype)
+    weights_alone(hm, M, 256, 1, True, group, True, dtype)
